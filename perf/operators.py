@@ -106,8 +106,9 @@ def draw(rng):
     if op == "preference":
         length = _log_int(rng, 2, 4096)
         pairs = _log_int(rng, 1, max(2, min(512, 500000 // length)))
-        return {k: v for k, v in _pref("", pairs, length, rng.choice(("sigmoid", "sigmoid", "hinge", "ipo")),
-                                       rng.random() < 0.4, rng.choice((0.0, 0.0, 0.1)),
+        kind = rng.choice(("sigmoid", "sigmoid", "hinge", "ipo"))
+        smoothing = rng.choice((0.0, 0.0, 0.1)) if kind == "sigmoid" else 0.0
+        return {k: v for k, v in _pref("", pairs, length, kind, rng.random() < 0.4, smoothing,
                                        rng.random() < 0.8).items() if k != "name"}
     length = _log_int(rng, 2, 4096)
     seqs = _log_int(rng, 1, max(2, min(1024, 2000000 // length)))
