@@ -228,7 +228,8 @@ def _run_own(c, s):
             average=c["average"])
         dlogp = L.lora_preference_loss_bwd(coef, s["cu"], s["n"], mask=s["mask"], dloss=s["dloss"])
         return {"loss": loss, "pair_loss": pair_loss, "rewards": rewards, "dlogp": dlogp}
-    args = dict(old_logp=s["old"], ref_logp=s["ref"], mask=s["mask"], eps_low=0.2, eps_high=0.28, beta=c["beta"])
+    args = dict(old_logp=s["old"], ref_logp=s["ref"], mask=s["mask"], eps_low=0.2, eps_high=0.28, beta=c["beta"],
+                per_token=c["per_token"])
     loss, stats, weight = L.lora_policy_loss_fwd(s["logp"], s["cu"], s["adv"], reduction=c["reduction"],
                                                  norm=float(c["length"]), **args)
     dlogp = L.lora_policy_loss_bwd(s["logp"], s["cu"], s["adv"], weight, dloss=s["dloss"], **args)
