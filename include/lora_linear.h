@@ -417,6 +417,99 @@ size_t lora_swiglu_workspace_bytes(int backward, int dtype, int64_t M, int64_t d
 int lora_transpose(const void* src, int64_t rows, int64_t cols, void* dst, void* stream);
 
 /*
+ * Log-probabilities of tokens from their logits (the head projection of a
+ * training step: preference and policy losses read them, and their gradient
+ * goes back through the head's LoRA layer).  For row i with target t_i:
+ *     logp_i = tau z_{i,t_i} - log sum_j e^(tau z_{i,j})
+ *     dz_{i,j} = dlogp_i tau (1[j = t_i] - e^(tau z_{i,j}) / sum_k e^(tau z_{i,k}))
+ * logits: [n, vocab] of the dtype, row stride ld >= vocab elements; targets:
+ * int64 [n]; tau = inv_temp, finite and above 0.  A target outside
+ * [0, vocab) names no token: logp is 0 and the row's gradient zeros.  stats
+ * [n, 2] fp32 receives each row's maximum logit m and log sum_j e^(tau (z_j - m))
+ * (their sum tau m + that is the log-sum-exp); the backward takes them back.
+ * Logits of -infinity (masked vocabulary) have probability 0; a row of
+ * -infinities, a +infinity or a NaN gives a NaN.  The backward writes
+ * dlogits [n, vocab] (row stride ld_d) in the dtype; it may be logits itself
+ * (ld_d = ld).  A row whose dlogp is 0, or whose target names no token, is not
+ * read and gets zeros.  Arithmetic is fp32.  Pointers need their element's
+ * alignment only, so rows may be sliced (logits[:-1], targets[1:]).
+ * 0 <= n < 2^31, 1 <= vocab < 2^31.
+ */
+int lora_token_logp_fwd(int dtype, int64_t n, int64_t vocab, const void* logits, int64_t ld, const int64_t* targets,
+                        float inv_temp, float* logp, float* stats, void* stream);
+int lora_token_logp_bwd(int dtype, int64_t n, int64_t vocab, const void* logits, int64_t ld, const int64_t* targets,
+                        float inv_temp, const float* stats, const float* dlogp, void* dlogits, int64_t ld_d,
+                        void* stream);
+
+/*
+ * Losses over packed sequences: n_tokens fp32 values, sequence s being the
+ * tokens [cu[s], cu[s + 1]) (cu: device int64 [n_seq + 1], non-decreasing;
+ * sequences may be empty).  mask: device bytes [n_tokens] (NULL: every token
+ * counts); a token whose byte is 0 counts nowhere, whatever its values.
+ * Tokens outside [cu[0], cu[n_seq]) belong to no sequence.  The host cannot
+ * read cu: offsets outside [0, n_tokens] are taken as the nearer end, and
+ * offsets that decrease give unspecified values but no access outside the
+ * arrays.  Sums over tokens, and what is derived from them, are formed in fp64
+ * in a fixed order.  Pointers need their element's alignment only (ws: 16
+ * bytes, of lora_loss_workspace_bytes).  dloss: device fp32 scalar, the
+ * upstream gradient of the loss (NULL: 1).  The backward writes dlogp for every
+ * token of [0, n_tokens): 0 where it does not count.
+ * 1 <= n_seq <= 2^30, 0 <= n_tokens < 2^40 (with 0 the token arrays may be NULL).
+ */
+enum { LORA_LOSS_PREFERENCE = 0, LORA_LOSS_POLICY = 1 };
+size_t lora_loss_workspace_bytes(int loss, int64_t n_seq, int64_t n_tokens);
+
+/*
+ * Preference loss of `pairs` pairs: sequences 0 .. pairs-1 are the chosen
+ * responses, pairs .. 2 pairs-1 the rejected ones (cu has 2 pairs + 1 entries).
+ *     D_s = sum of logp - ref_logp over the counted tokens of s (over their
+ *           number, if `average`; 0 for a sequence that counts none),
+ *     u = D_chosen - D_rejected,
+ *     SIGMOID: l = (1 - e) softplus(-beta u) + e softplus(beta u)
+ *     HINGE:   l = max(0, 1 - beta u)
+ *     IPO:     l = (u - 1 / (2 beta))^2
+ * and the loss is the mean of l over the pairs.  e = label_smoothing in
+ * [0, 1), 0 but for SIGMOID; beta > 0.  ref_logp NULL: no reference (zeros).
+ * Outputs fp32: loss [1], pair_loss [pairs], rewards [2 pairs] = beta D_s,
+ * coef [2 pairs] = d loss / d logp of a counted token of s, which the backward
+ * spreads over the tokens.
+ */
+enum { LORA_PREF_SIGMOID = 0, LORA_PREF_HINGE = 1, LORA_PREF_IPO = 2 };
+int lora_preference_loss_fwd(int kind, int64_t pairs, int64_t n_tokens, double beta, double label_smoothing,
+                             int average, const int64_t* cu, const uint8_t* mask, const float* logp,
+                             const float* ref_logp, float* loss, float* pair_loss, float* rewards, float* coef,
+                             void* ws, size_t ws_bytes, void* stream);
+int lora_preference_loss_bwd(int64_t pairs, int64_t n_tokens, const int64_t* cu, const uint8_t* mask,
+                             const float* coef, const float* dloss, float* dlogp, void* stream);
+
+/*
+ * Clipped policy loss with a KL term.  Per counted token, with advantage A (of
+ * its sequence, [n_seq], or its own, [n_tokens], if adv_per_token),
+ * x = logp - old_logp (old_logp NULL: 0, the policy that sampled), r = e^x and
+ * d = ref_logp - logp:
+ *     l = -min(r A, clip(r, 1 - eps_low, 1 + eps_high) A) + beta (e^d - d - 1)
+ *     dl / dlogp = (-r A where r A <= the clipped product, else 0) - beta (e^d - 1)
+ * A = 0 leaves the KL term alone.  The clip borders are compared as
+ * x > log(1 + eps_high) and x < log(1 - eps_low) in fp64.  The loss is
+ * sum_t w l with w = 1 / (n_seq T_s) (SEQUENCE: mean over sequences of their
+ * token mean, T_s counted tokens), 1 / sum_s T_s (TOKEN) or 1 / (n_seq norm)
+ * (CONSTANT).  0 <= eps_low <= 1, eps_high >= 0, beta >= 0 (beta > 0 needs
+ * ref_logp; with beta = 0 a ref_logp gives the KL statistic alone).
+ * Outputs fp32: loss [1]; stats [4] = the policy part, the KL part (before
+ * beta), the share of counted tokens whose clipped branch held, their number;
+ * weight [n_seq] = w, which the backward takes back with the same inputs.
+ */
+enum { LORA_POLICY_SEQUENCE = 0, LORA_POLICY_TOKEN = 1, LORA_POLICY_CONSTANT = 2 };
+int lora_policy_loss_fwd(int reduction, int64_t n_seq, int64_t n_tokens, double eps_low, double eps_high, double beta,
+                         double norm, const int64_t* cu, const uint8_t* mask, const float* logp,
+                         const float* old_logp, const float* ref_logp, const float* advantages, int adv_per_token,
+                         float* loss, float* stats, float* weight, void* ws, size_t ws_bytes, void* stream);
+int lora_policy_loss_bwd(int64_t n_seq, int64_t n_tokens, double eps_low, double eps_high, double beta,
+                         const int64_t* cu, const uint8_t* mask, const float* logp, const float* old_logp,
+                         const float* ref_logp, const float* advantages, int adv_per_token, const float* weight,
+                         const float* dloss, float* dlogp, void* stream);
+
+/*
  * Launch profiling (measurement hook, not part of the layer's arithmetic).
  * Between lora_profile_begin and lora_profile_end every kernel the library
  * launches is bracketed by two HIP events on its stream, and the launch's

@@ -29,7 +29,11 @@ from ._lib import (  # noqa: F401
     workspace_bytes,
 )
 from .functional import (  # noqa: F401
+    LoraHeadLogpFunction,
     LoraLinearFunction,
+    LoraPolicyLossFunction,
+    LoraPreferenceLossFunction,
+    LoraTokenLogpFunction,
     lora_dropout_bwd,
     lora_dropout_fwd,
     lora_dropout_mask,
@@ -41,10 +45,16 @@ from .functional import (  # noqa: F401
     lora_linear_fwd,
     lora_linear_fwd_noalloc,
     lora_merge,
+    lora_policy_loss_bwd,
+    lora_policy_loss_fwd,
+    lora_preference_loss_bwd,
+    lora_preference_loss_fwd,
     lora_qk_rope_bwd,
     lora_qk_rope_fwd,
     lora_swiglu_bwd,
     lora_swiglu_fwd,
+    lora_token_logp_bwd,
+    lora_token_logp_fwd,
     lora_transpose,
     nf4_dequant,
     nf4_lora_linear_bwd,

@@ -71,6 +71,14 @@ _SIGS = {
                                  _sz, _vp], _int),
     "lora_dropout_philox_bwd": ([_int, _i64, _i64, _i64, _i64, _f32, _f32, _u64, _u64, _vp, _vp, _vp, _vp, _vp, _vp,
                                  _vp, _vp, _vp, _sz, _vp], _int),
+    "lora_token_logp_fwd": ([_int, _i64, _i64, _vp, _i64, _vp, _f32, _vp, _vp, _vp], _int),
+    "lora_token_logp_bwd": ([_int, _i64, _i64, _vp, _i64, _vp, _f32, _vp, _vp, _vp, _i64, _vp], _int),
+    "lora_loss_workspace_bytes": ([_int, _i64, _i64], _sz),
+    "lora_preference_loss_fwd": ([_int, _i64, _i64, _dbl, _dbl, _int] + [_vp] * 9 + [_sz, _vp], _int),
+    "lora_preference_loss_bwd": ([_i64, _i64] + [_vp] * 6, _int),
+    "lora_policy_loss_fwd": ([_int, _i64, _i64, _dbl, _dbl, _dbl, _dbl] + [_vp] * 6 + [_int] + [_vp] * 4 + [_sz, _vp],
+                             _int),
+    "lora_policy_loss_bwd": ([_i64, _i64, _dbl, _dbl, _dbl] + [_vp] * 6 + [_int] + [_vp] * 4, _int),
     "lora_mfma_rate": ([_int, _int, _vp, _vp], _int),
     "lora_transpose": ([_vp, _i64, _i64, _vp, _vp], _int),
     "lora_profile_begin": ([_int], _int),

@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblora_linear.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["kernels.hip", "api.cpp"]
+SOURCES = ["kernels.hip", "loss.hip", "api.cpp"]
 FLAGS = [
     "--offload-arch=gfx950",
     "-O3",

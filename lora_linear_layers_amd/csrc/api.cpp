@@ -22,6 +22,8 @@ namespace {
 
 constexpr int64_t kMaxRank = 256;
 constexpr int64_t kMaxDim = int64_t(1) << 31;
+constexpr int64_t kMaxTokens = int64_t(1) << 40;  // of a loss over packed sequences
+constexpr int64_t kMaxSeqs = int64_t(1) << 30;
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t rup(int64_t a, int64_t b) { return cdiv(a, b) * b; }
@@ -353,6 +355,21 @@ int check_ptrs(std::initializer_list<const void*> ps) {
   return LORA_OK;
 }
 
+// Pointers that need their element's alignment only (token arrays are often
+// sliced: logits[:-1], targets[1:]).
+struct Elem {
+  const void* p;
+  size_t size;
+};
+int check_elems(std::initializer_list<Elem> es, bool required) {
+  if (required)
+    for (const Elem& e : es)
+      if (!e.p) return LORA_ERR_NULL;
+  for (const Elem& e : es)
+    if (reinterpret_cast<uintptr_t>(e.p) % e.size) return LORA_ERR_ALIGN;
+  return LORA_OK;
+}
+
 int check_ws(const Layout& L, const void* ws, size_t ws_bytes) {
   if (L.total == 0) return LORA_OK;
   if (!ws || ws_bytes < L.total) return LORA_ERR_WORKSPACE;
@@ -392,6 +409,8 @@ enum ProfKind : int {
   K_FEW_FWD,
   K_FEW_BWD,
   K_TINY,
+  K_TOKEN_LOGP,
+  K_LOSS,
   K_PROF_COUNT
 };
 
@@ -414,7 +433,8 @@ const char* kind_name(int k) {
       "split_finish",               "swiglu_elementwise",
       "dropout_mask_copy",          "transpose_w",                "skinny_fwd",
       "few_panel",                  "few_fwd",                    "few_bwd",
-      "tiny_f32"};
+      "tiny_f32",
+      "token_logp",                 "sequence_loss"};
   static_assert(sizeof(names) / sizeof(names[0]) == K_PROF_COUNT, "one name per launch kind");
   return (k >= 0 && k < K_PROF_COUNT) ? names[k] : "unknown";
 }
@@ -1821,6 +1841,152 @@ int lora_transpose(const void* src, int64_t rows, int64_t cols, void* dst, void*
     return launch_transpose_tile(static_cast<const uint16_t*>(src), cols, rows, cols, static_cast<uint16_t*>(dst), rows,
                                  rows, st);
   }));
+  return LORA_OK;
+}
+
+// ---- token log-probabilities ----
+static int check_logp(int dtype, int64_t n, int64_t vocab, int64_t ld, float inv_temp) {
+  if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_ERR_DTYPE;
+  if (n < 0 || n >= kMaxDim || vocab < 1 || vocab >= kMaxDim || ld < vocab || ld >= kMaxDim) return LORA_ERR_SHAPE;
+  if (!(inv_temp > 0.f) || std::isinf(inv_temp)) return LORA_ERR_SHAPE;
+  return LORA_OK;
+}
+
+int lora_token_logp_fwd(int dtype, int64_t n, int64_t vocab, const void* logits, int64_t ld, const int64_t* targets,
+                        float inv_temp, float* logp, float* stats, void* stream) {
+  TRY(check_logp(dtype, n, vocab, ld, inv_temp));
+  const size_t eb = elem_bytes(dtype);
+  if (n > 0) TRY(check_elems({{logits, eb}, {targets, 8}, {logp, 4}, {stats, 4}}, true));
+  TRY(check_device());
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const double el = double(n) * double(vocab);
+  HIPTRY(timed(K_TOKEN_LOGP, 4 * el, el * eb + 20.0 * n, st, [&] {
+    return launch_token_logp((int)eb, logits, ld, n, vocab, targets, inv_temp, logp, stats, st);
+  }));
+  return LORA_OK;
+}
+
+int lora_token_logp_bwd(int dtype, int64_t n, int64_t vocab, const void* logits, int64_t ld, const int64_t* targets,
+                        float inv_temp, const float* stats, const float* dlogp, void* dlogits, int64_t ld_d,
+                        void* stream) {
+  TRY(check_logp(dtype, n, vocab, ld, inv_temp));
+  if (ld_d < vocab || ld_d >= kMaxDim || (dlogits == logits && ld_d != ld)) return LORA_ERR_SHAPE;
+  const size_t eb = elem_bytes(dtype);
+  if (n > 0) TRY(check_elems({{logits, eb}, {targets, 8}, {stats, 4}, {dlogp, 4}, {dlogits, eb}}, true));
+  TRY(check_device());
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const double el = double(n) * double(vocab);
+  HIPTRY(timed(K_TOKEN_LOGP, 4 * el, 2 * el * eb + 20.0 * n, st, [&] {
+    return launch_token_logp_grad((int)eb, logits, ld, n, vocab, targets, inv_temp, stats, dlogp, dlogits, ld_d, st);
+  }));
+  return LORA_OK;
+}
+
+// ---- losses over packed sequences ----
+static int check_seqs(int64_t n_seq, int64_t n_tokens, const int64_t* cu) {
+  if (n_seq < 1 || n_seq > kMaxSeqs || n_tokens < 0 || n_tokens >= kMaxTokens) return LORA_ERR_SHAPE;
+  return check_elems({{cu, 8}}, true);
+}
+
+static int check_loss_ws(int nv, int64_t n_seq, int64_t n_tokens, const void* ws, size_t ws_bytes) {
+  if (!ws || ws_bytes < loss_workspace(n_seq, n_tokens, nv)) return LORA_ERR_WORKSPACE;
+  return aligned16(ws) ? LORA_OK : LORA_ERR_ALIGN;
+}
+
+size_t lora_loss_workspace_bytes(int loss, int64_t n_seq, int64_t n_tokens) {
+  if ((loss != LORA_LOSS_PREFERENCE && loss != LORA_LOSS_POLICY) || n_seq < 1 || n_seq > kMaxSeqs || n_tokens < 0 ||
+      n_tokens >= kMaxTokens)
+    return 0;
+  return loss_workspace(n_seq, n_tokens, loss == LORA_LOSS_PREFERENCE ? 2 : 4);
+}
+
+int lora_preference_loss_fwd(int kind, int64_t pairs, int64_t n_tokens, double beta, double label_smoothing,
+                             int average, const int64_t* cu, const uint8_t* mask, const float* logp,
+                             const float* ref_logp, float* loss, float* pair_loss, float* rewards, float* coef,
+                             void* ws, size_t ws_bytes, void* stream) {
+  if (kind < LORA_PREF_SIGMOID || kind > LORA_PREF_IPO || pairs < 1 || pairs > kMaxSeqs / 2) return LORA_ERR_SHAPE;
+  if (!(beta > 0.0) || std::isinf(beta)) return LORA_ERR_SHAPE;
+  if (!(label_smoothing >= 0.0 && label_smoothing < 1.0) || (kind != LORA_PREF_SIGMOID && label_smoothing != 0.0))
+    return LORA_ERR_SHAPE;
+  TRY(check_seqs(2 * pairs, n_tokens, cu));
+  if (n_tokens > 0) TRY(check_elems({{logp, 4}}, true));
+  TRY(check_elems({{ref_logp, 4}}, false));
+  TRY(check_elems({{loss, 4}, {pair_loss, 4}, {rewards, 4}, {coef, 4}}, true));
+  TRY(check_loss_ws(2, 2 * pairs, n_tokens, ws, ws_bytes));
+  TRY(check_device());
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const LossSeqs q{cu, mask, 2 * pairs, n_tokens};
+  const PrefLossArgs l{logp, ref_logp, kind, average ? 1 : 0, beta, label_smoothing, loss, pair_loss, rewards, coef};
+  const double N = double(n_tokens);
+  HIPTRY(timed(K_LOSS, 3 * N, N * (4 + (ref_logp ? 4 : 0) + (mask ? 1 : 0)) + 36.0 * pairs, st,
+               [&] { return launch_pref_loss(q, l, ws, st); }));
+  return LORA_OK;
+}
+
+int lora_preference_loss_bwd(int64_t pairs, int64_t n_tokens, const int64_t* cu, const uint8_t* mask,
+                             const float* coef, const float* dloss, float* dlogp, void* stream) {
+  if (pairs < 1 || pairs > kMaxSeqs / 2) return LORA_ERR_SHAPE;
+  TRY(check_seqs(2 * pairs, n_tokens, cu));
+  TRY(check_elems({{coef, 4}}, true));
+  if (n_tokens > 0) TRY(check_elems({{dlogp, 4}}, true));
+  TRY(check_elems({{dloss, 4}}, false));
+  TRY(check_device());
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const LossSeqs q{cu, mask, 2 * pairs, n_tokens};
+  HIPTRY(timed(K_LOSS, double(n_tokens), double(n_tokens) * (4 + (mask ? 1 : 0)) + 24.0 * pairs, st,
+               [&] { return launch_pref_grad(q, coef, dloss, dlogp, st); }));
+  return LORA_OK;
+}
+
+static int check_policy(int reduction, int64_t n_seq, int64_t n_tokens, double eps_low, double eps_high, double beta,
+                        double norm, const int64_t* cu, const float* logp, const float* old_logp, const float* ref_logp,
+                        const float* advantages) {
+  if (reduction < LORA_POLICY_SEQUENCE || reduction > LORA_POLICY_CONSTANT) return LORA_ERR_SHAPE;
+  if (!(eps_low >= 0.0 && eps_low <= 1.0) || !(eps_high >= 0.0) || std::isinf(eps_high)) return LORA_ERR_SHAPE;
+  if (!(beta >= 0.0) || std::isinf(beta)) return LORA_ERR_SHAPE;
+  if (reduction == LORA_POLICY_CONSTANT && (!(norm > 0.0) || std::isinf(norm))) return LORA_ERR_SHAPE;
+  TRY(check_seqs(n_seq, n_tokens, cu));
+  if (n_tokens > 0) TRY(check_elems({{logp, 4}, {advantages, 4}}, true));
+  if (beta > 0.0 && n_tokens > 0 && !ref_logp) return LORA_ERR_NULL;
+  return check_elems({{old_logp, 4}, {ref_logp, 4}}, false);
+}
+
+int lora_policy_loss_fwd(int reduction, int64_t n_seq, int64_t n_tokens, double eps_low, double eps_high, double beta,
+                         double norm, const int64_t* cu, const uint8_t* mask, const float* logp,
+                         const float* old_logp, const float* ref_logp, const float* advantages, int adv_per_token,
+                         float* loss, float* stats, float* weight, void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_policy(reduction, n_seq, n_tokens, eps_low, eps_high, beta, norm, cu, logp, old_logp, ref_logp,
+                   advantages));
+  TRY(check_elems({{loss, 4}, {stats, 4}, {weight, 4}}, true));
+  TRY(check_loss_ws(4, n_seq, n_tokens, ws, ws_bytes));
+  TRY(check_device());
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const LossSeqs q{cu, mask, n_seq, n_tokens};
+  const PolicyLossArgs l{logp, old_logp, ref_logp, advantages, adv_per_token ? 1 : 0, reduction, eps_low, eps_high,
+                         beta, norm, loss, stats, weight};
+  const double N = double(n_tokens);
+  HIPTRY(timed(K_LOSS, 20 * N, N * (4 + (old_logp ? 4 : 0) + (ref_logp ? 4 : 0) + (adv_per_token ? 4 : 0) + (mask ? 1 : 0)) + 16.0 * n_seq,
+               st, [&] { return launch_policy_loss(q, l, ws, st); }));
+  return LORA_OK;
+}
+
+int lora_policy_loss_bwd(int64_t n_seq, int64_t n_tokens, double eps_low, double eps_high, double beta,
+                         const int64_t* cu, const uint8_t* mask, const float* logp, const float* old_logp,
+                         const float* ref_logp, const float* advantages, int adv_per_token, const float* weight,
+                         const float* dloss, float* dlogp, void* stream) {
+  TRY(check_policy(LORA_POLICY_SEQUENCE, n_seq, n_tokens, eps_low, eps_high, beta, 1.0, cu, logp, old_logp, ref_logp,
+                   advantages));
+  TRY(check_elems({{weight, 4}}, true));
+  if (n_tokens > 0) TRY(check_elems({{dlogp, 4}}, true));
+  TRY(check_elems({{dloss, 4}}, false));
+  TRY(check_device());
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const LossSeqs q{cu, mask, n_seq, n_tokens};
+  const PolicyLossArgs l{logp, old_logp, ref_logp, advantages, adv_per_token ? 1 : 0, 0, eps_low, eps_high,
+                         beta, 1.0, nullptr, nullptr, const_cast<float*>(weight)};
+  const double N = double(n_tokens);
+  HIPTRY(timed(K_LOSS, 20 * N, N * (8 + (old_logp ? 4 : 0) + (ref_logp ? 4 : 0) + (adv_per_token ? 4 : 0) + (mask ? 1 : 0)) + 12.0 * n_seq,
+               st, [&] { return launch_policy_grad(q, l, dloss, dlogp, st); }));
   return LORA_OK;
 }
 

@@ -212,4 +212,52 @@ hipError_t launch_few_reduce(const FewArgs& a, hipStream_t st);  // backward: P_
 hipError_t launch_few_fwd(const FewArgs& a, int MB, bool nf4, hipStream_t st);
 hipError_t launch_few_bwd(const FewArgs& a, int MB, bool nf4, hipStream_t st);
 
+// Token log-probabilities (loss.hip): logp [rows] and stats [rows, 2] (row
+// maximum, log of the row's sum) from logits z [rows, V] (row stride ld, bf16
+// or fp32), and dz (row stride ldd) from dlogp [rows].  V < 2^31; a target
+// outside [0, V) gives logp 0 and a zero gradient row.
+hipError_t launch_token_logp(int elem_bytes, const void* z, int64_t ld, int64_t rows, int64_t V, const int64_t* target,
+                             float tau, float* logp, float* stats, hipStream_t st);
+hipError_t launch_token_logp_grad(int elem_bytes, const void* z, int64_t ld, int64_t rows, int64_t V,
+                                  const int64_t* target, float tau, const float* stats, const float* dlogp, void* dz,
+                                  int64_t ldd, hipStream_t st);
+
+// Losses over S packed sequences of N tokens (loss.hip): cu int64 [S + 1],
+// mask [N] or NULL.  The forward's workspace is loss_workspace(S, N, nv) bytes
+// (nv: 2 preference, 4 policy), 16-byte aligned.
+constexpr int64_t SEQ_SMALL = 8192;  // tokens up to which one block runs the whole forward
+struct LossSeqs {
+  const int64_t* cu;
+  const uint8_t* mask;
+  int64_t S, N;
+};
+struct PrefLossArgs {
+  const float* logp;
+  const float* ref;
+  int kind, average;
+  double beta, eps;
+  float* loss;
+  float* pair_loss;
+  float* rewards;
+  float* coef;
+};
+struct PolicyLossArgs {
+  const float* logp;
+  const float* old;
+  const float* ref;
+  const float* adv;
+  int adv_per_token, reduction;
+  double eps_low, eps_high, beta, norm;
+  float* loss;
+  float* stats;
+  float* weight;
+};
+int loss_chunk(int64_t N);
+size_t loss_workspace(int64_t S, int64_t N, int nv);
+hipError_t launch_pref_loss(const LossSeqs& q, const PrefLossArgs& l, void* ws, hipStream_t st);
+hipError_t launch_pref_grad(const LossSeqs& q, const float* coef, const float* dloss, float* dlogp, hipStream_t st);
+hipError_t launch_policy_loss(const LossSeqs& q, const PolicyLossArgs& l, void* ws, hipStream_t st);
+hipError_t launch_policy_grad(const LossSeqs& q, const PolicyLossArgs& l, const float* dloss, float* dlogp,
+                              hipStream_t st);
+
 }  // namespace lora

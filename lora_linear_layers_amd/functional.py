@@ -10,7 +10,10 @@ scale is s = alpha / r.  dA and dB come back in fp32.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib as L
 
@@ -438,3 +441,253 @@ class LoraLinearFunction(torch.autograd.Function):
         X, W, A, B = ctx.saved_tensors
         dX, dA, dB = lora_linear_bwd(X, W, A, B, ctx.scale, dY.contiguous(), need_dX=ctx.needs_input_grad[0])
         return dX, None, dA.to(A.dtype), dB.to(B.dtype), None
+
+
+# ---------------------------------------------------------------------------
+# token log-probabilities and the losses that read them
+# ---------------------------------------------------------------------------
+def _on(t):
+    """The device of t made current where it is not (launches go to the current device)."""
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _check_on(first, *named):
+    """Every (name, tensor or None, dtypes, numel or None): on first's GPU, contiguous, of a dtype and size."""
+    if not first.is_cuda:
+        raise ValueError("tensors must be on a GPU")
+    for name, t, dtypes, numel in named:
+        if t is None:
+            continue
+        if t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name} has dtype {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        if numel is not None and t.numel() != numel:
+            raise ValueError(f"{name} has {t.numel()} values, not {numel}")
+
+
+_F32, _I64, _MASK = (torch.float32,), (torch.int64,), (torch.bool, torch.uint8)
+
+
+def _logits_ld(name, z):
+    if z.dim() != 2:
+        raise ValueError(f"{name} must be [n, vocab]")
+    n, vocab = z.shape
+    if vocab > 1 and z.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return n, vocab, (z.stride(0) if n > 1 else vocab)
+
+
+def lora_token_logp_fwd(logits, targets, inv_temp: float = 1.0):
+    """(logp fp32 [n], stats fp32 [n, 2]) of int64 targets [n] under the rows of logits [n, vocab] (rows may be
+    strided); stats holds each row's maximum logit and the log of its shifted sum, which the backward takes."""
+    n, vocab, ld = _logits_ld("logits", logits)
+    _check_on(logits, ("targets", targets, _I64, n))
+    dt = L._dtype_code(logits)
+    logp = torch.empty(n, dtype=torch.float32, device=logits.device)
+    stats = torch.empty(n, 2, dtype=torch.float32, device=logits.device)
+    with _on(logits):
+        L._check("lora_token_logp_fwd", L.lib().lora_token_logp_fwd(
+            dt, n, vocab, L._ptr(logits), ld, L._ptr(targets), float(inv_temp), L._ptr(logp), L._ptr(stats),
+            L._stream(logits.device)))
+    return logp, stats
+
+
+def lora_token_logp_bwd(logits, targets, stats, dlogp, inv_temp: float = 1.0, dlogits=None):
+    """dlogits in the dtype of logits for the upstream gradient dlogp fp32 [n]; dlogits may be logits itself."""
+    n, vocab, ld = _logits_ld("logits", logits)
+    _check_on(logits, ("targets", targets, _I64, n), ("stats", stats, _F32, 2 * n), ("dlogp", dlogp, _F32, n))
+    dt = L._dtype_code(logits)
+    if dlogits is None:
+        dlogits = torch.empty(n, vocab, dtype=logits.dtype, device=logits.device)
+    nd, vd, ldd = _logits_ld("dlogits", dlogits)
+    if (nd, vd) != (n, vocab) or dlogits.dtype != logits.dtype or dlogits.device != logits.device:
+        raise ValueError("dlogits must have the shape, dtype and device of logits")
+    with _on(logits):
+        L._check("lora_token_logp_bwd", L.lib().lora_token_logp_bwd(
+            dt, n, vocab, L._ptr(logits), ld, L._ptr(targets), float(inv_temp), L._ptr(stats), L._ptr(dlogp),
+            L._ptr(dlogits), ldd, L._stream(logits.device)))
+    return dlogits
+
+
+def _loss_ws(loss, n_seq, n_tokens, device, ws):
+    if ws is not None:
+        return ws  # the library checks its size
+    return torch.empty(int(L.lib().lora_loss_workspace_bytes(loss, n_seq, n_tokens)), dtype=torch.uint8, device=device)
+
+
+PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}
+POLICY_REDUCTIONS = {"sequence": 0, "token": 1, "constant": 2}
+
+
+def _choice(name, table, value):
+    if value not in table:
+        raise ValueError(f"{name} must be one of {', '.join(table)}")
+    return table[value]
+
+
+def lora_preference_loss_fwd(logp, cu, beta: float, ref_logp=None, mask=None, kind: str = "sigmoid",
+                             label_smoothing: float = 0.0, average: bool = False, ws=None):
+    """(loss, pair_loss [P], rewards [2 P], coef [2 P]) of P pairs over packed sequences: logp (and ref_logp) fp32
+    [n], cu int64 [2 P + 1] with the chosen responses first, then the rejected ones in the same order; mask bool or
+    uint8 [n] (tokens that count).  coef goes to lora_preference_loss_bwd."""
+    n = logp.numel()
+    _check_on(logp, ("logp", logp, _F32, n), ("cu", cu, _I64, None), ("ref_logp", ref_logp, _F32, n),
+              ("mask", mask, _MASK, n))
+    if cu.numel() < 3 or cu.numel() % 2 == 0:
+        raise ValueError("cu must hold 2 P + 1 offsets")
+    P = (cu.numel() - 1) // 2
+    new = lambda *s: torch.empty(*s, dtype=torch.float32, device=logp.device)  # noqa: E731
+    loss, pair_loss, rewards, coef = new(()), new(P), new(2 * P), new(2 * P)
+    ws = _loss_ws(0, 2 * P, n, logp.device, ws)
+    with _on(logp):
+        L._check("lora_preference_loss_fwd", L.lib().lora_preference_loss_fwd(
+            _choice("kind", PREFERENCE_KINDS, kind), P, n, float(beta), float(label_smoothing), int(average),
+            L._ptr(cu), L._ptr(mask), L._ptr(logp), L._ptr(ref_logp), L._ptr(loss), L._ptr(pair_loss),
+            L._ptr(rewards), L._ptr(coef), L._ptr(ws), ws.numel(), L._stream(logp.device)))
+    return loss, pair_loss, rewards, coef
+
+
+def lora_preference_loss_bwd(coef, cu, n_tokens: int, mask=None, dloss=None):
+    """dlogp fp32 [n_tokens] of lora_preference_loss_fwd; dloss: fp32 scalar tensor (None: 1)."""
+    _check_on(coef, ("coef", coef, _F32, cu.numel() - 1), ("cu", cu, _I64, None), ("mask", mask, _MASK, n_tokens),
+              ("dloss", dloss, _F32, 1))
+    dlogp = torch.empty(n_tokens, dtype=torch.float32, device=coef.device)
+    with _on(coef):
+        L._check("lora_preference_loss_bwd", L.lib().lora_preference_loss_bwd(
+            coef.numel() // 2, n_tokens, L._ptr(cu), L._ptr(mask), L._ptr(coef), L._ptr(dloss), L._ptr(dlogp),
+            L._stream(coef.device)))
+    return dlogp
+
+
+def _policy_checks(logp, cu, advantages, old_logp, ref_logp, mask, per_token, more=()):
+    n, S = logp.numel(), cu.numel() - 1
+    if S < 1:
+        raise ValueError("cu must hold S + 1 offsets")
+    _check_on(logp, ("logp", logp, _F32, n), ("cu", cu, _I64, None),
+              ("advantages", advantages, _F32, n if per_token else S), ("old_logp", old_logp, _F32, n),
+              ("ref_logp", ref_logp, _F32, n), ("mask", mask, _MASK, n), *more)
+    return n, S
+
+
+def lora_policy_loss_fwd(logp, cu, advantages, old_logp=None, ref_logp=None, mask=None, eps_low: float = 0.2,
+                         eps_high: float = 0.2, beta: float = 0.0, reduction: str = "sequence", norm: float = 1.0,
+                         per_token: bool = False, ws=None):
+    """(loss, stats [4], weight [S]) of the clipped policy loss over packed sequences: logp (old_logp, ref_logp)
+    fp32 [n], cu int64 [S + 1], advantages fp32 [S], or [n] with per_token; stats: the policy part, the KL part, the share of
+    clipped tokens, the number of tokens.  weight goes to lora_policy_loss_bwd."""
+    n, S = _policy_checks(logp, cu, advantages, old_logp, ref_logp, mask, per_token)
+    new = lambda *s: torch.empty(*s, dtype=torch.float32, device=logp.device)  # noqa: E731
+    loss, stats, weight = new(()), new(4), new(S)
+    ws = _loss_ws(1, S, n, logp.device, ws)
+    with _on(logp):
+        L._check("lora_policy_loss_fwd", L.lib().lora_policy_loss_fwd(
+            _choice("reduction", POLICY_REDUCTIONS, reduction), S, n, float(eps_low), float(eps_high), float(beta),
+            float(norm), L._ptr(cu), L._ptr(mask), L._ptr(logp), L._ptr(old_logp), L._ptr(ref_logp),
+            L._ptr(advantages), int(per_token), L._ptr(loss), L._ptr(stats), L._ptr(weight), L._ptr(ws), ws.numel(),
+            L._stream(logp.device)))
+    return loss, stats, weight
+
+
+def lora_policy_loss_bwd(logp, cu, advantages, weight, old_logp=None, ref_logp=None, mask=None, eps_low: float = 0.2,
+                         eps_high: float = 0.2, beta: float = 0.0, per_token: bool = False,
+                         dloss=None):
+    """dlogp fp32 [n] of lora_policy_loss_fwd, given its weight and the same inputs; dloss: fp32 scalar tensor."""
+    n, S = _policy_checks(logp, cu, advantages, old_logp, ref_logp, mask, per_token,
+                          (("dloss", dloss, _F32, 1), ("weight", weight, _F32, cu.numel() - 1)))
+    dlogp = torch.empty(n, dtype=torch.float32, device=logp.device)
+    with _on(logp):
+        L._check("lora_policy_loss_bwd", L.lib().lora_policy_loss_bwd(
+            S, n, float(eps_low), float(eps_high), float(beta), L._ptr(cu), L._ptr(mask), L._ptr(logp),
+            L._ptr(old_logp), L._ptr(ref_logp), L._ptr(advantages), int(per_token), L._ptr(weight), L._ptr(dloss),
+            L._ptr(dlogp), L._stream(logp.device)))
+    return dlogp
+
+
+def _f32c(t):
+    return t.to(torch.float32).contiguous()
+
+
+class LoraTokenLogpFunction(torch.autograd.Function):
+    """logp = LoraTokenLogpFunction.apply(logits, targets, inv_temp); gradient for logits."""
+
+    @staticmethod
+    def forward(ctx, logits, targets, inv_temp=1.0):
+        logp, stats = lora_token_logp_fwd(logits, targets, inv_temp)
+        ctx.save_for_backward(logits, targets, stats)
+        ctx.inv_temp = inv_temp
+        return logp
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dlogp):
+        logits, targets, stats = ctx.saved_tensors
+        return lora_token_logp_bwd(logits, targets, stats, _f32c(dlogp), ctx.inv_temp), None, None
+
+
+class LoraHeadLogpFunction(torch.autograd.Function):
+    """logp = LoraHeadLogpFunction.apply(X, W, A, B, scale, targets, inv_temp): the log-probabilities of targets under
+    a LoRA head projection (W [vocab, d_in] frozen), the logits kept in X's dtype between the two; gradients for
+    X, A and B."""
+
+    @staticmethod
+    def forward(ctx, X, W, A, B, scale, targets, inv_temp=1.0):
+        logits = lora_linear_fwd(X, W, A, B, scale)
+        logp, stats = lora_token_logp_fwd(logits, targets, inv_temp)
+        ctx.save_for_backward(X, W, A, B, logits, targets, stats)
+        ctx.scale, ctx.inv_temp = scale, inv_temp
+        return logp
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dlogp):
+        X, W, A, B, logits, targets, stats = ctx.saved_tensors
+        dlogits = lora_token_logp_bwd(logits, targets, stats, _f32c(dlogp), ctx.inv_temp)
+        dX, dA, dB = lora_linear_bwd(X, W, A, B, ctx.scale, dlogits, need_dX=ctx.needs_input_grad[0])
+        return dX, None, dA.to(A.dtype), dB.to(B.dtype), None, None, None
+
+
+class LoraPreferenceLossFunction(torch.autograd.Function):
+    """(loss, pair_loss, rewards) = LoraPreferenceLossFunction.apply(logp, ref_logp, cu, mask, beta, kind,
+    label_smoothing, average); gradient of loss for logp (the reference is frozen, the other outputs are for logs)."""
+
+    @staticmethod
+    def forward(ctx, logp, ref_logp, cu, mask, beta, kind="sigmoid", label_smoothing=0.0, average=False):
+        loss, pair_loss, rewards, coef = lora_preference_loss_fwd(logp, cu, beta, ref_logp, mask, kind,
+                                                                  label_smoothing, average)
+        ctx.save_for_backward(cu, mask, coef)
+        ctx.n = logp.numel()
+        ctx.mark_non_differentiable(pair_loss, rewards)
+        return loss, pair_loss, rewards
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss, *_):
+        cu, mask, coef = ctx.saved_tensors
+        return (lora_preference_loss_bwd(coef, cu, ctx.n, mask, _f32c(dloss)),) + (None,) * 7
+
+
+class LoraPolicyLossFunction(torch.autograd.Function):
+    """(loss, stats) = LoraPolicyLossFunction.apply(logp, old_logp, ref_logp, cu, advantages, mask, eps_low, eps_high,
+    beta, reduction, norm, per_token); gradient of loss for logp."""
+
+    @staticmethod
+    def forward(ctx, logp, old_logp, ref_logp, cu, advantages, mask, eps_low=0.2, eps_high=0.2, beta=0.0,
+                reduction="sequence", norm=1.0, per_token=False):
+        loss, stats, weight = lora_policy_loss_fwd(logp, cu, advantages, old_logp, ref_logp, mask, eps_low, eps_high,
+                                                   beta, reduction, norm, per_token)
+        ctx.save_for_backward(logp, old_logp, ref_logp, cu, advantages, mask, weight)
+        ctx.args = dict(eps_low=eps_low, eps_high=eps_high, beta=beta, per_token=per_token)
+        ctx.mark_non_differentiable(stats)
+        return loss, stats
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss, *_):
+        logp, old_logp, ref_logp, cu, advantages, mask, weight = ctx.saved_tensors
+        d = lora_policy_loss_bwd(logp, cu, advantages, weight, old_logp, ref_logp, mask, dloss=_f32c(dloss), **ctx.args)
+        return (d,) + (None,) * 11

@@ -1,0 +1,262 @@
+"""Token log-probabilities and their gradient against the definition in 64
+bits, element by element.
+
+Tolerances (u = 2^-24, one fp32 rounding is off by at most u): an exponential
+is off by at most (3 |arg| + 4) u relative (the shifted logit, its product with
+tau log2 e, the exponential itself); a row's sum of n = V / threads terms a
+thread and the joins of its threads by (n + 24) u more, never fewer than 64
+threads.  So log s is off by at most u (V / 64 + 24 + 3 D + 4) + 2 u |log s|,
+D = max |tau (z - m)| over the terms that count (e^-D s above 2^-24: D < 40),
+and logp by that plus 3 u |tau (z_t - m)|.  A gradient element g (1[j=t] - p)
+is off by |g| p times p's relative error, plus one rounding of each of the two
+products and the difference, plus the output's rounding (half its eps), plus
+|g| 2^-126 where p is below the normals."""
+import numpy as np
+import pytest
+import torch
+
+U = 2.0 ** -24
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+
+
+def _plain(z, t, tau, g=None):
+    """logp, m, log s (and dz) in 64 bits on the CPU."""
+    z = z.detach().cpu().double()
+    t = t.cpu()
+    V = z.shape[1]
+    m = z.amax(1)
+    s = torch.exp((z - m[:, None]) * tau).sum(1)
+    has = (t >= 0) & (t < V)
+    at = torch.where(has, t, torch.zeros_like(t))
+    zt = z.gather(1, at[:, None]).squeeze(1)
+    logp = torch.where(has, (zt - m) * tau - s.log(), torch.zeros_like(m))
+    if g is None:
+        return logp, m, s.log()
+    g = torch.where(has, g.cpu().double(), torch.zeros_like(m)) * tau
+    p = torch.exp((z - m[:, None]) * tau - s.log()[:, None])
+    dz = -g[:, None] * p
+    dz[torch.arange(len(t)), at] += g
+    return logp, m, s.log(), torch.where(g[:, None] == 0, torch.zeros_like(dz), dz), p, g
+
+
+def _inputs(seed, n, V, dtype, ignored=True):
+    r = torch.Generator().manual_seed(seed)
+    z = (torch.randn(n, V, generator=r) * 2.5).to(dtype)
+    t = torch.randint(0, V, (n,), generator=r)
+    z[torch.arange(n), t] += (torch.rand(n, generator=r) * 16).to(dtype)
+    if ignored and n > 2:
+        t[n // 3] = -100
+        t[n // 2] = V
+    return z.cuda(), t.cuda(), torch.randn(n, generator=r).cuda()
+
+
+def _check(lib, z, t, g, tau, out=None):
+    V = z.shape[1]
+    z0 = z.clone()
+    logp, stats = lib.lora_token_logp_fwd(z, t, tau)
+    dz = lib.lora_token_logp_bwd(z, t, stats, g, tau, dlogits=out)
+    torch.cuda.synchronize()
+    lp, m, ls, d, p, gt = _plain(z0, t, tau, g)
+    assert torch.equal(stats[:, 0].cpu().double(), m)
+    tol_s = U * (V / 64 + 24 + 3 * 40 + 4 + 2 * ls.abs())
+    assert ((stats[:, 1].cpu().double() - ls).abs() <= tol_s).all()
+    tol = tol_s + 3 * U * (lp + ls).abs() + U * lp.abs()
+    assert ((logp.cpu().double() - lp).abs() <= tol).all()
+    arg = ((z0.cpu().double() - m[:, None]) * tau).abs().clamp(max=200) + ls[:, None].abs()
+    rel_p = U * (3 * arg + 8) + tol_s[:, None]
+    tol_d = gt.abs()[:, None] * (p * rel_p + 3 * U * (p + 1.0 * (d > 0))) + HALF[z.dtype] * d.abs()
+    # the hardware exponential flushes p below the smallest normal 2^-126 to 0: |g| p is then at most |g| 2^-126
+    # off, and an output below 2^-126 may be flushed itself
+    tol_d = tol_d + (gt.abs()[:, None] + 1) * 2.0 ** -126
+    err = (dz.cpu().double() - d).abs()
+    assert (err <= tol_d).all(), (err - tol_d).max()
+    return dz
+
+
+SHAPES = [(1, 1), (1, 7), (3, 64), (5, 255), (2, 2048), (3, 2049), (24, 32000), (2, 50001), (1100, 2500), (1, 128000)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES, ids=[f"{n}x{v}" for n, v in SHAPES])
+def test_logp_parity(lib, shape, dtype):
+    n, V = shape
+    z, t, g = _inputs(11 + n + V, n, V, dtype)
+    _check(lib, z, t, g, 1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tau", [0.7, 1.25, 8.0])
+def test_logp_temperature(lib, tau):
+    z, t, g = _inputs(5, 9, 1003, torch.float32)
+    _check(lib, z, t, g, tau)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_logp_padded_and_sliced_rows(lib, dtype):
+    # rows of a wider buffer, starting one row and 3 columns in: element alignment only
+    z, t, g = _inputs(6, 10, 1031, dtype)
+    view, tt, gg = z[1:, 3:1004], (t[1:] % 1001).contiguous(), g[1:]
+    keep = z.clone()
+    out = torch.full((9, 1013), 7.0, dtype=dtype, device="cuda")
+    _check(lib, view, tt, gg, 1.0, out=out[:, 5:1006])
+    assert torch.equal(z, keep)  # inputs untouched
+    assert (out[:, :5] == 7).all() and (out[:, 1006:] == 7).all()  # and what lies beside the rows
+    # sliced targets of the whole rows (t[1:] starts 8 bytes into its buffer)
+    _check(lib, z[:-1], t[1:], g[1:], 1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("V", [77, 4099])
+def test_logp_in_place(lib, V, dtype):
+    z, t, g = _inputs(8, 33, V, dtype)
+    _, stats = lib.lora_token_logp_fwd(z, t)
+    apart = lib.lora_token_logp_bwd(z, t, stats, g)
+    lib.lora_token_logp_bwd(z, t, stats, g, dlogits=z)
+    assert torch.equal(z, apart)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_logp_masked_vocabulary(lib, dtype):
+    # columns of -inf and of the type's lowest value have probability 0
+    z, t, g = _inputs(9, 6, 3001, dtype, ignored=False)
+    t = t % 1000
+    z[:, 1000:2000] = -float("inf")
+    z[:, 2000:] = torch.finfo(dtype).min
+    z[2, :1000] = -float("inf")
+    z[2, t[2]] = 0.5  # one finite column
+    lp, stats = lib.lora_token_logp_fwd(z, t)
+    dz = lib.lora_token_logp_bwd(z, t, stats, g)
+    ref, m, ls, d, _, _ = _plain(z, t, 1.0, g)
+    assert torch.equal(stats[:, 0].cpu().double(), m)
+    assert torch.allclose(lp.cpu().double(), ref, rtol=0, atol=2e-5) and lp[2] == 0
+    assert (dz[:, 1000:] == 0).all()
+    assert torch.allclose(dz.cpu().double(), d, rtol=HALF[dtype], atol=1e-5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_logp_not_finite(lib, dtype):
+    z, t, g = _inputs(10, 6, 2500, dtype, ignored=False)
+    z[0] = -float("inf")
+    z[1, 17] = float("nan")
+    z[2, 2499] = float("inf")
+    t[3] = 5
+    z[3, 5] = -float("inf")
+    lp, stats = lib.lora_token_logp_fwd(z, t)
+    dz = lib.lora_token_logp_bwd(z, t, stats, g)
+    assert lp[:3].isnan().all() and lp[3] == -float("inf") and lp[4:].isfinite().all()
+    assert dz[0].isnan().all() and dz[1].isnan().all() and dz[3:].isfinite().all()
+    # rows that carry no gradient are not read
+    t[1], g[0], g[2] = -100, 0.0, 0.0
+    lp, stats = lib.lora_token_logp_fwd(z, t)
+    dz = lib.lora_token_logp_bwd(z, t, stats, g)
+    assert lp[1] == 0 and (dz[:3] == 0).all() and dz[3:].isfinite().all()
+
+
+@pytest.mark.gpu
+def test_logp_no_rows(lib):
+    z = torch.empty(0, 50, dtype=torch.bfloat16, device="cuda")
+    t = torch.empty(0, dtype=torch.int64, device="cuda")
+    lp, stats = lib.lora_token_logp_fwd(z, t)
+    assert lp.shape == (0,) and stats.shape == (0, 2)
+    assert lib.lora_token_logp_bwd(z, t, stats, lp).shape == (0, 50)
+
+
+@pytest.mark.gpu
+def test_logp_offsets_past_32_bits(lib):
+    # 2^32 elements and more: rows at both ends against the same rows alone
+    n, V = 33100, 130003
+    z = torch.empty(n, V, dtype=torch.bfloat16, device="cuda")
+    rows = [0, 1, 16517, 33036, n - 1]
+    z.zero_()
+    small, t_s, g_s = _inputs(12, len(rows), V, torch.bfloat16, ignored=False)
+    t = torch.zeros(n, dtype=torch.int64, device="cuda")
+    g = torch.zeros(n, device="cuda")
+    for k, r in enumerate(rows):
+        z[r], t[r], g[r] = small[k], t_s[k], g_s[k]
+    lp, stats = lib.lora_token_logp_fwd(z, t)
+    lp_s, stats_s = lib.lora_token_logp_fwd(small, t_s)
+    at = torch.tensor(rows, device="cuda")
+    # (the few rows run with other threads a row: sums in another order)
+    assert torch.equal(stats[at, 0], stats_s[:, 0]) and torch.allclose(lp[at], lp_s, rtol=0, atol=1e-4)
+    dz = lib.lora_token_logp_bwd(z, t, stats, g)
+    assert torch.equal(dz[at], lib.lora_token_logp_bwd(small, t_s, stats[at], g_s))
+    assert (dz[2] == 0).all() and (dz[n - 2] == 0).all()
+
+
+@pytest.mark.gpu
+def test_logp_function_gradient_against_differences(lib):
+    # d/dz of sum g logp: central differences of the 64-bit definition at the same point
+    z, t, g = _inputs(13, 3, 11, torch.float32, ignored=False)
+    leaf = z.clone().requires_grad_()
+    lib.LoraTokenLogpFunction.apply(leaf, t, 0.9).backward(g)
+    z64, h = z.cpu().double(), 1e-5
+    for i in range(3):
+        for j in range(11):
+            up, dn = z64.clone(), z64.clone()
+            up[i, j] += h
+            dn[i, j] -= h
+            num = ((_plain(up, t, 0.9)[0] - _plain(dn, t, 0.9)[0]) * g.cpu().double()).sum() / (2 * h)
+            assert abs(float(leaf.grad[i, j]) - float(num)) <= 1e-5 * (1 + abs(float(num)))
+
+
+@pytest.mark.gpu
+def test_logp_on_another_stream_and_captured(lib):
+    z, t, g = _inputs(14, 40, 3000, torch.bfloat16)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    want = lib.lora_token_logp_fwd(z, t)
+    dwant = lib.lora_token_logp_bwd(z, t, want[1], g)
+    with torch.cuda.stream(st):
+        got = lib.lora_token_logp_fwd(z, t)
+        lib.lora_token_logp_bwd(z, t, got[1], g)
+    torch.cuda.synchronize()
+    assert torch.equal(want[0], got[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        glp, gst = lib.lora_token_logp_fwd(z, t)
+        gdz = lib.lora_token_logp_bwd(z, t, gst, g)
+    for k in range(3):
+        z.copy_(torch.roll(z, 1, 0))
+        t.copy_(torch.roll(t, 1, 0))
+        want = lib.lora_token_logp_fwd(z, t)
+        dwant = lib.lora_token_logp_bwd(z, t, want[1], g)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(glp, want[0]) and torch.equal(gdz, dwant)
+
+
+def test_logp_refusals():
+    import lora_linear_layers_amd as L
+
+    z, t = torch.zeros(4, 8), torch.zeros(4, dtype=torch.int64)
+    with pytest.raises(ValueError, match="GPU"):
+        L.lora_token_logp_fwd(z, t)
+    with pytest.raises(ValueError, match="vocab"):
+        L.lora_token_logp_fwd(z.view(-1), t)
+    with pytest.raises(ValueError, match="rows"):
+        L.lora_token_logp_fwd(z.t(), t)
+    lib = L.lib()
+    P = 0x100000
+
+    def fwd(dtype=1, n=4, V=8, z=P, ld=8, t=P, tau=1.0, lp=P, st=P):
+        return lib.lora_token_logp_fwd(dtype, n, V, z, ld, t, tau, lp, st, None)
+
+    def bwd(dtype=1, n=4, V=8, z=P, ld=8, t=P, tau=1.0, st=P, g=P, dz=P, ldd=8):
+        return lib.lora_token_logp_bwd(dtype, n, V, z, ld, t, tau, st, g, dz, ldd, None)
+
+    for f in (fwd, bwd):
+        assert f(dtype=2) == -4
+        assert f(n=-1) == -2 and f(V=0) == -2 and f(ld=7) == -2 and f(V=2 ** 31, ld=2 ** 31) == -2
+        assert f(tau=0.0) == -2 and f(tau=-1.0) == -2 and f(tau=float("nan")) == -2 and f(tau=float("inf")) == -2
+        assert f(z=None) == -1 and f(t=None) == -1 and f(st=None) == -1
+        assert f(z=P + 1) == -3 and f(dtype=0, z=P + 2) == -3 and f(t=P + 4) == -3 and f(st=P + 2) == -3
+    assert fwd(lp=None) == -1 and fwd(lp=P + 2) == -3
+    assert bwd(g=None) == -1 and bwd(dz=None) == -1 and bwd(ldd=7) == -2
+    assert bwd(dz=P, z=P, ldd=9) == -2  # in place with another stride
+    if torch.cuda.device_count() == 0:
+        assert fwd(z=P + 2, t=P + 8) == -6  # element alignment is enough: only the device is missing
