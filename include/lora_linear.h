@@ -410,6 +410,50 @@ size_t lora_swiglu_workspace_bytes(int backward, int dtype, int64_t M, int64_t d
                                    const lora_group_member* members);
 
 /*
+ * One projection with bias, activation and residual in its epilogue (page
+ * "Unsloth框架：高效LLM微调与LoRA优化实践", section 3.1: the graph rewriter merges
+ * a linear layer with its neighbours):
+ *     Z = X W^T + s (X A^T) B^T + bias,   Y = act(Z) + residual
+ * Z is activated in fp32 where the product is accumulated; Y is rounded once.
+ * `member` is one lora_group_member (rope = 0; W, or W_nf4 with absmax and
+ * the HOST table16 as in nf4_lora_linear_fwd; W_t as in the group calls); Y is
+ * member->Y.  Activations: RELU max(z, 0), SILU z / (1 + e^-z), GELU
+ * z P(N(0,1) <= z), GELU_TANH z / (1 + e^(-2 u)) with
+ * u = sqrt(2 / pi) (z + 0.044715 z^3).  bias [d_out], residual [M, d_out] and Z
+ * [M, d_out] are of the dtype; each may be NULL.  Z, where given, receives the
+ * pre-activation, which the backward of an activation needs.  residual may be
+ * Y itself (the sum formed in place); Y and Z may be no other input.
+ * Paths, workspace (its own sizing call) and errors as lora_linear_fwd and
+ * nf4_lora_linear_fwd.
+ *
+ * Backward, for member->dY:
+ *     dZ = dY act'(Z)  (rounded to the dtype; dY itself with LORA_ACT_NONE),
+ *     dbias = sum over tokens of dZ,
+ * and dX (NULL: skipped), dA, dB from dZ as lora_linear_bwd; the residual's
+ * gradient is dY.  act and Z are taken from `epilogue` (its bias and residual
+ * are not used).  RELU passes no gradient at 0.  dbias: fp32 [d_out]
+ * (overwritten) or NULL.
+ */
+enum { LORA_ACT_NONE = 0, LORA_ACT_RELU = 1, LORA_ACT_SILU = 2, LORA_ACT_GELU = 3, LORA_ACT_GELU_TANH = 4 };
+typedef struct lora_epilogue {
+  int act;
+  const void* bias;
+  const void* residual;
+  void* Z;
+} lora_epilogue;
+
+int lora_linear_epi_fwd(int dtype, int64_t M, int64_t d_in, const lora_group_member* member,
+                        const lora_epilogue* epilogue, const void* X, const float* table16, void* ws, size_t ws_bytes,
+                        void* stream);
+int lora_linear_epi_bwd(int dtype, int64_t M, int64_t d_in, const lora_group_member* member,
+                        const lora_epilogue* epilogue, const void* X, const float* table16, float* dbias, void* ws,
+                        size_t ws_bytes, void* stream);
+/* Workspace bytes of the two (backward = 0 / 1; act and the member's sizes and
+ * W_nf4 / W_t are read); 0 for invalid arguments. */
+size_t lora_linear_epi_workspace_bytes(int backward, int dtype, int64_t M, int64_t d_in,
+                                       const lora_group_member* member, const lora_epilogue* epilogue);
+
+/*
  * dst [cols, rows] = src [rows, cols]^T for bf16 matrices (rows and cols
  * multiples of 8), e.g. the frozen W^T that the backward can take as
  * lora_group_member.W_t.  Asynchronous on `stream`.

@@ -30,6 +30,7 @@ from ._lib import (  # noqa: F401
 )
 from .functional import (  # noqa: F401
     LoraHeadLogpFunction,
+    LoraLinearEpiFunction,
     LoraLinearFunction,
     LoraPolicyLossFunction,
     LoraPreferenceLossFunction,
@@ -42,6 +43,8 @@ from .functional import (  # noqa: F401
     lora_group_bwd,
     lora_group_fwd,
     lora_linear_bwd,
+    lora_linear_epi_bwd,
+    lora_linear_epi_fwd,
     lora_linear_fwd,
     lora_linear_fwd_noalloc,
     lora_merge,

@@ -37,6 +37,14 @@ class GroupMember(ctypes.Structure):
 
 _mp = ctypes.POINTER(GroupMember)
 
+
+class Epilogue(ctypes.Structure):
+    """struct lora_epilogue of the C ABI."""
+    _fields_ = [("act", _int), ("bias", _vp), ("residual", _vp), ("Z", _vp)]
+
+
+_ep = ctypes.POINTER(Epilogue)
+
 _SIGS = {
     "lora_abi_version": ([], _int),
     "lora_strerror": ([_int], ctypes.c_char_p),
@@ -61,6 +69,9 @@ _SIGS = {
     "lora_swiglu_fwd": ([_int, _i64, _i64, _mp, _vp, _fp, _vp, _vp, _sz, _vp], _int),
     "lora_swiglu_bwd": ([_int, _i64, _i64, _mp, _vp, _fp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _int),
     "lora_swiglu_workspace_bytes": ([_int, _int, _i64, _i64, _mp], _sz),
+    "lora_linear_epi_fwd": ([_int, _i64, _i64, _mp, _ep, _vp, _fp, _vp, _sz, _vp], _int),
+    "lora_linear_epi_bwd": ([_int, _i64, _i64, _mp, _ep, _vp, _fp, _vp, _vp, _sz, _vp], _int),
+    "lora_linear_epi_workspace_bytes": ([_int, _int, _i64, _i64, _mp, _ep], _sz),
     "lora_merge": ([_int, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _int),
     "lora_dropout_fwd": ([_int, _i64, _i64, _i64, _i64, _f32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
                          _int),

@@ -411,6 +411,7 @@ enum ProfKind : int {
   K_TINY,
   K_TOKEN_LOGP,
   K_LOSS,
+  K_EPI_GRAD,
   K_PROF_COUNT
 };
 
@@ -426,6 +427,8 @@ const char* kind_name(int k) {
       "gemm_nf4_128x128_nt_split",  "gemm_nf4_128x128_nn_split",  "merge_bf16_128x128",
       "merge_f32_64x128",           "gemm_bf16_256x256_swiglu",   "dropout_dx_bf16_128x128",
       "dropout_dx_f32_64x128",      "gemm_bf16_256x256_nt_group", "gemm_nf4_256x256_nt_whole",
+      "gemm_bf16_256x256_nt_epi",   "gemm_bf16_128x128_nt_epi",   "gemm_nf4_256x256_nt_epi",
+      "gemm_nf4_128x128_nt_epi",    "gemm_nf4_256x256_nt_whole_epi", "gemm_f32_64x128_nt_epi",
       "pad_cols",
       "rope_inverse",
       "reduce_splits",              "fill_zero",                  "rope_cache",
@@ -434,7 +437,7 @@ const char* kind_name(int k) {
       "dropout_mask_copy",          "transpose_w",                "skinny_fwd",
       "few_panel",                  "few_fwd",                    "few_bwd",
       "tiny_f32",
-      "token_logp",                 "sequence_loss"};
+      "token_logp",                 "sequence_loss",              "epilogue_grad"};
   static_assert(sizeof(names) / sizeof(names[0]) == K_PROF_COUNT, "one name per launch kind");
   return (k >= 0 && k < K_PROF_COUNT) ? names[k] : "unknown";
 }
@@ -567,17 +570,24 @@ FewArgs few_args(const FewPlan& F, int64_t M, int64_t d_in, int64_t d_out, int64
   return a;
 }
 
+// Bytes of the epilogue's own operands.
+double epi_bytes(const EpiArgs* ep, int64_t M, int64_t d_out, int eb) {
+  if (!ep) return 0;
+  return (double(M) * d_out * ((ep->res ? 1 : 0) + (ep->z ? 1 : 0)) + (ep->bias ? double(d_out) : 0)) * eb;
+}
+
 int few_forward(const FewPlan& F, int64_t M, int64_t d_in, int64_t d_out, int64_t r, float scale, const void* X,
                 const void* W, const Nf4W* nf4, const void* A, const void* B, const Rope* rope, void* Y, char* w,
-                hipStream_t st) {
+                hipStream_t st, const EpiArgs* ep) {
   FewArgs a = few_args(F, M, d_in, d_out, r, scale, X, W, nf4, A, B, rope, w);
   a.Y = static_cast<uint16_t*>(Y);
+  if (ep) a.ep = *ep;
   const double Md = double(M), ki = double(d_in), ko = double(d_out), rr = double(r);
   const double wb = nf4 ? ko * ki * (0.5 + 1.0 / 16) : 2.0 * ko * ki;
   HIPTRY(timed(K_FEW_PANEL, 2 * Md * rr * ki, (Md + rr) * ki * 2 + 4.0 * F.Sp * F.Mp * rr, st,
                [&] { return launch_few_panel(a, F.MB, st); }));
-  HIPTRY(timed(K_FEW_FWD, 2 * Md * ko * (ki + rr), wb + (Md * ki + ko * rr + Md * ko) * 2, st,
-               [&] { return launch_few_fwd(a, F.MB, nf4 != nullptr, st); }));
+  HIPTRY(timed(K_FEW_FWD, 2 * Md * ko * (ki + rr), wb + (Md * ki + ko * rr + Md * ko) * 2 + epi_bytes(ep, M, d_out, 2),
+               st, [&] { return launch_few_fwd(a, F.MB, nf4 != nullptr, ep != nullptr, st); }));
   return LORA_OK;
 }
 
@@ -607,10 +617,11 @@ int few_backward(const FewPlan& F, int64_t M, int64_t d_in, int64_t d_out, int64
 
 // Pext: when not NULL, the panel s X A^T is already in Pext (row stride
 // ldpext, columns r..r8 zero) and is not computed here (group calls).
+// ep: the bias / activation / residual epilogue (not with RoPE).
 int forward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, float scale, const void* X,
                  const void* W, const Nf4W* nf4, const void* A, const void* B, const Rope* rope, void* Y, void* ws,
                  const Layout& L, hipStream_t st, const void* Pext = nullptr, int64_t ldpext = 0,
-                 const void* Xa = nullptr) {
+                 const void* Xa = nullptr, const EpiArgs* ep = nullptr) {
   // Xa: the adapter's input when it differs from X (LoRA dropout)
   const void* Xp = Xa ? Xa : X;
   if (M == 0) return LORA_OK;
@@ -618,22 +629,22 @@ int forward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, f
   const int eb = elem_bytes(dtype);
   char* w = static_cast<char*>(ws);
   if (!f32 && L.few.ok && !Pext && !Xa)
-    return few_forward(L.few, M, d_in, d_out, r, scale, X, W, nf4, A, B, rope, Y, w, st);
+    return few_forward(L.few, M, d_in, d_out, r, scale, X, W, nf4, A, B, rope, Y, w, st, ep);
   // tiny fp32 problems: the whole forward in one launch
   if (f32 && !rope && !Pext && !Xa && tiny_fits(M, d_in, d_out, r)) {
     const double Md = double(M), ki = double(d_in), ko = double(d_out), rr = double(r);
     HIPTRY(timed(K_TINY, 2 * Md * ko * ki + 2 * Md * rr * (ki + ko),
-                 4 * (Md * ki + ko * ki + rr * ki + ko * rr + Md * ko), st, [&] {
+                 4 * (Md * ki + ko * ki + rr * ki + ko * rr + Md * ko) + epi_bytes(ep, M, d_out, 4), st, [&] {
                    return launch_tiny(false, static_cast<const float*>(X), static_cast<const float*>(W),
                                       static_cast<const float*>(A), static_cast<const float*>(B), nullptr,
                                       static_cast<float*>(Y), nullptr, nullptr, nullptr, nullptr, nullptr, M, d_in,
-                                      d_out, r, scale, st);
+                                      d_out, r, scale, st, ep);
                  }));
     return LORA_OK;
   }
   // few tokens: panel, GEMM, rank term and epilogue in one launch
   // (bf16 W; an NF4 W keeps the split path's load-stage dequantisation)
-  const int smode = rope ? sk::ROPE : sk::PLAIN;
+  const int smode = rope ? sk::ROPE : ep ? sk::EPIL : sk::PLAIN;
   if (!f32 && !nf4 && !Pext && !Xa && skinny_fits(M, d_in, d_out, r, smode)) {
     SkinnyArgs sa;
     memset(&sa, 0, sizeof(sa));
@@ -643,9 +654,11 @@ int forward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, f
     sa.Y = static_cast<uint16_t*>(Y);
     sa.M = (int)M; sa.N = (int)d_out; sa.K = (int)d_in; sa.r = (int)r; sa.s = scale;
     if (rope) { sa.pos = rope->pos; sa.cosc = rope->cosc; sa.sinc = rope->sinc; sa.max_pos = rope->max_pos; }
+    if (ep) sa.ep = *ep;
     const double Md = double(M), ki = double(d_in), ko = double(d_out), rr = double(r);
     HIPTRY(timed(K_SKINNY, 2 * Md * ko * ki + 2 * Md * rr * (ki + ko),
-                 (ko * ki + Md * ki + rr * ki + ko * rr + Md * ko) * 2 + (rope ? Md * 64 * 8 : 0), st,
+                 (ko * ki + Md * ki + rr * ki + ko * rr + Md * ko) * 2 + (rope ? Md * 64 * 8 : 0) +
+                     epi_bytes(ep, M, d_out, 2), st,
                  [&] { return launch_skinny_fwd(sa, smode, st); }));
     return LORA_OK;
   }
@@ -682,6 +695,8 @@ int forward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, f
   a.a2 = P; a.lda2 = ldp; a.b2 = Bsrc; a.ldb2 = L.r8; a.K2 = r;
   a.m_load = M; a.m_store = M; a.n_load = d_out; a.n_store = d_out;
   a.c = Y; a.ldc = d_out;
+  if (ep) a.ep = *ep;
+  const double xbytes = epi_bytes(ep, M, d_out, eb);
   GemmKind k;
   const bool big = use_big(M, d_out);
   if (nf4 && L.nf4_whole) {
@@ -689,14 +704,16 @@ int forward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, f
     a.codes = nf4->codes; a.absmax = nf4->absmax; a.codes_ld = d_in / 2; a.blocks_per_row = d_in / 64;
     for (int i = 0; i < 16; ++i) a.nf4_table[i] = nf4->table[i];
     const double flop = 2 * Md * ko * (ki + rr);
-    const double bytes = (Md * ki + Md * rr + ko * rr + Md * ko) * e + ko * ki * (0.5 + 1.0 / 16);
-    HIPTRY(gemm(G_NF4_WHOLE_NT_STORE, a, 1, st, flop, bytes));
+    const double bytes = (Md * ki + Md * rr + ko * rr + Md * ko) * e + ko * ki * (0.5 + 1.0 / 16) + xbytes;
+    HIPTRY(gemm(ep ? G_NF4_WHOLE_NT_EPI : G_NF4_WHOLE_NT_STORE, a, 1, st, flop, bytes));
     return LORA_OK;
   }
   if (nf4) {
     a.codes = nf4->codes; a.absmax = nf4->absmax; a.codes_ld = d_in / 2; a.blocks_per_row = d_in / 64;
     for (int i = 0; i < 16; ++i) a.nf4_table[i] = nf4->table[i];
-    k = big ? G_NF4_BIG_NT_STORE : G_NF4_MED_NT_STORE;
+    k = ep ? (big ? G_NF4_BIG_NT_EPI : G_NF4_MED_NT_EPI) : (big ? G_NF4_BIG_NT_STORE : G_NF4_MED_NT_STORE);
+  } else if (ep) {
+    k = f32 ? G_F32_NT_EPI : (big ? G_BF16_BIG_NT_EPI : G_BF16_MED_NT_EPI);
   } else if (rope) {
     a.pos = rope->pos; a.cosc = rope->cosc; a.sinc = rope->sinc; a.max_pos = rope->max_pos;
     k = f32 ? G_F32_NT_ROPE : (big ? G_BF16_BIG_NT_ROPE : G_BF16_MED_NT_ROPE);
@@ -713,14 +730,15 @@ int forward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, f
     a.k_split = L.ksplit_main; a.c = part; a.ldc = d_out; a.part_stride = M * d_out;
     HIPTRY(gemm(nf4 ? G_NF4_MED_NT_PARTIAL : G_BF16_MED_NT_PARTIAL, a, S, st, flop,
                 bytes - Md * ko * e + 4.0 * S * Md * ko));
-    HIPTRY(timed(K_FINISH, double(S) * Md * ko, 4.0 * S * Md * ko + Md * ko * e, st, [&] {
+    HIPTRY(timed(K_FINISH, double(S) * Md * ko, 4.0 * S * Md * ko + Md * ko * e + xbytes, st, [&] {
+      if (ep) return launch_split_finish_epi(part, S, M * d_out, M, d_out, static_cast<uint16_t*>(Y), *ep, st);
       return launch_split_finish(part, S, M * d_out, M, d_out, static_cast<uint16_t*>(Y), d_out,
                                  rope ? rope->pos : nullptr, rope ? rope->cosc : nullptr,
                                  rope ? rope->sinc : nullptr, rope ? rope->max_pos : 0, st);
     }));
     return LORA_OK;
   }
-  HIPTRY(gemm(k, a, 1, st, flop, bytes));
+  HIPTRY(gemm(k, a, 1, st, flop, bytes + xbytes));
   return LORA_OK;
 }
 
@@ -1449,6 +1467,62 @@ int swiglu_backward(int dtype, int64_t M, int64_t d_in, const lora_group_member*
 // host it is only a stand-in for the symbol): the device address of each
 // copy comes from hipGetSymbolAddress, called once per device with that
 // device current, and is kept here.
+// ---------------------------------------------------------------------------
+// one projection with bias, activation and residual
+// ---------------------------------------------------------------------------
+// Backward: the layer's own layout, then dZ (with an activation) and the bias
+// gradient's partials over up to 64 ranges of at least 64 tokens.
+struct EpiLayout {
+  Layout L;
+  size_t dz = 0, part = 0, total = 0;
+  int chunks = 1;
+};
+
+EpiLayout make_epi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, const lora_group_member& m,
+                          const lora_epilogue& e) {
+  EpiLayout E;
+  const int op = m.W_nf4 ? (bwd ? LORA_OP_NF4_BWD : LORA_OP_NF4_FWD) : (bwd ? LORA_OP_BWD : LORA_OP_FWD);
+  E.L = make_layout(op, dtype, M, d_in, m.d_out, m.r, m.W_t != nullptr && !m.W_nf4);
+  E.total = E.L.total;
+  if (bwd && M > 0) {
+    auto take = [&](size_t bytes) {
+      const size_t at = align256(E.total);
+      E.total = at + align256(bytes);
+      return at;
+    };
+    if (e.act != LORA_ACT_NONE) E.dz = take(size_t(M) * m.d_out * elem_bytes(dtype));
+    E.chunks = (int)std::min<int64_t>(64, cdiv(M, 64));
+    E.part = take(size_t(E.chunks) * m.d_out * 4);
+  }
+  return E;
+}
+
+int check_epi(bool bwd, int dtype, int64_t M, int64_t d_in, const lora_group_member* m, const lora_epilogue* e,
+              const void* X, const float* table16) {
+  if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_ERR_DTYPE;
+  if (!m || !e) return LORA_ERR_NULL;
+  TRY(check_sizes(M, d_in, m->d_out, m->r));
+  if (m->rope || e->act < LORA_ACT_NONE || e->act > LORA_ACT_GELU_TANH) return LORA_ERR_SHAPE;
+  TRY(check_ptrs({m->A, m->B}));
+  if (m->W_nf4) {
+    if (dtype != LORA_BF16) return LORA_ERR_DTYPE;
+    TRY(check_nf4(d_in, 64, m->W_nf4, m->absmax, table16));
+  } else {
+    TRY(check_ptrs({m->W}));
+  }
+  if (M > 0) TRY(check_ptrs({X}));
+  if (bwd) {
+    TRY(check_ptrs({m->dA, m->dB}));
+    if (M > 0) TRY(check_ptrs({m->dY}));
+    if (M > 0 && e->act != LORA_ACT_NONE) TRY(check_ptrs({e->Z}));
+    if ((m->dX && !aligned16(m->dX)) || (m->W_t && !aligned16(m->W_t))) return LORA_ERR_ALIGN;
+    return LORA_OK;
+  }
+  if (M > 0) TRY(check_ptrs({m->Y}));
+  if (!aligned16(e->bias) || !aligned16(e->residual) || !aligned16(e->Z)) return LORA_ERR_ALIGN;
+  return LORA_OK;
+}
+
 constexpr size_t kStaticScratchBytes = size_t(LORA_STATIC_SCRATCH_BYTES);
 
 std::mutex g_scratch_mu;
@@ -1830,6 +1904,62 @@ int lora_swiglu_bwd(int dtype, int64_t M, int64_t d_in, const lora_group_member*
   TRY(check_device());
   return swiglu_backward(dtype, M, d_in, members, X, table16, dH, G, U, dX, ws, S,
                          static_cast<hipStream_t>(stream));
+}
+
+size_t lora_linear_epi_workspace_bytes(int backward, int dtype, int64_t M, int64_t d_in,
+                                       const lora_group_member* member, const lora_epilogue* epilogue) {
+  if (dtype != LORA_F32 && dtype != LORA_BF16) return 0;
+  if (!member || !epilogue || check_sizes(M, d_in, member->d_out, member->r) != LORA_OK) return 0;
+  return make_epi_layout(backward != 0, dtype, M, d_in, *member, *epilogue).total;
+}
+
+int lora_linear_epi_fwd(int dtype, int64_t M, int64_t d_in, const lora_group_member* member,
+                        const lora_epilogue* epilogue, const void* X, const float* table16, void* ws, size_t ws_bytes,
+                        void* stream) {
+  TRY(check_epi(false, dtype, M, d_in, member, epilogue, X, table16));
+  const lora_group_member& m = *member;
+  const EpiLayout E = make_epi_layout(false, dtype, M, d_in, m, *epilogue);
+  TRY(check_ws_bytes(E.total, ws, ws_bytes));
+  TRY(check_device());
+  const Nf4W q{m.W_nf4, m.absmax, table16};
+  const EpiArgs ep{epilogue->bias, epilogue->residual, epilogue->Z, epilogue->act};
+  return forward_impl(dtype, M, d_in, m.d_out, m.r, m.scale, X, m.W, m.W_nf4 ? &q : nullptr, m.A, m.B, nullptr, m.Y,
+                      ws, E.L, static_cast<hipStream_t>(stream), nullptr, 0, nullptr, &ep);
+}
+
+int lora_linear_epi_bwd(int dtype, int64_t M, int64_t d_in, const lora_group_member* member,
+                        const lora_epilogue* epilogue, const void* X, const float* table16, float* dbias, void* ws,
+                        size_t ws_bytes, void* stream) {
+  TRY(check_epi(true, dtype, M, d_in, member, epilogue, X, table16));
+  if (!aligned16(dbias)) return LORA_ERR_ALIGN;
+  const lora_group_member& m = *member;
+  const EpiLayout E = make_epi_layout(true, dtype, M, d_in, m, *epilogue);
+  TRY(check_ws_bytes(E.total, ws, ws_bytes));
+  TRY(check_device());
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  char* w = static_cast<char*>(ws);
+  const int eb = elem_bytes(dtype);
+  const bool act = epilogue->act != LORA_ACT_NONE;
+  const double n = double(M) * m.d_out;
+  const void* dZ = m.dY;
+  if (M > 0 && (act || dbias)) {
+    float* part = dbias ? reinterpret_cast<float*>(w + E.part) : nullptr;
+    HIPTRY(timed(K_EPI_GRAD, 6 * n, n * eb * (act ? 3 : 1), st, [&] {
+      return launch_epi_grad(eb, m.dY, epilogue->Z, act ? w + E.dz : nullptr, part, E.chunks, M, m.d_out,
+                             epilogue->act, st);
+    }));
+    if (act) dZ = w + E.dz;
+    if (dbias)
+      HIPTRY(timed(K_REDUCE, double(E.chunks) * m.d_out, 4.0 * (E.chunks + 1) * m.d_out, st, [&] {
+        return launch_reduce_splits(part, E.chunks, 1, m.d_out, m.d_out, false, dbias, st);
+      }));
+  } else if (dbias) {
+    HIPTRY(timed(K_FILL, 0, 4.0 * m.d_out, st, [&] { return launch_fill_zero(dbias, m.d_out, st); }));
+  }
+  const Nf4W q{m.W_nf4, m.absmax, table16};
+  return backward_impl(dtype, M, d_in, m.d_out, m.r, m.scale, X, m.W, m.W_nf4 ? &q : nullptr, m.A, m.B, nullptr, dZ,
+                       m.dX, m.dA, m.dB, ws, E.L, st, nullptr, nullptr, nullptr,
+                       E.L.dx_nt && !m.W_nf4 ? m.W_t : nullptr);
 }
 
 int lora_transpose(const void* src, int64_t rows, int64_t cols, void* dst, void* stream) {

@@ -671,7 +671,7 @@ __device__ __forceinline__ void few_sum4_dev(const float* src, int S, int64_t zs
 // the pairs (f, f + 64) of each row.
 // part: the tile's first partial slab ([Mp][BNT] each, S of them, summed in
 // slab order).
-template <int BNT, int NTH = few::NT>
+template <int BNT, int NTH = few::NT, bool EPIL = false>
 __device__ __forceinline__ void few_finish(const FewArgs& p, const float* part, int S, int n0, int N, uint16_t* out,
                                            bool rope) {
   // NI items (16 bytes of 4 columns) of every slab in flight per thread (8
@@ -694,8 +694,13 @@ __device__ __forceinline__ void few_finish(const FewArgs& p, const float* part, 
       for (int i = 0; i < NI; ++i) {
         if (off[i] < 0) continue;
         const int it = i0 + i * NTH, t = it / (BNT / 4), c = 4 * (it % (BNT / 4));
-        *reinterpret_cast<uint2*>(out + (int64_t)t * N + n0 + c) =
-            make_uint2(pack_bf16x2(a[i].x, a[i].y), pack_bf16x2(a[i].z, a[i].w));
+        if constexpr (EPIL) {
+          float y[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
+          epi_apply(p.ep, out, (int64_t)t * N + n0 + c, n0 + c, y);
+        } else {
+          *reinterpret_cast<uint2*>(out + (int64_t)t * N + n0 + c) =
+              make_uint2(pack_bf16x2(a[i].x, a[i].y), pack_bf16x2(a[i].z, a[i].w));
+        }
       }
     }
     return;
@@ -789,7 +794,7 @@ struct FewNf4Ring {
   static_assert(NS >= 3, "at least three stages");
 };
 
-template <int MB>
+template <int MB, bool EPIL>
 __global__ void __launch_bounds__(few::NT4) __attribute__((amdgpu_waves_per_eu(2, 2)))
 few_fwd_nf4_kernel(const FewArgs p) {
   using namespace few;
@@ -981,8 +986,8 @@ few_fwd_nf4_kernel(const FewArgs p) {
     // (the rank term is in the partial of the tile's first block)
     const int a = sp.a0 + i;
     const int lo = few_blk_of(p, a * p.nkt), hi = few_blk_of(p, (a + 1) * p.nkt - 1);
-    few_finish<BNF, NT4>(p, p.Cp + (int64_t)(lo + a) * p.Mp * BNF, hi - lo + 1, a * BNF, p.d_out, p.Y,
-                         p.rope != 0);
+    few_finish<BNF, NT4, EPIL>(p, p.Cp + (int64_t)(lo + a) * p.Mp * BNF, hi - lo + 1, a * BNF, p.d_out, p.Y,
+                               !EPIL && p.rope != 0);
   }
 }
 
@@ -991,7 +996,7 @@ few_fwd_nf4_kernel(const FewArgs p) {
 // and finish as the NF4 form, with 64-deep stages of W (128 rows of 128 bytes,
 // NT layout) and of the activations landing by DMA; 4 waves of 32 columns.
 // ---------------------------------------------------------------------------
-template <int MB>
+template <int MB, bool EPIL>
 __global__ void __launch_bounds__(few::NT) __attribute__((amdgpu_waves_per_eu(1, 1)))
 few_fwd_bf16_kernel(const FewArgs p) {
   using namespace few;
@@ -1165,8 +1170,8 @@ few_fwd_bf16_kernel(const FewArgs p) {
     if (!(i ? fin1 : fin0)) continue;
     const int a = sp.a0 + i;
     const int lo = few_blk_of(p, a * p.nkt), hi = few_blk_of(p, (a + 1) * p.nkt - 1);
-    few_finish<BNF>(p, p.Cp + (int64_t)(lo + a) * p.Mp * BNF, hi - lo + 1, a * BNF, p.d_out, p.Y,
-                    p.rope != 0);
+    few_finish<BNF, NT, EPIL>(p, p.Cp + (int64_t)(lo + a) * p.Mp * BNF, hi - lo + 1, a * BNF, p.d_out, p.Y,
+                              !EPIL && p.rope != 0);
   }
 }
 

@@ -4,6 +4,8 @@
 
 #include <stdint.h>
 
+#include "epi.h"
+
 namespace lora {
 
 namespace few {
@@ -53,6 +55,7 @@ struct FewArgs {
   // launch 2: n_tiles column tiles of BN, nkt stages of BK each; block b of
   // nblk takes the stages [b T / nblk, (b + 1) T / nblk) of the T = n_tiles nkt
   int n_tiles, nkt, T, nblk;
+  EpiArgs ep;  // forward with an epilogue (epi.h)
   int fold;  // backward: the W stream sums P and Q from the partials itself (no few_reduce_kernel)
 };
 

@@ -43,6 +43,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "epi.h"
+
 namespace lora {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -58,7 +60,8 @@ enum Epi : int {
   EPI_ADD = 5,         // C[m, n] = alpha * acc + Cin[m, n]  (type T; C may be Cin)
   EPI_SWIGLU = 6,      // whole-tile kernel only: gate/up pair -> silu(g) * u (see gemm_w4.h)
   EPI_ADD_MASKED = 7,  // C[m, n] = keep(m, n) ? alpha * acc + Cin[m, n] : Cin[m, n]
-  EPI_GROUP = 8        // whole-tile kernel only: several projections' GEMMs, store or RoPE per member
+  EPI_GROUP = 8,       // whole-tile kernel only: several projections' GEMMs, store or RoPE per member
+  EPI_ACT = 9          // C = act(alpha acc + bias) + residual (epi.h)
 };
 
 enum BLoad : int { BL_PLAIN = 0, BL_NF4 = 1 };
@@ -137,6 +140,7 @@ struct GemmArgs {
   int mem_ldb2[kGroupGemmMax];
   int mem_ldc[kGroupGemmMax];
   int mem_rope[kGroupGemmMax];
+  EpiArgs ep;  // EPI_ACT (residual and z rows as long as C's: ldc)
 };
 
 __device__ __forceinline__ int lds_off(int row, int chunk) {
@@ -737,6 +741,36 @@ gemm_kernel(const GemmArgs p) {
           store_out<T>(p.c, row * p.ldc + col + 64, z2 * cs + z1 * sn);
         }
       }
+  } else if constexpr (EPI == EPI_ACT) {
+    // Staged through LDS, every wave PI of its 16-row blocks at a time (fp32,
+    // row pitch BN + 4 floats as below), so that bias, residual and output are
+    // read and written 8 columns a thread (n_store is a multiple of 8).
+    constexpr int PITCH = BN + 4;
+    constexpr int PI = FM % 2 == 0 && WM * 32 * PITCH * 4 <= C::LDS ? 2 : 1;
+    constexpr int ROWS = WM * PI * 16;
+    static_assert(ROWS * PITCH * 4 <= C::LDS, "the staged rows fit the LDS");
+    float* stile = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int i0 = 0; i0 < FM; i0 += PI) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < PI; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            stile[((wm * PI + i) * 16 + 4 * g + v) * PITCH + wn * C::TN + j * 16 + l16] = acc[i0 + i][j][v] * p.alpha;
+      __syncthreads();
+      for (int c = tid; c < ROWS * (BN / 8); c += NT) {
+        const int lr = c / (BN / 8), lc = (c % (BN / 8)) * 8;
+        const int64_t row = m0 + (lr / (PI * 16)) * C::TM + i0 * 16 + lr % (PI * 16), col = n0 + lc;
+        if (row >= p.m_store || col >= p.n_store) continue;
+        const float4 y0 = *reinterpret_cast<const float4*>(stile + lr * PITCH + lc);
+        const float4 y1 = *reinterpret_cast<const float4*>(stile + lr * PITCH + lc + 4);
+        float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+        epi_apply(p.ep, reinterpret_cast<T*>(p.c), row * p.ldc + col, col, y);
+      }
+    }
   } else if constexpr (EPI == EPI_ADD || EPI == EPI_ADD_MASKED) {
     // Staged through LDS in blocks of RB rows (fp32, row pitch BN + 4 floats:
     // the 16x16 output layout writes without bank conflicts), then each thread

@@ -67,6 +67,7 @@ constexpr uint32_t OOB = 0x40000000u;  // lane offset that reads zero
 //               projection of output columns n0 / 2 + 64 wn + 32 (j / 2) + l32;
 //               C = silu(g) u, and g / u are also stored to cg / cu when
 //               set.
+//   EPI_ACT:    C = act(alpha acc + bias) + residual, Z kept when asked for.
 template <int EPI>
 __device__ __forceinline__ void w4_epilogue(const GemmArgs& p, f32x16 (&acc)[w4::FM][w4::FN], char* smem,
                                             int64_t m0, int64_t n0, void* c_out, int64_t ldc) {
@@ -199,8 +200,63 @@ __device__ __forceinline__ void w4_epilogue(const GemmArgs& p, f32x16 (&acc)[w4:
       emit(std::integral_constant<int, 0>{});
     else
       emit(std::integral_constant<int, 2>{});
+  } else if constexpr (EPI == EPI_ACT) {
+    // Four passes of one 32-row MFMA block of every wave (64 rows of the
+    // tile) through LDS: fp32 with a row pitch of 256 + 8 floats (rows q and
+    // q + 4, which a wave's halves write together, lie 32 banks apart), then
+    // 8 columns of 8 rows a thread, so that residual and output move in
+    // 16-byte accesses and the bias is loaded once.  The pass's residual is
+    // requested before its tile is staged.
+    constexpr int PITCH = BN + 8;
+    static_assert(64 * PITCH * 4 <= 4 * BM * 128, "the staged rows fit every ring");
+    float* st = reinterpret_cast<float*>(smem);
+    const int cc = (te & 31) * 8, r0 = te >> 5;
+    const int64_t col = n0 + cc;
+    float b[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) b[e] = 0.f;
+    if (p.ep.bias) epi_load(static_cast<const uint16_t*>(p.ep.bias) + col, b);
+    const uint16_t* res = static_cast<const uint16_t*>(p.ep.res);
+    uint16_t* zo = static_cast<uint16_t*>(p.ep.z);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      u32x4 rv[8];
+      if (res) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int lr = r0 + 8 * k;
+          rv[k] = *reinterpret_cast<const u32x4*>(res + (m0 + (lr >> 5) * TM + 32 * i + (lr & 31)) * ldc + col);
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          st[(32 * wm + 8 * (v >> 2) + (v & 3) + 4 * hh) * PITCH + wn * TN + 32 * j + l32] = acc[i][j][v] * p.alpha;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int lr = r0 + 8 * k;
+        const int64_t o = (m0 + (lr >> 5) * TM + 32 * i + (lr & 31)) * ldc + col;
+        const float4 y0 = *reinterpret_cast<const float4*>(st + lr * PITCH + cc);
+        const float4 y1 = *reinterpret_cast<const float4*>(st + lr * PITCH + cc + 4);
+        float y[8] = {y0.x + b[0], y0.y + b[1], y0.z + b[2], y0.w + b[3],
+                      y1.x + b[4], y1.y + b[5], y1.z + b[6], y1.w + b[7]};
+        if (zo) epi_store(zo + o, y);
+        act_all<true>(y, p.ep.act);
+        if (res) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            y[2 * q] += __builtin_bit_cast(float, rv[k][q] << 16);
+            y[2 * q + 1] += __builtin_bit_cast(float, rv[k][q] & 0xFFFF0000u);
+          }
+        }
+        epi_store(out + o, y);
+      }
+    }
   } else {
-    static_assert(EPI == EPI_STORE, "store, RoPE or SwiGLU epilogue");
+    static_assert(EPI == EPI_STORE, "store, RoPE, SwiGLU or activation epilogue");
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll

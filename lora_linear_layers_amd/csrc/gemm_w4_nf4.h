@@ -58,6 +58,7 @@ constexpr int SLOT = w4::BM * 128;  // one operand tile of a stage (32 KiB)
 constexpr int LDS = 4 * SLOT;       // 128 KiB
 }  // namespace w4q
 
+template <int EPI>
 __global__ void __launch_bounds__(w4::NT) __attribute__((amdgpu_waves_per_eu(1, 1)))
 gemm_w4_nf4_kernel(const GemmArgs p) {
   using namespace w4;
@@ -340,7 +341,7 @@ gemm_w4_nf4_kernel(const GemmArgs p) {
   if (t + 1 < nk) stage(t++, F_{}, T_{}, A0{}, A0{}, T_{});
   stage(t, F_{}, F_{}, A0{}, A0{}, F_{});
 
-  w4_epilogue<EPI_STORE>(p, acc, smem, m0, n0, p.c, p.ldc);
+  w4_epilogue<EPI>(p, acc, smem, m0, n0, p.c, p.ldc);
 }
 
 }  // namespace lora

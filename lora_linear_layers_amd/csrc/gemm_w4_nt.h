@@ -76,8 +76,8 @@ gemm_w4_nt_kernel(const GemmArgs p) {
   using w4nt::SLOT;
   using w4nt::vmcnt_imm;
   constexpr int BKS = w4nt::BK;
-  static_assert(EPI == EPI_STORE || EPI == EPI_ROPE || EPI == EPI_SWIGLU || EPI == EPI_GROUP,
-                "store, RoPE, SwiGLU or group epilogue");
+  static_assert(EPI == EPI_STORE || EPI == EPI_ROPE || EPI == EPI_SWIGLU || EPI == EPI_GROUP || EPI == EPI_ACT,
+                "store, RoPE, SwiGLU, group or activation epilogue");
   constexpr bool SW = EPI == EPI_SWIGLU;
   constexpr bool GR = EPI == EPI_GROUP;
   __shared__ __attribute__((aligned(1024))) char smem[w4nt::LDS];

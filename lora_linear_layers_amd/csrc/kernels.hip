@@ -142,7 +142,13 @@ TileShape gemm_tile(GemmKind k) {
     case G_BF16_WHOLE_SWIGLU:
     case G_BF16_WHOLE_GROUP:
     case G_NF4_WHOLE_NT_STORE:
+    case G_NF4_WHOLE_NT_EPI:
+    case G_BF16_BIG_NT_EPI:
+    case G_NF4_BIG_NT_EPI:
       return {256, 256};
+    case G_BF16_MED_NT_EPI:
+    case G_NF4_MED_NT_EPI:
+      return {128, 128};
     case G_BF16_PANEL_SPLIT_NT:
       return {256, 64};
     case G_F32_NT_STORE:
@@ -150,6 +156,7 @@ TileShape gemm_tile(GemmKind k) {
     case G_F32_NN_STORE:
     case G_F32_NN_ADD:
     case G_F32_NN_ADD_MASKED:
+    case G_F32_NT_EPI:
       return {64, 128};
     default:
       return {0, 0};
@@ -202,6 +209,14 @@ hipError_t launch_gemm(GemmKind k, GemmArgs a, int splits, hipStream_t st) {
           (int64_t)a.mem_tile0[a.n_mem] != (a.m_store / w4::BM) * (a.n_store / w4::BN))
         return hipErrorInvalidValue;
       return run_whole<false, EPI_GROUP>(a, st);
+    case G_BF16_BIG_NT_EPI:
+      if (whole_tiles(a, splits)) return run_whole<false, EPI_ACT>(a, st);
+      return run<bf, 256, 256, 2, 4, false, EPI_ACT, BL_PLAIN>(a, splits, st);
+    case G_BF16_MED_NT_EPI: return run<bf, 128, 128, 4, 1, false, EPI_ACT, BL_PLAIN>(a, splits, st);
+    case G_NF4_BIG_NT_EPI: return run<bf, 256, 256, 2, 4, false, EPI_ACT, BL_NF4>(a, splits, st);
+    case G_NF4_MED_NT_EPI: return run<bf, 128, 128, 4, 1, false, EPI_ACT, BL_NF4>(a, splits, st);
+    case G_F32_NT_EPI: return run<float, 64, 128, 4, 1, false, EPI_ACT, BL_PLAIN>(a, splits, st);
+    case G_NF4_WHOLE_NT_EPI:
     case G_NF4_WHOLE_NT_STORE: {
       // whole tiles, codes and absmax present, every lane offset of a tile's
       // codes and absmax below the buffer-resource range
@@ -213,7 +228,10 @@ hipError_t launch_gemm(GemmKind k, GemmArgs a, int splits, hipStream_t st) {
       if (nblocks <= 0) return hipSuccess;
       if (nblocks > INT32_MAX) return hipErrorInvalidValue;
       a.tiles_m = (int)tiles_m;
-      hipLaunchKernelGGL(gemm_w4_nf4_kernel, dim3((unsigned)nblocks), dim3(w4::NT), 0, st, a);
+      if (k == G_NF4_WHOLE_NT_EPI)
+        hipLaunchKernelGGL((gemm_w4_nf4_kernel<EPI_ACT>), dim3((unsigned)nblocks), dim3(w4::NT), 0, st, a);
+      else
+        hipLaunchKernelGGL((gemm_w4_nf4_kernel<EPI_STORE>), dim3((unsigned)nblocks), dim3(w4::NT), 0, st, a);
       return hipGetLastError();
     }
     case G_F32_NN_ADD: return run<float, 64, 128, 4, 1, true, EPI_ADD, BL_PLAIN>(a, splits, st);
@@ -656,6 +674,94 @@ hipError_t launch_split_finish(const float* part, int splits, int64_t part_strid
     hipLaunchKernelGGL(split_finish_kernel<false>, dim3(grid_for(items, 256)), dim3(256), 0, st, part, splits,
                        part_stride, M, N, out, ldo, pos, cosc, sinc, max_pos);
   }
+  return hipGetLastError();
+}
+
+// The same sums with the bias / activation / residual epilogue; 4 columns a
+// thread.
+__global__ void __launch_bounds__(256) split_finish_epi_kernel(const float* __restrict__ part, int splits,
+                                                               int64_t part_stride, int64_t M, int64_t N, uint16_t* out,
+                                                               EpiArgs ep) {
+  const int64_t per_row = N / 4, items = M * per_row;
+  for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < items; e += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t m = e / per_row, c = (e - m * per_row) * 4;
+    const float* src = part + m * N + c;
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int z = 0; z < splits; ++z) {
+      const float4 v = *reinterpret_cast<const float4*>(src + (int64_t)z * part_stride);
+      a[0] += v.x; a[1] += v.y; a[2] += v.z; a[3] += v.w;
+    }
+    epi_apply(ep, out, m * N + c, c, a);
+  }
+}
+
+hipError_t launch_split_finish_epi(const float* part, int splits, int64_t part_stride, int64_t M, int64_t N,
+                                   uint16_t* out, const EpiArgs& ep, hipStream_t st) {
+  if (M <= 0 || N <= 0) return hipSuccess;
+  if (splits < 1 || splits > kMaxSplits || N % 8 || part_stride % 4) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(split_finish_epi_kernel, dim3(grid_for(M * (N / 4), 256)), dim3(256), 0, st, part, splits,
+                     part_stride, M, N, out, ep);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Backward of the epilogue: dZ = dY act'(Z) (one rounding to the type; not
+// written without an activation, where dZ is dY), and the bias gradient's
+// partial sums over the tokens.  A block takes 256 columns (8 a thread, 32
+// threads a row) and `rows` tokens, 8 of them at a time; its column sums,
+// joined over its 8 row groups in order, go to part[blockIdx.y][N].
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(256) epi_grad_kernel(const T* __restrict__ dY, const T* __restrict__ Z,
+                                                       T* __restrict__ dZ, float* __restrict__ part, int64_t M,
+                                                       int64_t N, int rows, int act) {
+  __shared__ float red[8][256 + 4];
+  const int tid = threadIdx.x, rg = tid >> 5, lc = (tid & 31) * 8;
+  const int64_t col = (int64_t)blockIdx.x * 256 + lc;
+  const int64_t m0 = (int64_t)blockIdx.y * rows, m1 = min(m0 + rows, M);
+  float s[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[e] = 0.f;
+  if (col < N) {
+    for (int64_t m = m0 + rg; m < m1; m += 8) {
+      const int64_t o = m * N + col;
+      float g[8];
+      epi_load(dY + o, g);
+      if (act != ACT_NONE) {
+        float z[8];
+        epi_load(Z + o, z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] *= act_grad<sizeof(T) == 2>(z[e], act);
+        epi_store(dZ + o, g);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] += g[e];
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) red[rg][lc + e] = s[e];
+  __syncthreads();
+  const int64_t c = (int64_t)blockIdx.x * 256 + tid;
+  if (c >= N) return;
+  float t = 0.f;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) t += red[q][tid];
+  part[(int64_t)blockIdx.y * N + c] = t;
+}
+
+hipError_t launch_epi_grad(int elem_bytes, const void* dY, const void* Z, void* dZ, float* part, int chunks, int64_t M,
+                           int64_t N, int act, hipStream_t st) {
+  if (M <= 0 || N <= 0) return hipSuccess;
+  if (N % 8 || chunks < 1 || chunks > kMaxSplits || (act != ACT_NONE && (!Z || !dZ))) return hipErrorInvalidValue;
+  const int64_t rows = ((M + chunks - 1) / chunks + 7) / 8 * 8;
+  const dim3 grid((unsigned)((N + 255) / 256), (unsigned)chunks);
+  if (elem_bytes == 2)
+    hipLaunchKernelGGL(epi_grad_kernel<uint16_t>, grid, dim3(256), 0, st, static_cast<const uint16_t*>(dY),
+                       static_cast<const uint16_t*>(Z), static_cast<uint16_t*>(dZ), part, M, N, (int)rows, act);
+  else
+    hipLaunchKernelGGL(epi_grad_kernel<float>, grid, dim3(256), 0, st, static_cast<const float*>(dY),
+                       static_cast<const float*>(Z), static_cast<float*>(dZ), part, M, N, (int)rows, act);
   return hipGetLastError();
 }
 
@@ -1191,10 +1297,11 @@ bool tiny_fits(int64_t M, int64_t K, int64_t N, int64_t r) {
 
 hipError_t launch_tiny(bool bwd, const float* X, const float* W, const float* A, const float* B, const float* G,
                        float* Y, float* dX, float* dA, float* dB, float* Ps, float* Qs, int64_t M, int64_t K,
-                       int64_t N, int64_t r, float s, hipStream_t st) {
+                       int64_t N, int64_t r, float s, hipStream_t st, const EpiArgs* ep) {
   if (!tiny_fits(M, K, N, r)) return hipErrorInvalidValue;
   if (bwd && (!Ps || !Qs)) return hipErrorInvalidValue;
   TinyArgs a;
+  a.ep = ep ? *ep : EpiArgs{};
   a.X = X; a.W = W; a.A = A; a.B = B; a.G = G;
   a.Y = Y; a.dX = dX; a.dA = dA; a.dB = dB; a.Ps = Ps; a.Qs = Qs;
   a.M = (int)M; a.K = (int)K; a.N = (int)N; a.r = (int)r; a.s = s;
@@ -1203,7 +1310,10 @@ hipError_t launch_tiny(bool bwd, const float* X, const float* W, const float* A,
   if (!bwd) {
     a.blocks_x = a.tiles_m * tn;
     a.blocks_a = 0;
-    hipLaunchKernelGGL(tiny_fwd_f32_kernel, dim3((unsigned)a.blocks_x), dim3(tiny::NT), 0, st, a);
+    if (ep)
+      hipLaunchKernelGGL(tiny_fwd_f32_kernel<true>, dim3((unsigned)a.blocks_x), dim3(tiny::NT), 0, st, a);
+    else
+      hipLaunchKernelGGL(tiny_fwd_f32_kernel<false>, dim3((unsigned)a.blocks_x), dim3(tiny::NT), 0, st, a);
   } else {
     a.blocks_x = dX ? a.tiles_m * tk : 0;
     a.blocks_a = tk;
@@ -1242,6 +1352,7 @@ hipError_t run_skinny_mode(const SkinnyArgs& a, int mode, hipStream_t st) {
   // blocks, so fewer re-reads of X from L2
   const bool wide = a.N >= 12288;
   if (mode == sk::ROPE) return run_skinny<MB, 2, RB, sk::ROPE>(a, st);
+  if (mode == sk::EPIL) return wide ? run_skinny<MB, 4, RB, sk::EPIL>(a, st) : run_skinny<MB, 1, RB, sk::EPIL>(a, st);
   return wide ? run_skinny<MB, 4, RB, sk::PLAIN>(a, st) : run_skinny<MB, 1, RB, sk::PLAIN>(a, st);
 }
 }  // namespace
@@ -1258,9 +1369,16 @@ hipError_t few_launch(const FewArgs& a, int what, bool nf4, hipStream_t st) {
     // the stream sums at most SMAX panel slabs
     if (a.Sp > (nf4 ? FewPanelPre<MB, few::NT4>::SMAX : FewPanelPre<MB, few::NT>::SMAX)) return hipErrorInvalidValue;
     if (nf4)
-      hipLaunchKernelGGL((few_fwd_nf4_kernel<MB>), dim3((unsigned)a.nblk), dim3(few::NT4), 0, st, a);
+      hipLaunchKernelGGL((few_fwd_nf4_kernel<MB, false>), dim3((unsigned)a.nblk), dim3(few::NT4), 0, st, a);
     else
-      hipLaunchKernelGGL((few_fwd_bf16_kernel<MB>), dim3((unsigned)a.nblk), dim3(few::NT), 0, st, a);
+      hipLaunchKernelGGL((few_fwd_bf16_kernel<MB, false>), dim3((unsigned)a.nblk), dim3(few::NT), 0, st, a);
+  } else if (what == 3) {  // the forward with an epilogue (no RoPE)
+    if (a.rope || a.Sp > (nf4 ? FewPanelPre<MB, few::NT4>::SMAX : FewPanelPre<MB, few::NT>::SMAX))
+      return hipErrorInvalidValue;
+    if (nf4)
+      hipLaunchKernelGGL((few_fwd_nf4_kernel<MB, true>), dim3((unsigned)a.nblk), dim3(few::NT4), 0, st, a);
+    else
+      hipLaunchKernelGGL((few_fwd_bf16_kernel<MB, true>), dim3((unsigned)a.nblk), dim3(few::NT), 0, st, a);
   } else {
     const dim3 grid((unsigned)a.nblk);
     if (nf4)
@@ -1281,8 +1399,9 @@ hipError_t few_dispatch(const FewArgs& a, int MB, int what, bool nf4, hipStream_
   // the W stream's tiles and stages cover its output columns and contraction
   // exactly (stages 128 deep in the NF4 forward, 64 otherwise)
   if (what > 0) {
-    const int64_t ncols = what == 1 ? a.d_out : a.d_in, K = what == 1 ? a.d_in : a.d_out;
-    if ((ncols + few::BN - 1) / few::BN != a.n_tiles || (int64_t)a.nkt * (what == 1 && nf4 ? 128 : 64) != K)
+    const bool fwd = what != 2;
+    const int64_t ncols = fwd ? a.d_out : a.d_in, K = fwd ? a.d_in : a.d_out;
+    if ((ncols + few::BN - 1) / few::BN != a.n_tiles || (int64_t)a.nkt * (fwd && nf4 ? 128 : 64) != K)
       return hipErrorInvalidValue;
   }
   switch (MB) {
@@ -1301,8 +1420,8 @@ hipError_t launch_few_reduce(const FewArgs& a, hipStream_t st) {
   hipLaunchKernelGGL(few_reduce_kernel, dim3(2 * nb), dim3(few::NT), 0, st, a);
   return hipGetLastError();
 }
-hipError_t launch_few_fwd(const FewArgs& a, int MB, bool nf4, hipStream_t st) {
-  return few_dispatch(a, MB, 1, nf4, st);
+hipError_t launch_few_fwd(const FewArgs& a, int MB, bool nf4, bool epil, hipStream_t st) {
+  return few_dispatch(a, MB, epil ? 3 : 1, nf4, st);
 }
 hipError_t launch_few_bwd(const FewArgs& a, int MB, bool nf4, hipStream_t st) {
   return few_dispatch(a, MB, 2, nf4, st);

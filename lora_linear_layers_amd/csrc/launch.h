@@ -56,6 +56,13 @@ enum GemmKind : int {
   G_F32_NN_ADD_MASKED,
   G_BF16_WHOLE_GROUP,  // several projections' forward GEMMs in one whole-tile launch (GemmArgs::n_mem)
   G_NF4_WHOLE_NT_STORE,  // whole-tile forward GEMM, NF4 W expanded in the load stage (gemm_w4_nf4_kernel)
+  // forwards with the bias / activation / residual epilogue (GemmArgs::ep)
+  G_BF16_BIG_NT_EPI,
+  G_BF16_MED_NT_EPI,
+  G_NF4_BIG_NT_EPI,
+  G_NF4_MED_NT_EPI,
+  G_NF4_WHOLE_NT_EPI,
+  G_F32_NT_EPI,
   G_KIND_COUNT
 };
 
@@ -156,6 +163,16 @@ hipError_t launch_split_finish(const float* part, int splits, int64_t part_strid
                                uint16_t* out, int64_t ldo, const int32_t* pos, const float* cosc, const float* sinc,
                                int64_t max_pos, hipStream_t st);
 
+// The same sums with an epilogue: out [M, N] = act(sum + bias) + residual.
+hipError_t launch_split_finish_epi(const float* part, int splits, int64_t part_stride, int64_t M, int64_t N,
+                                   uint16_t* out, const EpiArgs& ep, hipStream_t st);
+
+// Backward of the epilogue over [M, N]: dZ = dY act'(Z) (neither is touched
+// without an activation) and, with part, the column sums of dZ over `chunks`
+// (1 .. 64) ranges of the tokens, fp32 [chunks][N].
+hipError_t launch_epi_grad(int elem_bytes, const void* dY, const void* Z, void* dZ, float* part, int chunks, int64_t M,
+                           int64_t N, int act, hipStream_t st);
+
 hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t st);
 
 // SwiGLU elementwise passes over n elements of bf16 (elem_bytes 2) or fp32:
@@ -185,7 +202,7 @@ hipError_t launch_mfma_rate(int iters, int blocks, float* out, hipStream_t st);
 bool tiny_fits(int64_t M, int64_t K, int64_t N, int64_t r);
 hipError_t launch_tiny(bool bwd, const float* X, const float* W, const float* A, const float* B, const float* G,
                        float* Y, float* dX, float* dA, float* dB, float* Ps, float* Qs, int64_t M, int64_t K,
-                       int64_t N, int64_t r, float s, hipStream_t st);
+                       int64_t N, int64_t r, float s, hipStream_t st, const EpiArgs* ep = nullptr);
 
 // Few-token forward in one launch (skinny.h): Y = X W^T + bf16(s X A^T) B^T,
 // mode 0 plain, 1 RoPE (pos / cosc / sinc, N % 128 == 0), bf16 W.  Requires
@@ -209,7 +226,7 @@ hipError_t launch_nf4_dequant(const uint8_t* codes, const float* absmax, int64_t
 struct FewArgs;
 hipError_t launch_few_panel(const FewArgs& a, int MB, hipStream_t st);
 hipError_t launch_few_reduce(const FewArgs& a, hipStream_t st);  // backward: P_s, Q_s between the launches
-hipError_t launch_few_fwd(const FewArgs& a, int MB, bool nf4, hipStream_t st);
+hipError_t launch_few_fwd(const FewArgs& a, int MB, bool nf4, bool epil, hipStream_t st);
 hipError_t launch_few_bwd(const FewArgs& a, int MB, bool nf4, hipStream_t st);
 
 // Token log-probabilities (loss.hip): logp [rows] and stats [rows, 2] (row

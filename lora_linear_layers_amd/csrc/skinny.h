@@ -47,7 +47,7 @@ namespace lora {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 namespace sk {
-enum Mode : int { PLAIN = 0, ROPE = 1 };
+enum Mode : int { PLAIN = 0, ROPE = 1, EPIL = 2 };  // EPIL: bias, activation, residual (epi.h)
 constexpr int BIG = 0x40000000;        // buffer resource size (offsets stay below)
 constexpr uint32_t OOB = 0x40000000u;  // lane offset that reads zero
 }  // namespace sk
@@ -73,6 +73,7 @@ struct SkinnyArgs {
   const float* cosc;
   const float* sinc;
   int64_t max_pos;     // rows of the cos / sin cache
+  EpiArgs ep;          // EPIL
 };
 
 // MB: 16-row blocks of X (M <= 16 MB); NB: 16-column strips per block; RB:
@@ -268,7 +269,11 @@ skinny_fwd_kernel(const SkinnyArgs p) {
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const int n = col0(j) + l16;
-        if (n < p.N) p.Y[(int64_t)row * p.N + n] = f2bf(y[j][v]);
+        if constexpr (MODE == sk::EPIL) {
+          if (n < p.N) epi_apply1(p.ep, p.Y, (int64_t)row * p.N + n, n, y[j][v]);
+        } else {
+          if (n < p.N) p.Y[(int64_t)row * p.N + n] = f2bf(y[j][v]);
+        }
       }
     }
   }

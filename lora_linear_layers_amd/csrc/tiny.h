@@ -28,6 +28,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "epi.h"
+
 namespace lora {
 
 namespace tiny {
@@ -57,6 +59,7 @@ struct TinyArgs {
   int tiles_m;     // ceil(M / 32)
   int blocks_x;    // blocks of the Y (forward) or dX (backward) tiles
   int blocks_a;    // backward: blocks of the dA column tiles (then the dB row tiles)
+  EpiArgs ep;      // forward with an epilogue (epi.h)
 };
 
 // operand loads through the global address space (a generic pointer would
@@ -172,6 +175,7 @@ __device__ inline void tiny_mm(int kn, LF lf, RF rf, RF2 rf2, tiny::Tiles& sm, f
   if (TWO) reduce(pb, acc2);
 }
 
+template <bool EPIL>
 __global__ void __launch_bounds__(tiny::NT) tiny_fwd_f32_kernel(const TinyArgs a) {
   using namespace tiny;
   __shared__ Tiles sm;
@@ -202,7 +206,10 @@ __global__ void __launch_bounds__(tiny::NT) tiny_fwd_f32_kernel(const TinyArgs a
     if (j >= a.N) continue;
     float v = acc[c];
     for (int q = 0; q < a.r; ++q) v = __builtin_fmaf(Ps[ti * a.r + q], sm.R[tj + c][q], v);
-    a.Y[(int64_t)(i0 + ti) * a.N + j] = v;
+    if constexpr (EPIL)
+      epi_apply1(a.ep, a.Y, (int64_t)(i0 + ti) * a.N + j, j, v);
+    else
+      a.Y[(int64_t)(i0 + ti) * a.N + j] = v;
   }
 }
 

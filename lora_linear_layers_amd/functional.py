@@ -427,6 +427,105 @@ def lora_swiglu_bwd(X, members, dH, G, U, table16=None, need_dX: bool = True, ws
     return dX, grads
 
 
+# ---------------------------------------------------------------------------
+# one projection with bias, activation and residual
+# ---------------------------------------------------------------------------
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _epi_member(X, member, more):
+    """The ctypes member of a projection, its tensors checked against X's device and dtype."""
+    if X.dim() != 2:
+        raise ValueError("X must be [M, d_in]")
+    same = (X.dtype,)
+    _check_on(X, ("X", X, same, None), ("A", member["A"], same, None), ("B", member["B"], same, None),
+              ("W", member.get("W"), same, None), ("W_t", member.get("W_t"), (torch.bfloat16,), None),
+              ("codes", member.get("codes"), (torch.uint8,), None),
+              ("absmax", member.get("absmax"), (torch.float32,), None), *more)
+    arr = _group_members(X, [member])
+    codes, n = member.get("codes"), X.shape[1] * arr[0].d_out
+    if codes is not None and (codes.numel() * 2 != n or member.get("absmax") is None
+                              or member["absmax"].numel() * 64 != n):
+        raise ValueError("codes must hold d_out * d_in / 2 bytes and absmax d_out * d_in / 64 values")
+    return arr[0]
+
+
+def _epi_ws(backward, dt, M, d_in, m, e, device, ws):
+    if ws is not None:
+        return ws  # the library checks its size
+    n = int(L.lib().lora_linear_epi_workspace_bytes(int(backward), dt, M, d_in, m, e))
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+
+
+def lora_linear_epi_fwd(X, member, act: str = "none", bias=None, residual=None, table16=None, Y=None,
+                        store_z: bool = False, ws=None):
+    """(Y, Z or None): Y = act(Z) + residual, Z = X W^T + scale (X A^T) B^T + bias, for a member as lora_group_fwd
+    takes them (W or NF4 codes and absmax, A, B, scale).  Z comes back (for the backward) when store_z.  Y may be the
+    residual."""
+    dt = L._dtype_code(X)
+    M, d_out = X.shape[0], member["B"].shape[0]
+    same = (X.dtype,)
+    m = _epi_member(X, member, (("bias", bias, same, d_out), ("residual", residual, same, M * d_out),
+                                ("Y", Y, same, M * d_out)))
+    if Y is None:
+        Y = torch.empty(M, d_out, dtype=X.dtype, device=X.device)
+    Z = torch.empty(M, d_out, dtype=X.dtype, device=X.device) if store_z else None
+    m.Y = L._ptr(Y)
+    e = L.Epilogue(_choice("act", ACTIVATIONS, act), L._ptr(bias), L._ptr(residual), L._ptr(Z))
+    tab = L._table_ptr(table16) if table16 is not None else None
+    ws = _epi_ws(False, dt, M, X.shape[1], m, e, X.device, ws)
+    with _on(X):
+        L._check("lora_linear_epi_fwd", L.lib().lora_linear_epi_fwd(
+            dt, M, X.shape[1], m, e, L._ptr(X), tab, L._ptr(ws), ws.numel(), L._stream(X.device)))
+    return Y, Z
+
+
+def lora_linear_epi_bwd(X, member, dY, act: str = "none", Z=None, need_dX: bool = True, need_dbias: bool = False,
+                        table16=None, ws=None):
+    """(dX or None, dA fp32, dB fp32, dbias fp32 or None) of lora_linear_epi_fwd; Z: its pre-activation (not needed
+    with act "none").  The residual's gradient is dY."""
+    dt = L._dtype_code(X)
+    (M, d_in), d_out, r = X.shape, member["B"].shape[0], member["A"].shape[0]
+    same = (X.dtype,)
+    m = _epi_member(X, member, (("dY", dY, same, M * d_out), ("Z", Z, same, M * d_out)))
+    dX = torch.empty(M, d_in, dtype=X.dtype, device=X.device) if need_dX else None
+    dA = torch.empty(r, d_in, dtype=torch.float32, device=X.device)
+    dB = torch.empty(d_out, r, dtype=torch.float32, device=X.device)
+    dbias = torch.empty(d_out, dtype=torch.float32, device=X.device) if need_dbias else None
+    m.dY, m.dX, m.dA, m.dB = L._ptr(dY), L._ptr(dX), L._ptr(dA), L._ptr(dB)
+    e = L.Epilogue(_choice("act", ACTIVATIONS, act), None, None, L._ptr(Z))
+    tab = L._table_ptr(table16) if table16 is not None else None
+    ws = _epi_ws(True, dt, M, d_in, m, e, X.device, ws)
+    with _on(X):
+        L._check("lora_linear_epi_bwd", L.lib().lora_linear_epi_bwd(
+            dt, M, d_in, m, e, L._ptr(X), tab, L._ptr(dbias), L._ptr(ws), ws.numel(), L._stream(X.device)))
+    return dX, dA, dB, dbias
+
+
+class LoraLinearEpiFunction(torch.autograd.Function):
+    """Y = LoraLinearEpiFunction.apply(X, W, A, B, bias, residual, scale, act): gradients for X, A, B, bias and residual
+    (W frozen; bias and residual may be None)."""
+
+    @staticmethod
+    def forward(ctx, X, W, A, B, bias, residual, scale, act="none"):
+        member = {"W": W, "A": A, "B": B, "scale": scale}
+        Y, Z = lora_linear_epi_fwd(X, member, act, bias, residual, store_z=act != "none")
+        ctx.save_for_backward(X, W, A, B, Z)
+        ctx.scale, ctx.act = scale, act
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return Y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dY):
+        X, W, A, B, Z = ctx.saved_tensors
+        dY = dY.contiguous()
+        dX, dA, dB, dbias = lora_linear_epi_bwd(X, {"W": W, "A": A, "B": B, "scale": ctx.scale}, dY, ctx.act, Z,
+                                                need_dX=ctx.needs_input_grad[0], need_dbias=ctx.needs_input_grad[4])
+        return (dX, None, dA.to(A.dtype), dB.to(B.dtype), None if dbias is None else dbias.to(ctx.bias_dtype),
+                dY if ctx.needs_input_grad[5] else None, None, None)
+
+
 class LoraLinearFunction(torch.autograd.Function):
     """Autograd wrapper: gradients for X, A and B (W frozen); A and B grads in fp32."""
 
