@@ -242,7 +242,8 @@ hipError_t launch_token_logp_grad(int elem_bytes, const void* z, int64_t ld, int
 // Losses over S packed sequences of N tokens (loss.hip): cu int64 [S + 1],
 // mask [N] or NULL.  The forward's workspace is loss_workspace(S, N, nv) bytes
 // (nv: 2 preference, 4 policy), 16-byte aligned.
-constexpr int64_t SEQ_SMALL = 8192;  // tokens up to which one block runs the whole forward
+constexpr int64_t SEQ_SMALL = 8192;  // tokens up to which one block runs the whole forward,
+constexpr int SEQ_LDS = 1024;        // and sequences whose sums it holds in LDS
 struct LossSeqs {
   const int64_t* cu;
   const uint8_t* mask;
@@ -269,7 +270,7 @@ struct PolicyLossArgs {
   float* stats;
   float* weight;
 };
-int loss_chunk(int64_t N);
+int loss_chunk_log2(int64_t N);
 size_t loss_workspace(int64_t S, int64_t N, int nv);
 hipError_t launch_pref_loss(const LossSeqs& q, const PrefLossArgs& l, void* ws, hipStream_t st);
 hipError_t launch_pref_grad(const LossSeqs& q, const float* coef, const float* dloss, float* dlogp, hipStream_t st);

@@ -252,12 +252,16 @@ hipError_t launch_token_logp_grad(int elem_bytes, const void* z, int64_t ld, int
 // The losses over packed sequences: sequence s holds the tokens [cu[s],
 // cu[s + 1]) of N.  A wave takes one chunk of `ch` consecutive tokens whatever
 // sequences it holds (so one long response costs no more than many short
-// ones), finds the first of them by a 64-way search and leaves
+// ones) and leaves
 //   seqp[s]: the part of sequence s in the chunk it starts in,
 //   head[c]: the part in chunk c of a sequence that started before it;
 // a sequence's sum is seqp[s] plus head[c] over the later chunks it reaches,
 // always in that order.  Sums are held in 64 bits: a preference margin is the
 // difference of two sums over thousands of tokens.
+// What bounds it below a million tokens is not the 17 to 21 bytes a token but
+// the chain of dependent loads, so a chunk requests its tokens' values, the
+// offsets of 64 sequences and what those sequences carry (advantage, weight,
+// coefficient) at once, and picks the sequence's value from a lane afterwards.
 // cu is read on the device and cannot be checked before the launch: every
 // index that comes from it is clipped to [0, N], and tokens outside
 // [cu[0], cu[S]) belong to no sequence.
@@ -266,8 +270,18 @@ namespace {
 
 __device__ __forceinline__ int64_t clip_tok(int64_t t, int64_t N) { return t < 0 ? 0 : (t > N ? N : t); }
 
+// lane l's value, l uniform
+__device__ __forceinline__ int pick(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
+__device__ __forceinline__ float pick(float v, int l) {
+  return __builtin_bit_cast(float, pick(__builtin_bit_cast(int, v), l));
+}
+__device__ __forceinline__ int64_t pick(int64_t v, int l) {
+  const uint32_t lo = (uint32_t)pick((int)(uint32_t)v, l), hi = (uint32_t)pick((int)(uint32_t)((uint64_t)v >> 32), l);
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
 // The number of sequences that end at or before token t (the first that ends
-// after it), by the whole wave.
+// after it), by the whole wave: a 64-way search.
 __device__ __forceinline__ int first_seq(const int64_t* cu, int S, int64_t t, int lane) {
   int lo = 0, hi = S;
   while (hi > lo) {
@@ -281,65 +295,117 @@ __device__ __forceinline__ int first_seq(const int64_t* cu, int S, int64_t t, in
   return min(lo, S);
 }
 
-// f(s, b, lo, hi): every stretch [lo, hi) of tokens of [t0, t1) that lies in
-// one sequence s (which starts at b), in order; called by the whole wave with
-// uniform arguments.  gap(lo, hi): a stretch in no sequence.
-template <class F, class G>
-__device__ __forceinline__ void walk_chunk(const int64_t* cu, int S, int64_t N, int64_t t0, int64_t t1, int lane, F&& f,
-                                           G&& gap) {
-  int base = first_seq(cu, S, t0, lane);
-  int64_t pos = t0;
-  // lane l holds the end of sequence base + l
-  while (base < S && pos < t1) {
-    const bool in = base + lane < S;
-    const int64_t end = in ? clip_tok(cu[base + lane + 1], N) : 0;
-    int64_t beg0 = clip_tok(cu[base], N);
-    unsigned long long todo;
-    while (pos < t1 && (todo = __ballot(in && end > pos)) != 0) {
-      const int l = __ffsll(todo) - 1;
-      const int64_t prev = __shfl(end, l > 0 ? l - 1 : 0);
-      const int64_t b = l > 0 ? prev : beg0, e = __shfl(end, l);
-      if (b > pos) {  // before the first sequence
-        const int64_t to = b < t1 ? b : t1;
-        gap(pos, to);
-        pos = to;
-        continue;
-      }
-      const int64_t to = e < t1 ? e : t1;
-      f(base + l, b, pos, to);
-      pos = to;
-    }
-    base += 64;
-  }
-  if (pos < t1) gap(pos, t1);  // behind the last sequence
-}
+// Walks the sequences of a stretch of tokens, by the whole wave: lane l holds
+// the end of sequence base + l and that sequence's payload.
+template <class Pay>
+struct Walk {
+  const int64_t* cu;
+  int S, lane, base;
+  int64_t N, end, beg0;
+  const float* src[Pay::NP];  // payload arrays [S] (NULL: zeros)
+  float pay[Pay::NP];
 
-__device__ __forceinline__ double wave_sum(double v) {
+  __device__ __forceinline__ void window() {
+    const int s = base + lane;
+    const bool in = s < S;
+    end = in ? clip_tok(cu[s + 1], N) : 0;  // (0: never past a position)
+    beg0 = base < S ? clip_tok(cu[base], N) : 0;
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
-
-// preference: the log-ratios and the number of counted tokens
-struct PrefTerm {
-  static constexpr int NV = 2;
-  const float* logp;
-  const float* ref;
-  __device__ __forceinline__ void add(int64_t t, int, double (&v)[NV]) const {
-    v[0] += ref ? (double)logp[t] - (double)ref[t] : (double)logp[t];
-    v[1] += 1.0;
+    for (int k = 0; k < Pay::NP; ++k) pay[k] = in && src[k] ? src[k][s] : 0.f;
+  }
+  __device__ __forceinline__ void start(int64_t t) {
+    base = S <= 64 ? 0 : first_seq(cu, S, t, lane);
+    window();
+  }
+  // The stretch [pos, to) of [pos, t1) that lies in one sequence: its index
+  // (its first token b, its lane l of the window), or -1 between sequences.
+  __device__ __forceinline__ int next(int64_t pos, int64_t t1, int64_t& to, int64_t& b, int& l) {
+    while (base < S) {
+      const unsigned long long todo = __ballot(end > pos);
+      if (todo) {
+        l = __ffsll(todo) - 1;
+        b = l > 0 ? pick(end, l - 1) : pick(beg0, 0);
+        const int64_t e = pick(end, l);
+        const int64_t stop = b > pos ? b : e;
+        to = stop < t1 ? stop : t1;
+        return b > pos ? -1 : base + l;
+      }
+      base += 64;
+      if (base < S) window();
+    }
+    to = t1;
+    return -1;
   }
 };
 
-// e^d - d - 1: its series where the three cancel (the rest is below 2e-9 of
-// the sum there), else from expm1
-__device__ __forceinline__ float kl_term(float d) {
-  if (fabsf(d) < 0.25f) {
-    const float q =
-        0.5f + d * (1.f / 6 + d * (1.f / 24 + d * (1.f / 120 + d * (1.f / 720 + d * (1.f / 5040 + d / 40320)))));
-    return d * d * q;
+__device__ __forceinline__ double pick(double v, int l) {
+  return __builtin_bit_cast(double, pick(__builtin_bit_cast(int64_t, v), l));
+}
+
+// v + the value CTRL moves here (0 where it moves none), CTRL a data-parallel
+// primitive: no trip through the LDS crossbar
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+  return v + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// The sum over the wave, to every lane: within rows of 16 lanes (shifts by
+// 1, 2, 4, 8), then lane 15 of rows 0 and 2 into rows 1 and 3, then lane 31
+// into rows 2 and 3; lane 63 has it all.
+__device__ __forceinline__ double wave_sum(double v) {
+  v = dpp_add<0x111, 0xf>(v);
+  v = dpp_add<0x112, 0xf>(v);
+  v = dpp_add<0x114, 0xf>(v);
+  v = dpp_add<0x118, 0xf>(v);
+  v = dpp_add<0x142, 0xa>(v);
+  v = dpp_add<0x143, 0xc>(v);
+  return pick(v, 63);
+}
+__device__ __forceinline__ int count(bool b) { return (int)__popcll(__ballot(b)); }
+
+// Tokens of a wave's step: 64 lanes x UT, all their loads in flight at once.
+constexpr int UT = 4, STEP = 64 * UT;
+
+// A term adds a token's values to ND sums of its lane and counts NC properties
+// over the wave; in: the token counts, in the stretch at hand.
+// preference: the log-ratios and the number of counted tokens
+struct PrefTerm {
+  static constexpr int ND = 1, NC = 1, NV = ND + NC;
+  struct Pay {
+    static constexpr int NP = 1;
+  };
+  struct Raw {
+    float lp, ref;
+  };
+  const float* logp;
+  const float* ref;
+  __device__ __forceinline__ void payload(const float* (&src)[1]) const { src[0] = nullptr; }
+  __device__ __forceinline__ Raw load(int64_t t) const { return Raw{logp[t], ref ? ref[t] : 0.f}; }
+  __device__ __forceinline__ void add(const Raw& r, bool in, const float (&)[1], double (&v)[ND], int (&n)[NC]) const {
+    v[0] += in ? (double)r.lp - (double)r.ref : 0.0;
+    n[0] += count(in);
   }
-  return expm1f(d) - d;
+};
+
+// e^x for a log-ratio x: the hardware's base-2 exponential of the rounded
+// product, (2 + |x|) 2^-24 relative
+__device__ __forceinline__ float exp_ratio(float x) { return fexp2(x * LOG2E); }
+
+// e^d - d - 1: its series where the three cancel (cut after d^9: the rest is
+// below 2e-9 of the sum)
+__device__ __forceinline__ float kl_term(float d) {
+  float q = 1.f / 362880;
+  q = __builtin_fmaf(q, d, 1.f / 40320);
+  q = __builtin_fmaf(q, d, 1.f / 5040);
+  q = __builtin_fmaf(q, d, 1.f / 720);
+  q = __builtin_fmaf(q, d, 1.f / 120);
+  q = __builtin_fmaf(q, d, 1.f / 24);
+  q = __builtin_fmaf(q, d, 1.f / 6);
+  q = __builtin_fmaf(q, d, 0.5f);
+  return fabsf(d) < 0.5f ? d * d * q : exp_ratio(d) - 1.f - d;
 }
 
 struct PolicyArgs {
@@ -351,6 +417,17 @@ struct PolicyArgs {
   double log_lo, log_hi;  // the clip borders of logp - old: log(1 - eps_low), log(1 + eps_high)
   float r_lo, r_hi;       // and of the ratio itself
   float beta;
+  struct Raw {
+    float lp, old, ref, adv;
+  };
+  __device__ __forceinline__ Raw load(int64_t t) const {
+    Raw r;
+    r.lp = logp[t];
+    r.old = old ? old[t] : r.lp;
+    r.ref = ref ? ref[t] : r.lp;
+    r.adv = adv_per_token ? adv[t] : 0.f;
+    return r;
+  }
 };
 
 // The clip borders are compared on logp - old in 64 bits, where the difference
@@ -360,25 +437,32 @@ struct PolicyTok {
   float ratio, adv;
   bool cut;  // the clipped branch holds: no gradient through the ratio
 };
-__device__ __forceinline__ PolicyTok policy_tok(const PolicyArgs& p, int64_t t, int s) {
+__device__ __forceinline__ PolicyTok policy_tok(const PolicyArgs& p, const PolicyArgs::Raw& r, float seq_adv) {
   PolicyTok k;
-  k.adv = p.adv[p.adv_per_token ? t : (int64_t)s];
-  const double d = p.old ? (double)p.logp[t] - (double)p.old[t] : 0.0;
+  k.adv = p.adv_per_token ? r.adv : seq_adv;
+  const double d = p.old ? (double)r.lp - (double)r.old : 0.0;
   const bool over = k.adv > 0.f && d > p.log_hi, under = k.adv < 0.f && d < p.log_lo;
   k.cut = over || under;
-  k.ratio = over ? p.r_hi : (under ? p.r_lo : expf((float)d));
+  k.ratio = over ? p.r_hi : (under ? p.r_lo : exp_ratio((float)d));
   return k;
 }
 
 struct PolicyTerm {
-  static constexpr int NV = 4;
+  static constexpr int ND = 2, NC = 2, NV = ND + NC;
+  struct Pay {
+    static constexpr int NP = 1;
+  };
+  using Raw = PolicyArgs::Raw;
   PolicyArgs p;
-  __device__ __forceinline__ void add(int64_t t, int s, double (&v)[NV]) const {
-    const PolicyTok k = policy_tok(p, t, s);
-    v[0] += k.adv == 0.f ? 0.0 : -((double)k.ratio * (double)k.adv);
-    if (p.ref) v[1] += (double)kl_term((float)((double)p.ref[t] - (double)p.logp[t]));
-    v[2] += k.cut ? 1.0 : 0.0;
-    v[3] += 1.0;
+  __device__ __forceinline__ void payload(const float* (&src)[1]) const { src[0] = p.adv_per_token ? nullptr : p.adv; }
+  __device__ __forceinline__ Raw load(int64_t t) const { return p.load(t); }
+  __device__ __forceinline__ void add(const Raw& r, bool in, const float (&pay)[1], double (&v)[ND],
+                                      int (&n)[NC]) const {
+    const PolicyTok k = policy_tok(p, r, pay[0]);
+    v[0] -= in && k.adv != 0.f ? (double)(k.ratio * k.adv) : 0.0;
+    if (p.ref) v[1] += in ? (double)kl_term((float)((double)r.ref - (double)r.lp)) : 0.0;
+    n[0] += count(in && k.cut);
+    n[1] += count(in);
   }
 };
 
@@ -386,39 +470,96 @@ struct SeqArgs {
   const int64_t* cu;
   const uint8_t* mask;
   int64_t N;
-  int S, ch;
+  int S, lg;  // a chunk: 2^lg tokens
   int64_t chunks;
   double* head;  // [chunks][NV]
   double* seqp;  // [S][NV]; then the sequences' sums
 };
 
 template <class Term>
-__device__ __forceinline__ void sum_chunk(const SeqArgs& a, const Term& term, int64_t c, int lane) {
-  constexpr int NV = Term::NV;
-  const int64_t t0 = c * a.ch, t1 = min(t0 + a.ch, a.N);
-  walk_chunk(
-      a.cu, a.S, a.N, t0, t1, lane,
-      [&](int s, int64_t b, int64_t lo, int64_t hi) {
-        double v[NV];
+__device__ __forceinline__ void sum_chunk(const SeqArgs& a, const Term& term, int64_t c, int lane, double* head,
+                                          double* seqp) {
+  constexpr int ND = Term::ND, NC = Term::NC, NV = Term::NV;
+  const int64_t t0 = c << a.lg, t1 = min(t0 + (int64_t(1) << a.lg), a.N);
+  Walk<typename Term::Pay> w;
+  w.cu = a.cu;
+  w.S = a.S;
+  w.N = a.N;
+  w.lane = lane;
+  term.payload(w.src);
+  typename Term::Raw raw[UT];
+  bool keep[UT];
+  auto request = [&](int64_t p) {
 #pragma unroll
-        for (int q = 0; q < NV; ++q) v[q] = 0.0;
-#pragma unroll 4
-        for (int64_t t = lo + lane; t < hi; t += 64)
-          if (!a.mask || a.mask[t]) term.add(t, s, v);
-        double* out = b < t0 ? a.head + c * NV : a.seqp + (int64_t)s * NV;
+    for (int u = 0; u < UT; ++u) {
+      const int64_t t = p + 64 * u + lane;
+      const int64_t at = t < t1 ? t : t1 - 1;  // (every lane loads, none past the chunk)
+      raw[u] = term.load(at);
+      keep[u] = t < t1 && (!a.mask || a.mask[at]);
+    }
+  };
+  request(t0);
+  w.start(t0);
+  double v[ND];
+  int n[NC];
+  int cur = -1;
+  bool cur_head = false;
+  auto clear = [&] {
 #pragma unroll
-        for (int q = 0; q < NV; ++q) {
-          v[q] = wave_sum(v[q]);
-          if (lane == 0) out[q] = v[q];
+    for (int q = 0; q < ND; ++q) v[q] = 0.0;
+#pragma unroll
+    for (int q = 0; q < NC; ++q) n[q] = 0;
+  };
+  auto flush = [&] {
+    if (cur < 0) return;
+    double* out = cur_head ? head + c * NV : seqp + (int64_t)cur * NV;
+#pragma unroll
+    for (int q = 0; q < ND; ++q) v[q] = wave_sum(v[q]);
+    if (lane == 0) {
+#pragma unroll
+      for (int q = 0; q < ND; ++q) out[q] = v[q];
+#pragma unroll
+      for (int q = 0; q < NC; ++q) out[ND + q] = (double)n[q];
+    }
+  };
+  clear();
+  for (int64_t p = t0; p < t1; p += STEP) {
+    if (p > t0) request(p);
+    const int64_t pe = min(p + STEP, t1);
+    for (int64_t pos = p; pos < pe;) {
+      int64_t to, b;
+      int l;
+      const int s = w.next(pos, pe, to, b, l);
+      if (s >= 0) {
+        if (s != cur) {
+          flush();
+          clear();
+          cur = s;
+          cur_head = b < t0;
         }
-      },
-      [](int64_t, int64_t) {});
+        float pay[1] = {pick(w.pay[0], l)};
+        const int lo = (int)(pos - p), hi = (int)(to - p);
+#pragma unroll
+        for (int u = 0; u < UT; ++u)
+          if (64 * u < hi && 64 * u + 64 > lo)  // (uniform)
+            term.add(raw[u], keep[u] && 64 * u + lane >= lo && 64 * u + lane < hi, pay, v, n);
+      }
+      pos = to;
+    }
+  }
+  flush();
 }
 
-// seqp[s] = the sum of sequence s, for every s (one block): a lane takes a
+// tot[s] = the sum of sequence s, for every s (one block): a lane takes a
 // sequence of up to 8 later chunks by itself, the wave together a longer one.
+template <int NV>
+struct alignas(16) Part {
+  double v[NV];
+};
 template <int NV, int NT>
-__device__ __forceinline__ void sum_sequences(const SeqArgs& a) {
+__device__ __forceinline__ void sum_sequences(const SeqArgs& a, const double* head, const double* seqp, double* tot) {
+  static_assert(NV % 2 == 0, "16-byte parts");
+  const Part<NV>* hp = reinterpret_cast<const Part<NV>*>(head);
   const int lane = threadIdx.x & 63;
   for (int s0 = (threadIdx.x >> 6) * 64; s0 < a.S; s0 += NT) {
     const int s = s0 + lane;
@@ -428,47 +569,61 @@ __device__ __forceinline__ void sum_sequences(const SeqArgs& a) {
       e = clip_tok(a.cu[s + 1], a.N);
     }
     const bool any = e > b;
-    const int64_t c0 = any ? b / a.ch : 0, c1 = any ? (e - 1) / a.ch : 0;
-    double v[NV];
-#pragma unroll
-    for (int q = 0; q < NV; ++q) v[q] = any ? a.seqp[(int64_t)s * NV + q] : 0.0;
+    const int64_t c0 = any ? b >> a.lg : 0, c1 = any ? (e - 1) >> a.lg : 0;
+    Part<NV> v = {};
+    if (any) v = reinterpret_cast<const Part<NV>*>(seqp)[s];
     const bool longer = c1 - c0 > 8;
-    if (!longer)
-      for (int64_t c = c0 + 1; c <= c1; ++c)
 #pragma unroll
-        for (int q = 0; q < NV; ++q) v[q] += a.head[c * NV + q];
+    for (int h = 0; h < 2; ++h) {  // 4 parts' loads in flight at a time
+      if (longer || c0 + 4 * h >= c1) continue;
+      Part<NV> x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = hp[min(c0 + 1 + 4 * h + k, c1)];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int q = 0; q < NV; ++q) v.v[q] += c0 + 1 + 4 * h + k <= c1 ? x[k].v[q] : 0.0;
+    }
     for (unsigned long long todo = __ballot(longer); todo; todo &= todo - 1) {
       const int l = __ffsll(todo) - 1;
-      const int64_t cb = __shfl(c0, l) + 1, ce = __shfl(c1, l);
+      const int64_t cb = pick(c0, l) + 1, ce = pick(c1, l);
       double w[NV];
 #pragma unroll
       for (int q = 0; q < NV; ++q) w[q] = 0.0;
-      for (int64_t c = cb + lane; c <= ce; c += 64)
+#pragma unroll 4
+      for (int64_t c = cb + lane; c <= ce; c += 64) {
+        const Part<NV> x = hp[c];
 #pragma unroll
-        for (int q = 0; q < NV; ++q) w[q] += a.head[c * NV + q];
+        for (int q = 0; q < NV; ++q) w[q] += x.v[q];
+      }
 #pragma unroll
       for (int q = 0; q < NV; ++q) {
         w[q] = wave_sum(w[q]);
-        if (lane == l) v[q] += w[q];
+        if (lane == l) v.v[q] += w[q];
       }
     }
-    if (s < a.S)
-#pragma unroll
-      for (int q = 0; q < NV; ++q) a.seqp[(int64_t)s * NV + q] = v[q];
+    if (s < a.S) reinterpret_cast<Part<NV>*>(tot)[s] = v;
   }
 }
 
-// The sum over the block's threads, to every thread; fixed order.
+// The sums of two values over the block's threads, to every thread; fixed
+// order.
 template <int NT>
-__device__ __forceinline__ double block_sum(double v, double* red) {
-  v = wave_sum(v);
+__device__ __forceinline__ void block_sum2(double& x, double& y, double* red) {
+  x = wave_sum(x);
+  y = wave_sum(y);
   __syncthreads();  // red is free
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  if ((threadIdx.x & 63) == 0) {
+    red[2 * (threadIdx.x >> 6)] = x;
+    red[2 * (threadIdx.x >> 6) + 1] = y;
+  }
   __syncthreads();
-  double t = 0.0;
+  x = y = 0.0;
 #pragma unroll
-  for (int w = 0; w < NT / 64; ++w) t += red[w];
-  return t;
+  for (int w = 0; w < NT / 64; ++w) {
+    x += red[2 * w];
+    y += red[2 * w + 1];
+  }
 }
 
 // ---- preference ----
@@ -484,13 +639,13 @@ struct PrefArgs {
 __device__ __forceinline__ double softplus(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
 
 template <int NT>
-__device__ __forceinline__ void pref_finish(const SeqArgs& a, const PrefArgs& p) {
-  __shared__ double red[NT / 64];
-  double sum = 0.0;
+__device__ __forceinline__ void finish(const PrefArgs& p, int, const double* tot) {
+  __shared__ double red[2 * NT / 64];
+  double sum = 0.0, none = 0.0;
   for (int i = threadIdx.x; i < p.P; i += NT) {
-    const double nc = a.seqp[2 * (int64_t)i + 1], nr = a.seqp[2 * ((int64_t)p.P + i) + 1];
+    const double nc = tot[2 * (int64_t)i + 1], nr = tot[2 * ((int64_t)p.P + i) + 1];
     const double wc = p.average ? 1.0 / fmax(nc, 1.0) : 1.0, wr = p.average ? 1.0 / fmax(nr, 1.0) : 1.0;
-    const double c = a.seqp[2 * (int64_t)i] * wc, r = a.seqp[2 * ((int64_t)p.P + i)] * wr;
+    const double c = tot[2 * (int64_t)i] * wc, r = tot[2 * ((int64_t)p.P + i)] * wr;
     const double u = c - r, bu = p.beta * u;
     double l, du;
     if (p.kind == 0) {
@@ -516,7 +671,7 @@ __device__ __forceinline__ void pref_finish(const SeqArgs& a, const PrefArgs& p)
     p.coef[i] = (float)(du * wc / p.P);
     p.coef[p.P + i] = (float)(-du * wr / p.P);
   }
-  sum = block_sum<NT>(sum, red);
+  block_sum2<NT>(sum, none, red);
   if (threadIdx.x == 0) *p.loss = (float)(sum / p.P);
 }
 
@@ -531,27 +686,25 @@ struct PolicyOut {
 };
 
 template <int NT>
-__device__ __forceinline__ void policy_finish(const SeqArgs& a, const PolicyOut& p) {
-  __shared__ double red[NT / 64];
+__device__ __forceinline__ void finish(const PolicyOut& p, int S, const double* tot) {
+  __shared__ double red[2 * NT / 64];
   double tok = 0.0, cut = 0.0;
-  for (int s = threadIdx.x; s < a.S; s += NT) {
-    cut += a.seqp[4 * (int64_t)s + 2];
-    tok += a.seqp[4 * (int64_t)s + 3];
+  for (int s = threadIdx.x; s < S; s += NT) {
+    cut += tot[4 * (int64_t)s + 2];
+    tok += tot[4 * (int64_t)s + 3];
   }
-  tok = block_sum<NT>(tok, red);
-  cut = block_sum<NT>(cut, red);
+  block_sum2<NT>(tok, cut, red);
   double pol = 0.0, kl = 0.0;
-  for (int s = threadIdx.x; s < a.S; s += NT) {
-    const double* v = a.seqp + 4 * (int64_t)s;
-    const double w = p.reduction == 0   ? 1.0 / (a.S * fmax(v[3], 1.0))
+  for (int s = threadIdx.x; s < S; s += NT) {
+    const double* v = tot + 4 * (int64_t)s;
+    const double w = p.reduction == 0   ? 1.0 / (S * fmax(v[3], 1.0))
                      : p.reduction == 1 ? 1.0 / fmax(tok, 1.0)
-                                        : 1.0 / (a.S * p.norm);
+                                        : 1.0 / (S * p.norm);
     pol += w * v[0];
     kl += w * v[1];
     p.weight[s] = (float)w;
   }
-  pol = block_sum<NT>(pol, red);
-  kl = block_sum<NT>(kl, red);
+  block_sum2<NT>(pol, kl, red);
   if (threadIdx.x == 0) {
     *p.loss = (float)(p.beta != 0.f ? pol + (double)p.beta * kl : pol);
     p.stats[0] = (float)pol;
@@ -561,93 +714,147 @@ __device__ __forceinline__ void policy_finish(const SeqArgs& a, const PolicyOut&
   }
 }
 
-__device__ __forceinline__ void finish(const SeqArgs& a, const PrefArgs& p) { pref_finish<1024>(a, p); }
-__device__ __forceinline__ void finish(const SeqArgs& a, const PolicyOut& p) { policy_finish<1024>(a, p); }
+constexpr int FT = 1024;  // threads of the finishing block
 
 template <class Term>
 __global__ void __launch_bounds__(256) seq_sum_kernel(const SeqArgs a, const Term term) {
   const int64_t c = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (c < a.chunks) sum_chunk(a, term, c, threadIdx.x & 63);
+  if (c < a.chunks) sum_chunk(a, term, c, threadIdx.x & 63, a.head, a.seqp);
 }
 
 template <class Term, class Out>
-__global__ void __launch_bounds__(1024) seq_finish_kernel(const SeqArgs a, const Out out) {
-  sum_sequences<Term::NV, 1024>(a);
-  __syncthreads();
-  finish(a, out);
+__global__ void __launch_bounds__(FT) seq_finish_kernel(const SeqArgs a, const Out out) {
+  constexpr int NV = Term::NV;
+  __shared__ alignas(16) double tot[SEQ_LDS * NV];
+  if (a.S <= SEQ_LDS) {
+    sum_sequences<NV, FT>(a, a.head, a.seqp, tot);
+    __syncthreads();
+    finish<FT>(out, a.S, tot);
+  } else {
+    sum_sequences<NV, FT>(a, a.head, a.seqp, a.seqp);
+    __syncthreads();
+    finish<FT>(out, a.S, a.seqp);
+  }
 }
 
-// Few tokens: one block does both (the launch between them costs more than
-// the tokens).
+// Few tokens and sequences: one block does both, the parts in LDS (the launch
+// between them costs more than the tokens).
 template <class Term, class Out>
-__global__ void __launch_bounds__(1024) seq_small_kernel(const SeqArgs a, const Term term, const Out out) {
-  for (int64_t c = threadIdx.x >> 6; c < a.chunks; c += 16) sum_chunk(a, term, c, threadIdx.x & 63);
+__global__ void __launch_bounds__(FT) seq_small_kernel(const SeqArgs a, const Term term, const Out out) {
+  constexpr int NV = Term::NV;
+  __shared__ alignas(16) double tot[SEQ_LDS * NV];
+  __shared__ alignas(16) double head[FT / 64 * NV];
+  const int c = threadIdx.x >> 6;  // (at most FT / 64 chunks)
+  if (c < a.chunks) sum_chunk(a, term, c, threadIdx.x & 63, head, tot);
   __syncthreads();
-  sum_sequences<Term::NV, 1024>(a);
+  sum_sequences<NV, FT>(a, head, tot, tot);
   __syncthreads();
-  finish(a, out);
+  finish<FT>(out, a.S, tot);
 }
 
 template <class Term, class Out>
-hipError_t run_seq(const SeqArgs& a, const Term& term, const Out& out, hipStream_t st) {
-  if (a.N <= SEQ_SMALL) {
-    hipLaunchKernelGGL((seq_small_kernel<Term, Out>), dim3(1), dim3(1024), 0, st, a, term, out);
+hipError_t run_seq(SeqArgs a, const Term& term, const Out& out, hipStream_t st) {
+  if (a.N <= SEQ_SMALL && a.S <= SEQ_LDS) {
+    // a chunk for every wave of the one block, of 64 tokens at least
+    a.lg = 6;
+    while ((int64_t(FT / 64) << a.lg) < a.N) ++a.lg;
+    a.chunks = (a.N + (int64_t(1) << a.lg) - 1) >> a.lg;
+    hipLaunchKernelGGL((seq_small_kernel<Term, Out>), dim3(1), dim3(FT), 0, st, a, term, out);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((seq_sum_kernel<Term>), dim3((unsigned)((a.chunks + 3) / 4)), dim3(256), 0, st, a, term);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((seq_finish_kernel<Term, Out>), dim3(1), dim3(1024), 0, st, a, out);
+  if (a.chunks > 0) {
+    hipLaunchKernelGGL((seq_sum_kernel<Term>), dim3((unsigned)((a.chunks + 3) / 4)), dim3(256), 0, st, a, term);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((seq_finish_kernel<Term, Out>), dim3(1), dim3(FT), 0, st, a, out);
   return hipGetLastError();
 }
 
 // ---- gradients: one wave per chunk, dlogp of every token of [0, N) ----
-__global__ void __launch_bounds__(256) pref_grad_kernel(const SeqArgs a, const float* __restrict__ coef,
-                                                        const float* __restrict__ dloss, float* __restrict__ dlogp) {
+// payload 0: the sequence's coefficient or weight, 1: its advantage.
+struct GradPay {
+  static constexpr int NP = 2;
+};
+
+// f(raw, payload) of every counted token in a sequence, 0 elsewhere.
+template <class Load, class F>
+__device__ __forceinline__ void grad_chunk(const SeqArgs& a, const float* pay0, const float* pay1, float* dlogp,
+                                           Load&& load, F&& f) {
   const int lane = threadIdx.x & 63;
   const int64_t c = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (c >= a.chunks) return;
-  const int64_t t0 = c * a.ch, t1 = min(t0 + a.ch, a.N);
+  const int64_t t0 = c << a.lg, t1 = min(t0 + (int64_t(1) << a.lg), a.N);
+  Walk<GradPay> w;
+  w.cu = a.cu;
+  w.S = a.S;
+  w.N = a.N;
+  w.lane = lane;
+  w.src[0] = pay0;
+  w.src[1] = pay1;
+  decltype(load(t0)) raw[UT];
+  bool keep[UT];
+  auto request = [&](int64_t p) {
+#pragma unroll
+    for (int u = 0; u < UT; ++u) {
+      const int64_t t = p + 64 * u + lane;
+      const int64_t at = t < t1 ? t : t1 - 1;
+      raw[u] = load(at);
+      keep[u] = t < t1 && (!a.mask || a.mask[at]);
+    }
+  };
+  request(t0);
+  w.start(t0);
+  for (int64_t p = t0; p < t1; p += STEP) {
+    if (p > t0) request(p);
+    const int64_t pe = min(p + STEP, t1);
+    float d[UT];
+#pragma unroll
+    for (int u = 0; u < UT; ++u) d[u] = 0.f;
+    for (int64_t pos = p; pos < pe;) {
+      int64_t to, b;
+      int l;
+      if (w.next(pos, pe, to, b, l) >= 0) {
+        const float q0 = pick(w.pay[0], l), q1 = pick(w.pay[1], l);
+        const int lo = (int)(pos - p), hi = (int)(to - p);
+#pragma unroll
+        for (int u = 0; u < UT; ++u)
+          if (64 * u < hi && 64 * u + 64 > lo) {  // (uniform)
+            const float x = f(raw[u], q0, q1);
+            if (keep[u] && 64 * u + lane >= lo && 64 * u + lane < hi) d[u] = x;
+          }
+      }
+      pos = to;
+    }
+#pragma unroll
+    for (int u = 0; u < UT; ++u) {
+      const int64_t t = p + 64 * u + lane;
+      if (t < t1) dlogp[t] = d[u];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256) pref_grad_kernel(const SeqArgs a, const float* __restrict__ coef,
+                                                        const float* __restrict__ dloss, float* __restrict__ dlogp) {
   const float g = dloss ? *dloss : 1.f;
-  walk_chunk(
-      a.cu, a.S, a.N, t0, t1, lane,
-      [&](int s, int64_t, int64_t lo, int64_t hi) {
-        const float w = g * coef[s];
-#pragma unroll 4
-        for (int64_t t = lo + lane; t < hi; t += 64) dlogp[t] = (!a.mask || a.mask[t]) ? w : 0.f;
-      },
-      [&](int64_t lo, int64_t hi) {
-        for (int64_t t = lo + lane; t < hi; t += 64) dlogp[t] = 0.f;
-      });
+  grad_chunk(a, coef, nullptr, dlogp, [](int64_t) { return 0; }, [&](int, float q, float) { return g * q; });
 }
 
 __global__ void __launch_bounds__(256) policy_grad_kernel(const SeqArgs a, const PolicyArgs p,
                                                           const float* __restrict__ weight,
                                                           const float* __restrict__ dloss, float* __restrict__ dlogp) {
-  const int lane = threadIdx.x & 63;
-  const int64_t c = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (c >= a.chunks) return;
-  const int64_t t0 = c * a.ch, t1 = min(t0 + a.ch, a.N);
   const float g = dloss ? *dloss : 1.f;
-  walk_chunk(
-      a.cu, a.S, a.N, t0, t1, lane,
-      [&](int s, int64_t, int64_t lo, int64_t hi) {
-        const float w = g * weight[s];
-#pragma unroll 4
-        for (int64_t t = lo + lane; t < hi; t += 64) {
-          float d = 0.f;
-          if (!a.mask || a.mask[t]) {
-            const PolicyTok k = policy_tok(p, t, s);
-            if (!k.cut && k.adv != 0.f) d = -k.ratio * k.adv;
-            if (p.beta != 0.f) d -= p.beta * expm1f((float)((double)p.ref[t] - (double)p.logp[t]));
-            d *= w;
-          }
-          dlogp[t] = d;
-        }
-      },
-      [&](int64_t lo, int64_t hi) {
-        for (int64_t t = lo + lane; t < hi; t += 64) dlogp[t] = 0.f;
-      });
+  grad_chunk(a, weight, p.adv_per_token ? nullptr : p.adv, dlogp, [&](int64_t t) { return p.load(t); },
+             [&](const PolicyArgs::Raw& r, float w, float adv) {
+               const PolicyTok k = policy_tok(p, r, adv);
+               float d = 0.f;
+               if (!k.cut && k.adv != 0.f) d = -k.ratio * k.adv;
+               if (p.beta != 0.f) {  // e^d - 1 = d + (e^d - d - 1)
+                 const float x = (float)((double)r.ref - (double)r.lp);
+                 d -= p.beta * (x + kl_term(x));
+               }
+               return g * w * d;
+             });
 }
 
 SeqArgs seq_args(const LossSeqs& q, void* ws, int nv) {
@@ -656,8 +863,8 @@ SeqArgs seq_args(const LossSeqs& q, void* ws, int nv) {
   a.mask = q.mask;
   a.N = q.N;
   a.S = (int)q.S;
-  a.ch = loss_chunk(q.N);
-  a.chunks = (q.N + a.ch - 1) / a.ch;
+  a.lg = loss_chunk_log2(q.N);
+  a.chunks = (q.N + (int64_t(1) << a.lg) - 1) >> a.lg;
   a.head = static_cast<double*>(ws);
   a.seqp = a.head + a.chunks * nv;
   return a;
@@ -680,16 +887,17 @@ PolicyArgs policy_args(const PolicyLossArgs& q) {
 
 }  // namespace
 
-// Tokens per wave: about 2048 waves (two per SIMD), at least a wave's 4 rounds
-// of 64 and at most 4096.
-int loss_chunk(int64_t N) {
-  const int64_t c = ((N + 2047) / 2048 + 63) / 64 * 64;
-  return (int)std::min<int64_t>(4096, std::max<int64_t>(256, c));
+// Tokens per wave: one step of 256 while that gives at most 8192 waves (all
+// that are resident at once), then twice as many, up to 4096.
+int loss_chunk_log2(int64_t N) {
+  int lg = 8;
+  while (lg < 12 && (N >> lg) > 8192) ++lg;
+  return lg;
 }
 
 size_t loss_workspace(int64_t S, int64_t N, int nv) {
-  const int64_t ch = loss_chunk(N);
-  return (size_t)((N + ch - 1) / ch + S) * nv * sizeof(double);
+  const int lg = loss_chunk_log2(N);
+  return (size_t)(((N + (int64_t(1) << lg) - 1) >> lg) + S) * nv * sizeof(double);
 }
 
 hipError_t launch_pref_loss(const LossSeqs& q, const PrefLossArgs& l, void* ws, hipStream_t st) {

@@ -433,21 +433,34 @@ def lora_swiglu_bwd(X, members, dH, G, U, table16=None, need_dX: bool = True, ws
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 
-def _epi_member(X, member, more):
-    """The ctypes member of a projection, its tensors checked against X's device and dtype."""
+def _epi_member(X, member):
+    """(device, M, d_in, d_out, r, the ctypes member) of a projection, its tensors checked against X."""
+    dev, same = _gpu(X), (X.dtype,)
     if X.dim() != 2:
         raise ValueError("X must be [M, d_in]")
-    same = (X.dtype,)
-    _check_on(X, ("X", X, same, None), ("A", member["A"], same, None), ("B", member["B"], same, None),
-              ("W", member.get("W"), same, None), ("W_t", member.get("W_t"), (torch.bfloat16,), None),
-              ("codes", member.get("codes"), (torch.uint8,), None),
-              ("absmax", member.get("absmax"), (torch.float32,), None), *more)
-    arr = _group_members(X, [member])
-    codes, n = member.get("codes"), X.shape[1] * arr[0].d_out
-    if codes is not None and (codes.numel() * 2 != n or member.get("absmax") is None
-                              or member["absmax"].numel() * 64 != n):
-        raise ValueError("codes must hold d_out * d_in / 2 bytes and absmax d_out * d_in / 64 values")
-    return arr[0]
+    A, B, W, codes, absmax, Wt = (member.get(k) for k in ("A", "B", "W", "codes", "absmax", "W_t"))
+    (M, d_in), r, d_out = X.shape, A.shape[0], B.shape[0]
+    _check(dev, "X", X, same)
+    _check(dev, "A", A, same, r * d_in)
+    _check(dev, "B", B, same, d_out * r)
+    if (W is None) == (codes is None):
+        raise ValueError("a member takes exactly one of W and NF4 codes")
+    if A.dim() != 2 or B.dim() != 2 or (W is not None and W.shape != (d_out, d_in)):
+        raise ValueError("shape mismatch: X [M,d_in], W [d_out,d_in], A [r,d_in], B [d_out,r]")
+    if W is not None:
+        _check(dev, "W", W, same)
+    else:
+        _check(dev, "codes", codes, (torch.uint8,), d_out * d_in // 2)
+        if absmax is None:
+            raise ValueError("codes need absmax")
+        _check(dev, "absmax", absmax, _F32, d_out * d_in // 64)
+    if Wt is not None:
+        _check(dev, "W_t", Wt, (torch.bfloat16,), d_out * d_in)
+        if Wt.shape != (d_in, d_out):
+            raise ValueError("W_t must be the bf16 [d_in, d_out] transpose of W")
+    m = L.GroupMember(d_out, r, member["scale"], 1 if member.get("rope") else 0, L._ptr(W), L._ptr(codes),
+                      L._ptr(absmax), L._ptr(A), L._ptr(B), None, None, None, None, None, L._ptr(Wt))
+    return dev, M, d_in, d_out, r, m
 
 
 def _epi_ws(backward, dt, M, d_in, m, e, device, ws):
@@ -463,20 +476,24 @@ def lora_linear_epi_fwd(X, member, act: str = "none", bias=None, residual=None, 
     takes them (W or NF4 codes and absmax, A, B, scale).  Z comes back (for the backward) when store_z.  Y may be the
     residual."""
     dt = L._dtype_code(X)
-    M, d_out = X.shape[0], member["B"].shape[0]
+    dev, M, d_in, d_out, r, m = _epi_member(X, member)
     same = (X.dtype,)
-    m = _epi_member(X, member, (("bias", bias, same, d_out), ("residual", residual, same, M * d_out),
-                                ("Y", Y, same, M * d_out)))
+    if bias is not None:
+        _check(dev, "bias", bias, same, d_out)
+    if residual is not None:
+        _check(dev, "residual", residual, same, M * d_out)
     if Y is None:
-        Y = torch.empty(M, d_out, dtype=X.dtype, device=X.device)
-    Z = torch.empty(M, d_out, dtype=X.dtype, device=X.device) if store_z else None
+        Y = torch.empty(M, d_out, dtype=X.dtype, device=dev)
+    else:
+        _check(dev, "Y", Y, same, M * d_out)
+    Z = torch.empty(M, d_out, dtype=X.dtype, device=dev) if store_z else None
     m.Y = L._ptr(Y)
     e = L.Epilogue(_choice("act", ACTIVATIONS, act), L._ptr(bias), L._ptr(residual), L._ptr(Z))
     tab = L._table_ptr(table16) if table16 is not None else None
-    ws = _epi_ws(False, dt, M, X.shape[1], m, e, X.device, ws)
-    with _on(X):
+    ws = _epi_ws(False, dt, M, d_in, m, e, dev, ws)
+    with _on(dev):
         L._check("lora_linear_epi_fwd", L.lib().lora_linear_epi_fwd(
-            dt, M, X.shape[1], m, e, L._ptr(X), tab, L._ptr(ws), ws.numel(), L._stream(X.device)))
+            dt, M, d_in, m, e, L._ptr(X), tab, L._ptr(ws), ws.numel(), L._stream(dev)))
     return Y, Z
 
 
@@ -485,20 +502,22 @@ def lora_linear_epi_bwd(X, member, dY, act: str = "none", Z=None, need_dX: bool 
     """(dX or None, dA fp32, dB fp32, dbias fp32 or None) of lora_linear_epi_fwd; Z: its pre-activation (not needed
     with act "none").  The residual's gradient is dY."""
     dt = L._dtype_code(X)
-    (M, d_in), d_out, r = X.shape, member["B"].shape[0], member["A"].shape[0]
+    dev, M, d_in, d_out, r, m = _epi_member(X, member)
     same = (X.dtype,)
-    m = _epi_member(X, member, (("dY", dY, same, M * d_out), ("Z", Z, same, M * d_out)))
-    dX = torch.empty(M, d_in, dtype=X.dtype, device=X.device) if need_dX else None
-    dA = torch.empty(r, d_in, dtype=torch.float32, device=X.device)
-    dB = torch.empty(d_out, r, dtype=torch.float32, device=X.device)
-    dbias = torch.empty(d_out, dtype=torch.float32, device=X.device) if need_dbias else None
+    _check(dev, "dY", dY, same, M * d_out)
+    if Z is not None:
+        _check(dev, "Z", Z, same, M * d_out)
+    dX = torch.empty(M, d_in, dtype=X.dtype, device=dev) if need_dX else None
+    dA = torch.empty(r, d_in, dtype=torch.float32, device=dev)
+    dB = torch.empty(d_out, r, dtype=torch.float32, device=dev)
+    dbias = torch.empty(d_out, dtype=torch.float32, device=dev) if need_dbias else None
     m.dY, m.dX, m.dA, m.dB = L._ptr(dY), L._ptr(dX), L._ptr(dA), L._ptr(dB)
     e = L.Epilogue(_choice("act", ACTIVATIONS, act), None, None, L._ptr(Z))
     tab = L._table_ptr(table16) if table16 is not None else None
-    ws = _epi_ws(True, dt, M, d_in, m, e, X.device, ws)
-    with _on(X):
+    ws = _epi_ws(True, dt, M, d_in, m, e, dev, ws)
+    with _on(dev):
         L._check("lora_linear_epi_bwd", L.lib().lora_linear_epi_bwd(
-            dt, M, d_in, m, e, L._ptr(X), tab, L._ptr(dbias), L._ptr(ws), ws.numel(), L._stream(X.device)))
+            dt, M, d_in, m, e, L._ptr(X), tab, L._ptr(dbias), L._ptr(ws), ws.numel(), L._stream(dev)))
     return dX, dA, dB, dbias
 
 
@@ -545,28 +564,43 @@ class LoraLinearFunction(torch.autograd.Function):
 # ---------------------------------------------------------------------------
 # token log-probabilities and the losses that read them
 # ---------------------------------------------------------------------------
-def _on(t):
-    """The device of t made current where it is not (launches go to the current device)."""
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+class _OtherDevice:
+    """Makes a device current for one call (launches go to the current device)."""
+
+    def __init__(self, index):
+        self.index = index
+
+    def __enter__(self):
+        self.back = torch.cuda.current_device()
+        torch.cuda.set_device(self.index)
+
+    def __exit__(self, *_):
+        torch.cuda.set_device(self.back)
 
 
-def _check_on(first, *named):
-    """Every (name, tensor or None, dtypes, numel or None): on first's GPU, contiguous, of a dtype and size."""
-    if not first.is_cuda:
+_HERE = contextlib.nullcontext()
+
+
+def _on(device):
+    return _HERE if device.index == torch.cuda.current_device() else _OtherDevice(device.index)
+
+
+def _check(device, name, t, dtypes, numel=None):
+    """t is on the device, contiguous, of one of the dtypes and of numel values."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} has {t.numel()} values, not {numel}")
+
+
+def _gpu(t):
+    if not t.is_cuda:
         raise ValueError("tensors must be on a GPU")
-    for name, t, dtypes, numel in named:
-        if t is None:
-            continue
-        if t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
-        if t.dtype not in dtypes:
-            raise TypeError(f"{name} has dtype {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
-        if numel is not None and t.numel() != numel:
-            raise ValueError(f"{name} has {t.numel()} values, not {numel}")
+    return t.device
 
 
 _F32, _I64, _MASK = (torch.float32,), (torch.int64,), (torch.bool, torch.uint8)
@@ -585,31 +619,36 @@ def lora_token_logp_fwd(logits, targets, inv_temp: float = 1.0):
     """(logp fp32 [n], stats fp32 [n, 2]) of int64 targets [n] under the rows of logits [n, vocab] (rows may be
     strided); stats holds each row's maximum logit and the log of its shifted sum, which the backward takes."""
     n, vocab, ld = _logits_ld("logits", logits)
-    _check_on(logits, ("targets", targets, _I64, n))
+    dev = _gpu(logits)
+    _check(dev, "targets", targets, _I64, n)
     dt = L._dtype_code(logits)
-    logp = torch.empty(n, dtype=torch.float32, device=logits.device)
-    stats = torch.empty(n, 2, dtype=torch.float32, device=logits.device)
-    with _on(logits):
+    logp = torch.empty(n, dtype=torch.float32, device=dev)
+    stats = torch.empty(n, 2, dtype=torch.float32, device=dev)
+    with _on(dev):
         L._check("lora_token_logp_fwd", L.lib().lora_token_logp_fwd(
             dt, n, vocab, L._ptr(logits), ld, L._ptr(targets), float(inv_temp), L._ptr(logp), L._ptr(stats),
-            L._stream(logits.device)))
+            L._stream(dev)))
     return logp, stats
 
 
 def lora_token_logp_bwd(logits, targets, stats, dlogp, inv_temp: float = 1.0, dlogits=None):
     """dlogits in the dtype of logits for the upstream gradient dlogp fp32 [n]; dlogits may be logits itself."""
     n, vocab, ld = _logits_ld("logits", logits)
-    _check_on(logits, ("targets", targets, _I64, n), ("stats", stats, _F32, 2 * n), ("dlogp", dlogp, _F32, n))
+    dev = _gpu(logits)
+    _check(dev, "targets", targets, _I64, n)
+    _check(dev, "stats", stats, _F32, 2 * n)
+    _check(dev, "dlogp", dlogp, _F32, n)
     dt = L._dtype_code(logits)
     if dlogits is None:
-        dlogits = torch.empty(n, vocab, dtype=logits.dtype, device=logits.device)
-    nd, vd, ldd = _logits_ld("dlogits", dlogits)
-    if (nd, vd) != (n, vocab) or dlogits.dtype != logits.dtype or dlogits.device != logits.device:
-        raise ValueError("dlogits must have the shape, dtype and device of logits")
-    with _on(logits):
+        dlogits, ldd = torch.empty(n, vocab, dtype=logits.dtype, device=dev), vocab
+    else:
+        nd, vd, ldd = _logits_ld("dlogits", dlogits)
+        if (nd, vd) != (n, vocab) or dlogits.dtype != logits.dtype or dlogits.device != dev:
+            raise ValueError("dlogits must have the shape, dtype and device of logits")
+    with _on(dev):
         L._check("lora_token_logp_bwd", L.lib().lora_token_logp_bwd(
             dt, n, vocab, L._ptr(logits), ld, L._ptr(targets), float(inv_temp), L._ptr(stats), L._ptr(dlogp),
-            L._ptr(dlogits), ldd, L._stream(logits.device)))
+            L._ptr(dlogits), ldd, L._stream(dev)))
     return dlogits
 
 
@@ -629,81 +668,96 @@ def _choice(name, table, value):
     return table[value]
 
 
+def _check_tokens(dev, n, cu, ref_logp, mask):
+    _check(dev, "cu", cu, _I64)
+    if ref_logp is not None:
+        _check(dev, "ref_logp", ref_logp, _F32, n)
+    if mask is not None:
+        _check(dev, "mask", mask, _MASK, n)
+
+
 def lora_preference_loss_fwd(logp, cu, beta: float, ref_logp=None, mask=None, kind: str = "sigmoid",
                              label_smoothing: float = 0.0, average: bool = False, ws=None):
     """(loss, pair_loss [P], rewards [2 P], coef [2 P]) of P pairs over packed sequences: logp (and ref_logp) fp32
     [n], cu int64 [2 P + 1] with the chosen responses first, then the rejected ones in the same order; mask bool or
     uint8 [n] (tokens that count).  coef goes to lora_preference_loss_bwd."""
-    n = logp.numel()
-    _check_on(logp, ("logp", logp, _F32, n), ("cu", cu, _I64, None), ("ref_logp", ref_logp, _F32, n),
-              ("mask", mask, _MASK, n))
-    if cu.numel() < 3 or cu.numel() % 2 == 0:
+    n, dev = logp.numel(), _gpu(logp)
+    _check(dev, "logp", logp, _F32)
+    _check_tokens(dev, n, cu, ref_logp, mask)
+    S = cu.numel() - 1
+    if S < 2 or S % 2:
         raise ValueError("cu must hold 2 P + 1 offsets")
-    P = (cu.numel() - 1) // 2
-    new = lambda *s: torch.empty(*s, dtype=torch.float32, device=logp.device)  # noqa: E731
-    loss, pair_loss, rewards, coef = new(()), new(P), new(2 * P), new(2 * P)
-    ws = _loss_ws(0, 2 * P, n, logp.device, ws)
-    with _on(logp):
+    P = S // 2
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    pair_loss, rewards, coef = torch.empty(5 * P, dtype=torch.float32, device=dev).split((P, S, S))
+    ws = _loss_ws(0, S, n, dev, ws)
+    with _on(dev):
         L._check("lora_preference_loss_fwd", L.lib().lora_preference_loss_fwd(
             _choice("kind", PREFERENCE_KINDS, kind), P, n, float(beta), float(label_smoothing), int(average),
             L._ptr(cu), L._ptr(mask), L._ptr(logp), L._ptr(ref_logp), L._ptr(loss), L._ptr(pair_loss),
-            L._ptr(rewards), L._ptr(coef), L._ptr(ws), ws.numel(), L._stream(logp.device)))
+            L._ptr(rewards), L._ptr(coef), L._ptr(ws), ws.numel(), L._stream(dev)))
     return loss, pair_loss, rewards, coef
 
 
 def lora_preference_loss_bwd(coef, cu, n_tokens: int, mask=None, dloss=None):
     """dlogp fp32 [n_tokens] of lora_preference_loss_fwd; dloss: fp32 scalar tensor (None: 1)."""
-    _check_on(coef, ("coef", coef, _F32, cu.numel() - 1), ("cu", cu, _I64, None), ("mask", mask, _MASK, n_tokens),
-              ("dloss", dloss, _F32, 1))
-    dlogp = torch.empty(n_tokens, dtype=torch.float32, device=coef.device)
-    with _on(coef):
+    dev = _gpu(coef)
+    _check(dev, "coef", coef, _F32, cu.numel() - 1)
+    _check_tokens(dev, n_tokens, cu, None, mask)
+    if dloss is not None:
+        _check(dev, "dloss", dloss, _F32, 1)
+    dlogp = torch.empty(n_tokens, dtype=torch.float32, device=dev)
+    with _on(dev):
         L._check("lora_preference_loss_bwd", L.lib().lora_preference_loss_bwd(
             coef.numel() // 2, n_tokens, L._ptr(cu), L._ptr(mask), L._ptr(coef), L._ptr(dloss), L._ptr(dlogp),
-            L._stream(coef.device)))
+            L._stream(dev)))
     return dlogp
 
 
-def _policy_checks(logp, cu, advantages, old_logp, ref_logp, mask, per_token, more=()):
-    n, S = logp.numel(), cu.numel() - 1
+def _policy_checks(logp, cu, advantages, old_logp, ref_logp, mask, per_token):
+    n, S, dev = logp.numel(), cu.numel() - 1, _gpu(logp)
     if S < 1:
         raise ValueError("cu must hold S + 1 offsets")
-    _check_on(logp, ("logp", logp, _F32, n), ("cu", cu, _I64, None),
-              ("advantages", advantages, _F32, n if per_token else S), ("old_logp", old_logp, _F32, n),
-              ("ref_logp", ref_logp, _F32, n), ("mask", mask, _MASK, n), *more)
-    return n, S
+    _check(dev, "logp", logp, _F32)
+    _check_tokens(dev, n, cu, ref_logp, mask)
+    _check(dev, "advantages", advantages, _F32, n if per_token else S)
+    if old_logp is not None:
+        _check(dev, "old_logp", old_logp, _F32, n)
+    return n, S, dev
 
 
 def lora_policy_loss_fwd(logp, cu, advantages, old_logp=None, ref_logp=None, mask=None, eps_low: float = 0.2,
                          eps_high: float = 0.2, beta: float = 0.0, reduction: str = "sequence", norm: float = 1.0,
                          per_token: bool = False, ws=None):
     """(loss, stats [4], weight [S]) of the clipped policy loss over packed sequences: logp (old_logp, ref_logp)
-    fp32 [n], cu int64 [S + 1], advantages fp32 [S], or [n] with per_token; stats: the policy part, the KL part, the share of
-    clipped tokens, the number of tokens.  weight goes to lora_policy_loss_bwd."""
-    n, S = _policy_checks(logp, cu, advantages, old_logp, ref_logp, mask, per_token)
-    new = lambda *s: torch.empty(*s, dtype=torch.float32, device=logp.device)  # noqa: E731
-    loss, stats, weight = new(()), new(4), new(S)
-    ws = _loss_ws(1, S, n, logp.device, ws)
-    with _on(logp):
+    fp32 [n], cu int64 [S + 1], advantages fp32 [S], or [n] with per_token; stats: the policy part, the KL part, the
+    share of clipped tokens, the number of tokens.  weight goes to lora_policy_loss_bwd."""
+    n, S, dev = _policy_checks(logp, cu, advantages, old_logp, ref_logp, mask, per_token)
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    stats, weight = torch.empty(4 + S, dtype=torch.float32, device=dev).split((4, S))
+    ws = _loss_ws(1, S, n, dev, ws)
+    with _on(dev):
         L._check("lora_policy_loss_fwd", L.lib().lora_policy_loss_fwd(
             _choice("reduction", POLICY_REDUCTIONS, reduction), S, n, float(eps_low), float(eps_high), float(beta),
             float(norm), L._ptr(cu), L._ptr(mask), L._ptr(logp), L._ptr(old_logp), L._ptr(ref_logp),
             L._ptr(advantages), int(per_token), L._ptr(loss), L._ptr(stats), L._ptr(weight), L._ptr(ws), ws.numel(),
-            L._stream(logp.device)))
+            L._stream(dev)))
     return loss, stats, weight
 
 
 def lora_policy_loss_bwd(logp, cu, advantages, weight, old_logp=None, ref_logp=None, mask=None, eps_low: float = 0.2,
-                         eps_high: float = 0.2, beta: float = 0.0, per_token: bool = False,
-                         dloss=None):
+                         eps_high: float = 0.2, beta: float = 0.0, per_token: bool = False, dloss=None):
     """dlogp fp32 [n] of lora_policy_loss_fwd, given its weight and the same inputs; dloss: fp32 scalar tensor."""
-    n, S = _policy_checks(logp, cu, advantages, old_logp, ref_logp, mask, per_token,
-                          (("dloss", dloss, _F32, 1), ("weight", weight, _F32, cu.numel() - 1)))
-    dlogp = torch.empty(n, dtype=torch.float32, device=logp.device)
-    with _on(logp):
+    n, S, dev = _policy_checks(logp, cu, advantages, old_logp, ref_logp, mask, per_token)
+    _check(dev, "weight", weight, _F32, S)
+    if dloss is not None:
+        _check(dev, "dloss", dloss, _F32, 1)
+    dlogp = torch.empty(n, dtype=torch.float32, device=dev)
+    with _on(dev):
         L._check("lora_policy_loss_bwd", L.lib().lora_policy_loss_bwd(
             S, n, float(eps_low), float(eps_high), float(beta), L._ptr(cu), L._ptr(mask), L._ptr(logp),
             L._ptr(old_logp), L._ptr(ref_logp), L._ptr(advantages), int(per_token), L._ptr(weight), L._ptr(dloss),
-            L._ptr(dlogp), L._stream(logp.device)))
+            L._ptr(dlogp), L._stream(dev)))
     return dlogp
 
 
