@@ -1471,7 +1471,7 @@ int swiglu_backward(int dtype, int64_t M, int64_t d_in, const lora_group_member*
 // one projection with bias, activation and residual
 // ---------------------------------------------------------------------------
 // Backward: the layer's own layout, then dZ (with an activation) and the bias
-// gradient's partials over up to 64 ranges of at least 64 tokens.
+// gradient's partials over up to 64 ranges of the tokens.
 struct EpiLayout {
   Layout L;
   size_t dz = 0, part = 0, total = 0;
@@ -1491,7 +1491,8 @@ EpiLayout make_epi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, const lo
       return at;
     };
     if (e.act != LORA_ACT_NONE) E.dz = take(size_t(M) * m.d_out * elem_bytes(dtype));
-    E.chunks = (int)std::min<int64_t>(64, cdiv(M, 64));
+    // about two blocks of 256 columns a CU, at least 8 tokens each
+    E.chunks = (int)std::max<int64_t>(1, std::min<int64_t>({64, cdiv(M, 8), cdiv(512, cdiv(m.d_out, 256))}));
     E.part = take(size_t(E.chunks) * m.d_out * 4);
   }
   return E;
@@ -1951,7 +1952,7 @@ int lora_linear_epi_bwd(int dtype, int64_t M, int64_t d_in, const lora_group_mem
     if (act) dZ = w + E.dz;
     if (dbias)
       HIPTRY(timed(K_REDUCE, double(E.chunks) * m.d_out, 4.0 * (E.chunks + 1) * m.d_out, st, [&] {
-        return launch_reduce_splits(part, E.chunks, 1, m.d_out, m.d_out, false, dbias, st);
+        return launch_bias_grad(part, E.chunks, m.d_out, dbias, st);
       }));
   } else if (dbias) {
     HIPTRY(timed(K_FILL, 0, 4.0 * m.d_out, st, [&] { return launch_fill_zero(dbias, m.d_out, st); }));

@@ -123,6 +123,30 @@ __device__ __forceinline__ void act_all(float (&v)[N], int act) {
   }
 }
 
+// g *= act'(z)
+template <bool FAST, int N>
+__device__ __forceinline__ void act_grad_all(float (&g)[N], const float (&z)[N], int act) {
+  switch (act) {
+    case ACT_RELU:
+#pragma unroll
+      for (int e = 0; e < N; ++e) g[e] *= act_grad<FAST>(z[e], ACT_RELU);
+      break;
+    case ACT_SILU:
+#pragma unroll
+      for (int e = 0; e < N; ++e) g[e] *= act_grad<FAST>(z[e], ACT_SILU);
+      break;
+    case ACT_GELU:
+#pragma unroll
+      for (int e = 0; e < N; ++e) g[e] *= act_grad<FAST>(z[e], ACT_GELU);
+      break;
+    case ACT_GELU_TANH:
+#pragma unroll
+      for (int e = 0; e < N; ++e) g[e] *= act_grad<FAST>(z[e], ACT_GELU_TANH);
+      break;
+    default: break;
+  }
+}
+
 // N consecutive elements (N = 4 or 8) of a T array (bf16 patterns or fp32) at
 // an address aligned to N elements (16 bytes where that is less) as floats,
 // and back

@@ -709,7 +709,8 @@ hipError_t launch_split_finish_epi(const float* part, int splits, int64_t part_s
 // written without an activation, where dZ is dY), and the bias gradient's
 // partial sums over the tokens.  A block takes 256 columns (8 a thread, 32
 // threads a row) and `rows` tokens, 8 of them at a time; its column sums,
-// joined over its 8 row groups in order, go to part[blockIdx.y][N].
+// joined over its 8 row groups in order, go to part[blockIdx.y][N].  The loads
+// of 4 of a thread's rows are in flight at once.
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(256) epi_grad_kernel(const T* __restrict__ dY, const T* __restrict__ Z,
@@ -722,20 +723,26 @@ __global__ void __launch_bounds__(256) epi_grad_kernel(const T* __restrict__ dY,
   float s[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) s[e] = 0.f;
+  constexpr int U = 4;
   if (col < N) {
-    for (int64_t m = m0 + rg; m < m1; m += 8) {
-      const int64_t o = m * N + col;
-      float g[8];
-      epi_load(dY + o, g);
-      if (act != ACT_NONE) {
-        float z[8];
-        epi_load(Z + o, z);
+    for (int64_t m = m0 + rg; m < m1; m += 8 * U) {
+      float g[U][8], z[U][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] *= act_grad<sizeof(T) == 2>(z[e], act);
-        epi_store(dZ + o, g);
+      for (int u = 0; u < U; ++u) {
+        const int64_t o = min(m + 8 * u, m1 - 1) * N + col;
+        epi_load(dY + o, g[u]);
+        if (act != ACT_NONE) epi_load(Z + o, z[u]);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] += g[e];
+      for (int u = 0; u < U; ++u) {
+        if (m + 8 * u >= m1) continue;
+        if (act != ACT_NONE) {
+          act_grad_all<sizeof(T) == 2>(g[u], z[u], act);
+          epi_store(dZ + (m + 8 * u) * N + col, g[u]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] += g[u][e];
+      }
     }
   }
   if (!part) return;
@@ -748,6 +755,34 @@ __global__ void __launch_bounds__(256) epi_grad_kernel(const T* __restrict__ dY,
 #pragma unroll
   for (int q = 0; q < 8; ++q) t += red[q][tid];
   part[(int64_t)blockIdx.y * N + c] = t;
+}
+
+// dbias[c] = the sum over chunks of part[.][c]: 64 columns a block, 4 threads a
+// column take every fourth chunk (their loads in flight together) and meet in
+// order.
+__global__ void __launch_bounds__(256) bias_grad_kernel(const float* __restrict__ part, int chunks, int64_t N,
+                                                        float* __restrict__ dbias) {
+  __shared__ float red[4][64];
+  const int q = threadIdx.x >> 6, l = threadIdx.x & 63;
+  const int64_t c = (int64_t)blockIdx.x * 64 + l;
+  float s = 0.f;
+  if (c < N) {
+    float v[kMaxSplits / 4];
+#pragma unroll
+    for (int k = 0; k < kMaxSplits / 4; ++k) v[k] = q + 4 * k < chunks ? part[(int64_t)(q + 4 * k) * N + c] : 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxSplits / 4; ++k) s += v[k];
+  }
+  red[q][l] = s;
+  __syncthreads();
+  if (q == 0 && c < N) dbias[c] = ((red[0][l] + red[1][l]) + red[2][l]) + red[3][l];
+}
+
+hipError_t launch_bias_grad(const float* part, int chunks, int64_t N, float* dbias, hipStream_t st) {
+  if (N <= 0) return hipSuccess;
+  if (chunks < 1 || chunks > kMaxSplits) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(bias_grad_kernel, dim3((unsigned)((N + 63) / 64)), dim3(256), 0, st, part, chunks, N, dbias);
+  return hipGetLastError();
 }
 
 hipError_t launch_epi_grad(int elem_bytes, const void* dY, const void* Z, void* dZ, float* part, int chunks, int64_t M,

@@ -172,6 +172,8 @@ hipError_t launch_split_finish_epi(const float* part, int splits, int64_t part_s
 // (1 .. 64) ranges of the tokens, fp32 [chunks][N].
 hipError_t launch_epi_grad(int elem_bytes, const void* dY, const void* Z, void* dZ, float* part, int chunks, int64_t M,
                            int64_t N, int act, hipStream_t st);
+// dbias [N] = the sum over chunks (1 .. 64) of part [chunks][N].
+hipError_t launch_bias_grad(const float* part, int chunks, int64_t N, float* dbias, hipStream_t st);
 
 hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t st);
 
