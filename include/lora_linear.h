@@ -423,8 +423,8 @@ size_t lora_swiglu_workspace_bytes(int backward, int dtype, int64_t M, int64_t d
  * [M, d_out] are of the dtype; each may be NULL.  Z, where given, receives the
  * pre-activation, which the backward of an activation needs.  residual may be
  * Y itself (the sum formed in place); Y and Z may be no other input.
- * Paths, workspace (its own sizing call) and errors as lora_linear_fwd and
- * nf4_lora_linear_fwd.
+ * Workspace from its own sizing call; sizes and errors as lora_linear_fwd and
+ * nf4_lora_linear_fwd, and d_out <= LORA_EPI_MAX_D_OUT (2^20).
  *
  * Backward, for member->dY:
  *     dZ = dY act'(Z)  (rounded to the dtype; dY itself with LORA_ACT_NONE),
@@ -434,6 +434,7 @@ size_t lora_swiglu_workspace_bytes(int backward, int dtype, int64_t M, int64_t d
  * are not used).  RELU passes no gradient at 0.  dbias: fp32 [d_out]
  * (overwritten) or NULL.
  */
+#define LORA_EPI_MAX_D_OUT (1 << 20)
 enum { LORA_ACT_NONE = 0, LORA_ACT_RELU = 1, LORA_ACT_SILU = 2, LORA_ACT_GELU = 3, LORA_ACT_GELU_TANH = 4 };
 typedef struct lora_epilogue {
   int act;

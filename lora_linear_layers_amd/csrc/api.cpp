@@ -141,6 +141,51 @@ FewPlan few_plan(bool bwd, bool nf4, bool rope, int64_t M, int64_t d_in, int64_t
 }
 
 // ---------------------------------------------------------------------------
+// stream plan (gemm_w4_stream.h)
+// ---------------------------------------------------------------------------
+struct StreamPlan {
+  bool ok = false;
+  int full = 0, half = 0, early = 0;
+};
+
+// 256 x 256 tiles for an epilogue layer's Y or dX [M, N] over K where they are
+// ragged or no multiple of the 256 CUs, instead of the 128 x 128 (from 256
+// such tiles on, the register-staged 256 x 256) kernel.  Taken where measured
+// faster on MI355X, t tiles and nk 64-deep stages:
+//   t > 256: always (4100 x 4096 over 4096: 274 -> 189 us, 5000 x 4096: 276 ->
+//     194); its last t mod 256 tiles in two blocks each where 128 of them or
+//     fewer leave CUs free and a half is long enough to pay for the exchange
+//     of 256 KB a tile (4100 x 4096: 212 -> 189 us);
+//   128 < t <= 256 (256 whole tiles have their own kernel): the 128 x 128
+//     tiles need two rounds, 2.4 us a stage and 11 us; these one of 1.1 to 1.5
+//     us a stage and 19 us (2049 x 4104 over 4096: 182 -> 101 us);
+//   64 <= t <= 128: two blocks a tile, 0.66 us a stage and 37 us, against one
+//     round of 128 x 128 tiles, 1.22 us and 11 us: from 48 stages (2048 x 4096
+//     over 4096: 98 -> 91 us, over 14336: 308 -> 224; over 2048: 60 against 65);
+//   below 64 tiles the split 128 x 128 tiles are faster (512 x 4096: 54
+//     against 73 us).
+// transpose: W^T has to be made first (0.9 us a MB of it), so the gain must
+// carry that too: only from t > 128, where two rounds are saved.
+StreamPlan stream_plan(int64_t M, int64_t N, int64_t K, int64_t r, bool transpose) {
+  StreamPlan S;
+  const int64_t r8 = rup(r, 8), t = cdiv(M, 256) * cdiv(N, 256), nk = K / 64 + cdiv(r, 64);
+  if (M < 1 || K % 64 || K < 64 || !whole_ld_fits(std::max({K, r8, N})) || t > INT32_MAX / 2) return S;
+  if (M % 256 == 0 && N % 256 == 0 && t % 256 == 0) return S;  // the whole-tile kernel
+  const int64_t rest = t % 256;
+  if (t > 128) {
+    if (t <= 256 && nk < (transpose ? 32 : 12)) return S;
+    S.half = t > 256 && rest <= 128 && nk >= 24 ? (int)rest : 0;
+  } else {
+    if (t < 64 || nk < 48 || transpose || cdiv(M, 128) * cdiv(N, 128) < 256) return S;
+    S.half = (int)t;
+  }
+  S.full = (int)(t - S.half);
+  S.early = S.half ? 3 : 0;
+  S.ok = true;
+  return S;
+}
+
+// ---------------------------------------------------------------------------
 // workspace layout
 // ---------------------------------------------------------------------------
 struct Layout {
@@ -161,6 +206,8 @@ struct Layout {
   int64_t ksplit_p = 0, ksplit_q = 0;
   size_t partb = 0;  // bf16: the dB partials, apart from dA's so one launch sums both
   FewPlan few;       // few tokens: the two-launch path (its regions from offset 0)
+  StreamPlan stream;  // epilogue layer's Y or dX: ragged 256 x 256 tiles spread over the CUs
+  size_t st_part = 0, st_cnt = 0;
 };
 
 // 256x256 tiles when they still give at least one tile per CU, else 128x128.
@@ -429,6 +476,7 @@ const char* kind_name(int k) {
       "dropout_dx_f32_64x128",      "gemm_bf16_256x256_nt_group", "gemm_nf4_256x256_nt_whole",
       "gemm_bf16_256x256_nt_epi",   "gemm_bf16_128x128_nt_epi",   "gemm_nf4_256x256_nt_epi",
       "gemm_nf4_128x128_nt_epi",    "gemm_nf4_256x256_nt_whole_epi", "gemm_f32_64x128_nt_epi",
+      "gemm_bf16_256x256_nt_stream",
       "pad_cols",
       "rope_inverse",
       "reduce_splits",              "fill_zero",                  "rope_cache",
@@ -499,7 +547,8 @@ struct PanelSrc {
 
 int panel_bf16(const void* X, int64_t ldx, const void* R, int64_t ldr, int64_t M, int64_t rows, int64_t K, int64_t r,
                int64_t r8, int splits, int64_t ksplit, const ColScale& cs, float* part, uint16_t* out, int64_t ldo,
-               uint16_t* outt, int64_t ldot, hipStream_t st, const PanelSrc* src = nullptr) {
+               uint16_t* outt, int64_t ldot, hipStream_t st, const PanelSrc* src = nullptr, int* zero = nullptr,
+               int nzero = 0) {
   GemmArgs a = blank();
   a.a1 = X; a.lda1 = ldx; a.b1 = R; a.ldb1 = ldr; a.K1 = K;
   if (src) {
@@ -516,7 +565,7 @@ int panel_bf16(const void* X, int64_t ldx, const void* R, int64_t ldr, int64_t M
   HIPTRY(gemm(G_BF16_PANEL_SPLIT_NT, a, splits, st, 2 * Md * rd * kd,
               (Md * kd + rd * kd) * 2 + 4.0 * splits * rows * r8));
   HIPTRY(timed(K_PANEL, double(splits) * rows * r8, 4.0 * splits * rows * r8 + 2.0 * rows * r8 * ((out ? 1 : 0) + (outt ? 1 : 0)),
-               st, [&] { return launch_panel_reduce(part, splits, rows * r8, r8, rows, r8, cs, out, ldo, outt, ldot, st); }));
+               st, [&] { return launch_panel_reduce(part, splits, rows * r8, r8, rows, r8, cs, out, ldo, outt, ldot, st, zero, nzero); }));
   return LORA_OK;
 }
 
@@ -667,6 +716,8 @@ int forward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, f
     W = w + L.wdq;
     nf4 = nullptr;
   }
+  const bool stream = ep && L.stream.ok;
+  int* cnt = stream && L.stream.half > 0 ? reinterpret_cast<int*>(w + L.st_cnt) : nullptr;
   const void* Bsrc = B;
   if (r % 8) {
     HIPTRY(timed(K_PAD, 0, 2.0 * d_out * L.r8 * eb, st,
@@ -687,7 +738,8 @@ int forward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, f
     HIPTRY(gemm(G_F32_PANEL_NT_STORE, a, 1, st, 2 * Md * rr * ki, (Md * ki + rr * ki + Md * L.r8) * e));
   } else {
     TRY(panel_bf16(Xp, d_in, A, d_in, M, M, d_in, r, L.r8, L.splits_p, L.ksplit_p, col_scale(scale),
-                   reinterpret_cast<float*>(w + L.ppart), reinterpret_cast<uint16_t*>(w + L.p), L.r8, nullptr, 0, st));
+                   reinterpret_cast<float*>(w + L.ppart), reinterpret_cast<uint16_t*>(w + L.p), L.r8, nullptr, 0, st,
+                   nullptr, cnt, L.stream.half));
   }
   // main: Y = [X | P] [W | B]^T, optional RoPE epilogue
   GemmArgs a = blank();
@@ -722,6 +774,12 @@ int forward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, f
   }
   const double wbytes = nf4 ? ko * ki / 2 + ko * ki / 64 * 4 : ko * ki * e;
   const double flop = 2 * Md * ko * (ki + rr), bytes = (Md * ki + Md * rr + ko * rr + Md * ko) * e + wbytes;
+  if (stream) {
+    a.st_full = L.stream.full; a.st_half = L.stream.half; a.st_early = L.stream.early;
+    a.st_part = reinterpret_cast<float*>(w + L.st_part); a.st_cnt = cnt;
+    HIPTRY(gemm(G_BF16_STREAM_EPI, a, 1, st, flop, bytes + xbytes));
+    return LORA_OK;
+  }
   if (!f32 && L.splits_main > 1) {
     // few tokens: split partials over d_in (the rank-r segment in the last
     // split), then the fixed-order sum with the store / RoPE epilogue
@@ -874,7 +932,8 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
       }
     }
     TRY(panel_bf16(G, d_out, Bt, d_out, M, L.M8, d_out, r, L.r8, L.splits_q, L.ksplit_q, col_scale(scale), pp,
-                   static_cast<uint16_t*>(Qs), ldqs, static_cast<uint16_t*>(Qt), L.M8, st));
+                   static_cast<uint16_t*>(Qs), ldqs, static_cast<uint16_t*>(Qt), L.M8, st, nullptr,
+                   reinterpret_cast<int*>(w + L.st_cnt), dX ? L.stream.half : 0));
   }
   // dX = [G | Qs] [W ; A]; with a dropout mask the rank-r term is added
   // separately, masked: dX = G W, then dX += keep * (Qs A)
@@ -900,7 +959,11 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
     a.a2 = Qs; a.lda2 = ldqs; a.b2 = At; a.ldb2 = L.r8; a.K2 = keep ? 0 : r;
     a.m_load = M; a.m_store = M; a.n_load = d_in; a.n_store = d_in;
     a.c = dX; a.ldc = d_in;
-    HIPTRY(gemm(G_BF16_BIG_NT_STORE, a, 1, st, 2 * Md * ki * (ko + rr),
+    if (L.stream.ok) {
+      a.st_full = L.stream.full; a.st_half = L.stream.half; a.st_early = L.stream.early;
+      a.st_part = reinterpret_cast<float*>(w + L.st_part); a.st_cnt = reinterpret_cast<int*>(w + L.st_cnt);
+    }
+    HIPTRY(gemm(L.stream.ok ? G_BF16_STREAM_EPI : G_BF16_BIG_NT_STORE, a, 1, st, 2 * Md * ki * (ko + rr),
                 (Md * ko + Md * rr + rr * ki + Md * ki + ko * ki) * e));
   } else if (dX) {
     GemmArgs a = blank();
@@ -1484,12 +1547,31 @@ EpiLayout make_epi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, const lo
   const int op = m.W_nf4 ? (bwd ? LORA_OP_NF4_BWD : LORA_OP_NF4_FWD) : (bwd ? LORA_OP_BWD : LORA_OP_FWD);
   E.L = make_layout(op, dtype, M, d_in, m.d_out, m.r, m.W_t != nullptr && !m.W_nf4);
   E.total = E.L.total;
+  auto take = [&](size_t bytes) {
+    const size_t at = align256(E.total);
+    E.total = at + align256(bytes);
+    return at;
+  };
+  if (!bwd && dtype == LORA_BF16 && !E.L.few.ok && (!m.W_nf4 || E.L.dequant) &&
+      !(!m.W_nf4 && skinny_fits(M, d_in, m.d_out, m.r, sk::EPIL))) {
+    E.L.stream = stream_plan(M, m.d_out, d_in, m.r, false);
+  }
+  if (bwd && M > 0 && dtype == LORA_BF16 && !E.L.few.ok && !E.L.dx_nt && E.L.splits_main == 1 &&
+      (!m.W_nf4 || E.L.dequant)) {
+    // dX on the same tiles, through W^T and A^T (an NF4 W is dequantised into
+    // its transpose as cheaply as into itself)
+    E.L.stream = stream_plan(M, d_in, m.d_out, m.r, !m.W_t && !m.W_nf4);
+    if (E.L.stream.ok) {
+      E.L.dx_nt = true;
+      if (m.W_nf4 || !m.W_t) E.L.wt = take(size_t(d_in) * m.d_out * 2);
+      E.L.at = take(size_t(d_in) * E.L.r8 * 2);
+    }
+  }
+  if (E.L.stream.half > 0) {
+    E.L.st_part = take(size_t(E.L.stream.half) * 2 * 256 * 256 * 4);
+    E.L.st_cnt = take(size_t(E.L.stream.half) * 4);
+  }
   if (bwd && M > 0) {
-    auto take = [&](size_t bytes) {
-      const size_t at = align256(E.total);
-      E.total = at + align256(bytes);
-      return at;
-    };
     if (e.act != LORA_ACT_NONE) E.dz = take(size_t(M) * m.d_out * elem_bytes(dtype));
     // about two blocks of 256 columns a CU, at least 8 tokens each
     E.chunks = (int)std::max<int64_t>(1, std::min<int64_t>({64, cdiv(M, 8), cdiv(512, cdiv(m.d_out, 256))}));
@@ -1503,7 +1585,8 @@ int check_epi(bool bwd, int dtype, int64_t M, int64_t d_in, const lora_group_mem
   if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_ERR_DTYPE;
   if (!m || !e) return LORA_ERR_NULL;
   TRY(check_sizes(M, d_in, m->d_out, m->r));
-  if (m->rope || e->act < LORA_ACT_NONE || e->act > LORA_ACT_GELU_TANH) return LORA_ERR_SHAPE;
+  if (m->rope || e->act < LORA_ACT_NONE || e->act > LORA_ACT_GELU_TANH || m->d_out > LORA_EPI_MAX_D_OUT)
+    return LORA_ERR_SHAPE;
   TRY(check_ptrs({m->A, m->B}));
   if (m->W_nf4) {
     if (dtype != LORA_BF16) return LORA_ERR_DTYPE;

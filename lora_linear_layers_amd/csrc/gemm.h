@@ -141,6 +141,11 @@ struct GemmArgs {
   int mem_ldc[kGroupGemmMax];
   int mem_rope[kGroupGemmMax];
   EpiArgs ep;  // EPI_ACT (residual and z rows as long as C's: ldc)
+  // gemm_w4_stream_kernel: tiles of a block each, then tiles of two blocks each
+  // (the first's part st_early stages short of half); their slots and counters
+  int st_full, st_half, st_early;
+  float* st_part;
+  int* st_cnt;
 };
 
 __device__ __forceinline__ int lds_off(int row, int chunk) {

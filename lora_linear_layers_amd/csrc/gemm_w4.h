@@ -67,10 +67,27 @@ constexpr uint32_t OOB = 0x40000000u;  // lane offset that reads zero
 //               projection of output columns n0 / 2 + 64 wn + 32 (j / 2) + l32;
 //               C = silu(g) u, and g / u are also stored to cg / cu when
 //               set.
-//   EPI_ACT:    C = act(alpha acc + bias) + residual, Z kept when asked for.
-template <int EPI>
+//   EPI_ACT:    C = act(alpha acc + bias) + residual, Z kept when asked for
+//               (RAGGED: the tile may reach past m_store and n_store, and
+//               `part`, where given, is added to acc).
+// Rows of MFMA block row i of another block's accumulators of the tile (256 x
+// 256 floats in the registers' order: f32x4 q of block (i, j) of thread t at
+// (((i FN + j) 4 + q) 256 + t) 16 bytes), from the coherence point.
+__device__ __forceinline__ void w4_load_part(const float* part, int i, int t, f32x4 (&v)[w4::FN][4]) {
+  const __amdgpu_buffer_rsrc_t r =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(part), (short)0, w4::BM * w4::BN * 4, 0x00020000);
+#pragma unroll
+  for (int j = 0; j < w4::FN; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      v[j][q] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                              r, (j * 4 + q) * (w4::NT * 16) + t * 16, i * w4::FN * 4 * (w4::NT * 16), 16));
+}
+
+template <int EPI, bool RAGGED = false>
 __device__ __forceinline__ void w4_epilogue(const GemmArgs& p, f32x16 (&acc)[w4::FM][w4::FN], char* smem,
-                                            int64_t m0, int64_t n0, void* c_out, int64_t ldc) {
+                                            int64_t m0, int64_t n0, void* c_out, int64_t ldc,
+                                            const float* part = nullptr) {
   using namespace w4;
   auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
   int te = threadIdx.x;
@@ -206,54 +223,113 @@ __device__ __forceinline__ void w4_epilogue(const GemmArgs& p, f32x16 (&acc)[w4:
     // q + 4, which a wave's halves write together, lie 32 banks apart), then
     // 8 columns of 8 rows a thread, so that residual and output move in
     // 16-byte accesses and the bias is loaded once.  The pass's residual is
-    // requested before its tile is staged.
+    // requested before its tile is staged.  The barriers are LDS barriers: one
+    // that also waits for memory would wait for the pass's stores (measured
+    // on MI355X: 14 us more a tile).
     constexpr int PITCH = BN + 8;
     static_assert(64 * PITCH * 4 <= 4 * BM * 128, "the staged rows fit every ring");
     float* st = reinterpret_cast<float*>(smem);
     const int cc = (te & 31) * 8, r0 = te >> 5;
     const int64_t col = n0 + cc;
+    const bool cok = !RAGGED || col < p.n_store;  // (n_store is a multiple of 8)
+    // Y, R and Z through buffer resources at the tile's first element that end
+    // with its last existing row: what lies past it reads zeros and is not
+    // stored, with no branch; a column past n_store takes an offset past every
+    // resource.  (256 ldc elements stay below the resources' range.)
+    const int rows = RAGGED ? (int)min(p.m_store - m0, (int64_t)BM) : BM;
+    const int len = (int)(((rows - 1) * ldc + (RAGGED ? min(p.n_store - n0, (int64_t)BN) : BN)) * 2);
+    auto rsrc = [&](const void* q) {
+      return __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint16_t*>(static_cast<const uint16_t*>(q)) + (q ? m0 * ldc + n0 : 0), (short)0, q ? len : 0,
+          0x00020000);
+    };
+    const __amdgpu_buffer_rsrc_t ro = rsrc(out), rr = rsrc(p.ep.res), rz = rsrc(p.ep.z);
+    const uint32_t ldb = __builtin_amdgcn_readfirstlane((uint32_t)(ldc * 2));
+    const uint32_t vo = cok ? (uint32_t)r0 * ldb + (uint32_t)cc * 2 : 0x80000000u;
     float b[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) b[e] = 0.f;
-    if (p.ep.bias) epi_load(static_cast<const uint16_t*>(p.ep.bias) + col, b);
-    const uint16_t* res = static_cast<const uint16_t*>(p.ep.res);
-    uint16_t* zo = static_cast<uint16_t*>(p.ep.z);
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      u32x4 rv[8];
-      if (res) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int lr = r0 + 8 * k;
-          rv[k] = *reinterpret_cast<const u32x4*>(res + (m0 + (lr >> 5) * TM + 32 * i + (lr & 31)) * ldc + col);
-        }
-      }
-      __syncthreads();
+    if (p.ep.bias && cok) epi_load(static_cast<const uint16_t*>(p.ep.bias) + col, b);
+    const bool has_res = p.ep.res != nullptr, has_z = p.ep.z != nullptr;
+    const int act = p.ep.act;
+    f32x4 s[FN][4];  // RAGGED: the pass's rows of the other part
+    auto stage = [&](auto i_c, auto add_c) {
+      constexpr int i = decltype(i_c)::value;
+      constexpr bool ADD = decltype(add_c)::value;
 #pragma unroll
       for (int v = 0; v < 16; ++v)
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-          st[(32 * wm + 8 * (v >> 2) + (v & 3) + 4 * hh) * PITCH + wn * TN + 32 * j + l32] = acc[i][j][v] * p.alpha;
-      __syncthreads();
+        for (int j = 0; j < FN; ++j) {
+          float x = acc[i][j][v];
+          if constexpr (ADD) x += s[j][v >> 2][v & 3];
+          st[(32 * wm + 8 * (v >> 2) + (v & 3) + 4 * hh) * PITCH + wn * TN + 32 * j + l32] = x * p.alpha;
+        }
+    };
+    auto stage_of = [&](int i, auto add_c) {
+      switch (i) {
+        case 0: stage(std::integral_constant<int, 0>{}, add_c); break;
+        case 1: stage(std::integral_constant<int, 1>{}, add_c); break;
+        case 2: stage(std::integral_constant<int, 2>{}, add_c); break;
+        default: stage(std::integral_constant<int, 3>{}, add_c); break;
+      }
+    };
+    // One copy of the pass's code for the four: unrolled (and with the
+    // activations' variants in every row) it is 100 KB, which a block runs
+    // through once, at the rate of its instruction fetches.
+    if (RAGGED && part) w4_load_part(part, 0, te, s);
+#pragma unroll 1
+    for (int i = 0; i < FM; ++i) {
+      // row r0 + 8 k of the pass is the tile's row r0 + at(k)
+      auto at = [&](int k) { return (uint32_t)((k >> 2) * TM + 32 * i + 8 * (k & 3)) * ldb; };
+      u32x4 rv[8];
+      if (has_res) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          rv[k] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rr, (int)(vo + at(k)), 0, 0));
+      }
+      lds_barrier();
+      if (!RAGGED || !part)
+        stage_of(i, std::false_type{});
+      else
+        stage_of(i, std::true_type{});
+      // the next pass's part flies while this one's rows are finished
+      if (RAGGED && part && i + 1 < FM) w4_load_part(part, i + 1, te, s);
+      lds_barrier();
+      float y[64];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int lr = r0 + 8 * k;
-        const int64_t o = (m0 + (lr >> 5) * TM + 32 * i + (lr & 31)) * ldc + col;
-        const float4 y0 = *reinterpret_cast<const float4*>(st + lr * PITCH + cc);
-        const float4 y1 = *reinterpret_cast<const float4*>(st + lr * PITCH + cc + 4);
-        float y[8] = {y0.x + b[0], y0.y + b[1], y0.z + b[2], y0.w + b[3],
-                      y1.x + b[4], y1.y + b[5], y1.z + b[6], y1.w + b[7]};
-        if (zo) epi_store(zo + o, y);
-        act_all<true>(y, p.ep.act);
-        if (res) {
+        const float4 y0 = *reinterpret_cast<const float4*>(st + (r0 + 8 * k) * PITCH + cc);
+        const float4 y1 = *reinterpret_cast<const float4*>(st + (r0 + 8 * k) * PITCH + cc + 4);
+        y[8 * k] = y0.x + b[0];
+        y[8 * k + 1] = y0.y + b[1];
+        y[8 * k + 2] = y0.z + b[2];
+        y[8 * k + 3] = y0.w + b[3];
+        y[8 * k + 4] = y1.x + b[4];
+        y[8 * k + 5] = y1.y + b[5];
+        y[8 * k + 6] = y1.z + b[6];
+        y[8 * k + 7] = y1.w + b[7];
+      }
+      auto put = [&](__amdgpu_buffer_rsrc_t dst) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          u32x4 o;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) o[q] = pack_bf16x2(y[8 * k + 2 * q], y[8 * k + 2 * q + 1]);
+          __builtin_amdgcn_raw_buffer_store_b128(o, dst, (int)(vo + at(k)), 0, 0);
+        }
+      };
+      if (has_z) put(rz);
+      act_all<true>(y, act);
+      if (has_res) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            y[2 * q] += __builtin_bit_cast(float, rv[k][q] << 16);
-            y[2 * q + 1] += __builtin_bit_cast(float, rv[k][q] & 0xFFFF0000u);
+            y[8 * k + 2 * q] += __builtin_bit_cast(float, rv[k][q] << 16);
+            y[8 * k + 2 * q + 1] += __builtin_bit_cast(float, rv[k][q] & 0xFFFF0000u);
           }
-        }
-        epi_store(out + o, y);
       }
+      put(ro);
     }
   } else {
     static_assert(EPI == EPI_STORE, "store, RoPE, SwiGLU or activation epilogue");

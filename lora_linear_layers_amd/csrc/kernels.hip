@@ -11,6 +11,7 @@
 #include "gemm_w4.h"
 #include "gemm_w4_nt.h"
 #include "gemm_w4_nf4.h"
+#include "gemm_w4_stream.h"
 #include "gemm_panel.h"
 #include "skinny.h"
 #include "tiny.h"
@@ -146,6 +147,8 @@ TileShape gemm_tile(GemmKind k) {
     case G_BF16_BIG_NT_EPI:
     case G_NF4_BIG_NT_EPI:
       return {256, 256};
+    case G_BF16_STREAM_EPI:
+      return {256, 256};
     case G_BF16_MED_NT_EPI:
     case G_NF4_MED_NT_EPI:
       return {128, 128};
@@ -210,8 +213,24 @@ hipError_t launch_gemm(GemmKind k, GemmArgs a, int splits, hipStream_t st) {
         return hipErrorInvalidValue;
       return run_whole<false, EPI_GROUP>(a, st);
     case G_BF16_BIG_NT_EPI:
-      if (whole_tiles(a, splits)) return run_whole<false, EPI_ACT>(a, st);
+      if (whole_tiles(a, splits) && whole_ld_fits(a.ldc)) return run_whole<false, EPI_ACT>(a, st);
       return run<bf, 256, 256, 2, 4, false, EPI_ACT, BL_PLAIN>(a, splits, st);
+    case G_BF16_STREAM_EPI: {
+      // whole stages of the first segment, lane offsets below the resource
+      // range; every tile in a block of its own or in two, of two stages at least
+      const int64_t ld = std::max(std::max(a.lda1, a.lda2), std::max(a.ldb1, a.ldb2));
+      const int64_t tm = (a.m_store + w4::BM - 1) / w4::BM, tn = (a.n_store + w4::BN - 1) / w4::BN;
+      if (splits != 1 || a.m_load != a.m_store || a.n_load != a.n_store || a.n_store % 8 || a.K1 < w4::BK ||
+          a.K1 % w4::BK || !whole_ld_fits(std::max(ld, a.ldc)) || a.st_full < 0 || a.st_half < 0 ||
+          a.st_full + (int64_t)a.st_half != tm * tn || a.st_full + 2 * (int64_t)a.st_half > INT32_MAX ||
+          (a.st_half > 0 && (!a.st_part || !a.st_cnt || a.st_early < 0 || a.K1 / w4::BK / 2 - a.st_early < 2)))
+        return hipErrorInvalidValue;
+      if (tm * tn == 0) return hipSuccess;
+      a.tiles_m = (int)tm;
+      hipLaunchKernelGGL((gemm_w4_stream_kernel<EPI_ACT>), dim3((unsigned)(a.st_full + 2 * a.st_half)), dim3(w4::NT), 0,
+                         st, a);
+      return hipGetLastError();
+    }
     case G_BF16_MED_NT_EPI: return run<bf, 128, 128, 4, 1, false, EPI_ACT, BL_PLAIN>(a, splits, st);
     case G_NF4_BIG_NT_EPI: return run<bf, 256, 256, 2, 4, false, EPI_ACT, BL_NF4>(a, splits, st);
     case G_NF4_MED_NT_EPI: return run<bf, 128, 128, 4, 1, false, EPI_ACT, BL_NF4>(a, splits, st);
@@ -220,7 +239,7 @@ hipError_t launch_gemm(GemmKind k, GemmArgs a, int splits, hipStream_t st) {
     case G_NF4_WHOLE_NT_STORE: {
       // whole tiles, codes and absmax present, every lane offset of a tile's
       // codes and absmax below the buffer-resource range
-      if (!whole_tiles(a, splits) || !a.codes || !a.absmax || a.K1 < w4::BK || a.codes_ld * 2 != a.K1 ||
+      if (!whole_tiles(a, splits) || (k == G_NF4_WHOLE_NT_EPI && !whole_ld_fits(a.ldc)) || !a.codes || !a.absmax || a.K1 < w4::BK || a.codes_ld * 2 != a.K1 ||
           a.blocks_per_row * w4::BK != a.K1 || a.codes_ld * (w4::BN + 1) >= (int64_t)w4::BIG)
         return hipErrorInvalidValue;
       const int64_t tiles_m = a.m_store / w4::BM;
@@ -1101,9 +1120,12 @@ constexpr int kMaxPanelSplits = 32;
 __global__ void __launch_bounds__(256) panel_reduce_kernel(const float* __restrict__ part, int splits,
                                                            int64_t part_stride, int64_t ldp, int64_t rows, int64_t n,
                                                            ColScale scale, uint16_t* __restrict__ out, int64_t ldo,
-                                                           uint16_t* __restrict__ outt, int64_t ldot) {
+                                                           uint16_t* __restrict__ outt, int64_t ldot, int* __restrict__ zero,
+                                                           int nzero) {
   __shared__ float tile[16][65];
   const int tid = threadIdx.x;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = tid; i < nzero; i += 256) zero[i] = 0;
   const int64_t q0 = (int64_t)blockIdx.x * 16, c0 = (int64_t)blockIdx.y * 64;
   const int cl = 4 * (tid & 15), rl = tid >> 4;
   const int64_t c = c0 + cl, q = q0 + rl;
@@ -1143,8 +1165,8 @@ __global__ void __launch_bounds__(256) panel_reduce_kernel(const float* __restri
 
 hipError_t launch_panel_reduce(const float* part, int splits, int64_t part_stride, int64_t ldp, int64_t rows,
                                int64_t n, const ColScale& scale, uint16_t* out, int64_t ldo, uint16_t* outt,
-                               int64_t ldot, hipStream_t st) {
-  if (rows <= 0 || n <= 0) return hipSuccess;
+                               int64_t ldot, hipStream_t st, int* zero, int nzero) {
+  if (rows <= 0 || n <= 0) return nzero > 0 ? hipErrorInvalidValue : hipSuccess;
   if (splits < 1 || splits > kMaxPanelSplits || scale.n < 1 || scale.n > kColScaleMax) return hipErrorInvalidValue;
   // float4 partial loads, 4-column bf16 stores
   if (n % 4 || ldp % 4 || part_stride % 4 || reinterpret_cast<uintptr_t>(part) % 16 ||
@@ -1152,7 +1174,7 @@ hipError_t launch_panel_reduce(const float* part, int splits, int64_t part_strid
     return hipErrorInvalidValue;
   const dim3 grid((unsigned)((rows + 15) / 16), (unsigned)((n + 63) / 64));
   hipLaunchKernelGGL(panel_reduce_kernel, grid, dim3(256), 0, st, part, splits, part_stride, ldp, rows, n, scale, out,
-                     ldo, outt, ldot);
+                     ldo, outt, ldot, zero, nzero);
   return hipGetLastError();
 }
 

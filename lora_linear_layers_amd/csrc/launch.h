@@ -63,6 +63,7 @@ enum GemmKind : int {
   G_NF4_MED_NT_EPI,
   G_NF4_WHOLE_NT_EPI,
   G_F32_NT_EPI,
+  G_BF16_STREAM_EPI,  // 256 x 256 tiles, ragged and split over the CUs (gemm_w4_stream_kernel)
   G_KIND_COUNT
 };
 
@@ -151,9 +152,10 @@ inline ColScale col_scale(float s) {
 // Rank-r panel from split partials: v = scale(c) * sum over z < splits of
 // part[z][q, c] (fixed order) for q < rows, c < n; written as bf16 to
 // out[q * ldo + c] and/or outt[c * ldot + q] (either may be null).
+// Also clears zero[0 .. nzero) (a later launch's counters).
 hipError_t launch_panel_reduce(const float* part, int splits, int64_t part_stride, int64_t ldp, int64_t rows,
                                int64_t n, const ColScale& scale, uint16_t* out, int64_t ldo, uint16_t* outt,
-                               int64_t ldot, hipStream_t st);
+                               int64_t ldot, hipStream_t st, int* zero = nullptr, int nzero = 0);
 
 // out [M, N] bf16 (row stride ldo) = fixed-order sum of split partials
 // (part[z * part_stride + m * N + n]); with pos != NULL also the RoPE rotation

@@ -152,7 +152,12 @@ BF16 = [
     (1, 64, 64, 8, "skinny_fwd"), (16, 1000, 136, 8, "skinny_fwd"), (5, 4096, 12296, 16, "skinny_fwd"),
     (61, 72, 12296, 48, "skinny_fwd"), (40, 512, 768, 5, "split_finish"), (100, 1024, 2048, 16, "split_finish"),
     (129, 520, 136, 3, "split_finish"), (1, 8, 8, 1, "gemm_bf16_128x128_nt_epi"),
-    (300, 264, 392, 16, "gemm_bf16_128x128_nt_epi"), (2049, 256, 4104, 12, "gemm_bf16_128x128_nt_epi"),
+    (300, 264, 392, 16, "gemm_bf16_128x128_nt_epi"), (2049, 264, 4104, 12, "gemm_bf16_128x128_nt_epi"),
+    # 256 x 256 tiles, ragged or no multiple of the CUs: a block each; two blocks each; whole rounds and two blocks
+    # for each of the rest; the ragged tile alone in its column
+    (2049, 1024, 4104, 100, "gemm_bf16_256x256_nt_stream"), (2048, 3136, 2056, 16, "gemm_bf16_256x256_nt_stream"),
+    (4100, 1600, 4104, 8, "gemm_bf16_256x256_nt_stream"), (4353, 64, 4104, 1, "gemm_bf16_256x256_nt_stream"),
+    (2048, 3200, 2048, 24, "gemm_bf16_256x256_nt_stream"),
     (4090, 136, 4104, 12, "gemm_bf16_256x256_nt_epi"), (4096, 320, 4096, 72, "gemm_bf16_256x256_nt_epi"),
 ]
 F32 = [
@@ -239,7 +244,7 @@ def test_epilogue_activation_values(lib, dtype, act):
 @pytest.mark.gpu
 def test_epilogue_exact_on_integers(lib):
     # small integers: every product, sum, relu and residual is exact, on every kind of tile
-    for M, k, d, r in ((4096, 64, 4096, 8), (1, 128, 8192, 32), (300, 264, 392, 16), (40, 512, 768, 5), (9, 64, 64, 8)):
+    for M, k, d, r in ((4096, 64, 4096, 8), (2050, 1024, 4104, 8), (2048, 3200, 2056, 8), (1, 128, 8192, 32), (300, 264, 392, 16), (40, 512, 768, 5), (9, 64, 64, 8)):
         X, W, A, B, R = int_inputs(5 + M, M, k, d, r, "bf16")
         X = X * (torch.rand(M, k, generator=torch.Generator().manual_seed(M)) < 0.2).cuda()  # |Z| stays below 2^8
         A = A * (torch.arange(k, device="cuda") % 32 == 0)
@@ -253,7 +258,7 @@ def test_epilogue_exact_on_integers(lib):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("case", [c for c in BF16 if c[0] in (1, 5, 40, 300, 4090, 4096)], ids=_id)
+@pytest.mark.parametrize("case", [c for c in BF16 if c[0] in (1, 5, 40, 300, 2048, 2049, 4090, 4096, 4100)], ids=_id)
 def test_epilogue_residual_in_place_and_rows_behind(lib, case):
     M, k, d, r, _ = case
     X, m, bias, res, _ = _inputs(31, M, k, d, r, "bf16")
@@ -302,6 +307,28 @@ def test_epilogue_no_tokens(lib):
     assert dX.shape == (0, 64) and (dA == 0).all() and (dB == 0).all() and (db == 0).all()
 
 
+# dX on the tiles of the forward above: through the caller's W^T, through one made on the way, through an NF4 W
+DX = [(2048, 2056, 3136, 16, True), (4100, 4104, 1600, 8, False), (4100, 4104, 1600, 8, True),
+      (2049, 4104, 2112, 24, False), (2304, 4096, 2112, 64, None)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", DX, ids=lambda c: "%dx%dx%dr%d-%s" % c)
+def test_epilogue_input_gradient_tiles(lib, case):
+    M, k, d, r, kept = case
+    table = None
+    if kept is None:
+        X, m, _, _, dY, table = _nf4(40 + M, k, d, r, M)
+    else:
+        X, m, _, _, dY = _inputs(40 + M, M, k, d, r, "bf16")
+        if kept:
+            m["W_t"] = lib.lora_transpose(m["W"])
+    Z = torch.randn(M, d, generator=torch.Generator().manual_seed(5)).bfloat16().cuda()
+    kinds = _kinds(lambda: lib.lora_linear_epi_bwd(X, m, dY, "silu", Z, table16=table))
+    assert "gemm_bf16_256x256_nt_stream" in kinds, kinds
+    check_bwd(lib, X, m, dY, "silu", Z, table)
+
+
 @pytest.mark.gpu
 def test_epilogue_kept_transpose_of_w(lib):
     X, m, _, _, dY = _inputs(6, 4096, 4096, 256, 16, "bf16")
@@ -312,7 +339,8 @@ def test_epilogue_kept_transpose_of_w(lib):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("shape", [(1, 4096, 14336, 16), (300, 264, 392, 16), (4096, 128, 4096, 16)], ids=str)
+@pytest.mark.parametrize("shape", [(1, 4096, 14336, 16), (300, 264, 392, 16), (4096, 128, 4096, 16),
+                                   (2048, 3200, 2056, 24), (4100, 1600, 4104, 8)], ids=str)
 def test_epilogue_repeats_other_stream_and_captured(lib, shape):
     M, k, d, r = shape
     X, m, bias, res, dY = _inputs(8, M, k, d, r, "bf16")
@@ -441,7 +469,7 @@ def test_epilogue_refusals():
 
     for f in (fwd, bwd):
         assert f(dtype=2) == -4 and f(M=-1) == -2 and f(k=12) == -2 and f(m=mk(r=0)) == -2 and f(m=mk(d_out=12)) == -2
-        assert f(m=mk(rope=1)) == -2 and f(e=ep(act=5)) == -2 and f(e=ep(act=-1)) == -2
+        assert f(m=mk(rope=1)) == -2 and f(m=mk(d_out=2 ** 20 + 8)) == -2 and f(e=ep(act=5)) == -2 and f(e=ep(act=-1)) == -2
         assert f(m=mk(W=None)) == -1 and f(m=mk(A=None)) == -1 and f(X=None) == -1 and f(X=P + 8) == -3
         assert f(dtype=0, m=mk(W_nf4=P, absmax=P)) == -4 and f(m=mk(W_nf4=P)) == -1
         assert f(m=mk(W_nf4=P, absmax=P), table=None) == -1 and f(m=mk(W_nf4=P, absmax=P), k=96) == -2
