@@ -19,10 +19,16 @@ namespace {
 
 constexpr float LOG2E = 1.44269504088896340736f;
 
-// 16 bytes of a row whose address is a multiple of the element size only
-// (rows of an odd vocabulary): one global_load_dwordx4 either way.
+// 16 bytes of a row at a multiple of 4 bytes: one global_load_dwordx4, as fast
+// as at a multiple of 16.  Rows of an odd bf16 vocabulary start 2 bytes off
+// every other time, which costs 20 % (8192 x 127999: 427 against 349 us), so
+// their first element is taken apart (row_head).
 typedef uint32_t u32x4_e2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_e4 __attribute__((ext_vector_type(4), aligned(4)));
+template <typename T>
+__device__ __forceinline__ int row_head(const T* p) {
+  return sizeof(T) == 2 ? (int)((reinterpret_cast<uintptr_t>(p) >> 1) & 1) : 0;
+}
 
 template <typename T>
 struct Row;
@@ -110,17 +116,20 @@ __global__ void __launch_bounds__(NT) token_logp_kernel(const T* __restrict__ z,
       for (int e = 0; e < E; ++e) s += fexp2((x[e] - base) * c);
       m = nm;
     };
-    const int nv = V / E;
+    const int head = row_head(zr), nv = (V - head) / E;
+    const T* zv = zr + head;
     int i = tid;
     for (; i + (U - 1) * NT < nv; i += U * NT) {
       u32x4 v[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const typename R::V*>(zr + (int64_t)(i + u * NT) * E);
+      for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const typename R::V*>(zv + (int64_t)(i + u * NT) * E);
 #pragma unroll
       for (int u = 0; u < U; ++u) take(v[u]);
     }
-    for (; i < nv; i += NT) take(*reinterpret_cast<const typename R::V*>(zr + (int64_t)i * E));
-    if (tid < V - nv * E) join_max_sum(m, s, R::at(zr + (int64_t)nv * E + tid), 1.f, c);
+    for (; i < nv; i += NT) take(*reinterpret_cast<const typename R::V*>(zv + (int64_t)i * E));
+    // the elements before and behind the vectors (at most E)
+    const int rest = V - head - nv * E;
+    if (tid < rest + head) join_max_sum(m, s, tid < rest ? R::at(zv + (int64_t)nv * E + tid) : R::at(zr), 1.f, c);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) {
       const float m2 = __shfl_xor(m, o), s2 = __shfl_xor(s, o);
@@ -160,7 +169,6 @@ __global__ void __launch_bounds__(GRAD_NT) token_logp_grad_kernel(const T* z, in
                                                                   int64_t ldd) {
   using R = Row<T>;
   constexpr int E = R::E, U = GRAD_U, NT = GRAD_NT;
-  const int nv = V / E;
   const int64_t items = rows * segs;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int64_t row = it / segs;
@@ -169,6 +177,7 @@ __global__ void __launch_bounds__(GRAD_NT) token_logp_grad_kernel(const T* z, in
     const float g = t >= 0 && t < V ? dlogp[row] * tau : 0.f;
     const T* zr = z + row * ld;
     T* dr = dz + row * ldd;
+    const int head = row_head(zr), nv = (V - head) / E;
     const bool zero = g == 0.f;
     const float m = stats[2 * row], ls2 = stats[2 * row + 1] * LOG2E, c = tau * LOG2E;
     auto grad = [&](float x, int64_t j) { return (j == t ? g : 0.f) - g * fexp2((x - m) * c - ls2); };
@@ -177,11 +186,11 @@ __global__ void __launch_bounds__(GRAD_NT) token_logp_grad_kernel(const T* z, in
     if (!zero) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (i0 + u * NT < nv) v[u] = *reinterpret_cast<const typename R::V*>(zr + (int64_t)(i0 + u * NT) * E);
+        if (i0 + u * NT < nv) v[u] = *reinterpret_cast<const typename R::V*>(zr + head + (int64_t)(i0 + u * NT) * E);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t j = (int64_t)(i0 + u * NT) * E;
+      const int64_t j = head + (int64_t)(i0 + u * NT) * E;
       if (i0 + u * NT >= nv) continue;
       u32x4 o = {0u, 0u, 0u, 0u};
       if (!zero) {
@@ -193,9 +202,11 @@ __global__ void __launch_bounds__(GRAD_NT) token_logp_grad_kernel(const T* z, in
       }
       *reinterpret_cast<typename R::V*>(dr + j) = o;
     }
-    // the row's last V % E elements: the last segment's first threads
-    if (seg == segs - 1 && (int)threadIdx.x < V - nv * E) {
-      const int64_t j = (int64_t)nv * E + threadIdx.x;
+    // the elements before and behind the vectors (at most E): the last
+    // segment's first threads
+    const int rest = V - head - nv * E;
+    if (seg == segs - 1 && (int)threadIdx.x < rest + head) {
+      const int64_t j = (int)threadIdx.x < rest ? head + (int64_t)nv * E + threadIdx.x : 0;
       R::put(dr + j, zero ? 0.f : grad(R::at(zr + j), j));
     }
   }
@@ -211,8 +222,12 @@ hipError_t run_logp(const T* z, int64_t ld, int64_t rows, int64_t V, const int64
                        stats);
     return hipGetLastError();
   };
+  // threads a row (measured): a wave for a short one; 1024 where the row holds
+  // three rounds of their loads (8192 x 128000 bf16: 328 us against 349 with
+  // 256; 8192 x 50000: 167 against 146), or the rows alone do not fill the
+  // chip (64 x 128000: 11.7 us against 15.0)
   if (V <= 2048) return go(std::integral_constant<int, 64>{});
-  if (rows >= 1024) return go(std::integral_constant<int, 256>{});
+  if (V / Row<T>::E < 3 * 4 * 1024 && rows >= 512) return go(std::integral_constant<int, 256>{});
   return go(std::integral_constant<int, 1024>{});
 }
 
