@@ -522,14 +522,14 @@ def lora_linear_epi_bwd(X, member, dY, act: str = "none", Z=None, need_dX: bool 
 
 
 class LoraLinearEpiFunction(torch.autograd.Function):
-    """Y = LoraLinearEpiFunction.apply(X, W, A, B, bias, residual, scale, act): gradients for X, A, B, bias and residual
-    (W frozen; bias and residual may be None)."""
+    """Y = LoraLinearEpiFunction.apply(X, W, A, B, bias, residual, scale, act, W_t): gradients for X, A, B, bias and
+    residual (W frozen; bias and residual may be None; W_t: W's transpose, where the caller keeps one for dX)."""
 
     @staticmethod
-    def forward(ctx, X, W, A, B, bias, residual, scale, act="none"):
+    def forward(ctx, X, W, A, B, bias, residual, scale, act="none", W_t=None):
         member = {"W": W, "A": A, "B": B, "scale": scale}
         Y, Z = lora_linear_epi_fwd(X, member, act, bias, residual, store_z=act != "none")
-        ctx.save_for_backward(X, W, A, B, Z)
+        ctx.save_for_backward(X, W, A, B, Z, W_t)
         ctx.scale, ctx.act = scale, act
         ctx.bias_dtype = None if bias is None else bias.dtype
         return Y
@@ -537,12 +537,13 @@ class LoraLinearEpiFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dY):
-        X, W, A, B, Z = ctx.saved_tensors
+        X, W, A, B, Z, W_t = ctx.saved_tensors
         dY = dY.contiguous()
-        dX, dA, dB, dbias = lora_linear_epi_bwd(X, {"W": W, "A": A, "B": B, "scale": ctx.scale}, dY, ctx.act, Z,
-                                                need_dX=ctx.needs_input_grad[0], need_dbias=ctx.needs_input_grad[4])
+        member = {"W": W, "A": A, "B": B, "scale": ctx.scale, "W_t": W_t}
+        dX, dA, dB, dbias = lora_linear_epi_bwd(X, member, dY, ctx.act, Z, need_dX=ctx.needs_input_grad[0],
+                                                need_dbias=ctx.needs_input_grad[4])
         return (dX, None, dA.to(A.dtype), dB.to(B.dtype), None if dbias is None else dbias.to(ctx.bias_dtype),
-                dY if ctx.needs_input_grad[5] else None, None, None)
+                dY if ctx.needs_input_grad[5] else None, None, None, None)
 
 
 class LoraLinearFunction(torch.autograd.Function):

@@ -442,6 +442,56 @@ def test_block_head_and_policy_loss(lib):
         assert (a.grad.cpu().double() - b.grad).abs().max() <= 3e-5 * b.grad.abs().max()
 
 
+@pytest.mark.gpu
+def test_epilogue_two_calls_at_once(lib):
+    # the same layer twice on two streams, each call with its own workspace (slots and counters of the split tiles)
+    X, m, bias, res, dY = _inputs(12, 2048, 3200, 2048, 24, "bf16")
+    m["W_t"] = lib.lora_transpose(m["W"])
+
+    def step():
+        Y, Z = lib.lora_linear_epi_fwd(X, m, "silu", bias, res, store_z=True)
+        return (Y, Z) + lib.lora_linear_epi_bwd(X, m, dY, "silu", Z, need_dbias=True)
+
+    want = step()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(4):
+        for st in streams:
+            with torch.cuda.stream(st):
+                got.append(step())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(want, g))
+
+
+@pytest.mark.gpu
+def test_epilogue_function_with_kept_transpose(lib):
+    X, m, bias, res, dY = _inputs(13, 300, 264, 136, 8, "bf16")
+    out = []
+    for wt in (None, lib.lora_transpose(m["W"])):
+        leaves = [t.clone().requires_grad_() for t in (X, m["A"], m["B"], bias, res)]
+        Y = lib.LoraLinearEpiFunction.apply(leaves[0], m["W"], *leaves[1:], m["scale"], "silu", wt)
+        out.append([Y] + list(torch.autograd.grad(Y, leaves, dY)))
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    assert torch.equal(out[0][5], dY)  # the residual's gradient
+
+
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    from lora_linear_layers_amd import functional as F
+
+    now, seen = [0], []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "set_device", lambda i: (now.__setitem__(0, i), seen.append(i)))
+    with F._on(torch.device("cuda:0")):
+        assert now == [0]
+    assert seen == []
+    with pytest.raises(RuntimeError), F._on(torch.device("cuda:3")):
+        assert now == [3]
+        raise RuntimeError
+    assert now == [0] and seen == [3, 0]
+
+
 def test_epilogue_refusals():
     import ctypes
 
