@@ -458,9 +458,14 @@ def _epi_member(X, member):
         _check(dev, "W_t", Wt, (torch.bfloat16,), d_out * d_in)
         if Wt.shape != (d_in, d_out):
             raise ValueError("W_t must be the bf16 [d_in, d_out] transpose of W")
-    m = L.GroupMember(d_out, r, member["scale"], 1 if member.get("rope") else 0, L._ptr(W), L._ptr(codes),
-                      L._ptr(absmax), L._ptr(A), L._ptr(B), None, None, None, None, None, L._ptr(Wt))
-    return dev, M, d_in, d_out, r, m
+    return dev, M, d_in, d_out, r, _epi_struct(member, r, d_out)
+
+
+def _epi_struct(member, r, d_out):
+    get = member.get
+    return L.GroupMember(d_out, r, member["scale"], 1 if get("rope") else 0, L._ptr(get("W")), L._ptr(get("codes")),
+                         L._ptr(get("absmax")), L._ptr(member["A"]), L._ptr(member["B"]), None, None, None, None, None,
+                         L._ptr(get("W_t")))
 
 
 def _epi_ws(backward, dt, M, d_in, m, e, device, ws):
@@ -507,6 +512,11 @@ def lora_linear_epi_bwd(X, member, dY, act: str = "none", Z=None, need_dX: bool 
     _check(dev, "dY", dY, same, M * d_out)
     if Z is not None:
         _check(dev, "Z", Z, same, M * d_out)
+    return _epi_bwd(dt, dev, M, d_in, d_out, r, m, X, dY, act, Z, need_dX, need_dbias, table16, ws)
+
+
+def _epi_bwd(dt, dev, M, d_in, d_out, r, m, X, dY, act, Z, need_dX, need_dbias, table16=None, ws=None):
+    """lora_linear_epi_bwd of checked tensors."""
     dX = torch.empty(M, d_in, dtype=X.dtype, device=dev) if need_dX else None
     dA = torch.empty(r, d_in, dtype=torch.float32, device=dev)
     dB = torch.empty(d_out, r, dtype=torch.float32, device=dev)
@@ -527,7 +537,7 @@ class LoraLinearEpiFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, X, W, A, B, bias, residual, scale, act="none", W_t=None):
-        member = {"W": W, "A": A, "B": B, "scale": scale}
+        member = {"W": W, "A": A, "B": B, "scale": scale, "W_t": W_t}
         Y, Z = lora_linear_epi_fwd(X, member, act, bias, residual, store_z=act != "none")
         ctx.save_for_backward(X, W, A, B, Z, W_t)
         ctx.scale, ctx.act = scale, act
@@ -539,9 +549,11 @@ class LoraLinearEpiFunction(torch.autograd.Function):
     def backward(ctx, dY):
         X, W, A, B, Z, W_t = ctx.saved_tensors
         dY = dY.contiguous()
-        member = {"W": W, "A": A, "B": B, "scale": ctx.scale, "W_t": W_t}
-        dX, dA, dB, dbias = lora_linear_epi_bwd(X, member, dY, ctx.act, Z, need_dX=ctx.needs_input_grad[0],
-                                                need_dbias=ctx.needs_input_grad[4])
+        dev, (M, d_in), (d_out, r) = X.device, X.shape, B.shape
+        m = _epi_struct({"W": W, "A": A, "B": B, "scale": ctx.scale, "W_t": W_t}, r, d_out)
+        _check(dev, "the gradient of Y", dY, (X.dtype,), M * d_out)
+        dX, dA, dB, dbias = _epi_bwd(L._dtype_code(X), dev, M, d_in, d_out, r, m, X, dY, ctx.act, Z,
+                                     ctx.needs_input_grad[0], ctx.needs_input_grad[4])
         return (dX, None, dA.to(A.dtype), dB.to(B.dtype), None if dbias is None else dbias.to(ctx.bias_dtype),
                 dY if ctx.needs_input_grad[5] else None, None, None, None)
 
