@@ -223,9 +223,8 @@ __device__ __forceinline__ void w4_epilogue(const GemmArgs& p, f32x16 (&acc)[w4:
     // q + 4, which a wave's halves write together, lie 32 banks apart), then
     // 8 columns of 8 rows a thread, so that residual and output move in
     // 16-byte accesses and the bias is loaded once.  The pass's residual is
-    // requested before its tile is staged.  The barriers are LDS barriers: one
-    // that also waits for memory would wait for the pass's stores (measured
-    // on MI355X: 14 us more a tile).
+    // requested before its tile is staged.  The barriers order LDS accesses
+    // alone: a pass's stores stay in flight over the next one.
     constexpr int PITCH = BN + 8;
     static_assert(64 * PITCH * 4 <= 4 * BM * 128, "the staged rows fit every ring");
     float* st = reinterpret_cast<float*>(smem);

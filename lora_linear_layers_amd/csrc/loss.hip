@@ -78,6 +78,11 @@ struct Row<float> {
 // sum s of e^(tau (z - m)); logp = tau (z_t - m) - log s.  m and log s are
 // kept apart (their sum, the log-sum-exp, would round away what a confident
 // row's small log-probability is made of).
+// Bound by reading the logits: 8192 x 128000 bf16 in 329 us, 6.4 TB/s (a large
+// copy moves 5.2 TB/s, read and written); the exponential, a quarter-rate
+// instruction, would take 0.11 ms of it.  The gradient reads and writes them
+// once: 656 us behind the forward, 6.4 TB/s.  24 x 32000: 6.1 us, a launch, one
+// round of loads and the joins.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float fexp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -293,6 +298,10 @@ hipError_t launch_token_logp_grad(int elem_bytes, const void* z, int64_t ld, int
 // the chain of dependent loads, so a chunk requests its tokens' values, the
 // offsets of 64 sequences and what those sequences carry (advantage, weight,
 // coefficient) at once, and picks the sequence's value from a lane afterwards.
+// Measured on MI355X: 1.31 M tokens in 1024 sequences (27 MB), policy sums 9.5 us,
+// finish 10.8, gradient 8.2; 1250 tokens in 8, the whole forward 7.0 us and the
+// gradient 4.7; with a load chain per token (mask, then values) and sums through
+// the LDS crossbar these were 15.6, 8.1, 14.9 and 13.3, 6.7.
 // cu is read on the device and cannot be checked before the launch: every
 // index that comes from it is clipped to [0, N], and tokens outside
 // [cu[0], cu[S]) belong to no sequence.

@@ -665,10 +665,12 @@ def lora_token_logp_bwd(logits, targets, stats, dlogp, inv_temp: float = 1.0, dl
     return dlogits
 
 
-def _loss_ws(loss, n_seq, n_tokens, device, ws):
+def _loss_ws(loss, n_seq, n_tokens, logp, ws):
+    """(workspace, its bytes); the library checks a caller's."""
     if ws is not None:
-        return ws  # the library checks its size
-    return torch.empty(int(L.lib().lora_loss_workspace_bytes(loss, n_seq, n_tokens)), dtype=torch.uint8, device=device)
+        return ws, ws.numel() * ws.element_size()
+    nbytes = L.lib().lora_loss_workspace_bytes(loss, n_seq, n_tokens)
+    return logp.new_empty(nbytes // 4), nbytes
 
 
 PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}
@@ -701,14 +703,14 @@ def lora_preference_loss_fwd(logp, cu, beta: float, ref_logp=None, mask=None, ki
     if S < 2 or S % 2:
         raise ValueError("cu must hold 2 P + 1 offsets")
     P = S // 2
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    pair_loss, rewards, coef = torch.empty(5 * P, dtype=torch.float32, device=dev).split((P, S, S))
-    ws = _loss_ws(0, S, n, dev, ws)
+    new = logp.new_empty
+    loss, pair_loss, rewards, coef = new(()), new(P), new(S), new(S)
+    ws, ws_bytes = _loss_ws(0, S, n, logp, ws)
     with _on(dev):
         L._check("lora_preference_loss_fwd", L.lib().lora_preference_loss_fwd(
             _choice("kind", PREFERENCE_KINDS, kind), P, n, float(beta), float(label_smoothing), int(average),
             L._ptr(cu), L._ptr(mask), L._ptr(logp), L._ptr(ref_logp), L._ptr(loss), L._ptr(pair_loss),
-            L._ptr(rewards), L._ptr(coef), L._ptr(ws), ws.numel(), L._stream(dev)))
+            L._ptr(rewards), L._ptr(coef), L._ptr(ws), ws_bytes, L._stream(dev)))
     return loss, pair_loss, rewards, coef
 
 
@@ -719,7 +721,7 @@ def lora_preference_loss_bwd(coef, cu, n_tokens: int, mask=None, dloss=None):
     _check_tokens(dev, n_tokens, cu, None, mask)
     if dloss is not None:
         _check(dev, "dloss", dloss, _F32, 1)
-    dlogp = torch.empty(n_tokens, dtype=torch.float32, device=dev)
+    dlogp = coef.new_empty(n_tokens)
     with _on(dev):
         L._check("lora_preference_loss_bwd", L.lib().lora_preference_loss_bwd(
             coef.numel() // 2, n_tokens, L._ptr(cu), L._ptr(mask), L._ptr(coef), L._ptr(dloss), L._ptr(dlogp),
@@ -746,14 +748,14 @@ def lora_policy_loss_fwd(logp, cu, advantages, old_logp=None, ref_logp=None, mas
     fp32 [n], cu int64 [S + 1], advantages fp32 [S], or [n] with per_token; stats: the policy part, the KL part, the
     share of clipped tokens, the number of tokens.  weight goes to lora_policy_loss_bwd."""
     n, S, dev = _policy_checks(logp, cu, advantages, old_logp, ref_logp, mask, per_token)
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    stats, weight = torch.empty(4 + S, dtype=torch.float32, device=dev).split((4, S))
-    ws = _loss_ws(1, S, n, dev, ws)
+    new = logp.new_empty
+    loss, stats, weight = new(()), new(4), new(S)
+    ws, ws_bytes = _loss_ws(1, S, n, logp, ws)
     with _on(dev):
         L._check("lora_policy_loss_fwd", L.lib().lora_policy_loss_fwd(
             _choice("reduction", POLICY_REDUCTIONS, reduction), S, n, float(eps_low), float(eps_high), float(beta),
             float(norm), L._ptr(cu), L._ptr(mask), L._ptr(logp), L._ptr(old_logp), L._ptr(ref_logp),
-            L._ptr(advantages), int(per_token), L._ptr(loss), L._ptr(stats), L._ptr(weight), L._ptr(ws), ws.numel(),
+            L._ptr(advantages), int(per_token), L._ptr(loss), L._ptr(stats), L._ptr(weight), L._ptr(ws), ws_bytes,
             L._stream(dev)))
     return loss, stats, weight
 
@@ -765,7 +767,7 @@ def lora_policy_loss_bwd(logp, cu, advantages, weight, old_logp=None, ref_logp=N
     _check(dev, "weight", weight, _F32, S)
     if dloss is not None:
         _check(dev, "dloss", dloss, _F32, 1)
-    dlogp = torch.empty(n, dtype=torch.float32, device=dev)
+    dlogp = logp.new_empty(n)
     with _on(dev):
         L._check("lora_policy_loss_bwd", L.lib().lora_policy_loss_bwd(
             S, n, float(eps_low), float(eps_high), float(beta), L._ptr(cu), L._ptr(mask), L._ptr(logp),
