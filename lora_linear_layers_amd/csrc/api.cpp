@@ -164,21 +164,30 @@ struct StreamPlan {
 //     over 4096: 98 -> 91 us, over 14336: 308 -> 224; over 2048: 60 against 65);
 //   below 64 tiles the split 128 x 128 tiles are faster (512 x 4096: 54
 //     against 73 us).
-// transpose: W^T has to be made first (0.9 us a MB of it), so the gain must
-// carry that too: only from t > 128, where two rounds are saved.
+// transpose: W^T has to be made first, 0.37 us a MB of W (4096 x 4096: 13 us),
+// which the gain over the product through W itself (128 x 128 tiles, 1.4 us a
+// stage and round) has to carry: the backward of 2048 tokens, 4096 -> 4096, 149
+// -> 134 us, of 4100 tokens 318 -> 252; 512 tokens, 14336 -> 4096 would be 154 ->
+// 172.
 StreamPlan stream_plan(int64_t M, int64_t N, int64_t K, int64_t r, bool transpose) {
   StreamPlan S;
   const int64_t r8 = rup(r, 8), t = cdiv(M, 256) * cdiv(N, 256), nk = K / 64 + cdiv(r, 64);
   if (M < 1 || K % 64 || K < 64 || !whole_ld_fits(std::max({K, r8, N})) || t > INT32_MAX / 2) return S;
   if (M % 256 == 0 && N % 256 == 0 && t % 256 == 0) return S;  // the whole-tile kernel
   const int64_t rest = t % 256;
-  if (t > 128) {
-    if (t <= 256 && nk < (transpose ? 32 : 12)) return S;
-    S.half = t > 256 && rest <= 128 && nk >= 24 ? (int)rest : 0;
+  double gain;  // us over the product through W itself
+  if (t > 256) {
+    S.half = rest <= 128 && nk >= 24 ? (int)rest : 0;
+    gain = 0.5 * nk * cdiv(t, 256);
+  } else if (t > 128) {
+    if (nk < 12) return S;
+    gain = 1.5 * nk - 9;
   } else {
-    if (t < 64 || nk < 48 || transpose || cdiv(M, 128) * cdiv(N, 128) < 256) return S;
+    if (t < 64 || nk < 48 || cdiv(M, 128) * cdiv(N, 128) < 256) return S;
     S.half = (int)t;
+    gain = 0.74 * nk - 26;
   }
+  if (transpose && gain < 0.37e-6 * 2 * double(N) * double(K)) return StreamPlan();
   S.full = (int)(t - S.half);
   S.early = S.half ? 3 : 0;
   S.ok = true;
