@@ -448,6 +448,11 @@ __device__ __forceinline__ float kl_term(float d) {
   return fabsf(d) < 0.5f ? d * d * q : exp_ratio(d) - 1.f - d;
 }
 
+// e^d - 1: d and the sum's own series where the two cancel
+__device__ __forceinline__ float kl_slope(float d) {
+  return fabsf(d) < 0.5f ? d + kl_term(d) : exp_ratio(d) - 1.f;
+}
+
 struct PolicyArgs {
   const float* logp;
   const float* old;
@@ -889,10 +894,7 @@ __global__ void __launch_bounds__(256) policy_grad_kernel(const SeqArgs a, const
                const PolicyTok k = policy_tok(p, r, adv);
                float d = 0.f;
                if (!k.cut && k.adv != 0.f) d = -k.ratio * k.adv;
-               if (p.beta != 0.f) {  // e^d - 1 = d + (e^d - d - 1)
-                 const float x = (float)((double)r.ref - (double)r.lp);
-                 d -= p.beta * (x + kl_term(x));
-               }
+               if (p.beta != 0.f) d -= p.beta * kl_slope((float)((double)r.ref - (double)r.lp));
                return g * w * d;
              });
 }

@@ -323,6 +323,22 @@ def test_policy_kl_of_near_equal_policies(lib):
 
 
 @pytest.mark.gpu
+def test_policy_kl_gradient_of_distant_policies(lib):
+    # 1 - e^d keeps its digits where d itself has none left for it, and where the reference's probability is 0
+    lp = np.zeros(12, np.float32)
+    ref = np.array([-0.49, -0.51, -17.3, -1000.3, -123456.7, -3.0e8, -np.inf, 0.49, 0.51, 17.3, 80.2, 0.0], np.float32)
+    L, R, A, C = _dev(lp, ref, np.zeros(12, np.float32), np.arange(13, dtype=np.int64))
+    _, _, w = lib.lora_policy_loss_fwd(L, C, A, ref_logp=R, beta=0.5, reduction="constant", norm=1.0)
+    got = lib.lora_policy_loss_bwd(L, C, A, w, ref_logp=R, beta=0.5).cpu().double().numpy()
+    d = ref.astype(np.float64)
+    e = np.array([math.expm1(x) for x in d])
+    # the slope's bound of the head of this file, and 3 roundings of the products
+    shift = np.where(np.isinf(d), 0, np.abs(d))
+    tol = 0.5 / 12 * (np.where(np.isinf(d), 0, np.exp(d)) * (2 + shift) * 2 * U + U) + 4 * U * np.abs(0.5 * e / 12)
+    assert (np.abs(got + 0.5 * e / 12) <= tol).all(), got * -24 - e
+
+
+@pytest.mark.gpu
 def test_policy_gradient_against_differences(lib):
     cu, n = _packed([4, 0, 6, 3])
     lp, ref, old, mask, _ = _draw(31, n)
