@@ -97,7 +97,8 @@ __device__ __forceinline__ float act_grad(float z, int act) {
     }
     case ACT_GELU_TANH: {
       const float s = sigmoid<FAST>(2.f * gelu_tanh_arg(z));
-      return s + 2.f * z * s * (1.f - s) * 0.79788456080286536f * (1.f + 3.f * 0.044715f * z * z);
+      const float w = s * (1.f - s);  // (0 far out, where z^2 may be infinite)
+      return w == 0.f ? s : s + 2.f * z * w * 0.79788456080286536f * (1.f + 3.f * 0.044715f * z * z);
     }
     default: return 1.f;
   }

@@ -242,6 +242,25 @@ def test_epilogue_activation_values(lib, dtype, act):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_epilogue_activation_of_huge_values(lib, dtype):
+    # the activations' limits at values whose square or cube is no fp32 number: z or 0, slope 1 or 0
+    X = torch.zeros(8, 64, dtype=dtype, device="cuda")
+    X.view(-1)[:12] = torch.tensor([1e9, 1e13, 1e20, 3e38, 500.0, 95.0, -1e9, -1e13, -1e20, -3e38, -500.0, -120.0])
+    m = {"W": torch.eye(64, dtype=dtype, device="cuda"), "A": torch.zeros(8, 64, dtype=dtype, device="cuda"),
+         "B": torch.zeros(64, 8, dtype=dtype, device="cuda"), "scale": 1.0}
+    for act in ACTS:
+        if act == "none":
+            continue
+        Y, Z = lib.lora_linear_epi_fwd(X, m, act, store_z=True)
+        dX, _, _, _ = lib.lora_linear_epi_bwd(X, m, torch.ones_like(X), act, Z)
+        y, d, x = Y.view(-1)[:12].double(), dX.view(-1)[:12].double(), X.view(-1)[:12].double()
+        up = x > 0
+        assert torch.equal(y[up], x[up]) and (y[~up].abs() <= 1e-37).all(), act
+        assert (d[up] == 1).all() and (d[~up].abs() <= 1e-37).all(), (act, d)
+
+
+@pytest.mark.gpu
 def test_epilogue_exact_on_integers(lib):
     # small integers: every product, sum, relu and residual is exact, on every kind of tile
     for M, k, d, r in ((4096, 64, 4096, 8), (2050, 1024, 4104, 8), (2048, 3200, 2056, 8), (1, 128, 8192, 32), (300, 264, 392, 16), (40, 512, 768, 5), (9, 64, 64, 8)):
