@@ -296,7 +296,7 @@ def _group_members(X, members):
 
 def _group_ws(backward, dt, M, d_in, arr, device, ws):
     if ws is not None:
-        return ws  # the library checks its size
+        return _check_ws(device, ws)
     n = int(L.lib().lora_group_workspace_bytes(int(backward), dt, M, d_in, len(arr), arr))
     return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
 
@@ -371,7 +371,7 @@ def lora_group_bwd(X, members, dYs, positions=None, cos=None, sin=None, table16=
 
 def _swiglu_ws(backward, dt, M, d_in, arr, device, ws):
     if ws is not None:
-        return ws  # the library checks its size
+        return _check_ws(device, ws)
     n = int(L.lib().lora_swiglu_workspace_bytes(int(backward), dt, M, d_in, arr))
     return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
 
@@ -470,7 +470,7 @@ def _epi_struct(member, r, d_out):
 
 def _epi_ws(backward, dt, M, d_in, m, e, device, ws):
     if ws is not None:
-        return ws  # the library checks its size
+        return _check_ws(device, ws)
     n = int(L.lib().lora_linear_epi_workspace_bytes(int(backward), dt, M, d_in, m, e))
     return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
 
@@ -610,6 +610,12 @@ def _check(device, name, t, dtypes, numel=None):
         raise ValueError(f"{name} has {t.numel()} values, not {numel}")
 
 
+def _check_ws(device, ws):
+    """A caller's workspace, on the device (the library checks its size)."""
+    _check(device, "ws", ws, (ws.dtype,))
+    return ws
+
+
 def _gpu(t):
     if not t.is_cuda:
         raise ValueError("tensors must be on a GPU")
@@ -666,9 +672,9 @@ def lora_token_logp_bwd(logits, targets, stats, dlogp, inv_temp: float = 1.0, dl
 
 
 def _loss_ws(loss, n_seq, n_tokens, logp, ws):
-    """(workspace, its bytes); the library checks a caller's."""
+    """(workspace, its bytes)"""
     if ws is not None:
-        return ws, ws.numel() * ws.element_size()
+        return _check_ws(logp.device, ws), ws.numel() * ws.element_size()
     nbytes = L.lib().lora_loss_workspace_bytes(loss, n_seq, n_tokens)
     return logp.new_empty(nbytes // 4), nbytes
 
@@ -804,7 +810,8 @@ class LoraHeadLogpFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, X, W, A, B, scale, targets, inv_temp=1.0):
-        logits = lora_linear_fwd(X, W, A, B, scale)
+        with _on(_gpu(X)):
+            logits = lora_linear_fwd(X, W, A, B, scale)
         logp, stats = lora_token_logp_fwd(logits, targets, inv_temp)
         ctx.save_for_backward(X, W, A, B, logits, targets, stats)
         ctx.scale, ctx.inv_temp = scale, inv_temp
@@ -815,7 +822,8 @@ class LoraHeadLogpFunction(torch.autograd.Function):
     def backward(ctx, dlogp):
         X, W, A, B, logits, targets, stats = ctx.saved_tensors
         dlogits = lora_token_logp_bwd(logits, targets, stats, _f32c(dlogp), ctx.inv_temp)
-        dX, dA, dB = lora_linear_bwd(X, W, A, B, ctx.scale, dlogits, need_dX=ctx.needs_input_grad[0])
+        with _on(X.device):
+            dX, dA, dB = lora_linear_bwd(X, W, A, B, ctx.scale, dlogits, need_dX=ctx.needs_input_grad[0])
         return dX, None, dA.to(A.dtype), dB.to(B.dtype), None, None, None
 
 

@@ -511,6 +511,25 @@ def test_calls_run_on_their_tensors_device(monkeypatch):
     assert now == [0] and seen == [3, 0]
 
 
+@pytest.mark.gpu
+def test_host_workspaces_are_refused(lib):
+    X, m, _, _, dY = _inputs(3, 12, 64, 64, 8, "bf16")
+    ws = torch.empty(1 << 20, dtype=torch.uint8)
+    lp, cu = torch.zeros(4, device="cuda"), torch.tensor([0, 2, 4], device="cuda")
+    for call in (lambda: lib.lora_linear_epi_fwd(X, m, ws=ws), lambda: lib.lora_linear_epi_bwd(X, m, dY, ws=ws),
+                 lambda: lib.lora_preference_loss_fwd(lp, cu, 0.1, ws=ws),
+                 lambda: lib.lora_policy_loss_fwd(lp, cu, torch.zeros(2, device="cuda"), ws=ws)):
+        with pytest.raises(ValueError, match="ws is on cpu"):
+            call()
+
+
+def test_workspace_of_another_device_is_refused():
+    from lora_linear_layers_amd import functional as F
+
+    with pytest.raises(ValueError, match="ws is on cpu"):
+        F._check_ws(torch.device("cuda:0"), torch.empty(16, dtype=torch.uint8))
+
+
 def test_epilogue_refusals():
     import ctypes
 
