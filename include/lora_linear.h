@@ -468,7 +468,7 @@ int lora_transpose(const void* src, int64_t rows, int64_t cols, void* dst, void*
  *     logp_i = tau z_{i,t_i} - log sum_j e^(tau z_{i,j})
  *     dz_{i,j} = dlogp_i tau (1[j = t_i] - e^(tau z_{i,j}) / sum_k e^(tau z_{i,k}))
  * logits: [n, vocab] of the dtype, row stride ld >= vocab elements; targets:
- * int64 [n]; tau = inv_temp, finite and above 0.  A target outside
+ * int64 [n]; tau = inv_temp, above 0 and at most LORA_LOGP_MAX_INV_TEMP.  A target outside
  * [0, vocab) names no token: logp is 0 and the row's gradient zeros.  stats
  * [n, 2] fp32 receives each row's maximum logit m and log sum_j e^(tau (z_j - m))
  * (their sum tau m + that is the log-sum-exp); the backward takes them back.
@@ -480,6 +480,7 @@ int lora_transpose(const void* src, int64_t rows, int64_t cols, void* dst, void*
  * alignment only, so rows may be sliced (logits[:-1], targets[1:]).
  * 0 <= n < 2^31, 1 <= vocab < 2^31.
  */
+#define LORA_LOGP_MAX_INV_TEMP 1e38f /* (tau log2 e is an fp32 number) */
 int lora_token_logp_fwd(int dtype, int64_t n, int64_t vocab, const void* logits, int64_t ld, const int64_t* targets,
                         float inv_temp, float* logp, float* stats, void* stream);
 int lora_token_logp_bwd(int dtype, int64_t n, int64_t vocab, const void* logits, int64_t ld, const int64_t* targets,

@@ -2071,7 +2071,7 @@ int lora_transpose(const void* src, int64_t rows, int64_t cols, void* dst, void*
 static int check_logp(int dtype, int64_t n, int64_t vocab, int64_t ld, float inv_temp) {
   if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_ERR_DTYPE;
   if (n < 0 || n >= kMaxDim || vocab < 1 || vocab >= kMaxDim || ld < vocab || ld >= kMaxDim) return LORA_ERR_SHAPE;
-  if (!(inv_temp > 0.f) || std::isinf(inv_temp)) return LORA_ERR_SHAPE;
+  if (!(inv_temp > 0.f) || inv_temp > LORA_LOGP_MAX_INV_TEMP) return LORA_ERR_SHAPE;
   return LORA_OK;
 }
 

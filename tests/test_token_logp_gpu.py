@@ -253,6 +253,7 @@ def test_logp_refusals():
         assert f(dtype=2) == -4
         assert f(n=-1) == -2 and f(V=0) == -2 and f(ld=7) == -2 and f(V=2 ** 31, ld=2 ** 31) == -2
         assert f(tau=0.0) == -2 and f(tau=-1.0) == -2 and f(tau=float("nan")) == -2 and f(tau=float("inf")) == -2
+        assert f(tau=1.1e38) == -2  # tau log2 e would be infinite
         assert f(z=None) == -1 and f(t=None) == -1 and f(st=None) == -1
         assert f(z=P + 1) == -3 and f(dtype=0, z=P + 2) == -3 and f(t=P + 4) == -3 and f(st=P + 2) == -3
     assert fwd(lp=None) == -1 and fwd(lp=P + 2) == -3
