@@ -303,6 +303,33 @@ def test_epilogue_plain_layer_bit_for_bit(lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("k", [64, 72])  # 256 x 256 tiles past whole stages, the 256 x 256 general form
+def test_epilogue_offsets_past_32_bits(lib, k):
+    # 2^31 elements of Y, Z, the residual, dY and dZ and more, in small integers: every sum is exact whatever its
+    # order, so the rows at both ends are those of the same rows alone
+    M, d, r = 140003, 16384, 8
+    gen = torch.Generator("cuda").manual_seed(k)
+    draw = lambda *n: torch.randint(-2, 3, n, generator=gen, device="cuda", dtype=torch.int8).bfloat16()  # noqa: E731
+    X, R, dY, bias = draw(M, k), draw(M, d), draw(M, d), draw(d)
+    m = {"W": draw(d, k), "A": draw(r, k), "B": draw(d, r), "scale": 1.0}
+    Y, Z = lib.lora_linear_epi_fwd(X, m, "relu", bias, R, store_z=True)
+    dX, dA, dB, db = lib.lora_linear_epi_bwd(X, m, dY, "relu", Z, need_dbias=True)
+    for at in (slice(0, 40), slice(131060, 131090), slice(M - 40, M)):  # (131072 x 16384 = 2^31)
+        y, z = lib.lora_linear_epi_fwd(X[at], m, "relu", bias, R[at], store_z=True)
+        dx = lib.lora_linear_epi_bwd(X[at], m, dY[at], "relu", z)[0]
+        assert torch.equal(Y[at], y) and torch.equal(Z[at], z) and torch.equal(dX[at], dx)
+    P = X.float() @ m["A"].float().T  # below 2^9, exact
+    dZ = dY * (Z > 0)
+    sums, mags = torch.zeros(d, r + 1, device="cuda", dtype=torch.float64), torch.zeros(d, r, device="cuda", dtype=torch.float64)
+    for i in range(0, M, 20000):
+        g, p = dZ[i:i + 20000].double().T.contiguous(), P[i:i + 20000].bfloat16().double()
+        sums += g @ torch.cat([p, torch.ones_like(p[:, :1])], 1)
+        mags += g.abs() @ p.abs()
+    assert mags.max() < 2 ** 24  # (fp32 sums of integers: exact)
+    assert torch.equal(db.double(), sums[:, r]) and torch.equal(dB.double(), sums[:, :r]) and dA.isfinite().all()
+
+
+@pytest.mark.gpu
 def test_epilogue_not_finite(lib):
     X, m, bias, res, _ = _inputs(3, 12, 64, 64, 8, "bf16")
     res[3, 5], res[4, 6], bias[7] = float("nan"), float("inf"), -float("inf")
