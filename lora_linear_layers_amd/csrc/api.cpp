@@ -217,6 +217,8 @@ struct Layout {
   FewPlan few;       // few tokens: the two-launch path (its regions from offset 0)
   StreamPlan stream;  // epilogue layer's Y or dX: ragged 256 x 256 tiles spread over the CUs
   size_t st_part = 0, st_cnt = 0;
+  bool pair = false;  // epilogue layer's backward: both panels, then dB and dA, in a launch each
+  size_t ppart2 = 0;  // the second panel's partials
 };
 
 // 256x256 tiles when they still give at least one tile per CU, else 128x128.
@@ -554,12 +556,20 @@ struct PanelSrc {
   int rows[kPanelSrcMax] = {};
 };
 
+GemmArgs panel_args(const void* X, int64_t ldx, const void* R, int64_t ldr, int64_t M, int64_t rows, int64_t K,
+                    int64_t r, int64_t r8, int64_t ksplit, float* part) {
+  GemmArgs a = blank();
+  a.a1 = X; a.lda1 = ldx; a.b1 = R; a.ldb1 = ldr; a.K1 = K;
+  a.m_load = M; a.m_store = rows; a.n_load = r; a.n_store = r8;
+  a.k_split = ksplit; a.c = part; a.ldc = r8; a.part_stride = rows * r8;
+  return a;
+}
+
 int panel_bf16(const void* X, int64_t ldx, const void* R, int64_t ldr, int64_t M, int64_t rows, int64_t K, int64_t r,
                int64_t r8, int splits, int64_t ksplit, const ColScale& cs, float* part, uint16_t* out, int64_t ldo,
                uint16_t* outt, int64_t ldot, hipStream_t st, const PanelSrc* src = nullptr, int* zero = nullptr,
                int nzero = 0) {
-  GemmArgs a = blank();
-  a.a1 = X; a.lda1 = ldx; a.b1 = R; a.ldb1 = ldr; a.K1 = K;
+  GemmArgs a = panel_args(X, ldx, R, ldr, M, rows, K, r, r8, ksplit, part);
   if (src) {
     a.n_src = src->n;
     for (int g = 0; g < src->n; ++g) {
@@ -568,8 +578,6 @@ int panel_bf16(const void* X, int64_t ldx, const void* R, int64_t ldr, int64_t M
       a.rs_rows[g] = src->rows[g];
     }
   }
-  a.m_load = M; a.m_store = rows; a.n_load = r; a.n_store = r8;
-  a.k_split = ksplit; a.c = part; a.ldc = r8; a.part_stride = rows * r8;
   const double Md = double(M), kd = double(K), rd = double(r);
   HIPTRY(gemm(G_BF16_PANEL_SPLIT_NT, a, splits, st, 2 * Md * rd * kd,
               (Md * kd + rd * kd) * 2 + 4.0 * splits * rows * r8));
@@ -914,9 +922,10 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
   } else {
     // Pt = (s X A^T)^T  [r8, M8], recomputed from X (rows M..M8 and columns r..r8 are zeros)
     float* pp = reinterpret_cast<float*>(w + L.ppart);
-    if (!ov)
+    uint16_t* pt = reinterpret_cast<uint16_t*>(w + L.pt);
+    if (!ov && !L.pair)
       TRY(panel_bf16(Xp, d_in, A, d_in, M, L.M8, d_in, r, L.r8, L.splits_p, L.ksplit_p, col_scale(scale), pp,
-                     nullptr, 0, reinterpret_cast<uint16_t*>(w + L.pt), L.M8, st));
+                     nullptr, 0, pt, L.M8, st));
     // Bt = B^T [r8, d_out] (and A^T for the whole-tile dX below, in the same
     // launch); then Qs = s G B [M8, r8] and Qt = Qs^T [r8, M8]
     const void* Bt = ov ? ov->Bt : nullptr;
@@ -940,9 +949,25 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
         }));
       }
     }
-    TRY(panel_bf16(G, d_out, Bt, d_out, M, L.M8, d_out, r, L.r8, L.splits_q, L.ksplit_q, col_scale(scale), pp,
-                   static_cast<uint16_t*>(Qs), ldqs, static_cast<uint16_t*>(Qt), L.M8, st, nullptr,
-                   reinterpret_cast<int*>(w + L.st_cnt), dX ? L.stream.half : 0));
+    int* cnt = reinterpret_cast<int*>(w + L.st_cnt);
+    const int ncnt = dX ? L.stream.half : 0;
+    if (L.pair) {
+      float* pq = reinterpret_cast<float*>(w + L.ppart2);
+      const GemmArgs a = panel_args(Xp, d_in, A, d_in, M, L.M8, d_in, r, L.r8, L.ksplit_p, pp);
+      const GemmArgs b = panel_args(G, d_out, Bt, d_out, M, L.M8, d_out, r, L.r8, L.ksplit_q, pq);
+      const double el = double(L.M8) * L.r8;
+      HIPTRY(timed(G_BF16_PANEL_SPLIT_NT, 2 * Md * rr * (ki + ko),
+                   (Md + rr) * (ki + ko) * 2 + 4.0 * (L.splits_p + L.splits_q) * el, st,
+                   [&] { return launch_gemm_pair(G_BF16_PANEL_SPLIT_NT, a, L.splits_p, b, L.splits_q, st); }));
+      HIPTRY(timed(K_PANEL, (L.splits_p + L.splits_q) * el, (4.0 * (L.splits_p + L.splits_q) + 6) * el, st, [&] {
+        return launch_panel_reduce_pair({pp, L.splits_p, nullptr, pt},
+                                        {pq, L.splits_q, static_cast<uint16_t*>(Qs), static_cast<uint16_t*>(Qt)}, L.M8,
+                                        L.r8, col_scale(scale), st, cnt, ncnt);
+      }));
+    } else {
+      TRY(panel_bf16(G, d_out, Bt, d_out, M, L.M8, d_out, r, L.r8, L.splits_q, L.ksplit_q, col_scale(scale), pp,
+                     static_cast<uint16_t*>(Qs), ldqs, static_cast<uint16_t*>(Qt), L.M8, st, nullptr, cnt, ncnt));
+    }
   }
   // dX = [G | Qs] [W ; A]; with a dropout mask the rank-r term is added
   // separately, masked: dX = G W, then dX += keep * (Qs A)
@@ -1022,28 +1047,31 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
   ReduceBatch own;
   ReduceBatch* red = f32 ? nullptr : (ov && ov->red ? ov->red : &own);
   // dB^T = Pt G  -> partials [splits][r8, d_out] -> dB [d_out, r]
-  {
-    GemmArgs a = blank();
-    a.a1 = Pt; a.lda1 = L.M8; a.b1 = G; a.ldb1 = d_out; a.K1 = M;
-    a.m_load = L.r8; a.m_store = L.r8; a.n_load = d_out; a.n_store = d_out;
-    a.k_split = L.ksplit_dB; a.c = partb; a.ldc = d_out; a.part_stride = L.r8 * d_out;
-    HIPTRY(gemm(ksplit, a, L.splits_dB, st, 2 * rr * ko * Md,
-                (rr * Md + Md * ko) * e + 4.0 * L.splits_dB * L.r8 * ko));
-    if (red)
-      HIPTRY(red->add(partb, L.splits_dB, r, d_out, L.r8 * d_out, true, dB));
-    else
-      HIPTRY(timed(K_REDUCE, double(L.splits_dB) * rr * ko, 4.0 * (L.splits_dB + 1) * rr * ko, st, [&] {
-        return launch_reduce_splits(partb, L.splits_dB, r, d_out, L.r8 * d_out, true, dB, st);
-      }));
-  }
+  GemmArgs ab = blank();
+  ab.a1 = Pt; ab.lda1 = L.M8; ab.b1 = G; ab.ldb1 = d_out; ab.K1 = M;
+  ab.m_load = L.r8; ab.m_store = L.r8; ab.n_load = d_out; ab.n_store = d_out;
+  ab.k_split = L.ksplit_dB; ab.c = partb; ab.ldc = d_out; ab.part_stride = L.r8 * d_out;
+  const double fb = 2 * rr * ko * Md, bb = (rr * Md + Md * ko) * e + 4.0 * L.splits_dB * L.r8 * ko;
   // dA = Qt X -> partials [splits][r8, d_in] -> dA [r, d_in]
+  GemmArgs aa = blank();
+  aa.a1 = Qt; aa.lda1 = L.M8; aa.b1 = Xp; aa.ldb1 = d_in; aa.K1 = M;
+  aa.m_load = L.r8; aa.m_store = L.r8; aa.n_load = d_in; aa.n_store = d_in;
+  aa.k_split = L.ksplit_dA; aa.c = part; aa.ldc = d_in; aa.part_stride = L.r8 * d_in;
+  const double fa = 2 * rr * ki * Md, ba = (rr * Md + Md * ki) * e + 4.0 * L.splits_dA * L.r8 * ki;
+  const bool both = L.pair && gemm_pair_fits(ksplit, ab, aa);
+  if (both)
+    HIPTRY(timed(ksplit, fa + fb, ba + bb, st,
+                 [&] { return launch_gemm_pair(ksplit, ab, L.splits_dB, aa, L.splits_dA, st); }));
+  else
+    HIPTRY(gemm(ksplit, ab, L.splits_dB, st, fb, bb));
+  if (red)
+    HIPTRY(red->add(partb, L.splits_dB, r, d_out, L.r8 * d_out, true, dB));
+  else
+    HIPTRY(timed(K_REDUCE, double(L.splits_dB) * rr * ko, 4.0 * (L.splits_dB + 1) * rr * ko, st, [&] {
+      return launch_reduce_splits(partb, L.splits_dB, r, d_out, L.r8 * d_out, true, dB, st);
+    }));
   if (!ov) {
-    GemmArgs a = blank();
-    a.a1 = Qt; a.lda1 = L.M8; a.b1 = Xp; a.ldb1 = d_in; a.K1 = M;
-    a.m_load = L.r8; a.m_store = L.r8; a.n_load = d_in; a.n_store = d_in;
-    a.k_split = L.ksplit_dA; a.c = part; a.ldc = d_in; a.part_stride = L.r8 * d_in;
-    HIPTRY(gemm(ksplit, a, L.splits_dA, st, 2 * rr * ki * Md,
-                (rr * Md + Md * ki) * e + 4.0 * L.splits_dA * L.r8 * ki));
+    if (!both) HIPTRY(gemm(ksplit, aa, L.splits_dA, st, fa, ba));
     if (red)
       HIPTRY(red->add(part, L.splits_dA, r, d_in, L.r8 * d_in, false, dA));
     else
@@ -1584,7 +1612,11 @@ EpiLayout make_epi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, const lo
     if (e.act != LORA_ACT_NONE) E.dz = take(size_t(M) * m.d_out * elem_bytes(dtype));
     // about two blocks of 256 columns a CU, at least 8 tokens each
     E.chunks = (int)std::max<int64_t>(1, std::min<int64_t>({64, cdiv(M, 8), cdiv(512, cdiv(m.d_out, 256))}));
-    E.part = take(size_t(E.chunks) * m.d_out * 4);
+    // (read before the panels start: the second one's partials take its place)
+    E.L.pair = dtype == LORA_BF16 && panel_dma_fits(E.L.r8, d_in, d_in) && panel_dma_fits(E.L.r8, m.d_out, m.d_out);
+    const size_t p2 = E.L.pair ? size_t(E.L.splits_q) * E.L.M8 * E.L.r8 * 4 : 0;
+    E.part = take(std::max(size_t(E.chunks) * m.d_out * 4, p2));
+    E.L.ppart2 = E.part;
   }
   return E;
 }

@@ -63,9 +63,9 @@ struct Cfg {
 constexpr int vmcnt_imm(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }
 }  // namespace pdma
 
+// the partial of row tile mt over split z
 template <int BM, int BN>
-__global__ void __launch_bounds__(pdma::NT) __attribute__((amdgpu_waves_per_eu(1, 1)))
-panel_dma_kernel(const GemmArgs p) {
+__device__ __forceinline__ void panel_dma_tile(const GemmArgs& p, const int mt, const int z) {
   using namespace pdma;
   using C = Cfg<BM, BN>;
   constexpr int NS = C::NS, LEAD = NS - 1, FM = C::FM, FN = C::FN;
@@ -77,7 +77,6 @@ panel_dma_kernel(const GemmArgs p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l32 = lane & 31, hh = lane >> 5;
   const int wm = wave / C::WN, wn = wave % C::WN;
-  const int mt = (int)(blockIdx.x % p.tiles_m), z = (int)(blockIdx.x / p.tiles_m);
   const int64_t m0 = (int64_t)mt * BM;
   const int64_t kbeg = (int64_t)z * p.k_split;
   const int64_t kend = kbeg + p.k_split < p.K1 ? kbeg + p.k_split : p.K1;
@@ -207,6 +206,28 @@ panel_dma_kernel(const GemmArgs p) {
     }
 }
 
+template <int BM, int BN>
+__global__ void __launch_bounds__(pdma::NT) __attribute__((amdgpu_waves_per_eu(1, 1)))
+panel_dma_kernel(const GemmArgs p) {
+  panel_dma_tile<BM, BN>(p, (int)(blockIdx.x % p.tiles_m), (int)(blockIdx.x / p.tiles_m));
+}
+
+// Two of a layer's launches at once (an epilogue layer's backward: the panels
+// s X A^T and s dZ B, then dB and dA): at a few thousand tokens each alone
+// fills half of the CUs.  Grid rows [0, s0) are the first one's splits, the
+// rest the second's.
+struct GemmPair {
+  GemmArgs g[2];
+  int s0;
+};
+
+template <int BM, int BN>
+__global__ void __launch_bounds__(pdma::NT) __attribute__((amdgpu_waves_per_eu(1, 1)))
+panel_dma_pair_kernel(const GemmPair q) {
+  const int y = (int)blockIdx.y, w = y >= q.s0 ? 1 : 0;
+  panel_dma_tile<BM, BN>(q.g[w], (int)blockIdx.x, w ? y - q.s0 : y);
+}
+
 // ---------------------------------------------------------------------------
 // Token-split partials of the adapters' gradients for up to 128 rows of C
 // (BR = 64: one adapter's rank; BR = 128: a group's stacked ranks):
@@ -246,9 +267,9 @@ struct Cfg {
 };
 }  // namespace sdma
 
+// column tile nt over split z
 template <int BR, int NS_>
-__global__ void __launch_bounds__(sdma::NT) __attribute__((amdgpu_waves_per_eu(1, 2)))
-splitnn_dma_kernel(const GemmArgs p) {
+__device__ __forceinline__ void splitnn_dma_tile(const GemmArgs& p, const int nt, const int z) {
   using namespace sdma;
   using C = Cfg<BR, NS_>;
   constexpr int NS = C::NS, LEAD = NS - 1, FM = C::FM, FN = C::FN;
@@ -263,7 +284,6 @@ splitnn_dma_kernel(const GemmArgs p) {
   // scalar; the DMA resources built from them must be (a coordinate left
   // in vector registers, as a division of a flat id leaves it, makes the
   // compiler wrap every DMA in a loop over the lanes' values)
-  const int nt = (int)blockIdx.x, z = (int)blockIdx.y;
   const int64_t n0 = (int64_t)nt * BN;
   const int64_t kbeg = (int64_t)z * p.k_split;
   const int64_t kend = kbeg + p.k_split < p.K1 ? kbeg + p.k_split : p.K1;
@@ -402,6 +422,20 @@ splitnn_dma_kernel(const GemmArgs p) {
         if (col < p.n_store) out[row * p.ldc + col] = acc[i][j][v];
       }
     }
+}
+
+template <int BR, int NS_>
+__global__ void __launch_bounds__(sdma::NT) __attribute__((amdgpu_waves_per_eu(1, 2)))
+splitnn_dma_kernel(const GemmArgs p) {
+  splitnn_dma_tile<BR, NS_>(p, (int)blockIdx.x, (int)blockIdx.y);
+}
+
+template <int BR, int NS_>
+__global__ void __launch_bounds__(sdma::NT) __attribute__((amdgpu_waves_per_eu(1, 2)))
+splitnn_dma_pair_kernel(const GemmPair q) {
+  const int y = (int)blockIdx.y, w = y >= q.s0 ? 1 : 0;
+  if ((int64_t)blockIdx.x * sdma::BN >= q.g[w].n_store) return;  // (the grid is as wide as the wider one)
+  splitnn_dma_tile<BR, NS_>(q.g[w], (int)blockIdx.x, w ? y - q.s0 : y);
 }
 
 }  // namespace lora

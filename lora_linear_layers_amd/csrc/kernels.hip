@@ -102,9 +102,49 @@ bool panel_fits(const GemmArgs& a) {
   return a.K2 == 0 && a.n_load <= a.n_store && panel_dma_fits(a.n_store, a.lda1, a.ldb1);
 }
 
+// Both of a pair (GemmPair) by one of the two launches above.
+hipError_t run_panel_pair(const GemmPair& q, int s1, hipStream_t st) {
+  constexpr int BM = PANEL_BM;
+  const int64_t tm = (q.g[0].m_store + BM - 1) / BM;
+  if (tm <= 0) return hipSuccess;
+  const dim3 grid((unsigned)tm, (unsigned)(q.s0 + s1));
+  if (q.g[0].n_store <= 64)
+    hipLaunchKernelGGL((panel_dma_pair_kernel<BM, 64>), grid, dim3(pdma::NT), 0, st, q);
+  else if (q.g[0].n_store <= 128)
+    hipLaunchKernelGGL((panel_dma_pair_kernel<BM, 128>), grid, dim3(pdma::NT), 0, st, q);
+  else
+    hipLaunchKernelGGL((panel_dma_pair_kernel<BM, 256>), grid, dim3(pdma::NT), 0, st, q);
+  return hipGetLastError();
+}
+
+hipError_t run_splitnn_pair(const GemmPair& q, int s1, hipStream_t st) {
+  const int64_t t0 = (q.g[0].n_store + sdma::BN - 1) / sdma::BN, t1 = (q.g[1].n_store + sdma::BN - 1) / sdma::BN;
+  if (t0 <= 0 || t1 <= 0) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)std::max(t0, t1), (unsigned)(q.s0 + s1));
+  if (q.g[0].m_store <= 64 && t0 * q.s0 + t1 * s1 > 256)
+    hipLaunchKernelGGL((splitnn_dma_pair_kernel<64, 2>), grid, dim3(sdma::NT), 0, st, q);
+  else if (q.g[0].m_store <= 64)
+    hipLaunchKernelGGL((splitnn_dma_pair_kernel<64, 4>), grid, dim3(sdma::NT), 0, st, q);
+  else
+    hipLaunchKernelGGL((splitnn_dma_pair_kernel<128, 3>), grid, dim3(sdma::NT), 0, st, q);
+  return hipGetLastError();
+}
+
 using bf = uint16_t;
 
 }  // namespace
+
+bool gemm_pair_fits(GemmKind k, const GemmArgs& a, const GemmArgs& b) {
+  if (a.m_store != b.m_store || a.n_src || b.n_src) return false;
+  if (k == G_BF16_PANEL_SPLIT_NT) return a.n_store == b.n_store && panel_fits(a) && panel_fits(b);
+  return k == G_BF16_SPLIT_NN_PARTIAL && splitnn_fits(a) && splitnn_fits(b);
+}
+
+hipError_t launch_gemm_pair(GemmKind k, const GemmArgs& a, int sa, const GemmArgs& b, int sb, hipStream_t st) {
+  if (!gemm_pair_fits(k, a, b) || sa < 1 || sb < 1) return hipErrorInvalidValue;
+  const GemmPair q{{a, b}, sa};
+  return k == G_BF16_PANEL_SPLIT_NT ? run_panel_pair(q, sb, st) : run_splitnn_pair(q, sb, st);
+}
 
 bool whole_ld_fits(int64_t ld) { return ld * 2 * (w4::BM + w4::BK) < (int64_t)w4::BIG; }
 
@@ -1117,15 +1157,12 @@ constexpr int kMaxPanelSplits = 32;
 // t >> 4, the loads of up to 8 splits in flight before their sums), the
 // column scale, then the row-major and/or (through LDS) the transposed bf16
 // stores.
-__global__ void __launch_bounds__(256) panel_reduce_kernel(const float* __restrict__ part, int splits,
-                                                           int64_t part_stride, int64_t ldp, int64_t rows, int64_t n,
-                                                           ColScale scale, uint16_t* __restrict__ out, int64_t ldo,
-                                                           uint16_t* __restrict__ outt, int64_t ldot, int* __restrict__ zero,
-                                                           int nzero) {
+__device__ __forceinline__ void panel_reduce_tile(const float* __restrict__ part, int splits, int64_t part_stride,
+                                                  int64_t ldp, int64_t rows, int64_t n, const ColScale& scale,
+                                                  uint16_t* __restrict__ out, int64_t ldo, uint16_t* __restrict__ outt,
+                                                  int64_t ldot) {
   __shared__ float tile[16][65];
   const int tid = threadIdx.x;
-  if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int i = tid; i < nzero; i += 256) zero[i] = 0;
   const int64_t q0 = (int64_t)blockIdx.x * 16, c0 = (int64_t)blockIdx.y * 64;
   const int cl = 4 * (tid & 15), rl = tid >> 4;
   const int64_t c = c0 + cl, q = q0 + rl;
@@ -1161,6 +1198,41 @@ __global__ void __launch_bounds__(256) panel_reduce_kernel(const float* __restri
     const int64_t qg = q0 + qq, cg = c0 + cc;
     if (qg < rows && cg < n) outt[cg * ldot + qg] = f2bf(tile[qq][cc]);
   }
+}
+
+__device__ __forceinline__ void clear_ints(int* zero, int nzero) {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+    for (int i = threadIdx.x; i < nzero; i += 256) zero[i] = 0;
+}
+
+__global__ void __launch_bounds__(256) panel_reduce_kernel(const float* __restrict__ part, int splits,
+                                                           int64_t part_stride, int64_t ldp, int64_t rows, int64_t n,
+                                                           ColScale scale, uint16_t* __restrict__ out, int64_t ldo,
+                                                           uint16_t* __restrict__ outt, int64_t ldot, int* __restrict__ zero,
+                                                           int nzero) {
+  clear_ints(zero, nzero);
+  panel_reduce_tile(part, splits, part_stride, ldp, rows, n, scale, out, ldo, outt, ldot);
+}
+
+// Two panels of the same rows, columns and scale at once (blockIdx.z).
+__global__ void __launch_bounds__(256) panel_reduce_pair_kernel(PanelSum a, PanelSum b, int64_t rows, int64_t n,
+                                                                ColScale scale, int* __restrict__ zero, int nzero) {
+  clear_ints(zero, nzero);
+  const bool second = blockIdx.z != 0;
+  panel_reduce_tile(second ? b.part : a.part, second ? b.splits : a.splits, rows * n, n, rows, n, scale,
+                    second ? b.out : a.out, n, second ? b.outt : a.outt, rows);
+}
+
+hipError_t launch_panel_reduce_pair(const PanelSum& a, const PanelSum& b, int64_t rows, int64_t n,
+                                    const ColScale& scale, hipStream_t st, int* zero, int nzero) {
+  for (const PanelSum* p : {&a, &b})
+    if (!p->part || p->splits < 1 || p->splits > kMaxPanelSplits || reinterpret_cast<uintptr_t>(p->part) % 16 ||
+        reinterpret_cast<uintptr_t>(p->out) % 8)
+      return hipErrorInvalidValue;
+  if (rows < 1 || n < 1 || n % 4 || scale.n < 1 || scale.n > kColScaleMax) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)((rows + 15) / 16), (unsigned)((n + 63) / 64), 2);
+  hipLaunchKernelGGL(panel_reduce_pair_kernel, grid, dim3(256), 0, st, a, b, rows, n, scale, zero, nzero);
+  return hipGetLastError();
 }
 
 hipError_t launch_panel_reduce(const float* part, int splits, int64_t part_stride, int64_t ldp, int64_t rows,

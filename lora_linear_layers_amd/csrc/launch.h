@@ -74,6 +74,11 @@ TileShape gemm_tile(GemmKind k);
 
 // Sets a.tiles_m from a.m_store and launches over (tiles_m * tiles_n, 1, splits).
 hipError_t launch_gemm(GemmKind k, GemmArgs a, int splits, hipStream_t st);
+// Two G_BF16_PANEL_SPLIT_NT (of the same panel size) or two
+// G_BF16_SPLIT_NN_PARTIAL (of as many rows) with sa and sb splits in one
+// launch, bit for bit what each alone gives; where gemm_pair_fits.
+bool gemm_pair_fits(GemmKind k, const GemmArgs& a, const GemmArgs& b);
+hipError_t launch_gemm_pair(GemmKind k, const GemmArgs& a, int sa, const GemmArgs& b, int sb, hipStream_t st);
 
 // Bt[q, i] = q < r ? B[i, q] : 0, bf16 [rows, r] -> [r_pad, rows].
 hipError_t launch_transpose_pad(const uint16_t* src, uint16_t* dst, int64_t rows, int64_t r, int64_t r_pad,
@@ -156,6 +161,16 @@ inline ColScale col_scale(float s) {
 hipError_t launch_panel_reduce(const float* part, int splits, int64_t part_stride, int64_t ldp, int64_t rows,
                                int64_t n, const ColScale& scale, uint16_t* out, int64_t ldo, uint16_t* outt,
                                int64_t ldot, hipStream_t st, int* zero = nullptr, int nzero = 0);
+// The same of two panels of `rows` rows and n columns (row-major outputs n
+// wide, transposed ones `rows` wide).
+struct PanelSum {
+  const float* part;
+  int splits;
+  uint16_t* out;
+  uint16_t* outt;
+};
+hipError_t launch_panel_reduce_pair(const PanelSum& a, const PanelSum& b, int64_t rows, int64_t n,
+                                    const ColScale& scale, hipStream_t st, int* zero, int nzero);
 
 // out [M, N] bf16 (row stride ldo) = fixed-order sum of split partials
 // (part[z * part_stride + m * N + n]); with pos != NULL also the RoPE rotation
