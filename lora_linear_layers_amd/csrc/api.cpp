@@ -145,52 +145,65 @@ FewPlan few_plan(bool bwd, bool nf4, bool rope, int64_t M, int64_t d_in, int64_t
 // ---------------------------------------------------------------------------
 struct StreamPlan {
   bool ok = false;
+  bool low = false;  // 128 x 256 tiles, one each a block (gemm_w4_half.h)
   int full = 0, half = 0, early = 0;
 };
 
-// 256 x 256 tiles for an epilogue layer's Y or dX [M, N] over K where they are
-// ragged or no multiple of the 256 CUs, instead of the 128 x 128 (from 256
-// such tiles on, the register-staged 256 x 256) kernel.  Taken where measured
-// faster on MI355X, t tiles and nk 64-deep stages:
-//   t > 256: always (4100 x 4096 over 4096: 274 -> 189 us, 5000 x 4096: 276 ->
-//     194); its last t mod 256 tiles in two blocks each where 128 of them or
-//     fewer leave CUs free and a half is long enough to pay for the exchange
-//     of 256 KB a tile (4100 x 4096: 212 -> 189 us);
+// 128 x 256 tiles (gemm_w4_half.h) or ragged 256 x 256 ones (gemm_w4_stream.h)
+// for an epilogue layer's Y or dX [M, N] over K instead of the 128 x 128
+// kernel (from 256 tiles of 256 x 256 on, the register-staged one of those).
+// Taken where measured faster on MI355X, with t tiles of 256 x 256, `low` of
+// 128 x 256 and nk 64-deep stages (times of a forward pass, X's panel among them):
+//   low of 80 to 256, at most one a CU, 16 us and 0.6 (half the CUs at work) to
+//     0.81 us a stage: 2048 x 4096 outputs over 4096: 83 us, against 95 by two
+//     blocks for each of 128 tiles of 256 x 256 and 98 by 512 tiles of 128 x 128;
+//     over 2048: 51 against 65; 768 x 4096 over 4096: 63 against 84 by a split of
+//     the contraction; 300 x 14336: 64 against 85.  From 8 stages (5: 26.5 us
+//     against 26.9, 22.6 against 22.3) to 224, or 320 where t < 64, where two
+//     blocks a tile and the split of few tiles catch up (2048 x 4096 over 14336:
+//     220 against 220; 768 x 4096 over 14336: 166 against 211, 640 x 4096 over
+//     27392: 371 against 331);
+//   low of 48 to 79: 8 to 24 stages (512 x 4096 over 1024: 30 against 33 us, over
+//     2048 40 against 39; 32 tiles, 256 x 4096 over 1024: 30 against 30);
+//   t > 256: 256 x 256 tiles always (4100 x 4096 over 4096: 274 -> 189 us, 5000 x
+//     4096: 276 -> 194); the last t mod 256 of them in two blocks each where 128
+//     of them or fewer leave CUs free and a half is long enough to pay for the
+//     exchange of 256 KB a tile (4100 x 4096: 212 -> 189 us);
 //   128 < t <= 256 (256 whole tiles have their own kernel): the 128 x 128
 //     tiles need two rounds, 2.4 us a stage and 11 us; these one of 1.1 to 1.5
 //     us a stage and 19 us (2049 x 4104 over 4096: 182 -> 101 us);
-//   64 <= t <= 128: two blocks a tile, 0.66 us a stage and 37 us, against one
-//     round of 128 x 128 tiles, 1.22 us and 11 us: from 48 stages (2048 x 4096
-//     over 4096: 98 -> 91 us, over 14336: 308 -> 224; over 2048: 60 against 65);
-//   below 64 tiles the split 128 x 128 tiles are faster (512 x 4096: 54
-//     against 73 us).
+//   64 <= t <= 128, past 224 stages: two blocks a tile, 0.66 us a stage and 37 us.
 // transpose: W^T has to be made first, 0.37 us a MB of W (4096 x 4096: 13 us),
 // which the gain over the product through W itself (128 x 128 tiles, 1.4 us a
-// stage and round) has to carry: the backward of 2048 tokens, 4096 -> 4096, 149
-// -> 134 us, of 4100 tokens 318 -> 252; 512 tokens, 14336 -> 4096 would be 154 ->
-// 172.
+// stage and round, or split) has to carry: the backward of 2048 tokens, 4096 ->
+// 4096, 149 -> 113 us, of 4100 tokens 318 -> 252, of 768 tokens 120 -> 87.
 StreamPlan stream_plan(int64_t M, int64_t N, int64_t K, int64_t r, bool transpose) {
   StreamPlan S;
   const int64_t r8 = rup(r, 8), t = cdiv(M, 256) * cdiv(N, 256), nk = K / 64 + cdiv(r, 64);
+  const int64_t low = cdiv(M, 128) * cdiv(N, 256), t128 = cdiv(M, 128) * cdiv(N, 128);
   if (M < 1 || K % 64 || K < 64 || !whole_ld_fits(std::max({K, r8, N})) || t > INT32_MAX / 2) return S;
   if (M % 256 == 0 && N % 256 == 0 && t % 256 == 0) return S;  // the whole-tile kernel
-  const int64_t rest = t % 256;
   double gain;  // us over the product through W itself
-  if (t > 256) {
+  S.low = low <= 256 && nk >= 8 && (low >= 80 ? nk <= (t < 64 ? 320 : 224) || t > 128 : low >= 48 && nk <= 24);
+  const int64_t rest = t % 256;
+  if (S.low) {
+    gain = t128 >= 256 ? 0.59 * nk - 5 : low >= 80 ? 8 + 0.5 * nk : 4;
+  } else if (t > 256) {
     S.half = rest <= 128 && nk >= 24 ? (int)rest : 0;
     gain = 0.5 * nk * cdiv(t, 256);
   } else if (t > 128) {
     if (nk < 12) return S;
     gain = 1.5 * nk - 9;
   } else {
-    if (t < 64 || nk < 48 || cdiv(M, 128) * cdiv(N, 128) < 256) return S;
+    if (t < 64 || nk < 48 || t128 < 256) return S;
     S.half = (int)t;
     gain = 0.74 * nk - 26;
   }
   if (transpose && gain < 0.37e-6 * 2 * double(N) * double(K)) return StreamPlan();
+  S.ok = true;
+  if (S.low) return S;
   S.full = (int)(t - S.half);
   S.early = S.half ? 3 : 0;
-  S.ok = true;
   return S;
 }
 
@@ -487,7 +500,7 @@ const char* kind_name(int k) {
       "dropout_dx_f32_64x128",      "gemm_bf16_256x256_nt_group", "gemm_nf4_256x256_nt_whole",
       "gemm_bf16_256x256_nt_epi",   "gemm_bf16_128x128_nt_epi",   "gemm_nf4_256x256_nt_epi",
       "gemm_nf4_128x128_nt_epi",    "gemm_nf4_256x256_nt_whole_epi", "gemm_f32_64x128_nt_epi",
-      "gemm_bf16_256x256_nt_stream",
+      "gemm_bf16_128x256_nt_epi",   "gemm_bf16_256x256_nt_stream",
       "pad_cols",
       "rope_inverse",
       "reduce_splits",              "fill_zero",                  "rope_cache",
@@ -794,7 +807,7 @@ int forward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, f
   if (stream) {
     a.st_full = L.stream.full; a.st_half = L.stream.half; a.st_early = L.stream.early;
     a.st_part = reinterpret_cast<float*>(w + L.st_part); a.st_cnt = cnt;
-    HIPTRY(gemm(G_BF16_STREAM_EPI, a, 1, st, flop, bytes + xbytes));
+    HIPTRY(gemm(L.stream.low ? G_BF16_HALF_EPI : G_BF16_STREAM_EPI, a, 1, st, flop, bytes + xbytes));
     return LORA_OK;
   }
   if (!f32 && L.splits_main > 1) {
@@ -997,7 +1010,7 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
       a.st_full = L.stream.full; a.st_half = L.stream.half; a.st_early = L.stream.early;
       a.st_part = reinterpret_cast<float*>(w + L.st_part); a.st_cnt = reinterpret_cast<int*>(w + L.st_cnt);
     }
-    HIPTRY(gemm(L.stream.ok ? G_BF16_STREAM_EPI : G_BF16_BIG_NT_STORE, a, 1, st, 2 * Md * ki * (ko + rr),
+    HIPTRY(gemm(!L.stream.ok ? G_BF16_BIG_NT_STORE : L.stream.low ? G_BF16_HALF_EPI : G_BF16_STREAM_EPI, a, 1, st, 2 * Md * ki * (ko + rr),
                 (Md * ko + Md * rr + rr * ki + Md * ki + ko * ki) * e));
   } else if (dX) {
     GemmArgs a = blank();
@@ -1593,8 +1606,7 @@ EpiLayout make_epi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, const lo
       !(!m.W_nf4 && skinny_fits(M, d_in, m.d_out, m.r, sk::EPIL))) {
     E.L.stream = stream_plan(M, m.d_out, d_in, m.r, false);
   }
-  if (bwd && M > 0 && dtype == LORA_BF16 && !E.L.few.ok && !E.L.dx_nt && E.L.splits_main == 1 &&
-      (!m.W_nf4 || E.L.dequant)) {
+  if (bwd && M > 0 && dtype == LORA_BF16 && !E.L.few.ok && !E.L.dx_nt && (!m.W_nf4 || E.L.dequant)) {
     // dX on the same tiles, through W^T and A^T (an NF4 W is dequantised into
     // its transpose as cheaply as into itself)
     E.L.stream = stream_plan(M, d_in, m.d_out, m.r, !m.W_t && !m.W_nf4);

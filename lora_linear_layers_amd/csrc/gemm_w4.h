@@ -84,11 +84,13 @@ __device__ __forceinline__ void w4_load_part(const float* part, int i, int t, f3
                                               r, (j * 4 + q) * (w4::NT * 16) + t * 16, i * w4::FN * 4 * (w4::NT * 16), 16));
 }
 
-template <int EPI, bool RAGGED = false>
-__device__ __forceinline__ void w4_epilogue(const GemmArgs& p, f32x16 (&acc)[w4::FM][w4::FN], char* smem,
+template <int EPI, bool RAGGED = false, int FMT = w4::FM>
+__device__ __forceinline__ void w4_epilogue(const GemmArgs& p, f32x16 (&acc)[FMT][w4::FN], char* smem,
                                             int64_t m0, int64_t n0, void* c_out, int64_t ldc,
                                             const float* part = nullptr) {
   using namespace w4;
+  constexpr int TMT = 32 * FMT, BMT = 2 * TMT;  // rows of a wave's and of the block's tile
+  static_assert(FMT == FM || EPI == EPI_ACT, "lower tiles have the activation epilogue alone");
   auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
   int te = threadIdx.x;
   asm volatile("" : "+v"(te));
@@ -218,8 +220,8 @@ __device__ __forceinline__ void w4_epilogue(const GemmArgs& p, f32x16 (&acc)[w4:
     else
       emit(std::integral_constant<int, 2>{});
   } else if constexpr (EPI == EPI_ACT) {
-    // Four passes of one 32-row MFMA block of every wave (64 rows of the
-    // tile) through LDS: fp32 with a row pitch of 256 + 8 floats (rows q and
+    // FMT (4 or 2) passes of one 32-row MFMA block of every wave (64 rows of
+    // the tile) through LDS: fp32 with a row pitch of 256 + 8 floats (rows q and
     // q + 4, which a wave's halves write together, lie 32 banks apart), then
     // 8 columns of 8 rows a thread, so that residual and output move in
     // 16-byte accesses and the bias is loaded once.  The pass's residual is
@@ -235,7 +237,7 @@ __device__ __forceinline__ void w4_epilogue(const GemmArgs& p, f32x16 (&acc)[w4:
     // with its last existing row: what lies past it reads zeros and is not
     // stored, with no branch; a column past n_store takes an offset past every
     // resource.  (256 ldc elements stay below the resources' range.)
-    const int rows = RAGGED ? (int)min(p.m_store - m0, (int64_t)BM) : BM;
+    const int rows = RAGGED ? (int)min(p.m_store - m0, (int64_t)BMT) : BMT;
     const int len = (int)(((rows - 1) * ldc + (RAGGED ? min(p.n_store - n0, (int64_t)BN) : BN)) * 2);
     auto rsrc = [&](const void* q) {
       return __builtin_amdgcn_make_buffer_rsrc(
@@ -251,7 +253,8 @@ __device__ __forceinline__ void w4_epilogue(const GemmArgs& p, f32x16 (&acc)[w4:
     if (p.ep.bias && cok) epi_load(static_cast<const uint16_t*>(p.ep.bias) + col, b);
     const bool has_res = p.ep.res != nullptr, has_z = p.ep.z != nullptr;
     const int act = p.ep.act;
-    f32x4 s[FN][4];  // RAGGED: the pass's rows of the other part
+    constexpr bool PART = RAGGED && FMT == FM;
+    f32x4 s[FN][4];  // PART: the pass's rows of the other part
     auto stage = [&](auto i_c, auto add_c) {
       constexpr int i = decltype(i_c)::value;
       constexpr bool ADD = decltype(add_c)::value;
@@ -265,21 +268,29 @@ __device__ __forceinline__ void w4_epilogue(const GemmArgs& p, f32x16 (&acc)[w4:
         }
     };
     auto stage_of = [&](int i, auto add_c) {
-      switch (i) {
-        case 0: stage(std::integral_constant<int, 0>{}, add_c); break;
-        case 1: stage(std::integral_constant<int, 1>{}, add_c); break;
-        case 2: stage(std::integral_constant<int, 2>{}, add_c); break;
-        default: stage(std::integral_constant<int, 3>{}, add_c); break;
+      if constexpr (FMT == 2) {
+        if (i == 0)
+          stage(std::integral_constant<int, 0>{}, add_c);
+        else
+          stage(std::integral_constant<int, 1>{}, add_c);
+      } else {
+        switch (i) {
+          case 0: stage(std::integral_constant<int, 0>{}, add_c); break;
+          case 1: stage(std::integral_constant<int, 1>{}, add_c); break;
+          case 2: stage(std::integral_constant<int, 2>{}, add_c); break;
+          default: stage(std::integral_constant<int, 3>{}, add_c); break;
+        }
       }
     };
     // One copy of the pass's code for the four: unrolled (and with the
     // activations' variants in every row) it is 100 KB, which a block runs
     // through once, at the rate of its instruction fetches.
-    if (RAGGED && part) w4_load_part(part, 0, te, s);
+    if constexpr (PART)
+      if (part) w4_load_part(part, 0, te, s);
 #pragma unroll 1
-    for (int i = 0; i < FM; ++i) {
+    for (int i = 0; i < FMT; ++i) {
       // row r0 + 8 k of the pass is the tile's row r0 + at(k)
-      auto at = [&](int k) { return (uint32_t)((k >> 2) * TM + 32 * i + 8 * (k & 3)) * ldb; };
+      auto at = [&](int k) { return (uint32_t)((k >> 2) * TMT + 32 * i + 8 * (k & 3)) * ldb; };
       u32x4 rv[8];
       if (has_res) {
 #pragma unroll
@@ -287,12 +298,16 @@ __device__ __forceinline__ void w4_epilogue(const GemmArgs& p, f32x16 (&acc)[w4:
           rv[k] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rr, (int)(vo + at(k)), 0, 0));
       }
       lds_barrier();
-      if (!RAGGED || !part)
+      if constexpr (PART) {
+        if (part)
+          stage_of(i, std::true_type{});
+        else
+          stage_of(i, std::false_type{});
+        // the next pass's part flies while this one's rows are finished
+        if (part && i + 1 < FMT) w4_load_part(part, i + 1, te, s);
+      } else {
         stage_of(i, std::false_type{});
-      else
-        stage_of(i, std::true_type{});
-      // the next pass's part flies while this one's rows are finished
-      if (RAGGED && part && i + 1 < FM) w4_load_part(part, i + 1, te, s);
+      }
       lds_barrier();
       float y[64];
 #pragma unroll

@@ -10,8 +10,8 @@
 //
 // Work split: the first st_full tiles are a block each; each of the st_half
 // tiles after them is two blocks, the first and the second part of its
-// contraction, so that 65 to 128 tiles fill 256 CUs (2048 x 4096 outputs are
-// 128).  A part's block leaves its accumulators in its slot, in the registers'
+// contraction, so that 64 to 128 tiles fill 256 CUs (2048 x 4096 outputs are
+// 128; up to 224 stages gemm_w4_half.h takes those).  A part's block leaves its accumulators in its slot, in the registers'
 // order, and counts itself in; the one that comes second adds the other's slot
 // as it stages the rows of its epilogue (a sum of two does not depend on their
 // order) and stores.  Nobody waits for anybody.  The first part is `st_early`
@@ -30,7 +30,8 @@
 // over 14336: 197 us.  What bounds it: the CUs without a tile, then the fixed
 // part; contiguous ranges that span tiles (three slots of 256 KB to read back
 // for some) and no stagger between the parts measured slower (137 and 85 us
-// against 86 and 76).
+// against 86 and 76); tiles in bands by XCD gained nothing (2049 x 4104 over 4096:
+// 109 us a pass against 108).
 #pragma once
 
 #include "gemm_w4_nt.h"

@@ -11,6 +11,7 @@
 #include "gemm_w4.h"
 #include "gemm_w4_nt.h"
 #include "gemm_w4_nf4.h"
+#include "gemm_w4_half.h"
 #include "gemm_w4_stream.h"
 #include "gemm_panel.h"
 #include "skinny.h"
@@ -189,6 +190,8 @@ TileShape gemm_tile(GemmKind k) {
       return {256, 256};
     case G_BF16_STREAM_EPI:
       return {256, 256};
+    case G_BF16_HALF_EPI:
+      return {128, 256};
     case G_BF16_MED_NT_EPI:
     case G_NF4_MED_NT_EPI:
       return {128, 128};
@@ -269,6 +272,18 @@ hipError_t launch_gemm(GemmKind k, GemmArgs a, int splits, hipStream_t st) {
       a.tiles_m = (int)tm;
       hipLaunchKernelGGL((gemm_w4_stream_kernel<EPI_ACT>), dim3((unsigned)(a.st_full + 2 * a.st_half)), dim3(w4::NT), 0,
                          st, a);
+      return hipGetLastError();
+    }
+    case G_BF16_HALF_EPI: {
+      // whole stages of the first segment, lane offsets below the resource range
+      const int64_t ld = std::max(std::max(a.lda1, a.lda2), std::max(a.ldb1, a.ldb2));
+      const int64_t tm = (a.m_store + w4h::BM - 1) / w4h::BM, tn = (a.n_store + w4::BN - 1) / w4::BN;
+      if (splits != 1 || a.m_load != a.m_store || a.n_load != a.n_store || a.n_store % 8 || a.K1 < w4::BK ||
+          a.K1 % w4::BK || !whole_ld_fits(std::max(ld, a.ldc)) || tm * tn > INT32_MAX)
+        return hipErrorInvalidValue;
+      if (tm * tn == 0) return hipSuccess;
+      a.tiles_m = (int)tm;
+      hipLaunchKernelGGL((gemm_w4_half_kernel<EPI_ACT>), dim3((unsigned)(tm * tn)), dim3(w4::NT), 0, st, a);
       return hipGetLastError();
     }
     case G_BF16_MED_NT_EPI: return run<bf, 128, 128, 4, 1, false, EPI_ACT, BL_PLAIN>(a, splits, st);

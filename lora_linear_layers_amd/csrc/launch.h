@@ -63,6 +63,7 @@ enum GemmKind : int {
   G_NF4_MED_NT_EPI,
   G_NF4_WHOLE_NT_EPI,
   G_F32_NT_EPI,
+  G_BF16_HALF_EPI,    // 128 x 256 tiles, up to one a CU (gemm_w4_half_kernel)
   G_BF16_STREAM_EPI,  // 256 x 256 tiles, ragged and split over the CUs (gemm_w4_stream_kernel)
   G_KIND_COUNT
 };

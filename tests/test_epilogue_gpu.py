@@ -155,9 +155,15 @@ BF16 = [
     (300, 264, 392, 16, "gemm_bf16_128x128_nt_epi"), (2049, 264, 4104, 12, "gemm_bf16_128x128_nt_epi"),
     # 256 x 256 tiles, ragged or no multiple of the CUs: a block each; two blocks each; whole rounds and two blocks
     # for each of the rest; the ragged tile alone in its column
-    (2049, 1024, 4104, 100, "gemm_bf16_256x256_nt_stream"), (2048, 3136, 2056, 16, "gemm_bf16_256x256_nt_stream"),
+    (2049, 1024, 4104, 100, "gemm_bf16_256x256_nt_stream"), (2048, 14336, 2056, 100, "gemm_bf16_256x256_nt_stream"),
     (4100, 1600, 4104, 8, "gemm_bf16_256x256_nt_stream"), (4353, 64, 4104, 1, "gemm_bf16_256x256_nt_stream"),
-    (2048, 3200, 2048, 24, "gemm_bf16_256x256_nt_stream"),
+    (2048, 14400, 2048, 24, "gemm_bf16_256x256_nt_stream"),
+    # 128 x 256 tiles: whole, ragged in either direction, one row or one group of columns in the last, ranks of two
+    # stages, the fewest stages
+    (2048, 3200, 2048, 24, "gemm_bf16_128x256_nt_epi"), (2048, 3136, 2056, 16, "gemm_bf16_128x256_nt_epi"),
+    (1153, 512, 4096, 3, "gemm_bf16_128x256_nt_epi"), (700, 1024, 4360, 100, "gemm_bf16_128x256_nt_epi"),
+    (257, 448, 21512, 8, "gemm_bf16_128x256_nt_epi"), (384, 512, 4088, 256, "gemm_bf16_128x256_nt_epi"),
+    (2047, 448, 4096, 1, "gemm_bf16_128x256_nt_epi"),
     (4090, 136, 4104, 12, "gemm_bf16_256x256_nt_epi"), (4096, 320, 4096, 72, "gemm_bf16_256x256_nt_epi"),
 ]
 F32 = [
@@ -263,7 +269,7 @@ def test_epilogue_activation_of_huge_values(lib, dtype):
 @pytest.mark.gpu
 def test_epilogue_exact_on_integers(lib):
     # small integers: every product, sum, relu and residual is exact, on every kind of tile
-    for M, k, d, r in ((4096, 64, 4096, 8), (2050, 1024, 4104, 8), (2048, 3200, 2056, 8), (1, 128, 8192, 32), (300, 264, 392, 16), (40, 512, 768, 5), (9, 64, 64, 8)):
+    for M, k, d, r in ((4096, 64, 4096, 8), (2050, 1024, 4104, 8), (2048, 3200, 2056, 8), (4100, 1600, 4104, 8), (1, 128, 8192, 32), (300, 264, 392, 16), (40, 512, 768, 5), (9, 64, 64, 8)):
         X, W, A, B, R = int_inputs(5 + M, M, k, d, r, "bf16")
         X = X * (torch.rand(M, k, generator=torch.Generator().manual_seed(M)) < 0.2).cuda()  # |Z| stays below 2^8
         A = A * (torch.arange(k, device="cuda") % 32 == 0)
@@ -277,7 +283,7 @@ def test_epilogue_exact_on_integers(lib):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("case", [c for c in BF16 if c[0] in (1, 5, 40, 300, 2048, 2049, 4090, 4096, 4100)], ids=_id)
+@pytest.mark.parametrize("case", [c for c in BF16 if c[0] in (1, 5, 40, 300, 700, 1153, 2048, 2049, 4090, 4096, 4100)], ids=_id)
 def test_epilogue_residual_in_place_and_rows_behind(lib, case):
     M, k, d, r, _ = case
     X, m, bias, res, _ = _inputs(31, M, k, d, r, "bf16")
@@ -354,14 +360,17 @@ def test_epilogue_no_tokens(lib):
 
 
 # dX on the tiles of the forward above: through the caller's W^T, through one made on the way, through an NF4 W
-DX = [(2048, 2056, 3136, 16, True), (2048, 2056, 3200, 16, False), (4100, 4104, 1600, 8, False), (4100, 4104, 1600, 8, True),
-      (2049, 4104, 2112, 24, False), (2304, 4096, 2112, 64, None)]
+BIG, LOW = "gemm_bf16_256x256_nt_stream", "gemm_bf16_128x256_nt_epi"
+DX = [(2048, 2056, 14400, 16, True, BIG), (4100, 4104, 1600, 8, False, BIG), (4100, 4104, 1600, 8, True, BIG),
+      (2049, 4104, 2112, 24, False, BIG), (2304, 4096, 2112, 64, None, BIG),
+      (2048, 2056, 3136, 16, True, LOW), (2048, 2056, 3200, 16, False, LOW), (700, 4360, 1024, 100, False, LOW),
+      (1153, 4096, 448, 3, True, LOW), (640, 4096, 512, 8, None, LOW), (384, 4088, 1024, 24, True, LOW)]
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("case", DX, ids=lambda c: "%dx%dx%dr%d-%s" % c)
+@pytest.mark.parametrize("case", DX, ids=lambda c: "%dx%dx%dr%d-%s" % c[:5])
 def test_epilogue_input_gradient_tiles(lib, case):
-    M, k, d, r, kept = case
+    M, k, d, r, kept, kind = case
     table = None
     if kept is None:
         X, m, _, _, dY, table = _nf4(40 + M, k, d, r, M)
@@ -371,7 +380,7 @@ def test_epilogue_input_gradient_tiles(lib, case):
             m["W_t"] = lib.lora_transpose(m["W"])
     Z = torch.randn(M, d, generator=torch.Generator().manual_seed(5)).bfloat16().cuda()
     kinds = _kinds(lambda: lib.lora_linear_epi_bwd(X, m, dY, "silu", Z, table16=table))
-    assert "gemm_bf16_256x256_nt_stream" in kinds, kinds
+    assert kind in kinds, kinds
     check_bwd(lib, X, m, dY, "silu", Z, table)
 
 
@@ -489,9 +498,10 @@ def test_block_head_and_policy_loss(lib):
 
 
 @pytest.mark.gpu
-def test_epilogue_two_calls_at_once(lib):
+@pytest.mark.parametrize("k", [3200, 14400])
+def test_epilogue_two_calls_at_once(lib, k):
     # the same layer twice on two streams, each call with its own workspace (slots and counters of the split tiles)
-    X, m, bias, res, dY = _inputs(12, 2048, 3200, 2048, 24, "bf16")
+    X, m, bias, res, dY = _inputs(12, 2048, k, 2048, 24, "bf16")
     m["W_t"] = lib.lora_transpose(m["W"])
 
     def step():
