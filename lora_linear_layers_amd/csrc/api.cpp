@@ -173,16 +173,19 @@ struct StreamPlan {
 //     tiles need two rounds, 2.4 us a stage and 11 us; these one of 1.1 to 1.5
 //     us a stage and 19 us (2049 x 4104 over 4096: 182 -> 101 us);
 //   64 <= t <= 128, past 224 stages: two blocks a tile, 0.66 us a stage and 37 us.
+// A contraction of no whole number of stages gains more, the 128 x 128 kernel
+// checking every piece it loads: 4716 x 912 over 4056 151 -> 84 us, 2049 x 4096
+// over 4104 190 -> 116, 4090 x 4104 over 520 86 -> 70.
 // transpose: W^T has to be made first, 0.37 us a MB of W (4096 x 4096: 13 us),
 // which the gain over the product through W itself (128 x 128 tiles, 1.4 us a
 // stage and round, or split) has to carry: the backward of 2048 tokens, 4096 ->
 // 4096, 149 -> 113 us, of 4100 tokens 318 -> 252, of 768 tokens 120 -> 87.
 StreamPlan stream_plan(int64_t M, int64_t N, int64_t K, int64_t r, bool transpose) {
   StreamPlan S;
-  const int64_t r8 = rup(r, 8), t = cdiv(M, 256) * cdiv(N, 256), nk = K / 64 + cdiv(r, 64);
+  const int64_t r8 = rup(r, 8), t = cdiv(M, 256) * cdiv(N, 256), nk = cdiv(K, 64) + cdiv(r, 64);
   const int64_t low = cdiv(M, 128) * cdiv(N, 256), t128 = cdiv(M, 128) * cdiv(N, 128);
-  if (M < 1 || K % 64 || K < 64 || !whole_ld_fits(std::max({K, r8, N})) || t > INT32_MAX / 2) return S;
-  if (M % 256 == 0 && N % 256 == 0 && t % 256 == 0) return S;  // the whole-tile kernel
+  if (M < 1 || K < 64 || !whole_ld_fits(std::max({K, r8, N})) || t > INT32_MAX / 2) return S;
+  if (M % 256 == 0 && N % 256 == 0 && t % 256 == 0 && K % 64 == 0) return S;  // the whole-tile kernel
   double gain;  // us over the product through W itself
   S.low = low <= 256 && nk >= 8 && (low >= 80 ? nk <= (t < 64 ? 320 : 224) || t > 128 : low >= 48 && nk <= 24);
   const int64_t rest = t % 256;

@@ -18,7 +18,8 @@
 // of stage t-1.
 //
 // Ragged edges: a tile's rows past M (or N) are cut off by the buffer
-// resource's length, so they read zeros, and are not stored.
+// resource's length, so they read zeros, and are not stored; a last stage of
+// fewer than 64 columns takes offsets past the resource for the others.
 //
 // Why this tile.  2048 x 4096 outputs are 256 of them and 128 of 256 x 256,
 // which leave half of the CUs idle or have to be cut along the contraction.
@@ -73,8 +74,9 @@ gemm_w4_half_kernel(const GemmArgs p) {
   // keep the MFMA accumulators in the accumulation registers
   asm volatile("" ::: "a0");
 
-  const int n1 = (int)(p.K1 / BKS);  // stages of the main segment
-  const int n = n1 + (int)((p.K2 + BKS - 1) / BKS);
+  const int n1 = (int)(p.K1 / BKS), kt = (int)(p.K1 % BKS);  // whole stages of the main segment, columns of a last one
+  const int n1t = n1 + (kt ? 1 : 0);
+  const int n = n1t + (int)((p.K2 + BKS - 1) / BKS);
 
   auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
   using I0 = std::integral_constant<int, 0>;
@@ -148,14 +150,21 @@ gemm_w4_half_kernel(const GemmArgs p) {
       vo = op == 0 ? va1[odd] : vb1[odd];
       is = op == 0 ? isa1 : isb1;
     } else {
-      const int tt = u - n1;
+      const int tt = u - n1t;
       const int dc = odd ? dco : dce;
-      const int kk = tt * BKS + 8 * dc;  // the lane's first rank column
-      const uint32_t kc = (uint32_t)(tt * BKS * 2 + dc * 16);
-      base = op == 0 ? ga2 : gb2;
-      len = op == 0 ? la2 : lb2;
-      vo = kk < k2 ? (op == 0 ? ra2 + (odd ? oda2 : 0u) : rb2 + (odd ? odb2 : 0u)) + kc : w4::OOB;
-      is = op == 0 ? isa2 : isb2;
+      if (tt < 0) {  // the main segment's last columns
+        base = (op == 0 ? ga1 : gb1) + (int64_t)u * (BKS * 2);
+        len = (op == 0 ? la1 : lb1) - u * (BKS * 2);
+        vo = 8 * dc < kt ? (op == 0 ? va1[odd] : vb1[odd]) : w4::OOB;
+        is = op == 0 ? isa1 : isb1;
+      } else {
+        const int kk = tt * BKS + 8 * dc;  // the lane's first rank column
+        const uint32_t kc = (uint32_t)(tt * BKS * 2 + dc * 16);
+        base = op == 0 ? ga2 : gb2;
+        len = op == 0 ? la2 : lb2;
+        vo = kk < k2 ? (op == 0 ? ra2 + (odd ? oda2 : 0u) : rb2 + (odd ? odb2 : 0u)) + kc : w4::OOB;
+        is = op == 0 ? isa2 : isb2;
+      }
     }
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, len, 0x00020000);
@@ -173,14 +182,12 @@ gemm_w4_half_kernel(const GemmArgs p) {
   // prologue: stages 0 and 1 in flight; wait for stage 0
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    if (u < n) {
+    if (u < n1) {
 #pragma unroll
-      for (int i = 0; i < 12; ++i) {
-        if (u < n1)
-          dma(u, u, i < 4 ? 0 : 1, i < 4 ? i : i - 4, F_{});
-        else
-          dma(u, u, i < 4 ? 0 : 1, i < 4 ? i : i - 4, T_{});
-      }
+      for (int i = 0; i < 12; ++i) dma(u, u, i < 4 ? 0 : 1, i < 4 ? i : i - 4, F_{});
+    } else if (u < n) {
+#pragma unroll
+      for (int i = 0; i < 12; ++i) dma(u, u, i < 4 ? 0 : 1, i < 4 ? i : i - 4, T_{});
     }
   }
   if (n >= 2)
@@ -191,8 +198,8 @@ gemm_w4_half_kernel(const GemmArgs p) {
 #pragma unroll
   for (int k = 0; k < 6; ++k) rd1(0, 0, I0{}, k);
 
-  // One stage.  ISSUE: 0 none, 1 stage t+2 of the main segment, 2 of the rank
-  // segment.  NEXT: stage t+1 exists.
+  // One stage.  ISSUE: 0 none, 1 a whole stage t+2 of the main segment, 2 its
+  // ragged last one or one of the rank segment.  NEXT: stage t+1 exists.
   auto stage = [&](int t, auto issue_c, auto next_c) {
     constexpr int ISSUE = decltype(issue_c)::value;
     constexpr bool NEXT = decltype(next_c)::value;

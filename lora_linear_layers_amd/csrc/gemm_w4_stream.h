@@ -6,17 +6,19 @@
 //     C = act(A1 B1^T + A2 B2^T + bias) + residual
 //
 // Ragged edges: a tile's rows past M (or N) are cut off by the buffer
-// resource's length, so they read zeros, and are not stored.
+// resource's length, so they read zeros, and are not stored; a last stage of
+// fewer than 64 columns takes offsets past the resource for the others.
 //
 // Work split: the first st_full tiles are a block each; each of the st_half
 // tiles after them is two blocks, the first and the second part of its
 // contraction, so that 64 to 128 tiles fill 256 CUs (2048 x 4096 outputs are
-// 128; up to 224 stages gemm_w4_half.h takes those).  A part's block leaves its accumulators in its slot, in the registers'
-// order, and counts itself in; the one that comes second adds the other's slot
-// as it stages the rows of its epilogue (a sum of two does not depend on their
-// order) and stores.  Nobody waits for anybody.  The first part is `st_early`
-// stages short of half and the second as much longer, so that the first's
-// slot is usually there when the second ends, which then writes none.
+// 128; up to 224 stages gemm_w4_half.h takes those).  A part's block leaves
+// its accumulators in its slot, in the registers' order, and counts itself in;
+// the one that comes second adds the other's slot as it stages the rows of its
+// epilogue (a sum of two does not depend on their order) and stores.  Nobody
+// waits for anybody.  The first part is `st_early` stages short of half and the
+// second as much longer, so that the first's slot is usually there when the
+// second ends, which then writes none.
 //
 // Slots, counters: fp32 [2 st_half][256 * 256] and int [st_half], zero before
 // the launch.  They cross XCDs, so they are written and read at the device's
@@ -52,8 +54,9 @@ gemm_w4_stream_kernel(const GemmArgs p) {
   // keep the MFMA accumulators in the accumulation registers
   asm volatile("" ::: "a0");
 
-  const int nk1 = (int)(p.K1 / BKS);
-  const int nk = nk1 + (int)((p.K2 + BKS - 1) / BKS);
+  const int nk1 = (int)(p.K1 / BKS), kt = (int)(p.K1 % BKS);  // whole stages of the main segment, columns of a last one
+  const int nk1t = nk1 + (kt ? 1 : 0);
+  const int nk = nk1t + (int)((p.K2 + BKS - 1) / BKS);
 
   // the block's tile and its stages [s0, s0 + n) of it
   const int bid = blockIdx.x, hb = bid - p.st_full;
@@ -134,14 +137,21 @@ gemm_w4_stream_kernel(const GemmArgs p) {
       vo = op == 0 ? va1[odd] : vb1[odd];
       is = op == 0 ? isa1 : isb1;
     } else {
-      const int tt = s0 + u - nk1;
+      const int tt = s0 + u - nk1t;
       const int dc = odd ? dco : dce;
-      const int kk = tt * BKS + 8 * dc;  // the lane's first rank column
-      const uint32_t kc = (uint32_t)(tt * BKS * 2 + dc * 16);
-      base = op == 0 ? ga2 : gb2;
-      len = op == 0 ? la2 : lb2;
-      vo = kk < k2 ? (op == 0 ? ra2 + (odd ? oda2 : 0u) : rb2 + (odd ? odb2 : 0u)) + kc : w4::OOB;
-      is = op == 0 ? isa2 : isb2;
+      if (tt < 0) {  // the main segment's last columns
+        base = (op == 0 ? ga1 : gb1) + (int64_t)u * (BKS * 2);
+        len = (op == 0 ? la1 : lb1) - u * (BKS * 2);
+        vo = 8 * dc < kt ? (op == 0 ? va1[odd] : vb1[odd]) : w4::OOB;
+        is = op == 0 ? isa1 : isb1;
+      } else {
+        const int kk = tt * BKS + 8 * dc;  // the lane's first rank column
+        const uint32_t kc = (uint32_t)(tt * BKS * 2 + dc * 16);
+        base = op == 0 ? ga2 : gb2;
+        len = op == 0 ? la2 : lb2;
+        vo = kk < k2 ? (op == 0 ? ra2 + (odd ? oda2 : 0u) : rb2 + (odd ? odb2 : 0u)) + kc : w4::OOB;
+        is = op == 0 ? isa2 : isb2;
+      }
     }
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, len, 0x00020000);
@@ -159,16 +169,12 @@ gemm_w4_stream_kernel(const GemmArgs p) {
   // prologue: stages 0 and 1 in flight (slots 0 .. 3); wait for stage 0
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    if (u < n) {
+    if (u < n1) {
 #pragma unroll
-      for (int op = 0; op < 2; ++op)
+      for (int i = 0; i < 16; ++i) dma(u, 2 * u + (i >> 3), i >> 3, i & 7, F_{});
+    } else if (u < n) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (u < n1)
-            dma(u, 2 * u + op, op, i, F_{});
-          else
-            dma(u, 2 * u + op, op, i, T_{});
-        }
+      for (int i = 0; i < 16; ++i) dma(u, 2 * u + (i >> 3), i >> 3, i & 7, T_{});
     }
   }
   if (n >= 2)
@@ -179,8 +185,8 @@ gemm_w4_stream_kernel(const GemmArgs p) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) rd1(0, 1, 0, I0{}, k);
 
-  // One stage, as in gemm_w4_nt_kernel.  ISSUE: 0 none, 1 stage t+2 of the
-  // main segment, 2 of the rank segment.  NEXT: stage t+1 exists.
+  // One stage, as in gemm_w4_nt_kernel.  ISSUE: 0 none, 1 a whole stage t+2 of
+  // the main segment, 2 its ragged last one or one of the rank segment.  NEXT: stage t+1 exists.
   auto stage = [&](int t, auto issue_c, auto next_c) {
     constexpr int ISSUE = decltype(issue_c)::value;
     constexpr bool NEXT = decltype(next_c)::value;

@@ -259,12 +259,12 @@ hipError_t launch_gemm(GemmKind k, GemmArgs a, int splits, hipStream_t st) {
       if (whole_tiles(a, splits) && whole_ld_fits(a.ldc)) return run_whole<false, EPI_ACT>(a, st);
       return run<bf, 256, 256, 2, 4, false, EPI_ACT, BL_PLAIN>(a, splits, st);
     case G_BF16_STREAM_EPI: {
-      // whole stages of the first segment, lane offsets below the resource
-      // range; every tile in a block of its own or in two, of two stages at least
+      // a whole stage of the first segment at least, lane offsets below the
+      // resource range; every tile in a block of its own or in two, of two stages at least
       const int64_t ld = std::max(std::max(a.lda1, a.lda2), std::max(a.ldb1, a.ldb2));
       const int64_t tm = (a.m_store + w4::BM - 1) / w4::BM, tn = (a.n_store + w4::BN - 1) / w4::BN;
       if (splits != 1 || a.m_load != a.m_store || a.n_load != a.n_store || a.n_store % 8 || a.K1 < w4::BK ||
-          a.K1 % w4::BK || !whole_ld_fits(std::max(ld, a.ldc)) || a.st_full < 0 || a.st_half < 0 ||
+          a.K1 % 8 || !whole_ld_fits(std::max(ld, a.ldc)) || a.st_full < 0 || a.st_half < 0 ||
           a.st_full + (int64_t)a.st_half != tm * tn || a.st_full + 2 * (int64_t)a.st_half > INT32_MAX ||
           (a.st_half > 0 && (!a.st_part || !a.st_cnt || a.st_early < 0 || a.K1 / w4::BK / 2 - a.st_early < 2)))
         return hipErrorInvalidValue;
@@ -275,11 +275,11 @@ hipError_t launch_gemm(GemmKind k, GemmArgs a, int splits, hipStream_t st) {
       return hipGetLastError();
     }
     case G_BF16_HALF_EPI: {
-      // whole stages of the first segment, lane offsets below the resource range
+      // a whole stage of the first segment at least, lane offsets below the resource range
       const int64_t ld = std::max(std::max(a.lda1, a.lda2), std::max(a.ldb1, a.ldb2));
       const int64_t tm = (a.m_store + w4h::BM - 1) / w4h::BM, tn = (a.n_store + w4::BN - 1) / w4::BN;
       if (splits != 1 || a.m_load != a.m_store || a.n_load != a.n_store || a.n_store % 8 || a.K1 < w4::BK ||
-          a.K1 % w4::BK || !whole_ld_fits(std::max(ld, a.ldc)) || tm * tn > INT32_MAX)
+          a.K1 % 8 || !whole_ld_fits(std::max(ld, a.ldc)) || tm * tn > INT32_MAX)
         return hipErrorInvalidValue;
       if (tm * tn == 0) return hipSuccess;
       a.tiles_m = (int)tm;

@@ -164,7 +164,11 @@ BF16 = [
     (1153, 512, 4096, 3, "gemm_bf16_128x256_nt_epi"), (700, 1024, 4360, 100, "gemm_bf16_128x256_nt_epi"),
     (257, 448, 21512, 8, "gemm_bf16_128x256_nt_epi"), (384, 512, 4088, 256, "gemm_bf16_128x256_nt_epi"),
     (2047, 448, 4096, 1, "gemm_bf16_128x256_nt_epi"),
-    (4090, 136, 4104, 12, "gemm_bf16_256x256_nt_epi"), (4096, 320, 4096, 72, "gemm_bf16_256x256_nt_epi"),
+    # a last stage of 8, 56, 24 columns
+    (700, 1032, 4360, 100, "gemm_bf16_128x256_nt_epi"), (2047, 504, 4096, 1, "gemm_bf16_128x256_nt_epi"),
+    (2049, 1080, 4104, 100, "gemm_bf16_256x256_nt_stream"), (4100, 1592, 4104, 8, "gemm_bf16_256x256_nt_stream"),
+    (4096, 72, 4104, 256, "gemm_bf16_256x256_nt_stream"), (2048, 14344, 2056, 100, "gemm_bf16_256x256_nt_stream"),
+    (4090, 136, 4096, 12, "gemm_bf16_256x256_nt_epi"), (4096, 320, 4096, 72, "gemm_bf16_256x256_nt_epi"),
 ]
 F32 = [
     (1, 8, 8, 1, "tiny_f32"), (128, 256, 256, 8, "tiny_f32"), (33, 72, 40, 3, "tiny_f32"),
@@ -309,7 +313,7 @@ def test_epilogue_plain_layer_bit_for_bit(lib):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("k", [64, 72])  # 256 x 256 tiles past whole stages, the 256 x 256 general form
+@pytest.mark.parametrize("k", [64, 72])  # 256 x 256 tiles of whole stages, with a ragged one
 def test_epilogue_offsets_past_32_bits(lib, k):
     # 2^31 elements of Y, Z, the residual, dY and dZ and more, in small integers: every sum is exact whatever its
     # order, so the rows at both ends are those of the same rows alone
@@ -364,7 +368,8 @@ BIG, LOW = "gemm_bf16_256x256_nt_stream", "gemm_bf16_128x256_nt_epi"
 DX = [(2048, 2056, 14400, 16, True, BIG), (4100, 4104, 1600, 8, False, BIG), (4100, 4104, 1600, 8, True, BIG),
       (2049, 4104, 2112, 24, False, BIG), (2304, 4096, 2112, 64, None, BIG),
       (2048, 2056, 3136, 16, True, LOW), (2048, 2056, 3200, 16, False, LOW), (700, 4360, 1024, 100, False, LOW),
-      (1153, 4096, 448, 3, True, LOW), (640, 4096, 512, 8, None, LOW), (384, 4088, 1024, 24, True, LOW)]
+      (1153, 4096, 448, 3, True, LOW), (640, 4096, 512, 8, None, LOW), (384, 4088, 1024, 24, True, LOW),
+      (2049, 4096, 4104, 24, False, BIG), (700, 4096, 1032, 16, False, LOW)]
 
 
 @pytest.mark.gpu
