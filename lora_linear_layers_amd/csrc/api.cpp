@@ -235,6 +235,11 @@ struct Layout {
   size_t st_part = 0, st_cnt = 0;
   bool pair = false;  // epilogue layer's backward: both panels, then dB and dA, in a launch each
   size_t ppart2 = 0;  // the second panel's partials
+  // epilogue layer, fp32: splits of the contraction of Y or dX (y), X A^T (p) and
+  // dZ B (q), 1 = none, and their partials (one after the other)
+  int fs_y = 1, fs_p = 1, fs_q = 1;
+  int64_t fk_y = 0, fk_p = 0, fk_q = 0;
+  size_t fpart = 0;
 };
 
 // 256x256 tiles when they still give at least one tile per CU, else 128x128.
@@ -504,6 +509,8 @@ const char* kind_name(int k) {
       "gemm_bf16_256x256_nt_epi",   "gemm_bf16_128x128_nt_epi",   "gemm_nf4_256x256_nt_epi",
       "gemm_nf4_128x128_nt_epi",    "gemm_nf4_256x256_nt_whole_epi", "gemm_f32_64x128_nt_epi",
       "gemm_bf16_128x256_nt_epi",   "gemm_bf16_256x256_nt_stream",
+      "gemm_f32_64x128_nt_split",   "gemm_f32_64x128_nn_split",   "panel_f32_nt_split",
+      "panel_f32_nn_split",
       "pad_cols",
       "rope_inverse",
       "reduce_splits",              "fill_zero",                  "rope_cache",
@@ -599,6 +606,18 @@ int panel_bf16(const void* X, int64_t ldx, const void* R, int64_t ldr, int64_t M
               (Md * kd + rd * kd) * 2 + 4.0 * splits * rows * r8));
   HIPTRY(timed(K_PANEL, double(splits) * rows * r8, 4.0 * splits * rows * r8 + 2.0 * rows * r8 * ((out ? 1 : 0) + (outt ? 1 : 0)),
                st, [&] { return launch_panel_reduce(part, splits, rows * r8, r8, rows, r8, cs, out, ldo, outt, ldot, st, zero, nzero); }));
+  return LORA_OK;
+}
+
+// out [m_store, n_store] and / or outt, its transpose, = scale * the product of
+// `a`, its contraction split into partials.
+int panel_f32_split(GemmKind k, GemmArgs a, int splits, int64_t ksplit, float scale, float* part, float* out, float* outt,
+                    hipStream_t st) {
+  a.k_split = ksplit; a.c = part; a.ldc = a.n_store; a.part_stride = a.m_store * a.n_store; a.alpha = 1.f;
+  const double el = double(a.m_store) * a.n_store, K = double(a.K1);
+  HIPTRY(gemm(k, a, splits, st, 2 * el * K, 4 * ((double(a.m_load) + a.n_load) * K + splits * el)));
+  HIPTRY(timed(K_PANEL, splits * el, 4.0 * (splits + (out ? 1 : 0) + (outt ? 1 : 0)) * el, st,
+               [&] { return launch_panel_sum_f32(part, splits, a.m_store, a.n_store, scale, out, outt, st); }));
   return LORA_OK;
 }
 
@@ -767,8 +786,13 @@ int forward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, f
     GemmArgs a = blank();
     a.a1 = Xp; a.lda1 = d_in; a.b1 = A; a.ldb1 = d_in; a.K1 = d_in;
     a.m_load = M; a.m_store = M; a.n_load = r; a.n_store = L.r8;
-    a.c = w + L.p; a.ldc = L.r8; a.alpha = scale;
-    HIPTRY(gemm(G_F32_PANEL_NT_STORE, a, 1, st, 2 * Md * rr * ki, (Md * ki + rr * ki + Md * L.r8) * e));
+    if (L.fs_p > 1) {
+      TRY(panel_f32_split(G_F32_PANEL_NT_PARTIAL, a, L.fs_p, L.fk_p, scale, reinterpret_cast<float*>(w + L.fpart),
+                          reinterpret_cast<float*>(w + L.p), nullptr, st));
+    } else {
+      a.c = w + L.p; a.ldc = L.r8; a.alpha = scale;
+      HIPTRY(gemm(G_F32_PANEL_NT_STORE, a, 1, st, 2 * Md * rr * ki, (Md * ki + rr * ki + Md * L.r8) * e));
+    }
   } else {
     TRY(panel_bf16(Xp, d_in, A, d_in, M, M, d_in, r, L.r8, L.splits_p, L.ksplit_p, col_scale(scale),
                    reinterpret_cast<float*>(w + L.ppart), reinterpret_cast<uint16_t*>(w + L.p), L.r8, nullptr, 0, st,
@@ -813,6 +837,16 @@ int forward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, f
     HIPTRY(gemm(L.stream.low ? G_BF16_HALF_EPI : G_BF16_STREAM_EPI, a, 1, st, flop, bytes + xbytes));
     return LORA_OK;
   }
+  if (f32 && L.fs_y > 1) {
+    float* part = reinterpret_cast<float*>(w + L.fpart);
+    const int S = L.fs_y;
+    a.k_split = L.fk_y; a.c = part; a.ldc = d_out; a.part_stride = M * d_out;
+    HIPTRY(gemm(G_F32_NT_PARTIAL, a, S, st, flop, bytes + 4.0 * (S - 1) * Md * ko));
+    HIPTRY(timed(K_FINISH, double(S) * Md * ko, 4.0 * (S + 1) * Md * ko + xbytes, st, [&] {
+      return launch_split_finish_epi(4, part, S, M * d_out, M, d_out, Y, *ep, st);
+    }));
+    return LORA_OK;
+  }
   if (!f32 && L.splits_main > 1) {
     // few tokens: split partials over d_in (the rank-r segment in the last
     // split), then the fixed-order sum with the store / RoPE epilogue
@@ -822,7 +856,7 @@ int forward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, f
     HIPTRY(gemm(nf4 ? G_NF4_MED_NT_PARTIAL : G_BF16_MED_NT_PARTIAL, a, S, st, flop,
                 bytes - Md * ko * e + 4.0 * S * Md * ko));
     HIPTRY(timed(K_FINISH, double(S) * Md * ko, 4.0 * S * Md * ko + Md * ko * e + xbytes, st, [&] {
-      if (ep) return launch_split_finish_epi(part, S, M * d_out, M, d_out, static_cast<uint16_t*>(Y), *ep, st);
+      if (ep) return launch_split_finish_epi(2, part, S, M * d_out, M, d_out, Y, *ep, st);
       return launch_split_finish(part, S, M * d_out, M, d_out, static_cast<uint16_t*>(Y), d_out,
                                  rope ? rope->pos : nullptr, rope ? rope->cosc : nullptr,
                                  rope ? rope->sinc : nullptr, rope ? rope->max_pos : 0, st);
@@ -924,16 +958,26 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
       GemmArgs a = blank();
       a.a1 = Xp; a.lda1 = d_in; a.b1 = A; a.ldb1 = d_in; a.K1 = d_in;
       a.m_load = M; a.m_store = L.M8; a.n_load = r; a.n_store = L.r8;
-      a.ct = w + L.pt; a.ldct = L.M8; a.alpha = scale;
-      HIPTRY(gemm(G_F32_PANEL_NT_STORE_T, a, 1, st, 2 * Md * rr * ki, (Md * ki + rr * ki + Md * L.r8) * e));
+      if (L.fs_p > 1) {
+        TRY(panel_f32_split(G_F32_PANEL_NT_PARTIAL, a, L.fs_p, L.fk_p, scale, reinterpret_cast<float*>(w + L.fpart),
+                            nullptr, reinterpret_cast<float*>(w + L.pt), st));
+      } else {
+        a.ct = w + L.pt; a.ldct = L.M8; a.alpha = scale;
+        HIPTRY(gemm(G_F32_PANEL_NT_STORE_T, a, 1, st, 2 * Md * rr * ki, (Md * ki + rr * ki + Md * L.r8) * e));
+      }
     }
     // Qs = s G B [M8, r8] and Qt = Qs^T [r8, M8]
     {
       GemmArgs a = blank();
       a.a1 = G; a.lda1 = d_out; a.b1 = Bsrc; a.ldb1 = L.r8; a.K1 = d_out;
       a.m_load = M; a.m_store = L.M8; a.n_load = L.r8; a.n_store = L.r8;
-      a.c = Qs; a.ldc = L.r8; a.ct = Qt; a.ldct = L.M8; a.alpha = scale;
-      HIPTRY(gemm(G_F32_PANEL_NN_BOTH, a, 1, st, 2 * Md * rr * ko, (Md * ko + rr * ko + 2 * Md * L.r8) * e));
+      if (L.fs_q > 1) {
+        TRY(panel_f32_split(G_F32_PANEL_NN_PARTIAL, a, L.fs_q, L.fk_q, scale, reinterpret_cast<float*>(w + L.fpart),
+                            static_cast<float*>(Qs), static_cast<float*>(Qt), st));
+      } else {
+        a.c = Qs; a.ldc = L.r8; a.ct = Qt; a.ldct = L.M8; a.alpha = scale;
+        HIPTRY(gemm(G_F32_PANEL_NN_BOTH, a, 1, st, 2 * Md * rr * ko, (Md * ko + rr * ko + 2 * Md * L.r8) * e));
+      }
     }
   } else {
     // Pt = (s X A^T)^T  [r8, M8], recomputed from X (rows M..M8 and columns r..r8 are zeros)
@@ -1032,7 +1076,15 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
     }
     const double wbytes = nf4 ? ko * ki / 2 + ko * ki / 64 * 4 : ko * ki * e;
     const double flop = 2 * Md * ki * (ko + rr), bytes = (Md * ko + Md * rr + rr * ki + Md * ki) * e + wbytes;
-    if (!f32 && L.splits_main > 1) {
+    if (f32 && L.fs_y > 1) {
+      const int S = L.fs_y;
+      float* sp = reinterpret_cast<float*>(w + L.fpart);
+      a.k_split = L.fk_y; a.c = sp; a.ldc = d_in; a.part_stride = M * d_in;
+      HIPTRY(gemm(G_F32_NN_PARTIAL, a, S, st, flop, bytes + 4.0 * (S - 1) * Md * ki));
+      HIPTRY(timed(K_FINISH, double(S) * Md * ki, 4.0 * (S + 1) * Md * ki, st, [&] {
+        return launch_split_finish_epi(4, sp, S, M * d_in, M, d_in, dX, EpiArgs{}, st);
+      }));
+    } else if (!f32 && L.splits_main > 1) {
       // few tokens: split partials over d_out (the rank-r segment in the last
       // split), then the fixed-order sum
       const int S = L.splits_main;
@@ -1594,6 +1646,16 @@ struct EpiLayout {
   int chunks = 1;
 };
 
+// Splits of an epilogue layer's fp32 contraction K whose tiles leave CUs
+// idle: about two blocks a CU, each at least 512 long.
+void f32_split(int64_t tiles, int64_t K, int* splits, int64_t* ksplit) {
+  if (tiles >= 256) return;
+  const int64_t s = std::min<int64_t>({cdiv(512, tiles), K / 512, 64});
+  if (s < 2) return;
+  *ksplit = rup(cdiv(K, s), 64);
+  *splits = (int)cdiv(K, *ksplit);
+}
+
 EpiLayout make_epi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, const lora_group_member& m,
                           const lora_epilogue& e) {
   EpiLayout E;
@@ -1618,6 +1680,15 @@ EpiLayout make_epi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, const lo
       if (m.W_nf4 || !m.W_t) E.L.wt = take(size_t(d_in) * m.d_out * 2);
       E.L.at = take(size_t(d_in) * E.L.r8 * 2);
     }
+  }
+  if (dtype == LORA_F32 && M > 0 && !tiny_fits(M, d_in, m.d_out, m.r)) {
+    const int64_t rows = bwd ? E.L.M8 : M, N = bwd ? d_in : m.d_out, K = bwd ? m.d_out : d_in;
+    f32_split(cdiv(M, 64) * cdiv(N, 128), K, &E.L.fs_y, &E.L.fk_y);
+    f32_split(cdiv(rows, 64) * cdiv(E.L.r8, 64), d_in, &E.L.fs_p, &E.L.fk_p);
+    if (bwd) f32_split(cdiv(rows, 64) * cdiv(E.L.r8, 64), m.d_out, &E.L.fs_q, &E.L.fk_q);
+    const int64_t sp = std::max(E.L.fs_p, E.L.fs_q);
+    const size_t most = std::max(E.L.fs_y > 1 ? size_t(E.L.fs_y) * M * N : 0, sp > 1 ? size_t(sp) * rows * E.L.r8 : 0);
+    if (most) E.L.fpart = take(most * 4);
   }
   if (E.L.stream.half > 0) {
     E.L.st_part = take(size_t(E.L.stream.half) * 2 * 256 * 256 * 4);

@@ -177,6 +177,8 @@ TileShape gemm_tile(GemmKind k) {
     case G_F32_PANEL_NT_STORE:
     case G_F32_PANEL_NT_STORE_T:
     case G_F32_PANEL_NN_BOTH:
+    case G_F32_PANEL_NT_PARTIAL:
+    case G_F32_PANEL_NN_PARTIAL:
       return {64, 64};
     case G_BF16_SPLIT_NN_PARTIAL:
     case G_F32_SPLIT_NN_PARTIAL:
@@ -203,6 +205,8 @@ TileShape gemm_tile(GemmKind k) {
     case G_F32_NN_ADD:
     case G_F32_NN_ADD_MASKED:
     case G_F32_NT_EPI:
+    case G_F32_NT_PARTIAL:
+    case G_F32_NN_PARTIAL:
       return {64, 128};
     default:
       return {0, 0};
@@ -289,6 +293,10 @@ hipError_t launch_gemm(GemmKind k, GemmArgs a, int splits, hipStream_t st) {
     case G_BF16_MED_NT_EPI: return run<bf, 128, 128, 4, 1, false, EPI_ACT, BL_PLAIN>(a, splits, st);
     case G_NF4_BIG_NT_EPI: return run<bf, 256, 256, 2, 4, false, EPI_ACT, BL_NF4>(a, splits, st);
     case G_NF4_MED_NT_EPI: return run<bf, 128, 128, 4, 1, false, EPI_ACT, BL_NF4>(a, splits, st);
+    case G_F32_NT_PARTIAL: return run<float, 64, 128, 4, 1, false, EPI_PARTIAL, BL_PLAIN>(a, splits, st);
+    case G_F32_NN_PARTIAL: return run<float, 64, 128, 4, 1, true, EPI_PARTIAL, BL_PLAIN>(a, splits, st);
+    case G_F32_PANEL_NT_PARTIAL: return run<float, 64, 64, 2, 2, false, EPI_PARTIAL, BL_PLAIN>(a, splits, st);
+    case G_F32_PANEL_NN_PARTIAL: return run<float, 64, 64, 2, 2, true, EPI_PARTIAL, BL_PLAIN>(a, splits, st);
     case G_F32_NT_EPI: return run<float, 64, 128, 4, 1, false, EPI_ACT, BL_PLAIN>(a, splits, st);
     case G_NF4_WHOLE_NT_EPI:
     case G_NF4_WHOLE_NT_STORE: {
@@ -753,28 +761,61 @@ hipError_t launch_split_finish(const float* part, int splits, int64_t part_strid
 
 // The same sums with the bias / activation / residual epilogue; 4 columns a
 // thread.
+template <typename T>
 __global__ void __launch_bounds__(256) split_finish_epi_kernel(const float* __restrict__ part, int splits,
-                                                               int64_t part_stride, int64_t M, int64_t N, uint16_t* out,
+                                                               int64_t part_stride, int64_t M, int64_t N, T* out,
                                                                EpiArgs ep) {
   const int64_t per_row = N / 4, items = M * per_row;
   for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < items; e += (int64_t)gridDim.x * blockDim.x) {
     const int64_t m = e / per_row, c = (e - m * per_row) * 4;
-    const float* src = part + m * N + c;
-    float a[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int z = 0; z < splits; ++z) {
-      const float4 v = *reinterpret_cast<const float4*>(src + (int64_t)z * part_stride);
-      a[0] += v.x; a[1] += v.y; a[2] += v.z; a[3] += v.w;
-    }
+    const float4 v = sum_splits(part + m * N + c, splits, part_stride);
+    float a[4] = {v.x, v.y, v.z, v.w};
     epi_apply(ep, out, m * N + c, c, a);
   }
 }
 
-hipError_t launch_split_finish_epi(const float* part, int splits, int64_t part_stride, int64_t M, int64_t N,
-                                   uint16_t* out, const EpiArgs& ep, hipStream_t st) {
+hipError_t launch_split_finish_epi(int elem_bytes, const float* part, int splits, int64_t part_stride, int64_t M,
+                                   int64_t N, void* out, const EpiArgs& ep, hipStream_t st) {
   if (M <= 0 || N <= 0) return hipSuccess;
   if (splits < 1 || splits > kMaxSplits || N % 8 || part_stride % 4) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(split_finish_epi_kernel, dim3(grid_for(M * (N / 4), 256)), dim3(256), 0, st, part, splits,
-                     part_stride, M, N, out, ep);
+  const dim3 grid(grid_for(M * (N / 4), 256));
+  if (elem_bytes == 2)
+    hipLaunchKernelGGL(split_finish_epi_kernel<uint16_t>, grid, dim3(256), 0, st, part, splits, part_stride, M, N,
+                       static_cast<uint16_t*>(out), ep);
+  else
+    hipLaunchKernelGGL(split_finish_epi_kernel<float>, grid, dim3(256), 0, st, part, splits, part_stride, M, N,
+                       static_cast<float*>(out), ep);
+  return hipGetLastError();
+}
+
+// An fp32 panel from its partials: one thread per 4 columns of a row.
+__global__ void __launch_bounds__(256) panel_sum_f32_kernel(const float* __restrict__ part, int splits, int64_t rows,
+                                                            int64_t n, float scale, float* __restrict__ out,
+                                                            float* __restrict__ outt) {
+  const int64_t per_row = n / 4, items = rows * per_row;
+  for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < items; e += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t q = e / per_row, c = (e - q * per_row) * 4;
+    float4 v = sum_splits(part + q * n + c, splits, rows * n);
+    v.x *= scale;
+    v.y *= scale;
+    v.z *= scale;
+    v.w *= scale;
+    if (out) *reinterpret_cast<float4*>(out + q * n + c) = v;
+    if (outt) {
+      outt[c * rows + q] = v.x;
+      outt[(c + 1) * rows + q] = v.y;
+      outt[(c + 2) * rows + q] = v.z;
+      outt[(c + 3) * rows + q] = v.w;
+    }
+  }
+}
+
+hipError_t launch_panel_sum_f32(const float* part, int splits, int64_t rows, int64_t n, float scale, float* out,
+                                float* outt, hipStream_t st) {
+  if (rows <= 0 || n <= 0) return hipSuccess;
+  if (splits < 1 || splits > kMaxSplits || n % 4) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(panel_sum_f32_kernel, dim3(grid_for(rows * (n / 4), 256)), dim3(256), 0, st, part, splits, rows, n,
+                     scale, out, outt);
   return hipGetLastError();
 }
 

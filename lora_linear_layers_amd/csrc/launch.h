@@ -65,6 +65,11 @@ enum GemmKind : int {
   G_F32_NT_EPI,
   G_BF16_HALF_EPI,    // 128 x 256 tiles, up to one a CU (gemm_w4_half_kernel)
   G_BF16_STREAM_EPI,  // 256 x 256 tiles, ragged and split over the CUs (gemm_w4_stream_kernel)
+  // fp32 partials over splits of the contraction (an epilogue layer's few tiles)
+  G_F32_NT_PARTIAL,
+  G_F32_NN_PARTIAL,
+  G_F32_PANEL_NT_PARTIAL,
+  G_F32_PANEL_NN_PARTIAL,
   G_KIND_COUNT
 };
 
@@ -181,9 +186,14 @@ hipError_t launch_split_finish(const float* part, int splits, int64_t part_strid
                                uint16_t* out, int64_t ldo, const int32_t* pos, const float* cosc, const float* sinc,
                                int64_t max_pos, hipStream_t st);
 
-// The same sums with an epilogue: out [M, N] = act(sum + bias) + residual.
-hipError_t launch_split_finish_epi(const float* part, int splits, int64_t part_stride, int64_t M, int64_t N,
-                                   uint16_t* out, const EpiArgs& ep, hipStream_t st);
+// The same sums with an epilogue: out [M, N] (bf16 or fp32, by elem_bytes) =
+// act(sum + bias) + residual.
+hipError_t launch_split_finish_epi(int elem_bytes, const float* part, int splits, int64_t part_stride, int64_t M,
+                                   int64_t N, void* out, const EpiArgs& ep, hipStream_t st);
+// fp32 panel: out [rows, n] and / or outt [n, rows] = scale * the sum over splits
+// of part [splits][rows, n].
+hipError_t launch_panel_sum_f32(const float* part, int splits, int64_t rows, int64_t n, float scale, float* out,
+                                float* outt, hipStream_t st);
 
 // Backward of the epilogue over [M, N]: dZ = dY act'(Z) (neither is touched
 // without an activation) and, with part, the column sums of dZ over `chunks`

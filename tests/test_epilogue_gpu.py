@@ -173,6 +173,9 @@ BF16 = [
 F32 = [
     (1, 8, 8, 1, "tiny_f32"), (128, 256, 256, 8, "tiny_f32"), (33, 72, 40, 3, "tiny_f32"),
     (1000, 520, 392, 24, "gemm_f32_64x128_nt_epi"), (33, 520, 1032, 64, "gemm_f32_64x128_nt_epi"),
+    (107, 8704, 384, 32, "gemm_f32_64x128_nt_split"), (79, 1096, 1216, 5, "gemm_f32_64x128_nt_split"),
+    (2, 2024, 7144, 16, "gemm_f32_64x128_nt_split"), (700, 1024, 256, 256, "gemm_f32_64x128_nt_split"),
+    (1, 4104, 8, 1, "gemm_f32_64x128_nt_split"),
 ]
 NF4 = [
     (1, 512, 384, 16, "few_fwd"), (128, 256, 256, 64, "few_fwd"), (200, 512, 1024, 16, "split_finish"),
