@@ -1646,12 +1646,15 @@ struct EpiLayout {
   int chunks = 1;
 };
 
-// Splits of an epilogue layer's fp32 contraction K whose tiles leave CUs
-// idle: about two blocks a CU, each at least 512 long.
+// Splits of an epilogue layer's fp32 contraction K whose tiles are fewer than
+// two a CU: about four blocks a CU, which hide each other's loads, each at least
+// 256 long, from 768 on.  Measured on MI355X, none / two a CU of 512 / these:
+// 107 tokens, 8704 -> 384: 754 / 72 / 59 us forward, 16 tokens, 4096 -> 4096: 322 /
+// 61 / 52, 512 tokens: 344 / 246 / 225, 341 tokens, 13760 -> 5440 (258 tiles): 1672
+// / 1202 / 750; backward 16 tokens 510 / 103 / 86, 512 tokens 556 / 320 / 301.
 void f32_split(int64_t tiles, int64_t K, int* splits, int64_t* ksplit) {
-  if (tiles >= 256) return;
-  const int64_t s = std::min<int64_t>({cdiv(512, tiles), K / 512, 64});
-  if (s < 2) return;
+  if (tiles >= 512 || K < 768) return;
+  const int64_t s = std::min<int64_t>({cdiv(1024, tiles), K / 256, 64});
   *ksplit = rup(cdiv(K, s), 64);
   *splits = (int)cdiv(K, *ksplit);
 }
