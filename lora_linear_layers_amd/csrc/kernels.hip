@@ -820,8 +820,10 @@ hipError_t launch_panel_sum_f32(const float* part, int splits, int64_t rows, int
 }
 
 // ---------------------------------------------------------------------------
-// Backward of the epilogue: dZ = dY act'(Z) (one rounding to the type; not
-// written without an activation, where dZ is dY), and the bias gradient's
+// Backward of the epilogue: dZ = dY act'(Z), rounded once to the type (it is an
+// operand of the products for dX, Q and dB, which take bf16 on the matrix cores:
+// at most 2^-8 of a value, 0.0017 in the mean; not written without an
+// activation, where dZ is dY), and the bias gradient's
 // partial sums over the tokens.  A block takes 256 columns (8 a thread, 32
 // threads a row) and `rows` tokens, 8 of them at a time; its column sums,
 // joined over its 8 row groups in order, go to part[blockIdx.y][N].  The loads

@@ -517,18 +517,24 @@ def lora_linear_epi_bwd(X, member, dY, act: str = "none", Z=None, need_dX: bool 
 
 def _epi_bwd(dt, dev, M, d_in, d_out, r, m, X, dY, act, Z, need_dX, need_dbias, table16=None, ws=None):
     """lora_linear_epi_bwd of checked tensors."""
-    dX = torch.empty(M, d_in, dtype=X.dtype, device=dev) if need_dX else None
     dA = torch.empty(r, d_in, dtype=torch.float32, device=dev)
     dB = torch.empty(d_out, r, dtype=torch.float32, device=dev)
     dbias = torch.empty(d_out, dtype=torch.float32, device=dev) if need_dbias else None
-    m.dY, m.dX, m.dA, m.dB = L._ptr(dY), L._ptr(dX), L._ptr(dA), L._ptr(dB)
+    dX = _epi_bwd_into(dt, dev, M, d_in, m, X, dY, act, Z, need_dX, L._ptr(dA), L._ptr(dB), L._ptr(dbias), table16, ws)
+    return dX, dA, dB, dbias
+
+
+def _epi_bwd_into(dt, dev, M, d_in, m, X, dY, act, Z, need_dX, dA, dB, dbias, table16=None, ws=None):
+    """dX, and the gradients at the addresses dA, dB and dbias."""
+    dX = torch.empty(M, d_in, dtype=X.dtype, device=dev) if need_dX else None
+    m.dY, m.dX, m.dA, m.dB = L._ptr(dY), L._ptr(dX), dA, dB
     e = L.Epilogue(_choice("act", ACTIVATIONS, act), None, None, L._ptr(Z))
     tab = L._table_ptr(table16) if table16 is not None else None
     ws = _epi_ws(True, dt, M, d_in, m, e, dev, ws)
     with _on(dev):
         L._check("lora_linear_epi_bwd", L.lib().lora_linear_epi_bwd(
-            dt, M, d_in, m, e, L._ptr(X), tab, L._ptr(dbias), L._ptr(ws), ws.numel(), L._stream(dev)))
-    return dX, dA, dB, dbias
+            dt, M, d_in, m, e, L._ptr(X), tab, dbias, L._ptr(ws), ws.numel(), L._stream(dev)))
+    return dX
 
 
 class LoraLinearEpiFunction(torch.autograd.Function):
@@ -541,7 +547,6 @@ class LoraLinearEpiFunction(torch.autograd.Function):
         Y, Z = lora_linear_epi_fwd(X, member, act, bias, residual, store_z=act != "none")
         ctx.save_for_backward(X, W, A, B, Z, W_t)
         ctx.scale, ctx.act = scale, act
-        ctx.bias_dtype = None if bias is None else bias.dtype
         return Y
 
     @staticmethod
@@ -552,10 +557,19 @@ class LoraLinearEpiFunction(torch.autograd.Function):
         dev, (M, d_in), (d_out, r) = X.device, X.shape, B.shape
         m = _epi_struct({"W": W, "A": A, "B": B, "scale": ctx.scale, "W_t": W_t}, r, d_out)
         _check(dev, "the gradient of Y", dY, (X.dtype,), M * d_out)
-        dX, dA, dB, dbias = _epi_bwd(L._dtype_code(X), dev, M, d_in, d_out, r, m, X, dY, ctx.act, Z,
-                                     ctx.needs_input_grad[0], ctx.needs_input_grad[4])
-        return (dX, None, dA.to(A.dtype), dB.to(B.dtype), None if dbias is None else dbias.to(ctx.bias_dtype),
-                dY if ctx.needs_input_grad[5] else None, None, None, None)
+        dt, need_dX, need_dbias = L._dtype_code(X), ctx.needs_input_grad[0], ctx.needs_input_grad[4]
+        if A.dtype == torch.float32:
+            dX, dA, dB, dbias = _epi_bwd(dt, dev, M, d_in, d_out, r, m, X, dY, ctx.act, Z, need_dX, need_dbias)
+        else:
+            # the fp32 gradients side by side (each a multiple of 8 values), rounded by one launch instead of three
+            na, nb = r * d_in, d_out * r
+            g = torch.empty(na + nb + (d_out if need_dbias else 0), dtype=torch.float32, device=dev)
+            at = g.data_ptr()
+            dX = _epi_bwd_into(dt, dev, M, d_in, m, X, dY, ctx.act, Z, need_dX, at, at + 4 * na,
+                               at + 4 * (na + nb) if need_dbias else None)
+            dA, dB, *rest = g.to(A.dtype).split([na, nb] + ([d_out] if need_dbias else []))
+            dA, dB, dbias = dA.view(r, d_in), dB.view(d_out, r), rest[0] if rest else None
+        return (dX, None, dA, dB, dbias, dY if ctx.needs_input_grad[5] else None, None, None, None)
 
 
 class LoraLinearFunction(torch.autograd.Function):
