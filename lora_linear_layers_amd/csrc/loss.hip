@@ -38,6 +38,7 @@ struct Row<uint16_t> {  // bf16 bit patterns
   typedef u32x4_e2 V;
   static __device__ __forceinline__ float at(const uint16_t* p) { return __builtin_bit_cast(float, (uint32_t)*p << 16); }
   static __device__ __forceinline__ void put(uint16_t* p, float v) { *p = f2bf(v); }
+  static __device__ __forceinline__ u32x4 none() { return u32x4{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u}; }  // -inf
   static __device__ __forceinline__ void unpack(const u32x4& v, float (&f)[8]) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -58,6 +59,7 @@ struct Row<float> {
   typedef u32x4_e4 V;
   static __device__ __forceinline__ float at(const float* p) { return *p; }
   static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
+  static __device__ __forceinline__ u32x4 none() { return u32x4{0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u}; }
   static __device__ __forceinline__ void unpack(const u32x4& v, float (&f)[4]) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -75,31 +77,38 @@ struct Row<float> {
 
 // ---------------------------------------------------------------------------
 // log-probabilities: one pass over a row with the running maximum m and the
-// sum s of e^(tau (z - m)); logp = tau (z_t - m) - log s.  m and log s are
-// kept apart (their sum, the log-sum-exp, would round away what a confident
-// row's small log-probability is made of).
-// Bound by reading the logits: 8192 x 128000 bf16 in 329 us, 6.4 TB/s (a large
-// copy moves 5.2 TB/s, read and written); the exponential, a quarter-rate
-// instruction, would take 0.11 ms of it.  The gradient reads and writes them
-// once: 656 us behind the forward, 6.4 TB/s.  24 x 32000: 6.1 us, a launch, one
-// round of loads and the joins.
+// rest r of the sum, that of e^(tau (z - m)) but for one element of the maximum:
+// logp = tau (z_t - m) - log(1 + r).  m, and log(1 + r) from r alone, are kept
+// apart (the log-sum-exp, or 1 + r, would round away what a confident row's small
+// log-probability is made of).
+// Bound by reading the logits and, not far behind, by the instructions: 8192 x
+// 128000 bf16 in 353 us, 5.9 TB/s (a large copy moves 5.2 TB/s, read and
+// written; with the sum in one number and its digits lost, 337 us); the
+// exponential, a quarter-rate instruction, would take 0.11 ms of it.  More than 64
+// registers a thread would leave one block of 1024 a CU (432 us).  The gradient
+// reads and writes them once: 656 us behind the forward, 6.4 TB/s.  24 x 32000:
+// 7.1 us, a launch, one round of loads and the joins.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float fexp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// (m, s) of two parts of a row; a part with no finite value has m = -inf,
-// s = 0 and adds nothing.  c = tau log2 e.
-__device__ __forceinline__ void join_max_sum(float& m, float& s, float m2, float s2, float c) {
+// A part of a row is (m, r): its maximum and the sum of e^(tau (z - m)) over its
+// other elements, one element of the maximum left out, so that the sum is 1 + r.
+// Held in one number, 1 + r would round away the digits of a small r, which are
+// all that a confident row's log-probability -log(1 + r) is made of.  A part
+// with no finite value has m = -inf, r = 0 and adds nothing.  c = tau log2 e.
+__device__ __forceinline__ void join_max_rest(float& m, float& r, float m2, float r2, float c) {
   const float nm = fmaxf(m, m2), base = nm == -INFINITY ? 0.f : nm;
-  s = s * fexp2((m - base) * c) + s2 * fexp2((m2 - base) * c);
+  const float f = fexp2((m - base) * c), f2 = fexp2((m2 - base) * c);
+  r = r * f + r2 * f2 + fminf(f, f2);  // (the lower maximum joins the rest)
   m = nm;
 }
 
 template <typename T, int NT>
-__global__ void __launch_bounds__(NT) token_logp_kernel(const T* __restrict__ z, int64_t ld, int64_t rows, int V,
+__global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8, 8))) token_logp_kernel(const T* __restrict__ z, int64_t ld, int64_t rows, int V,
                                                         const int64_t* __restrict__ target, float tau,
                                                         float* __restrict__ logp, float* __restrict__ stats) {
   using R = Row<T>;
-  constexpr int E = R::E, U = 4;
+  constexpr int E = R::E, U = 4, G = 2;
   __shared__ float red[2][NT / 64];
   const float c = tau * LOG2E;
   const int tid = threadIdx.x;
@@ -108,51 +117,91 @@ __global__ void __launch_bounds__(NT) token_logp_kernel(const T* __restrict__ z,
     const int64_t t = target[row];
     const bool has = t >= 0 && t < V;
     const float zt = has ? R::at(zr + t) : 0.f;
-    float m = -INFINITY, s = 0.f;
-    auto take = [&](const u32x4 v) {
-      float x[E];
-      R::unpack(v, x);
-      float cm = x[0];
+    // top: the vector that brought the thread's maximum, st: its sum with the
+    // maximum in it, sr: the sum of all the other vectors
+    float m = -INFINITY, st = 0.f, sr = 0.f;
+    u32x4 top = {0u, 0u, 0u, 0u};
+    auto take = [&](const u32x4* v) {  // G vectors at one scale: one rescaling for all of them
+      float cm[G], nm = m;
 #pragma unroll
-      for (int e = 1; e < E; ++e) cm = fmaxf(cm, x[e]);
-      const float nm = fmaxf(m, cm), base = nm == -INFINITY ? 0.f : nm;
-      s *= fexp2((m - base) * c);
+      for (int u = 0; u < G; ++u) {
+        float x[E];
+        R::unpack(v[u], x);
+        cm[u] = x[0];
 #pragma unroll
-      for (int e = 0; e < E; ++e) s += fexp2((x[e] - base) * c);
-      m = nm;
+        for (int e = 1; e < E; ++e) cm[u] = fmaxf(cm[u], x[e]);
+        nm = fmaxf(nm, cm[u]);
+      }
+      const float base = nm == -INFINITY ? 0.f : nm, f = fexp2((m - base) * c);
+      sr *= f;
+      st *= f;
+#pragma unroll
+      for (int u = 0; u < G; ++u) {
+        float x[E], sv = 0.f;
+        R::unpack(v[u], x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) sv += fexp2((x[e] - base) * c);
+        const bool up = cm[u] > m;
+        sr += up ? st : sv;
+        st = up ? sv : st;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top[k] = up ? v[u][k] : top[k];
+        m = up ? cm[u] : m;
+      }
     };
     const int head = row_head(zr), nv = (V - head) / E;
     const T* zv = zr + head;
+    auto vec = [&](int k) { return *reinterpret_cast<const typename R::V*>(zv + (int64_t)k * E); };
     int i = tid;
+    u32x4 v[U];
     for (; i + (U - 1) * NT < nv; i += U * NT) {
-      u32x4 v[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const typename R::V*>(zv + (int64_t)(i + u * NT) * E);
+      for (int u = 0; u < U; ++u) v[u] = vec(i + u * NT);
 #pragma unroll
-      for (int u = 0; u < U; ++u) take(v[u]);
+      for (int u = 0; u < U; u += G) take(v + u);
     }
-    for (; i < nv; i += NT) take(*reinterpret_cast<const typename R::V*>(zv + (int64_t)i * E));
+    if (i < nv) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        v[u] = R::none();
+        if (i + u * NT < nv) v[u] = vec(i + u * NT);
+      }
+#pragma unroll
+      for (int u = 0; u < U; u += G) take(v + u);
+    }
+    float r = sr;
+    if (m > -INFINITY) {  // the rest of the top vector, one element of the maximum left out
+      float x[E];
+      R::unpack(top, x);
+      bool left = false;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const bool here = !left && x[e] == m;
+        r += here ? 0.f : fexp2((x[e] - m) * c);
+        left = left || here;
+      }
+    }
     // the elements before and behind the vectors (at most E)
     const int rest = V - head - nv * E;
-    if (tid < rest + head) join_max_sum(m, s, tid < rest ? R::at(zv + (int64_t)nv * E + tid) : R::at(zr), 1.f, c);
+    if (tid < rest + head) join_max_rest(m, r, tid < rest ? R::at(zv + (int64_t)nv * E + tid) : R::at(zr), 0.f, c);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) {
-      const float m2 = __shfl_xor(m, o), s2 = __shfl_xor(s, o);
-      join_max_sum(m, s, m2, s2, c);
+      const float m2 = __shfl_xor(m, o), r2 = __shfl_xor(r, o);
+      join_max_rest(m, r, m2, r2, c);
     }
     if constexpr (NT > 64) {
       if ((tid & 63) == 0) {
         red[0][tid >> 6] = m;
-        red[1][tid >> 6] = s;
+        red[1][tid >> 6] = r;
       }
       __syncthreads();
       m = red[0][0];
-      s = red[1][0];
+      r = red[1][0];
 #pragma unroll
-      for (int w = 1; w < NT / 64; ++w) join_max_sum(m, s, red[0][w], red[1][w], c);
+      for (int w = 1; w < NT / 64; ++w) join_max_rest(m, r, red[0][w], red[1][w], c);
     }
     if (tid == 0) {
-      const float ls = logf(s);
+      const float ls = m == -INFINITY ? logf(r) : log1pf(r);
       logp[row] = has ? (zt - m) * tau - ls : 0.f;
       stats[2 * row] = m;
       stats[2 * row + 1] = ls;
@@ -161,7 +210,7 @@ __global__ void __launch_bounds__(NT) token_logp_kernel(const T* __restrict__ z,
   }
 }
 
-// dz_j = g tau (1[j = t] - e^(tau (z_j - m) - log s)).  A row without a token
+// dz_j = g tau (1[j = t] - e^(tau (z_j - m) - log(1 + r))).  A row without a token
 // or with g = 0 is not read: its gradient is zero whatever it holds.  dz may
 // be z (every thread reads its elements before it writes them).
 // STREAM: past the caches (logits that exceed the 256 MB of the last level,
@@ -187,9 +236,19 @@ __global__ void __launch_bounds__(GRAD_NT) token_logp_grad_kernel(const T* z, in
     T* dr = dz + row * ldd;
     const int head = row_head(zr), nv = (V - head) / E;
     const bool zero = g == 0.f;
-    const float m = stats[2 * row], ls2 = stats[2 * row + 1] * LOG2E, c = tau * LOG2E;
-    auto grad = [&](float x, int64_t j) { return (j == t ? g : 0.f) - g * fexp2((x - m) * c - ls2); };
+    const float m = stats[2 * row], ls = stats[2 * row + 1], ls2 = ls * LOG2E, c = tau * LOG2E;
+    auto grad = [&](float x) { return -g * fexp2((x - m) * c - ls2); };
+    // the target's own: g (1 - p), from p = 1/2 on with 1 - p as -(e^logp - 1),
+    // which keeps its digits where p is near 1
+    auto grad_t = [&](float x) {
+      const float p = fexp2((x - m) * c - ls2);
+      return p < 0.5f ? g - g * p : -g * expm1f((x - m) * tau - ls);
+    };
     const int i0 = seg * (U * NT) + threadIdx.x;
+    // the thread whose vectors hold the target (dz may be z: its logit is read before any of them is written)
+    const int vt = (int)t - head < 0 ? -1 : ((int)t - head) / E, dt = vt - i0;
+    const bool owner = !zero && vt >= 0 && vt < nv && dt >= 0 && dt < U * NT && dt % NT == 0;
+    const float zt = owner ? R::at(zr + t) : 0.f;
     u32x4 v[U];
     if (!zero) {
 #pragma unroll
@@ -211,7 +270,7 @@ __global__ void __launch_bounds__(GRAD_NT) token_logp_grad_kernel(const T* z, in
         float x[E];
         R::unpack(v[u], x);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = grad(x[e], j + e);
+        for (int e = 0; e < E; ++e) x[e] = grad(x[e]);
         o = R::pack(x);
       }
       if constexpr (STREAM)
@@ -219,12 +278,14 @@ __global__ void __launch_bounds__(GRAD_NT) token_logp_grad_kernel(const T* z, in
       else
         *reinterpret_cast<typename R::V*>(dr + j) = o;
     }
+    if (owner) R::put(dr + t, grad_t(zt));
     // the elements before and behind the vectors (at most E): the last
     // segment's first threads
     const int rest = V - head - nv * E;
     if (seg == segs - 1 && (int)threadIdx.x < rest + head) {
       const int64_t j = (int)threadIdx.x < rest ? head + (int64_t)nv * E + threadIdx.x : 0;
-      R::put(dr + j, zero ? 0.f : grad(R::at(zr + j), j));
+      const float x = zero ? 0.f : R::at(zr + j);
+      R::put(dr + j, zero ? 0.f : (j == t ? grad_t(x) : grad(x)));
     }
   }
 }
@@ -240,9 +301,9 @@ hipError_t run_logp(const T* z, int64_t ld, int64_t rows, int64_t V, const int64
     return hipGetLastError();
   };
   // threads a row (measured): a wave for a short one; 1024 where the row holds
-  // three rounds of their loads (8192 x 128000 bf16: 328 us against 349 with
-  // 256; 8192 x 50000: 167 against 146), or the rows alone do not fill the
-  // chip (64 x 128000: 11.7 us against 15.0)
+  // three rounds of their loads (8192 x 96000 bf16: 255 us against 269 with
+  // 256; 8192 x 50000: 167 against 147), or the rows alone do not fill the
+  // chip (64 x 128000: 13.1 us against 17.1)
   if (V <= 2048) return go(std::integral_constant<int, 64>{});
   if (V / Row<T>::E < 3 * 4 * 1024 && rows >= 512) return go(std::integral_constant<int, 256>{});
   return go(std::integral_constant<int, 1024>{});

@@ -261,3 +261,70 @@ def test_logp_refusals():
     assert bwd(dz=P, z=P, ldd=9) == -2  # in place with another stride
     if torch.cuda.device_count() == 0:
         assert fwd(z=P + 2, t=P + 8) == -6  # element alignment is enough: only the device is missing
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("V", [2, 64, 777, 2500, 50001])
+@pytest.mark.parametrize("tau", [1.0, 0.75])
+def test_logp_of_confident_rows_keeps_its_digits(lib, V, dtype, tau):
+    # a target that stands far out: logp = -log(1 + rest) with rest = sum of the others' e^(tau (z_j - z_t)), down to
+    # 1e-30, and the target's gradient g (1 - p).  Relative tolerance: rest's terms are off by (3 D + 4) u each, once
+    # more for their rescaling on the way (D = the largest tau |z_j - z_t|, at most one rescaling a vector of 4 and one
+    # a join, 6 u each), their sum by V / 64 u, log1p and the last products by 16 u
+    r = torch.Generator().manual_seed(V)
+    margins = [4.0, 9.0, 13.8, 14.5, 17.0, 25.0, 40.0, 80.0]
+    n = 3 * len(margins)
+    z = (torch.randn(n, V, generator=r) * 0.5).to(dtype)
+    t = torch.tensor([(0, V - 1, V // 2 + i % 7)[i % 3] % V for i in range(n)])
+    z[torch.arange(n), t] = torch.tensor([margins[i // 3] for i in range(n)]).to(dtype)
+    g = torch.randn(n, generator=r).cuda()
+    lp, stats = lib.lora_token_logp_fwd(z.cuda(), t.cuda(), tau)
+    dz = lib.lora_token_logp_bwd(z.cuda(), t.cuda(), stats, g, tau)
+    a = (z.double() - z.double().gather(1, t[:, None])) * tau
+    e = a.exp()
+    e[torch.arange(n), t] = 0  # (not subtracted afterwards: 1 + rest - 1 would lose the digits here too)
+    rest = e.sum(1)
+    want = -torch.log1p(rest)
+    rel = U * (6 * a.abs().amax(1) + 4 + 6 * (V / 256 + 24) + V / 64 + 16)
+    got = lp.cpu().double()
+    assert ((got - want).abs() <= rel * want.abs() + 2.0 ** -126).all(), ((got - want) / want).abs().max()
+    assert ((stats[:, 1].cpu().double() + want).abs() <= rel * want.abs() + 2.0 ** -126).all()
+    at = dz.cpu().double()[torch.arange(n), t]
+    wd = g.cpu().double() * tau * rest / (1 + rest)
+    assert ((at - wd).abs() <= (rel + HALF[dtype]) * wd.abs() + 2.0 ** -125).all(), ((at - wd) / wd).abs().max()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("V", [1, 5, 9, 64, 2049, 50001])
+def test_logp_of_tied_maxima(lib, V, dtype):
+    # k elements share the maximum, wherever they lie (one vector, neighbouring ones, the row's ends): the row's sum
+    # is k and every tied element's probability 1 / k
+    r = torch.Generator().manual_seed(V)
+    sets = [[0], [V - 1], [0, V - 1], list(range(min(V, 3))), list(range(min(V, 8))), list(range(max(0, V - 9), V)),
+            list(range(V)), torch.randperm(V, generator=r)[:min(V, 40)].tolist()]
+    z = torch.full((len(sets), V), -200.0)
+    for i, s in enumerate(sets):
+        z[i, s] = 3.5
+    t = torch.tensor([s[len(s) // 2] for s in sets]).cuda()
+    k = torch.tensor([float(len(set(s))) for s in sets]).double()
+    z = z.to(dtype).cuda()
+    lp, stats = lib.lora_token_logp_fwd(z, t)
+    dz = lib.lora_token_logp_bwd(z, t, stats, torch.ones(len(sets), device="cuda"))
+    assert (stats[:, 0] == 3.5).all()
+    assert ((lp.cpu().double() + k.log()).abs() <= 4 * U * k.log()).all()
+    at = dz.cpu().double()[torch.arange(len(sets)), t.cpu()]
+    assert ((at - (1 - 1 / k)).abs() <= (HALF[dtype] + 40 * U) * (1 - 1 / k)).all()
+
+
+@pytest.mark.gpu
+def test_logp_infinite_row_with_one_vector(lib):
+    # +infinity as the only element, in a vector of its own and beside a NaN: NaN, not a finite sum of the rest
+    z = torch.zeros(4, 9, device="cuda")
+    z[0, 0] = z[1, 8] = z[2, 3] = float("inf")
+    z[3, 1], z[3, 2] = float("inf"), float("nan")
+    t = torch.tensor([0, 8, 5, 1], device="cuda")
+    lp, _ = lib.lora_token_logp_fwd(z, t)
+    assert lp.isnan().all()
+    assert lib.lora_token_logp_fwd(z[:1, :1], t[:1])[0].isnan().all()
