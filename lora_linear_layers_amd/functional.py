@@ -843,14 +843,15 @@ class LoraHeadLogpFunction(torch.autograd.Function):
 
 class LoraPreferenceLossFunction(torch.autograd.Function):
     """(loss, pair_loss, rewards) = LoraPreferenceLossFunction.apply(logp, ref_logp, cu, mask, beta, kind,
-    label_smoothing, average); gradient of loss for logp (the reference is frozen, the other outputs are for logs)."""
+    label_smoothing, average); gradient of loss for logp (the reference is frozen, the other outputs are for logs).
+    logp may have any shape, its tokens in order."""
 
     @staticmethod
     def forward(ctx, logp, ref_logp, cu, mask, beta, kind="sigmoid", label_smoothing=0.0, average=False):
         loss, pair_loss, rewards, coef = lora_preference_loss_fwd(logp, cu, beta, ref_logp, mask, kind,
                                                                   label_smoothing, average)
         ctx.save_for_backward(cu, mask, coef)
-        ctx.n = logp.numel()
+        ctx.shape = logp.shape
         ctx.mark_non_differentiable(pair_loss, rewards)
         return loss, pair_loss, rewards
 
@@ -858,12 +859,13 @@ class LoraPreferenceLossFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dloss, *_):
         cu, mask, coef = ctx.saved_tensors
-        return (lora_preference_loss_bwd(coef, cu, ctx.n, mask, _f32c(dloss)),) + (None,) * 7
+        d = lora_preference_loss_bwd(coef, cu, ctx.shape.numel(), mask, _f32c(dloss))
+        return (d.view(ctx.shape),) + (None,) * 7
 
 
 class LoraPolicyLossFunction(torch.autograd.Function):
     """(loss, stats) = LoraPolicyLossFunction.apply(logp, old_logp, ref_logp, cu, advantages, mask, eps_low, eps_high,
-    beta, reduction, norm, per_token); gradient of loss for logp."""
+    beta, reduction, norm, per_token); gradient of loss for logp, which may have any shape, its tokens in order."""
 
     @staticmethod
     def forward(ctx, logp, old_logp, ref_logp, cu, advantages, mask, eps_low=0.2, eps_high=0.2, beta=0.0,
@@ -880,4 +882,4 @@ class LoraPolicyLossFunction(torch.autograd.Function):
     def backward(ctx, dloss, *_):
         logp, old_logp, ref_logp, cu, advantages, mask, weight = ctx.saved_tensors
         d = lora_policy_loss_bwd(logp, cu, advantages, weight, old_logp, ref_logp, mask, dloss=_f32c(dloss), **ctx.args)
-        return (d,) + (None,) * 11
+        return (d.view(logp.shape),) + (None,) * 11

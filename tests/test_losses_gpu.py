@@ -490,3 +490,20 @@ def test_loss_refusals():
     assert h(3, 100, 2.0, 0.2, 0.1, P, None, P, P, P, P, 0, P, P, P, None) == -2
     if torch.cuda.device_count() == 0:
         assert pref() == -6 and pol() == -6 and pol(ref=None, beta=0.0, old=None) == -6
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(1, 40), (5, 8), (2, 4, 5), (40,)], ids=str)
+def test_loss_gradients_have_the_shape_of_logp(lib, shape):
+    lens = [12, 9, 9, 10]
+    cu, n = _packed(lens)
+    lp, ref, old, mask, _ = _draw(51, n)
+    L, R, O, C, M = _dev(lp, ref, old, cu, mask)
+    adv = torch.tensor([0.7, 1.0, -1.2, 0.4], device="cuda")
+    calls = (lambda x: lib.LoraPreferenceLossFunction.apply(x, R, C, M, 0.1)[0],
+             lambda x: lib.LoraPolicyLossFunction.apply(x, O, R, C, adv, M, 0.2, 0.28, 0.05)[0])
+    for call in calls:
+        flat, x = L.clone().requires_grad_(), L.clone().view(shape).requires_grad_()
+        call(flat).backward()
+        call(x).backward()
+        assert x.grad.shape == torch.Size(shape) and torch.equal(x.grad.view(-1), flat.grad)
