@@ -711,6 +711,14 @@ def _check_tokens(dev, n, cu, ref_logp, mask):
         _check(dev, "mask", mask, _MASK, n)
 
 
+def _pairs(cu):
+    """P of the 2 P + 1 offsets of response pairs."""
+    S = cu.numel() - 1
+    if S < 2 or S % 2:
+        raise ValueError("cu must hold 2 P + 1 offsets")
+    return S // 2
+
+
 def lora_preference_loss_fwd(logp, cu, beta: float, ref_logp=None, mask=None, kind: str = "sigmoid",
                              label_smoothing: float = 0.0, average: bool = False, ws=None):
     """(loss, pair_loss [P], rewards [2 P], coef [2 P]) of P pairs over packed sequences: logp (and ref_logp) fp32
@@ -719,10 +727,8 @@ def lora_preference_loss_fwd(logp, cu, beta: float, ref_logp=None, mask=None, ki
     n, dev = logp.numel(), _gpu(logp)
     _check(dev, "logp", logp, _F32)
     _check_tokens(dev, n, cu, ref_logp, mask)
-    S = cu.numel() - 1
-    if S < 2 or S % 2:
-        raise ValueError("cu must hold 2 P + 1 offsets")
-    P = S // 2
+    P = _pairs(cu)
+    S = 2 * P
     new = logp.new_empty
     loss, pair_loss, rewards, coef = new(()), new(P), new(S), new(S)
     ws, ws_bytes = _loss_ws(0, S, n, logp, ws)
@@ -736,15 +742,15 @@ def lora_preference_loss_fwd(logp, cu, beta: float, ref_logp=None, mask=None, ki
 
 def lora_preference_loss_bwd(coef, cu, n_tokens: int, mask=None, dloss=None):
     """dlogp fp32 [n_tokens] of lora_preference_loss_fwd; dloss: fp32 scalar tensor (None: 1)."""
-    dev = _gpu(coef)
-    _check(dev, "coef", coef, _F32, cu.numel() - 1)
+    dev, P = _gpu(coef), _pairs(cu)
+    _check(dev, "coef", coef, _F32, 2 * P)
     _check_tokens(dev, n_tokens, cu, None, mask)
     if dloss is not None:
         _check(dev, "dloss", dloss, _F32, 1)
     dlogp = coef.new_empty(n_tokens)
     with _on(dev):
         L._check("lora_preference_loss_bwd", L.lib().lora_preference_loss_bwd(
-            coef.numel() // 2, n_tokens, L._ptr(cu), L._ptr(mask), L._ptr(coef), L._ptr(dloss), L._ptr(dlogp),
+            P, n_tokens, L._ptr(cu), L._ptr(mask), L._ptr(coef), L._ptr(dloss), L._ptr(dlogp),
             L._stream(dev)))
     return dlogp
 

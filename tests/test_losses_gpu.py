@@ -507,3 +507,9 @@ def test_loss_gradients_have_the_shape_of_logp(lib, shape):
         call(flat).backward()
         call(x).backward()
         assert x.grad.shape == torch.Size(shape) and torch.equal(x.grad.view(-1), flat.grad)
+
+
+@pytest.mark.gpu
+def test_preference_backward_refuses_an_odd_number_of_sequences(lib):
+    with pytest.raises(ValueError, match="2 P"):
+        lib.lora_preference_loss_bwd(torch.zeros(3, device="cuda"), torch.tensor([0, 1, 2, 3], device="cuda"), 3)
