@@ -620,3 +620,27 @@ def test_epilogue_refusals():
     assert size(0, 3, 8, 64, mk(), ep()) == 0 and size(0, 1, 8, 12, mk(), ep()) == 0
     if torch.cuda.device_count() == 0:
         assert fwd() == -6 and bwd(e=ep(act=0, Z=None)) == -6
+
+
+@pytest.mark.gpu
+def test_epilogue_adapter_gradient_past_32_bits(lib):
+    # dA where dZ has 2^31 elements and more: one token in 64 carries input, the rows at both ends and around
+    # element 2^31 among them, so that every sum of integers is exact in fp32 whatever its order
+    M, k, d, r = 140003, 64, 16384, 8
+    gen = torch.Generator("cuda").manual_seed(3)
+    draw = lambda *n: torch.randint(-2, 3, n, generator=gen, device="cuda", dtype=torch.int8).bfloat16()  # noqa: E731
+    X, dY, Z = draw(M, k), draw(M, d), draw(M, d)
+    rows = torch.arange(M, device="cuda")
+    X *= ((rows % 64 == 5) | (rows < 20) | (rows >= M - 20) | ((rows - 131072).abs() < 20))[:, None]
+    m = {"W": draw(d, k), "A": draw(r, k), "B": draw(d, r), "scale": 1.0}
+    _, dA, _, _ = lib.lora_linear_epi_bwd(X, m, dY, "relu", Z, need_dX=False)
+    want, mag = torch.zeros(r, k, device="cuda", dtype=torch.float64), torch.zeros(r, k, device="cuda", dtype=torch.float64)
+    for i in range(0, M, 20000):
+        x = X[i:i + 20000].double()
+        at = x.abs().sum(1) > 0
+        q = (dY[i:i + 20000][at] * (Z[i:i + 20000][at] > 0)).double() @ m["B"].double()  # below 2^17, exact
+        q = q.bfloat16().double().T.contiguous()  # Q is rounded to bf16, the product's operand
+        want += q @ x[at]
+        mag += q.abs() @ x[at].abs()
+    assert 0 < mag.max() < 2 ** 24
+    assert torch.equal(dA.double(), want)

@@ -513,3 +513,212 @@ def test_loss_gradients_have_the_shape_of_logp(lib, shape):
 def test_preference_backward_refuses_an_odd_number_of_sequences(lib):
     with pytest.raises(ValueError, match="2 P"):
         lib.lora_preference_loss_bwd(torch.zeros(3, device="cuda"), torch.tensor([0, 1, 2, 3], device="cuda"), 3)
+
+
+# ---------------------------------------------------------------------------
+# guarded outputs, many tokens, and shapes
+# ---------------------------------------------------------------------------
+class _Guards:
+    """Arrays in the middle of larger ones, to see what is written beside them."""
+
+    def __init__(self):
+        self.all = []
+
+    def new(self, n):
+        b = torch.full((n + 128,), 7.25, device="cuda")
+        self.all.append((b, n))
+        return b[64:64 + n]
+
+    def intact(self):
+        return all(bool((b[:64] == 7.25).all()) and bool((b[64 + n:] == 7.25).all()) for b, n in self.all)
+
+
+def _offsets(kind, n, S, seed):
+    r = np.random.default_rng(seed)
+    if kind == "outside":  # in order, but reaching past both ends of the tokens
+        cu = np.sort(r.integers(0, n, S + 1))
+        cu[0], cu[-1] = -50, n + 999
+        return cu
+    if kind == "random":
+        return r.integers(-50, n + 51, S + 1)
+    return np.sort(r.integers(0, n + 1, S + 1))[::-1].copy()  # decreasing
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["outside", "random", "decreasing"])
+@pytest.mark.parametrize("n,S", [(3000, 4), (3000, 130), (8192, 1024), (8193, 4), (70001, 130), (70001, 2050)])
+def test_losses_write_nothing_beside_their_outputs(lib, kind, n, S):
+    # every output and the workspace between guards, the token arrays NaN behind n: offsets outside the tokens are
+    # taken as their ends, disordered ones give some value, and nothing beside the outputs is written
+    G = _Guards()
+    C = lib.load()
+    P = S // 2
+    lp = torch.full((n + 256,), NAN, device="cuda")
+    ref, old = lp.clone(), lp.clone()
+    h = _draw(n + S, n)
+    lp[:n], ref[:n], old[:n] = (torch.from_numpy(h[i]).cuda() for i in (0, 1, 2))
+    cu_h = _offsets(kind, n, S, n + S)
+    cu = torch.from_numpy(cu_h.astype(np.int64)).cuda()
+    adv = torch.from_numpy(np.random.default_rng(1).normal(size=S).astype(np.float32)).cuda()
+    p = lambda t: t.data_ptr()  # noqa: E731
+    wb = [C.lora_loss_workspace_bytes(k, S, n) for k in (0, 1)]
+    ws = [G.new(b // 4) for b in wb]
+    loss, pair, rew, coef, d = G.new(1), G.new(P), G.new(S), G.new(S), G.new(n)
+    assert C.lora_preference_loss_fwd(0, P, n, 0.1, 0.0, 0, p(cu), None, p(lp), p(ref), p(loss), p(pair), p(rew),
+                                      p(coef), p(ws[0]), wb[0], None) == 0
+    assert C.lora_preference_loss_bwd(P, n, p(cu), None, p(coef), None, p(d), None) == 0
+    ploss, stats, weight, pd = G.new(1), G.new(4), G.new(S), G.new(n)
+    args = (0.2, 0.28, 0.05)
+    assert C.lora_policy_loss_fwd(0, S, n, *args, 1.0, p(cu), None, p(lp), p(old), p(ref), p(adv), 0, p(ploss), p(stats),
+                                  p(weight), p(ws[1]), wb[1], None) == 0
+    assert C.lora_policy_loss_bwd(S, n, *args, p(cu), None, p(lp), p(old), p(ref), p(adv), 0, p(weight), None, p(pd),
+                                  None) == 0
+    torch.cuda.synchronize()
+    assert G.intact()
+    assert not (d == 7.25).any() and not (pd == 7.25).any()  # every token's gradient is written
+    if kind == "outside":
+        c = np.clip(cu_h, 0, n)
+        wl, wp, wr, wd, mag = _pref_plain(h[0], h[1], c, None, 0.1, "sigmoid", 0.0, False)
+        a = 1e-9 * max(mag, 1.0)
+        _near(loss, [wl], 2 * U, a)
+        _near(pair, wp, 2 * U, a)
+        _near(rew, wr, 2 * U, a)
+        _near(d, wd, 4 * U, a / S)
+        wl, wst, wd, tol, mag = _policy_plain(h[0], h[2], h[1], adv.cpu().numpy(), c, None, 0.2, 0.28, 0.05, "sequence",
+                                              1.0, False)
+        _near(ploss, [wl], 2 * U, mag)
+        _near(stats[2:], wst[2:], 2 * U, 0)
+        assert (np.abs(pd.cpu().double().numpy() - wd) <= tol).all()
+
+
+def _walk_chunk(cu, S, N, t0, t1):
+    """The stretches (sequence or -1, its first token, from, to) in which a wave walks the tokens [t0, t1): the
+    kernels' steps on plain integers, every index checked."""
+    clip = lambda t: min(max(t, 0), N)  # noqa: E731
+    lo, hi = 0, S
+    while S > 64 and hi > lo:  # the first sequence that ends after t0, by a 64-way search
+        step = (hi - lo + 63) // 64
+        at = [lo + lane * step + step - 1 for lane in range(64)]
+        lo += sum(cu[i + 1] <= t0 for i in at if i < hi) * step
+        if step == 1:
+            break
+        hi = min(lo + step, hi)
+    base, pos, out = (min(lo, S) if S > 64 else 0), t0, []
+    while base < S and pos < t1:
+        end = [clip(cu[base + lane + 1]) if base + lane < S else 0 for lane in range(64)]
+        first = clip(cu[base])
+        while pos < t1:
+            todo = [lane for lane in range(64) if end[lane] > pos]
+            if not todo:
+                break
+            lane = todo[0]
+            assert base + lane < S
+            b = end[lane - 1] if lane else first
+            to = min(b if b > pos else end[lane], t1)
+            assert to > pos  # every step moves on
+            out.append((-1 if b > pos else base + lane, b, pos, to))
+            pos = to
+        base += 64
+    if pos < t1:
+        out.append((-1, 0, pos, t1))
+    return out
+
+
+def test_losses_walk_covers_every_token_once():
+    # the walk of loss.hip (Walk, first_seq, sum_chunk, sum_sequences) for ordered and disordered offsets: stretches
+    # join up over the chunk, and for ordered ones each sequence's parts are where its sum looks for them
+    import random
+
+    rng = random.Random(3)
+    for k in range(400):
+        S, N, ch = rng.choice([1, 2, 63, 64, 65, 130, 300]), rng.choice([1, 5, 64, 257, 1000]), rng.choice([64, 256])
+        if k % 3 == 0:
+            cu = [rng.randint(-50, N + 50) for _ in range(S + 1)]
+        elif k % 3 == 1:
+            cu = sorted(rng.randint(0, N) for _ in range(S + 1))
+        else:
+            cu = sorted(rng.choice([0, N // 3, N // 2, N]) for _ in range(S + 1))
+        head, seqp = {}, {}
+        for c in range(-(-N // ch)):
+            at = c * ch
+            for s, b, lo, hi in _walk_chunk(cu, S, N, at, min(at + ch, N)):
+                assert lo == at
+                at = hi
+                if s >= 0:
+                    where, key = (head, c) if b < c * ch else (seqp, s)
+                    where[key] = where.get(key, 0) + hi - lo
+            assert at == min(c * ch + ch, N)
+        if k % 3:
+            for s in range(S):
+                n = cu[s + 1] - cu[s]
+                if n:
+                    c0, c1 = cu[s] // ch, (cu[s + 1] - 1) // ch
+                    assert seqp[s] + sum(head[c] for c in range(c0 + 1, c1 + 1)) == n
+
+
+def _many_lens(total, seed):
+    """Lengths that sum to total: on and beside steps of 256 and chunks of 512 to 4096, empty ones, one of 40 %."""
+    r = np.random.default_rng(seed)
+    lens = [256, 0, 512, 1024, 4096, 255, 257, 1, 511, 513, 2048, 4095, 4097, 0]
+    lens += [int(total * 0.4)]
+    left = total - sum(lens)
+    while left > 0:
+        n = min(left, int(r.choice([r.integers(1, 700), 256, 768, r.integers(3000, 9000)])))
+        lens.append(n)
+        left -= n
+    if len(lens) % 2:
+        lens.append(0)
+    return lens
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("total", [2_200_003, 5_000_001, 20_000_003])
+def test_losses_of_many_tokens(lib, total):
+    # chunks of several steps (512 tokens above 2.1 M, up to 4096), both losses forward and backward
+    lens = _many_lens(total, total)
+    S, P = len(lens), len(lens) // 2
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), device="cuda")
+    n = int(cu[-1])
+    gen = torch.Generator("cuda").manual_seed(5)
+    rand = lambda *s: torch.rand(*s, generator=gen, device="cuda")  # noqa: E731
+    randn = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    ref = 2.5 * torch.log1p(-rand(n) * 0.999)
+    lp = ref + 0.3 * randn(n)
+    old = lp + 0.15 * randn(n)
+    mask = rand(n) > 0.25
+    adv = randn(S)
+    g = torch.tensor(0.5, device="cuda")
+    seq = torch.repeat_interleave(torch.arange(S, device="cuda"), torch.tensor(lens, device="cuda"))
+    m = mask.double()
+    # (summed on the CPU: one sequence has millions of the entries, which an atomic sum would add one by one)
+    add = lambda v: torch.stack([c.sum() for c in v.cpu().split(lens)]).cuda()  # noqa: E731
+    T = add(m)
+    # preference, averaged
+    loss, pair, rew, coef = lib.lora_preference_loss_fwd(lp, cu, 0.1, ref, mask, average=True)
+    d = lib.lora_preference_loss_bwd(coef, cu, n, mask, g)
+    x = lp.double() - ref.double()
+    D = add(x * m) / T.clamp(min=1)
+    u = D[:P] - D[P:]
+    want = torch.nn.functional.softplus(-0.1 * u)
+    cw = -0.1 * torch.sigmoid(-0.1 * u) / P
+    cw = torch.cat([cw, -cw]) / T.clamp(min=1)
+    near = lambda a, b, r, t: bool(((a.double() - b).abs() <= r * b.abs() + t).all())  # noqa: E731
+    assert near(pair, want, 2 * U, 1e-9) and near(loss, want.mean(), 2 * U, 1e-9) and near(rew, 0.1 * D, 2 * U, 1e-9)
+    assert near(d, cw[seq] * m * 0.5, 4 * U, 1e-13)
+    # policy, every token alike
+    kw = dict(old_logp=old, ref_logp=ref, mask=mask, eps_low=0.2, eps_high=0.28, beta=0.05)
+    loss, stats, w = lib.lora_policy_loss_fwd(lp, cu, adv, reduction="token", **kw)
+    d = lib.lora_policy_loss_bwd(lp, cu, adv, w, dloss=g, **kw)
+    A, y, dd = adv.double()[seq], lp.double() - old.double(), -x
+    over, under = (A > 0) & (y > math.log1p(0.28)), (A < 0) & (y < math.log1p(-0.2))
+    r, e = y.exp(), torch.expm1(dd)
+    pol = torch.where(over, 1.28, torch.where(under, 0.8, r)) * -A
+    W = 1 / float(T.sum())
+    # (the bounds of the head of this file, token by token)
+    mag = W * (m * (pol.abs() * (2 + y.abs()) * 2 * U + (e - dd) * 10 * U + dd * dd * 2e-9)).sum()
+    sums = torch.stack([(pol * m).sum() * W, ((e - dd) * m).sum() * W, ((over | under) & mask).sum() * W, T.sum()])
+    assert near(stats, sums, 2 * U, torch.stack([mag, mag, 0 * mag, 0 * mag]))
+    assert near(loss, sums[0] + 0.05 * sums[1], 2 * U, mag)
+    gr = W * 0.5 * (torch.where(over | under, 0.0, -r * A) - 0.05 * e) * m
+    tol = W * 0.5 * ((r * A).abs() * (2 + y.abs()) * 2 * U + 0.05 * ((e + 1) * (2 + dd.abs()) * 2 * U + U)) + 4 * U * gr.abs()
+    assert bool(((d.double() - gr).abs() <= tol + 1e-37).all())

@@ -328,3 +328,61 @@ def test_logp_infinite_row_with_one_vector(lib):
     lp, _ = lib.lora_token_logp_fwd(z, t)
     assert lp.isnan().all()
     assert lib.lora_token_logp_fwd(z[:1, :1], t[:1])[0].isnan().all()
+
+
+@pytest.mark.gpu
+def test_logp_gradient_on_another_stream(lib):
+    z, t, g = _inputs(15, 40, 3000, torch.bfloat16)
+    want = lib.lora_token_logp_fwd(z, t)
+    dwant = lib.lora_token_logp_bwd(z, t, want[1], g)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        got = lib.lora_token_logp_fwd(z, t)
+        dgot = lib.lora_token_logp_bwd(z, t, got[1], g)
+    torch.cuda.synchronize()
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1]) and torch.equal(dwant, dgot)
+
+
+@pytest.mark.gpu
+def test_logp_fp32_logits_past_the_caches(lib):
+    # above 256 MB the gradient streams past the caches: the same bits as the same rows alone, and those right
+    n, V = 1400, 50001
+    small, t_s, g_s = _inputs(16, 8, V, torch.float32, ignored=False)
+    z, t, g = small.repeat(n // 8, 1), t_s.repeat(n // 8), g_s.repeat(n // 8)
+    assert z.numel() * 4 > 256 << 20
+    _check(lib, small.clone(), t_s, g_s, 1.25)
+    lp_s, stats_s = lib.lora_token_logp_fwd(small, t_s, 1.25)
+    want = lib.lora_token_logp_bwd(small, t_s, stats_s, g_s, 1.25)
+    lp, stats = lib.lora_token_logp_fwd(z, t, 1.25)
+    assert torch.equal(lp.view(-1, 8), lp_s.expand(n // 8, 8)) and torch.equal(stats, stats_s.repeat(n // 8, 1))
+    apart = lib.lora_token_logp_bwd(z, t, stats, g, 1.25)
+    assert torch.equal(apart.view(-1, 8, V), want.expand(n // 8, 8, V))
+    lib.lora_token_logp_bwd(z, t, stats, g, 1.25, dlogits=z)
+    assert torch.equal(z, apart)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 8), (torch.bfloat16, 9)], ids=["f32", "bf16"])
+def test_logp_more_rows_than_blocks(lib, dtype, V):
+    # blocks take several rows (2^20 of them) and the gradient's several segments (2^22): every row against its
+    # definition in 64 bits, at the bounds of the head of this file
+    n = (1 << 22) + 5
+    gen = torch.Generator("cuda").manual_seed(17)
+    z = (torch.randn(n, V, generator=gen, device="cuda") * 2.5).to(dtype)
+    t = torch.randint(-1, V, (n,), generator=gen, device="cuda")
+    g = torch.randn(n, generator=gen, device="cuda")
+    lp, stats = lib.lora_token_logp_fwd(z, t)
+    dz = lib.lora_token_logp_bwd(z, t, stats, g)
+    full = torch.log_softmax(z.double(), 1)
+    has = t >= 0
+    at = t.clamp(min=0)[:, None]
+    want = torch.where(has, full.gather(1, at).squeeze(1), 0.0)
+    tol = U * (V / 64 + 24 + 3 * 40 + 4 + 8 * (full.abs().amax(1) + 1))
+    assert torch.equal(stats[:, 0], z.float().amax(1))
+    assert ((lp.double() - want).abs() <= tol).all()
+    gz = torch.where(has, g, 0.0).double()[:, None]
+    d = -gz * full.exp()
+    d.scatter_add_(1, at, gz)
+    err = (dz.double() - d).abs()
+    assert (err <= gz.abs() * (tol[:, None] + 8 * U) + HALF[dtype] * d.abs() + 2.0 ** -126).all()
