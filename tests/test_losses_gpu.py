@@ -722,3 +722,21 @@ def test_losses_of_many_tokens(lib, total):
     gr = W * 0.5 * (torch.where(over | under, 0.0, -r * A) - 0.05 * e) * m
     tol = W * 0.5 * ((r * A).abs() * (2 + y.abs()) * 2 * U + 0.05 * ((e + 1) * (2 + dd.abs()) * 2 * U + U)) + 4 * U * gr.abs()
     assert bool(((d.double() - gr).abs() <= tol + 1e-37).all())
+
+
+@pytest.mark.gpu
+def test_policy_kl_around_its_series(lib):
+    # e^d - 1 - d: a series below |d| = 0.5 (cut after d^9: the rest is below 2.5e-9 of the sum, at d = -0.5; 8
+    # roundings of its Horner steps and products), the difference above it.  There e^d is off by (2 + 1.25 |d|) u and
+    # its products, e^d - 1 by u of itself and the last difference by u of itself
+    d0 = np.array([-0.499, -0.5, -0.501, 0.499, 0.5, 0.501, 0.6, -0.6, 0.75, 1.0, -1.0, 2.0, -2.0, 6.0, -17.0], np.float32)
+    for x32 in d0:
+        L, R, A, C = _dev(np.zeros(1, np.float32), np.array([x32]), np.zeros(1, np.float32), np.array([0, 1], np.int64))
+        kl = float(lib.lora_policy_loss_fwd(L, C, A, ref_logp=R, beta=1.0)[0])
+        x = float(x32)
+        want = math.expm1(x) - x
+        if abs(x) < 0.5:
+            tol = 2.5e-9 * want + 10 * U * want
+        else:
+            tol = math.exp(x) * (2 + 1.25 * abs(x)) * U + abs(math.expm1(x)) * U + 2 * U * want
+        assert abs(kl - want) <= tol, (x, kl, want, abs(kl - want) / tol)
