@@ -547,6 +547,7 @@ class LoraLinearEpiFunction(torch.autograd.Function):
         Y, Z = lora_linear_epi_fwd(X, member, act, bias, residual, store_z=act != "none")
         ctx.save_for_backward(X, W, A, B, Z, W_t)
         ctx.scale, ctx.act = scale, act
+        ctx.shapes = [None if t is None else t.shape for t in (bias, residual)]
         return Y
 
     @staticmethod
@@ -569,7 +570,9 @@ class LoraLinearEpiFunction(torch.autograd.Function):
                                at + 4 * (na + nb) if need_dbias else None)
             dA, dB, *rest = g.to(A.dtype).split([na, nb] + ([d_out] if need_dbias else []))
             dA, dB, dbias = dA.view(r, d_in), dB.view(d_out, r), rest[0] if rest else None
-        return (dX, None, dA, dB, dbias, dY if ctx.needs_input_grad[5] else None, None, None, None)
+        bias, residual = ctx.shapes
+        return (dX, None, dA, dB, dbias.view(bias) if need_dbias else None,
+                dY.view(residual) if ctx.needs_input_grad[5] else None, None, None, None)
 
 
 class LoraLinearFunction(torch.autograd.Function):

@@ -644,3 +644,17 @@ def test_epilogue_adapter_gradient_past_32_bits(lib):
         mag += q.abs() @ x[at].abs()
     assert 0 < mag.max() < 2 ** 24
     assert torch.equal(dA.double(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_epilogue_function_gradients_have_their_inputs_shapes(lib, dtype):
+    X, m, bias, res, dY = _inputs(14, 20, 64, 72, 8, dtype)
+    out = []
+    for b, r in ((bias, res), (bias.view(1, 72), res.view(4, 5, 72)), (bias.view(72, 1), res.view(-1))):
+        leaves = [t.clone().requires_grad_() for t in (X, m["A"], m["B"], b, r)]
+        Y = lib.LoraLinearEpiFunction.apply(leaves[0], m["W"], *leaves[1:], m["scale"], "silu")
+        Y.backward(dY)
+        assert all(t.grad.shape == t.shape for t in leaves)
+        out.append([Y] + [t.grad.reshape(-1) for t in leaves])
+    assert all(torch.equal(a, b) for o in out[1:] for a, b in zip(out[0], o))
