@@ -571,8 +571,10 @@ class LoraLinearEpiFunction(torch.autograd.Function):
             dA, dB, *rest = g.to(A.dtype).split([na, nb] + ([d_out] if need_dbias else []))
             dA, dB, dbias = dA.view(r, d_in), dB.view(d_out, r), rest[0] if rest else None
         bias, residual = ctx.shapes
-        return (dX, None, dA, dB, dbias.view(bias) if need_dbias else None,
-                dY.view(residual) if ctx.needs_input_grad[5] else None, None, None, None)
+        dR = None
+        if ctx.needs_input_grad[5]:  # dY itself, or a copy: autograd would keep a view of it, the caller's memory
+            dR = dY if dY.shape == residual else dY.clone().view(residual)
+        return (dX, None, dA, dB, dbias.view(bias) if need_dbias else None, dR, None, None, None)
 
 
 class LoraLinearFunction(torch.autograd.Function):

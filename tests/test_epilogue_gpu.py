@@ -658,3 +658,15 @@ def test_epilogue_function_gradients_have_their_inputs_shapes(lib, dtype):
         assert all(t.grad.shape == t.shape for t in leaves)
         out.append([Y] + [t.grad.reshape(-1) for t in leaves])
     assert all(torch.equal(a, b) for o in out[1:] for a, b in zip(out[0], o))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(20, 72), (4, 5, 72)], ids=str)
+def test_epilogue_residual_gradient_is_not_the_callers(lib, shape):
+    # the residual's gradient is dY: what a step then does to residual.grad leaves the caller's dY as it was
+    X, m, bias, res, dY = _inputs(19, 20, 64, 72, 8, "f32")
+    r, keep = res.view(shape).requires_grad_(), dY.clone()
+    lib.LoraLinearEpiFunction.apply(X, m["W"], m["A"], m["B"], bias, r, m["scale"]).backward(dY)
+    assert torch.equal(r.grad.view(20, 72), dY)
+    r.grad.zero_()
+    assert torch.equal(dY, keep)
