@@ -517,24 +517,18 @@ def lora_linear_epi_bwd(X, member, dY, act: str = "none", Z=None, need_dX: bool 
 
 def _epi_bwd(dt, dev, M, d_in, d_out, r, m, X, dY, act, Z, need_dX, need_dbias, table16=None, ws=None):
     """lora_linear_epi_bwd of checked tensors."""
+    dX = torch.empty(M, d_in, dtype=X.dtype, device=dev) if need_dX else None
     dA = torch.empty(r, d_in, dtype=torch.float32, device=dev)
     dB = torch.empty(d_out, r, dtype=torch.float32, device=dev)
     dbias = torch.empty(d_out, dtype=torch.float32, device=dev) if need_dbias else None
-    dX = _epi_bwd_into(dt, dev, M, d_in, m, X, dY, act, Z, need_dX, L._ptr(dA), L._ptr(dB), L._ptr(dbias), table16, ws)
-    return dX, dA, dB, dbias
-
-
-def _epi_bwd_into(dt, dev, M, d_in, m, X, dY, act, Z, need_dX, dA, dB, dbias, table16=None, ws=None):
-    """dX, and the gradients at the addresses dA, dB and dbias."""
-    dX = torch.empty(M, d_in, dtype=X.dtype, device=dev) if need_dX else None
-    m.dY, m.dX, m.dA, m.dB = L._ptr(dY), L._ptr(dX), dA, dB
+    m.dY, m.dX, m.dA, m.dB = L._ptr(dY), L._ptr(dX), L._ptr(dA), L._ptr(dB)
     e = L.Epilogue(_choice("act", ACTIVATIONS, act), None, None, L._ptr(Z))
     tab = L._table_ptr(table16) if table16 is not None else None
     ws = _epi_ws(True, dt, M, d_in, m, e, dev, ws)
     with _on(dev):
         L._check("lora_linear_epi_bwd", L.lib().lora_linear_epi_bwd(
-            dt, M, d_in, m, e, L._ptr(X), tab, dbias, L._ptr(ws), ws.numel(), L._stream(dev)))
-    return dX
+            dt, M, d_in, m, e, L._ptr(X), tab, L._ptr(dbias), L._ptr(ws), ws.numel(), L._stream(dev)))
+    return dX, dA, dB, dbias
 
 
 class LoraLinearEpiFunction(torch.autograd.Function):
@@ -559,17 +553,10 @@ class LoraLinearEpiFunction(torch.autograd.Function):
         m = _epi_struct({"W": W, "A": A, "B": B, "scale": ctx.scale, "W_t": W_t}, r, d_out)
         _check(dev, "the gradient of Y", dY, (X.dtype,), M * d_out)
         dt, need_dX, need_dbias = L._dtype_code(X), ctx.needs_input_grad[0], ctx.needs_input_grad[4]
-        if A.dtype == torch.float32:
-            dX, dA, dB, dbias = _epi_bwd(dt, dev, M, d_in, d_out, r, m, X, dY, ctx.act, Z, need_dX, need_dbias)
-        else:
-            # the fp32 gradients side by side (each a multiple of 8 values), rounded by one launch instead of three
-            na, nb = r * d_in, d_out * r
-            g = torch.empty(na + nb + (d_out if need_dbias else 0), dtype=torch.float32, device=dev)
-            at = g.data_ptr()
-            dX = _epi_bwd_into(dt, dev, M, d_in, m, X, dY, ctx.act, Z, need_dX, at, at + 4 * na,
-                               at + 4 * (na + nb) if need_dbias else None)
-            dA, dB, *rest = g.to(A.dtype).split([na, nb] + ([d_out] if need_dbias else []))
-            dA, dB, dbias = dA.view(r, d_in), dB.view(d_out, r), rest[0] if rest else None
+        dX, dA, dB, dbias = _epi_bwd(dt, dev, M, d_in, d_out, r, m, X, dY, ctx.act, Z, need_dX, need_dbias)
+        dA, dB = dA.to(A.dtype), dB.to(B.dtype)  # (each gradient in a storage of its own)
+        if need_dbias:
+            dbias = dbias.to(X.dtype)
         bias, residual = ctx.shapes
         dR = None
         if ctx.needs_input_grad[5]:  # dY itself, or a copy: autograd would keep a view of it, the caller's memory

@@ -670,3 +670,18 @@ def test_epilogue_residual_gradient_is_not_the_callers(lib, shape):
     assert torch.equal(r.grad.view(20, 72), dY)
     r.grad.zero_()
     assert torch.equal(dY, keep)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_epilogue_function_gradients_own_their_storage(lib, dtype):
+    # one gradient's storage may be freed or resized without the others (sharded training does); and the rounded
+    # gradients are the fp32 ones, each rounded once
+    X, m, bias, res, dY = _inputs(15, 20, 64, 72, 8, dtype)
+    leaves = [t.clone().requires_grad_() for t in (X, m["A"], m["B"], bias, res)]
+    lib.LoraLinearEpiFunction.apply(leaves[0], m["W"], *leaves[1:], m["scale"]).backward(dY)
+    grads = [t.grad for t in leaves[:4]]
+    assert len({g.untyped_storage().data_ptr() for g in grads}) == 4
+    assert all(g.untyped_storage().nbytes() == g.numel() * g.element_size() for g in grads)
+    dX, dA, dB, db = lib.lora_linear_epi_bwd(X, m, dY, need_dbias=True)
+    assert all(torch.equal(g, w.to(X.dtype)) for g, w in zip(grads, (dX, dA, dB, db)))
