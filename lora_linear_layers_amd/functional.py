@@ -538,7 +538,9 @@ class LoraLinearEpiFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, W, A, B, bias, residual, scale, act="none", W_t=None):
         member = {"W": W, "A": A, "B": B, "scale": scale, "W_t": W_t}
-        Y, Z = lora_linear_epi_fwd(X, member, act, bias, residual, store_z=act != "none")
+        # (the residual's gradient alone needs no Z)
+        Y, Z = lora_linear_epi_fwd(X, member, act, bias, residual,
+                                   store_z=act != "none" and any(ctx.needs_input_grad[i] for i in (0, 2, 3, 4)))
         ctx.save_for_backward(X, W, A, B, Z, W_t)
         ctx.scale, ctx.act = scale, act
         ctx.shapes = [None if t is None else t.shape for t in (bias, residual)]
@@ -550,18 +552,21 @@ class LoraLinearEpiFunction(torch.autograd.Function):
         X, W, A, B, Z, W_t = ctx.saved_tensors
         dY = dY.contiguous()
         dev, (M, d_in), (d_out, r) = X.device, X.shape, B.shape
-        m = _epi_struct({"W": W, "A": A, "B": B, "scale": ctx.scale, "W_t": W_t}, r, d_out)
         _check(dev, "the gradient of Y", dY, (X.dtype,), M * d_out)
-        dt, need_dX, need_dbias = L._dtype_code(X), ctx.needs_input_grad[0], ctx.needs_input_grad[4]
-        dX, dA, dB, dbias = _epi_bwd(dt, dev, M, d_in, d_out, r, m, X, dY, ctx.act, Z, need_dX, need_dbias)
-        dA, dB = dA.to(A.dtype), dB.to(B.dtype)  # (each gradient in a storage of its own)
-        if need_dbias:
-            dbias = dbias.to(X.dtype)
         bias, residual = ctx.shapes
-        dR = None
-        if ctx.needs_input_grad[5]:  # dY itself, or a copy: autograd would keep a view of it, the caller's memory
+        need_dX, _, need_dA, need_dB, need_dbias, need_dR = ctx.needs_input_grad[:6]
+        dX = dA = dB = dbias = dR = None
+        if need_dX or need_dA or need_dB or need_dbias:
+            m = _epi_struct({"W": W, "A": A, "B": B, "scale": ctx.scale, "W_t": W_t}, r, d_out)
+            dX, dA, dB, dbias = _epi_bwd(L._dtype_code(X), dev, M, d_in, d_out, r, m, X, dY, ctx.act, Z, need_dX,
+                                         need_dbias)
+            # (each gradient in a storage of its own)
+            dA = dA.to(A.dtype) if need_dA else None
+            dB = dB.to(B.dtype) if need_dB else None
+            dbias = dbias.to(X.dtype).view(bias) if need_dbias else None
+        if need_dR:  # dY itself, or a copy: autograd would keep a view of it, the caller's memory
             dR = dY if dY.shape == residual else dY.clone().view(residual)
-        return (dX, None, dA, dB, dbias.view(bias) if need_dbias else None, dR, None, None, None)
+        return (dX, None, dA, dB, dbias, dR, None, None, None)
 
 
 class LoraLinearFunction(torch.autograd.Function):

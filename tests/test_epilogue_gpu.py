@@ -685,3 +685,25 @@ def test_epilogue_function_gradients_own_their_storage(lib, dtype):
     assert all(g.untyped_storage().nbytes() == g.numel() * g.element_size() for g in grads)
     dX, dA, dB, db = lib.lora_linear_epi_bwd(X, m, dY, need_dbias=True)
     assert all(torch.equal(g, w.to(X.dtype)) for g, w in zip(grads, (dX, dA, dB, db)))
+
+
+@pytest.mark.gpu
+def test_epilogue_function_does_only_what_is_asked_for(lib, monkeypatch):
+    from lora_linear_layers_amd import functional as F
+
+    X, m, bias, res, dY = _inputs(16, 20, 64, 72, 8, "bf16")
+    kept, ran = [], []
+    fwd, bwd = F.lora_linear_epi_fwd, F._epi_bwd
+    monkeypatch.setattr(F, "lora_linear_epi_fwd", lambda *a, **k: (kept.append(k["store_z"]), fwd(*a, **k))[1])
+    monkeypatch.setattr(F, "_epi_bwd", lambda *a, **k: (ran.append(1), bwd(*a, **k))[1])
+    base = (X, m["A"], m["B"], bias, res)
+    for need in ((), (4,), (0,), (1,), (3,), (0, 1, 2, 3, 4)):
+        leaves = [t.clone().requires_grad_(i in need) for i, t in enumerate(base)]
+        Y = lib.LoraLinearEpiFunction.apply(leaves[0], m["W"], *leaves[1:], m["scale"], "silu")
+        if need:
+            Y.backward(dY)
+        assert kept.pop() == bool(set(need) - {4}) and len(ran) == (1 if set(need) - {4} else 0)
+        ran.clear()
+        assert [t.grad is not None for t in leaves] == [i in need for i in range(5)]
+        if 4 in need:
+            assert torch.equal(leaves[4].grad, dY)
