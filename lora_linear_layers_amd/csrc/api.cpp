@@ -1710,16 +1710,22 @@ EpiLayout make_epi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, const lo
   return E;
 }
 
-int check_epi(bool bwd, int dtype, int64_t M, int64_t d_in, const lora_group_member* m, const lora_epilogue* e,
-              const void* X, const float* table16) {
+// What both the calls and their sizing read.
+int check_epi_sizes(int dtype, int64_t M, int64_t d_in, const lora_group_member* m, const lora_epilogue* e) {
   if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_ERR_DTYPE;
   if (!m || !e) return LORA_ERR_NULL;
   TRY(check_sizes(M, d_in, m->d_out, m->r));
   if (m->rope || e->act < LORA_ACT_NONE || e->act > LORA_ACT_GELU_TANH || m->d_out > LORA_EPI_MAX_D_OUT)
     return LORA_ERR_SHAPE;
+  if (m->W_nf4 && dtype != LORA_BF16) return LORA_ERR_DTYPE;
+  return m->W_nf4 && d_in % 64 ? LORA_ERR_SHAPE : LORA_OK;
+}
+
+int check_epi(bool bwd, int dtype, int64_t M, int64_t d_in, const lora_group_member* m, const lora_epilogue* e,
+              const void* X, const float* table16) {
+  TRY(check_epi_sizes(dtype, M, d_in, m, e));
   TRY(check_ptrs({m->A, m->B}));
   if (m->W_nf4) {
-    if (dtype != LORA_BF16) return LORA_ERR_DTYPE;
     TRY(check_nf4(d_in, 64, m->W_nf4, m->absmax, table16));
   } else {
     TRY(check_ptrs({m->W}));
@@ -2122,8 +2128,7 @@ int lora_swiglu_bwd(int dtype, int64_t M, int64_t d_in, const lora_group_member*
 
 size_t lora_linear_epi_workspace_bytes(int backward, int dtype, int64_t M, int64_t d_in,
                                        const lora_group_member* member, const lora_epilogue* epilogue) {
-  if (dtype != LORA_F32 && dtype != LORA_BF16) return 0;
-  if (!member || !epilogue || check_sizes(M, d_in, member->d_out, member->r) != LORA_OK) return 0;
+  if (check_epi_sizes(dtype, M, d_in, member, epilogue) != LORA_OK) return 0;
   return make_epi_layout(backward != 0, dtype, M, d_in, *member, *epilogue).total;
 }
 

@@ -707,3 +707,20 @@ def test_epilogue_function_does_only_what_is_asked_for(lib, monkeypatch):
         assert [t.grad is not None for t in leaves] == [i in need for i in range(5)]
         if 4 in need:
             assert torch.equal(leaves[4].grad, dY)
+
+
+def test_epilogue_sizing_refuses_what_the_calls_refuse():
+    import lora_linear_layers_amd as L
+    from lora_linear_layers_amd import _lib
+
+    size, P = L.lib().lora_linear_epi_workspace_bytes, 0x100000
+
+    def n(bwd, dtype=1, M=1000, k=512, d_out=768, r=16, rope=0, nf4=None, act=2):
+        return size(bwd, dtype, M, k, _lib.GroupMember(d_out, r, 1.0, rope, None if nf4 else P, nf4),
+                    _lib.Epilogue(act))
+
+    for b in (0, 1):
+        assert n(b) > 0 and n(b, nf4=P) > 0
+        assert n(b, act=5) == 0 and n(b, act=-1) == 0 and n(b, rope=1) == 0 and n(b, d_out=2 ** 20 + 8) == 0
+        assert n(b, nf4=P, dtype=0) == 0 and n(b, nf4=P, k=520) == 0
+        assert n(b, r=0) == 0 and n(b, M=-1) == 0
