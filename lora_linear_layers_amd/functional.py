@@ -469,10 +469,11 @@ def _epi_struct(member, r, d_out):
 
 
 def _epi_ws(backward, dt, M, d_in, m, e, device, ws):
+    """(workspace, its bytes)"""
     if ws is not None:
-        return _check_ws(device, ws)
+        return _check_ws(device, ws), ws.numel() * ws.element_size()
     n = int(L.lib().lora_linear_epi_workspace_bytes(int(backward), dt, M, d_in, m, e))
-    return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=device), n
 
 
 def lora_linear_epi_fwd(X, member, act: str = "none", bias=None, residual=None, table16=None, Y=None,
@@ -495,10 +496,10 @@ def lora_linear_epi_fwd(X, member, act: str = "none", bias=None, residual=None, 
     m.Y = L._ptr(Y)
     e = L.Epilogue(_choice("act", ACTIVATIONS, act), L._ptr(bias), L._ptr(residual), L._ptr(Z))
     tab = L._table_ptr(table16) if table16 is not None else None
-    ws = _epi_ws(False, dt, M, d_in, m, e, dev, ws)
+    ws, ws_bytes = _epi_ws(False, dt, M, d_in, m, e, dev, ws)
     with _on(dev):
         L._check("lora_linear_epi_fwd", L.lib().lora_linear_epi_fwd(
-            dt, M, d_in, m, e, L._ptr(X), tab, L._ptr(ws), ws.numel(), L._stream(dev)))
+            dt, M, d_in, m, e, L._ptr(X), tab, L._ptr(ws), ws_bytes, L._stream(dev)))
     return Y, Z
 
 
@@ -524,10 +525,10 @@ def _epi_bwd(dt, dev, M, d_in, d_out, r, m, X, dY, act, Z, need_dX, need_dbias, 
     m.dY, m.dX, m.dA, m.dB = L._ptr(dY), L._ptr(dX), L._ptr(dA), L._ptr(dB)
     e = L.Epilogue(_choice("act", ACTIVATIONS, act), None, None, L._ptr(Z))
     tab = L._table_ptr(table16) if table16 is not None else None
-    ws = _epi_ws(True, dt, M, d_in, m, e, dev, ws)
+    ws, ws_bytes = _epi_ws(True, dt, M, d_in, m, e, dev, ws)
     with _on(dev):
         L._check("lora_linear_epi_bwd", L.lib().lora_linear_epi_bwd(
-            dt, M, d_in, m, e, L._ptr(X), tab, L._ptr(dbias), L._ptr(ws), ws.numel(), L._stream(dev)))
+            dt, M, d_in, m, e, L._ptr(X), tab, L._ptr(dbias), L._ptr(ws), ws_bytes, L._stream(dev)))
     return dX, dA, dB, dbias
 
 

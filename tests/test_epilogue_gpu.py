@@ -724,3 +724,22 @@ def test_epilogue_sizing_refuses_what_the_calls_refuse():
         assert n(b, act=5) == 0 and n(b, act=-1) == 0 and n(b, rope=1) == 0 and n(b, d_out=2 ** 20 + 8) == 0
         assert n(b, nf4=P, dtype=0) == 0 and n(b, nf4=P, k=520) == 0
         assert n(b, r=0) == 0 and n(b, M=-1) == 0
+
+
+@pytest.mark.gpu
+def test_epilogue_workspaces_are_measured_in_bytes(lib):
+    from lora_linear_layers_amd import _lib
+
+    X, m, bias, _, dY = _inputs(17, 300, 264, 392, 16, "bf16")
+    mem = _lib.GroupMember(392, 16, 1.0, 0, 1)
+    size = [lib.lib().lora_linear_epi_workspace_bytes(b, 1, 300, 264, mem, _lib.Epilogue()) for b in (0, 1)]
+    assert all(n and n % 4 == 0 for n in size)
+    ws = [torch.empty(n // 4, device="cuda") for n in size]
+    Y, _ = lib.lora_linear_epi_fwd(X, m, "none", bias, ws=ws[0])
+    assert torch.equal(Y, lib.lora_linear_epi_fwd(X, m, "none", bias)[0])
+    got, want = lib.lora_linear_epi_bwd(X, m, dY, ws=ws[1]), lib.lora_linear_epi_bwd(X, m, dY)
+    assert all(torch.equal(a, b) for a, b in zip(got[:3], want[:3]))
+    for call in (lambda: lib.lora_linear_epi_fwd(X, m, "none", bias, ws=ws[0][:-1]),
+                 lambda: lib.lora_linear_epi_bwd(X, m, dY, ws=ws[1][:-1])):
+        with pytest.raises(RuntimeError):
+            call()
