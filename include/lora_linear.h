@@ -431,8 +431,8 @@ size_t lora_swiglu_workspace_bytes(int backward, int dtype, int64_t M, int64_t d
  *     dbias = sum over tokens of dZ,
  * and dX (NULL: skipped), dA, dB from dZ as lora_linear_bwd; the residual's
  * gradient is dY.  act and Z are taken from `epilogue` (its bias and residual
- * are not used).  RELU passes no gradient at 0.  dbias: fp32 [d_out]
- * (overwritten) or NULL.
+ * are not used).  RELU passes no gradient at 0 and below, whatever dY holds
+ * there.  dbias: fp32 [d_out] (overwritten) or NULL.
  */
 #define LORA_EPI_MAX_D_OUT (1 << 20)
 enum { LORA_ACT_NONE = 0, LORA_ACT_RELU = 1, LORA_ACT_SILU = 2, LORA_ACT_GELU = 3, LORA_ACT_GELU_TANH = 4 };

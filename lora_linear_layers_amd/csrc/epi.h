@@ -86,7 +86,6 @@ __device__ __forceinline__ float act_fwd(float z, int act) {
 template <bool FAST>
 __device__ __forceinline__ float act_grad(float z, int act) {
   switch (act) {
-    case ACT_RELU: return z > 0.f ? 1.f : 0.f;
     case ACT_SILU: {
       const float s = sigmoid<FAST>(z);
       return s * (1.f + z * (1.f - s));
@@ -128,13 +127,14 @@ __device__ __forceinline__ void act_all(float (&v)[N], int act) {
   }
 }
 
-// g *= act'(z)
+// g *= act'(z); what relu stops stays out whatever it is (an infinity times 0 is
+// no gradient)
 template <bool FAST, int N>
 __device__ __forceinline__ void act_grad_all(float (&g)[N], const float (&z)[N], int act) {
   switch (act) {
     case ACT_RELU:
 #pragma unroll
-      for (int e = 0; e < N; ++e) g[e] *= act_grad<FAST>(z[e], ACT_RELU);
+      for (int e = 0; e < N; ++e) g[e] = z[e] > 0.f ? g[e] : 0.f;
       break;
     case ACT_SILU:
 #pragma unroll

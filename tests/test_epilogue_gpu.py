@@ -743,3 +743,20 @@ def test_epilogue_workspaces_are_measured_in_bytes(lib):
                  lambda: lib.lora_linear_epi_bwd(X, m, dY, ws=ws[1][:-1])):
         with pytest.raises(RuntimeError):
             call()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_epilogue_relu_passes_no_gradient_below_zero(lib, dtype):
+    # not even an infinite one or a NaN: those where Z <= 0 leave every gradient as zeros there do
+    X, m, _, _, dY = _inputs(18, 40, 64, 72, 8, dtype)
+    Z = dY.flip(0).contiguous()
+    Z[3, 5] = 0.0
+    off = Z <= 0
+    assert off[3, 5] and off.sum() > 100
+    bad = dY.clone()
+    bad[off] = torch.tensor([float("inf"), -float("inf"), float("nan")], device="cuda").repeat(int(off.sum()))[:int(off.sum())].to(dY.dtype)
+    zero = dY.masked_fill(off, 0.0)
+    got = lib.lora_linear_epi_bwd(X, m, bad, "relu", Z, need_dbias=True)
+    want = lib.lora_linear_epi_bwd(X, m, zero, "relu", Z, need_dbias=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and got[0].isfinite().all()
