@@ -471,7 +471,7 @@ def _epi_struct(member, r, d_out):
 def _epi_ws(backward, dt, M, d_in, m, e, device, ws):
     """(workspace, its bytes)"""
     if ws is not None:
-        return _check_ws(device, ws), ws.numel() * ws.element_size()
+        return _check_ws(device, ws, ws.nbytes), ws.nbytes
     n = int(L.lib().lora_linear_epi_workspace_bytes(int(backward), dt, M, d_in, m, e))
     return torch.empty(max(n, 1), dtype=torch.uint8, device=device), n
 
@@ -622,9 +622,13 @@ def _check(device, name, t, dtypes, numel=None):
         raise ValueError(f"{name} has {t.numel()} values, not {numel}")
 
 
-def _check_ws(device, ws):
-    """A caller's workspace, on the device (the library checks its size)."""
-    _check(device, "ws", ws, (ws.dtype,))
+def _check_ws(device, ws, nbytes=None):
+    """A caller's workspace: on the device or pinned, with nbytes (its elements' number by default) behind its first
+    element, however it is laid out.  The library is told that size and checks it."""
+    if ws.device != device and not ws.is_pinned():
+        raise ValueError(f"ws is on {ws.device}, not on {device}")
+    if ws.untyped_storage().nbytes() - ws.storage_offset() * ws.element_size() < (ws.numel() if nbytes is None else nbytes):
+        raise ValueError("ws holds fewer bytes than it has elements")
     return ws
 
 
@@ -686,7 +690,7 @@ def lora_token_logp_bwd(logits, targets, stats, dlogp, inv_temp: float = 1.0, dl
 def _loss_ws(loss, n_seq, n_tokens, logp, ws):
     """(workspace, its bytes)"""
     if ws is not None:
-        return _check_ws(logp.device, ws), ws.numel() * ws.element_size()
+        return _check_ws(logp.device, ws, ws.nbytes), ws.nbytes
     nbytes = L.lib().lora_loss_workspace_bytes(loss, n_seq, n_tokens)
     return logp.new_empty(nbytes // 4), nbytes
 

@@ -760,3 +760,19 @@ def test_epilogue_relu_passes_no_gradient_below_zero(lib, dtype):
     got = lib.lora_linear_epi_bwd(X, m, bad, "relu", Z, need_dbias=True)
     want = lib.lora_linear_epi_bwd(X, m, zero, "relu", Z, need_dbias=True)
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and got[0].isfinite().all()
+
+
+def test_workspaces_of_groups_and_pairs_are_taken_as_before():
+    # a workspace given to the group and SwiGLU calls: any memory that the device reaches, of at least as many bytes
+    # from its first element on as it has elements (which is the size that the library is told)
+    from lora_linear_layers_amd import functional as F
+
+    here, buf = torch.device("cpu"), torch.empty(4096, dtype=torch.uint8)
+    for f in (F._group_ws, F._swiglu_ws):
+        for ws in (buf, buf[::2], buf.view(64, 64).t(), buf.view(torch.float32), buf[16:1040]):
+            assert f(False, 1, 8, 64, None, here, ws) is ws
+        for ws in (torch.empty(1, dtype=torch.uint8).expand(4096), buf[-64:].as_strided((65,), (0,))):
+            with pytest.raises(ValueError, match="fewer bytes"):
+                f(False, 1, 8, 64, None, here, ws)
+        with pytest.raises(ValueError, match="ws is on cpu"):
+            f(False, 1, 8, 64, None, torch.device("cuda:0"), buf)
