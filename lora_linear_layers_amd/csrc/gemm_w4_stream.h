@@ -50,7 +50,6 @@ gemm_w4_stream_kernel(const GemmArgs p) {
   constexpr int BKS = w4nt::BK;
   static_assert(EPI == EPI_ACT, "the epilogue of epi.h");
   __shared__ __attribute__((aligned(1024))) char smem[w4nt::LDS];
-  int* last = reinterpret_cast<int*>(smem);  // (between a tile's last reads of the ring and the next use)
   // keep the MFMA accumulators in the accumulation registers
   asm volatile("" ::: "a0");
 
