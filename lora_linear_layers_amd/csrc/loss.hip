@@ -82,12 +82,12 @@ struct Row<float> {
 // apart (the log-sum-exp, or 1 + r, would round away what a confident row's small
 // log-probability is made of).
 // Bound by reading the logits and, not far behind, by the instructions: 8192 x
-// 128000 bf16 in 353 us, 5.9 TB/s (a large copy moves 5.2 TB/s, read and
+// 128000 bf16 in 354 us, 5.9 TB/s (a large copy moves 5.2 TB/s, read and
 // written; with the sum in one number and its digits lost, 337 us); the
 // exponential, a quarter-rate instruction, would take 0.11 ms of it.  More than 64
 // registers a thread would leave one block of 1024 a CU (432 us).  The gradient
 // reads and writes them once: 656 us behind the forward, 6.4 TB/s.  24 x 32000:
-// 7.1 us, a launch, one round of loads and the joins.
+// 6.7 us, a launch, one round of loads and the joins.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float fexp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -195,10 +195,15 @@ __global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8, 8)))
         red[1][tid >> 6] = r;
       }
       __syncthreads();
-      m = red[0][0];
-      r = red[1][0];
+      if (tid < 64) {  // (the first wave alone: by every thread it would be a fifth of the row's instructions)
+        m = tid < NT / 64 ? red[0][tid] : -INFINITY;
+        r = tid < NT / 64 ? red[1][tid] : 0.f;
 #pragma unroll
-      for (int w = 1; w < NT / 64; ++w) join_max_rest(m, r, red[0][w], red[1][w], c);
+        for (int o = NT / 128; o > 0; o >>= 1) {
+          const float m2 = __shfl_xor(m, o), r2 = __shfl_xor(r, o);
+          join_max_rest(m, r, m2, r2, c);
+        }
+      }
     }
     if (tid == 0) {
       const float ls = m == -INFINITY ? logf(r) : log1pf(r);
