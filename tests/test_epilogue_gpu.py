@@ -776,3 +776,68 @@ def test_workspaces_of_groups_and_pairs_are_taken_as_before():
                 f(False, 1, 8, 64, None, here, ws)
         with pytest.raises(ValueError, match="ws is on cpu"):
             f(False, 1, 8, 64, None, torch.device("cuda:0"), buf)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [("bf16", 1, 4096, 1024, 16), ("bf16", 33, 256, 512, 64), ("bf16", 300, 264, 392, 16),
+                                  ("bf16", 2048, 3200, 2056, 24), ("bf16", 2048, 14400, 2048, 24), ("f32", 128, 256, 256, 8),
+                                  ("f32", 107, 4352, 384, 32), ("nf4", 128, 256, 256, 64), ("nf4", 640, 4096, 512, 8)], ids=str)
+def test_epilogue_backward_without_the_inputs_gradient(lib, case):
+    # a first layer's step: no dX, on every path that has one with it
+    kind, M, k, d, r = case
+    table = None
+    if kind == "nf4":
+        X, m, _, _, dY, table = _nf4(60 + M, k, d, r, M)
+    else:
+        X, m, _, _, dY = _inputs(60 + M, M, k, d, r, kind)
+    Z = torch.randn(M, d, generator=torch.Generator().manual_seed(5)).to(X.dtype).cuda()
+
+    class NoDX:
+        nf4_dequant = staticmethod(lib.nf4_dequant)
+
+        @staticmethod
+        def lora_linear_epi_bwd(*a, **kw):
+            none, *grads = lib.lora_linear_epi_bwd(*a, need_dX=False, **kw)
+            assert none is None
+            return (lib.lora_linear_epi_bwd(*a, **kw)[0], *grads)
+
+    check_bwd(NoDX, X, m, dY, "silu", Z, table)
+
+
+@pytest.mark.gpu
+def test_whole_step_captured_and_replayed(lib):
+    # epilogue layer, head, log-probabilities and policy loss with every gradient, captured once (no eager graph of the
+    # leaves alive then) and replayed on new inputs with eager work between the replays
+    d, V, n, r = 128, 520, 96, 8
+    X, up, bias, res, _ = _inputs(1, n, d, d, r, "bf16")
+    _, head, _, _, _ = _inputs(2, n, d, V, r, "bf16")
+    gen = torch.Generator().manual_seed(4)
+    t = torch.randint(0, V, (n,), generator=gen).cuda()
+    cu = torch.tensor([0, 40, 40, 96], device="cuda")
+    adv, old = torch.tensor([0.8, -0.5, 1.0], device="cuda"), (-6 + torch.randn(n, generator=gen)).cuda()
+    leaves = [v.clone().requires_grad_() for v in (X, up["A"], up["B"], bias, res, head["A"], head["B"])]
+
+    def step():
+        x, a, b, bi, rs, ha, hb = leaves
+        y = lib.LoraLinearEpiFunction.apply(x, up["W"], a, b, bi, rs, up["scale"], "silu")
+        lp = lib.LoraHeadLogpFunction.apply(y, head["W"], ha, hb, head["scale"], t)
+        loss, _ = lib.LoraPolicyLossFunction.apply(lp, old, old, cu, adv, None, 0.2, 0.2, 0.05)
+        return [loss.detach(), *torch.autograd.grad(loss, leaves)]
+
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(st)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for _ in range(3):
+        with torch.no_grad():
+            leaves[0].copy_(torch.roll(leaves[0], 1, 0))
+            old.add_(0.05)
+        want = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, held))
