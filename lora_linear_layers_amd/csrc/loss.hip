@@ -82,12 +82,13 @@ struct Row<float> {
 // apart (the log-sum-exp, or 1 + r, would round away what a confident row's small
 // log-probability is made of).
 // Bound by reading the logits and, not far behind, by the instructions: 8192 x
-// 128000 bf16 in 354 us, 5.9 TB/s (a large copy moves 5.2 TB/s, read and
-// written; with the sum in one number and its digits lost, 337 us); the
+// 128000 bf16 in 333 us, 6.3 TB/s (a large copy moves 5.2 TB/s, read and
+// written; with the sum in one number and its digits lost, 328 us); the
 // exponential, a quarter-rate instruction, would take 0.11 ms of it.  More than 64
 // registers a thread would leave one block of 1024 a CU (432 us).  The gradient
-// reads and writes them once: 656 us behind the forward, 6.4 TB/s.  24 x 32000:
-// 6.7 us, a launch, one round of loads and the joins.
+// reads and writes them once: 671 us behind the forward, 6.2 TB/s.  24 x 32000:
+// 6.6 us, a launch, one round of loads and the joins.  (Medians of calls 100 to
+// 200 of a loop.)
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float fexp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(GRAD_NT) token_logp_grad_kernel(const T* z, in
     const int head = row_head(zr), nv = (V - head) / E;
     const bool zero = g == 0.f;
     const float m = stats[2 * row], ls = stats[2 * row + 1], ls2 = ls * LOG2E, c = tau * LOG2E;
-    auto grad = [&](float x) { return -g * fexp2((x - m) * c - ls2); };
+    auto grad = [&](float x, int64_t j) { return (j == t ? g : 0.f) - g * fexp2((x - m) * c - ls2); };
     // the target's own: g (1 - p), from p = 1/2 on with 1 - p as -(e^logp - 1),
     // which keeps its digits where p is near 1
     auto grad_t = [&](float x) {
@@ -250,10 +251,6 @@ __global__ void __launch_bounds__(GRAD_NT) token_logp_grad_kernel(const T* z, in
       return p < 0.5f ? g - g * p : -g * expm1f((x - m) * tau - ls);
     };
     const int i0 = seg * (U * NT) + threadIdx.x;
-    // the thread whose vectors hold the target (dz may be z: its logit is read before any of them is written)
-    const int vt = (int)t - head < 0 ? -1 : ((int)t - head) / E, dt = vt - i0;
-    const bool owner = !zero && vt >= 0 && vt < nv && dt >= 0 && dt < U * NT && dt % NT == 0;
-    const float zt = owner ? R::at(zr + t) : 0.f;
     u32x4 v[U];
     if (!zero) {
 #pragma unroll
@@ -275,7 +272,7 @@ __global__ void __launch_bounds__(GRAD_NT) token_logp_grad_kernel(const T* z, in
         float x[E];
         R::unpack(v[u], x);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = grad(x[e]);
+        for (int e = 0; e < E; ++e) x[e] = grad(x[e], j + e);
         o = R::pack(x);
       }
       if constexpr (STREAM)
@@ -283,14 +280,27 @@ __global__ void __launch_bounds__(GRAD_NT) token_logp_grad_kernel(const T* z, in
       else
         *reinterpret_cast<typename R::V*>(dr + j) = o;
     }
-    if (owner) R::put(dr + t, grad_t(zt));
+    // the target's element again, by the thread whose vector holds it (in place
+    // of the compare above, or with the loads unconditional, the pass over 8192 x
+    // 128000 takes 687 us instead of 671)
+    const int vt = (int)t - head < 0 ? nv : ((int)t - head) / E, dt = vt - i0;
+    if (!zero && vt < nv && dt >= 0 && dt < U * NT && dt % NT == 0) {
+      u32x4 w = v[0];
+#pragma unroll
+      for (int u = 1; u < U; ++u) w = dt == u * NT ? v[u] : w;
+      float x[E], xt = 0.f;
+      R::unpack(w, x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) xt = head + vt * E + e == (int)t ? x[e] : xt;
+      R::put(dr + t, grad_t(xt));
+    }
     // the elements before and behind the vectors (at most E): the last
     // segment's first threads
     const int rest = V - head - nv * E;
     if (seg == segs - 1 && (int)threadIdx.x < rest + head) {
       const int64_t j = (int)threadIdx.x < rest ? head + (int64_t)nv * E + threadIdx.x : 0;
       const float x = zero ? 0.f : R::at(zr + j);
-      R::put(dr + j, zero ? 0.f : (j == t ? grad_t(x) : grad(x)));
+      R::put(dr + j, zero ? 0.f : (j == t ? grad_t(x) : grad(x, j)));
     }
   }
 }
