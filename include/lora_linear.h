@@ -476,7 +476,8 @@ int lora_transpose(const void* src, int64_t rows, int64_t cols, void* dst, void*
  * -infinities, a +infinity or a NaN gives a NaN.  The backward writes
  * dlogits [n, vocab] (row stride ld_d) in the dtype; it may be logits itself
  * (ld_d = ld).  A row whose dlogp is 0, or whose target names no token, is not
- * read and gets zeros.  Arithmetic is fp32.  Pointers need their element's
+ * read and gets zeros.  Arithmetic is fp32; a logp near 0 and 1 - p of such a
+ * target keep their relative accuracy.  Pointers need their element's
  * alignment only, so rows may be sliced (logits[:-1], targets[1:]).
  * 0 <= n < 2^31, 1 <= vocab < 2^31.
  */

@@ -27,8 +27,8 @@
 // What it measures (MI355X, r = 16 to 64, bias / SiLU / residual): a tile alone
 // on its CU costs 18.5 us (launch, first stages, epilogue) and 1.1 to 1.5 us a
 // 64-deep stage, with 128 to 256 CUs at work; two blocks a tile 37 us and 0.66 us
-// a stage.  2049 x 4104 over 4096 (153 tiles): 86 us, 34 % of the chip's MFMA
-// cycles, 60 % of its CUs; 2048 x 4096 over 4096 (128 tiles in two): 76 us, 39 %;
+// a stage.  2049 x 4104 over 4096 (153 tiles): 86 us (91 in a sustained loop, 101
+// in its first calls), 34 % of the chip's MFMA cycles, 60 % of its CUs; 2048 x 4096 over 4096 (128 tiles in two): 76 us, 39 %;
 // over 14336: 197 us.  What bounds it: the CUs without a tile, then the fixed
 // part; contiguous ranges that span tiles (three slots of 256 KB to read back
 // for some) and no stagger between the parts measured slower (137 and 85 us
