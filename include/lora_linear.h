@@ -462,6 +462,65 @@ size_t lora_linear_epi_workspace_bytes(int backward, int dtype, int64_t M, int64
 int lora_transpose(const void* src, int64_t rows, int64_t cols, void* dst, void* stream);
 
 /*
+ * Root-mean-square norm in front of a block's projections, with the residual
+ * stream's addition:
+ *     h = x + residual (rounded to the type; x itself without a residual)
+ *     rstd = 1 / sqrt(mean of h^2 over the row + eps),   y = h rstd w
+ * X [M, d] (row stride ldx >= d elements), residual [M, d] (row stride ldr, or
+ * NULL) and weight [d] of the dtype.  Outputs, each of them optional (NULL; one
+ * at least): H [M, d] = h, Y [M, d] = y, rstd fp32 [M], and codes [M, d] with
+ * scale8 [M]: y as lora_act8_pack keeps it, rounded once (from y before its
+ * rounding to the dtype).  H may be X or the residual (the stream updated in
+ * place), Y may be X without a residual; with row strides of d.  Sums are fp32:
+ * a row whose sum of squares passes fp32's range gives zeros.  Pointers need their
+ * element's alignment only.  1 <= d <= LORA_NORM_MAX_DIM, 0 <= M < 2^31, eps >= 0
+ * (a row of zeros with eps 0 gives NaN).
+ *
+ * Backward, for dY [M, d] and, where the stream goes on, dH [M, d] (NULL: 0),
+ * from H and rstd as the forward gave them:
+ *     g = dY w,  xh = h rstd,  dX = rstd (g - xh mean(g xh)) + dH,
+ *     dweight = sum over rows of dY xh
+ * dX is the gradient of x and of the residual.  dX [M, d] may be NULL, or dY or
+ * dH itself; dweight [d] of dweight_dtype may be NULL (then no workspace is
+ * needed).  Rows are summed in fp32 in a fixed order.  M = 0: dweight is zeros.
+ */
+#define LORA_NORM_MAX_DIM 32768
+int lora_rmsnorm_fwd(int dtype, int64_t M, int64_t d, float eps, const void* X, int64_t ldx, const void* residual,
+                     int64_t ldr, const void* weight, void* H, void* Y, uint8_t* codes, float* scale8, float* rstd,
+                     void* stream);
+int lora_rmsnorm_bwd(int dtype, int64_t M, int64_t d, const void* H, const void* weight, const float* rstd,
+                     const void* dY, const void* dH, void* dX, void* dweight, int dweight_dtype, void* ws,
+                     size_t ws_bytes, void* stream);
+size_t lora_rmsnorm_workspace_bytes(int64_t M, int64_t d);
+
+/*
+ * Activations kept in 8 bits between a forward and its backward (page
+ * "Unsloth教程：本地微调大模型速度提升数倍，显存节省60%", section 显存优化策略).  Row t
+ * of X [M, d] (row stride ldx) is codes [M, d], e4m3 (OCP: 4 exponent and 3
+ * mantissa bits, largest 448), times scale8[t] = 2^e with the smallest
+ * e >= -126 that keeps the row's largest finite magnitude at or below 448 (1
+ * for a row of zeros):
+ *     code = e4m3(x 2^-e), rounded to nearest even;   x is taken as code 2^e.
+ * A value is off by at most 2^-4 of itself, or 2^(e - 10) where it is below
+ * 2^(e - 6).  Infinities and NaNs become NaN codes.  lora_act8_unpack
+ * writes code 2^e, a number of either type, [M, d].
+ *
+ * lora_act8_linear_bwd is the backward of lora_linear_fwd (and of its NF4 form)
+ * with the checkpoint in X's place: of the three gradients only the
+ * adapter's read X, through X A^T and (dY B)^T X.  member as in
+ * lora_linear_epi_bwd (W, or W_nf4 with absmax and the HOST table16; W_t; dY, dX
+ * or NULL, dA, dB); codes 16-byte aligned; its own sizing call;
+ * d_in <= LORA_NORM_MAX_DIM.  dX does not depend on X.
+ */
+int lora_act8_pack(int dtype, int64_t M, int64_t d, const void* X, int64_t ldx, uint8_t* codes, float* scale8,
+                   void* stream);
+int lora_act8_unpack(int dtype, int64_t M, int64_t d, const uint8_t* codes, const float* scale8, void* X,
+                     void* stream);
+int lora_act8_linear_bwd(int dtype, int64_t M, int64_t d_in, const lora_group_member* member, const uint8_t* codes,
+                         const float* scale8, const float* table16, void* ws, size_t ws_bytes, void* stream);
+size_t lora_act8_linear_workspace_bytes(int dtype, int64_t M, int64_t d_in, const lora_group_member* member);
+
+/*
  * Log-probabilities of tokens from their logits (the head projection of a
  * training step: preference and policy losses read them, and their gradient
  * goes back through the head's LoRA layer).  For row i with target t_i:

@@ -90,6 +90,13 @@ _SIGS = {
     "lora_policy_loss_fwd": ([_int, _i64, _i64, _dbl, _dbl, _dbl, _dbl] + [_vp] * 6 + [_int] + [_vp] * 4 + [_sz, _vp],
                              _int),
     "lora_policy_loss_bwd": ([_i64, _i64, _dbl, _dbl, _dbl] + [_vp] * 6 + [_int] + [_vp] * 4, _int),
+    "lora_rmsnorm_fwd": ([_int, _i64, _i64, _f32, _vp, _i64, _vp, _i64] + [_vp] * 7, _int),
+    "lora_rmsnorm_bwd": ([_int, _i64, _i64] + [_vp] * 7 + [_int, _vp, _sz, _vp], _int),
+    "lora_rmsnorm_workspace_bytes": ([_i64, _i64], _sz),
+    "lora_act8_pack": ([_int, _i64, _i64, _vp, _i64, _vp, _vp, _vp], _int),
+    "lora_act8_unpack": ([_int, _i64, _i64, _vp, _vp, _vp, _vp], _int),
+    "lora_act8_linear_bwd": ([_int, _i64, _i64, _mp, _vp, _vp, _fp, _vp, _sz, _vp], _int),
+    "lora_act8_linear_workspace_bytes": ([_int, _i64, _i64, _mp], _sz),
     "lora_mfma_rate": ([_int, _int, _vp, _vp], _int),
     "lora_transpose": ([_vp, _i64, _i64, _vp, _vp], _int),
     "lora_profile_begin": ([_int], _int),

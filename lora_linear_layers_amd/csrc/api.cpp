@@ -491,6 +491,8 @@ enum ProfKind : int {
   K_TOKEN_LOGP,
   K_LOSS,
   K_EPI_GRAD,
+  K_NORM,
+  K_ACT8,
   K_PROF_COUNT
 };
 
@@ -519,7 +521,8 @@ const char* kind_name(int k) {
       "dropout_mask_copy",          "transpose_w",                "skinny_fwd",
       "few_panel",                  "few_fwd",                    "few_bwd",
       "tiny_f32",
-      "token_logp",                 "sequence_loss",              "epilogue_grad"};
+      "token_logp",                 "sequence_loss",              "epilogue_grad",
+      "rmsnorm",                    "act8"};
   static_assert(sizeof(names) / sizeof(names[0]) == K_PROF_COUNT, "one name per launch kind");
   return (k >= 0 && k < K_PROF_COUNT) ? names[k] : "unknown";
 }
@@ -1743,6 +1746,21 @@ int check_epi(bool bwd, int dtype, int64_t M, int64_t d_in, const lora_group_mem
   return LORA_OK;
 }
 
+// Backward from an 8-bit checkpoint: the epilogue layer's backward (no
+// activation, no bias) and the checkpoint's values in the type.
+struct Act8Layout {
+  EpiLayout E;
+  size_t x = 0, total = 0;
+};
+
+Act8Layout make_act8_layout(int dtype, int64_t M, int64_t d_in, const lora_group_member& m) {
+  Act8Layout A;
+  A.E = make_epi_layout(true, dtype, M, d_in, m, lora_epilogue{LORA_ACT_NONE, nullptr, nullptr, nullptr});
+  A.x = align256(A.E.total);
+  A.total = A.x + align256(size_t(M) * d_in * elem_bytes(dtype));
+  return A;
+}
+
 constexpr size_t kStaticScratchBytes = size_t(LORA_STATIC_SCRATCH_BYTES);
 
 std::mutex g_scratch_mu;
@@ -2191,6 +2209,115 @@ int lora_transpose(const void* src, int64_t rows, int64_t cols, void* dst, void*
                                  rows, st);
   }));
   return LORA_OK;
+}
+
+// ---- root-mean-square norm, rows in 8 bits ----
+static int check_rows(int dtype, int64_t M, int64_t d) {
+  if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_ERR_DTYPE;
+  return M < 0 || M >= kMaxDim || d < 1 || d > LORA_NORM_MAX_DIM ? LORA_ERR_SHAPE : LORA_OK;
+}
+
+int lora_rmsnorm_fwd(int dtype, int64_t M, int64_t d, float eps, const void* X, int64_t ldx, const void* residual,
+                     int64_t ldr, const void* weight, void* H, void* Y, uint8_t* codes, float* scale8, float* rstd,
+                     void* stream) {
+  TRY(check_rows(dtype, M, d));
+  if (!(eps >= 0.f) || std::isinf(eps) || ldx < d || ldx >= kMaxDim || (residual && (ldr < d || ldr >= kMaxDim)))
+    return LORA_ERR_SHAPE;
+  const size_t eb = elem_bytes(dtype);
+  if (M > 0) {
+    TRY(check_elems({{X, eb}, {weight, eb}}, true));
+    if (!codes != !scale8 || (!Y && !codes && !H && !rstd)) return LORA_ERR_NULL;
+    TRY(check_elems({{residual, eb}, {H, eb}, {Y, eb}, {scale8, 4}, {rstd, 4}}, false));
+  }
+  TRY(check_device());
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const double n = double(M) * d;
+  const RmsNormArgs a{X, ldx, residual, residual ? ldr : 0, weight, H, Y, codes, scale8, rstd, M, (int)d, eps};
+  HIPTRY(timed(K_NORM, 4 * n, n * (eb * (1 + (residual ? 1 : 0) + (H ? 1 : 0) + (Y ? 1 : 0)) + (codes ? 1 : 0)), st,
+               [&] { return launch_rmsnorm((int)eb, a, st); }));
+  return LORA_OK;
+}
+
+size_t lora_rmsnorm_workspace_bytes(int64_t M, int64_t d) {
+  if (check_rows(LORA_F32, M, d) != LORA_OK) return 0;
+  return size_t(rmsnorm_grad_blocks(M, (int)d)) * d * 4;
+}
+
+int lora_rmsnorm_bwd(int dtype, int64_t M, int64_t d, const void* H, const void* weight, const float* rstd,
+                     const void* dY, const void* dH, void* dX, void* dweight, int dweight_dtype, void* ws,
+                     size_t ws_bytes, void* stream) {
+  TRY(check_rows(dtype, M, d));
+  if (dweight && dweight_dtype != LORA_F32 && dweight_dtype != LORA_BF16) return LORA_ERR_DTYPE;
+  const size_t eb = elem_bytes(dtype), wb = elem_bytes(dweight_dtype);
+  if (M > 0) TRY(check_elems({{H, eb}, {weight, eb}, {rstd, 4}, {dY, eb}}, true));
+  if (!dX && !dweight) return LORA_ERR_NULL;
+  TRY(check_elems({{dH, eb}, {dX, eb}, {dweight, wb}}, false));
+  if (dweight) {
+    if (!ws || ws_bytes < lora_rmsnorm_workspace_bytes(M, d)) return LORA_ERR_WORKSPACE;
+    if (!aligned16(ws)) return LORA_ERR_ALIGN;
+  }
+  TRY(check_device());
+  if (M == 0 && !dweight) return LORA_OK;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const double n = double(M) * d;
+  const RmsNormGradArgs a{H, weight, rstd, dY, dH, dX, dweight ? static_cast<float*>(ws) : nullptr, M, (int)d};
+  HIPTRY(timed(K_NORM, 8 * n, n * eb * (2 + (dH ? 1 : 0) + (dX ? 1 : 0)), st,
+               [&] { return launch_rmsnorm_grad((int)eb, a, dweight, (int)wb, st); }));
+  return LORA_OK;
+}
+
+int lora_act8_pack(int dtype, int64_t M, int64_t d, const void* X, int64_t ldx, uint8_t* codes, float* scale8,
+                   void* stream) {
+  TRY(check_rows(dtype, M, d));
+  if (ldx < d || ldx >= kMaxDim) return LORA_ERR_SHAPE;
+  const size_t eb = elem_bytes(dtype);
+  if (M > 0) TRY(check_elems({{X, eb}, {codes, 1}, {scale8, 4}}, true));
+  TRY(check_device());
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const double n = double(M) * d;
+  HIPTRY(timed(K_ACT8, 2 * n, n * (eb + 1), st,
+               [&] { return launch_act8_pack((int)eb, X, ldx, M, (int)d, codes, scale8, st); }));
+  return LORA_OK;
+}
+
+int lora_act8_unpack(int dtype, int64_t M, int64_t d, const uint8_t* codes, const float* scale8, void* X,
+                     void* stream) {
+  TRY(check_rows(dtype, M, d));
+  if (M > 0) TRY(check_ptrs({codes, X}));
+  if (M > 0) TRY(check_elems({{scale8, 4}}, true));
+  TRY(check_device());
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const double n = double(M) * d;
+  HIPTRY(timed(K_ACT8, n, n * (elem_bytes(dtype) + 1), st,
+               [&] { return launch_act8_unpack(elem_bytes(dtype), codes, scale8, M, d, X, st); }));
+  return LORA_OK;
+}
+
+size_t lora_act8_linear_workspace_bytes(int dtype, int64_t M, int64_t d_in, const lora_group_member* member) {
+  const lora_epilogue none{LORA_ACT_NONE, nullptr, nullptr, nullptr};
+  if (check_epi_sizes(dtype, M, d_in, member, &none) != LORA_OK || d_in > LORA_NORM_MAX_DIM) return 0;
+  return make_act8_layout(dtype, M, d_in, *member).total;
+}
+
+int lora_act8_linear_bwd(int dtype, int64_t M, int64_t d_in, const lora_group_member* member, const uint8_t* codes,
+                         const float* scale8, const float* table16, void* ws, size_t ws_bytes, void* stream) {
+  const lora_epilogue none{LORA_ACT_NONE, nullptr, nullptr, nullptr};
+  TRY(check_epi(true, dtype, M, d_in, member, &none, codes, table16));
+  if (d_in > LORA_NORM_MAX_DIM) return LORA_ERR_SHAPE;
+  if (M > 0) TRY(check_elems({{scale8, 4}}, true));
+  const lora_group_member& m = *member;
+  const Act8Layout E = make_act8_layout(dtype, M, d_in, m);
+  TRY(check_ws_bytes(E.total, ws, ws_bytes));
+  TRY(check_device());
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  void* X = static_cast<char*>(ws) + E.x;
+  if (M > 0)
+    HIPTRY(timed(K_ACT8, double(M) * d_in, double(M) * d_in * (elem_bytes(dtype) + 1), st,
+                 [&] { return launch_act8_unpack(elem_bytes(dtype), codes, scale8, M, d_in, X, st); }));
+  const Nf4W q{m.W_nf4, m.absmax, table16};
+  return backward_impl(dtype, M, d_in, m.d_out, m.r, m.scale, X, m.W, m.W_nf4 ? &q : nullptr, m.A, m.B, nullptr, m.dY,
+                       m.dX, m.dA, m.dB, ws, E.E.L, st, nullptr, nullptr, nullptr,
+                       E.E.L.dx_nt && !m.W_nf4 ? m.W_t : nullptr);
 }
 
 // ---- token log-probabilities ----

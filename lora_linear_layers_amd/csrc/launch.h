@@ -308,4 +308,48 @@ hipError_t launch_policy_loss(const LossSeqs& q, const PolicyLossArgs& l, void* 
 hipError_t launch_policy_grad(const LossSeqs& q, const PolicyLossArgs& l, const float* dloss, float* dlogp,
                               hipStream_t st);
 
+// Root-mean-square norm (norm.hip) of M rows of d (1 .. kNormMaxDim) elements:
+// h = X + residual (NULL: X), H = h, Y = h rstd weight, codes / scale8 = Y in 8
+// bits; H, Y, codes (with scale8) and rstd may each be NULL.  X and residual
+// have row strides, the others d.  H may be X or the residual, Y too.
+constexpr int64_t kNormMaxDim = 32768;
+struct RmsNormArgs {
+  const void* X;
+  int64_t ldx;
+  const void* residual;
+  int64_t ldr;
+  const void* weight;
+  void* H;
+  void* Y;
+  uint8_t* codes;
+  float* scale8;
+  float* rstd;
+  int64_t M;
+  int d;
+  float eps;
+};
+hipError_t launch_rmsnorm(int elem_bytes, const RmsNormArgs& a, hipStream_t st);
+// dX = rstd (dY w - xh mean(dY w xh)) + dH (dX and dH may be NULL, dX may be dY
+// or dH) and, with part (fp32 [rmsnorm_grad_blocks][d]), dw [d] (2 or 4 bytes
+// an element) = the sum over rows of dY xh.  M = 0 gives zeros.
+struct RmsNormGradArgs {
+  const void* H;
+  const void* weight;
+  const float* rstd;
+  const void* dY;
+  const void* dH;
+  void* dX;
+  float* part;
+  int64_t M;
+  int d;
+};
+int rmsnorm_grad_blocks(int64_t M, int d);
+hipError_t launch_rmsnorm_grad(int elem_bytes, const RmsNormGradArgs& a, void* dw, int dw_bytes, hipStream_t st);
+
+// Rows kept in 8 bits (norm.hip): e4m3 codes [M, d] and a power of two a row.
+hipError_t launch_act8_pack(int elem_bytes, const void* X, int64_t ldx, int64_t M, int d, uint8_t* codes, float* scale8,
+                            hipStream_t st);
+hipError_t launch_act8_unpack(int elem_bytes, const uint8_t* codes, const float* scale8, int64_t M, int64_t d, void* X,
+                              hipStream_t st);
+
 }  // namespace lora

@@ -891,3 +891,208 @@ class LoraPolicyLossFunction(torch.autograd.Function):
         logp, old_logp, ref_logp, cu, advantages, mask, weight = ctx.saved_tensors
         d = lora_policy_loss_bwd(logp, cu, advantages, weight, old_logp, ref_logp, mask, dloss=_f32c(dloss), **ctx.args)
         return (d.view(logp.shape),) + (None,) * 11
+
+
+# ---------------------------------------------------------------------------
+# the norm in front of the projections, and activations kept in 8 bits
+# ---------------------------------------------------------------------------
+_F8 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _rows(name, dev, t, shape, dtypes):
+    """The row stride of a [M, d] tensor with contiguous rows."""
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    M, d = shape
+    if d > 1 and M > 0 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.stride(0) if M > 1 else d
+
+
+def lora_rmsnorm_fwd(X, weight, eps: float = 1e-5, residual=None, pack: bool = False, need_y: bool = True, H=None):
+    """(Y, H, rstd, codes, scale8): H = X + residual (X itself without one), rstd = 1 / sqrt(mean(H^2) + eps) fp32 [M],
+    Y = H rstd weight (None unless need_y), and Y as lora_act8_pack keeps it where pack (else None, None).  X and
+    residual [M, d] may have a row stride; H, where given, receives the sum and may be X or the residual."""
+    dev, same = _gpu(X), (X.dtype,)
+    dt = L._dtype_code(X)
+    if X.dim() != 2:
+        raise ValueError("X must be [M, d]")
+    M, d = X.shape
+    ldx = _rows("X", dev, X, X.shape, same)
+    _check(dev, "weight", weight, same, d)
+    ldr = 0
+    if residual is not None:
+        ldr = _rows("residual", dev, residual, X.shape, same)
+        if H is None:
+            H = torch.empty(M, d, dtype=X.dtype, device=dev)
+    if H is not None:
+        _check(dev, "H", H, same, M * d)
+    new = lambda t: torch.empty(M, d, dtype=t, device=dev)  # noqa: E731
+    Y = new(X.dtype) if need_y else None
+    codes = new(torch.float8_e4m3fn) if pack else None
+    stats = torch.empty(2 if pack else 1, M, dtype=torch.float32, device=dev)
+    rstd, scale8 = stats[0], stats[1] if pack else None
+    with _on(dev):
+        L._check("lora_rmsnorm_fwd", L.lib().lora_rmsnorm_fwd(
+            dt, M, d, float(eps), L._ptr(X), ldx, L._ptr(residual), ldr, L._ptr(weight), L._ptr(H), L._ptr(Y),
+            L._ptr(codes), L._ptr(scale8), L._ptr(rstd), L._stream(dev)))
+    return Y, X if H is None else H, rstd, codes, scale8
+
+
+def lora_rmsnorm_bwd(H, weight, rstd, dY, dH=None, need_dX: bool = True, need_dweight: bool = True,
+                     dweight_dtype=torch.float32, ws=None):
+    """(dX or None, dweight or None) of lora_rmsnorm_fwd from its H and rstd; dH: the gradient of H itself, where the
+    residual stream goes on.  dX is the gradient of X and of the residual."""
+    dev, same = _gpu(H), (H.dtype,)
+    dt = L._dtype_code(H)
+    if H.dim() != 2:
+        raise ValueError("H must be [M, d]")
+    M, d = H.shape
+    _check(dev, "H", H, same)
+    _check(dev, "weight", weight, same, d)
+    _check(dev, "rstd", rstd, _F32, M)
+    _check(dev, "dY", dY, same, M * d)
+    if dH is not None:
+        _check(dev, "dH", dH, same, M * d)
+    if not need_dX and not need_dweight:
+        return None, None
+    dX = torch.empty(M, d, dtype=H.dtype, device=dev) if need_dX else None
+    dw, ws_bytes = None, 0
+    if need_dweight:
+        dw = torch.empty(d, dtype=dweight_dtype, device=dev)
+        if ws is None:
+            ws_bytes = int(L.lib().lora_rmsnorm_workspace_bytes(M, d))
+            ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+        else:
+            ws_bytes = _check_ws(dev, ws, ws.nbytes).nbytes
+    with _on(dev):
+        L._check("lora_rmsnorm_bwd", L.lib().lora_rmsnorm_bwd(
+            dt, M, d, L._ptr(H), L._ptr(weight), L._ptr(rstd), L._ptr(dY), L._ptr(dH), L._ptr(dX), L._ptr(dw),
+            0 if dw is None else L._dtype_code(dw), L._ptr(ws), ws_bytes, L._stream(dev)))
+    return dX, dw
+
+
+class LoraRmsNormFunction(torch.autograd.Function):
+    """(Y, H) = LoraRmsNormFunction.apply(X, residual, weight, eps, pack), or (Y, H, codes, scale8) with pack: Y the
+    norm of H = X + residual, or of X where residual is None (H is then None); gradients for X, residual and weight
+    from those of Y and H.  codes and scale8 keep Y in 8 bits, for LoraLinearAct8Function."""
+
+    @staticmethod
+    def forward(ctx, X, residual, weight, eps=1e-5, pack=False):
+        Y, H, rstd, codes, scale8 = lora_rmsnorm_fwd(X, weight, eps, residual, pack)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(H.contiguous(), weight, rstd)
+        H = H if residual is not None else None
+        if not pack:
+            return Y, H
+        ctx.mark_non_differentiable(codes, scale8)
+        return Y, H, codes, scale8
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dY, dH, *_):
+        H, weight, rstd = ctx.saved_tensors
+        need_X, need_R, need_w = ctx.needs_input_grad[:3]
+        if dY is None:  # the stream alone went on
+            return dH if need_X else None, dH if need_R else None, None, None, None
+        dX, dw = lora_rmsnorm_bwd(H, weight, rstd, dY.contiguous(), None if dH is None else dH.contiguous(),
+                                  need_X or need_R, need_w, weight.dtype)
+        return dX if need_X else None, dX if need_R else None, None if dw is None else dw.view_as(weight), None, None
+
+
+def lora_act8_pack(X):
+    """(codes float8_e4m3fn [M, d], scale8 fp32 [M]) of X [M, d] (rows may be strided): row t is codes[t] * scale8[t],
+    scale8[t] the smallest power of two that keeps the row at or below 448."""
+    dev = _gpu(X)
+    dt = L._dtype_code(X)
+    if X.dim() != 2:
+        raise ValueError("X must be [M, d]")
+    M, d = X.shape
+    ldx = _rows("X", dev, X, X.shape, (X.dtype,))
+    codes = torch.empty(M, d, dtype=torch.float8_e4m3fn, device=dev)
+    scale8 = torch.empty(M, dtype=torch.float32, device=dev)
+    with _on(dev):
+        L._check("lora_act8_pack", L.lib().lora_act8_pack(dt, M, d, L._ptr(X), ldx, L._ptr(codes), L._ptr(scale8),
+                                                          L._stream(dev)))
+    return codes, scale8
+
+
+def _packed(codes, scale8, M=None):
+    dev = _gpu(codes)
+    if codes.dim() != 2:
+        raise ValueError("codes must be [M, d]")
+    _check(dev, "codes", codes, _F8, None if M is None else M * codes.shape[1])
+    _check(dev, "scale8", scale8, _F32, codes.shape[0])
+    return dev, codes.shape
+
+
+def lora_act8_unpack(codes, scale8, dtype=torch.bfloat16):
+    """codes * scale8 [M, d] in bf16 or fp32 (exact in both)."""
+    dev, (M, d) = _packed(codes, scale8)
+    X = torch.empty(M, d, dtype=dtype, device=dev)
+    with _on(dev):
+        L._check("lora_act8_unpack", L.lib().lora_act8_unpack(L._dtype_code(X), M, d, L._ptr(codes), L._ptr(scale8),
+                                                              L._ptr(X), L._stream(dev)))
+    return X
+
+
+def lora_act8_linear_bwd(codes, scale8, member, dY, need_dX: bool = True, table16=None, ws=None):
+    """(dX or None, dA fp32, dB fp32) of a projection whose input was kept as codes and scale8 (lora_act8_pack, or
+    lora_rmsnorm_fwd with pack), for a member as lora_linear_epi_bwd takes it."""
+    dev, (M, d_in) = _packed(codes, scale8)
+    A, B = member["A"], member["B"]
+    if A.dim() != 2 or B.dim() != 2 or dY.dim() != 2:
+        raise ValueError("shape mismatch: codes [M,d_in], W [d_out,d_in], A [r,d_in], B [d_out,r], dY [M,d_out]")
+    # (a [0, d_in] tensor of the layer's type stands for X in the checks of the member)
+    _, _, _, d_out, r, m = _epi_member(dY.new_empty(0, d_in), member)
+    if A.shape != (r, d_in) or B.shape != (d_out, r) or dY.shape != (M, d_out):
+        raise ValueError("shape mismatch: codes [M,d_in], W [d_out,d_in], A [r,d_in], B [d_out,r], dY [M,d_out]")
+    dt = L._dtype_code(dY)
+    _check(dev, "dY", dY, (dY.dtype,), M * d_out)
+    dX = torch.empty(M, d_in, dtype=dY.dtype, device=dev) if need_dX else None
+    dA = torch.empty(r, d_in, dtype=torch.float32, device=dev)
+    dB = torch.empty(d_out, r, dtype=torch.float32, device=dev)
+    m.dY, m.dX, m.dA, m.dB = L._ptr(dY), L._ptr(dX), L._ptr(dA), L._ptr(dB)
+    tab = L._table_ptr(table16) if table16 is not None else None
+    if ws is None:
+        ws_bytes = int(L.lib().lora_act8_linear_workspace_bytes(dt, M, d_in, m))
+        ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+    else:
+        ws_bytes = _check_ws(dev, ws, ws.nbytes).nbytes
+    with _on(dev):
+        L._check("lora_act8_linear_bwd", L.lib().lora_act8_linear_bwd(
+            dt, M, d_in, m, L._ptr(codes), L._ptr(scale8), tab, L._ptr(ws), ws_bytes, L._stream(dev)))
+    return dX, dA, dB
+
+
+class LoraLinearAct8Function(torch.autograd.Function):
+    """Y = LoraLinearAct8Function.apply(X, W, A, B, scale, codes, scale8, W_t): LoraLinearFunction that keeps its input
+    in 8 bits for the backward (a quarter of fp32's bytes, half of bf16's): codes and scale8 where the caller has them
+    (the norm's, one checkpoint for all the projections that read it), else X packed here.  Y and dX are those of X itself;
+    dA and dB are of the kept values."""
+
+    @staticmethod
+    def forward(ctx, X, W, A, B, scale, codes=None, scale8=None, W_t=None):
+        Y, _ = lora_linear_epi_fwd(X, {"W": W, "A": A, "B": B, "scale": scale})
+        if any(ctx.needs_input_grad[i] for i in (0, 2, 3)):
+            if codes is None:
+                codes, scale8 = lora_act8_pack(X)
+            elif codes.shape != X.shape:
+                raise ValueError("codes must have X's shape")
+            _packed(codes, scale8)
+            ctx.save_for_backward(codes, scale8, W, A, B, W_t)
+        ctx.scale = scale
+        return Y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dY):
+        codes, scale8, W, A, B, W_t = ctx.saved_tensors
+        member = {"W": W, "A": A, "B": B, "scale": ctx.scale, "W_t": W_t}
+        need_dX, _, need_dA, need_dB = ctx.needs_input_grad[:4]
+        dX, dA, dB = lora_act8_linear_bwd(codes, scale8, member, dY.contiguous(), need_dX)
+        return (dX, None, dA.to(A.dtype) if need_dA else None, dB.to(B.dtype) if need_dB else None) + (None,) * 4

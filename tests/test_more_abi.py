@@ -1,0 +1,87 @@
+"""Refusals of the norm, 8-bit and adapter-per-token entry points: validation comes before any HIP call, so no GPU is needed."""
+import ctypes
+import math
+
+import pytest
+
+import lora_linear_layers_amd as L
+from lora_linear_layers_amd import _lib
+
+OK, ENULL, ESHAPE, EALIGN, EDTYPE, EWS, EDEV = 0, -1, -2, -3, -4, -5, -6
+P = 1 << 20  # an aligned address that nothing reads
+
+
+def _norm(lib, dtype=1, M=4, d=64, eps=1e-5, X=P, ldx=64, R=None, ldr=0, w=P, H=None, Y=P, codes=None, s8=None, rstd=None):
+    return lib.lora_rmsnorm_fwd(dtype, M, d, eps, X, ldx, R, ldr, w, H, Y, codes, s8, rstd, None)
+
+
+def test_norm_validation():
+    lib = L.load()
+    assert _norm(lib, dtype=2) == EDTYPE
+    assert _norm(lib, d=0) == ESHAPE
+    assert _norm(lib, d=32769, ldx=32769) == ESHAPE
+    assert _norm(lib, M=-1) == ESHAPE
+    assert _norm(lib, M=1 << 31) == ESHAPE
+    assert _norm(lib, ldx=63) == ESHAPE
+    assert _norm(lib, R=P, ldr=63) == ESHAPE
+    for eps in (-1e-9, math.nan, math.inf):
+        assert _norm(lib, eps=eps) == ESHAPE
+    assert _norm(lib, X=None) == ENULL
+    assert _norm(lib, w=None) == ENULL
+    assert _norm(lib, Y=None) == ENULL  # no output at all
+    assert _norm(lib, codes=P) == ENULL
+    assert _norm(lib, s8=P) == ENULL
+    assert _norm(lib, X=P + 1) == EALIGN
+    assert _norm(lib, dtype=0, Y=P + 2) == EALIGN
+    assert _norm(lib, rstd=P + 2) == EALIGN
+
+
+def test_norm_bwd_validation():
+    lib = L.load()
+
+    def call(dtype=1, M=4, d=64, H=P, w=P, rstd=P, dY=P, dH=None, dX=P, dw=None, wt=0, ws=None, n=0):
+        return lib.lora_rmsnorm_bwd(dtype, M, d, H, w, rstd, dY, dH, dX, dw, wt, ws, n, None)
+    assert call(dtype=5) == EDTYPE
+    assert call(dw=P, wt=3, ws=P, n=1 << 30) == EDTYPE
+    assert call(d=40000) == ESHAPE
+    assert call(H=None) == ENULL
+    assert call(rstd=None) == ENULL
+    assert call(dX=None) == ENULL
+    assert call(dY=P + 1) == EALIGN
+    need = lib.lora_rmsnorm_workspace_bytes(4, 64)
+    assert need > 0 and lib.lora_rmsnorm_workspace_bytes(-1, 64) == 0 and lib.lora_rmsnorm_workspace_bytes(4, 0) == 0
+    assert call(dw=P) == EWS
+    assert call(dw=P, ws=P, n=need - 1) == EWS
+    assert call(dw=P, ws=P + 8, n=need) == EALIGN
+
+
+def test_act8_validation():
+    lib = L.load()
+    assert lib.lora_act8_pack(2, 4, 64, P, 64, P, P, None) == EDTYPE
+    assert lib.lora_act8_pack(1, 4, 64, P, 60, P, P, None) == ESHAPE
+    assert lib.lora_act8_pack(1, 4, 64, None, 64, P, P, None) == ENULL
+    assert lib.lora_act8_pack(1, 4, 64, P, 64, P, None, None) == ENULL
+    assert lib.lora_act8_pack(1, 4, 64, P + 1, 64, P, P, None) == EALIGN
+    assert lib.lora_act8_unpack(1, 4, 64, P, None, P, None) == ENULL
+    assert lib.lora_act8_unpack(1, 4, 64, P + 4, P, P, None) == EALIGN
+    assert lib.lora_act8_unpack(1, 4, 0, P, P, P, None) == ESHAPE
+    member = _lib.GroupMember(32, 8, 1.0, 0, P, None, None, P, P, None, P, P, P, P, None)
+
+    def call(m=member, dtype=1, M=4, d_in=64, codes=P, s8=P, ws=P, n=1 << 30):
+        return lib.lora_act8_linear_bwd(dtype, M, d_in, m, codes, s8, None, ws, n, None)
+    assert call(dtype=2) == EDTYPE
+    assert call(d_in=12) == ESHAPE
+    assert call(d_in=32776) == ESHAPE
+    assert call(m=None) == ENULL
+    assert call(codes=None) == ENULL
+    assert call(codes=P + 8) == EALIGN
+    assert call(s8=None) == ENULL
+    assert call(s8=P + 2) == EALIGN
+    assert call(ws=None) == EWS
+    need = lib.lora_act8_linear_workspace_bytes(1, 4, 64, member)
+    assert need > 0 and call(n=need - 1) == EWS
+    assert lib.lora_act8_linear_workspace_bytes(1, 4, 12, member) == 0
+    rope = _lib.GroupMember(128, 8, 1.0, 1, P, None, None, P, P, None, P, P, P, P, None)
+    assert call(m=rope) == ESHAPE
+    no_grad = _lib.GroupMember(32, 8, 1.0, 0, P, None, None, P, P, None, P, P, None, P, None)
+    assert call(m=no_grad) == ENULL
