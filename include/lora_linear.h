@@ -521,6 +521,44 @@ int lora_act8_linear_bwd(int dtype, int64_t M, int64_t d_in, const lora_group_me
 size_t lora_act8_linear_workspace_bytes(int dtype, int64_t M, int64_t d_in, const lora_group_member* member);
 
 /*
+ * A projection whose rows each carry an adapter of their own: requests that
+ * share a base weight (decode steps and packed prompts) and several adapters
+ * trained at once.  n adapters of one rank (smaller ones padded with zeros),
+ * A [n, r, d_in], B [n, d_out, r] of the dtype, scales fp32 [n] (s_a = alpha / r),
+ * index: device int32 [M], the row's adapter; a row whose index lies outside
+ * [0, n) has none:
+ *     y_t = W x_t + s_a B_a (A_a x_t),   a = index[t]
+ * Rows may come in any order.  What it costs grows with the number of adapters
+ * that meet in 128 or 256 consecutive rows, so requests' tokens should lie together.
+ * r a multiple of 8 up to LORA_MULTI_MAX_RANK, 1 <= n <= LORA_MULTI_MAX_ADAPTERS,
+ * d_in and d_out as in lora_linear_fwd and at most LORA_EPI_MAX_D_OUT.
+ * An infinity or NaN stays with its own: one in an adapter's A or B makes its
+ * rows' outputs (dX) NaN where the definition may leave some finite, one in a
+ * row of X or dY its adapter's gradients; other adapters and rows do not see it.
+ * index and scales need their element's alignment only.  Workspace from its own
+ * sizing call (with backward != 0: have_w_t whether W_t is given, need_dx
+ * whether dX is).
+ *
+ * Backward, for dY [M, d_out]:
+ *     dX_t = W^T dy_t + s_a A_a^T (B_a^T dy_t)
+ *     dB_a = s_a sum_{t in a} dy_t (A_a x_t)^T,  dA_a = s_a sum_{t in a} (B_a^T dy_t) x_t^T
+ * dX [M, d_in] or NULL; dA [n, r, d_in] and dB [n, d_out, r] of grad_dtype, zeros for
+ * an adapter without rows, sums over rows in a fixed order.  W_t: W^T [d_in,
+ * d_out] (bf16, lora_transpose) where the caller keeps one, else NULL (a bf16
+ * call that needs it makes its own); fp32 calls do not read it.
+ */
+#define LORA_MULTI_MAX_RANK 128
+#define LORA_MULTI_MAX_ADAPTERS 4096
+size_t lora_multi_workspace_bytes(int backward, int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r,
+                                  int have_w_t, int need_dx);
+int lora_multi_fwd(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r, const void* X, const void* W,
+                   const void* A, const void* B, const float* scales, const int32_t* index, void* Y, void* ws,
+                   size_t ws_bytes, void* stream);
+int lora_multi_bwd(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r, const void* X, const void* W,
+                   const void* W_t, const void* A, const void* B, const float* scales, const int32_t* index, const void* dY,
+                   void* dX, void* dA, void* dB, int grad_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Log-probabilities of tokens from their logits (the head projection of a
  * training step: preference and policy losses read them, and their gradient
  * goes back through the head's LoRA layer).  For row i with target t_i:

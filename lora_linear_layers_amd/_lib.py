@@ -97,6 +97,9 @@ _SIGS = {
     "lora_act8_unpack": ([_int, _i64, _i64, _vp, _vp, _vp, _vp], _int),
     "lora_act8_linear_bwd": ([_int, _i64, _i64, _mp, _vp, _vp, _fp, _vp, _sz, _vp], _int),
     "lora_act8_linear_workspace_bytes": ([_int, _i64, _i64, _mp], _sz),
+    "lora_multi_workspace_bytes": ([_int, _int] + [_i64] * 5 + [_int, _int], _sz),
+    "lora_multi_fwd": ([_int] + [_i64] * 5 + [_vp] * 8 + [_sz, _vp], _int),
+    "lora_multi_bwd": ([_int] + [_i64] * 5 + [_vp] * 11 + [_int, _vp, _sz, _vp], _int),
     "lora_mfma_rate": ([_int, _int, _vp, _vp], _int),
     "lora_transpose": ([_vp, _i64, _i64, _vp, _vp], _int),
     "lora_profile_begin": ([_int], _int),

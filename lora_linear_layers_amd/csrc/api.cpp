@@ -493,6 +493,12 @@ enum ProfKind : int {
   K_EPI_GRAD,
   K_NORM,
   K_ACT8,
+  K_MULTI_LISTS,
+  K_MULTI_PANEL,
+  K_MULTI_STRIP,
+  K_MULTI_GEMM,
+  K_MULTI_UPDATE,
+  K_MULTI_GRAD,
   K_PROF_COUNT
 };
 
@@ -522,7 +528,9 @@ const char* kind_name(int k) {
       "few_panel",                  "few_fwd",                    "few_bwd",
       "tiny_f32",
       "token_logp",                 "sequence_loss",              "epilogue_grad",
-      "rmsnorm",                    "act8"};
+      "rmsnorm",                    "act8",
+      "multi_lists",                "multi_panel",                "multi_strip",
+      "multi_gemm",                 "multi_update",               "multi_grad"};
   static_assert(sizeof(names) / sizeof(names[0]) == K_PROF_COUNT, "one name per launch kind");
   return (k >= 0 && k < K_PROF_COUNT) ? names[k] : "unknown";
 }
@@ -1761,6 +1769,340 @@ Act8Layout make_act8_layout(int dtype, int64_t M, int64_t d_in, const lora_group
   return A;
 }
 
+// ---------------------------------------------------------------------------
+// an adapter of its own for every row (multi.hip)
+// ---------------------------------------------------------------------------
+// One product [M, N] over K with the rows' strips: on the tiles of the epilogue
+// layer with the adapters' columns as a second segment (gemm), else the strips'
+// part into the output first and the base product added to it by the layer's
+// other kernels (few tiles, short contractions).
+struct MultiProduct {
+  bool gemm = false;
+  StreamPlan plan;
+  EpiLayout base;  // the other kernels' layout
+};
+
+MultiProduct multi_product(int dtype, int64_t M, int64_t N, int64_t K, int64_t n, int64_t r) {
+  MultiProduct P;
+  if (dtype == LORA_BF16 && M > 0 && K >= 64 && n * N * r * 2 < 0xE0000000ll) {
+    const int64_t t = cdiv(M, 256) * cdiv(N, 256);
+    if (M % 256 == 0 && N % 256 == 0 && t % 256 == 0 && K % 64 == 0 && t <= INT32_MAX / 2 &&
+        whole_ld_fits(std::max(K, N))) {
+      P.plan.ok = true;  // whole tiles, a block each
+      P.plan.full = (int)t;
+    } else {
+      P.plan = stream_plan(M, N, K, 64, false);
+    }
+    P.gemm = P.plan.ok;
+  }
+  if (!P.gemm) {
+    lora_group_member m;
+    memset(&m, 0, sizeof(m));
+    m.d_out = N;
+    m.r = 8;
+    P.base = make_epi_layout(false, dtype, M, K, m, lora_epilogue{LORA_ACT_NONE, nullptr, nullptr, nullptr});
+  }
+  return P;
+}
+
+struct MultiLayout {
+  MultiProduct y, dx;
+  int64_t M8 = 0;
+  int per = 1, groups = 0;  // adapters of 64 rows of the stacked ones (one, from a rank above 64 on); such groups
+  bool need256 = false;
+  int splits_p = 1, splits_q = 1, splits_a = 1, splits_b = 1;
+  int64_t ksplit_p = 0, ksplit_q = 0;
+  size_t list128 = 0, cnt128 = 0, list256 = 0, cnt256 = 0, glist = 0, gcnt = 0, part = 0, partq = 0, p = 0, pt = 0, qt = 0,
+         bt = 0, at = 0, wt = 0, st_part = 0, st_cnt = 0, base = 0, parta = 0, partb = 0, bad = 0, gbad = 0, mask = 0, total = 0;
+  int chunks = 0;  // of an adapter's second operand in the product, looked at for infinities and NaNs
+};
+
+// Token splits of a row group's gradient [64, N]: about two blocks a CU.
+int multi_grad_splits(int64_t M, int64_t N, int64_t groups) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(1, cdiv(N, 256) * groups), cdiv(M, 512), 16}));
+}
+
+MultiLayout make_multi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r,
+                              bool have_wt, bool need_dx) {
+  MultiLayout L;
+  if (M == 0) return L;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  L.M8 = rup(M, 8);
+  L.per = (int)std::max<int64_t>(1, 64 / r);
+  L.groups = (int)cdiv(n, L.per);
+  const bool f32 = dtype == LORA_F32;
+  if (!bwd) L.y = multi_product(dtype, M, d_out, d_in, n, r);
+  if (bwd && need_dx) L.dx = multi_product(dtype, M, d_in, d_out, n, r);
+  const MultiProduct& g = bwd ? L.dx : L.y;
+  if (f32) {
+    L.p = take(size_t(M) * r * 4);
+    if (bwd) {
+      L.pt = take(size_t(M) * r * 4);  // Q
+      L.bt = take(size_t(n) * r * d_out * 4);
+      if (need_dx) L.at = take(size_t(n) * r * d_in * 4);
+    }
+  } else {
+    const int64_t t128 = cdiv(M, 128), t256 = cdiv(M, 256);
+    L.need256 = g.gemm && !g.plan.low;
+    L.list128 = take(size_t(t128) * std::min<int64_t>(n, 128) * 4);
+    L.cnt128 = take(size_t(t128) * 4);
+    if (L.need256) {
+      L.list256 = take(size_t(t256) * std::min<int64_t>(n, 256) * 4);
+      L.cnt256 = take(size_t(t256) * 4);
+    }
+    if (g.gemm) {
+      L.chunks = (int)cdiv((bwd ? d_in : d_out) * r * 2, 65536);
+      L.bad = take(size_t(n) * L.chunks * 4);
+    }
+    // cleared together: the stream kernel's counters and the spoilt gradients
+    L.st_cnt = take(size_t(g.gemm ? g.plan.half : 0) * 4 + (bwd ? size_t(n) * 4 : 0));
+    L.gbad = L.st_cnt + size_t(g.gemm ? g.plan.half : 0) * 4;
+    if (g.gemm && g.plan.half > 0) L.st_part = take(size_t(g.plan.half) * 2 * 256 * 256 * 4);
+    panel_split(M, d_in, 64, &L.splits_p, &L.ksplit_p);
+    L.part = take(size_t(L.splits_p) * M * r * 4);
+    if (!bwd || need_dx) L.p = take(size_t(M) * r * 2);
+    if (bwd) {
+      panel_split(M, d_out, 64, &L.splits_q, &L.ksplit_q);
+      L.partq = take(size_t(L.splits_q) * M * r * 4);
+      L.glist = take(size_t(L.groups) * cdiv(M, 64) * 4);
+      L.gcnt = take(size_t(L.groups) * 4);
+      L.mask = take(size_t(cdiv(M, 64)) * 8);
+      L.pt = take(size_t(n) * r * L.M8 * 2);
+      L.qt = take(size_t(n) * r * L.M8 * 2);
+      L.bt = take(size_t(n) * r * d_out * 2);
+      if (need_dx) {
+        L.at = take(size_t(n) * r * d_in * 2);
+        if (!have_wt) L.wt = take(size_t(d_in) * d_out * 2);
+      }
+      L.splits_a = multi_grad_splits(M, d_in, L.groups);
+      L.splits_b = multi_grad_splits(M, d_out, L.groups);
+      L.parta = take(size_t(L.splits_a) * n * r * d_in * 4);
+      L.partb = take(size_t(L.splits_b) * n * r * d_out * 4);
+    }
+  }
+  if (!bwd && !g.gemm) L.base = take(g.base.total);
+  if (bwd && need_dx && !g.gemm) {
+    if (f32) {
+      int S = 1;
+      int64_t ks = 0;
+      f32_split(cdiv(M, 64) * cdiv(d_in, 128), d_out, &S, &ks);
+      if (S > 1) L.base = take(size_t(S) * M * d_in * 4);
+    } else {
+      L.base = take(g.base.total);
+    }
+  }
+  L.total = off;
+  return L;
+}
+
+struct MultiCall {
+  int dtype;
+  int64_t M, d_in, d_out, n, r;
+  const float* scales;
+  const int32_t* index;
+};
+
+// scan: the product's second operands, by adapter, as the caller holds them.
+int multi_lists(const MultiCall& c, const MultiLayout& L, const MultiProduct& g, bool bwd, const void* scan, char* w,
+                hipStream_t st) {
+  MultiLists q;
+  memset(&q, 0, sizeof(q));
+  q.index = c.index; q.M = c.M; q.n = (int)c.n; q.per = L.per;
+  q.t128 = (int)cdiv(c.M, 128);
+  q.list128 = reinterpret_cast<int*>(w + L.list128); q.cnt128 = reinterpret_cast<int*>(w + L.cnt128);
+  if (L.need256) {
+    q.t256 = (int)cdiv(c.M, 256);
+    q.list256 = reinterpret_cast<int*>(w + L.list256); q.cnt256 = reinterpret_cast<int*>(w + L.cnt256);
+  }
+  if (bwd) {
+    q.groups = L.groups;
+    q.glist = reinterpret_cast<int*>(w + L.glist); q.gcnt = reinterpret_cast<int*>(w + L.gcnt);
+  }
+  q.zero = reinterpret_cast<int*>(w + L.st_cnt);
+  q.nzero = (g.gemm ? g.plan.half : 0) + (bwd ? (int)c.n : 0);
+  if (L.chunks) {
+    q.scan = scan; q.scan16 = (bwd ? c.d_in : c.d_out) * c.r / 8; q.chunks = L.chunks;
+    q.bad = reinterpret_cast<int*>(w + L.bad);
+  }
+  HIPTRY(timed(K_MULTI_LISTS, 0, 4.0 * c.M, st, [&] { return launch_multi_lists(q, st); }));
+  return LORA_OK;
+}
+
+MultiStrip multi_strips(const MultiCall& c, const MultiLayout& L, const MultiProduct& g, char* w) {
+  MultiStrip s;
+  memset(&s, 0, sizeof(s));
+  s.ops = 1; s.index = c.index; s.scales = c.scales; s.M = c.M; s.n = (int)c.n; s.r = (int)c.r; s.per = L.per;
+  s.chunks = L.chunks; s.bad = reinterpret_cast<int*>(w + L.bad);
+  if (g.gemm && g.plan.low) { s.list128 = reinterpret_cast<int*>(w + L.list128); s.cnt128 = reinterpret_cast<int*>(w + L.cnt128); }
+  if (g.gemm && !g.plan.low) { s.list256 = reinterpret_cast<int*>(w + L.list256); s.cnt256 = reinterpret_cast<int*>(w + L.cnt256); }
+  return s;
+}
+
+GemmArgs multi_panel_args(const MultiCall& c, const MultiLayout& L, const void* X, int64_t K, const void* A, int64_t ksplit,
+                          float* part, char* w) {
+  GemmArgs a = blank();
+  a.a1 = X; a.lda1 = K; a.b1 = A; a.ldb1 = K; a.K1 = K;
+  a.m_load = a.m_store = c.M; a.k_split = ksplit; a.c = part; a.ldc = c.r; a.part_stride = c.M * c.r;
+  a.ad_of = c.index; a.ad_list = reinterpret_cast<int*>(w + L.list128); a.ad_cnt = reinterpret_cast<int*>(w + L.cnt128);
+  a.ad_cap = (int)std::min<int64_t>(c.n, 128); a.ad_r = (int)c.r; a.ad_n = (int)c.n;
+  return a;
+}
+
+// out [M, N] = X W^T + the strips P of the rows' adapters times their second
+// operands B [n][N, r]; bf16, W [N, K].
+int multi_bf16(const MultiCall& c, const MultiLayout& L, const MultiProduct& g, const void* X, int64_t K, const void* W,
+               int64_t N, const uint16_t* P, const void* B, void* out, char* w, hipStream_t st) {
+  const double Md = double(c.M), flop = 2 * Md * N * (K + c.r), bytes = 2 * (Md * (K + N) + double(N) * K);
+  if (g.gemm) {
+    GemmArgs a = blank();
+    a.a1 = X; a.lda1 = K; a.b1 = W; a.ldb1 = K; a.K1 = K;
+    a.a2 = P; a.lda2 = c.r; a.b2 = B; a.ldb2 = c.r;
+    a.m_load = a.m_store = c.M; a.n_load = a.n_store = N; a.c = out; a.ldc = N;
+    const int rows = g.plan.low ? 128 : 256;
+    a.ad_of = c.index;
+    a.ad_list = reinterpret_cast<int*>(w + (g.plan.low ? L.list128 : L.list256));
+    a.ad_cnt = reinterpret_cast<int*>(w + (g.plan.low ? L.cnt128 : L.cnt256));
+    a.ad_cap = (int)std::min<int64_t>(c.n, rows); a.ad_r = (int)c.r; a.ad_n = (int)c.n; a.ad_step = N * c.r;
+    a.st_full = g.plan.full; a.st_half = g.plan.half; a.st_early = g.plan.early;
+    a.st_part = reinterpret_cast<float*>(w + L.st_part); a.st_cnt = reinterpret_cast<int*>(w + L.st_cnt);
+    HIPTRY(timed(K_MULTI_GEMM, flop, bytes, st, [&] { return launch_multi_gemm(a, g.plan.low, st); }));
+    return LORA_OK;
+  }
+  HIPTRY(timed(K_MULTI_UPDATE, 2 * Md * N * c.r, 2 * Md * N, st, [&] {
+    return launch_multi_update(2, P, B, c.index, c.M, N, (int)c.n, (int)c.r, false, out, st);
+  }));
+  const EpiArgs ep{nullptr, out, nullptr, LORA_ACT_NONE};
+  return forward_impl(LORA_BF16, c.M, K, N, 0, 0.f, X, W, nullptr, nullptr, nullptr, nullptr, out, w + L.base, g.base.L, st, P,
+                      c.r, nullptr, &ep);
+}
+
+int multi_forward(const MultiCall& c, const MultiLayout& L, const void* X, const void* W, const void* A, const void* B,
+                  void* Y, char* w, hipStream_t st) {
+  const double Md = double(c.M), kr = double(c.d_in) * c.r;
+  if (c.dtype == LORA_F32) {
+    float* P = reinterpret_cast<float*>(w + L.p);
+    HIPTRY(timed(K_MULTI_PANEL, 2 * Md * kr, 4 * Md * c.d_in, st, [&] {
+      return launch_multi_dot(4, X, A, c.scales, c.index, c.M, c.d_in, (int)c.n, (int)c.r, P, st);
+    }));
+    HIPTRY(timed(K_MULTI_UPDATE, 2 * Md * c.d_out * c.r, 4 * Md * c.d_out, st, [&] {
+      return launch_multi_update(4, P, B, c.index, c.M, c.d_out, (int)c.n, (int)c.r, false, Y, st);
+    }));
+    const EpiArgs ep{nullptr, Y, nullptr, LORA_ACT_NONE};
+    return forward_impl(LORA_F32, c.M, c.d_in, c.d_out, 0, 0.f, X, W, nullptr, nullptr, nullptr, nullptr, Y, w + L.base,
+                        L.y.base.L, st, P, c.r, nullptr, &ep);
+  }
+  TRY(multi_lists(c, L, L.y, false, B, w, st));
+  float* part = reinterpret_cast<float*>(w + L.part);
+  uint16_t* P = reinterpret_cast<uint16_t*>(w + L.p);
+  const GemmArgs a = multi_panel_args(c, L, X, c.d_in, A, L.ksplit_p, part, w);
+  HIPTRY(timed(K_MULTI_PANEL, 2 * Md * kr, 2 * Md * c.d_in + 4 * Md * c.r * L.splits_p, st,
+               [&] { return launch_multi_panel(a, L.splits_p, nullptr, 0, st); }));
+  MultiStrip s = multi_strips(c, L, L.y, w);
+  s.part[0] = part; s.splits[0] = L.splits_p; s.P[0] = P;
+  HIPTRY(timed(K_MULTI_STRIP, 0, 4 * Md * c.r * L.splits_p, st, [&] { return launch_multi_strip(s, st); }));
+  return multi_bf16(c, L, L.y, X, c.d_in, W, c.d_out, P, B, Y, w, st);
+}
+
+int multi_backward(const MultiCall& c, const MultiLayout& L, const void* X, const void* W, const void* W_t, const void* A,
+                   const void* B, const void* dY, void* dX, void* dA, void* dB, int gb, char* w, hipStream_t st) {
+  const int n = (int)c.n, r = (int)c.r, eb = elem_bytes(c.dtype);
+  const double Md = double(c.M);
+  const MultiTranspose tb{B, w + L.bt, c.d_out, c.r}, ta{A, w + L.at, c.r, c.d_in};
+  HIPTRY(timed(K_TRANSPOSE, 0, 2.0 * eb * n * r * (c.d_out + (dX ? c.d_in : 0)), st,
+               [&] { return launch_multi_transpose(eb, tb, dX ? &ta : nullptr, n, st); }));
+  if (c.dtype == LORA_F32) {
+    float *P = reinterpret_cast<float*>(w + L.p), *Q = reinterpret_cast<float*>(w + L.pt);
+    HIPTRY(timed(K_MULTI_PANEL, 2 * Md * r * (c.d_in + c.d_out), 4 * Md * (c.d_in + c.d_out), st, [&] {
+      const hipError_t e = launch_multi_dot(4, X, A, c.scales, c.index, c.M, c.d_in, n, r, P, st);
+      return e != hipSuccess ? e : launch_multi_dot(4, dY, w + L.bt, c.scales, c.index, c.M, c.d_out, n, r, Q, st);
+    }));
+    if (dX) {
+      int S = 1;
+      int64_t ks = 0;
+      f32_split(cdiv(c.M, 64) * cdiv(c.d_in, 128), c.d_out, &S, &ks);
+      auto update = [&](bool add) {
+        return timed(K_MULTI_UPDATE, 2 * Md * c.d_in * r, 4 * Md * c.d_in, st, [&] {
+          return launch_multi_update(4, Q, w + L.at, c.index, c.M, c.d_in, n, r, add, dX, st);
+        });
+      };
+      GemmArgs a = blank();
+      a.a1 = dY; a.lda1 = c.d_out; a.b1 = W; a.ldb1 = c.d_in; a.K1 = c.d_out;
+      a.m_load = a.m_store = c.M; a.n_load = a.n_store = c.d_in; a.c = dX; a.ldc = c.d_in;
+      const double flop = 2 * Md * c.d_in * c.d_out, bytes = 4 * (Md * (c.d_in + c.d_out) + double(c.d_in) * c.d_out);
+      if (S > 1) {
+        float* sp = reinterpret_cast<float*>(w + L.base);
+        HIPTRY(update(false));
+        a.k_split = ks; a.c = sp; a.part_stride = c.M * c.d_in;
+        HIPTRY(gemm(G_F32_NN_PARTIAL, a, S, st, flop, bytes));
+        HIPTRY(timed(K_FINISH, double(S) * Md * c.d_in, 4.0 * (S + 2) * Md * c.d_in, st, [&] {
+          return launch_split_finish_epi(4, sp, S, c.M * c.d_in, c.M, c.d_in, dX, EpiArgs{nullptr, dX, nullptr, LORA_ACT_NONE},
+                                         st);
+        }));
+      } else {
+        HIPTRY(gemm(G_F32_NN_STORE, a, 1, st, flop, bytes));
+        HIPTRY(update(true));
+      }
+    }
+    HIPTRY(timed(K_MULTI_GRAD, 2 * Md * r * (c.d_in + c.d_out), 4 * Md * (c.d_in + c.d_out), st, [&] {
+      const hipError_t e = launch_multi_outer(P, static_cast<const float*>(dY), c.index, c.M, c.d_out, n, r, true, gb, dB, st);
+      return e != hipSuccess ? e : launch_multi_outer(Q, static_cast<const float*>(X), c.index, c.M, c.d_in, n, r, false, gb, dA, st);
+    }));
+    return LORA_OK;
+  }
+  if (dX && !W_t) {
+    HIPTRY(timed(K_TRANSPOSE_W, 0, 4.0 * c.d_in * c.d_out, st, [&] {
+      return launch_transpose_tile(static_cast<const uint16_t*>(W), c.d_in, c.d_out, c.d_in,
+                                   reinterpret_cast<uint16_t*>(w + L.wt), c.d_out, c.d_out, st);
+    }));
+    W_t = w + L.wt;
+  }
+  TRY(multi_lists(c, L, L.dx, true, A, w, st));
+  float *pp = reinterpret_cast<float*>(w + L.part), *pq = reinterpret_cast<float*>(w + L.partq);
+  const GemmArgs a = multi_panel_args(c, L, X, c.d_in, A, L.ksplit_p, pp, w);
+  const GemmArgs b = multi_panel_args(c, L, dY, c.d_out, w + L.bt, L.ksplit_q, pq, w);
+  HIPTRY(timed(K_MULTI_PANEL, 2 * Md * r * (c.d_in + c.d_out), 2 * Md * (c.d_in + c.d_out), st,
+               [&] { return launch_multi_panel(a, L.splits_p, &b, L.splits_q, st); }));
+  uint16_t *Q = dX ? reinterpret_cast<uint16_t*>(w + L.p) : nullptr, *Pt = reinterpret_cast<uint16_t*>(w + L.pt),
+           *Qt = reinterpret_cast<uint16_t*>(w + L.qt);
+  MultiStrip s = multi_strips(c, L, L.dx, w);
+  s.ops = 2;
+  s.part[0] = pp; s.splits[0] = L.splits_p; s.Pt[0] = Pt;
+  s.part[1] = pq; s.splits[1] = L.splits_q; s.P[1] = Q; s.Pt[1] = Qt;
+  s.mask = reinterpret_cast<int*>(w + L.mask); s.gbad = reinterpret_cast<int*>(w + L.gbad);
+  HIPTRY(timed(K_MULTI_STRIP, 0, 4 * Md * r * (L.splits_p + L.splits_q), st, [&] { return launch_multi_strip(s, st); }));
+  if (dX) TRY(multi_bf16(c, L, L.dx, dY, c.d_out, W_t, c.d_in, Q, w + L.at, dX, w, st));
+  auto grad = [&](const uint16_t* At, const void* T, int64_t N, size_t part) {
+    GemmArgs g = blank();
+    g.a1 = At; g.lda1 = L.M8; g.b1 = T; g.ldb1 = N; g.K1 = c.M;
+    g.n_load = g.n_store = N; g.c = w + part; g.ldc = N; g.part_stride = c.n * c.r * N;
+    g.ad_list = reinterpret_cast<int*>(w + L.glist); g.ad_cnt = reinterpret_cast<int*>(w + L.gcnt); g.ad_cap = (int)cdiv(c.M, 64);
+    g.ad_of = reinterpret_cast<int*>(w + L.mask);
+    return g;
+  };
+  const GemmArgs gB = grad(Pt, dY, c.d_out, L.partb), gA = grad(Qt, X, c.d_in, L.parta);
+  HIPTRY(timed(K_MULTI_GRAD, 2 * Md * r * (c.d_in + c.d_out), 2 * Md * (c.d_in + c.d_out), st,
+               [&] { return launch_multi_grad(gB, L.splits_b, gA, L.splits_a, L.per * r, n * r, st); }));
+  const MultiGradSum mb{reinterpret_cast<float*>(w + L.partb), L.splits_b, c.d_out, 1, dB},
+      ma{reinterpret_cast<float*>(w + L.parta), L.splits_a, c.d_in, 0, dA};
+  HIPTRY(timed(K_REDUCE, 0, 4.0 * n * r * (L.splits_b * double(c.d_out) + L.splits_a * double(c.d_in)), st,
+               [&] { return launch_multi_grad_sum(gb, mb, ma, reinterpret_cast<int*>(w + L.gbad), n, r, st); }));
+  return LORA_OK;
+}
+
+int check_multi(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r) {
+  if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_ERR_DTYPE;
+  TRY(check_sizes(M, d_in, d_out, r));
+  if (d_in > LORA_EPI_MAX_D_OUT || d_out > LORA_EPI_MAX_D_OUT || r % 8 || r > LORA_MULTI_MAX_RANK || n < 1 ||
+      n > LORA_MULTI_MAX_ADAPTERS)
+    return LORA_ERR_SHAPE;
+  return LORA_OK;
+}
+
 constexpr size_t kStaticScratchBytes = size_t(LORA_STATIC_SCRATCH_BYTES);
 
 std::mutex g_scratch_mu;
@@ -2318,6 +2660,58 @@ int lora_act8_linear_bwd(int dtype, int64_t M, int64_t d_in, const lora_group_me
   return backward_impl(dtype, M, d_in, m.d_out, m.r, m.scale, X, m.W, m.W_nf4 ? &q : nullptr, m.A, m.B, nullptr, m.dY,
                        m.dX, m.dA, m.dB, ws, E.E.L, st, nullptr, nullptr, nullptr,
                        E.E.L.dx_nt && !m.W_nf4 ? m.W_t : nullptr);
+}
+
+// ---- an adapter of its own for every row ----
+size_t lora_multi_workspace_bytes(int backward, int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r,
+                                  int have_w_t, int need_dx) {
+  if (check_multi(dtype, M, d_in, d_out, n, r) != LORA_OK) return 0;
+  return make_multi_layout(backward != 0, dtype, M, d_in, d_out, n, r, have_w_t != 0, need_dx != 0).total;
+}
+
+int lora_multi_fwd(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r, const void* X, const void* W,
+                   const void* A, const void* B, const float* scales, const int32_t* index, void* Y, void* ws,
+                   size_t ws_bytes, void* stream) {
+  TRY(check_multi(dtype, M, d_in, d_out, n, r));
+  TRY(check_ptrs({W, A, B}));
+  TRY(check_elems({{scales, 4}}, true));
+  if (M > 0) {
+    TRY(check_ptrs({X, Y}));
+    TRY(check_elems({{index, 4}}, true));
+  }
+  const MultiLayout L = make_multi_layout(false, dtype, M, d_in, d_out, n, r, false, false);
+  TRY(check_ws_bytes(L.total, ws, ws_bytes));
+  TRY(check_device());
+  if (M == 0) return LORA_OK;
+  const MultiCall c{dtype, M, d_in, d_out, n, r, scales, index};
+  return multi_forward(c, L, X, W, A, B, Y, static_cast<char*>(ws), static_cast<hipStream_t>(stream));
+}
+
+int lora_multi_bwd(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r, const void* X, const void* W,
+                   const void* W_t, const void* A, const void* B, const float* scales, const int32_t* index, const void* dY,
+                   void* dX, void* dA, void* dB, int grad_dtype, void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_multi(dtype, M, d_in, d_out, n, r));
+  if (grad_dtype != LORA_F32 && grad_dtype != LORA_BF16) return LORA_ERR_DTYPE;
+  TRY(check_ptrs({W, A, B, dA, dB}));
+  TRY(check_elems({{scales, 4}}, true));
+  if (!aligned16(W_t) || !aligned16(dX)) return LORA_ERR_ALIGN;
+  if (M > 0) {
+    TRY(check_ptrs({X, dY}));
+    TRY(check_elems({{index, 4}}, true));
+  }
+  const MultiLayout L = make_multi_layout(true, dtype, M, d_in, d_out, n, r, W_t != nullptr, dX != nullptr);
+  TRY(check_ws_bytes(L.total, ws, ws_bytes));
+  TRY(check_device());
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const int gb = elem_bytes(grad_dtype);
+  if (M == 0) {
+    // (an even number of elements)
+    HIPTRY(timed(K_FILL, 0, double(gb) * n * r * d_in, st, [&] { return launch_fill_zero(static_cast<float*>(dA), n * r * d_in * gb / 4, st); }));
+    HIPTRY(timed(K_FILL, 0, double(gb) * n * r * d_out, st, [&] { return launch_fill_zero(static_cast<float*>(dB), n * r * d_out * gb / 4, st); }));
+    return LORA_OK;
+  }
+  const MultiCall c{dtype, M, d_in, d_out, n, r, scales, index};
+  return multi_backward(c, L, X, W, W_t, A, B, dY, dX, dA, dB, gb, static_cast<char*>(ws), st);
 }
 
 // ---- token log-probabilities ----

@@ -146,7 +146,26 @@ struct GemmArgs {
   int st_full, st_half, st_early;
   float* st_part;
   int* st_cnt;
+  // An adapter of its own for every row (multi.hip).  ad_of [rows]: the row's
+  // adapter; per tile of rows ad_list [tile][ad_cap], the ad_cnt[tile] adapters
+  // its rows carry.  A GEMM's second segment is then those adapters one after
+  // the other, ad_r columns each: a2 [rows, ad_r] holds each row's own columns
+  // (the others' read as zeros), b2 [adapters][n_load, ad_r] at ad_step elements
+  // each.  A panel's columns are theirs likewise, 64 a block, b1
+  // [adapters * ad_r, K1], and C [rows, ad_r] takes each row's own.
+  const int* ad_of;
+  const int* ad_list;
+  const int* ad_cnt;
+  int ad_cap, ad_r, ad_n;  // (ad_n adapters)
+  int64_t ad_step;
 };
+
+// What a kernel reads through the scalar cache: uniform addresses, written
+// before the launch.  (Loaded the ordinary way such a value would be waited for
+// in the order of the loads, with every LDS DMA in flight before it.)
+__device__ __forceinline__ int scalar_at(const int* p, int64_t i) {
+  return reinterpret_cast<const __attribute__((address_space(4))) int*>(reinterpret_cast<uintptr_t>(p))[i];
+}
 
 __device__ __forceinline__ int lds_off(int row, int chunk) {
   return (row << 7) + ((chunk ^ (row & 7)) << 4);

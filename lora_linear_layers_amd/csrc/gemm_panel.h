@@ -63,9 +63,12 @@ struct Cfg {
 constexpr int vmcnt_imm(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }
 }  // namespace pdma
 
-// the partial of row tile mt over split z
-template <int BM, int BN>
-__device__ __forceinline__ void panel_dma_tile(const GemmArgs& p, const int mt, const int z) {
+// The partial of row tile mt over split z.  MULTI: rows with an adapter of their
+// own (GemmArgs::ad_list); the columns are the 64 from 64 cg of the adapters
+// that the tile's rows carry, and C takes each row's own.
+template <int BM, int BN, bool MULTI = false>
+__device__ __forceinline__ void panel_dma_tile(const GemmArgs& p, const int mt, const int z, const int cg = 0) {
+  static_assert(!MULTI || BN == 64, "64 columns a block");
   using namespace pdma;
   using C = Cfg<BM, BN>;
   constexpr int NS = C::NS, LEAD = NS - 1, FM = C::FM, FN = C::FN;
@@ -98,7 +101,15 @@ __device__ __forceinline__ void panel_dma_tile(const GemmArgs& p, const int mt, 
     const int row8 = 8 * (i + C::IB * wave);
     const void* src = p.b1;
     int off = 0, lim = (int)p.n_load;
-    for (int g = 0; g < p.n_src; ++g)
+    if constexpr (MULTI) {  // (ad_r is a multiple of 8: 8 rows lie in one adapter)
+      const int c8 = 8 * cg + i + C::IB * wave, rc = p.ad_r >> 3, slot = c8 / rc;
+      const bool in = slot < scalar_at(p.ad_cnt, mt);
+      const int64_t a = in ? scalar_at(p.ad_list, (int64_t)mt * p.ad_cap + slot) : 0;
+      src = static_cast<const char*>(p.b1) + (a * p.ad_r + 8 * (c8 - slot * rc)) * p.ldb1 * 2;
+      off = row8;
+      lim = in ? 8 : 0;
+    }
+    for (int g = 0; g < (MULTI ? 0 : p.n_src); ++g)
       if (row8 >= p.rs_beg[g]) {
         src = p.rs[g];
         off = p.rs_beg[g];
@@ -192,6 +203,22 @@ __device__ __forceinline__ void panel_dma_tile(const GemmArgs& p, const int mt, 
   // fp32 partial: acc[i][j][v] = C[m0 + wm BM / WM + 32 i + 8 (v / 4) + 4 hh + v % 4,
   //                                  wn BN / WN + 32 j + l32]
   float* out = reinterpret_cast<float*>(p.c) + (int64_t)z * p.part_stride;
+  if constexpr (MULTI) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int col = 64 * cg + wn * (BN / C::WN) + 32 * j + l32, slot = col / p.ad_r;
+      if (slot >= p.ad_cnt[mt]) continue;
+      const int a = p.ad_list[(int64_t)mt * p.ad_cap + slot];
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int64_t row = m0 + wm * (BM / C::WM) + 32 * i + 8 * (v >> 2) + 4 * hh + (v & 3);
+          if (row < p.m_store && p.ad_of[row] == a) out[row * p.ad_r + col - slot * p.ad_r] = acc[i][j][v];
+        }
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -267,9 +294,14 @@ struct Cfg {
 };
 }  // namespace sdma
 
-// column tile nt over split z
-template <int BR, int NS_>
-__device__ __forceinline__ void splitnn_dma_tile(const GemmArgs& p, const int nt, const int z) {
+// Column tile nt over split z.  LISTED: the tokens are those of the 64-token tiles
+// that p.ad_list names for row group rg (p.ad_cnt of them, in order), cut into
+// `splits` equal parts; Aop and C start at the group's first row.  p.ad_of holds
+// 64 bits a tile: tokens whose bit is clear are read as zeros from Bop (they
+// may hold anything; Aop has zeros for them).
+template <int BR, int NS_, bool LISTED = false>
+__device__ __forceinline__ void splitnn_dma_tile(const GemmArgs& p, const int nt, const int z, const int rg = 0,
+                                                 const int splits = 1) {
   using namespace sdma;
   using C = Cfg<BR, NS_>;
   constexpr int NS = C::NS, LEAD = NS - 1, FM = C::FM, FN = C::FN;
@@ -285,9 +317,12 @@ __device__ __forceinline__ void splitnn_dma_tile(const GemmArgs& p, const int nt
   // in vector registers, as a division of a flat id leaves it, makes the
   // compiler wrap every DMA in a loop over the lanes' values)
   const int64_t n0 = (int64_t)nt * BN;
-  const int64_t kbeg = (int64_t)z * p.k_split;
-  const int64_t kend = kbeg + p.k_split < p.K1 ? kbeg + p.k_split : p.K1;
-  const int nk = kend > kbeg ? (int)((kend - kbeg + BK - 1) / BK) : 0;
+  const int64_t kbeg = LISTED ? 0 : (int64_t)z * p.k_split;
+  const int64_t kend = LISTED ? p.K1 : kbeg + p.k_split < p.K1 ? kbeg + p.k_split : p.K1;
+  const int ngl = LISTED ? scalar_at(p.ad_cnt, rg) : 0;  // token tiles of the group, and this part's first
+  const int64_t lo = LISTED ? (int64_t)ngl * z / splits : 0;
+  const int nk = LISTED ? (int)((int64_t)ngl * (z + 1) / splits - lo)
+                        : kend > kbeg ? (int)((kend - kbeg + BK - 1) / BK) : 0;
   const int klen = (int)(kend - kbeg);
 
   // ---- DMA addressing ----
@@ -295,15 +330,18 @@ __device__ __forceinline__ void splitnn_dma_tile(const GemmArgs& p, const int nt
   const char* ga = reinterpret_cast<const char*>(p.a1) + kbeg * 2;                   // Aop [R, ld] at token kbeg
   const char* gb = reinterpret_cast<const char*>(p.b1) + (kbeg * p.ldb1 + n0) * 2;  // Bop token row kbeg, column n0
   const int64_t ncols = p.n_load - n0;  // columns of Bop left from n0
+  int64_t tk = 0;  // LISTED: the first token of the stage being requested, and the tokens left from it
+  int trem = 0;
+  uint32_t tmask[2] = {0u, 0u};
   auto dma_a = [&](int u, int s, int i) {
     const int dc = (i & 1) ? dco : dce;
     const int row = 8 * (i + C::IA * wave) + (lane >> 3);
-    const int kk = u * BK + 8 * dc;
-    const bool ok = kk < klen && row < p.m_load;
+    const int kk = (LISTED ? 0 : u * BK) + 8 * dc;
+    const bool ok = kk < (LISTED ? trem : klen) && row < p.m_load;
     uint32_t vo = ok ? (uint32_t)(row * p.lda1 * 2 + kk * 2) : w4::OOB;
     asm volatile("" : "+v"(vo));
-    const __amdgpu_buffer_rsrc_t r =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(ga), (short)0, w4::BIG, 0x00020000);
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(LISTED ? ga + tk * 2 : ga), (short)0, w4::BIG, 0x00020000);
     char* dst = smem + s * C::STAGE + (8 * (i + C::IA * wave)) * 128;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, (int)vo, 0, 0,
                                              0);
@@ -312,17 +350,25 @@ __device__ __forceinline__ void splitnn_dma_tile(const GemmArgs& p, const int nt
     const int k = 16 * wave + 2 * i + (lane >> 5);  // token row within the stage
     const int f = (k & 3) | ((k >> 1) & 4);
     const int c = (lane & 31) ^ (2 * f);  // logical 16-byte chunk
-    const bool ok = u * BK + k < klen && 8 * c < ncols;
-    uint32_t vo = ok ? (uint32_t)(((int64_t)(u * BK + k) * p.ldb1 + 8 * c) * 2) : w4::OOB;
+    const int kk = (LISTED ? 0 : u * BK) + k;
+    const bool ok = (LISTED ? ((k & 32 ? tmask[1] : tmask[0]) >> (k & 31) & 1u) != 0 : kk < klen) && 8 * c < ncols;
+    uint32_t vo = ok ? (uint32_t)(((int64_t)kk * p.ldb1 + 8 * c) * 2) : w4::OOB;
     asm volatile("" : "+v"(vo));
-    const __amdgpu_buffer_rsrc_t r =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(gb), (short)0, w4::BIG, 0x00020000);
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(LISTED ? gb + tk * p.ldb1 * 2 : gb), (short)0, w4::BIG, 0x00020000);
     char* dst = smem + s * C::STAGE + A_BYTES + (16 * wave + 2 * i) * 512;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, (int)vo, 0, 0,
                                              0);
   };
   auto issue = [&](int u) {
     const int s = u % NS;
+    if constexpr (LISTED) {
+      const int64_t tile = u < nk ? scalar_at(p.ad_list, (int64_t)rg * p.ad_cap + lo + u) : 0;
+      tk = tile * BK;
+      trem = u < nk ? (int)min(p.K1 - tk, (int64_t)BK) : 0;
+      tmask[0] = u < nk ? (uint32_t)scalar_at(p.ad_of, 2 * tile) : 0u;
+      tmask[1] = u < nk ? (uint32_t)scalar_at(p.ad_of, 2 * tile + 1) : 0u;
+    }
 #pragma unroll
     for (int i = 0; i < C::IA; ++i) dma_a(u, s, i);
 #pragma unroll

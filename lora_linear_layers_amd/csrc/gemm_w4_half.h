@@ -56,7 +56,7 @@ __device__ __forceinline__ void w4h_tile(int b, int blocks, int tm, int tn, int&
   mt = 8 * band + in - nt * rows;
 }
 
-template <int EPI>
+template <int EPI, bool MULTI = false>
 __global__ void __launch_bounds__(w4::NT) __attribute__((amdgpu_waves_per_eu(1, 1)))
 gemm_w4_half_kernel(const GemmArgs p) {
   using w4::BN;
@@ -76,7 +76,27 @@ gemm_w4_half_kernel(const GemmArgs p) {
 
   const int n1 = (int)(p.K1 / BKS), kt = (int)(p.K1 % BKS);  // whole stages of the main segment, columns of a last one
   const int n1t = n1 + (kt ? 1 : 0);
-  const int n = n1t + (int)((p.K2 + BKS - 1) / BKS);
+
+  int mt, nt;
+  w4h_tile((int)blockIdx.x, (int)gridDim.x, p.tiles_m, (int)((p.n_store + BN - 1) / BN), mt, nt);
+  mt = __builtin_amdgcn_readfirstlane(mt);
+  nt = __builtin_amdgcn_readfirstlane(nt);
+  const int64_t m0 = (int64_t)mt * BM, n0 = (int64_t)nt * BN;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // A instruction i (< 4) of wave w moves rows 32 w + 8 i + lane / 8, B instruction
+  // i (< 8) rows 64 w + 8 i + lane / 8
+  const int rowa = 32 * wave + (lane >> 3), rowb = 64 * wave + (lane >> 3);
+  // MULTI: the tile's adapters, and those of the rows that this lane moves
+  int ads = 0;
+  uint32_t adl[1], rad[2];
+  if constexpr (MULTI) {
+    ads = scalar_at(p.ad_cnt, mt);
+    ad_load_list(p, mt, ads, lane, adl);
+    ad_load_rows(p, m0 + rowa, rad);
+  }
+  const int rank2 = MULTI ? ads * p.ad_r : (int)p.K2;  // columns of the second segment
+  const int n = n1t + (rank2 + BKS - 1) / BKS;
 
   auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
   using I0 = std::integral_constant<int, 0>;
@@ -84,15 +104,9 @@ gemm_w4_half_kernel(const GemmArgs p) {
   using T_ = std::true_type;
   using F_ = std::false_type;
 
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int l32 = lane & 31, hh = lane >> 5;
-  const int dr = lane >> 3;
   const int dce = (lane & 7) ^ (lane >> 4), dco = (lane & 7) ^ ((lane >> 4) | 4);
-  // A instruction i (< 4) of wave w moves rows 32 w + 8 i + dr, B instruction
-  // i (< 8) rows 64 w + 8 i + dr
-  const int rowa = 32 * wave + dr, rowb = 64 * wave + dr;
   const uint32_t ra1 = (uint32_t)(rowa * p.lda1 * 2), ra2 = (uint32_t)(rowa * p.lda2 * 2);
   const uint32_t rb1 = (uint32_t)(rowb * p.ldb1 * 2), rb2 = (uint32_t)(rowb * p.ldb2 * 2);
   const uint32_t va1[2] = {ra1 + (uint32_t)(dce * 16), ra1 + (uint32_t)(8 * p.lda1 * 2 + dco * 16)};
@@ -124,10 +138,6 @@ gemm_w4_half_kernel(const GemmArgs p) {
         __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[f][q >> 2], fb[f][q & 3], acc[q >> 2][q & 3], 0, 0, 0);
   };
 
-  int mt, nt;
-  w4h_tile((int)blockIdx.x, (int)gridDim.x, p.tiles_m, (int)((p.n_store + BN - 1) / BN), mt, nt);
-  const int64_t m0 = (int64_t)__builtin_amdgcn_readfirstlane(mt) * BM;
-  const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane(nt) * BN;
   const char* ga1 = reinterpret_cast<const char*>(p.a1) + m0 * p.lda1 * 2;
   const char* ga2 = reinterpret_cast<const char*>(p.a2) + m0 * p.lda2 * 2;
   const char* gb1 = reinterpret_cast<const char*>(p.b1) + n0 * p.ldb1 * 2;
@@ -137,8 +147,18 @@ gemm_w4_half_kernel(const GemmArgs p) {
   const int la1 = (int)(ma * p.lda1 * 2), la2 = (int)(ma * p.lda2 * 2);
   const int lb1 = (int)(nb * p.ldb1 * 2), lb2 = (int)(nb * p.ldb2 * 2);
 
+  // MULTI: the lane's rows of a strip and of the second operand, in bytes; the latter's end
+  const uint32_t isr = (uint32_t)(p.ad_r * 2), ar2 = rowa * isr, br2 = rowb * isr;
+  const int adlen = MULTI ? (int)(uint32_t)(p.ad_n * p.ad_step * 2 - n0 * p.ldb2 * 2) : 0;
+  auto seg_of = [&](int u) {
+    if constexpr (MULTI)
+      return ad_seg(p, adl, ads, u - n1t, dce, dco);
+    else
+      return AdSeg{};
+  };
+
   // One DMA: stage u, operand op (0 A, 1 B), instruction i, ring stage s.
-  auto dma = [&](int u, int s, int op, int i, auto seg2_c) {
+  auto dma = [&](int u, int s, int op, int i, auto seg2_c, const AdSeg& sg) {
     constexpr bool SEG2 = decltype(seg2_c)::value;
     const int odd = i & 1, pair = i >> 1;
     const char* base;
@@ -157,6 +177,17 @@ gemm_w4_half_kernel(const GemmArgs p) {
         len = (op == 0 ? la1 : lb1) - u * (BKS * 2);
         vo = 8 * dc < kt ? (op == 0 ? va1[odd] : vb1[odd]) : w4::OOB;
         is = op == 0 ? isa1 : isb1;
+      } else if constexpr (MULTI) {
+        if (op == 0) {
+          base = ga2;
+          len = la2;
+          vo = (rad[(i >> 1) & 1] >> (16 * (i & 1)) & 0xFFFFu) == sg.a[odd] ? ar2 + (uint32_t)(8 * i) * isr + sg.q[odd] : AD_OOB;
+        } else {  // (rows past the last read the next adapter's, into columns that are not stored)
+          base = gb2;
+          len = adlen;
+          vo = sg.b[odd] + br2 + (uint32_t)(8 * i) * isr;
+        }
+        is = 0;
       } else {
         const int kk = tt * BKS + 8 * dc;  // the lane's first rank column
         const uint32_t kc = (uint32_t)(tt * BKS * 2 + dc * 16);
@@ -184,10 +215,11 @@ gemm_w4_half_kernel(const GemmArgs p) {
   for (int u = 0; u < 2; ++u) {
     if (u < n1) {
 #pragma unroll
-      for (int i = 0; i < 12; ++i) dma(u, u, i < 4 ? 0 : 1, i < 4 ? i : i - 4, F_{});
+      for (int i = 0; i < 12; ++i) dma(u, u, i < 4 ? 0 : 1, i < 4 ? i : i - 4, F_{}, AdSeg{});
     } else if (u < n) {
+      const AdSeg sg = seg_of(u);
 #pragma unroll
-      for (int i = 0; i < 12; ++i) dma(u, u, i < 4 ? 0 : 1, i < 4 ? i : i - 4, T_{});
+      for (int i = 0; i < 12; ++i) dma(u, u, i < 4 ? 0 : 1, i < 4 ? i : i - 4, T_{}, sg);
     }
   }
   if (n >= 2)
@@ -204,26 +236,27 @@ gemm_w4_half_kernel(const GemmArgs p) {
     constexpr int ISSUE = decltype(issue_c)::value;
     constexpr bool NEXT = decltype(next_c)::value;
     using S2 = std::integral_constant<bool, ISSUE == 2>;
+    const AdSeg sg = ISSUE == 2 ? seg_of(t + 2) : AdSeg{};
     const int s = t % NS, s1 = (t + 1) % NS, s2 = (t + 2) % NS;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       mf(I0{}, q);
       if (q < 6) rd1(s, 1, I1{}, q);
-      if (ISSUE && (q & 1)) dma(t + 2, s2, 0, q >> 1, S2{});
+      if (ISSUE && (q & 1)) dma(t + 2, s2, 0, q >> 1, S2{}, sg);
       fence();
     }
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       mf(I1{}, q);
       if (q < 6) rd1(s, 2, I0{}, q);
-      if (ISSUE && (q & 1)) dma(t + 2, s2, 1, q >> 1, S2{});
+      if (ISSUE && (q & 1)) dma(t + 2, s2, 1, q >> 1, S2{}, sg);
       fence();
     }
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       mf(I0{}, q);
       if (q < 6) rd1(s, 3, I1{}, q);
-      if (ISSUE && (q & 1)) dma(t + 2, s2, 1, 4 + (q >> 1), S2{});
+      if (ISSUE && (q & 1)) dma(t + 2, s2, 1, 4 + (q >> 1), S2{}, sg);
       fence();
     }
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(ISSUE ? 12 : 0));

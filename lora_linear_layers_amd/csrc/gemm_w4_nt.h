@@ -68,6 +68,76 @@ constexpr int vmcnt_imm(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }
 
 typedef __attribute__((address_space(3))) void lds_void_t;
 
+// Rows with an adapter of their own: the adapters' second operands lie in one
+// resource of less than AD_MAX bytes; a lane without a value takes AD_OOB.
+constexpr uint32_t AD_MAX = 0xE0000000u, AD_OOB = 0xF0000000u;
+// A list's entry is an adapter below AD_BAD, or with AD_BAD one whose second
+// operand holds an infinity or a NaN: it is read as zeros (times the other rows'
+// zeros it would be a NaN), and its own rows have strips of NaNs.
+constexpr uint32_t AD_NONE = 0xFFFFu, AD_BAD = 0x4000u;
+
+// A tile's adapters (GemmArgs::ad_list) over the lanes, 128 a register: entry e
+// in lane e % 64, low half for e % 128 < 64.
+template <int NL>
+__device__ __forceinline__ void ad_load_list(const GemmArgs& p, int tile, int ads, int lane, uint32_t (&l)[NL]) {
+  const int* list = p.ad_list + (int64_t)tile * p.ad_cap;
+#pragma unroll
+  for (int k = 0; k < NL; ++k) {
+    const int e = 128 * k + lane;
+    const uint32_t lo = e < ads ? (uint32_t)list[e] : AD_NONE, hi = e + 64 < ads ? (uint32_t)list[e + 64] : AD_NONE;
+    l[k] = lo | hi << 16;
+    asm volatile("" : "+v"(l[k]));  // (loaded here, ahead of the DMAs, not where it is used, behind them)
+  }
+}
+template <int NL>
+__device__ __forceinline__ uint32_t ad_entry(const uint32_t (&l)[NL], int e) {
+  uint32_t v = __shfl(l[0], e & 63);
+#pragma unroll
+  for (int k = 1; k < NL; ++k) {
+    const uint32_t w = __shfl(l[k], e & 63);
+    v = (e >> 7) == k ? w : v;
+  }
+  return (e & 64) ? v >> 16 : v & 0xFFFFu;
+}
+// What the lane's two chunks (of even and odd DMA instructions) of stage tt of
+// such a segment are: an adapter (AD_NONE + 1: none), the byte offset of its 8
+// columns in a strip, and that of its first row's in the second operand.
+struct AdSeg {
+  uint32_t a[2], q[2], b[2];
+};
+template <int NL>
+__device__ __forceinline__ AdSeg ad_seg(const GemmArgs& p, const uint32_t (&l)[NL], int ads, int tt, int dce, int dco) {
+  AdSeg s;
+  const uint32_t rc = (uint32_t)p.ad_r >> 3, step = (uint32_t)(p.ad_step * 2);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t c8 = (uint32_t)(8 * tt + (h ? dco : dce)), slot = c8 / rc;  // (8 columns lie in one adapter)
+    const uint32_t a = ad_entry(l, (int)slot);
+    const bool in = slot < (uint32_t)ads;
+    s.a[h] = in ? a & ~AD_BAD : AD_NONE + 1;
+    s.q[h] = 16 * (c8 - slot * rc);
+    s.b[h] = in && !(a & AD_BAD) ? a * step + s.q[h] : AD_OOB;
+  }
+  return s;
+}
+
+// The adapters of 2 NR rows 8 apart, two a register (AD_NONE: no such row, or no adapter).
+template <int NR>
+__device__ __forceinline__ void ad_load_rows(const GemmArgs& p, int64_t row, uint32_t (&a)[NR]) {
+#pragma unroll
+  for (int k = 0; k < NR; ++k) {
+    uint32_t v[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t r = row + 16 * k + 8 * h;
+      const uint32_t x = r < p.m_load ? (uint32_t)p.ad_of[r] : AD_NONE;
+      v[h] = x < (uint32_t)p.ad_n ? x : AD_NONE;
+    }
+    a[k] = v[0] | v[1] << 16;
+    asm volatile("" : "+v"(a[k]));
+  }
+}
+
 template <int EPI>
 __global__ void __launch_bounds__(w4::NT) __attribute__((amdgpu_waves_per_eu(1, 1)))
 gemm_w4_nt_kernel(const GemmArgs p) {

@@ -40,7 +40,7 @@
 
 namespace lora {
 
-template <int EPI>
+template <int EPI, bool MULTI = false>
 __global__ void __launch_bounds__(w4::NT) __attribute__((amdgpu_waves_per_eu(1, 1)))
 gemm_w4_stream_kernel(const GemmArgs p) {
   using namespace w4;
@@ -55,12 +55,26 @@ gemm_w4_stream_kernel(const GemmArgs p) {
 
   const int nk1 = (int)(p.K1 / BKS), kt = (int)(p.K1 % BKS);  // whole stages of the main segment, columns of a last one
   const int nk1t = nk1 + (kt ? 1 : 0);
-  const int nk = nk1t + (int)((p.K2 + BKS - 1) / BKS);
 
   // the block's tile and its stages [s0, s0 + n) of it
   const int bid = blockIdx.x, hb = bid - p.st_full;
   const bool part = hb >= 0;
   const int tile = part ? p.st_full + (hb >> 1) : bid;
+  const int mt = __builtin_amdgcn_readfirstlane(tile % p.tiles_m), nt = __builtin_amdgcn_readfirstlane(tile / p.tiles_m);
+  const int64_t m0 = (int64_t)mt * BM, n0 = (int64_t)nt * BN;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int row0 = 64 * wave + (lane >> 3);
+  // MULTI: the tile's adapters, and those of the rows that this lane moves
+  int ads = 0;
+  uint32_t adl[2], rad[4];
+  if constexpr (MULTI) {
+    ads = scalar_at(p.ad_cnt, mt);
+    ad_load_list(p, mt, ads, lane, adl);
+    ad_load_rows(p, m0 + row0, rad);
+  }
+  const int rank2 = MULTI ? ads * p.ad_r : (int)p.K2;  // columns of the second segment
+  const int nk = nk1t + (rank2 + BKS - 1) / BKS;
   const int mid = nk / 2 - p.st_early;
   const int s0 = part && (hb & 1) ? mid : 0;
   const int n = part ? (hb & 1 ? nk - mid : mid) : nk;
@@ -71,13 +85,9 @@ gemm_w4_stream_kernel(const GemmArgs p) {
   using T_ = std::true_type;
   using F_ = std::false_type;
 
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int l32 = lane & 31, hh = lane >> 5;
-  const int dr = lane >> 3;
   const int dce = (lane & 7) ^ (lane >> 4), dco = (lane & 7) ^ ((lane >> 4) | 4);
-  const int row0 = 64 * wave + dr;
   const uint32_t ra1 = (uint32_t)(row0 * p.lda1 * 2), ra2 = (uint32_t)(row0 * p.lda2 * 2);
   const uint32_t rb1 = (uint32_t)(row0 * p.ldb1 * 2), rb2 = (uint32_t)(row0 * p.ldb2 * 2);
   const uint32_t va1[2] = {ra1 + (uint32_t)(dce * 16), ra1 + (uint32_t)(8 * p.lda1 * 2 + dco * 16)};
@@ -110,8 +120,6 @@ gemm_w4_stream_kernel(const GemmArgs p) {
         __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[f][q >> 2], fb[f][q & 3], acc[q >> 2][q & 3], 0, 0, 0);
   };
 
-  const int64_t m0 = (int64_t)(tile % p.tiles_m) * BM;
-  const int64_t n0 = (int64_t)(tile / p.tiles_m) * BN;
   const int n1 = max(0, min(nk1 - s0, n));  // stages of the main segment
   const char* ga1 = reinterpret_cast<const char*>(p.a1) + m0 * p.lda1 * 2 + (int64_t)s0 * (BKS * 2);
   const char* ga2 = reinterpret_cast<const char*>(p.a2) + m0 * p.lda2 * 2;
@@ -122,9 +130,19 @@ gemm_w4_stream_kernel(const GemmArgs p) {
   const int la1 = (int)(ma * p.lda1 * 2) - s0 * (BKS * 2), la2 = (int)(ma * p.lda2 * 2);
   const int lb1 = (int)(nb_ * p.ldb1 * 2) - s0 * (BKS * 2), lb2 = (int)(nb_ * p.ldb2 * 2);
 
+  // MULTI: the lane's rows of a strip and of the second operand, in bytes; the latter's end
+  const uint32_t isr = (uint32_t)(p.ad_r * 2), ar2 = row0 * isr, br2 = row0 * isr;
+  const int adlen = MULTI ? (int)(uint32_t)(p.ad_n * p.ad_step * 2 - n0 * p.ldb2 * 2) : 0;
+  auto seg_of = [&](int u) {
+    if constexpr (MULTI)
+      return ad_seg(p, adl, ads, s0 + u - nk1t, dce, dco);
+    else
+      return AdSeg{};
+  };
+
   // One DMA: the block's stage u, operand op (0 A, 1 B), instruction i (< 8),
   // slot s.
-  auto dma = [&](int u, int s, int op, int i, auto seg2_c) {
+  auto dma = [&](int u, int s, int op, int i, auto seg2_c, const AdSeg& sg) {
     constexpr bool SEG2 = decltype(seg2_c)::value;
     const int odd = i & 1, pair = i >> 1;
     const char* base;
@@ -143,6 +161,17 @@ gemm_w4_stream_kernel(const GemmArgs p) {
         len = (op == 0 ? la1 : lb1) - u * (BKS * 2);
         vo = 8 * dc < kt ? (op == 0 ? va1[odd] : vb1[odd]) : w4::OOB;
         is = op == 0 ? isa1 : isb1;
+      } else if constexpr (MULTI) {
+        if (op == 0) {
+          base = ga2;
+          len = la2;
+          vo = (rad[(i >> 1) & 3] >> (16 * (i & 1)) & 0xFFFFu) == sg.a[odd] ? ar2 + (uint32_t)(8 * i) * isr + sg.q[odd] : AD_OOB;
+        } else {  // (rows past the last read the next adapter's, into columns that are not stored)
+          base = gb2;
+          len = adlen;
+          vo = sg.b[odd] + br2 + (uint32_t)(8 * i) * isr;
+        }
+        is = 0;
       } else {
         const int kk = tt * BKS + 8 * dc;  // the lane's first rank column
         const uint32_t kc = (uint32_t)(tt * BKS * 2 + dc * 16);
@@ -170,10 +199,11 @@ gemm_w4_stream_kernel(const GemmArgs p) {
   for (int u = 0; u < 2; ++u) {
     if (u < n1) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) dma(u, 2 * u + (i >> 3), i >> 3, i & 7, F_{});
+      for (int i = 0; i < 16; ++i) dma(u, 2 * u + (i >> 3), i >> 3, i & 7, F_{}, AdSeg{});
     } else if (u < n) {
+      const AdSeg sg = seg_of(u);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) dma(u, 2 * u + (i >> 3), i >> 3, i & 7, T_{});
+      for (int i = 0; i < 16; ++i) dma(u, 2 * u + (i >> 3), i >> 3, i & 7, T_{}, sg);
     }
   }
   if (n >= 2)
@@ -190,6 +220,7 @@ gemm_w4_stream_kernel(const GemmArgs p) {
     constexpr int ISSUE = decltype(issue_c)::value;
     constexpr bool NEXT = decltype(next_c)::value;
     using S2 = std::integral_constant<bool, ISSUE == 2>;
+    const AdSeg sg = ISSUE == 2 ? seg_of(t + 2) : AdSeg{};
     const int sa = (2 * t) % NSLOT, sbl = (2 * t + 1) % NSLOT;
     const int na = (2 * t + 2) % NSLOT, nb = (2 * t + 3) % NSLOT;
     const int fa2 = (2 * t + 4) % NSLOT;  // A(t+2): the slot of B(t-1)
@@ -200,7 +231,7 @@ gemm_w4_stream_kernel(const GemmArgs p) {
       if (q < 8)
         rd1(sa, sbl, 1, I1{}, q);
       else if (ISSUE && (q & 1) == 0)
-        dma(t + 2, fa2, 0, (q - 8) >> 1, S2{});
+        dma(t + 2, fa2, 0, (q - 8) >> 1, S2{}, sg);
       fence();
     }
 #pragma unroll
@@ -209,7 +240,7 @@ gemm_w4_stream_kernel(const GemmArgs p) {
       if (q < 8)
         rd1(sa, sbl, 2, I0{}, q);
       else if (ISSUE && (q & 1) == 0)
-        dma(t + 2, fa2, 0, 4 + ((q - 8) >> 1), S2{});
+        dma(t + 2, fa2, 0, 4 + ((q - 8) >> 1), S2{}, sg);
       fence();
     }
 #pragma unroll
@@ -226,7 +257,7 @@ gemm_w4_stream_kernel(const GemmArgs p) {
       if (q < 8) {
         if (NEXT) rd1(na, nb, 0, I0{}, q);
       } else if (ISSUE) {
-        dma(t + 2, fb2, 1, q - 8, S2{});
+        dma(t + 2, fb2, 1, q - 8, S2{}, sg);
       }
       fence();
     }

@@ -352,4 +352,84 @@ hipError_t launch_act8_pack(int elem_bytes, const void* X, int64_t ldx, int64_t 
 hipError_t launch_act8_unpack(int elem_bytes, const uint8_t* codes, const float* scale8, int64_t M, int64_t d, void* X,
                               hipStream_t st);
 
+// Rows with an adapter of their own (multi.hip).  index int [M]: a row's adapter,
+// none outside [0, n).  Lists: per 128- and per 256-row tile its adapters
+// (rows of min(rows, n) entries and counts), per group of `per` adapters
+// (ceil(n / per) = groups) the 64-token tiles they occur in (rows of
+// ceil(M / 64)); counts of 0 blocks leave that list out.
+constexpr int kMultiMaxRank = 128;
+struct MultiLists {
+  const int* index;
+  int64_t M;
+  int n, per;
+  int t128, t256, groups;
+  int* list128;
+  int* cnt128;
+  int* list256;
+  int* cnt256;
+  int* glist;
+  int* gcnt;
+  int* zero;  // nzero ints cleared
+  int nzero;
+  // whether an adapter of a row holds infinities or NaNs in `scan` (bf16,
+  // scan16 16-byte pieces an adapter): bad [n][chunks], a chunk 4096 pieces
+  const void* scan;
+  int64_t scan16;
+  int chunks;
+  int* bad;
+  __host__ __device__ int cap(int rows) const { return n < rows ? n : rows; }
+};
+hipError_t launch_multi_lists(const MultiLists& q, hipStream_t st);
+// bf16 strip partials: GemmArgs with ad_of, ad_list (128-row tiles), ad_cnt,
+// ad_cap, ad_r; C = fp32 [splits][M, ad_r].  b (may be NULL): another in the same launch.
+hipError_t launch_multi_panel(const GemmArgs& a, int sa, const GemmArgs* b, int sb, hipStream_t st);
+struct MultiStrip {
+  int ops;               // strips of one operand or of two
+  const float* part[2];  // [splits][M, r]
+  int splits[2];
+  uint16_t* P[2];        // [M, r], or NULL
+  uint16_t* Pt[2];       // [n r, ceil8(M)] in the groups' tiles, or NULL (both)
+  int* mask;             // with Pt: 64 bits a 64-token tile
+  int* gbad;             // with Pt: [n], cleared before
+  const int* index;
+  const float* scales;
+  int64_t M;
+  int n, r, per;
+  const int* bad;        // [n][chunks] of the lists (chunks 0: none)
+  int chunks;
+  int* list128;          // the product's lists, marked (one of the two, or none)
+  const int* cnt128;
+  int* list256;
+  const int* cnt256;
+};
+hipError_t launch_multi_strip(const MultiStrip& s, hipStream_t st);
+// The product with its rows' adapters (ad_list of 128-row tiles where low, else of 256-row ones).
+hipError_t launch_multi_gemm(GemmArgs a, bool low, hipStream_t st);
+// fp32 P [M, r] = s_a X A_a^T; out (+)= P B_a^T with B [n][N, r] and P of out's type;
+// transposes of [n][R, C] stacks.
+hipError_t launch_multi_dot(int elem_bytes, const void* X, const void* A, const float* scales, const int* index, int64_t M,
+                            int64_t K, int n, int r, float* P, hipStream_t st);
+hipError_t launch_multi_update(int elem_bytes, const void* P, const void* B, const int* index, int64_t M, int64_t N, int n, int r,
+                               bool add, void* out, hipStream_t st);
+struct MultiTranspose {
+  const void* src;
+  void* dst;
+  int64_t R, C;
+};
+hipError_t launch_multi_transpose(int elem_bytes, const MultiTranspose& a, const MultiTranspose* b, int n, hipStream_t st);
+// Gradient partials [splits][total, N] of two products Pt X (ad_list: the groups'
+// token tiles), `rows` rows of Pt a group; their sums.
+hipError_t launch_multi_grad(const GemmArgs& a, int sa, const GemmArgs& b, int sb, int rows, int total, hipStream_t st);
+struct MultiGradSum {
+  const float* part;
+  int splits;
+  int64_t N;
+  int tr;
+  void* out;
+};
+hipError_t launch_multi_grad_sum(int out_bytes, const MultiGradSum& a, const MultiGradSum& b, const int* gbad, int n, int r,
+                                 hipStream_t st);
+hipError_t launch_multi_outer(const float* P, const float* X, const int* index, int64_t M, int64_t N, int n, int r, bool tr,
+                              int out_bytes, void* out, hipStream_t st);
+
 }  // namespace lora

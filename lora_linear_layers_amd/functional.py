@@ -1096,3 +1096,86 @@ class LoraLinearAct8Function(torch.autograd.Function):
         need_dX, _, need_dA, need_dB = ctx.needs_input_grad[:4]
         dX, dA, dB = lora_act8_linear_bwd(codes, scale8, member, dY.contiguous(), need_dX)
         return (dX, None, dA.to(A.dtype) if need_dA else None, dB.to(B.dtype) if need_dB else None) + (None,) * 4
+
+
+# ---------------------------------------------------------------------------
+# an adapter of its own for every row
+# ---------------------------------------------------------------------------
+_I32 = (torch.int32,)
+
+
+def _multi_dims(X, W, A, B, scales, index):
+    dev, same = _gpu(X), (X.dtype,)
+    dt = L._dtype_code(X)
+    if X.dim() != 2 or W.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+        raise ValueError("shape mismatch: X [M,d_in], W [d_out,d_in], A [n,r,d_in], B [n,d_out,r]")
+    (M, d_in), d_out, (n, r, _) = X.shape, W.shape[0], A.shape
+    if W.shape != (d_out, d_in) or A.shape != (n, r, d_in) or B.shape != (n, d_out, r):
+        raise ValueError("shape mismatch: X [M,d_in], W [d_out,d_in], A [n,r,d_in], B [n,d_out,r]")
+    for name, t in (("X", X), ("W", W), ("A", A), ("B", B)):
+        _check(dev, name, t, same)
+    _check(dev, "scales", scales, _F32, n)
+    _check(dev, "index", index, _I32, M)
+    return dt, dev, M, d_in, d_out, n, r
+
+
+def _multi_ws(backward, dt, M, d_in, d_out, n, r, have_wt, need_dX, dev, ws):
+    """(workspace, its bytes)"""
+    if ws is not None:
+        return _check_ws(dev, ws, ws.nbytes), ws.nbytes
+    nb = int(L.lib().lora_multi_workspace_bytes(backward, dt, M, d_in, d_out, n, r, have_wt, need_dX))
+    return torch.empty(max(nb, 1), dtype=torch.uint8, device=dev), nb
+
+
+def lora_multi_fwd(X, W, A, B, scales, index, Y=None, ws=None):
+    """Y [M, d_out]: row t is W x_t + scales[a] B[a] (A[a] x_t) with a = index[t] (int32 [M]; outside [0, n): W x_t
+    alone), for n adapters A [n, r, d_in], B [n, d_out, r] and fp32 scales [n] over one frozen W [d_out, d_in]."""
+    dt, dev, M, d_in, d_out, n, r = _multi_dims(X, W, A, B, scales, index)
+    if Y is None:
+        Y = torch.empty(M, d_out, dtype=X.dtype, device=dev)
+    else:
+        _check(dev, "Y", Y, (X.dtype,), M * d_out)
+    ws, ws_bytes = _multi_ws(0, dt, M, d_in, d_out, n, r, 0, 0, dev, ws)
+    with _on(dev):
+        L._check("lora_multi_fwd", L.lib().lora_multi_fwd(
+            dt, M, d_in, d_out, n, r, L._ptr(X), L._ptr(W), L._ptr(A), L._ptr(B), L._ptr(scales), L._ptr(index),
+            L._ptr(Y), L._ptr(ws), ws_bytes, L._stream(dev)))
+    return Y
+
+
+def lora_multi_bwd(X, W, A, B, scales, index, dY, need_dX: bool = True, W_t=None, grad_dtype=torch.float32, ws=None):
+    """(dX or None, dA [n, r, d_in], dB [n, d_out, r]) of lora_multi_fwd, the adapters' gradients in grad_dtype (zeros for
+    an adapter without rows); W_t: W's transpose (bf16), where the caller keeps one."""
+    dt, dev, M, d_in, d_out, n, r = _multi_dims(X, W, A, B, scales, index)
+    _check(dev, "dY", dY, (X.dtype,), M * d_out)
+    if W_t is not None:
+        _check(dev, "W_t", W_t, (torch.bfloat16,), d_in * d_out)
+        if W_t.shape != (d_in, d_out):
+            raise ValueError("W_t must be the bf16 [d_in, d_out] transpose of W")
+    dX = torch.empty(M, d_in, dtype=X.dtype, device=dev) if need_dX else None
+    dA = torch.empty(n, r, d_in, dtype=grad_dtype, device=dev)
+    dB = torch.empty(n, d_out, r, dtype=grad_dtype, device=dev)
+    ws, ws_bytes = _multi_ws(1, dt, M, d_in, d_out, n, r, int(W_t is not None), int(need_dX), dev, ws)
+    with _on(dev):
+        L._check("lora_multi_bwd", L.lib().lora_multi_bwd(
+            dt, M, d_in, d_out, n, r, L._ptr(X), L._ptr(W), L._ptr(W_t), L._ptr(A), L._ptr(B), L._ptr(scales),
+            L._ptr(index), L._ptr(dY), L._ptr(dX), L._ptr(dA), L._ptr(dB), L._dtype_code(dA), L._ptr(ws), ws_bytes,
+            L._stream(dev)))
+    return dX, dA, dB
+
+
+class LoraMultiFunction(torch.autograd.Function):
+    """Y = LoraMultiFunction.apply(X, W, A, B, scales, index, W_t): lora_multi_fwd with gradients for X, A and B (W frozen)."""
+
+    @staticmethod
+    def forward(ctx, X, W, A, B, scales, index, W_t=None):
+        ctx.save_for_backward(X, W, A, B, scales, index, W_t)
+        return lora_multi_fwd(X, W, A, B, scales, index)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dY):
+        X, W, A, B, scales, index, W_t = ctx.saved_tensors
+        need_dX, _, need_dA, need_dB = ctx.needs_input_grad[:4]
+        dX, dA, dB = lora_multi_bwd(X, W, A, B, scales, index, dY.contiguous(), need_dX, W_t, X.dtype)
+        return dX, None, dA if need_dA else None, dB if need_dB else None, None, None, None

@@ -85,3 +85,34 @@ def test_act8_validation():
     assert call(m=rope) == ESHAPE
     no_grad = _lib.GroupMember(32, 8, 1.0, 0, P, None, None, P, P, None, P, P, None, P, None)
     assert call(m=no_grad) == ENULL
+
+
+def test_multi_validation():
+    lib = L.load()
+
+    def fwd(dtype=1, M=4, k=64, d=64, n=3, r=8, X=P, W=P, A=P, B=P, s=P, idx=P, Y=P, ws=P, nb=1 << 30):
+        return lib.lora_multi_fwd(dtype, M, k, d, n, r, X, W, A, B, s, idx, Y, ws, nb, None)
+
+    def bwd(dtype=1, M=4, n=3, W_t=None, dY=P, dX=P, dA=P, dB=P, gt=0, ws=P, nb=1 << 30):
+        return lib.lora_multi_bwd(dtype, M, 64, 64, n, 8, P, P, W_t, P, P, P, P, dY, dX, dA, dB, gt, ws, nb, None)
+    assert fwd(dtype=2) == EDTYPE
+    for kw in (dict(k=12), dict(d=0), dict(r=0), dict(r=12), dict(r=136), dict(n=0), dict(n=4097), dict(M=-1), dict(M=1 << 31),
+               dict(k=(1 << 20) + 8), dict(d=(1 << 20) + 8)):
+        assert fwd(**kw) == ESHAPE, kw
+    for kw in (dict(X=None), dict(W=None), dict(A=None), dict(B=None), dict(s=None), dict(idx=None), dict(Y=None)):
+        assert fwd(**kw) == ENULL, kw
+    for kw in (dict(X=P + 8), dict(B=P + 4), dict(s=P + 2), dict(idx=P + 1), dict(ws=P + 8)):
+        assert fwd(**kw) == EALIGN, kw
+    need = lib.lora_multi_workspace_bytes(0, 1, 4, 64, 64, 3, 8, 0, 0)
+    assert need > 0 and fwd(nb=need - 1) == EWS and fwd(ws=None) == EWS
+    assert lib.lora_multi_workspace_bytes(0, 1, 4, 64, 64, 3, 12, 0, 0) == 0
+    assert bwd(gt=2) == EDTYPE
+    assert bwd(dA=None) == ENULL
+    assert bwd(dY=None) == ENULL
+    assert bwd(W_t=P + 2) == EALIGN
+    assert bwd(dX=P + 8) == EALIGN
+    need = lib.lora_multi_workspace_bytes(1, 1, 4, 64, 64, 3, 8, 0, 1)
+    assert bwd(nb=need - 1) == EWS
+    # what the caller keeps (W^T) and does not ask for (dX) takes no room
+    big = [lib.lora_multi_workspace_bytes(1, 1, 4096, 4096, 4096, 8, 16, *a) for a in ((0, 1), (1, 1), (1, 0))]
+    assert big[0] >= big[1] + 2 * 4096 * 4096 and big[1] > big[2]
