@@ -1817,9 +1817,10 @@ struct MultiLayout {
   int chunks = 0;  // of an adapter's second operand in the product, looked at for infinities and NaNs
 };
 
-// Token splits of a row group's gradient [64, N]: about two blocks a CU.
-int multi_grad_splits(int64_t M, int64_t N, int64_t groups) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(1, cdiv(N, 256) * groups), cdiv(M, 512), 16}));
+// Token splits of the row groups' gradients [64, N] of both operands, which share
+// a launch of `tiles` column tiles: about two blocks a CU.
+int multi_grad_splits(int64_t M, int64_t tiles, int64_t groups) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(1, tiles * groups), cdiv(M, 512), 16}));
 }
 
 MultiLayout make_multi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r,
@@ -1879,8 +1880,7 @@ MultiLayout make_multi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, int6
         L.at = take(size_t(n) * r * d_in * 2);
         if (!have_wt) L.wt = take(size_t(d_in) * d_out * 2);
       }
-      L.splits_a = multi_grad_splits(M, d_in, L.groups);
-      L.splits_b = multi_grad_splits(M, d_out, L.groups);
+      L.splits_a = L.splits_b = multi_grad_splits(M, cdiv(d_in, 256) + cdiv(d_out, 256), L.groups);
       L.parta = take(size_t(L.splits_a) * n * r * d_in * 4);
       L.partb = take(size_t(L.splits_b) * n * r * d_out * 4);
     }

@@ -44,6 +44,8 @@ __device__ __forceinline__ float val(T x) {
     return x;
 }
 
+constexpr int kScanPieces = 4096;  // 16-byte pieces of a block that looks for infinities
+
 __device__ __forceinline__ int adapter_at(const int* index, int64_t t, int64_t M, int n) {
   const int a = t < M ? index[t] : -1;
   return a >= 0 && a < n ? a : -1;
@@ -57,9 +59,24 @@ __device__ __forceinline__ int adapter_at(const int* index, int64_t t, int64_t M
 // an adapter, which look for infinities and NaNs in their 64 KB of its second
 // operand if a row carries it: one adapter's must not reach the others' rows.
 // ---------------------------------------------------------------------------
+// The distinct values >= 0 of a wave's 64, in the order of their first lanes:
+// lane k < the returned number gets the k-th.
+__device__ __forceinline__ int wave_distinct(int v, int lane, int& mine) {
+  uint64_t left = __ballot(v >= 0);
+  int k = 0;
+  mine = -1;
+  while (left) {
+    const int x = __builtin_amdgcn_readlane(v, __builtin_ctzll(left));
+    left &= ~__ballot(v == x);
+    mine = lane == k ? x : mine;
+    ++k;
+  }
+  return k;
+}
+
 __global__ void __launch_bounds__(256) multi_lists_kernel(const MultiLists q) {
   __shared__ int ids[256];
-  __shared__ int wsum[5];
+  __shared__ int wsum[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int b = blockIdx.x;
   if (b == 0)
@@ -84,13 +101,18 @@ __global__ void __launch_bounds__(256) multi_lists_kernel(const MultiLists q) {
     int* list = (b < q.t128 ? q.list128 : q.list256) + (int64_t)tile * q.cap(rows);
     int* cnt = (b < q.t128 ? q.cnt128 : q.cnt256) + tile;
     const int a = tid < rows ? adapter_at(q.index, (int64_t)tile * rows + tid, q.M, q.n) : -1;
-    ids[tid] = a;
+    // each wave's own, then those that no wave before it has
+    int mine;
+    const int k = wave_distinct(a, lane, mine);
+    ids[tid] = mine;
+    if (lane == 0) wsum[wave] = k;
     __syncthreads();
-    bool first = a >= 0;
-    for (int j = 0; j < 256; ++j) first = first && !(j < tid && ids[j] == a);
+    bool keep = lane < k;
+    for (int w = 0; w < wave; ++w)
+      for (int e = 0; e < wsum[w]; ++e) keep = keep && ids[64 * w + e] != mine;
     int count;
-    const int at = place(first, count);
-    if (first) list[at] = a;
+    const int at = place(keep, count);
+    if (keep) list[at] = mine;
     if (tid == 0) *cnt = count;
     return;
   }
@@ -99,16 +121,17 @@ __global__ void __launch_bounds__(256) multi_lists_kernel(const MultiLists q) {
     b -= q.groups;
     const int a = b / q.chunks, c = b - a * q.chunks;
     int any = 0;
+#pragma unroll 16
     for (int64_t t = tid; t < q.M; t += 256) any |= q.index[t] == a;
     if (!__syncthreads_or(any)) {
       if (tid == 0) q.bad[b] = 0;
       return;
     }
-    const int64_t end = min((int64_t)(c + 1) * 4096, q.scan16);
+    const int64_t end = min((int64_t)(c + 1) * kScanPieces, q.scan16);
     const u32x4* v = reinterpret_cast<const u32x4*>(q.scan) + (int64_t)a * q.scan16;
     uint32_t found = 0;
 #pragma unroll 8
-    for (int64_t i = (int64_t)c * 4096 + tid; i < end; i += 256) {
+    for (int64_t i = (int64_t)c * kScanPieces + tid; i < end; i += 256) {
       const u32x4 x = v[i];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -120,20 +143,25 @@ __global__ void __launch_bounds__(256) multi_lists_kernel(const MultiLists q) {
     if (tid == 0) q.bad[b] = bad ? 1 : 0;
     return;
   }
-  // row group g: adapters [g per, (g + 1) per)
-  const int lo = b * q.per, hi = lo + q.per;
+  // row group: adapters [lo, hi).  A wave's 64 tokens are a tile; 256 tiles a round
+  const int lo = b * q.per, hi = min(lo + q.per, q.n);
   const int64_t t64 = (q.M + 63) / 64;
   int* list = q.glist + (int64_t)b * t64;
   int n = 0;
   for (int64_t base = 0; base < t64; base += 256) {
-    const int64_t first = (base + tid) * 64;  // this thread's tile
-    bool mine = false;
+    const int steps = (int)min((t64 - base + 3) / 4, (int64_t)64);
+    __syncthreads();
+    ids[tid] = 0;
+    __syncthreads();
 #pragma unroll 16
-    for (int k = 0; k < 64; ++k) {
-      const int a = first + k < q.M ? q.index[first + k] : -1;
-      mine = mine || (a >= lo && a < min(hi, q.n));
+    for (int i = 0; i < steps; ++i) {
+      const int64_t t = (base + 4 * i) * 64 + tid;
+      const int a = t < q.M ? q.index[t] : -1;
+      if (__ballot(a >= lo && a < hi) && lane == 0) ids[4 * i + wave] = 1;
     }
+    __syncthreads();
     int count;
+    const bool mine = ids[tid] != 0;
     const int at = place(mine, count);
     if (mine) list[n + at] = (int)(base + tid);
     n += count;
@@ -166,39 +194,64 @@ multi_panel_kernel(const GemmPair q) {
 // there, its bit in `mask` is clear like that of a token without adapter, and
 // its adapter's gradients are NaNs (gbad).
 __global__ void __launch_bounds__(256) multi_strip_kernel(const MultiStrip s) {
-  __shared__ int ids[64], spoilt[64];
-  __shared__ uint16_t v[2][64 * (kMultiMaxRank + 2)];
-  const int tid = threadIdx.x, r = s.r, pitch = r + 2;
+  __shared__ int ids[64], spoilt[64], bad[64], groups[64];
+  __shared__ float sc[64];
+  __shared__ int ngroups;
+  __shared__ __attribute__((aligned(16))) uint16_t v[2][64 * (kMultiMaxRank + 4)];
+  const int tid = threadIdx.x, r = s.r, pitch = r + 4;
   const int64_t t0 = (int64_t)blockIdx.x * 64;
   auto is_bad = [&](int a) {
     int b = 0;
     for (int c = 0; c < s.chunks; ++c) b |= s.bad[(int64_t)a * s.chunks + c];
-    return b != 0;
+    return b;
   };
   if (tid < 64) {
-    ids[tid] = adapter_at(s.index, t0 + tid, s.M, s.n);
+    const int a = adapter_at(s.index, t0 + tid, s.M, s.n);
+    ids[tid] = a;
     spoilt[tid] = 0;
+    sc[tid] = a >= 0 ? s.scales[a] : 0.f;
+    bad[tid] = a >= 0 && s.chunks ? is_bad(a) : 0;
+    int g;
+    const int k = wave_distinct(a >= 0 ? a / s.per : -1, tid, g);
+    if (tid < k) groups[tid] = g;
+    if (tid == 0) ngroups = k;
+  } else if (s.chunks && tid >= 192) {
+    // the lists that this block's tile starts
+    auto mark = [&](int* list, int count) {
+      for (int e = tid - 192; e < count; e += 64)
+        if (is_bad(list[e])) list[e] |= (int)AD_BAD;
+    };
+    const int b = blockIdx.x;
+    if (s.list128 && b % 2 == 0) mark(s.list128 + (int64_t)(b / 2) * min(s.n, 128), s.cnt128[b / 2]);
+    if (s.list256 && b % 4 == 0) mark(s.list256 + (int64_t)(b / 4) * min(s.n, 256), s.cnt256[b / 4]);
   }
-  auto mark = [&](int* list, int count) {
-    for (int e = tid; e < count; e += 256)
-      if (is_bad(list[e])) list[e] |= (int)AD_BAD;
-  };
-  if (s.chunks && s.list128 && blockIdx.x % 2 == 0) mark(s.list128 + (int64_t)(blockIdx.x / 2) * min(s.n, 128), s.cnt128[blockIdx.x / 2]);
-  if (s.chunks && s.list256 && blockIdx.x % 4 == 0) mark(s.list256 + (int64_t)(blockIdx.x / 4) * min(s.n, 256), s.cnt256[blockIdx.x / 4]);
   __syncthreads();
+  const int r4 = r >> 2, items = 64 * r4;
   for (int o = 0; o < s.ops; ++o) {
-    const float* part = s.part[o];
-    for (int e = tid; e < 64 * r; e += 256) {
-      const int t = e / r, q = e - t * r, a = ids[t];
-      float x = 0.f;
-      if (a >= 0) {
-        for (int z = 0; z < s.splits[o]; ++z) x += part[(int64_t)z * s.M * r + (t0 + t) * r + q];
-        x *= s.scales[a];
+    const int64_t slab = s.M * r;
+    const int S = s.splits[o];
+    for (int e = tid; e < items; e += 256) {
+      const int t = e / r4, q = 4 * (e - t * r4);
+      const float* part = s.part[o] + (t0 + t) * r + q;
+      f32x4 x = {0.f, 0.f, 0.f, 0.f};
+      if (ids[t] >= 0) {
+        for (int z0 = 0; z0 < S; z0 += 8) {  // 8 slabs' loads in flight, summed in order
+          f32x4 w[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (z0 + u < S) w[u] = *reinterpret_cast<const f32x4*>(part + (z0 + u) * slab);
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (z0 + u < S) x += w[u];
+        }
+        x *= sc[t];
       }
-      const uint16_t h = f2bf(x);
-      v[o][t * pitch + q] = h;
-      if ((h & 0x7F80u) == 0x7F80u) spoilt[t] = 1;
-      if (s.P[o] && t0 + t < s.M) s.P[o][(t0 + t) * r + q] = a >= 0 && s.chunks && is_bad(a) ? (uint16_t)0x7FC0u : h;
+      const u32x2 h = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+      *reinterpret_cast<u32x2*>(&v[o][t * pitch + q]) = h;
+      auto inf = [](uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; };
+      if (inf(h[0]) || inf(h[1])) spoilt[t] = 1;
+      if (s.P[o] && t0 + t < s.M)
+        *reinterpret_cast<u32x2*>(s.P[o] + (t0 + t) * r + q) = bad[t] ? u32x2{0x7FC07FC0u, 0x7FC07FC0u} : h;
     }
   }
   if (!s.Pt[0]) return;
@@ -210,22 +263,21 @@ __global__ void __launch_bounds__(256) multi_strip_kernel(const MultiStrip s) {
     if (a >= 0 && spoilt[tid]) s.gbad[a] = 1;  // (more than one may store it)
   }
   const int64_t M8 = (s.M + 7) / 8 * 8;
-  for (int i = 0; i < 64; ++i) {
-    const int g = ids[i] < 0 ? -1 : ids[i] / s.per;
-    bool seen = g < 0;  // (uniform: every thread walks the same ids)
-    for (int j = 0; j < i && !seen; ++j) seen = ids[j] >= 0 && ids[j] / s.per == g;
-    if (seen) continue;
-    const int rows = min(s.per, s.n - g * s.per) * r;
-    for (int o = 0; o < s.ops; ++o) {
-      uint16_t* out = s.Pt[o] + (int64_t)g * s.per * r * M8 + t0;
-      for (int e = tid; e < rows * 8; e += 256) {
-        const int row = e >> 3, c = (e & 7) * 8, a = g * s.per + row / r, q = row % r;
-        if (t0 + c >= M8) continue;
-        uint32_t w[4];
-        auto at = [&](int t) { return ids[t] == a && !spoilt[t] ? (uint32_t)v[o][t * pitch + q] : 0u; };
+  const int c = (tid & 7) * 8;  // this thread's 8 tokens
+  int mine[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = at(c + 2 * k) | at(c + 2 * k + 1) << 16;
-        *reinterpret_cast<u32x4*>(out + (int64_t)row * M8 + c) = u32x4{w[0], w[1], w[2], w[3]};
+  for (int k = 0; k < 8; ++k) mine[k] = spoilt[c + k] ? -1 : ids[c + k];
+  if (t0 + c >= M8) return;
+  for (int i = 0; i < ngroups; ++i) {
+    const int g = groups[i], rows = min(s.per, s.n - g * s.per) * r;
+    for (int row = tid >> 3; row < rows; row += 32) {
+      const int k0 = row / r, a = g * s.per + k0, q = row - k0 * r;
+      for (int o = 0; o < s.ops; ++o) {
+        uint32_t w[4];
+        auto at = [&](int k) { return mine[k] == a ? (uint32_t)v[o][(c + k) * pitch + q] : 0u; };
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = at(2 * k) | at(2 * k + 1) << 16;
+        *reinterpret_cast<u32x4*>(s.Pt[o] + ((int64_t)g * s.per * r + row) * M8 + t0 + c) = u32x4{w[0], w[1], w[2], w[3]};
       }
     }
   }
