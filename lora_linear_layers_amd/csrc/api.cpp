@@ -78,7 +78,8 @@ struct FewPlan {
 // in turn, on d_out = 27392, cost 3-7 us; fewer blocks with every wave busy,
 // on d_out = 4096, cost 3 us more than 32 blocks with one); summed with P
 // between the backward's launches, 32 slabs' loads in flight.
-FewPlan few_plan(bool bwd, bool nf4, bool rope, int64_t M, int64_t d_in, int64_t d_out, int64_t r) {
+// (multi: rows with an adapter of their own, which have no panel of X here.)
+FewPlan few_plan(bool bwd, bool nf4, bool rope, int64_t M, int64_t d_in, int64_t d_out, int64_t r, bool multi = false) {
   FewPlan F;
   if (M < 1 || M > 16 * few::MAXMB || r % 8 || r > few::MAXR || d_in % 64 || d_out % 64) return F;
   if ((rope && d_out % 128) || ((bwd || nf4) && d_in % 128)) return F;
@@ -91,7 +92,7 @@ FewPlan few_plan(bool bwd, bool nf4, bool rope, int64_t M, int64_t d_in, int64_t
   // re-reads much of A: RoPE (4 skinny blocks per head), more than 16 tokens,
   // a rank above 16, or W of 2^25 elements or more.  Small plain problems keep
   // skinny's single launch (4096 x 4096, r = 16, 1 token: 16.6 us against 20.7).
-  if (!bwd && !nf4 && !(M <= 64 && (rope || M > 16 || r > 16 || d_in * d_out >= (int64_t(1) << 25)))) return F;
+  if (!bwd && !nf4 && !multi && !(M <= 64 && (rope || M > 16 || r > 16 || d_in * d_out >= (int64_t(1) << 25)))) return F;
   F.MB = M <= 16 ? 1 : (M <= 32 ? 2 : (M <= 64 ? 4 : 8));
   F.Mp = 16 * F.MB;
   const int64_t ncols = bwd ? d_in : d_out, K = bwd ? d_out : d_in;
@@ -1776,14 +1777,25 @@ Act8Layout make_act8_layout(int dtype, int64_t M, int64_t d_in, const lora_group
 // layer with the adapters' columns as a second segment (gemm), else the strips'
 // part into the output first and the base product added to it by the layer's
 // other kernels (few tiles, short contractions).
+//
+// Up to 64 rows: the strips in fp32 by a launch of their own, then one launch of
+// the base product that adds them where it finishes its outputs: the W stream
+// (few) or the one-launch kernel (skinny).
 struct MultiProduct {
-  bool gemm = false;
+  bool gemm = false, few_ = false, skinny = false;
+  FewPlan few;
   StreamPlan plan;
   EpiLayout base;  // the other kernels' layout
 };
 
-MultiProduct multi_product(int dtype, int64_t M, int64_t N, int64_t K, int64_t n, int64_t r) {
+MultiProduct multi_product(int dtype, int64_t M, int64_t N, int64_t K, int64_t n, int64_t r, bool bwd = false) {
   MultiProduct P;
+  if (dtype == LORA_BF16 && M > 0 && M <= 64 && !bwd) {
+    P.few = few_plan(false, false, false, M, K, N, 8, true);
+    P.few_ = P.few.ok && (M > 16 || N * K >= (int64_t(1) << 25));
+    P.skinny = !P.few_ && skinny_fits(M, K, N, 8, sk::STRIP);
+    if (P.few_ || P.skinny) return P;
+  }
   if (dtype == LORA_BF16 && M > 0 && K >= 64 && n * N * r * 2 < 0xE0000000ll) {
     const int64_t t = cdiv(M, 256) * cdiv(N, 256);
     if (M % 256 == 0 && N % 256 == 0 && t % 256 == 0 && K % 64 == 0 && t <= INT32_MAX / 2 &&
@@ -1838,8 +1850,14 @@ MultiLayout make_multi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, int6
   L.groups = (int)cdiv(n, L.per);
   const bool f32 = dtype == LORA_F32;
   if (!bwd) L.y = multi_product(dtype, M, d_out, d_in, n, r);
-  if (bwd && need_dx) L.dx = multi_product(dtype, M, d_in, d_out, n, r);
+  if (bwd && need_dx) L.dx = multi_product(dtype, M, d_in, d_out, n, r, true);
   const MultiProduct& g = bwd ? L.dx : L.y;
+  if (!bwd && (g.few_ || g.skinny)) {
+    L.p = take(size_t(M) * r * 4);
+    if (g.few_) L.base = take(g.few.total);
+    L.total = off;
+    return L;
+  }
   if (f32) {
     L.p = take(size_t(M) * r * 4);
     if (bwd) {
@@ -1995,6 +2013,33 @@ int multi_forward(const MultiCall& c, const MultiLayout& L, const void* X, const
     const EpiArgs ep{nullptr, Y, nullptr, LORA_ACT_NONE};
     return forward_impl(LORA_F32, c.M, c.d_in, c.d_out, 0, 0.f, X, W, nullptr, nullptr, nullptr, nullptr, Y, w + L.base,
                         L.y.base.L, st, P, c.r, nullptr, &ep);
+  }
+  if (L.y.few_ || L.y.skinny) {
+    const MultiProduct& g = L.y;
+    float* P = reinterpret_cast<float*>(w + L.p);
+    int* cnt = g.few_ ? reinterpret_cast<int*>(w + L.base + g.few.cnt) : nullptr;
+    HIPTRY(timed(K_MULTI_PANEL, 2 * Md * kr, 2 * (Md * c.d_in + double(std::min(c.n, c.M)) * kr), st, [&] {
+      return launch_multi_dot(2, X, A, c.scales, c.index, c.M, c.d_in, (int)c.n, (int)c.r, P, st, cnt, g.few_ ? g.few.n_tiles : 0);
+    }));
+    const StripArgs ad{P, c.index, static_cast<const uint16_t*>(B), (int)c.n, (int)c.r};
+    const double ko = double(c.d_out), flop = 2 * Md * ko * (c.d_in + c.r),
+                 bytes = 2 * (ko * c.d_in + Md * (c.d_in + ko) + double(std::min(c.n, c.M)) * ko * c.r);
+    if (g.few_) {
+      FewArgs a = few_args(g.few, c.M, c.d_in, c.d_out, 8, 1.f, X, W, nullptr, nullptr, nullptr, nullptr, w + L.base);
+      a.Y = static_cast<uint16_t*>(Y);
+      a.ad = ad;
+      HIPTRY(timed(K_FEW_FWD, flop, bytes, st, [&] { return launch_few_multi(a, g.few.MB, st); }));
+      return LORA_OK;
+    }
+    SkinnyArgs a;
+    memset(&a, 0, sizeof(a));
+    a.X = static_cast<const uint16_t*>(X); a.ldx = c.d_in;
+    a.W = static_cast<const uint16_t*>(W); a.ldw = c.d_in;
+    a.Y = static_cast<uint16_t*>(Y);
+    a.M = (int)c.M; a.N = (int)c.d_out; a.K = (int)c.d_in; a.r = 8; a.s = 1.f;
+    a.ad = ad;
+    HIPTRY(timed(K_SKINNY, flop, bytes, st, [&] { return launch_skinny_fwd(a, sk::STRIP, st); }));
+    return LORA_OK;
   }
   TRY(multi_lists(c, L, L.y, false, B, w, st));
   float* part = reinterpret_cast<float*>(w + L.part);

@@ -996,7 +996,7 @@ few_fwd_nf4_kernel(const FewArgs p) {
 // and finish as the NF4 form, with 64-deep stages of W (128 rows of 128 bytes,
 // NT layout) and of the activations landing by DMA; 4 waves of 32 columns.
 // ---------------------------------------------------------------------------
-template <int MB, bool EPIL>
+template <int MB, bool EPIL, bool MULTI = false>
 __global__ void __launch_bounds__(few::NT) __attribute__((amdgpu_waves_per_eu(1, 1)))
 few_fwd_bf16_kernel(const FewArgs p) {
   using namespace few;
@@ -1091,13 +1091,14 @@ few_fwd_bf16_kernel(const FewArgs p) {
   // contiguous) and the panel partials are loaded ahead of the DMAs, with no
   // branch; P_s goes to LDS no stage uses yet (the last ring slot) while the
   // first stages fly.
+  // (MULTI: the rows' strips are added below, behind the stages.)
   const bool rk0 = sp.s0 == 0;
-  const __amdgpu_buffer_rsrc_t rbr = few_rsrc(p.B, (int64_t)p.d_out * p.r8 * 2);
+  const __amdgpu_buffer_rsrc_t rbr = few_rsrc(p.B, MULTI ? 0 : (int64_t)p.d_out * p.r8 * 2);
   FewPanelPre<MB, NT> pre;
-  pre.load(p);
+  if constexpr (!MULTI) pre.load(p);
   bf16x8 bq[2][2][NJ];
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
+  for (int u = 0; u < (MULTI ? 0 : 2); ++u)
 #pragma unroll
     for (int sstep = 0; sstep < 2; ++sstep)
 #pragma unroll
@@ -1110,7 +1111,7 @@ few_fwd_bf16_kernel(const FewArgs p) {
   // stages 0 .. NS - 2 in flight, with no branch (as in the NF4 form)
   few_issue_order();
   few_unroll<NS - 1>([&](auto sc) { issue(min((int)decltype(sc)::value, nk - 1), decltype(sc)::value); });
-  if (rk0 || two) {
+  if (!MULTI && (rk0 || two)) {
     char* ps = wslot(NS - 1);
     pre.store(p, ps);
     lds_barrier();  // (LDS only: a __syncthreads would also wait for every DMA in flight)
@@ -1142,8 +1143,46 @@ few_fwd_bf16_kernel(const FewArgs p) {
     });
   }
 
-  // ---- one partial per covered tile, then the last block of a tile sums ----
   const int b = blockIdx.x, na = two ? 2 : 1;
+  // MULTI: the strips of tile a0's rows, dealt in 16-row blocks to the blocks
+  // whose range starts in the tile (one at least: ranges are no longer than a
+  // tile), so that all CUs read the adapters' second operands.  (By the one block
+  // that finishes a tile, with a tile for every second CU, they took 20 us of
+  // 51: 48 rows, 4096 -> 14336, r = 16.)
+  if constexpr (MULTI) {
+    auto first = [&](int a) { return (int)(((int64_t)a * p.nblk + p.n_tiles - 1) / p.n_tiles); };
+    const int j0 = b - first(sp.a0), cnt = first(sp.a0 + 1) - first(sp.a0);
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      if (mb % cnt != j0) continue;
+      int t[4 * NJ];
+      int64_t c[4 * NJ];
+      float y[4 * NJ][1];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int row = 16 * mb + 4 * g + v, col = sp.a0 * BNF + 32 * wave + 16 * j + l16;
+          t[4 * j + v] = row < p.M && col < p.d_out ? row : -1;
+          c[4 * j + v] = col;
+          y[4 * j + v][0] = two ? acc0[mb][j][v] : acc[mb][j][v];
+        }
+      StripAdd<4 * NJ, 1> strip;
+      strip.load(p.ad, p.d_out, t, c);
+      strip.add(p.ad, y);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          if (two)
+            acc0[mb][j][v] = y[4 * j + v][0];
+          else
+            acc[mb][j][v] = y[4 * j + v][0];
+        }
+    }
+  }
+
+  // ---- one partial per covered tile, then the last block of a tile sums ----
   auto store_part = [&](const f32x4 (&v)[MB][NJ], int a) {
     float* cp = p.Cp + (int64_t)(b + a) * p.Mp * BNF;
 #pragma unroll
@@ -1171,7 +1210,7 @@ few_fwd_bf16_kernel(const FewArgs p) {
     const int a = sp.a0 + i;
     const int lo = few_blk_of(p, a * p.nkt), hi = few_blk_of(p, (a + 1) * p.nkt - 1);
     few_finish<BNF, NT, EPIL>(p, p.Cp + (int64_t)(lo + a) * p.Mp * BNF, hi - lo + 1, a * BNF, p.d_out, p.Y,
-                              !EPIL && p.rope != 0);
+                              !EPIL && !MULTI && p.rope != 0);
   }
 }
 

@@ -56,6 +56,7 @@ struct FewArgs {
   // nblk takes the stages [b T / nblk, (b + 1) T / nblk) of the T = n_tiles nkt
   int n_tiles, nkt, T, nblk;
   EpiArgs ep;  // forward with an epilogue (epi.h)
+  StripArgs ad;  // forward of rows with an adapter of their own: no panel (A, B, Pp unused)
   int fold;  // backward: the W stream sums P and Q from the partials itself (no few_reduce_kernel)
 };
 

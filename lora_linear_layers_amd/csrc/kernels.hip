@@ -1539,6 +1539,9 @@ hipError_t run_skinny_mode(const SkinnyArgs& a, int mode, hipStream_t st) {
   // blocks, so fewer re-reads of X from L2
   const bool wide = a.N >= 12288;
   if (mode == sk::ROPE) return run_skinny<MB, 2, RB, sk::ROPE>(a, st);
+  if constexpr (RB == 1)
+    if (mode == sk::STRIP) return wide ? run_skinny<MB, 4, 1, sk::STRIP>(a, st) : run_skinny<MB, 1, 1, sk::STRIP>(a, st);
+  if (mode == sk::STRIP) return hipErrorInvalidValue;
   if (mode == sk::EPIL) return wide ? run_skinny<MB, 4, RB, sk::EPIL>(a, st) : run_skinny<MB, 1, RB, sk::EPIL>(a, st);
   return wide ? run_skinny<MB, 4, RB, sk::PLAIN>(a, st) : run_skinny<MB, 1, RB, sk::PLAIN>(a, st);
 }
@@ -1566,6 +1569,10 @@ hipError_t few_launch(const FewArgs& a, int what, bool nf4, hipStream_t st) {
       hipLaunchKernelGGL((few_fwd_nf4_kernel<MB, true>), dim3((unsigned)a.nblk), dim3(few::NT4), 0, st, a);
     else
       hipLaunchKernelGGL((few_fwd_bf16_kernel<MB, true>), dim3((unsigned)a.nblk), dim3(few::NT), 0, st, a);
+  } else if (what == 4) {  // rows with an adapter of their own
+    if (a.rope || nf4 || MB > 4) return hipErrorInvalidValue;
+    if constexpr (MB <= 4)
+      hipLaunchKernelGGL((few_fwd_bf16_kernel<MB, false, true>), dim3((unsigned)a.nblk), dim3(few::NT), 0, st, a);
   } else {
     const dim3 grid((unsigned)a.nblk);
     if (nf4)
@@ -1610,6 +1617,7 @@ hipError_t launch_few_reduce(const FewArgs& a, hipStream_t st) {
 hipError_t launch_few_fwd(const FewArgs& a, int MB, bool nf4, bool epil, hipStream_t st) {
   return few_dispatch(a, MB, epil ? 3 : 1, nf4, st);
 }
+hipError_t launch_few_multi(const FewArgs& a, int MB, hipStream_t st) { return few_dispatch(a, MB, 4, false, st); }
 hipError_t launch_few_bwd(const FewArgs& a, int MB, bool nf4, hipStream_t st) {
   return few_dispatch(a, MB, 2, nf4, st);
 }

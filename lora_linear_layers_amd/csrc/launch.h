@@ -257,6 +257,7 @@ struct FewArgs;
 hipError_t launch_few_panel(const FewArgs& a, int MB, hipStream_t st);
 hipError_t launch_few_reduce(const FewArgs& a, hipStream_t st);  // backward: P_s, Q_s between the launches
 hipError_t launch_few_fwd(const FewArgs& a, int MB, bool nf4, bool epil, hipStream_t st);
+hipError_t launch_few_multi(const FewArgs& a, int MB, hipStream_t st);  // bf16 W, strips of FewArgs::ad
 hipError_t launch_few_bwd(const FewArgs& a, int MB, bool nf4, hipStream_t st);
 
 // Token log-probabilities (loss.hip): logp [rows] and stats [rows, 2] (row
@@ -405,10 +406,10 @@ struct MultiStrip {
 hipError_t launch_multi_strip(const MultiStrip& s, hipStream_t st);
 // The product with its rows' adapters (ad_list of 128-row tiles where low, else of 256-row ones).
 hipError_t launch_multi_gemm(GemmArgs a, bool low, hipStream_t st);
-// fp32 P [M, r] = s_a X A_a^T; out (+)= P B_a^T with B [n][N, r] and P of out's type;
-// transposes of [n][R, C] stacks.
+// fp32 P [M, r] = s_a X A_a^T (also clears zero[0 .. nzero)); out (+)= P B_a^T with
+// B [n][N, r] and P of out's type; transposes of [n][R, C] stacks.
 hipError_t launch_multi_dot(int elem_bytes, const void* X, const void* A, const float* scales, const int* index, int64_t M,
-                            int64_t K, int n, int r, float* P, hipStream_t st);
+                            int64_t K, int n, int r, float* P, hipStream_t st, int* zero = nullptr, int nzero = 0);
 hipError_t launch_multi_update(int elem_bytes, const void* P, const void* B, const int* index, int64_t M, int64_t N, int n, int r,
                                bool add, void* out, hipStream_t st);
 struct MultiTranspose {

@@ -283,19 +283,35 @@ __global__ void __launch_bounds__(256) multi_strip_kernel(const MultiStrip s) {
   }
 }
 
-// fp32 strips P [M, r], one wave a value.
+// fp32 strips P [M, r], one wave a value; rows of whole 16-byte pieces.
 template <typename T>
 __global__ void __launch_bounds__(256) multi_dot_kernel(const T* X, const T* A, const float* scales, const int* index,
-                                                        int64_t M, int64_t K, int n, int r, float* P) {
+                                                        int64_t M, int64_t K, int n, int r, float* P, int* zero, int nzero) {
+  constexpr int E = 16 / sizeof(T);
   const int64_t t = blockIdx.x;
   const int q = blockIdx.y * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < nzero; i += 256) zero[i] = 0;
   if (q >= r) return;
   const int a = adapter_at(index, t, M, n);
   float s = 0.f;
   if (a >= 0) {
-    const T* x = X + t * K;
-    const T* w = A + ((int64_t)a * r + q) * K;
-    for (int64_t k = lane; k < K; k += 64) s = __builtin_fmaf(val(x[k]), val(w[k]), s);
+    const u32x4* x = reinterpret_cast<const u32x4*>(X + t * K);
+    const u32x4* w = reinterpret_cast<const u32x4*>(A + ((int64_t)a * r + q) * K);
+#pragma unroll 8
+    for (int64_t k = lane; k < K / E; k += 64) {
+      const u32x4 u = x[k], v = w[k];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 2) {
+          s = __builtin_fmaf(__builtin_bit_cast(float, u[e] << 16), __builtin_bit_cast(float, v[e] << 16), s);
+          s = __builtin_fmaf(__builtin_bit_cast(float, u[e] & 0xFFFF0000u), __builtin_bit_cast(float, v[e] & 0xFFFF0000u), s);
+        } else {
+          const uint32_t ue = u[e], ve = v[e];  // (a vector's element has no address to cast at)
+          s = __builtin_fmaf(__builtin_bit_cast(float, ue), __builtin_bit_cast(float, ve), s);
+        }
+      }
+    }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
     s *= scales[a];
@@ -482,16 +498,16 @@ hipError_t launch_multi_gemm(GemmArgs a, bool low, hipStream_t st) {
 }
 
 hipError_t launch_multi_dot(int elem_bytes, const void* X, const void* A, const float* scales, const int* index, int64_t M,
-                            int64_t K, int n, int r, float* P, hipStream_t st) {
+                            int64_t K, int n, int r, float* P, hipStream_t st, int* zero, int nzero) {
   if (M <= 0) return hipSuccess;
   if (M > INT32_MAX) return hipErrorInvalidValue;
   const dim3 grid((unsigned)M, (unsigned)((r + 3) / 4));
   if (elem_bytes == 2)
     hipLaunchKernelGGL((multi_dot_kernel<uint16_t>), grid, dim3(256), 0, st, static_cast<const uint16_t*>(X),
-                       static_cast<const uint16_t*>(A), scales, index, M, K, n, r, P);
+                       static_cast<const uint16_t*>(A), scales, index, M, K, n, r, P, zero, nzero);
   else
     hipLaunchKernelGGL((multi_dot_kernel<float>), grid, dim3(256), 0, st, static_cast<const float*>(X),
-                       static_cast<const float*>(A), scales, index, M, K, n, r, P);
+                       static_cast<const float*>(A), scales, index, M, K, n, r, P, zero, nzero);
   return hipGetLastError();
 }
 

@@ -47,7 +47,8 @@ namespace lora {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 namespace sk {
-enum Mode : int { PLAIN = 0, ROPE = 1, EPIL = 2 };  // EPIL: bias, activation, residual (epi.h)
+// EPIL: bias, activation, residual (epi.h); STRIP: rows with an adapter of their own (StripArgs), no panel here
+enum Mode : int { PLAIN = 0, ROPE = 1, EPIL = 2, STRIP = 3 };
 constexpr int BIG = 0x40000000;        // buffer resource size (offsets stay below)
 constexpr uint32_t OOB = 0x40000000u;  // lane offset that reads zero
 }  // namespace sk
@@ -74,6 +75,7 @@ struct SkinnyArgs {
   const float* sinc;
   int64_t max_pos;     // rows of the cos / sin cache
   EpiArgs ep;          // EPIL
+  StripArgs ad;        // STRIP
 };
 
 // MB: 16-row blocks of X (M <= 16 MB); NB: 16-column strips per block; RB:
@@ -87,7 +89,9 @@ skinny_fwd_kernel(const SkinnyArgs p) {
   constexpr int NT = 64 * NW;
   // prefetch depth (steps of 32 contraction elements), bounded by the
   // registers a wave has at NW / 4 waves per SIMD
-  constexpr int REGS = (MB + RB + NB) * 4;
+  constexpr bool ST = MODE == sk::STRIP;
+  constexpr int RBL = ST ? 0 : RB;  // (panel blocks that run)
+  constexpr int REGS = (MB + RBL + NB) * 4;
   constexpr int BUDGET = NW == 16 ? 48 : (NW == 8 ? 112 : 160);
   constexpr int D0 = BUDGET / REGS;
   constexpr int D = D0 > 8 ? 8 : (D0 < 2 ? 2 : D0);
@@ -137,7 +141,7 @@ skinny_fwd_kernel(const SkinnyArgs p) {
       xf[d][mb] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, (int)o, 0, 0));
     }
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
+    for (int rb = 0; rb < RBL; ++rb) {
       const int row = 16 * rb + l16;
       const uint32_t o = kin && row < p.r ? (uint32_t)((row * (int64_t)p.K + k) * 2) : sk::OOB;
       af[d][rb] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, (int)o, 0, 0));
@@ -169,7 +173,7 @@ skinny_fwd_kernel(const SkinnyArgs p) {
 #pragma unroll
       for (int j = 0; j < NB; ++j) ay[mb][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, wv[j], ay[mb][j], 0, 0, 0);
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
+      for (int rb = 0; rb < RBL; ++rb)
         ap[mb][rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, __builtin_bit_cast(bf16x8, af[d][rb]), ap[mb][rb],
                                                              0, 0, 0);
     }
@@ -197,7 +201,7 @@ skinny_fwd_kernel(const SkinnyArgs p) {
 #pragma unroll
       for (int v = 0; v < 4; ++v) red[((wave * E + mb * (NB + RB) + j) * 4 + v) * 64 + lane] = ay[mb][j][v];
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb)
+    for (int rb = 0; rb < RBL; ++rb)
 #pragma unroll
       for (int v = 0; v < 4; ++v)
         red[((wave * E + mb * (NB + RB) + NB + rb) * 4 + v) * 64 + lane] = ap[mb][rb][v];
@@ -217,7 +221,7 @@ skinny_fwd_kernel(const SkinnyArgs p) {
       y[j][v] = a;
     }
 #pragma unroll
-  for (int rb = 0; rb < RB; ++rb)
+  for (int rb = 0; rb < RBL; ++rb)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       float a = 0.f;
@@ -229,7 +233,7 @@ skinny_fwd_kernel(const SkinnyArgs p) {
   // into LDS [16][16 RB] and back in the A layout (row l16, rank 8 g ..)
   uint16_t* pw = plds + wave * 16 * 16 * RB;
 #pragma unroll
-  for (int rb = 0; rb < RB; ++rb)
+  for (int rb = 0; rb < RBL; ++rb)
 #pragma unroll
     for (int v = 0; v < 4; ++v) pw[(4 * g + v) * (16 * RB) + 16 * rb + l16] = f2bf(p.s * pp[rb][v]);
   // (the wave reads back only what it wrote; LDS operations of a wave
@@ -237,7 +241,7 @@ skinny_fwd_kernel(const SkinnyArgs p) {
   const __amdgpu_buffer_rsrc_t rbb =
       __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p.B), (short)0, sk::BIG, 0x00020000);
 #pragma unroll
-  for (int kr = 0; kr < RK; ++kr) {
+  for (int kr = 0; kr < (ST ? 0 : RK); ++kr) {
     const int c = 32 * kr + 8 * g;  // the lane's first rank column
     u32x4 pv = {0u, 0u, 0u, 0u};
     if (c < 16 * RB) pv = *reinterpret_cast<const u32x4*>(pw + l16 * (16 * RB) + c);
@@ -248,6 +252,28 @@ skinny_fwd_kernel(const SkinnyArgs p) {
       const u32x4 bv = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rbb, (int)o, 0, 0));
       y[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, pv), __builtin_bit_cast(bf16x8, bv),
                                                      y[j], 0, 0, 0);
+    }
+  }
+
+  if constexpr (ST) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int n = col0(j) + l16;
+      int t[4];
+      int64_t c[4];
+      float o[4][1];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int row = 16 * mb + 4 * g + v;
+        t[v] = row < p.M && n < p.N ? row : -1;
+        c[v] = n;
+        o[v][0] = y[j][v];
+      }
+      StripAdd<4, 1> strip;
+      strip.load(p.ad, p.N, t, c);
+      strip.add(p.ad, o);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) y[j][v] = o[v][0];
     }
   }
 
