@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblora_linear.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["kernels.hip", "loss.hip", "norm.hip", "multi.hip", "api.cpp"]
+SOURCES = ["kernels.hip", "loss.hip", "norm.hip", "act8.hip", "multi.hip", "api.cpp"]
 FLAGS = [
     "--offload-arch=gfx950",
     "-O3",

@@ -903,7 +903,9 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
                   const void* W, const Nf4W* nf4, const void* A, const void* B, const Rope* rope, const void* dY,
                   void* dX, float* dA, float* dB, void* ws, const Layout& L, hipStream_t st,
                   const PanelSlices* ov = nullptr, const void* Xa = nullptr, const uint8_t* keep = nullptr,
-                  const void* Wt_in = nullptr) {
+                  const void* Wt_in = nullptr, Act8Args* x8 = nullptr) {
+  // x8: X in 8 bits (act8.hip) instead of X, for layouts that run the panels and
+  // the gradients in pairs
   // LoRA dropout: Xa is the adapter's (masked) input and `keep` the mask that
   // the rank-r term of dX passes through; X itself still feeds the base path
   const void* Xp = Xa ? Xa : X;
@@ -1028,13 +1030,21 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
       const GemmArgs a = panel_args(Xp, d_in, A, d_in, M, L.M8, d_in, r, L.r8, L.ksplit_p, pp);
       const GemmArgs b = panel_args(G, d_out, Bt, d_out, M, L.M8, d_out, r, L.r8, L.ksplit_q, pq);
       const double el = double(L.M8) * L.r8;
+      const int splits_p = x8 ? x8->splits : L.splits_p;
+      if (x8) {
+        x8->part = pp;
+        x8->Qt = static_cast<const uint16_t*>(Qt);
+      }
       HIPTRY(timed(G_BF16_PANEL_SPLIT_NT, 2 * Md * rr * (ki + ko),
-                   (Md + rr) * (ki + ko) * 2 + 4.0 * (L.splits_p + L.splits_q) * el, st,
-                   [&] { return launch_gemm_pair(G_BF16_PANEL_SPLIT_NT, a, L.splits_p, b, L.splits_q, st); }));
-      HIPTRY(timed(K_PANEL, (L.splits_p + L.splits_q) * el, (4.0 * (L.splits_p + L.splits_q) + 6) * el, st, [&] {
-        return launch_panel_reduce_pair({pp, L.splits_p, nullptr, pt},
-                                        {pq, L.splits_q, static_cast<uint16_t*>(Qs), static_cast<uint16_t*>(Qt)}, L.M8,
-                                        L.r8, col_scale(scale), st, cnt, ncnt);
+                   (Md + rr) * (ki + ko) * 2 - (x8 ? Md * ki : 0) + 4.0 * (splits_p + L.splits_q) * el, st, [&] {
+                     if (x8) return launch_act8_panel_pair(*x8, b, L.splits_q, st);
+                     return launch_gemm_pair(G_BF16_PANEL_SPLIT_NT, a, L.splits_p, b, L.splits_q, st);
+                   }));
+      HIPTRY(timed(K_PANEL, (splits_p + L.splits_q) * el, (4.0 * (splits_p + L.splits_q) + 6) * el, st, [&] {
+        return launch_panel_reduce_pair({pp, splits_p, nullptr, pt},
+                                        {pq, L.splits_q, static_cast<uint16_t*>(Qs), static_cast<uint16_t*>(Qt),
+                                         x8 ? x8->scale8 : nullptr, M},
+                                        L.M8, L.r8, col_scale(scale), st, cnt, ncnt);
       }));
     } else {
       TRY(panel_bf16(G, d_out, Bt, d_out, M, L.M8, d_out, r, L.r8, L.splits_q, L.ksplit_q, col_scale(scale), pp,
@@ -1138,8 +1148,11 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
   aa.m_load = L.r8; aa.m_store = L.r8; aa.n_load = d_in; aa.n_store = d_in;
   aa.k_split = L.ksplit_dA; aa.c = part; aa.ldc = d_in; aa.part_stride = L.r8 * d_in;
   const double fa = 2 * rr * ki * Md, ba = (rr * Md + Md * ki) * e + 4.0 * L.splits_dA * L.r8 * ki;
-  const bool both = L.pair && gemm_pair_fits(ksplit, ab, aa);
-  if (both)
+  const bool both = x8 || (L.pair && gemm_pair_fits(ksplit, ab, aa));
+  if (x8) {
+    x8->gpart = part;
+    HIPTRY(timed(ksplit, fa + fb, ba + bb - Md * ki, st, [&] { return launch_act8_grad_pair(*x8, ab, L.splits_dB, st); }));
+  } else if (both)
     HIPTRY(timed(ksplit, fa + fb, ba + bb, st,
                  [&] { return launch_gemm_pair(ksplit, ab, L.splits_dB, aa, L.splits_dA, st); }));
   else
@@ -1756,17 +1769,33 @@ int check_epi(bool bwd, int dtype, int64_t M, int64_t d_in, const lora_group_mem
 }
 
 // Backward from an 8-bit checkpoint: the epilogue layer's backward (no
-// activation, no bias) and the checkpoint's values in the type.
+// activation, no bias).  bf16, ranks up to 128 and rows of whole 16-byte pieces
+// read the codes where the layer reads X (direct); else the checkpoint's values are
+// written in the type first (x).  Up to 128 tokens the few-token backward, one
+// stream of W with X in bf16, is the faster one behind that: X is small.
 struct Act8Layout {
   EpiLayout E;
+  bool direct = false;
+  int splits = 1;
+  int64_t ksplit = 0;
   size_t x = 0, total = 0;
 };
 
 Act8Layout make_act8_layout(int dtype, int64_t M, int64_t d_in, const lora_group_member& m) {
   Act8Layout A;
   A.E = make_epi_layout(true, dtype, M, d_in, m, lora_epilogue{LORA_ACT_NONE, nullptr, nullptr, nullptr});
-  A.x = align256(A.E.total);
-  A.total = A.x + align256(size_t(M) * d_in * elem_bytes(dtype));
+  const Layout& L = A.E.L;
+  A.total = A.E.total;
+  A.direct = M > 0 && dtype == LORA_BF16 && L.pair && !(L.few.ok && m.dX) && act8_fits(d_in, L.r8) && L.M8 * 2 * 128 < (1 << 30) &&
+             (L.ksplit_dB + 64) * m.d_out * 2 + m.d_out * 2 < (1 << 30) && L.M8 * d_in < (int64_t(1) << 40);
+  if (A.direct) {
+    // (stages of 128: no more splits than the panel's partials have room for)
+    A.ksplit = rup(L.ksplit_p, 128);
+    A.splits = (int)cdiv(d_in, A.ksplit);
+  } else {
+    A.x = align256(A.total);
+    A.total = A.x + align256(size_t(M) * d_in * elem_bytes(dtype));
+  }
   return A;
 }
 
@@ -2698,13 +2727,21 @@ int lora_act8_linear_bwd(int dtype, int64_t M, int64_t d_in, const lora_group_me
   TRY(check_device());
   hipStream_t st = static_cast<hipStream_t>(stream);
   void* X = static_cast<char*>(ws) + E.x;
-  if (M > 0)
+  Act8Args x8;
+  memset(&x8, 0, sizeof(x8));
+  if (E.direct) {
+    const Layout& L = E.E.L;
+    x8.codes = codes; x8.scale8 = scale8; x8.M = M; x8.d = d_in;
+    x8.A = static_cast<const uint16_t*>(m.A); x8.rows = L.M8; x8.r = m.r; x8.r8 = L.r8;
+    x8.splits = E.splits; x8.ksplit = E.ksplit; x8.gsplits = L.splits_dA; x8.gksplit = L.ksplit_dA;
+  } else if (M > 0) {
     HIPTRY(timed(K_ACT8, double(M) * d_in, double(M) * d_in * (elem_bytes(dtype) + 1), st,
                  [&] { return launch_act8_unpack(elem_bytes(dtype), codes, scale8, M, d_in, X, st); }));
+  }
   const Nf4W q{m.W_nf4, m.absmax, table16};
   return backward_impl(dtype, M, d_in, m.d_out, m.r, m.scale, X, m.W, m.W_nf4 ? &q : nullptr, m.A, m.B, nullptr, m.dY,
                        m.dX, m.dA, m.dB, ws, E.E.L, st, nullptr, nullptr, nullptr,
-                       E.E.L.dx_nt && !m.W_nf4 ? m.W_t : nullptr);
+                       E.E.L.dx_nt && !m.W_nf4 ? m.W_t : nullptr, E.direct ? &x8 : nullptr);
 }
 
 // ---- an adapter of its own for every row ----

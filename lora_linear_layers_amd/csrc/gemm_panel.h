@@ -53,6 +53,7 @@ struct Cfg {
   static constexpr int IA = BM / 8 / 4;         // A instructions per wave
   static constexpr int IB = BN / 8 / 4;         // B instructions per wave
   static constexpr int PER = IA + IB;           // DMAs per wave per stage
+  static constexpr int LDS = NS * STAGE;
   // waves: 4 x 1 over 256 rows, else 2 x 2
   static constexpr int WM = BM == 256 ? 4 : 2, WN = 4 / WM;
   static constexpr int FM = BM / WM / 32, FN = BN / WN / 32;  // MFMA blocks per wave
@@ -67,13 +68,12 @@ constexpr int vmcnt_imm(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }
 // own (GemmArgs::ad_list); the columns are the 64 from 64 cg of the adapters
 // that the tile's rows carry, and C takes each row's own.
 template <int BM, int BN, bool MULTI = false>
-__device__ __forceinline__ void panel_dma_tile(const GemmArgs& p, const int mt, const int z, const int cg = 0) {
+__device__ __forceinline__ void panel_dma_tile(char* smem, const GemmArgs& p, const int mt, const int z, const int cg = 0) {
   static_assert(!MULTI || BN == 64, "64 columns a block");
   using namespace pdma;
   using C = Cfg<BM, BN>;
   constexpr int NS = C::NS, LEAD = NS - 1, FM = C::FM, FN = C::FN;
   constexpr int A_BYTES = C::A_BYTES;
-  __shared__ __attribute__((aligned(1024))) char smem[NS * C::STAGE];
   asm volatile("" ::: "a0");
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -236,7 +236,8 @@ __device__ __forceinline__ void panel_dma_tile(const GemmArgs& p, const int mt, 
 template <int BM, int BN>
 __global__ void __launch_bounds__(pdma::NT) __attribute__((amdgpu_waves_per_eu(1, 1)))
 panel_dma_kernel(const GemmArgs p) {
-  panel_dma_tile<BM, BN>(p, (int)(blockIdx.x % p.tiles_m), (int)(blockIdx.x / p.tiles_m));
+  __shared__ __attribute__((aligned(1024))) char smem[pdma::Cfg<BM, BN>::LDS];
+  panel_dma_tile<BM, BN>(smem, p, (int)(blockIdx.x % p.tiles_m), (int)(blockIdx.x / p.tiles_m));
 }
 
 // Two of a layer's launches at once (an epilogue layer's backward: the panels
@@ -251,8 +252,9 @@ struct GemmPair {
 template <int BM, int BN>
 __global__ void __launch_bounds__(pdma::NT) __attribute__((amdgpu_waves_per_eu(1, 1)))
 panel_dma_pair_kernel(const GemmPair q) {
+  __shared__ __attribute__((aligned(1024))) char smem[pdma::Cfg<BM, BN>::LDS];
   const int y = (int)blockIdx.y, w = y >= q.s0 ? 1 : 0;
-  panel_dma_tile<BM, BN>(q.g[w], (int)blockIdx.x, w ? y - q.s0 : y);
+  panel_dma_tile<BM, BN>(smem, q.g[w], (int)blockIdx.x, w ? y - q.s0 : y);
 }
 
 // ---------------------------------------------------------------------------
@@ -290,6 +292,7 @@ struct Cfg {
   static constexpr int IB = BK / 2 / 4;  // Bop instructions per wave
   static constexpr int PER = IA + IB;
   static constexpr int FM = BR / 32, FN = 2;
+  static constexpr int LDS = NS * STAGE;
   static_assert(IA % 2 == 0, "row parity pattern of the Aop lane mapping");
 };
 }  // namespace sdma
@@ -300,13 +303,12 @@ struct Cfg {
 // 64 bits a tile: tokens whose bit is clear are read as zeros from Bop (they
 // may hold anything; Aop has zeros for them).
 template <int BR, int NS_, bool LISTED = false>
-__device__ __forceinline__ void splitnn_dma_tile(const GemmArgs& p, const int nt, const int z, const int rg = 0,
-                                                 const int splits = 1) {
+__device__ __forceinline__ void splitnn_dma_tile(char* smem, const GemmArgs& p, const int nt, const int z,
+                                                 const int rg = 0, const int splits = 1) {
   using namespace sdma;
   using C = Cfg<BR, NS_>;
   constexpr int NS = C::NS, LEAD = NS - 1, FM = C::FM, FN = C::FN;
   constexpr int A_BYTES = C::A_BYTES;
-  __shared__ __attribute__((aligned(1024))) char smem[NS * C::STAGE];
   asm volatile("" ::: "a0");
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -473,15 +475,17 @@ __device__ __forceinline__ void splitnn_dma_tile(const GemmArgs& p, const int nt
 template <int BR, int NS_>
 __global__ void __launch_bounds__(sdma::NT) __attribute__((amdgpu_waves_per_eu(1, 2)))
 splitnn_dma_kernel(const GemmArgs p) {
-  splitnn_dma_tile<BR, NS_>(p, (int)blockIdx.x, (int)blockIdx.y);
+  __shared__ __attribute__((aligned(1024))) char smem[sdma::Cfg<BR, NS_>::LDS];
+  splitnn_dma_tile<BR, NS_>(smem, p, (int)blockIdx.x, (int)blockIdx.y);
 }
 
 template <int BR, int NS_>
 __global__ void __launch_bounds__(sdma::NT) __attribute__((amdgpu_waves_per_eu(1, 2)))
 splitnn_dma_pair_kernel(const GemmPair q) {
+  __shared__ __attribute__((aligned(1024))) char smem[sdma::Cfg<BR, NS_>::LDS];
   const int y = (int)blockIdx.y, w = y >= q.s0 ? 1 : 0;
   if ((int64_t)blockIdx.x * sdma::BN >= q.g[w].n_store) return;  // (the grid is as wide as the wider one)
-  splitnn_dma_tile<BR, NS_>(q.g[w], (int)blockIdx.x, w ? y - q.s0 : y);
+  splitnn_dma_tile<BR, NS_>(smem, q.g[w], (int)blockIdx.x, w ? y - q.s0 : y);
 }
 
 }  // namespace lora

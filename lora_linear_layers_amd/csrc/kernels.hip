@@ -1218,7 +1218,7 @@ constexpr int kMaxPanelSplits = 32;
 __device__ __forceinline__ void panel_reduce_tile(const float* __restrict__ part, int splits, int64_t part_stride,
                                                   int64_t ldp, int64_t rows, int64_t n, const ColScale& scale,
                                                   uint16_t* __restrict__ out, int64_t ldo, uint16_t* __restrict__ outt,
-                                                  int64_t ldot) {
+                                                  int64_t ldot, const float* __restrict__ tscale = nullptr, int64_t tn = 0) {
   __shared__ float tile[16][65];
   const int tid = threadIdx.x;
   const int64_t q0 = (int64_t)blockIdx.x * 16, c0 = (int64_t)blockIdx.y * 64;
@@ -1244,10 +1244,11 @@ __device__ __forceinline__ void panel_reduce_tile(const float* __restrict__ part
   }
   if (!outt) return;
   float* trow = &tile[rl][cl];
-  trow[0] = y[0];
-  trow[1] = y[1];
-  trow[2] = y[2];
-  trow[3] = y[3];
+  const float ts = tscale ? (q < tn ? tscale[q] : 0.f) : 1.f;  // (a power of two)
+  trow[0] = y[0] * ts;
+  trow[1] = y[1] * ts;
+  trow[2] = y[2] * ts;
+  trow[3] = y[3] * ts;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -1278,7 +1279,8 @@ __global__ void __launch_bounds__(256) panel_reduce_pair_kernel(PanelSum a, Pane
   clear_ints(zero, nzero);
   const bool second = blockIdx.z != 0;
   panel_reduce_tile(second ? b.part : a.part, second ? b.splits : a.splits, rows * n, n, rows, n, scale,
-                    second ? b.out : a.out, n, second ? b.outt : a.outt, rows);
+                    second ? b.out : a.out, n, second ? b.outt : a.outt, rows, second ? b.tscale : a.tscale,
+                    second ? b.tn : a.tn);
 }
 
 hipError_t launch_panel_reduce_pair(const PanelSum& a, const PanelSum& b, int64_t rows, int64_t n,

@@ -174,6 +174,8 @@ struct PanelSum {
   int splits;
   uint16_t* out;
   uint16_t* outt;
+  const float* tscale = nullptr;  // outt's values times their row's power of two (rows [0, tn), 0 past them)
+  int64_t tn = 0;
 };
 hipError_t launch_panel_reduce_pair(const PanelSum& a, const PanelSum& b, int64_t rows, int64_t n,
                                     const ColScale& scale, hipStream_t st, int* zero, int nzero);
@@ -432,5 +434,27 @@ hipError_t launch_multi_grad_sum(int out_bytes, const MultiGradSum& a, const Mul
                                  hipStream_t st);
 hipError_t launch_multi_outer(const float* P, const float* X, const int* index, int64_t M, int64_t N, int n, int r, bool tr,
                               int out_bytes, void* out, hipStream_t st);
+
+// The panel s X A^T and the adapter's gradient from X in 8 bits (act8.hip): fp32
+// partials of codes A^T times the rows' scales, [splits][rows, r8] (zeros from row
+// M and column r on), and of Qt codes over ranges of tokens, [gsplits][r8, d].
+struct Act8Args {
+  const uint8_t* codes;  // [M, d], 16-byte aligned, d a multiple of 16
+  const float* scale8;   // [M]
+  int64_t M, d;
+  const uint16_t* A;     // [r, d]
+  int64_t rows, r, r8;   // r8 <= 128
+  int splits;
+  int64_t ksplit;        // a multiple of 128
+  float* part;
+  const uint16_t* Qt;    // [r8, rows], its rows' values times the tokens' scales
+  int gsplits;
+  int64_t gksplit;       // a multiple of 64
+  float* gpart;
+};
+bool act8_fits(int64_t d, int64_t r8);
+// Beside a bf16 panel (its splits sb) and beside a bf16 gradient, as launch_gemm_pair.
+hipError_t launch_act8_panel_pair(const Act8Args& a, const GemmArgs& b, int sb, hipStream_t st);
+hipError_t launch_act8_grad_pair(const Act8Args& a, const GemmArgs& b, int sb, hipStream_t st);
 
 }  // namespace lora

@@ -178,10 +178,11 @@ __global__ void __launch_bounds__(256) multi_lists_kernel(const MultiLists q) {
 __global__ void __launch_bounds__(pdma::NT) __attribute__((amdgpu_waves_per_eu(1, 1)))
 multi_panel_kernel(const GemmPair q) {
   const int y = (int)blockIdx.z, w = y >= q.s0 ? 1 : 0;
+  __shared__ __attribute__((aligned(1024))) char smem[pdma::Cfg<PANEL_BM, 64>::LDS];
   const GemmArgs& p = q.g[w];
   const int mt = blockIdx.x, cg = blockIdx.y;
   if (64 * cg >= scalar_at(p.ad_cnt, mt) * p.ad_r) return;
-  panel_dma_tile<PANEL_BM, 64, true>(p, mt, w ? y - q.s0 : y, cg);
+  panel_dma_tile<PANEL_BM, 64, true>(smem, p, mt, w ? y - q.s0 : y, cg);
 }
 
 // The strips of a 64-token tile from their partials, bf16(s_a sum), of one or
@@ -370,7 +371,8 @@ multi_grad_kernel(const GemmPair q, int s1, int rows, int total) {
   p.a1 = static_cast<const uint16_t*>(p.a1) + (int64_t)g * rows * p.lda1;
   p.c = static_cast<float*>(p.c) + (int64_t)g * rows * p.ldc;
   p.m_load = p.m_store = min(rows, total - g * rows);
-  splitnn_dma_tile<BR, NS, true>(p, (int)blockIdx.x, w ? y - q.s0 : y, g, w ? s1 : q.s0);
+  __shared__ __attribute__((aligned(1024))) char smem[sdma::Cfg<BR, NS>::LDS];
+  splitnn_dma_tile<BR, NS, true>(smem, p, (int)blockIdx.x, w ? y - q.s0 : y, g, w ? s1 : q.s0);
 }
 
 // out [n r, N] = the sum over splits of part [splits][n r, N]; transposed within
