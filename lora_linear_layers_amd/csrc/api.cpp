@@ -1812,6 +1812,7 @@ Act8Layout make_act8_layout(int dtype, int64_t M, int64_t d_in, const lora_group
 // (few) or the one-launch kernel (skinny).
 struct MultiProduct {
   bool gemm = false, few_ = false, skinny = false;
+  bool dot = false;  // neither: a few rows' strips by fp32 dot products (one launch, no lists)
   FewPlan few;
   StreamPlan plan;
   EpiLayout base;  // the other kernels' layout
@@ -1842,6 +1843,9 @@ MultiProduct multi_product(int dtype, int64_t M, int64_t N, int64_t K, int64_t n
     m.d_out = N;
     m.r = 8;
     P.base = make_epi_layout(false, dtype, M, K, m, lora_epilogue{LORA_ACT_NONE, nullptr, nullptr, nullptr});
+    // X is read r times from the caches: up to 64 MB of that one launch of 4 to 8 us
+    // takes the place of three (lists, panel, strips) of 4 each
+    P.dot = !bwd && (dtype == LORA_F32 || M * r * K <= int64_t(1) << 25);
   }
   return P;
 }
@@ -1887,7 +1891,7 @@ MultiLayout make_multi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, int6
     L.total = off;
     return L;
   }
-  if (f32) {
+  if (f32 || g.dot) {
     L.p = take(size_t(M) * r * 4);
     if (bwd) {
       L.pt = take(size_t(M) * r * 4);  // Q
@@ -2021,7 +2025,7 @@ int multi_bf16(const MultiCall& c, const MultiLayout& L, const MultiProduct& g, 
     return LORA_OK;
   }
   HIPTRY(timed(K_MULTI_UPDATE, 2 * Md * N * c.r, 2 * Md * N, st, [&] {
-    return launch_multi_update(2, P, B, c.index, c.M, N, (int)c.n, (int)c.r, false, out, st);
+    return launch_multi_update(2, P, false, B, c.index, c.M, N, (int)c.n, (int)c.r, false, out, st);
   }));
   const EpiArgs ep{nullptr, out, nullptr, LORA_ACT_NONE};
   return forward_impl(LORA_BF16, c.M, K, N, 0, 0.f, X, W, nullptr, nullptr, nullptr, nullptr, out, w + L.base, g.base.L, st, P,
@@ -2031,16 +2035,17 @@ int multi_bf16(const MultiCall& c, const MultiLayout& L, const MultiProduct& g, 
 int multi_forward(const MultiCall& c, const MultiLayout& L, const void* X, const void* W, const void* A, const void* B,
                   void* Y, char* w, hipStream_t st) {
   const double Md = double(c.M), kr = double(c.d_in) * c.r;
-  if (c.dtype == LORA_F32) {
+  if (L.y.dot) {
+    const int eb = elem_bytes(c.dtype);
     float* P = reinterpret_cast<float*>(w + L.p);
-    HIPTRY(timed(K_MULTI_PANEL, 2 * Md * kr, 4 * Md * c.d_in, st, [&] {
-      return launch_multi_dot(4, X, A, c.scales, c.index, c.M, c.d_in, (int)c.n, (int)c.r, P, st);
+    HIPTRY(timed(K_MULTI_PANEL, 2 * Md * kr, eb * Md * c.d_in, st, [&] {
+      return launch_multi_dot(eb, X, A, c.scales, c.index, c.M, c.d_in, (int)c.n, (int)c.r, P, st);
     }));
-    HIPTRY(timed(K_MULTI_UPDATE, 2 * Md * c.d_out * c.r, 4 * Md * c.d_out, st, [&] {
-      return launch_multi_update(4, P, B, c.index, c.M, c.d_out, (int)c.n, (int)c.r, false, Y, st);
+    HIPTRY(timed(K_MULTI_UPDATE, 2 * Md * c.d_out * c.r, eb * Md * c.d_out, st, [&] {
+      return launch_multi_update(eb, P, true, B, c.index, c.M, c.d_out, (int)c.n, (int)c.r, false, Y, st);
     }));
     const EpiArgs ep{nullptr, Y, nullptr, LORA_ACT_NONE};
-    return forward_impl(LORA_F32, c.M, c.d_in, c.d_out, 0, 0.f, X, W, nullptr, nullptr, nullptr, nullptr, Y, w + L.base,
+    return forward_impl(c.dtype, c.M, c.d_in, c.d_out, 0, 0.f, X, W, nullptr, nullptr, nullptr, nullptr, Y, w + L.base,
                         L.y.base.L, st, P, c.r, nullptr, &ep);
   }
   if (L.y.few_ || L.y.skinny) {
@@ -2101,7 +2106,7 @@ int multi_backward(const MultiCall& c, const MultiLayout& L, const void* X, cons
       f32_split(cdiv(c.M, 64) * cdiv(c.d_in, 128), c.d_out, &S, &ks);
       auto update = [&](bool add) {
         return timed(K_MULTI_UPDATE, 2 * Md * c.d_in * r, 4 * Md * c.d_in, st, [&] {
-          return launch_multi_update(4, Q, w + L.at, c.index, c.M, c.d_in, n, r, add, dX, st);
+          return launch_multi_update(4, Q, true, w + L.at, c.index, c.M, c.d_in, n, r, add, dX, st);
         });
       };
       GemmArgs a = blank();

@@ -409,10 +409,10 @@ hipError_t launch_multi_strip(const MultiStrip& s, hipStream_t st);
 // The product with its rows' adapters (ad_list of 128-row tiles where low, else of 256-row ones).
 hipError_t launch_multi_gemm(GemmArgs a, bool low, hipStream_t st);
 // fp32 P [M, r] = s_a X A_a^T (also clears zero[0 .. nzero)); out (+)= P B_a^T with
-// B [n][N, r] and P of out's type; transposes of [n][R, C] stacks.
+// B [n][N, r] and P fp32 (P32) or bf16; transposes of [n][R, C] stacks.
 hipError_t launch_multi_dot(int elem_bytes, const void* X, const void* A, const float* scales, const int* index, int64_t M,
                             int64_t K, int n, int r, float* P, hipStream_t st, int* zero = nullptr, int nzero = 0);
-hipError_t launch_multi_update(int elem_bytes, const void* P, const void* B, const int* index, int64_t M, int64_t N, int n, int r,
+hipError_t launch_multi_update(int elem_bytes, const void* P, bool P32, const void* B, const int* index, int64_t M, int64_t N, int n, int r,
                                bool add, void* out, hipStream_t st);
 struct MultiTranspose {
   const void* src;

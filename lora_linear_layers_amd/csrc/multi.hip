@@ -320,18 +320,29 @@ __global__ void __launch_bounds__(256) multi_dot_kernel(const T* X, const T* A, 
   if (lane == 0) P[t * r + q] = s;
 }
 
-// out [M, N] (+)= P_t . B_a[j, :], B [n][N, r].
+// out [M, N] (+)= P_t . B_a[j, :], B [n][N, r]; a thread one output, 16 bytes of B
+// at a time.
 template <typename T, typename TP>
 __global__ void __launch_bounds__(256) multi_update_kernel(const TP* P, const T* B, const int* index, int64_t M, int64_t N,
                                                            int n, int r, int add, T* out) {
+  constexpr int E = 16 / sizeof(T);
   const int64_t t = blockIdx.y, j = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (j >= N) return;
   const int a = adapter_at(index, t, M, n);
   float s = add ? val(out[t * N + j]) : 0.f;
   if (a >= 0) {
-    const T* b = B + ((int64_t)a * N + j) * r;
+    const u32x4* b = reinterpret_cast<const u32x4*>(B + ((int64_t)a * N + j) * r);
     const TP* p = P + t * r;
-    for (int q = 0; q < r; ++q) s = __builtin_fmaf(val(p[q]), val(b[q]), s);
+#pragma unroll 4
+    for (int q = 0; q < r / E; ++q) {
+      const u32x4 v = b[q];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t u = v[e * sizeof(T) / 4];
+        const float x = __builtin_bit_cast(float, sizeof(T) == 4 ? u : e & 1 ? u & 0xFFFF0000u : u << 16);
+        s = __builtin_fmaf(val(p[q * E + e]), x, s);
+      }
+    }
   }
   store_out<T>(out, t * N + j, s);
 }
@@ -513,18 +524,24 @@ hipError_t launch_multi_dot(int elem_bytes, const void* X, const void* A, const 
   return hipGetLastError();
 }
 
-hipError_t launch_multi_update(int elem_bytes, const void* P, const void* B, const int* index, int64_t M, int64_t N, int n, int r,
-                               bool add, void* out, hipStream_t st) {
+hipError_t launch_multi_update(int elem_bytes, const void* P, bool P32, const void* B, const int* index, int64_t M, int64_t N,
+                               int n, int r, bool add, void* out, hipStream_t st) {
+  if (elem_bytes == 4 && !P32) return hipErrorInvalidValue;
   // (rows on the grid's y, 65535 at most)
   for (int64_t t0 = 0; t0 < M; t0 += 65535) {
     const int64_t m = std::min<int64_t>(65535, M - t0);
     const dim3 grid((unsigned)((N + 255) / 256), (unsigned)m);
-    if (elem_bytes == 2)
-      hipLaunchKernelGGL((multi_update_kernel<uint16_t, uint16_t>), grid, dim3(256), 0, st, static_cast<const uint16_t*>(P) + t0 * r,
-                         static_cast<const uint16_t*>(B), index + t0, m, N, n, r, add ? 1 : 0, static_cast<uint16_t*>(out) + t0 * N);
+    const float* p32 = static_cast<const float*>(P) + t0 * r;
+    const uint16_t* p16 = static_cast<const uint16_t*>(P) + t0 * r;
+    if (elem_bytes == 4)
+      hipLaunchKernelGGL((multi_update_kernel<float, float>), grid, dim3(256), 0, st, p32, static_cast<const float*>(B), index + t0,
+                         m, N, n, r, add ? 1 : 0, static_cast<float*>(out) + t0 * N);
+    else if (P32)
+      hipLaunchKernelGGL((multi_update_kernel<uint16_t, float>), grid, dim3(256), 0, st, p32, static_cast<const uint16_t*>(B),
+                         index + t0, m, N, n, r, add ? 1 : 0, static_cast<uint16_t*>(out) + t0 * N);
     else
-      hipLaunchKernelGGL((multi_update_kernel<float, float>), grid, dim3(256), 0, st, static_cast<const float*>(P) + t0 * r,
-                         static_cast<const float*>(B), index + t0, m, N, n, r, add ? 1 : 0, static_cast<float*>(out) + t0 * N);
+      hipLaunchKernelGGL((multi_update_kernel<uint16_t, uint16_t>), grid, dim3(256), 0, st, p16, static_cast<const uint16_t*>(B),
+                         index + t0, m, N, n, r, add ? 1 : 0, static_cast<uint16_t*>(out) + t0 * N);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -124,6 +124,22 @@ __device__ __forceinline__ float row_join(float v, float* red) {
   return v;
 }
 
+template <int TPR>
+__device__ __forceinline__ double row_join64(double v, double* red) {
+  constexpr int W = TPR < 64 ? TPR : 64;
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  if constexpr (TPR > 64) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int q = 1; q < TPR / 64; ++q) v += red[q];
+  }
+  return v;
+}
+
 __device__ __forceinline__ bool finite(float x) { return (__builtin_bit_cast(uint32_t, x) & 0x7F800000u) != 0x7F800000u; }
 
 // The power of two a row is kept at: the smallest 2^e, e >= -126, with
@@ -143,23 +159,67 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
 }
 
-// The row's codes and scale from its values y.
-template <int TPR, int NV, bool VEC>
-__device__ __forceinline__ void pack_row(const float (&y)[NV][8], int d, int t, uint8_t* codes, float* scale, float* red) {
+// The nearest float to v on the odd side: where v lies between two floats, the one
+// with the odd last bit.  Rounded again to fewer bits, it gives what v itself would.
+__device__ __forceinline__ float to_odd(double v) {
+  const float f = (float)v;
+  const double g = f;
+  uint32_t b = __builtin_bit_cast(uint32_t, f);
+  if (g != v && !(b & 1u)) b += fabs(v) > fabs(g) ? 1u : 0xFFFFFFFFu;
+  return __builtin_bit_cast(float, b);
+}
+
+// The row's codes and scale from its values y.  NEAR: y is off by less than 2^-18
+// of itself; where that could decide a code or the scale, exact(k, y8) gives the
+// 8 values of chunk k in 64 bits, which then do (a chunk in some thousands).
+template <int TPR, int NV, bool VEC, bool NEAR, class F>
+__device__ __forceinline__ void pack_row(const float (&y)[NV][8], int d, int t, uint8_t* codes, float* scale, float* red, F exact) {
   using R = Row<TPR, NV, VEC>;
+  constexpr float REL = 3.814697265625e-06f;  // 2^-18
   float top = 0.f;
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = fmaxf(top, finite(y[k][e]) ? fabsf(y[k][e]) : 0.f);
-  const int ex = pack_exponent(row_join<TPR, true>(top, red));
+  top = row_join<TPR, true>(top, red);
+  bool border = false;
+  if constexpr (NEAR) {
+    border = pack_exponent(top * (1.f + REL)) != pack_exponent(top * (1.f - REL));
+    if (border) {  // (of the whole row)
+      top = 0.f;
+#pragma unroll 1
+      for (int k = 0; k < NV; ++k) {
+        double v[8];
+        exact(k, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float o = fabsf(to_odd(v[e]));
+          top = fmaxf(top, finite(o) ? o : 0.f);
+        }
+      }
+      top = row_join<TPR, true>(top, red);
+    }
+  }
+  const int ex = pack_exponent(top);
   const float inv = pow2(-ex);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     float u[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) u[e] = finite(y[k][e]) ? y[k][e] * inv : __builtin_nanf("");
-    const u32x2 v = {codes4(u[0], u[1], u[2], u[3]), codes4(u[4], u[5], u[6], u[7])};
+    u32x2 v = {codes4(u[0], u[1], u[2], u[3]), codes4(u[4], u[5], u[6], u[7])};
+    if constexpr (NEAR) {
+      constexpr float UP = 1.f + REL, DN = 1.f - REL;
+      const uint32_t a = codes4(u[0] * UP, u[1] * UP, u[2] * UP, u[3] * UP) ^ codes4(u[0] * DN, u[1] * DN, u[2] * DN, u[3] * DN);
+      const uint32_t b = codes4(u[4] * UP, u[5] * UP, u[6] * UP, u[7] * UP) ^ codes4(u[4] * DN, u[5] * DN, u[6] * DN, u[7] * DN);
+      if (a | b) {
+        double w[8];
+        exact(k, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = finite(y[k][e]) ? to_odd(w[e] * (double)inv) : __builtin_nanf("");
+        v = u32x2{codes4(u[0], u[1], u[2], u[3]), codes4(u[4], u[5], u[6], u[7])};
+      }
+    }
     if constexpr (VEC) {
       const int c = R::col(t, k, 0);
       if (c < d) *reinterpret_cast<u32x2*>(codes + c) = v;
@@ -177,10 +237,15 @@ __device__ __forceinline__ void pack_row(const float (&y)[NV][8], int d, int t, 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-template <typename T, int TPR, int NV, bool VEC>
+// The sum of squares is kept in 64 bits (an instruction an element).  PACK: the codes
+// are those of the row's exact values: one whose code 32 bits leave open is formed
+// in 64 again (pack_row).  (From 32 bits alone a few codes in a million are the
+// neighbour's.)
+template <typename T, int TPR, int NV, bool VEC, bool PACK>
 __global__ void __launch_bounds__((Row<TPR, NV, VEC>::NT)) rmsnorm_kernel(const RmsNormArgs a) {
   using R = Row<TPR, NV, VEC>;
   __shared__ float red[16];
+  __shared__ double red64[16];
   const int t = threadIdx.x % TPR;
   const int64_t row0 = (int64_t)blockIdx.x * R::RPB + threadIdx.x / TPR;
   if (TPR < 256 && row0 >= a.M) return;  // (rows of a wave's part: nothing of the block is waited for)
@@ -204,28 +269,44 @@ __global__ void __launch_bounds__((Row<TPR, NV, VEC>::NT)) rmsnorm_kernel(const 
 #pragma unroll
     for (int k = 0; k < NV; ++k) put8<T, TPR, NV, VEC>(o, d, t, k, h[k]);
   }
-  float s = 0.f;
+  double s = 0;
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s = __builtin_fmaf(h[k][e], h[k][e], s);
-  const float rstd = 1.f / sqrtf(row_join<TPR, false>(s, red) / (float)d + a.eps);
+    for (int e = 0; e < 8; ++e) s = __builtin_fma((double)h[k][e], (double)h[k][e], s);
+  s = row_join64<TPR>(s, red64) * (1.0 / d) + (double)a.eps;
+  // 1 / sqrt(s): in 32 bits, then one Newton step (a sum past fp32's range gives 0, one of 0 an infinity)
+  const float r32 = 1.f / sqrtf((float)s);
+  const double r0 = r32, r64 = finite(r32) && r32 != 0.f ? r0 * (1.5 - 0.5 * s * r0 * r0) : r0;
+  const float rstd = (float)r64;
   if (a.rstd && t == 0) a.rstd[row0] = rstd;
   const T* w = reinterpret_cast<const T*>(a.weight);
+  float y[NV][8];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     float v[8];
     get8<T, TPR, NV, VEC>(w, d, t, k, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[k][e] = h[k][e] * rstd * v[e];
+    for (int e = 0; e < 8; ++e) y[k][e] = h[k][e] * rstd * v[e];
   }
   if (a.Y) {
     T* o = reinterpret_cast<T*>(a.Y) + row0 * (int64_t)d;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) put8<T, TPR, NV, VEC>(o, d, t, k, h[k]);
+    for (int k = 0; k < NV; ++k) put8<T, TPR, NV, VEC>(o, d, t, k, y[k]);
   }
-  // (from the values before their rounding to the type: one rounding, not two)
-  if (a.codes) pack_row<TPR, NV, VEC>(h, d, t, a.codes + row0 * (int64_t)d, a.scale8 + row0, red);
+  if constexpr (PACK) {
+    pack_row<TPR, NV, VEC, true>(y, d, t, a.codes + row0 * (int64_t)d, a.scale8 + row0, red, [&](int k, double (&v)[8]) {
+      float f[8];
+      get8<T, TPR, NV, VEC>(w, d, t, k, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float x = h[0][e];
+#pragma unroll
+        for (int i = 1; i < NV; ++i) x = k == i ? h[i][e] : x;
+        v[e] = (double)x * r64 * (double)f[e];
+      }
+    });
+  }
 }
 
 template <typename T, int TPR, int NV, bool VEC>
@@ -239,7 +320,7 @@ __global__ void __launch_bounds__((Row<TPR, NV, VEC>::NT)) act8_pack_kernel(cons
   float x[NV][8];
 #pragma unroll
   for (int k = 0; k < NV; ++k) get8<T, TPR, NV, VEC>(X + row * ldx, d, t, k, x[k]);
-  pack_row<TPR, NV, VEC>(x, d, t, codes + row * (int64_t)d, scale8 + row, red);
+  pack_row<TPR, NV, VEC, false>(x, d, t, codes + row * (int64_t)d, scale8 + row, red, [](int, double (&)[8]) {});
 }
 
 // x = code * scale, a number of either type: 8 elements a thread.
@@ -362,7 +443,13 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* __restric
   const int c = (int)blockIdx.x * 32 + l;
   float s = 0.f;
   if (c < d)
-    for (int b = q; b < blocks; b += 32) s += part[(int64_t)b * d + c];
+    for (int b0 = q; b0 < blocks; b0 += 32 * 8) {  // 8 loads in flight
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = b0 + 32 * k < blocks ? part[(int64_t)(b0 + 32 * k) * d + c] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += v[k];
+    }
   red[q][l] = s;
   __syncthreads();
   if (q == 0 && c < d) {
@@ -406,7 +493,11 @@ void run_norm(const RmsNormArgs& a, hipStream_t st) {
   by_width(a.d, [&](auto tpr, auto nv) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
     using R = Row<TPR, NV, VEC>;
-    hipLaunchKernelGGL((rmsnorm_kernel<T, TPR, NV, VEC>), dim3((unsigned)((a.M + R::RPB - 1) / R::RPB)), dim3(R::NT), 0, st, a);
+    const dim3 grid((unsigned)((a.M + R::RPB - 1) / R::RPB));
+    if (a.codes)
+      hipLaunchKernelGGL((rmsnorm_kernel<T, TPR, NV, VEC, true>), grid, dim3(R::NT), 0, st, a);
+    else
+      hipLaunchKernelGGL((rmsnorm_kernel<T, TPR, NV, VEC, false>), grid, dim3(R::NT), 0, st, a);
   });
 }
 

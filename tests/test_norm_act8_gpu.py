@@ -502,3 +502,32 @@ def test_side_stream_does_not_need_its_own_device_guard(lib):
         got = lib.lora_rmsnorm_fwd(Z, w)[0]
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_norm_codes_are_those_of_the_exact_values(lib, dtype):
+    """Among 4 million values some lie within fp32's error of the middle of two codes, and some rows' largest next to a
+    power of two's border: all are rounded as the exact value is."""
+    M, d = 2048, 2048
+    X, R, w = _randn(1, M, d, dtype=dtype) * 3, _randn(2, M, d, dtype=dtype), (1 + 0.3 * _randn(3, d)).to(dtype)
+    _, Hh, rstd, codes, s8 = lib.lora_rmsnorm_fwd(X, w, 1e-5, residual=R, pack=True)
+    h = Hh.double()
+    y = h / torch.sqrt(h.square().mean(1, keepdim=True) + torch.tensor(1e-5).double().item()) * w.double()
+    c, s = pack64(y)
+    assert torch.equal(s8.double(), s)
+    assert torch.equal(codes.double(), c)
+    # and the other outputs are the same without them
+    Y, Hp, rp, _, _ = lib.lora_rmsnorm_fwd(X, w, 1e-5, residual=R)
+    assert torch.equal(Y, lib.lora_rmsnorm_fwd(X, w, 1e-5, residual=R, pack=True)[0]) and torch.equal(rp, rstd) and torch.equal(Hp, Hh)
+    # rows whose largest value is 448 or 224 to 32 bits, above or below it by less
+    d = 4
+    X = torch.zeros(2000, d)
+    X[:, 0] = torch.arange(1, 2001) / 7.0
+    X = X.to(dtype).cuda()
+    for target in (1.75, 1.75 * 2 ** 8):
+        w = torch.full((d,), target / 2, device="cuda").to(dtype)
+        _, _, _, codes, s8 = lib.lora_rmsnorm_fwd(X, w, 0.0, pack=True)
+        h = X.double()
+        c, s = pack64(h / torch.sqrt(h.square().mean(1, keepdim=True)) * w.double())
+        near = (h[:, 0] / torch.sqrt(h.square().mean(1)) * w.double()[0] / target - 1).abs() < 1e-15  # (64 bits' own border)
+        assert torch.equal(s8.double()[~near], s[~near]) and torch.equal(codes.double()[~near], c[~near])
