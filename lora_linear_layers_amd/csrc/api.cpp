@@ -1850,7 +1850,15 @@ MultiProduct multi_product(int dtype, int64_t M, int64_t N, int64_t K, int64_t n
   return P;
 }
 
+// Backward with the simple kernels: fp32, and bf16 up to 256 rows, where the seven
+// launches of the lists, strips and tiles cost more than their work.
+bool multi_simple(int dtype, int64_t M) { return dtype == LORA_F32 || M <= 256; }
+
 struct MultiLayout {
+  bool simple = false;    // backward
+  int splits_x = 1;       // simple: splits of dX's contraction, and of the gradients' tokens
+  int64_t ksplit_x = 0;
+  int splits_t = 1;
   MultiProduct y, dx;
   int64_t M8 = 0;
   int per = 1, groups = 0;  // adapters of 64 rows of the stacked ones (one, from a rank above 64 on); such groups
@@ -1883,7 +1891,7 @@ MultiLayout make_multi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, int6
   L.groups = (int)cdiv(n, L.per);
   const bool f32 = dtype == LORA_F32;
   if (!bwd) L.y = multi_product(dtype, M, d_out, d_in, n, r);
-  if (bwd && need_dx) L.dx = multi_product(dtype, M, d_in, d_out, n, r, true);
+  if (bwd && need_dx && !multi_simple(dtype, M)) L.dx = multi_product(dtype, M, d_in, d_out, n, r, true);
   const MultiProduct& g = bwd ? L.dx : L.y;
   if (!bwd && (g.few_ || g.skinny)) {
     L.p = take(size_t(M) * r * 4);
@@ -1891,13 +1899,25 @@ MultiLayout make_multi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, int6
     L.total = off;
     return L;
   }
-  if (f32 || g.dot) {
+  if (bwd && multi_simple(dtype, M)) {
+    L.simple = true;
     L.p = take(size_t(M) * r * 4);
-    if (bwd) {
-      L.pt = take(size_t(M) * r * 4);  // Q
-      L.bt = take(size_t(n) * r * d_out * 4);
-      if (need_dx) L.at = take(size_t(n) * r * d_in * 4);
+    L.pt = take(size_t(M) * r * 4);  // Q
+    if (need_dx && f32)
+      f32_split(cdiv(M, 64) * cdiv(d_in, 128), d_out, &L.splits_x, &L.ksplit_x);
+    else if (need_dx)
+      main_split(M, d_in, d_out, &L.splits_x, &L.ksplit_x);
+    if (L.splits_x > 1) L.base = take(size_t(L.splits_x) * M * d_in * 4);
+    L.splits_t = (int)std::max<int64_t>(1, std::min<int64_t>(16, M / 512));
+    if (L.splits_t > 1) {
+      L.parta = take(size_t(L.splits_t) * n * r * d_in * 4);
+      L.partb = take(size_t(L.splits_t) * n * r * d_out * 4);
     }
+    L.total = off;
+    return L;
+  }
+  if (g.dot) {
+    L.p = take(size_t(M) * r * 4);
   } else {
     const int64_t t128 = cdiv(M, 128), t256 = cdiv(M, 256);
     L.need256 = g.gemm && !g.plan.low;
@@ -1937,16 +1957,7 @@ MultiLayout make_multi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, int6
     }
   }
   if (!bwd && !g.gemm) L.base = take(g.base.total);
-  if (bwd && need_dx && !g.gemm) {
-    if (f32) {
-      int S = 1;
-      int64_t ks = 0;
-      f32_split(cdiv(M, 64) * cdiv(d_in, 128), d_out, &S, &ks);
-      if (S > 1) L.base = take(size_t(S) * M * d_in * 4);
-    } else {
-      L.base = take(g.base.total);
-    }
-  }
+  if (bwd && need_dx && !g.gemm) L.base = take(g.base.total);
   L.total = off;
   return L;
 }
@@ -1960,7 +1971,7 @@ struct MultiCall {
 
 // scan: the product's second operands, by adapter, as the caller holds them.
 int multi_lists(const MultiCall& c, const MultiLayout& L, const MultiProduct& g, bool bwd, const void* scan, char* w,
-                hipStream_t st) {
+                hipStream_t st, const MultiTranspose* tr = nullptr) {
   MultiLists q;
   memset(&q, 0, sizeof(q));
   q.index = c.index; q.M = c.M; q.n = (int)c.n; q.per = L.per;
@@ -1980,7 +1991,12 @@ int multi_lists(const MultiCall& c, const MultiLayout& L, const MultiProduct& g,
     q.scan = scan; q.scan16 = (bwd ? c.d_in : c.d_out) * c.r / 8; q.chunks = L.chunks;
     q.bad = reinterpret_cast<int*>(w + L.bad);
   }
-  HIPTRY(timed(K_MULTI_LISTS, 0, 4.0 * c.M, st, [&] { return launch_multi_lists(q, st); }));
+  double bytes = 4.0 * c.M;
+  for (int i = 0; tr && i < 2; ++i) {
+    q.tr[i] = tr[i];
+    bytes += tr[i].src ? 4.0 * c.n * tr[i].R * tr[i].C : 0;
+  }
+  HIPTRY(timed(K_MULTI_LISTS, 0, bytes, st, [&] { return launch_multi_lists(q, st); }));
   return LORA_OK;
 }
 
@@ -2025,11 +2041,19 @@ int multi_bf16(const MultiCall& c, const MultiLayout& L, const MultiProduct& g, 
     return LORA_OK;
   }
   HIPTRY(timed(K_MULTI_UPDATE, 2 * Md * N * c.r, 2 * Md * N, st, [&] {
-    return launch_multi_update(2, P, false, B, c.index, c.M, N, (int)c.n, (int)c.r, false, out, st);
+    return launch_multi_update(2, P, false, B, c.index, c.M, N, (int)c.n, (int)c.r, out, st);
   }));
   const EpiArgs ep{nullptr, out, nullptr, LORA_ACT_NONE};
   return forward_impl(LORA_BF16, c.M, K, N, 0, 0.f, X, W, nullptr, nullptr, nullptr, nullptr, out, w + L.base, g.base.L, st, P,
                       c.r, nullptr, &ep);
+}
+
+MultiDot multi_dot(const MultiCall& c, const void* X, const void* A, float* P) {
+  MultiDot d;
+  memset(&d, 0, sizeof(d));
+  d.X = X; d.A = A; d.P = P; d.scales = c.scales; d.index = c.index; d.M = c.M; d.K = c.d_in; d.N = c.d_out;
+  d.n = (int)c.n; d.r = (int)c.r;
+  return d;
 }
 
 int multi_forward(const MultiCall& c, const MultiLayout& L, const void* X, const void* W, const void* A, const void* B,
@@ -2039,10 +2063,10 @@ int multi_forward(const MultiCall& c, const MultiLayout& L, const void* X, const
     const int eb = elem_bytes(c.dtype);
     float* P = reinterpret_cast<float*>(w + L.p);
     HIPTRY(timed(K_MULTI_PANEL, 2 * Md * kr, eb * Md * c.d_in, st, [&] {
-      return launch_multi_dot(eb, X, A, c.scales, c.index, c.M, c.d_in, (int)c.n, (int)c.r, P, st);
+      return launch_multi_dot(eb, multi_dot(c, X, A, P), st);
     }));
     HIPTRY(timed(K_MULTI_UPDATE, 2 * Md * c.d_out * c.r, eb * Md * c.d_out, st, [&] {
-      return launch_multi_update(eb, P, true, B, c.index, c.M, c.d_out, (int)c.n, (int)c.r, false, Y, st);
+      return launch_multi_update(eb, P, true, B, c.index, c.M, c.d_out, (int)c.n, (int)c.r, Y, st);
     }));
     const EpiArgs ep{nullptr, Y, nullptr, LORA_ACT_NONE};
     return forward_impl(c.dtype, c.M, c.d_in, c.d_out, 0, 0.f, X, W, nullptr, nullptr, nullptr, nullptr, Y, w + L.base,
@@ -2053,7 +2077,10 @@ int multi_forward(const MultiCall& c, const MultiLayout& L, const void* X, const
     float* P = reinterpret_cast<float*>(w + L.p);
     int* cnt = g.few_ ? reinterpret_cast<int*>(w + L.base + g.few.cnt) : nullptr;
     HIPTRY(timed(K_MULTI_PANEL, 2 * Md * kr, 2 * (Md * c.d_in + double(std::min(c.n, c.M)) * kr), st, [&] {
-      return launch_multi_dot(2, X, A, c.scales, c.index, c.M, c.d_in, (int)c.n, (int)c.r, P, st, cnt, g.few_ ? g.few.n_tiles : 0);
+      MultiDot d = multi_dot(c, X, A, P);
+      d.zero = cnt;
+      d.nzero = cnt ? g.few.n_tiles : 0;
+      return launch_multi_dot(2, d, st);
     }));
     const StripArgs ad{P, c.index, static_cast<const uint16_t*>(B), (int)c.n, (int)c.r};
     const double ko = double(c.d_out), flop = 2 * Md * ko * (c.d_in + c.r),
@@ -2091,46 +2118,49 @@ int multi_backward(const MultiCall& c, const MultiLayout& L, const void* X, cons
                    const void* B, const void* dY, void* dX, void* dA, void* dB, int gb, char* w, hipStream_t st) {
   const int n = (int)c.n, r = (int)c.r, eb = elem_bytes(c.dtype);
   const double Md = double(c.M);
-  const MultiTranspose tb{B, w + L.bt, c.d_out, c.r}, ta{A, w + L.at, c.r, c.d_in};
-  HIPTRY(timed(K_TRANSPOSE, 0, 2.0 * eb * n * r * (c.d_out + (dX ? c.d_in : 0)), st,
-               [&] { return launch_multi_transpose(eb, tb, dX ? &ta : nullptr, n, st); }));
-  if (c.dtype == LORA_F32) {
+  if (L.simple) {
     float *P = reinterpret_cast<float*>(w + L.p), *Q = reinterpret_cast<float*>(w + L.pt);
-    HIPTRY(timed(K_MULTI_PANEL, 2 * Md * r * (c.d_in + c.d_out), 4 * Md * (c.d_in + c.d_out), st, [&] {
-      const hipError_t e = launch_multi_dot(4, X, A, c.scales, c.index, c.M, c.d_in, n, r, P, st);
-      return e != hipSuccess ? e : launch_multi_dot(4, dY, w + L.bt, c.scales, c.index, c.M, c.d_out, n, r, Q, st);
+    const double both = double(c.d_in) + c.d_out;
+    HIPTRY(timed(K_MULTI_PANEL, 2 * Md * r * both, eb * Md * both, st, [&] {
+      MultiDot d = multi_dot(c, X, A, P);
+      d.dY = dY; d.B = B; d.Q = Q;
+      return launch_multi_dot(eb, d, st);
     }));
     if (dX) {
-      int S = 1;
-      int64_t ks = 0;
-      f32_split(cdiv(c.M, 64) * cdiv(c.d_in, 128), c.d_out, &S, &ks);
-      auto update = [&](bool add) {
-        return timed(K_MULTI_UPDATE, 2 * Md * c.d_in * r, 4 * Md * c.d_in, st, [&] {
-          return launch_multi_update(4, Q, true, w + L.at, c.index, c.M, c.d_in, n, r, add, dX, st);
-        });
-      };
+      // the strips' part first, then the base product added to it
+      HIPTRY(timed(K_MULTI_UPDATE, 2 * Md * c.d_in * r, eb * Md * c.d_in, st, [&] {
+        return launch_multi_update_rows(eb, Q, A, c.index, c.M, c.d_in, n, r, dX, st);
+      }));
+      const bool f32 = c.dtype == LORA_F32;
       GemmArgs a = blank();
       a.a1 = dY; a.lda1 = c.d_out; a.b1 = W; a.ldb1 = c.d_in; a.K1 = c.d_out;
       a.m_load = a.m_store = c.M; a.n_load = a.n_store = c.d_in; a.c = dX; a.ldc = c.d_in;
-      const double flop = 2 * Md * c.d_in * c.d_out, bytes = 4 * (Md * (c.d_in + c.d_out) + double(c.d_in) * c.d_out);
+      const double flop = 2 * Md * c.d_in * c.d_out, bytes = eb * (Md * both + double(c.d_in) * c.d_out);
+      const int S = L.splits_x;
       if (S > 1) {
         float* sp = reinterpret_cast<float*>(w + L.base);
-        HIPTRY(update(false));
-        a.k_split = ks; a.c = sp; a.part_stride = c.M * c.d_in;
-        HIPTRY(gemm(G_F32_NN_PARTIAL, a, S, st, flop, bytes));
-        HIPTRY(timed(K_FINISH, double(S) * Md * c.d_in, 4.0 * (S + 2) * Md * c.d_in, st, [&] {
-          return launch_split_finish_epi(4, sp, S, c.M * c.d_in, c.M, c.d_in, dX, EpiArgs{nullptr, dX, nullptr, LORA_ACT_NONE},
+        a.k_split = L.ksplit_x; a.c = sp; a.part_stride = c.M * c.d_in;
+        HIPTRY(gemm(f32 ? G_F32_NN_PARTIAL : G_BF16_MED_NN_PARTIAL, a, S, st, flop, bytes));
+        HIPTRY(timed(K_FINISH, double(S) * Md * c.d_in, (4.0 * S + 2 * eb) * Md * c.d_in, st, [&] {
+          return launch_split_finish_epi(eb, sp, S, c.M * c.d_in, c.M, c.d_in, dX, EpiArgs{nullptr, dX, nullptr, LORA_ACT_NONE},
                                          st);
         }));
       } else {
-        HIPTRY(gemm(G_F32_NN_STORE, a, 1, st, flop, bytes));
-        HIPTRY(update(true));
+        a.cin = dX; a.ldcin = c.d_in;
+        HIPTRY(gemm(f32 ? G_F32_NN_ADD : G_BF16_MED_NN_ADD, a, 1, st, flop, bytes));
       }
     }
-    HIPTRY(timed(K_MULTI_GRAD, 2 * Md * r * (c.d_in + c.d_out), 4 * Md * (c.d_in + c.d_out), st, [&] {
-      const hipError_t e = launch_multi_outer(P, static_cast<const float*>(dY), c.index, c.M, c.d_out, n, r, true, gb, dB, st);
-      return e != hipSuccess ? e : launch_multi_outer(Q, static_cast<const float*>(X), c.index, c.M, c.d_in, n, r, false, gb, dA, st);
+    float* pa = L.splits_t > 1 ? reinterpret_cast<float*>(w + L.parta) : nullptr;
+    float* pb = L.splits_t > 1 ? reinterpret_cast<float*>(w + L.partb) : nullptr;
+    HIPTRY(timed(K_MULTI_GRAD, 2 * Md * r * both, eb * Md * both, st, [&] {
+      return launch_multi_outer(eb, MultiOuter{P, dY, c.d_out, 1, dB, pb}, MultiOuter{Q, X, c.d_in, 0, dA, pa}, c.index, c.M, n, r,
+                                L.splits_t, gb, st);
     }));
+    if (L.splits_t > 1)
+      HIPTRY(timed(K_REDUCE, 0, 4.0 * n * r * L.splits_t * both, st, [&] {
+        return launch_multi_grad_sum(gb, MultiGradSum{pb, L.splits_t, c.d_out, 1, dB}, MultiGradSum{pa, L.splits_t, c.d_in, 0, dA},
+                                     nullptr, n, r, st);
+      }));
     return LORA_OK;
   }
   if (dX && !W_t) {
@@ -2140,7 +2170,8 @@ int multi_backward(const MultiCall& c, const MultiLayout& L, const void* X, cons
     }));
     W_t = w + L.wt;
   }
-  TRY(multi_lists(c, L, L.dx, true, A, w, st));
+  const MultiTranspose tr[2] = {{B, w + L.bt, c.d_out, c.r}, {dX ? A : nullptr, w + L.at, c.r, c.d_in}};
+  TRY(multi_lists(c, L, L.dx, true, A, w, st, tr));
   float *pp = reinterpret_cast<float*>(w + L.part), *pq = reinterpret_cast<float*>(w + L.partq);
   const GemmArgs a = multi_panel_args(c, L, X, c.d_in, A, L.ksplit_p, pp, w);
   const GemmArgs b = multi_panel_args(c, L, dY, c.d_out, w + L.bt, L.ksplit_q, pq, w);

@@ -355,11 +355,18 @@ hipError_t launch_act8_pack(int elem_bytes, const void* X, int64_t ldx, int64_t 
 hipError_t launch_act8_unpack(int elem_bytes, const uint8_t* codes, const float* scale8, int64_t M, int64_t d, void* X,
                               hipStream_t st);
 
+// Stacks transposed: dst [n][C, R] = src [n][R, C], bf16.
+struct MultiTranspose {
+  const void* src;  // NULL: none
+  void* dst;
+  int64_t R, C;
+};
+
 // Rows with an adapter of their own (multi.hip).  index int [M]: a row's adapter,
 // none outside [0, n).  Lists: per 128- and per 256-row tile its adapters
 // (rows of min(rows, n) entries and counts), per group of `per` adapters
 // (ceil(n / per) = groups) the 64-token tiles they occur in (rows of
-// ceil(M / 64)); counts of 0 blocks leave that list out.
+// ceil(M / 64)); counts of 0 blocks leave that list out.  Transposes in the same launch.
 constexpr int kMultiMaxRank = 128;
 struct MultiLists {
   const int* index;
@@ -380,9 +387,11 @@ struct MultiLists {
   int64_t scan16;
   int chunks;
   int* bad;
+  MultiTranspose tr[2];
+  int64_t tr0;  // (set by the launch)
   __host__ __device__ int cap(int rows) const { return n < rows ? n : rows; }
 };
-hipError_t launch_multi_lists(const MultiLists& q, hipStream_t st);
+hipError_t launch_multi_lists(MultiLists q, hipStream_t st);
 // bf16 strip partials: GemmArgs with ad_of, ad_list (128-row tiles), ad_cnt,
 // ad_cap, ad_r; C = fp32 [splits][M, ad_r].  b (may be NULL): another in the same launch.
 hipError_t launch_multi_panel(const GemmArgs& a, int sa, const GemmArgs* b, int sb, hipStream_t st);
@@ -408,18 +417,28 @@ struct MultiStrip {
 hipError_t launch_multi_strip(const MultiStrip& s, hipStream_t st);
 // The product with its rows' adapters (ad_list of 128-row tiles where low, else of 256-row ones).
 hipError_t launch_multi_gemm(GemmArgs a, bool low, hipStream_t st);
-// fp32 P [M, r] = s_a X A_a^T (also clears zero[0 .. nzero)); out (+)= P B_a^T with
-// B [n][N, r] and P fp32 (P32) or bf16; transposes of [n][R, C] stacks.
-hipError_t launch_multi_dot(int elem_bytes, const void* X, const void* A, const float* scales, const int* index, int64_t M,
-                            int64_t K, int n, int r, float* P, hipStream_t st, int* zero = nullptr, int nzero = 0);
-hipError_t launch_multi_update(int elem_bytes, const void* P, bool P32, const void* B, const int* index, int64_t M, int64_t N, int n, int r,
-                               bool add, void* out, hipStream_t st);
-struct MultiTranspose {
-  const void* src;
-  void* dst;
-  int64_t R, C;
+// The simple kernels (few rows, fp32).  fp32 strips P = s_a X A_a^T and, with Q, Q =
+// s_a dY B_a (also clears zero[0 .. nzero)); out = P B_a^T with B [n][N, r], P fp32 (P32) or
+// bf16; out = Q A_a with A [n][r, K].
+struct MultiDot {
+  const void* X;  // [M, K]
+  const void* A;  // [n][r, K]
+  float* P;
+  const void* dY;  // [M, N]
+  const void* B;   // [n][N, r]
+  float* Q;        // or NULL
+  const float* scales;
+  const int* index;
+  int64_t M, K, N;
+  int n, r;
+  int* zero;
+  int nzero;
 };
-hipError_t launch_multi_transpose(int elem_bytes, const MultiTranspose& a, const MultiTranspose* b, int n, hipStream_t st);
+hipError_t launch_multi_dot(int elem_bytes, const MultiDot& d, hipStream_t st);
+hipError_t launch_multi_update(int elem_bytes, const void* P, bool P32, const void* B, const int* index, int64_t M, int64_t N, int n, int r,
+                               void* out, hipStream_t st);
+hipError_t launch_multi_update_rows(int elem_bytes, const float* Q, const void* A, const int* index, int64_t M, int64_t K, int n, int r,
+                                    void* out, hipStream_t st);
 // Gradient partials [splits][total, N] of two products Pt X (ad_list: the groups'
 // token tiles), `rows` rows of Pt a group; their sums.
 hipError_t launch_multi_grad(const GemmArgs& a, int sa, const GemmArgs& b, int sb, int rows, int total, hipStream_t st);
@@ -432,8 +451,18 @@ struct MultiGradSum {
 };
 hipError_t launch_multi_grad_sum(int out_bytes, const MultiGradSum& a, const MultiGradSum& b, const int* gbad, int n, int r,
                                  hipStream_t st);
-hipError_t launch_multi_outer(const float* P, const float* X, const int* index, int64_t M, int64_t N, int n, int r, bool tr,
-                              int out_bytes, void* out, hipStream_t st);
+// gbad may be NULL.  The simple gradients: two sums over tokens of P[t, q] X[t, j],
+// with partials for multi_grad_sum where splits > 1.
+struct MultiOuter {
+  const float* P;  // [M, r]
+  const void* X;   // [M, N]
+  int64_t N;
+  int tr;
+  void* out;
+  float* part;
+};
+hipError_t launch_multi_outer(int elem_bytes, const MultiOuter& a, const MultiOuter& b, const int* index, int64_t M, int n, int r, int splits,
+                              int out_bytes, hipStream_t st);
 
 // The panel s X A^T and the adapter's gradient from X in 8 bits (act8.hip): fp32
 // partials of codes A^T times the rows' scales, [splits][rows, r8] (zeros from row

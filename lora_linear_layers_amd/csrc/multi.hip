@@ -74,8 +74,34 @@ __device__ __forceinline__ int wave_distinct(int v, int lane, int& mine) {
   return k;
 }
 
+// dst [n][C, R] = src [n][R, C] (bf16) transposed, block b of its 64 x 32 tiles
+// (64 along C): rows in 8-byte pieces on both sides (R and C multiples of 8).
+__device__ __forceinline__ void transpose_stack(const MultiTranspose& q, int64_t b, uint16_t (*tile)[36]) {
+  const int64_t tc = (q.C + 63) / 64, per = tc * ((q.R + 31) / 32), z = b / per, id = b - z * per;
+  const int64_t r0 = id / tc * 32, c0 = id % tc * 64;
+  const uint16_t* src = static_cast<const uint16_t*>(q.src) + z * q.R * q.C;
+  uint16_t* dst = static_cast<uint16_t*>(q.dst) + z * q.R * q.C;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {  // 16 rows of 16 pieces a pass
+    const int rr = (threadIdx.x >> 4) + 16 * h, cc = (threadIdx.x & 15) * 4;
+    if (r0 + rr < q.R && c0 + cc < q.C) {
+      const u32x2 v = *reinterpret_cast<const u32x2*>(src + (r0 + rr) * q.C + c0 + cc);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tile[cc + e][rr] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {  // 32 columns of 8 pieces a pass
+    const int cc = (threadIdx.x >> 3) + 32 * h, rr = (threadIdx.x & 7) * 4;
+    if (c0 + cc < q.C && r0 + rr < q.R)
+      *reinterpret_cast<u32x2*>(dst + (c0 + cc) * q.R + r0 + rr) = *reinterpret_cast<const u32x2*>(&tile[cc][rr]);
+  }
+}
+
 __global__ void __launch_bounds__(256) multi_lists_kernel(const MultiLists q) {
   __shared__ int ids[256];
+  __shared__ __attribute__((aligned(8))) uint16_t tile[64][36];
   __shared__ int wsum[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int b = blockIdx.x;
@@ -117,6 +143,11 @@ __global__ void __launch_bounds__(256) multi_lists_kernel(const MultiLists q) {
     return;
   }
   b -= q.t128 + q.t256;
+  if (b >= q.groups + q.n * q.chunks) {
+    const int64_t k = b - (q.groups + (int64_t)q.n * q.chunks);
+    transpose_stack(q.tr[k >= q.tr0 ? 1 : 0], k >= q.tr0 ? k - q.tr0 : k, tile);
+    return;
+  }
   if (b >= q.groups) {
     b -= q.groups;
     const int a = b / q.chunks, c = b - a * q.chunks;
@@ -284,52 +315,123 @@ __global__ void __launch_bounds__(256) multi_strip_kernel(const MultiStrip s) {
   }
 }
 
-// fp32 strips P [M, r], one wave a value; rows of whole 16-byte pieces.
+// fp32 strips by dot products.  blockIdx.z 0: P [M, r] = s_a X A_a^T, one wave a
+// value, 16 bytes of both rows a lane; 1: Q [M, r] = s_a dY B_a with B [n][N, r] as
+// it is, one wave 8 values, a lane an element of dY's row and 8 ranks of B's.
 template <typename T>
-__global__ void __launch_bounds__(256) multi_dot_kernel(const T* X, const T* A, const float* scales, const int* index,
-                                                        int64_t M, int64_t K, int n, int r, float* P, int* zero, int nzero) {
+__global__ void __launch_bounds__(256) multi_dot_kernel(const MultiDot d) {
   constexpr int E = 16 / sizeof(T);
   const int64_t t = blockIdx.x;
-  const int q = blockIdx.y * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int i = threadIdx.x; i < nzero; i += 256) zero[i] = 0;
-  if (q >= r) return;
-  const int a = adapter_at(index, t, M, n);
-  float s = 0.f;
-  if (a >= 0) {
-    const u32x4* x = reinterpret_cast<const u32x4*>(X + t * K);
-    const u32x4* w = reinterpret_cast<const u32x4*>(A + ((int64_t)a * r + q) * K);
+  const int lane = threadIdx.x & 63, wave = blockIdx.y * 4 + (threadIdx.x >> 6);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+    for (int i = threadIdx.x; i < d.nzero; i += 256) d.zero[i] = 0;
+  const int a = adapter_at(d.index, t, d.M, d.n), r = d.r;
+  if (blockIdx.z == 0) {
+    const int q = wave;
+    if (q >= r) return;
+    float s = 0.f;
+    if (a >= 0) {
+      const u32x4* x = reinterpret_cast<const u32x4*>(static_cast<const T*>(d.X) + t * d.K);
+      const u32x4* w = reinterpret_cast<const u32x4*>(static_cast<const T*>(d.A) + ((int64_t)a * r + q) * d.K);
 #pragma unroll 8
-    for (int64_t k = lane; k < K / E; k += 64) {
-      const u32x4 u = x[k], v = w[k];
+      for (int64_t k = lane; k < d.K / E; k += 64) {
+        const u32x4 u = x[k], v = w[k];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (sizeof(T) == 2) {
-          s = __builtin_fmaf(__builtin_bit_cast(float, u[e] << 16), __builtin_bit_cast(float, v[e] << 16), s);
-          s = __builtin_fmaf(__builtin_bit_cast(float, u[e] & 0xFFFF0000u), __builtin_bit_cast(float, v[e] & 0xFFFF0000u), s);
-        } else {
+        for (int e = 0; e < 4; ++e) {
           const uint32_t ue = u[e], ve = v[e];  // (a vector's element has no address to cast at)
-          s = __builtin_fmaf(__builtin_bit_cast(float, ue), __builtin_bit_cast(float, ve), s);
+          if constexpr (sizeof(T) == 2) {
+            s = __builtin_fmaf(__builtin_bit_cast(float, ue << 16), __builtin_bit_cast(float, ve << 16), s);
+            s = __builtin_fmaf(__builtin_bit_cast(float, ue & 0xFFFF0000u), __builtin_bit_cast(float, ve & 0xFFFF0000u), s);
+          } else {
+            s = __builtin_fmaf(__builtin_bit_cast(float, ue), __builtin_bit_cast(float, ve), s);
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+      s *= d.scales[a];
+    }
+    if (lane == 0) d.P[t * r + q] = s;
+    return;
+  }
+  const int q = 8 * wave;
+  if (q >= r) return;
+  float s[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[e] = 0.f;
+  if (a >= 0) {
+    const T* g = static_cast<const T*>(d.dY) + t * d.N;
+    const T* b = static_cast<const T*>(d.B) + (int64_t)a * d.N * r + q;
+#pragma unroll 8
+    for (int64_t k = lane; k < d.N; k += 64) {
+      const float x = val(g[k]);
+      const u32x4* w = reinterpret_cast<const u32x4*>(b + k * r);
+#pragma unroll
+      for (int h = 0; h < 8 / E; ++h) {
+        const u32x4 v = w[h];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const uint32_t u = v[e * sizeof(T) / 4];
+          s[h * E + e] = __builtin_fmaf(x, __builtin_bit_cast(float, sizeof(T) == 4 ? u : e & 1 ? u & 0xFFFF0000u : u << 16), s[h * E + e]);
         }
       }
     }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-    s *= scales[a];
   }
-  if (lane == 0) P[t * r + q] = s;
+  const float sc = a >= 0 ? d.scales[a] : 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s[e] += __shfl_xor(s[e], o);
+    if (lane == e) d.Q[t * r + q + e] = a >= 0 ? s[e] * sc : 0.f;
+  }
 }
 
-// out [M, N] (+)= P_t . B_a[j, :], B [n][N, r]; a thread one output, 16 bytes of B
+// out [M, K] = Q_t A_a, A [n][r, K]: a thread 16 bytes of a row.
+template <typename T>
+__global__ void __launch_bounds__(256) multi_update_rows_kernel(const float* Q, const T* A, const int* index, int64_t M, int64_t K,
+                                                                int n, int r, T* out) {
+  constexpr int E = 16 / sizeof(T);
+  const int64_t t = blockIdx.y, k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * E;
+  if (k >= K) return;
+  const int a = adapter_at(index, t, M, n);
+  float s[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) s[e] = 0.f;
+  if (a >= 0) {
+    const T* w = A + (int64_t)a * r * K + k;
+    const float* p = Q + t * r;
+#pragma unroll 8
+    for (int q = 0; q < r; ++q) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(w + (int64_t)q * K);
+      const float x = p[q];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t u = v[e * sizeof(T) / 4];
+        s[e] = __builtin_fmaf(x, __builtin_bit_cast(float, sizeof(T) == 4 ? u : e & 1 ? u & 0xFFFF0000u : u << 16), s[e]);
+      }
+    }
+  }
+  u32x4 o;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (sizeof(T) == 2)
+      o[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
+    else
+      o[e] = __builtin_bit_cast(uint32_t, s[e]);
+  }
+  *reinterpret_cast<u32x4*>(out + t * K + k) = o;
+}
+
+// out [M, N] = P_t . B_a[j, :], B [n][N, r]; a thread one output, 16 bytes of B
 // at a time.
 template <typename T, typename TP>
 __global__ void __launch_bounds__(256) multi_update_kernel(const TP* P, const T* B, const int* index, int64_t M, int64_t N,
-                                                           int n, int r, int add, T* out) {
+                                                           int n, int r, T* out) {
   constexpr int E = 16 / sizeof(T);
   const int64_t t = blockIdx.y, j = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (j >= N) return;
   const int a = adapter_at(index, t, M, n);
-  float s = add ? val(out[t * N + j]) : 0.f;
+  float s = 0.f;
   if (a >= 0) {
     const u32x4* b = reinterpret_cast<const u32x4*>(B + ((int64_t)a * N + j) * r);
     const TP* p = P + t * r;
@@ -345,27 +447,6 @@ __global__ void __launch_bounds__(256) multi_update_kernel(const TP* P, const T*
     }
   }
   store_out<T>(out, t * N + j, s);
-}
-
-// dst [n][C, R] = src [n][R, C] transposed, through 32 x 32 tiles; two stacks in
-// one launch (blockIdx.z < n: the first).
-template <typename T>
-__global__ void __launch_bounds__(256) multi_transpose_kernel(const MultiTranspose a, const MultiTranspose b, int n) {
-  __shared__ T tile[32][33];
-  const int w = (int)blockIdx.z >= n ? 1 : 0;
-  const MultiTranspose& q = w ? b : a;
-  const int64_t z = (int64_t)blockIdx.z - (w ? n : 0);
-  const int64_t tc = (q.C + 31) / 32, id = blockIdx.x;
-  if (id >= tc * ((q.R + 31) / 32)) return;
-  const int64_t r0 = id / tc * 32, c0 = id % tc * 32;
-  const T* src = static_cast<const T*>(q.src) + z * q.R * q.C;
-  T* dst = static_cast<T*>(q.dst) + z * q.R * q.C;
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  for (int k = y; k < 32; k += 8)
-    if (r0 + k < q.R && c0 + x < q.C) tile[k][x] = src[(r0 + k) * q.C + c0 + x];
-  __syncthreads();
-  for (int k = y; k < 32; k += 8)
-    if (c0 + k < q.C && r0 + x < q.R) dst[(c0 + k) * q.R + r0 + x] = tile[x][k];
 }
 
 // ---------------------------------------------------------------------------
@@ -398,7 +479,7 @@ __global__ void __launch_bounds__(256) multi_grad_sum_kernel(const MultiGradSum 
   __shared__ float tile[64][33];
   const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
   const int64_t stride = (int64_t)n * r * g.N;
-  const float spoil = gbad[a] ? __builtin_nanf("") : 0.f;
+  const float spoil = gbad && gbad[a] ? __builtin_nanf("") : 0.f;
   for (int q0 = 0; q0 < r; q0 += 32) {
     const int rows = min(32, r - q0);
     if (g.tr) __syncthreads();
@@ -422,42 +503,77 @@ __global__ void __launch_bounds__(256) multi_grad_sum_kernel(const MultiGradSum 
   }
 }
 
-// fp32: out [n][r, N] (or [n][N, r], tr) = sum over the adapter's tokens of
-// P[t, q] X[t, j]; a block is 64 columns and one adapter, a thread one column
-// and a quarter of the ranks; tokens in order.
-template <typename T, typename TO>
-__global__ void __launch_bounds__(256) multi_outer_kernel(const float* P, const T* X, const int* index, int64_t M, int64_t N,
-                                                          int n, int r, int tr, TO* out) {
-  __shared__ int ids[256];
-  const int a = blockIdx.y, x = threadIdx.x & 63, y = threadIdx.x >> 6;
-  const int64_t j = (int64_t)blockIdx.x * 64 + x;
-  float acc[32];
+// Simple gradients, from fp32 strips: out [n][r, N] (or [n][N, r], tr) = sum over the
+// adapter's tokens of P[t, q] X[t, j].  A block is 64 columns of one adapter over a
+// range of tokens (partials [splits][n r, N] where there are several), a wave a
+// quarter of the ranks, QK at most; tokens in order, 64 at a time: the adapter's
+// are found, their strips go to LDS, 8 rows of X are in flight.
+template <typename T, typename TO, int QK>
+__global__ void __launch_bounds__(256) multi_outer_kernel(const MultiOuter o0, const MultiOuter o1, const int* index, int64_t M, int n, int r,
+                                                          int splits) {
+  const int w = (int)blockIdx.z >= splits ? 1 : 0;
+  const MultiOuter& o = w ? o1 : o0;
+  const int z = blockIdx.z - (w ? splits : 0);
+  const int64_t j = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+  if ((int64_t)blockIdx.x * 64 >= o.N) return;
+  __shared__ int list[64];
+  __shared__ int found;
+  __shared__ __attribute__((aligned(16))) float strip[64][4 * QK];
+  const int a = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const T* X = static_cast<const T*>(o.X);
+  const int64_t per = ((M + splits - 1) / splits + 63) / 64 * 64, end = min(M, (z + 1) * per);
+  float acc[QK];
 #pragma unroll
-  for (int k = 0; k < 32; ++k) acc[k] = 0.f;
-  for (int64_t t0 = 0; t0 < M; t0 += 256) {
+  for (int k = 0; k < QK; ++k) acc[k] = 0.f;
+  for (int64_t t0 = z * per; t0 < end; t0 += 64) {
     __syncthreads();
-    ids[threadIdx.x] = adapter_at(index, t0 + threadIdx.x, M, n);
+    if (wave == 0) {
+      const bool is = adapter_at(index, t0 + lane, end, n) == a;
+      const uint64_t m = __ballot(is);
+      if (is) list[__popcll(m & ((1ull << lane) - 1))] = lane;
+      if (lane == 0) found = __popcll(m);
+    }
     __syncthreads();
-    for (int i = 0; i < 256; ++i) {
-      if (ids[i] != a) continue;
-      const float v = j < N ? val(X[(t0 + i) * N + j]) : 0.f;
+    const int cnt = found;
+    if (cnt == 0) continue;  // (uniform)
+    for (int e = threadIdx.x; e < cnt * 4 * QK; e += 256) {
+      const int i = e / (4 * QK), q = e - i * 4 * QK;
+      strip[i][q] = q < r ? o.P[(t0 + list[i]) * r + q] : 0.f;
+    }
+    __syncthreads();
+    for (int i0 = 0; i0 < cnt; i0 += 8) {
+      float x[8];
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (y + 4 * k < r) acc[k] = __builtin_fmaf(P[(t0 + i) * r + y + 4 * k], v, acc[k]);
+      for (int u = 0; u < 8; ++u) x[u] = i0 + u < cnt && j < o.N ? val(X[(t0 + list[i0 + u]) * o.N + j]) : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i0 + u < cnt) {
+#pragma unroll
+          for (int k = 0; k < QK; ++k) acc[k] = __builtin_fmaf(strip[i0 + u][wave * QK + k], x[u], acc[k]);
+        }
     }
   }
-  if (j >= N) return;
+  if (j >= o.N) return;
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    const int q = y + 4 * k;
-    if (q < r) store_out<TO>(out, tr ? ((int64_t)a * N + j) * r + q : ((int64_t)a * r + q) * N + j, acc[k]);
+  for (int k = 0; k < QK; ++k) {
+    const int q = wave * QK + k;
+    if (q >= r) continue;
+    const int64_t at = ((int64_t)a * r + q) * o.N + j;
+    if (splits > 1)
+      o.part[(int64_t)z * n * r * o.N + at] = acc[k];
+    else
+      store_out<TO>(o.out, o.tr ? ((int64_t)a * o.N + j) * r + q : at, acc[k]);
   }
 }
 
 }  // namespace
 
-hipError_t launch_multi_lists(const MultiLists& q, hipStream_t st) {
-  const int64_t blocks = (int64_t)q.t128 + q.t256 + q.groups + (int64_t)q.n * q.chunks;
+hipError_t launch_multi_lists(MultiLists q, hipStream_t st) {
+  auto tiles = [&](const MultiTranspose& t) { return t.src ? (t.R + 31) / 32 * ((t.C + 63) / 64) * q.n : 0; };
+  q.tr0 = tiles(q.tr[0]);
+  const int64_t blocks = (int64_t)q.t128 + q.t256 + q.groups + (int64_t)q.n * q.chunks + q.tr0 + tiles(q.tr[1]);
+  for (const MultiTranspose& t : q.tr)
+    if (t.src && (t.R % 8 || t.C % 8)) return hipErrorInvalidValue;
   if (blocks <= 0) return hipSuccess;
   if (q.M <= 0 || q.n < 1 || blocks > INT32_MAX) return hipErrorInvalidValue;
   hipLaunchKernelGGL(multi_lists_kernel, dim3((unsigned)blocks), dim3(256), 0, st, q);
@@ -510,22 +626,37 @@ hipError_t launch_multi_gemm(GemmArgs a, bool low, hipStream_t st) {
   return hipGetLastError();
 }
 
-hipError_t launch_multi_dot(int elem_bytes, const void* X, const void* A, const float* scales, const int* index, int64_t M,
-                            int64_t K, int n, int r, float* P, hipStream_t st, int* zero, int nzero) {
-  if (M <= 0) return hipSuccess;
-  if (M > INT32_MAX) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)M, (unsigned)((r + 3) / 4));
+hipError_t launch_multi_dot(int elem_bytes, const MultiDot& d, hipStream_t st) {
+  if (d.M <= 0) return hipSuccess;
+  if (d.M > INT32_MAX || d.r % 8 || d.K % 8) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)d.M, (unsigned)((d.r + 3) / 4), d.Q ? 2u : 1u);
   if (elem_bytes == 2)
-    hipLaunchKernelGGL((multi_dot_kernel<uint16_t>), grid, dim3(256), 0, st, static_cast<const uint16_t*>(X),
-                       static_cast<const uint16_t*>(A), scales, index, M, K, n, r, P, zero, nzero);
+    hipLaunchKernelGGL((multi_dot_kernel<uint16_t>), grid, dim3(256), 0, st, d);
   else
-    hipLaunchKernelGGL((multi_dot_kernel<float>), grid, dim3(256), 0, st, static_cast<const float*>(X),
-                       static_cast<const float*>(A), scales, index, M, K, n, r, P, zero, nzero);
+    hipLaunchKernelGGL((multi_dot_kernel<float>), grid, dim3(256), 0, st, d);
   return hipGetLastError();
 }
 
+hipError_t launch_multi_update_rows(int elem_bytes, const float* Q, const void* A, const int* index, int64_t M, int64_t K, int n, int r,
+                                    void* out, hipStream_t st) {
+  if (K % 8) return hipErrorInvalidValue;
+  for (int64_t t0 = 0; t0 < M; t0 += 65535) {  // (rows on the grid's y)
+    const int64_t m = std::min<int64_t>(65535, M - t0);
+    const dim3 grid((unsigned)((K * elem_bytes / 16 + 255) / 256), (unsigned)m);
+    if (elem_bytes == 2)
+      hipLaunchKernelGGL((multi_update_rows_kernel<uint16_t>), grid, dim3(256), 0, st, Q + t0 * r, static_cast<const uint16_t*>(A),
+                         index + t0, m, K, n, r, static_cast<uint16_t*>(out) + t0 * K);
+    else
+      hipLaunchKernelGGL((multi_update_rows_kernel<float>), grid, dim3(256), 0, st, Q + t0 * r, static_cast<const float*>(A), index + t0,
+                         m, K, n, r, static_cast<float*>(out) + t0 * K);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 hipError_t launch_multi_update(int elem_bytes, const void* P, bool P32, const void* B, const int* index, int64_t M, int64_t N,
-                               int n, int r, bool add, void* out, hipStream_t st) {
+                               int n, int r, void* out, hipStream_t st) {
   if (elem_bytes == 4 && !P32) return hipErrorInvalidValue;
   // (rows on the grid's y, 65535 at most)
   for (int64_t t0 = 0; t0 < M; t0 += 65535) {
@@ -535,29 +666,17 @@ hipError_t launch_multi_update(int elem_bytes, const void* P, bool P32, const vo
     const uint16_t* p16 = static_cast<const uint16_t*>(P) + t0 * r;
     if (elem_bytes == 4)
       hipLaunchKernelGGL((multi_update_kernel<float, float>), grid, dim3(256), 0, st, p32, static_cast<const float*>(B), index + t0,
-                         m, N, n, r, add ? 1 : 0, static_cast<float*>(out) + t0 * N);
+                         m, N, n, r, static_cast<float*>(out) + t0 * N);
     else if (P32)
       hipLaunchKernelGGL((multi_update_kernel<uint16_t, float>), grid, dim3(256), 0, st, p32, static_cast<const uint16_t*>(B),
-                         index + t0, m, N, n, r, add ? 1 : 0, static_cast<uint16_t*>(out) + t0 * N);
+                         index + t0, m, N, n, r, static_cast<uint16_t*>(out) + t0 * N);
     else
       hipLaunchKernelGGL((multi_update_kernel<uint16_t, uint16_t>), grid, dim3(256), 0, st, p16, static_cast<const uint16_t*>(B),
-                         index + t0, m, N, n, r, add ? 1 : 0, static_cast<uint16_t*>(out) + t0 * N);
+                         index + t0, m, N, n, r, static_cast<uint16_t*>(out) + t0 * N);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
-}
-
-hipError_t launch_multi_transpose(int elem_bytes, const MultiTranspose& a, const MultiTranspose* b, int n, hipStream_t st) {
-  auto tiles = [](const MultiTranspose& q) { return (q.R + 31) / 32 * ((q.C + 31) / 32); };
-  const int64_t t = std::max(tiles(a), b ? tiles(*b) : 0);
-  if (n < 1 || 2 * (int64_t)n > 65535 || t > INT32_MAX) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)t, 1, (unsigned)(b ? 2 * n : n));
-  if (elem_bytes == 2)
-    hipLaunchKernelGGL((multi_transpose_kernel<uint16_t>), grid, dim3(256), 0, st, a, b ? *b : a, n);
-  else
-    hipLaunchKernelGGL((multi_transpose_kernel<float>), grid, dim3(256), 0, st, a, b ? *b : a, n);
-  return hipGetLastError();
 }
 
 hipError_t launch_multi_grad(const GemmArgs& a, int sa, const GemmArgs& b, int sb, int rows, int total, hipStream_t st) {
@@ -589,16 +708,35 @@ hipError_t launch_multi_grad_sum(int out_bytes, const MultiGradSum& a, const Mul
   return hipGetLastError();
 }
 
-hipError_t launch_multi_outer(const float* P, const float* X, const int* index, int64_t M, int64_t N, int n, int r, bool tr,
-                              int out_bytes, void* out, hipStream_t st) {
-  if (n < 1 || n > 65535 || r > kMultiMaxRank) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)((N + 63) / 64), (unsigned)n);
-  if (out_bytes == 2)
-    hipLaunchKernelGGL((multi_outer_kernel<float, uint16_t>), grid, dim3(256), 0, st, P, X, index, M, N, n, r, tr ? 1 : 0,
-                       static_cast<uint16_t*>(out));
+namespace {
+template <typename T, typename TO>
+void run_outer(const MultiOuter& a, const MultiOuter& b, const int* index, int64_t M, int n, int r, int splits, hipStream_t st) {
+  const dim3 grid((unsigned)((std::max(a.N, b.N) + 63) / 64), (unsigned)n, (unsigned)(2 * splits));
+  auto go = [&](auto qk) {
+    hipLaunchKernelGGL((multi_outer_kernel<T, TO, decltype(qk)::value>), grid, dim3(256), 0, st, a, b, index, M, n, r, splits);
+  };
+  if (r <= 8)
+    go(std::integral_constant<int, 2>{});
+  else if (r <= 16)
+    go(std::integral_constant<int, 4>{});
+  else if (r <= 32)
+    go(std::integral_constant<int, 8>{});
+  else if (r <= 64)
+    go(std::integral_constant<int, 16>{});
   else
-    hipLaunchKernelGGL((multi_outer_kernel<float, float>), grid, dim3(256), 0, st, P, X, index, M, N, n, r, tr ? 1 : 0,
-                       static_cast<float*>(out));
+    go(std::integral_constant<int, 32>{});
+}
+}  // namespace
+
+hipError_t launch_multi_outer(int elem_bytes, const MultiOuter& a, const MultiOuter& b, const int* index, int64_t M, int n, int r, int splits,
+                              int out_bytes, hipStream_t st) {
+  if (M < 1 || n < 1 || n > 65535 || r > kMultiMaxRank || splits < 1 || splits > 32 || (splits > 1 && (!a.part || !b.part)))
+    return hipErrorInvalidValue;
+  if (elem_bytes == 2)
+    out_bytes == 2 ? run_outer<uint16_t, uint16_t>(a, b, index, M, n, r, splits, st)
+                   : run_outer<uint16_t, float>(a, b, index, M, n, r, splits, st);
+  else
+    out_bytes == 2 ? run_outer<float, uint16_t>(a, b, index, M, n, r, splits, st) : run_outer<float, float>(a, b, index, M, n, r, splits, st);
   return hipGetLastError();
 }
 
