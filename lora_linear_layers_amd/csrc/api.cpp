@@ -1873,7 +1873,7 @@ struct MultiLayout {
 // Token splits of the row groups' gradients [64, N] of both operands, which share
 // a launch of `tiles` column tiles: about two blocks a CU.
 int multi_grad_splits(int64_t M, int64_t tiles, int64_t groups) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(1, tiles * groups), cdiv(M, 512), 16}));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({256 / std::max<int64_t>(1, tiles * groups), cdiv(M, 512), 16}));
 }
 
 MultiLayout make_multi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r,
@@ -1940,6 +1940,14 @@ MultiLayout make_multi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, int6
     if (!bwd || need_dx) L.p = take(size_t(M) * r * 2);
     if (bwd) {
       panel_split(M, d_out, 64, &L.splits_q, &L.ksplit_q);
+      // (both share a launch: about a block a CU together)
+      auto halve = [](int64_t K, int* splits, int64_t* ksplit) {
+        if (*splits < 2) return;
+        *ksplit = rup(cdiv(K, (*splits + 1) / 2), 64);
+        *splits = (int)cdiv(K, *ksplit);
+      };
+      halve(d_in, &L.splits_p, &L.ksplit_p);
+      halve(d_out, &L.splits_q, &L.ksplit_q);
       L.partq = take(size_t(L.splits_q) * M * r * 4);
       L.glist = take(size_t(L.groups) * cdiv(M, 64) * 4);
       L.gcnt = take(size_t(L.groups) * 4);

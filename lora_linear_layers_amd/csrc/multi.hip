@@ -690,7 +690,9 @@ hipError_t launch_multi_grad(const GemmArgs& a, int sa, const GemmArgs& b, int s
   const GemmPair q{{a, b}, sa};
   const int64_t t = (std::max(a.n_store, b.n_store) + sdma::BN - 1) / sdma::BN;
   const dim3 grid((unsigned)t, (unsigned)(sa + sb), (unsigned)groups);
-  if (rows <= 64)
+  if (rows <= 64 && t * (sa + sb) * groups <= 512)
+    hipLaunchKernelGGL((multi_grad_kernel<64, 4>), grid, dim3(sdma::NT), 0, st, q, sb, rows, total);
+  else if (rows <= 64)
     hipLaunchKernelGGL((multi_grad_kernel<64, 2>), grid, dim3(sdma::NT), 0, st, q, sb, rows, total);
   else
     hipLaunchKernelGGL((multi_grad_kernel<128, 3>), grid, dim3(sdma::NT), 0, st, q, sb, rows, total);
