@@ -509,16 +509,18 @@ size_t lora_rmsnorm_workspace_bytes(int64_t M, int64_t d);
  * with the checkpoint in X's place: of the three gradients only the
  * adapter's read X, through X A^T and (dY B)^T X.  member as in
  * lora_linear_epi_bwd (W, or W_nf4 with absmax and the HOST table16; W_t; dY, dX
- * or NULL, dA, dB); codes 16-byte aligned; its own sizing call;
- * d_in <= LORA_NORM_MAX_DIM.  dX does not depend on X.
+ * or NULL, dA, dB; with grad_dtype LORA_BF16 the latter two are bf16 arrays); codes
+ * 16-byte aligned; its own sizing call; d_in <= LORA_NORM_MAX_DIM.  dX does not
+ * depend on X.
  */
 int lora_act8_pack(int dtype, int64_t M, int64_t d, const void* X, int64_t ldx, uint8_t* codes, float* scale8,
                    void* stream);
 int lora_act8_unpack(int dtype, int64_t M, int64_t d, const uint8_t* codes, const float* scale8, void* X,
                      void* stream);
 int lora_act8_linear_bwd(int dtype, int64_t M, int64_t d_in, const lora_group_member* member, const uint8_t* codes,
-                         const float* scale8, const float* table16, void* ws, size_t ws_bytes, void* stream);
-size_t lora_act8_linear_workspace_bytes(int dtype, int64_t M, int64_t d_in, const lora_group_member* member);
+                         const float* scale8, const float* table16, int grad_dtype, void* ws, size_t ws_bytes,
+                         void* stream);
+size_t lora_act8_linear_workspace_bytes(int dtype, int64_t M, int64_t d_in, const lora_group_member* member, int grad_dtype);
 
 /*
  * A projection whose rows each carry an adapter of their own: requests that

@@ -95,8 +95,8 @@ _SIGS = {
     "lora_rmsnorm_workspace_bytes": ([_i64, _i64], _sz),
     "lora_act8_pack": ([_int, _i64, _i64, _vp, _i64, _vp, _vp, _vp], _int),
     "lora_act8_unpack": ([_int, _i64, _i64, _vp, _vp, _vp, _vp], _int),
-    "lora_act8_linear_bwd": ([_int, _i64, _i64, _mp, _vp, _vp, _fp, _vp, _sz, _vp], _int),
-    "lora_act8_linear_workspace_bytes": ([_int, _i64, _i64, _mp], _sz),
+    "lora_act8_linear_bwd": ([_int, _i64, _i64, _mp, _vp, _vp, _fp, _int, _vp, _sz, _vp], _int),
+    "lora_act8_linear_workspace_bytes": ([_int, _i64, _i64, _mp, _int], _sz),
     "lora_multi_workspace_bytes": ([_int, _int] + [_i64] * 5 + [_int, _int], _sz),
     "lora_multi_fwd": ([_int] + [_i64] * 5 + [_vp] * 8 + [_sz, _vp], _int),
     "lora_multi_bwd": ([_int] + [_i64] * 5 + [_vp] * 11 + [_int, _vp, _sz, _vp], _int),

@@ -903,9 +903,9 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
                   const void* W, const Nf4W* nf4, const void* A, const void* B, const Rope* rope, const void* dY,
                   void* dX, float* dA, float* dB, void* ws, const Layout& L, hipStream_t st,
                   const PanelSlices* ov = nullptr, const void* Xa = nullptr, const uint8_t* keep = nullptr,
-                  const void* Wt_in = nullptr, Act8Args* x8 = nullptr) {
+                  const void* Wt_in = nullptr, Act8Args* x8 = nullptr, bool low = false) {
   // x8: X in 8 bits (act8.hip) instead of X, for layouts that run the panels and
-  // the gradients in pairs
+  // the gradients in pairs; low: dA and dB in bf16 there
   // LoRA dropout: Xa is the adapter's (masked) input and `keep` the mask that
   // the rank-r term of dX passes through; X itself still feeds the base path
   const void* Xp = Xa ? Xa : X;
@@ -1135,6 +1135,7 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
   // launch (a group's: one for all its members, after the group's dA)
   float* partb = f32 ? part : (ov && ov->partb ? ov->partb : reinterpret_cast<float*>(w + L.partb));
   ReduceBatch own;
+  own.low = low;
   ReduceBatch* red = f32 ? nullptr : (ov && ov->red ? ov->red : &own);
   // dB^T = Pt G  -> partials [splits][r8, d_out] -> dB [d_out, r]
   GemmArgs ab = blank();
@@ -1778,10 +1779,10 @@ struct Act8Layout {
   bool direct = false;
   int splits = 1;
   int64_t ksplit = 0;
-  size_t x = 0, total = 0;
+  size_t x = 0, ga = 0, gb = 0, total = 0;  // (ga, gb: gradients in fp32 before they are rounded)
 };
 
-Act8Layout make_act8_layout(int dtype, int64_t M, int64_t d_in, const lora_group_member& m) {
+Act8Layout make_act8_layout(int dtype, int64_t M, int64_t d_in, const lora_group_member& m, bool low) {
   Act8Layout A;
   A.E = make_epi_layout(true, dtype, M, d_in, m, lora_epilogue{LORA_ACT_NONE, nullptr, nullptr, nullptr});
   const Layout& L = A.E.L;
@@ -1793,8 +1794,16 @@ Act8Layout make_act8_layout(int dtype, int64_t M, int64_t d_in, const lora_group
     A.ksplit = rup(L.ksplit_p, 128);
     A.splits = (int)cdiv(d_in, A.ksplit);
   } else {
-    A.x = align256(A.total);
-    A.total = A.x + align256(size_t(M) * d_in * elem_bytes(dtype));
+    auto take = [&](size_t bytes) {
+      const size_t at = align256(A.total);
+      A.total = at + align256(bytes);
+      return at;
+    };
+    A.x = take(size_t(M) * d_in * elem_bytes(dtype));
+    if (low) {
+      A.ga = take(size_t(m.r) * d_in * 4);
+      A.gb = take(size_t(m.r) * m.d_out * 4);
+    }
   }
   return A;
 }
@@ -1867,7 +1876,7 @@ struct MultiLayout {
   int64_t ksplit_p = 0, ksplit_q = 0;
   size_t list128 = 0, cnt128 = 0, list256 = 0, cnt256 = 0, glist = 0, gcnt = 0, part = 0, partq = 0, p = 0, pt = 0, qt = 0,
          bt = 0, at = 0, wt = 0, st_part = 0, st_cnt = 0, base = 0, parta = 0, partb = 0, bad = 0, gbad = 0, mask = 0, total = 0;
-  int chunks = 0;  // of an adapter's second operand in the product, looked at for infinities and NaNs
+  int chunks = 0, pieces = 0;  // of an adapter's second operand in the product, looked at for infinities and NaNs
 };
 
 // Token splits of the row groups' gradients [64, N] of both operands, which share
@@ -1928,7 +1937,10 @@ MultiLayout make_multi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, int6
       L.cnt256 = take(size_t(t256) * 4);
     }
     if (g.gemm) {
-      L.chunks = (int)cdiv((bwd ? d_in : d_out) * r * 2, 65536);
+      // (16 KB a block, more where that would be over two blocks a CU)
+      const int64_t bytes = (bwd ? d_in : d_out) * r * 2;
+      L.chunks = (int)std::max<int64_t>(1, std::min(cdiv(bytes, 16384), 512 / n));
+      L.pieces = (int)cdiv(bytes / 16, L.chunks);
       L.bad = take(size_t(n) * L.chunks * 4);
     }
     // cleared together: the stream kernel's counters and the spoilt gradients
@@ -1996,7 +2008,7 @@ int multi_lists(const MultiCall& c, const MultiLayout& L, const MultiProduct& g,
   q.zero = reinterpret_cast<int*>(w + L.st_cnt);
   q.nzero = (g.gemm ? g.plan.half : 0) + (bwd ? (int)c.n : 0);
   if (L.chunks) {
-    q.scan = scan; q.scan16 = (bwd ? c.d_in : c.d_out) * c.r / 8; q.chunks = L.chunks;
+    q.scan = scan; q.scan16 = (bwd ? c.d_in : c.d_out) * c.r / 8; q.chunks = L.chunks; q.pieces = L.pieces;
     q.bad = reinterpret_cast<int*>(w + L.bad);
   }
   double bytes = 4.0 * c.M;
@@ -2753,24 +2765,28 @@ int lora_act8_unpack(int dtype, int64_t M, int64_t d, const uint8_t* codes, cons
   return LORA_OK;
 }
 
-size_t lora_act8_linear_workspace_bytes(int dtype, int64_t M, int64_t d_in, const lora_group_member* member) {
+size_t lora_act8_linear_workspace_bytes(int dtype, int64_t M, int64_t d_in, const lora_group_member* member, int grad_dtype) {
   const lora_epilogue none{LORA_ACT_NONE, nullptr, nullptr, nullptr};
   if (check_epi_sizes(dtype, M, d_in, member, &none) != LORA_OK || d_in > LORA_NORM_MAX_DIM) return 0;
-  return make_act8_layout(dtype, M, d_in, *member).total;
+  return make_act8_layout(dtype, M, d_in, *member, grad_dtype == LORA_BF16).total;
 }
 
 int lora_act8_linear_bwd(int dtype, int64_t M, int64_t d_in, const lora_group_member* member, const uint8_t* codes,
-                         const float* scale8, const float* table16, void* ws, size_t ws_bytes, void* stream) {
+                         const float* scale8, const float* table16, int grad_dtype, void* ws, size_t ws_bytes,
+                         void* stream) {
   const lora_epilogue none{LORA_ACT_NONE, nullptr, nullptr, nullptr};
   TRY(check_epi(true, dtype, M, d_in, member, &none, codes, table16));
+  if (grad_dtype != LORA_F32 && grad_dtype != LORA_BF16) return LORA_ERR_DTYPE;
   if (d_in > LORA_NORM_MAX_DIM) return LORA_ERR_SHAPE;
   if (M > 0) TRY(check_elems({{scale8, 4}}, true));
   const lora_group_member& m = *member;
-  const Act8Layout E = make_act8_layout(dtype, M, d_in, m);
+  const bool low = grad_dtype == LORA_BF16;
+  const Act8Layout E = make_act8_layout(dtype, M, d_in, m, low);
   TRY(check_ws_bytes(E.total, ws, ws_bytes));
   TRY(check_device());
   hipStream_t st = static_cast<hipStream_t>(stream);
-  void* X = static_cast<char*>(ws) + E.x;
+  char* w = static_cast<char*>(ws);
+  void* X = w + E.x;
   Act8Args x8;
   memset(&x8, 0, sizeof(x8));
   if (E.direct) {
@@ -2782,10 +2798,20 @@ int lora_act8_linear_bwd(int dtype, int64_t M, int64_t d_in, const lora_group_me
     HIPTRY(timed(K_ACT8, double(M) * d_in, double(M) * d_in * (elem_bytes(dtype) + 1), st,
                  [&] { return launch_act8_unpack(elem_bytes(dtype), codes, scale8, M, d_in, X, st); }));
   }
+  // (the other backwards write their gradients in fp32)
+  const bool wide = low && !E.direct;
+  float* dA = wide ? reinterpret_cast<float*>(w + E.ga) : m.dA;
+  float* dB = wide ? reinterpret_cast<float*>(w + E.gb) : m.dB;
   const Nf4W q{m.W_nf4, m.absmax, table16};
-  return backward_impl(dtype, M, d_in, m.d_out, m.r, m.scale, X, m.W, m.W_nf4 ? &q : nullptr, m.A, m.B, nullptr, m.dY,
-                       m.dX, m.dA, m.dB, ws, E.E.L, st, nullptr, nullptr, nullptr,
-                       E.E.L.dx_nt && !m.W_nf4 ? m.W_t : nullptr, E.direct ? &x8 : nullptr);
+  TRY(backward_impl(dtype, M, d_in, m.d_out, m.r, m.scale, X, m.W, m.W_nf4 ? &q : nullptr, m.A, m.B, nullptr, m.dY, m.dX,
+                    dA, dB, ws, E.E.L, st, nullptr, nullptr, nullptr, E.E.L.dx_nt && !m.W_nf4 ? m.W_t : nullptr,
+                    E.direct ? &x8 : nullptr, low && E.direct));
+  if (wide)
+    HIPTRY(timed(K_ACT8, 0, 6.0 * m.r * (d_in + m.d_out), st, [&] {
+      return launch_to_bf16(dA, m.r * d_in, reinterpret_cast<uint16_t*>(m.dA), dB, m.r * m.d_out,
+                            reinterpret_cast<uint16_t*>(m.dB), st);
+    }));
+  return LORA_OK;
 }
 
 // ---- an adapter of its own for every row ----

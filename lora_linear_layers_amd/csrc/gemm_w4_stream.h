@@ -48,7 +48,7 @@ gemm_w4_stream_kernel(const GemmArgs p) {
   using w4nt::SLOT;
   using w4nt::vmcnt_imm;
   constexpr int BKS = w4nt::BK;
-  static_assert(EPI == EPI_ACT, "the epilogue of epi.h");
+  static_assert(EPI == EPI_ACT || (MULTI && EPI == EPI_STORE), "the epilogue of epi.h, or (whole tiles, none in two parts) the store");
   __shared__ __attribute__((aligned(1024))) char smem[w4nt::LDS];
   // keep the MFMA accumulators in the accumulation registers
   asm volatile("" ::: "a0");
@@ -271,6 +271,10 @@ gemm_w4_stream_kernel(const GemmArgs p) {
   if (t + 1 < n) stage(t++, N0{}, T_{});
   stage(t, N0{}, F_{});
 
+  if constexpr (EPI == EPI_STORE) {
+    w4_epilogue<EPI_STORE>(p, acc, smem, m0, n0, p.c, p.ldc);
+    return;
+  }
   const float* other = nullptr;
   if (part) {
     int* cnt = p.st_cnt + (hb >> 1);
@@ -300,7 +304,7 @@ gemm_w4_stream_kernel(const GemmArgs p) {
     asm volatile("" ::: "memory");
     other = p.st_part + (int64_t)(hb ^ 1) * (BM * BN);
   }
-  w4_epilogue<EPI, true>(p, acc, smem, m0, n0, p.c, p.ldc, other);
+  if constexpr (EPI == EPI_ACT) w4_epilogue<EPI, true>(p, acc, smem, m0, n0, p.c, p.ldc, other);
 }
 
 }  // namespace lora

@@ -607,8 +607,10 @@ __device__ __forceinline__ float4 sum_splits(const float* __restrict__ src, int 
 // row t >> 4, with the float4 loads of up to 8 splits in flight before their
 // sums.  The transposed store goes through an LDS tile so that consecutive
 // threads write consecutive q.
+// (Out uint16_t: bf16.)
+template <typename Out>
 __device__ __forceinline__ void reduce_tile(const float* __restrict__ part, int splits, int64_t rows, int64_t N,
-                                            int64_t part_stride, int transpose, float* __restrict__ out,
+                                            int64_t part_stride, int transpose, Out* __restrict__ out,
                                             int64_t c0, int64_t q0, float (*tile)[65]) {
   const int tid = threadIdx.x;
   const int cl = 4 * (tid & 15), rl = tid >> 4;
@@ -617,13 +619,19 @@ __device__ __forceinline__ void reduce_tile(const float* __restrict__ part, int 
   // past the end: a valid element is read and nothing is stored
   const float* src = part + (ok ? q * N + c : 0);
   const float4 acc = sum_splits(src, splits, part_stride);
+  auto to = [](float v) {
+    if constexpr (sizeof(Out) == 2)
+      return f2bf(v);
+    else
+      return v;
+  };
   if (!transpose) {
     if (ok) {
-      float* d = out + q * N + c;
-      d[0] = acc.x;
-      d[1] = acc.y;
-      d[2] = acc.z;
-      d[3] = acc.w;
+      Out* d = out + q * N + c;
+      d[0] = to(acc.x);
+      d[1] = to(acc.y);
+      d[2] = to(acc.z);
+      d[3] = to(acc.w);
     }
     return;
   }
@@ -638,7 +646,7 @@ __device__ __forceinline__ void reduce_tile(const float* __restrict__ part, int 
     const int idx = k * 256 + tid;
     const int cc = idx >> 4, qq = idx & 15;
     const int64_t qg = q0 + qq, cg = c0 + cc;
-    if (qg < rows && cg < N) out[cg * rows + qg] = tile[qq][cc];
+    if (qg < rows && cg < N) out[cg * rows + qg] = to(tile[qq][cc]);
   }
 }
 
@@ -651,6 +659,7 @@ __global__ void __launch_bounds__(256) reduce_splits_kernel(const float* __restr
 }
 
 // the jobs' tiles, job by job (the job of a block: a scalar search)
+template <typename Out>
 __global__ void __launch_bounds__(256) reduce_batch_kernel(const ReduceBatch b) {
   __shared__ float tile[16][65];
   const int blk = blockIdx.x;
@@ -658,7 +667,7 @@ __global__ void __launch_bounds__(256) reduce_batch_kernel(const ReduceBatch b) 
   for (int i = 1; i < b.n; ++i) g = blk >= b.j[i].block0 ? i : g;
   const ReduceJob& J = b.j[g];
   const int lb = blk - J.block0;
-  reduce_tile(J.part, J.splits, J.rows, J.N, J.part_stride, J.transpose, J.out, (int64_t)(lb % J.tiles_n) * 64,
+  reduce_tile(J.part, J.splits, J.rows, J.N, J.part_stride, J.transpose, reinterpret_cast<Out*>(J.out), (int64_t)(lb % J.tiles_n) * 64,
               (int64_t)(lb / J.tiles_n) * 16, tile);
 }
 
@@ -678,7 +687,10 @@ hipError_t ReduceBatch::add(const float* part, int splits, int64_t rows, int64_t
 
 hipError_t launch_reduce_batch(const ReduceBatch& b, hipStream_t st) {
   if (b.n == 0 || b.blocks == 0) return hipSuccess;
-  hipLaunchKernelGGL(reduce_batch_kernel, dim3((unsigned)b.blocks), dim3(256), 0, st, b);
+  if (b.low)
+    hipLaunchKernelGGL(reduce_batch_kernel<uint16_t>, dim3((unsigned)b.blocks), dim3(256), 0, st, b);
+  else
+    hipLaunchKernelGGL(reduce_batch_kernel<float>, dim3((unsigned)b.blocks), dim3(256), 0, st, b);
   return hipGetLastError();
 }
 

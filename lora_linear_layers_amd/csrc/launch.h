@@ -125,6 +125,7 @@ struct ReduceJob {
 };
 struct ReduceBatch {
   int n = 0, blocks = 0;
+  bool low = false;  // the outputs are bf16 arrays
   ReduceJob j[kBatchJobsMax];
   hipError_t add(const float* part, int splits, int64_t rows, int64_t N, int64_t part_stride, bool transpose,
                  float* out);
@@ -352,6 +353,8 @@ hipError_t launch_rmsnorm_grad(int elem_bytes, const RmsNormGradArgs& a, void* d
 // Rows kept in 8 bits (norm.hip): e4m3 codes [M, d] and a power of two a row.
 hipError_t launch_act8_pack(int elem_bytes, const void* X, int64_t ldx, int64_t M, int d, uint8_t* codes, float* scale8,
                             hipStream_t st);
+// out = in in bf16, two arrays (either may be empty).
+hipError_t launch_to_bf16(const float* a, int64_t na, uint16_t* oa, const float* b, int64_t nb, uint16_t* ob, hipStream_t st);
 hipError_t launch_act8_unpack(int elem_bytes, const uint8_t* codes, const float* scale8, int64_t M, int64_t d, void* X,
                               hipStream_t st);
 
@@ -382,10 +385,10 @@ struct MultiLists {
   int* zero;  // nzero ints cleared
   int nzero;
   // whether an adapter of a row holds infinities or NaNs in `scan` (bf16,
-  // scan16 16-byte pieces an adapter): bad [n][chunks], a chunk 4096 pieces
+  // scan16 16-byte pieces an adapter): bad [n][chunks], a chunk `pieces` pieces
   const void* scan;
   int64_t scan16;
-  int chunks;
+  int chunks, pieces;
   int* bad;
   MultiTranspose tr[2];
   int64_t tr0;  // (set by the launch)

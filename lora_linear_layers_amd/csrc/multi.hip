@@ -44,8 +44,6 @@ __device__ __forceinline__ float val(T x) {
     return x;
 }
 
-constexpr int kScanPieces = 4096;  // 16-byte pieces of a block that looks for infinities
-
 __device__ __forceinline__ int adapter_at(const int* index, int64_t t, int64_t M, int n) {
   const int a = t < M ? index[t] : -1;
   return a >= 0 && a < n ? a : -1;
@@ -56,7 +54,7 @@ __device__ __forceinline__ int adapter_at(const int* index, int64_t t, int64_t M
 // their first rows; then T256 blocks, of a 256-row tile; then the row groups of
 // the gradients: the 64-token tiles in which an adapter of the group occurs.
 // The first block also clears the stream kernel's counters.  Then `chunks` blocks
-// an adapter, which look for infinities and NaNs in their 64 KB of its second
+// an adapter, which look for infinities and NaNs in their part of its second
 // operand if a row carries it: one adapter's must not reach the others' rows.
 // ---------------------------------------------------------------------------
 // The distinct values >= 0 of a wave's 64, in the order of their first lanes:
@@ -158,11 +156,11 @@ __global__ void __launch_bounds__(256) multi_lists_kernel(const MultiLists q) {
       if (tid == 0) q.bad[b] = 0;
       return;
     }
-    const int64_t end = min((int64_t)(c + 1) * kScanPieces, q.scan16);
+    const int64_t end = min((int64_t)(c + 1) * q.pieces, q.scan16);
     const u32x4* v = reinterpret_cast<const u32x4*>(q.scan) + (int64_t)a * q.scan16;
     uint32_t found = 0;
 #pragma unroll 8
-    for (int64_t i = (int64_t)c * kScanPieces + tid; i < end; i += 256) {
+    for (int64_t i = (int64_t)c * q.pieces + tid; i < end; i += 256) {
       const u32x4 x = v[i];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -203,17 +201,21 @@ __global__ void __launch_bounds__(256) multi_lists_kernel(const MultiLists q) {
 // ---------------------------------------------------------------------------
 // strips
 // ---------------------------------------------------------------------------
-// bf16: partials of the tile's strips (gemm_panel.h), column groups of 64 past
-// the tile's own leave at once.  Two of them in one launch (the backward's P
-// and Q): splits [0, s0) of the grid are the first one's.
+// bf16: partials of the tile's strips (gemm_panel.h), 64 columns of its adapters
+// after the other, dealt to gridDim.z blocks.  (A block for every 64 columns that a
+// tile could have, most of which leave at once, cost 5 of 16 us with 32 adapters:
+// each takes a CU's LDS for its launch.)  Two panels in one launch (the backward's
+// P and Q): splits [0, s0) of the grid are the first one's.
 __global__ void __launch_bounds__(pdma::NT) __attribute__((amdgpu_waves_per_eu(1, 1)))
 multi_panel_kernel(const GemmPair q) {
-  const int y = (int)blockIdx.z, w = y >= q.s0 ? 1 : 0;
+  const int y = (int)blockIdx.y, w = y >= q.s0 ? 1 : 0;
   __shared__ __attribute__((aligned(1024))) char smem[pdma::Cfg<PANEL_BM, 64>::LDS];
   const GemmArgs& p = q.g[w];
-  const int mt = blockIdx.x, cg = blockIdx.y;
-  if (64 * cg >= scalar_at(p.ad_cnt, mt) * p.ad_r) return;
-  panel_dma_tile<PANEL_BM, 64, true>(smem, p, mt, w ? y - q.s0 : y, cg);
+  const int mt = blockIdx.x, cols = scalar_at(p.ad_cnt, mt) * p.ad_r;
+  for (int cg = blockIdx.z; 64 * cg < cols; cg += gridDim.z) {
+    panel_dma_tile<PANEL_BM, 64, true>(smem, p, mt, w ? y - q.s0 : y, cg);
+    __syncthreads();  // (the ring is free again)
+  }
 }
 
 // The strips of a 64-token tile from their partials, bf16(s_a sum), of one or
@@ -588,11 +590,12 @@ static bool panel_ok(const GemmArgs& a) {
 hipError_t launch_multi_panel(const GemmArgs& a, int sa, const GemmArgs* b, int sb, hipStream_t st) {
   if (a.m_store <= 0) return hipSuccess;
   const int64_t tiles = (a.m_store + PANEL_BM - 1) / PANEL_BM, cols = ((int64_t)a.ad_cap * a.ad_r + 63) / 64;
-  if (!panel_ok(a) || sa < 1 || tiles > INT32_MAX || cols > 65535 ||
+  if (!panel_ok(a) || sa < 1 || tiles > INT32_MAX || sa + sb > 65535 ||
       (b && (!panel_ok(*b) || sb < 1 || b->m_store != a.m_store || b->ad_cap != a.ad_cap || b->ad_r != a.ad_r)))
     return hipErrorInvalidValue;
   const GemmPair q{{a, b ? *b : a}, sa};
-  hipLaunchKernelGGL(multi_panel_kernel, dim3((unsigned)tiles, (unsigned)cols, (unsigned)(sa + (b ? sb : 0))), dim3(pdma::NT),
+  const int64_t y = sa + (b ? sb : 0), z = std::max<int64_t>(1, std::min<int64_t>(cols, 384 / (tiles * y)));
+  hipLaunchKernelGGL(multi_panel_kernel, dim3((unsigned)tiles, (unsigned)y, (unsigned)z), dim3(pdma::NT),
                      0, st, q);
   return hipGetLastError();
 }
@@ -622,7 +625,12 @@ hipError_t launch_multi_gemm(GemmArgs a, bool low, hipStream_t st) {
       a.st_full + 2 * (int64_t)a.st_half > INT32_MAX ||
       (a.st_half > 0 && (!a.st_part || !a.st_cnt || a.st_early < 0 || a.K1 / w4::BK / 2 - a.st_early < 2)))
     return hipErrorInvalidValue;
-  hipLaunchKernelGGL((gemm_w4_stream_kernel<EPI_ACT, true>), dim3((unsigned)(a.st_full + 2 * a.st_half)), dim3(w4::NT), 0, st, a);
+  // whole tiles store from the accumulators, without the passes through LDS that
+  // ragged ones need (8192 x 4096 over 4096: 205 against 219 us)
+  if (a.st_half == 0 && a.m_store % w4::BM == 0 && a.n_store % w4::BN == 0)
+    hipLaunchKernelGGL((gemm_w4_stream_kernel<EPI_STORE, true>), dim3((unsigned)a.st_full), dim3(w4::NT), 0, st, a);
+  else
+    hipLaunchKernelGGL((gemm_w4_stream_kernel<EPI_ACT, true>), dim3((unsigned)(a.st_full + 2 * a.st_half)), dim3(w4::NT), 0, st, a);
   return hipGetLastError();
 }
 

@@ -361,6 +361,14 @@ __global__ void __launch_bounds__(256) act8_unpack_kernel(const uint8_t* __restr
   }
 }
 
+__global__ void __launch_bounds__(256) to_bf16_kernel(const float* a, int64_t na, uint16_t* oa, const float* b, int64_t nb, uint16_t* ob) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < na + nb; i += (int64_t)gridDim.x * 256)
+    if (i < na)
+      oa[i] = f2bf(a[i]);
+    else
+      ob[i - na] = f2bf(b[i - na]);
+}
+
 // ---------------------------------------------------------------------------
 // backward: with xh = h rstd and g = dY w,
 //     dX = rstd (g - xh mean(g xh)) + dH,   dw = sum over rows of dY xh
@@ -555,6 +563,12 @@ hipError_t launch_act8_unpack(int elem_bytes, const uint8_t* codes, const float*
     hipLaunchKernelGGL((act8_unpack_kernel<uint16_t>), dim3(blocks), dim3(256), 0, st, codes, scale8, M, d, static_cast<uint16_t*>(X));
   else
     hipLaunchKernelGGL((act8_unpack_kernel<float>), dim3(blocks), dim3(256), 0, st, codes, scale8, M, d, static_cast<float*>(X));
+  return hipGetLastError();
+}
+
+hipError_t launch_to_bf16(const float* a, int64_t na, uint16_t* oa, const float* b, int64_t nb, uint16_t* ob, hipStream_t st) {
+  const unsigned blocks = (unsigned)std::max<int64_t>(1, std::min<int64_t>((na + nb + 255) / 256, 2048));
+  hipLaunchKernelGGL(to_bf16_kernel, dim3(blocks), dim3(256), 0, st, a, na, oa, b, nb, ob);
   return hipGetLastError();
 }
 

@@ -1040,9 +1040,10 @@ def lora_act8_unpack(codes, scale8, dtype=torch.bfloat16):
     return X
 
 
-def lora_act8_linear_bwd(codes, scale8, member, dY, need_dX: bool = True, table16=None, ws=None):
-    """(dX or None, dA fp32, dB fp32) of a projection whose input was kept as codes and scale8 (lora_act8_pack, or
-    lora_rmsnorm_fwd with pack), for a member as lora_linear_epi_bwd takes it."""
+def lora_act8_linear_bwd(codes, scale8, member, dY, need_dX: bool = True, table16=None, grad_dtype=torch.float32,
+                         ws=None):
+    """(dX or None, dA, dB) of a projection whose input was kept as codes and scale8 (lora_act8_pack, or
+    lora_rmsnorm_fwd with pack), for a member as lora_linear_epi_bwd takes it; dA and dB in grad_dtype."""
     dev, (M, d_in) = _packed(codes, scale8)
     A, B = member["A"], member["B"]
     if A.dim() != 2 or B.dim() != 2 or dY.dim() != 2:
@@ -1051,21 +1052,25 @@ def lora_act8_linear_bwd(codes, scale8, member, dY, need_dX: bool = True, table1
     _, _, _, d_out, r, m = _epi_member(dY.new_empty(0, d_in), member)
     if A.shape != (r, d_in) or B.shape != (d_out, r) or dY.shape != (M, d_out):
         raise ValueError("shape mismatch: codes [M,d_in], W [d_out,d_in], A [r,d_in], B [d_out,r], dY [M,d_out]")
-    dt = L._dtype_code(dY)
     _check(dev, "dY", dY, (dY.dtype,), M * d_out)
-    dX = torch.empty(M, d_in, dtype=dY.dtype, device=dev) if need_dX else None
-    dA = torch.empty(r, d_in, dtype=torch.float32, device=dev)
-    dB = torch.empty(d_out, r, dtype=torch.float32, device=dev)
+    return _act8_bwd(codes, scale8, m, dY, M, d_in, d_out, r, need_dX, table16, grad_dtype, ws)
+
+
+def _act8_bwd(codes, scale8, m, dY, M, d_in, d_out, r, need_dX, table16, grad_dtype, ws=None):
+    """lora_act8_linear_bwd of checked tensors."""
+    dev, dt, new = dY.device, L._dtype_code(dY), torch.empty
+    dX = new(M, d_in, dtype=dY.dtype, device=dev) if need_dX else None
+    dA, dB = new(r, d_in, dtype=grad_dtype, device=dev), new(d_out, r, dtype=grad_dtype, device=dev)
     m.dY, m.dX, m.dA, m.dB = L._ptr(dY), L._ptr(dX), L._ptr(dA), L._ptr(dB)
-    tab = L._table_ptr(table16) if table16 is not None else None
+    tab, gt = L._table_ptr(table16) if table16 is not None else None, L._dtype_code(dA)
     if ws is None:
-        ws_bytes = int(L.lib().lora_act8_linear_workspace_bytes(dt, M, d_in, m))
-        ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+        ws_bytes = L.lib().lora_act8_linear_workspace_bytes(dt, M, d_in, m, gt)
+        ws = new(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
     else:
         ws_bytes = _check_ws(dev, ws, ws.nbytes).nbytes
     with _on(dev):
         L._check("lora_act8_linear_bwd", L.lib().lora_act8_linear_bwd(
-            dt, M, d_in, m, L._ptr(codes), L._ptr(scale8), tab, L._ptr(ws), ws_bytes, L._stream(dev)))
+            dt, M, d_in, m, L._ptr(codes), L._ptr(scale8), tab, gt, L._ptr(ws), ws_bytes, L._stream(dev)))
     return dX, dA, dB
 
 
@@ -1077,13 +1082,14 @@ class LoraLinearAct8Function(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, X, W, A, B, scale, codes=None, scale8=None, W_t=None):
-        Y, _ = lora_linear_epi_fwd(X, {"W": W, "A": A, "B": B, "scale": scale})
+        Y, _ = lora_linear_epi_fwd(X, {"W": W, "A": A, "B": B, "scale": scale, "W_t": W_t})
         if any(ctx.needs_input_grad[i] for i in (0, 2, 3)):
             if codes is None:
                 codes, scale8 = lora_act8_pack(X)
-            elif codes.shape != X.shape:
-                raise ValueError("codes must have X's shape")
-            _packed(codes, scale8)
+            else:
+                if codes.shape != X.shape:
+                    raise ValueError("codes must have X's shape")
+                _packed(codes, scale8)
             ctx.save_for_backward(codes, scale8, W, A, B, W_t)
         ctx.scale = scale
         return Y
@@ -1092,10 +1098,13 @@ class LoraLinearAct8Function(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dY):
         codes, scale8, W, A, B, W_t = ctx.saved_tensors
-        member = {"W": W, "A": A, "B": B, "scale": ctx.scale, "W_t": W_t}
+        dY = dY.contiguous()
+        (M, d_in), (d_out, r) = codes.shape, B.shape
+        _check(codes.device, "the gradient of Y", dY, (A.dtype,), M * d_out)
+        m = _epi_struct({"W": W, "A": A, "B": B, "scale": ctx.scale, "W_t": W_t}, r, d_out)
         need_dX, _, need_dA, need_dB = ctx.needs_input_grad[:4]
-        dX, dA, dB = lora_act8_linear_bwd(codes, scale8, member, dY.contiguous(), need_dX)
-        return (dX, None, dA.to(A.dtype) if need_dA else None, dB.to(B.dtype) if need_dB else None) + (None,) * 4
+        dX, dA, dB = _act8_bwd(codes, scale8, m, dY, M, d_in, d_out, r, need_dX, None, A.dtype)
+        return dX, None, dA if need_dA else None, dB if need_dB else None, None, None, None, None
 
 
 # ---------------------------------------------------------------------------

@@ -67,9 +67,10 @@ def test_act8_validation():
     assert lib.lora_act8_unpack(1, 4, 0, P, P, P, None) == ESHAPE
     member = _lib.GroupMember(32, 8, 1.0, 0, P, None, None, P, P, None, P, P, P, P, None)
 
-    def call(m=member, dtype=1, M=4, d_in=64, codes=P, s8=P, ws=P, n=1 << 30):
-        return lib.lora_act8_linear_bwd(dtype, M, d_in, m, codes, s8, None, ws, n, None)
+    def call(m=member, dtype=1, M=4, d_in=64, codes=P, s8=P, gt=0, ws=P, n=1 << 30):
+        return lib.lora_act8_linear_bwd(dtype, M, d_in, m, codes, s8, None, gt, ws, n, None)
     assert call(dtype=2) == EDTYPE
+    assert call(gt=3) == EDTYPE
     assert call(d_in=12) == ESHAPE
     assert call(d_in=32776) == ESHAPE
     assert call(m=None) == ENULL
@@ -78,9 +79,9 @@ def test_act8_validation():
     assert call(s8=None) == ENULL
     assert call(s8=P + 2) == EALIGN
     assert call(ws=None) == EWS
-    need = lib.lora_act8_linear_workspace_bytes(1, 4, 64, member)
+    need = lib.lora_act8_linear_workspace_bytes(1, 4, 64, member, 0)
     assert need > 0 and call(n=need - 1) == EWS
-    assert lib.lora_act8_linear_workspace_bytes(1, 4, 12, member) == 0
+    assert lib.lora_act8_linear_workspace_bytes(1, 4, 12, member, 0) == 0
     rope = _lib.GroupMember(128, 8, 1.0, 1, P, None, None, P, P, None, P, P, P, P, None)
     assert call(m=rope) == ESHAPE
     no_grad = _lib.GroupMember(32, 8, 1.0, 0, P, None, None, P, P, None, P, P, None, P, None)

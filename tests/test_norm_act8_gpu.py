@@ -329,6 +329,9 @@ def check_act8_bwd(lib, X, W, A, B, scale, dY, member=None, Wd=None, table=None,
     if dX is not None:
         _near(dX, want, t + H[dt] * (want.abs() + t) + 1e-37, "dX")
     _near(dA, Q.T @ K, eQ.T @ K.abs() + (M + 2) * U * (magQ.T @ K.abs()) + 1e-37, "dA")
+    if not kw:  # in 16 bits: the same rounded
+        low = lib.lora_act8_linear_bwd(codes, s8, member, dY, table16=table, grad_dtype=torch.bfloat16)
+        assert torch.equal(low[1], dA.bfloat16()) and torch.equal(low[2], dB.bfloat16())
     _near(dB, g.T @ P, g.abs().T @ eP + (M + 2) * U * (g.abs().T @ magP) + 1e-37, "dB")
     return dX, dA, dB
 
