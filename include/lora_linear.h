@@ -471,9 +471,9 @@ int lora_transpose(const void* src, int64_t rows, int64_t cols, void* dst, void*
  * at least): H [M, d] = h, Y [M, d] = y, rstd fp32 [M], and codes [M, d] with
  * scale8 [M]: y as lora_act8_pack keeps it, rounded once (from y before its
  * rounding to the dtype).  H may be X or the residual (the stream updated in
- * place), Y may be X without a residual; with row strides of d.  Sums are fp32:
- * a row whose sum of squares passes fp32's range gives zeros.  Pointers need their
- * element's alignment only.  1 <= d <= LORA_NORM_MAX_DIM, 0 <= M < 2^31, eps >= 0
+ * place), Y may be X without a residual; with row strides of d.  The sum of
+ * squares is kept in 64 bits, rstd in fp32 (root mean squares from 2^-126 to 2^126 have
+ * one).  Pointers need their element's alignment only.  1 <= d <= LORA_NORM_MAX_DIM, 0 <= M < 2^31, eps >= 0
  * (a row of zeros with eps 0 gives NaN).
  *
  * Backward, for dY [M, d] and, where the stream goes on, dH [M, d] (NULL: 0),
@@ -535,8 +535,9 @@ size_t lora_act8_linear_workspace_bytes(int dtype, int64_t M, int64_t d_in, cons
  * r a multiple of 8 up to LORA_MULTI_MAX_RANK, 1 <= n <= LORA_MULTI_MAX_ADAPTERS,
  * d_in and d_out as in lora_linear_fwd and at most LORA_EPI_MAX_D_OUT.
  * An infinity or NaN stays with its own: one in an adapter's A or B makes its
- * rows' outputs (dX) NaN where the definition may leave some finite, one in a
- * row of X or dY its adapter's gradients; other adapters and rows do not see it.
+ * rows' outputs (dX) and its gradients NaN where the definition may leave some
+ * finite, one in a row of X or dY its adapter's gradients; other adapters and rows do
+ * not see it.  Y and dX overlap no input.
  * index and scales need their element's alignment only.  Workspace from its own
  * sizing call (with backward != 0: have_w_t whether W_t is given, need_dx
  * whether dX is).
@@ -547,10 +548,12 @@ size_t lora_act8_linear_workspace_bytes(int dtype, int64_t M, int64_t d_in, cons
  * dX [M, d_in] or NULL; dA [n, r, d_in] and dB [n, d_out, r] of grad_dtype, zeros for
  * an adapter without rows, sums over rows in a fixed order.  W_t: W^T [d_in,
  * d_out] (bf16, lora_transpose) where the caller keeps one, else NULL (a bf16
- * call that needs it makes its own); fp32 calls do not read it.
+ * call that needs it makes its own); fp32 calls do not read it.  The backward takes
+ * LORA_MULTI_MAX_BWD_ROWS rows at most.
  */
 #define LORA_MULTI_MAX_RANK 128
 #define LORA_MULTI_MAX_ADAPTERS 4096
+#define LORA_MULTI_MAX_BWD_ROWS (1 << 21)
 size_t lora_multi_workspace_bytes(int backward, int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r,
                                   int have_w_t, int need_dx);
 int lora_multi_fwd(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r, const void* X, const void* W,

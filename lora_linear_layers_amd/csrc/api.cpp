@@ -2060,6 +2060,8 @@ int multi_bf16(const MultiCall& c, const MultiLayout& L, const MultiProduct& g, 
     HIPTRY(timed(K_MULTI_GEMM, flop, bytes, st, [&] { return launch_multi_gemm(a, g.plan.low, st); }));
     return LORA_OK;
   }
+  // (the strips' part is rounded to bf16 on its way: 2^-9 of that part, beside the
+  // output's own rounding; in fp32 it would be written and read at twice the bytes)
   HIPTRY(timed(K_MULTI_UPDATE, 2 * Md * N * c.r, 2 * Md * N, st, [&] {
     return launch_multi_update(2, P, false, B, c.index, c.M, N, (int)c.n, (int)c.r, out, st);
   }));
@@ -2224,11 +2226,11 @@ int multi_backward(const MultiCall& c, const MultiLayout& L, const void* X, cons
   return LORA_OK;
 }
 
-int check_multi(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r) {
+int check_multi(bool bwd, int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r) {
   if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_ERR_DTYPE;
   TRY(check_sizes(M, d_in, d_out, r));
   if (d_in > LORA_EPI_MAX_D_OUT || d_out > LORA_EPI_MAX_D_OUT || r % 8 || r > LORA_MULTI_MAX_RANK || n < 1 ||
-      n > LORA_MULTI_MAX_ADAPTERS)
+      n > LORA_MULTI_MAX_ADAPTERS || (bwd && M > LORA_MULTI_MAX_BWD_ROWS))
     return LORA_ERR_SHAPE;
   return LORA_OK;
 }
@@ -2817,14 +2819,14 @@ int lora_act8_linear_bwd(int dtype, int64_t M, int64_t d_in, const lora_group_me
 // ---- an adapter of its own for every row ----
 size_t lora_multi_workspace_bytes(int backward, int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r,
                                   int have_w_t, int need_dx) {
-  if (check_multi(dtype, M, d_in, d_out, n, r) != LORA_OK) return 0;
+  if (check_multi(backward != 0, dtype, M, d_in, d_out, n, r) != LORA_OK) return 0;
   return make_multi_layout(backward != 0, dtype, M, d_in, d_out, n, r, have_w_t != 0, need_dx != 0).total;
 }
 
 int lora_multi_fwd(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r, const void* X, const void* W,
                    const void* A, const void* B, const float* scales, const int32_t* index, void* Y, void* ws,
                    size_t ws_bytes, void* stream) {
-  TRY(check_multi(dtype, M, d_in, d_out, n, r));
+  TRY(check_multi(false, dtype, M, d_in, d_out, n, r));
   TRY(check_ptrs({W, A, B}));
   TRY(check_elems({{scales, 4}}, true));
   if (M > 0) {
@@ -2842,7 +2844,7 @@ int lora_multi_fwd(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n,
 int lora_multi_bwd(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r, const void* X, const void* W,
                    const void* W_t, const void* A, const void* B, const float* scales, const int32_t* index, const void* dY,
                    void* dX, void* dA, void* dB, int grad_dtype, void* ws, size_t ws_bytes, void* stream) {
-  TRY(check_multi(dtype, M, d_in, d_out, n, r));
+  TRY(check_multi(true, dtype, M, d_in, d_out, n, r));
   if (grad_dtype != LORA_F32 && grad_dtype != LORA_BF16) return LORA_ERR_DTYPE;
   TRY(check_ptrs({W, A, B, dA, dB}));
   TRY(check_elems({{scales, 4}}, true));

@@ -234,6 +234,18 @@ __device__ __forceinline__ void pack_row(const float (&y)[NV][8], int d, int t, 
   if (t == 0) *scale = pow2(ex);
 }
 
+// 1 / sqrt(s), s >= 0: of s 4^-k in [1, 4) in 32 bits, then one Newton step (squares
+// of bf16 numbers leave fp32's range at 2^64; 0 gives an infinity, an infinity 0).
+__device__ __forceinline__ double rsqrt64(double s) {
+  const int64_t b = __builtin_bit_cast(int64_t, s);
+  const int e = (int)(b >> 52) - 1023, k2 = e & ~1;
+  if (e <= -1023 || e == 1024) return 1.f / sqrtf((float)s);
+  const double m = __builtin_bit_cast(double, b - ((int64_t)k2 << 52));
+  const double r = 1.f / sqrtf((float)m);
+  const double r1 = r * (1.5 - 0.5 * m * r * r);
+  return __builtin_bit_cast(double, __builtin_bit_cast(int64_t, r1) - ((int64_t)(k2 / 2) << 52));
+}
+
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
@@ -275,9 +287,7 @@ __global__ void __launch_bounds__((Row<TPR, NV, VEC>::NT)) rmsnorm_kernel(const 
 #pragma unroll
     for (int e = 0; e < 8; ++e) s = __builtin_fma((double)h[k][e], (double)h[k][e], s);
   s = row_join64<TPR>(s, red64) * (1.0 / d) + (double)a.eps;
-  // 1 / sqrt(s): in 32 bits, then one Newton step (a sum past fp32's range gives 0, one of 0 an infinity)
-  const float r32 = 1.f / sqrtf((float)s);
-  const double r0 = r32, r64 = finite(r32) && r32 != 0.f ? r0 * (1.5 - 0.5 * s * r0 * r0) : r0;
+  const double r64 = rsqrt64(s);
   const float rstd = (float)r64;
   if (a.rstd && t == 0) a.rstd[row0] = rstd;
   const T* w = reinterpret_cast<const T*>(a.weight);

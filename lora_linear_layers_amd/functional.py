@@ -1087,8 +1087,8 @@ class LoraLinearAct8Function(torch.autograd.Function):
             if codes is None:
                 codes, scale8 = lora_act8_pack(X)
             else:
-                if codes.shape != X.shape:
-                    raise ValueError("codes must have X's shape")
+                if codes.shape != X.shape or codes.device != X.device:
+                    raise ValueError("codes must have X's shape and device")
                 _packed(codes, scale8)
             ctx.save_for_backward(codes, scale8, W, A, B, W_t)
         ctx.scale = scale

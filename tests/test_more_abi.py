@@ -117,3 +117,12 @@ def test_multi_validation():
     # what the caller keeps (W^T) and does not ask for (dX) takes no room
     big = [lib.lora_multi_workspace_bytes(1, 1, 4096, 4096, 4096, 8, 16, *a) for a in ((0, 1), (1, 1), (1, 0))]
     assert big[0] >= big[1] + 2 * 4096 * 4096 and big[1] > big[2]
+
+
+def test_multi_backward_rows():
+    lib = L.load()
+    assert lib.lora_multi_workspace_bytes(1, 1, 1 << 21, 64, 64, 2, 8, 0, 1) > 0
+    for dtype in (0, 1):
+        assert lib.lora_multi_workspace_bytes(1, dtype, (1 << 21) + 1, 64, 64, 2, 8, 0, 1) == 0
+        assert lib.lora_multi_workspace_bytes(0, dtype, (1 << 21) + 1, 64, 64, 2, 8, 0, 0) > 0
+        assert lib.lora_multi_bwd(dtype, (1 << 21) + 1, 64, 64, 2, 8, P, P, None, P, P, P, P, P, P, P, P, 0, P, 1 << 40, None) == ESHAPE

@@ -272,3 +272,91 @@ def test_refusals(lib):
         lib.lora_multi_bwd(X, W, A, B, scales, index, dY[:5])
     with pytest.raises(TypeError):
         lib.lora_multi_bwd(X, W, A, B, scales, index, dY, grad_dtype=torch.float16)
+
+
+def _norm64(h, w):
+    return h / torch.sqrt(h.square().mean(1, keepdim=True) + 1e-5) * w
+
+
+def _rel(got, want, tol, what):
+    assert float((got.double() - want).norm()) <= tol * float(want.norm()), what
+
+
+def test_served_block(lib):
+    """A decode step of requests with adapters of their own: residual norm, a projection up and one down, captured once
+    and replayed for new tokens, requests and adapters, two of them in turn; a prompt batch by the same calls."""
+    k, d, n, r = 512, 1024, 12, 16
+    _, W1, A1, B1, s1, _, _ = make(1, 1, k, d, n, r, torch.bfloat16)
+    _, W2, A2, B2, s2, _, _ = make(2, 1, d, k, n, r, torch.bfloat16)
+    w = (1 + 0.2 * _randn(torch.Generator().manual_seed(3), k)).bfloat16().cuda()
+
+    def block(X, R, index):
+        Y, Hh, _, _, _ = lib.lora_rmsnorm_fwd(X, w, residual=R)
+        U1 = lib.lora_multi_fwd(Y, W1, A1, B1, s1, index)
+        return Hh, lib.lora_multi_fwd(U1, W2, A2, B2, s2, index)
+
+    def inputs(seed, M):
+        g = torch.Generator().manual_seed(seed)
+        return [_randn(g, M, k).bfloat16().cuda() for _ in range(2)] + [_index(g, M, n, "random").cuda()]
+
+    def proj(y, W, A, B, s, index):
+        out = y @ W.double().T
+        for i in range(n):
+            rows = index == i
+            out[rows] += s.double()[i] * (y[rows] @ A[i].double().T) @ B[i].double().T
+        return out
+    graphs = []
+    for M in (5, 40):
+        ins = inputs(10 + M, M)
+        block(*ins)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = block(*ins)
+        graphs.append((M, ins, graph, outs))
+    for seed in range(3):
+        for M, ins, _, _ in graphs:
+            for t, v in zip(ins, inputs(20 + seed, M)):
+                t.copy_(v)
+        for _, _, graph, _ in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for M, ins, _, outs in graphs:
+            for a, b in zip(outs, block(*ins)):
+                assert torch.equal(a, b)
+    for M in (5, 40, 700):
+        X, R, index = inputs(30, M)
+        Hh, Z = block(X, R, index)
+        y = _norm64((X.float() + R.float()).bfloat16().double(), w.double())
+        want = proj(proj(y, W1, A1, B1, s1, index), W2, A2, B2, s2, index)
+        _rel(Z, want, 6 * 2.0 ** -8, M)  # the norm's output, both strips (and their parts) and both outputs rounded
+
+
+@pytest.mark.parametrize("M", [200, 1100])
+def test_trained_block(lib, M):
+    """Several adapters trained behind one norm, through the autograd functions, while another graph of the same leaves
+    lives."""
+    k, d, n, r = 512, 768, 5, 16
+    X, W, A, B, s, index, dY = make(7, M, k, d, n, r, torch.bfloat16)
+    g = torch.Generator().manual_seed(8)
+    R, w = _randn(g, M, k).bfloat16().cuda(), (1 + 0.2 * _randn(g, k)).bfloat16().cuda()
+    leaves = [t.requires_grad_() for t in (X, R, w, A, B)]
+
+    def forward():
+        Y, Hh = lib.LoraRmsNormFunction.apply(X, R, w, 1e-5, False)
+        return lib.LoraMultiFunction.apply(Y, W, A, B, s, index), Hh
+    dH = _randn(g, M, k).bfloat16().cuda()
+    one, two = forward(), forward()
+    first = torch.autograd.grad(one, leaves, (dY, dH))
+    for a, b in zip(first, torch.autograd.grad(two, leaves, (dY, dH))):
+        assert torch.equal(a, b)
+    h = (X.float() + R.float()).bfloat16().detach().double().requires_grad_()
+    wd, ad, bd = (t.detach().double().requires_grad_() for t in (w, A, B))
+    y = _norm64(h, wd)
+    z = y @ W.double().T
+    for i in range(n):
+        m = (index == i).double()[:, None]
+        z = z + m * s.double()[i] * (y @ ad[i].T) @ bd[i].T
+    gh, gw, ga, gb = torch.autograd.grad((z, h), (h, wd, ad, bd), (dY.double(), dH.double()), allow_unused=True)
+    for got, want, what in zip(first, (gh, gh, gw, ga, gb), ("X", "residual", "weight", "A", "B")):
+        _rel(got, want, 4 * 2.0 ** -8, what)  # the norm's output, a strip, dY W and the gradient rounded

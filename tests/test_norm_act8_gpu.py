@@ -534,3 +534,24 @@ def test_norm_codes_are_those_of_the_exact_values(lib, dtype):
         c, s = pack64(h / torch.sqrt(h.square().mean(1, keepdim=True)) * w.double())
         near = (h[:, 0] / torch.sqrt(h.square().mean(1)) * w.double()[0] / target - 1).abs() < 1e-15  # (64 bits' own border)
         assert torch.equal(s8.double()[~near], s[~near]) and torch.equal(codes.double()[~near], c[~near])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 1001, 4096])
+def test_norm_magnitudes(lib, dtype, d):
+    """Rows whose squares lie outside fp32's range."""
+    w = (1 + 0.3 * _randn(1, d)).to(dtype)
+    X = _randn(2, 5, d) * torch.tensor([1e30, 1e-30, 3e-20, 2e19, 1e37]).cuda()[:, None]
+    check_norm(lib, X.to(dtype), w, 0.0, None, True)
+
+
+def test_act8_function_takes_codes_of_its_input_only(lib):
+    X, W = _randn(1, 8, 64, dtype=torch.bfloat16).requires_grad_(), _randn(2, 32, 64, dtype=torch.bfloat16)
+    A, B = _randn(3, 8, 64, dtype=torch.bfloat16), _randn(4, 32, 8, dtype=torch.bfloat16)
+    codes, s8 = lib.lora_act8_pack(X.detach())
+    f = lib.LoraLinearAct8Function.apply
+    for bad in ((codes.cpu(), s8.cpu()), (codes[:7], s8[:7]), (codes, s8[:7]), (codes, s8.cpu())):
+        with pytest.raises(ValueError):
+            f(X, W, A, B, 0.5, *bad)
+    with pytest.raises(TypeError):
+        f(X, W, A, B, 0.5, codes, s8.double())
