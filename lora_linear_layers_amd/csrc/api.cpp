@@ -1817,8 +1817,16 @@ Act8Layout make_act8_layout(int dtype, int64_t M, int64_t d_in, const lora_group
 // other kernels (few tiles, short contractions).
 //
 // Up to 64 rows: the strips in fp32 by a launch of their own, then one launch of
-// the base product that adds them where it finishes its outputs: the W stream
-// (few) or the one-launch kernel (skinny).
+// the base product that adds them where it finishes its outputs.  By us a call, with 16
+// adapters in random order, skinny / few / dot:
+//   the one-launch kernel (skinny) for a W of up to 2^24 values, and up to 4 rows for any
+//   (1 row, 4096 -> 4096, r = 16: 15 / 16 / 23; 16: 19 / 22 / 26; 64, 2048 -> 4096:
+//   20 / 25 / 24; 1, 4096 -> 8192: 23 / 26 / 27), unless its blocks, of 16 columns over
+//   the whole contraction, are few and long (32, 4096 -> 1024: 23 / 24 / 22.5, 64: 28 / 30 / 23);
+//   the W stream (few) from 2^25 values and 5 rows on (8, 4096 -> 14336: 36 / 33 / 46; 48:
+//   46 / 42 / 54; 48, 14336 -> 4096: 72 / 46 / 49; 64, 4096 -> 8192, r = 64: 61 / 43 / 43),
+//   and from 2^24 and 17 rows at low ranks (32, 4096 -> 4096, r = 16: 26 / 23 / 28; r = 64:
+//   27 / 29 / 31: its strips come behind the stream).
 struct MultiProduct {
   bool gemm = false, few_ = false, skinny = false;
   bool dot = false;  // neither: a few rows' strips by fp32 dot products (one launch, no lists)
@@ -1831,8 +1839,9 @@ MultiProduct multi_product(int dtype, int64_t M, int64_t N, int64_t K, int64_t n
   MultiProduct P;
   if (dtype == LORA_BF16 && M > 0 && M <= 64 && !bwd) {
     P.few = few_plan(false, false, false, M, K, N, 8, true);
-    P.few_ = P.few.ok && (M > 16 || N * K >= (int64_t(1) << 25));
-    P.skinny = !P.few_ && skinny_fits(M, K, N, 8, sk::STRIP);
+    const bool fits = skinny_fits(M, K, N, 8, sk::STRIP), large = N * K >= (int64_t(1) << 25);
+    P.few_ = P.few.ok && (large ? M > 4 || !fits : N * K >= (int64_t(1) << 24) && M > 16 && r <= 32);
+    P.skinny = !P.few_ && fits && (M <= 16 || K <= 2048 || N >= 4096);
     if (P.few_ || P.skinny) return P;
   }
   if (dtype == LORA_BF16 && M > 0 && K >= 64 && n * N * r * 2 < 0xE0000000ll) {
@@ -1852,16 +1861,24 @@ MultiProduct multi_product(int dtype, int64_t M, int64_t N, int64_t K, int64_t n
     m.d_out = N;
     m.r = 8;
     P.base = make_epi_layout(false, dtype, M, K, m, lora_epilogue{LORA_ACT_NONE, nullptr, nullptr, nullptr});
-    // X is read r times from the caches: up to 64 MB of that one launch of 4 to 8 us
-    // takes the place of three (lists, panel, strips) of 4 each
-    P.dot = !bwd && (dtype == LORA_F32 || M * r * K <= int64_t(1) << 25);
+    // X is read r times from the caches: one launch takes the place of three (lists,
+    // panel, strips) of 4 us at least (600 rows, 1024 -> 1024, r = 64: 39 us of kernels
+    // against 51; 400, 4096 -> 4096, r = 64: 79 against 90; 600, 4096 -> 1024, r = 64,
+    // 300 MB: 67 against 69)
+    P.dot = !bwd && (dtype == LORA_F32 || M * r * K <= int64_t(1) << 27);
   }
   return P;
 }
 
 // Backward with the simple kernels: fp32, and bf16 up to 256 rows, where the seven
-// launches of the lists, strips and tiles cost more than their work.
-bool multi_simple(int dtype, int64_t M) { return dtype == LORA_F32 || M <= 256; }
+// launches of the lists, strips and tiles cost more than their work (256 rows,
+// 8 adapters of 16: 1024 -> 1024 37 us of kernels against 54, 4096 -> 4096 79 against 82;
+// 384 rows of the latter 112 against 100).  Where W is larger its product through W
+// itself costs more than that, unless the adapters are many (128 rows, 4096 -> 14336: 8 of
+// 16 140 against 128, 64 of 16 236 against 251).
+bool multi_simple(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r) {
+  return dtype == LORA_F32 || (M <= 256 && (d_in * d_out <= int64_t(1) << 25 || n * r >= 512));
+}
 
 struct MultiLayout {
   bool simple = false;    // backward
@@ -1900,7 +1917,7 @@ MultiLayout make_multi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, int6
   L.groups = (int)cdiv(n, L.per);
   const bool f32 = dtype == LORA_F32;
   if (!bwd) L.y = multi_product(dtype, M, d_out, d_in, n, r);
-  if (bwd && need_dx && !multi_simple(dtype, M)) L.dx = multi_product(dtype, M, d_in, d_out, n, r, true);
+  if (bwd && need_dx && !multi_simple(dtype, M, d_in, d_out, n, r)) L.dx = multi_product(dtype, M, d_in, d_out, n, r, true);
   const MultiProduct& g = bwd ? L.dx : L.y;
   if (!bwd && (g.few_ || g.skinny)) {
     L.p = take(size_t(M) * r * 4);
@@ -1908,7 +1925,7 @@ MultiLayout make_multi_layout(bool bwd, int dtype, int64_t M, int64_t d_in, int6
     L.total = off;
     return L;
   }
-  if (bwd && multi_simple(dtype, M)) {
+  if (bwd && multi_simple(dtype, M, d_in, d_out, n, r)) {
     L.simple = true;
     L.p = take(size_t(M) * r * 4);
     L.pt = take(size_t(M) * r * 4);  // Q

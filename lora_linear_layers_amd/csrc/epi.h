@@ -43,55 +43,6 @@ struct StripArgs {
   const uint16_t* B;
   int n, r;
 };
-// E consecutive columns from c[i] of NI rows t[i] (t[i] < 0: none): the loads of
-// all of them in flight together, 8 ranks at a time.  load() issues the first 8,
-// add() waits for them.
-template <int NI, int E>
-struct StripAdd {
-  typedef uint32_t v4 __attribute__((ext_vector_type(4)));
-  typedef float f4 __attribute__((ext_vector_type(4)));
-  const uint16_t* b[NI];
-  const float* p[NI];
-  bool on[NI];
-  v4 w[NI][E];
-  f4 x[NI][2];
-  __device__ __forceinline__ void fetch(int r, int q) {
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) w[i][e] = on[i] ? *reinterpret_cast<const v4*>(b[i] + e * r + q) : v4{0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) x[i][h] = on[i] ? *reinterpret_cast<const f4*>(p[i] + q + 4 * h) : f4{0.f, 0.f, 0.f, 0.f};
-    }
-  }
-  __device__ __forceinline__ void load(const StripArgs& s, int64_t N, const int (&t)[NI], const int64_t (&c)[NI]) {
-    int a[NI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) a[i] = t[i] >= 0 ? s.index[t[i]] : -1;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      on[i] = a[i] >= 0 && a[i] < s.n;
-      b[i] = s.B + (on[i] ? (a[i] * N + c[i]) * s.r : 0);
-      p[i] = s.P + (on[i] ? (int64_t)t[i] * s.r : 0);
-    }
-    fetch(s.r, 0);
-  }
-  __device__ __forceinline__ void add(const StripArgs& s, float (&y)[NI][E]) {
-    for (int q = 0; q < s.r; q += 8) {
-      if (q) fetch(s.r, q);
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float lo = __builtin_bit_cast(float, w[i][e][k] << 16), hi = __builtin_bit_cast(float, w[i][e][k] & 0xFFFF0000u);
-            y[i][e] = __builtin_fmaf(x[i][k >> 1][2 * (k & 1)], lo, y[i][e]);
-            y[i][e] = __builtin_fmaf(x[i][k >> 1][2 * (k & 1) + 1], hi, y[i][e]);
-          }
-    }
-  }
-};
 
 // P(N(0, 1) > a) for a >= 0: e^(-a^2/2) t q(t), t = 1 / (1 + 0.32 a), q fitted
 // to the scaled complementary error function (relative error below 1.7e-5,

@@ -53,6 +53,7 @@
 
 #include "few_args.h"
 #include "gemm.h"
+#include "strip.h"
 
 namespace lora {
 
@@ -1128,6 +1129,48 @@ few_fwd_bf16_kernel(const FewArgs p) {
       }
     // (the slot's first DMA, at stage 0, follows the loop's first barrier)
   }
+  // MULTI: the strips of tile a0's rows, dealt in 16-row blocks to the blocks whose
+  // range starts in the tile (one at least: ranges are no longer than a tile), so that
+  // all CUs read the adapters' second operands.  (By the one block that finishes a tile,
+  // with a tile for every second CU, they took 20 us of 51: 48 rows, 4096 -> 14336,
+  // r = 16.)  Half of the blocks of an XCD add theirs ahead of their stages, half
+  // behind: while one half waits for strips the other has the memory's rate to
+  // itself (48 rows, 4096 -> 14336: 47 us a call with all of them behind, 45.5 so).
+  const int b = blockIdx.x;
+  const bool early = MULTI && (b >> 3 & 1);
+  auto strips = [&](auto&& into) {
+    auto first = [&](int a) { return (int)(((int64_t)a * p.nblk + p.n_tiles - 1) / p.n_tiles); };
+    const int j0 = b - first(sp.a0), cnt = first(sp.a0 + 1) - first(sp.a0);
+    int mine[MB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m) mine[m] = strip_row(p.ad, p.M, 16 * m);
+    int64_t c[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) c[j] = sp.a0 * BNF + 32 * wave + 16 * j + l16;
+    for (int mb = j0; 16 * mb < p.M; mb += cnt) {
+      float y[NJ][4];
+      int a = mine[0];
+#pragma unroll
+      for (int m = 1; m < MB; ++m) a = m == mb ? mine[m] : a;  // (indexes of registers are constants)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) y[j][v] = 0.f;
+      strip_add<NJ, 8>(p.ad, p.M, p.d_out, 16 * mb, a, c, y);
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        if (m != mb) continue;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          f32x4& to = into(acc[m][j], acc0[m][j]);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) to[v] += y[j][v];
+        }
+      }
+    }
+  };
+  if constexpr (MULTI)
+    if (early) strips([](f32x4& a, f32x4&) -> f32x4& { return a; });
   // The stage loop, unrolled so that every ring slot index is a constant.
   constexpr int U = (NS % 2) ? 2 * NS : NS;
   for (int t0 = 0; t0 < nk; t0 += U) {
@@ -1143,44 +1186,9 @@ few_fwd_bf16_kernel(const FewArgs p) {
     });
   }
 
-  const int b = blockIdx.x, na = two ? 2 : 1;
-  // MULTI: the strips of tile a0's rows, dealt in 16-row blocks to the blocks
-  // whose range starts in the tile (one at least: ranges are no longer than a
-  // tile), so that all CUs read the adapters' second operands.  (By the one block
-  // that finishes a tile, with a tile for every second CU, they took 20 us of
-  // 51: 48 rows, 4096 -> 14336, r = 16.)
-  if constexpr (MULTI) {
-    auto first = [&](int a) { return (int)(((int64_t)a * p.nblk + p.n_tiles - 1) / p.n_tiles); };
-    const int j0 = b - first(sp.a0), cnt = first(sp.a0 + 1) - first(sp.a0);
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-      if (mb % cnt != j0) continue;
-      int t[4 * NJ];
-      int64_t c[4 * NJ];
-      float y[4 * NJ][1];
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int row = 16 * mb + 4 * g + v, col = sp.a0 * BNF + 32 * wave + 16 * j + l16;
-          t[4 * j + v] = row < p.M && col < p.d_out ? row : -1;
-          c[4 * j + v] = col;
-          y[4 * j + v][0] = two ? acc0[mb][j][v] : acc[mb][j][v];
-        }
-      StripAdd<4 * NJ, 1> strip;
-      strip.load(p.ad, p.d_out, t, c);
-      strip.add(p.ad, y);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          if (two)
-            acc0[mb][j][v] = y[4 * j + v][0];
-          else
-            acc[mb][j][v] = y[4 * j + v][0];
-        }
-    }
-  }
+  const int na = two ? 2 : 1;
+  if constexpr (MULTI)
+    if (!early) strips([&](f32x4& a, f32x4& a0) -> f32x4& { return two ? a0 : a; });
 
   // ---- one partial per covered tile, then the last block of a tile sums ----
   auto store_part = [&](const f32x4 (&v)[MB][NJ], int a) {

@@ -360,3 +360,22 @@ def test_trained_block(lib, M):
     gh, gw, ga, gb = torch.autograd.grad((z, h), (h, wd, ad, bd), (dY.double(), dH.double()), allow_unused=True)
     for got, want, what in zip(first, (gh, gh, gw, ga, gb), ("X", "residual", "weight", "A", "B")):
         _rel(got, want, 4 * 2.0 ** -8, what)  # the norm's output, a strip, dY W and the gradient rounded
+
+
+# one launch over strips of W's columns, or a stream of W, that adds the rows' strips itself; ranks in steps of 32
+@pytest.mark.parametrize("order", ["packed", "random"])
+@pytest.mark.parametrize("shape", [(1, 4096, 4096, 3, 128), (16, 1024, 1032, 9, 72), (40, 2048, 2056, 30, 128), (64, 1024, 1024, 64, 64),
+                                   (33, 520, 4104, 40, 24), (20, 4096, 4096, 20, 32), (64, 4096, 4104, 64, 24), (5, 4096, 8192, 5, 128),
+                                   (48, 4096, 8200, 64, 64), (64, 8192, 4096, 7, 40), (3, 4096, 8192, 2, 16)])
+def test_few_rows(lib, shape, order):
+    M, k, d, n, r = shape
+    args = make(M + k + n, M, k, d, n, r, torch.bfloat16, order)
+    Y = lib.lora_multi_fwd(*args[:6])
+    (want, tol), *_ = reference(*args)
+    _near(Y, want, tol, "Y")
+    assert torch.equal(Y, lib.lora_multi_fwd(*args[:6]))
+
+
+@pytest.mark.parametrize("M,k,d", [(20, 4096, 4096), (40, 4096, 8192), (60, 1024, 1024)])
+def test_infinities_of_few_rows_stay_with_their_own(lib, M, k, d):
+    test_infinities_stay_with_their_own(lib, torch.bfloat16, M, k, d)
