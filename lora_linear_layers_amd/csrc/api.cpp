@@ -1844,7 +1844,7 @@ MultiProduct multi_product(int dtype, int64_t M, int64_t N, int64_t K, int64_t n
     P.skinny = !P.few_ && fits && (M <= 16 || K <= 2048 || N >= 4096);
     if (P.few_ || P.skinny) return P;
   }
-  if (dtype == LORA_BF16 && M > 0 && K >= 64 && n * N * r * 2 < 0xE0000000ll) {
+  if (dtype == LORA_BF16 && M > 0 && K >= 64 && n * N * r * 2 < 0xE0000000ll) {  // (gemm_w4_nt.h)
     const int64_t t = cdiv(M, 256) * cdiv(N, 256);
     if (M % 256 == 0 && N % 256 == 0 && t % 256 == 0 && K % 64 == 0 && t <= INT32_MAX / 2 &&
         whole_ld_fits(std::max(K, N))) {

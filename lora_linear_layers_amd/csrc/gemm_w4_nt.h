@@ -68,9 +68,15 @@ constexpr int vmcnt_imm(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }
 
 typedef __attribute__((address_space(3))) void lds_void_t;
 
-// Rows with an adapter of their own: the adapters' second operands lie in one
-// resource of less than AD_MAX bytes; a lane without a value takes AD_OOB.
-constexpr uint32_t AD_MAX = 0xE0000000u, AD_OOB = 0xF0000000u;
+// Rows with an adapter of their own (gemm_w4_stream.h, gemm_w4_half.h, MULTI): the
+// second segment is the tile's adapters', list by list, so that a tile's stages are
+// its contraction's and one for each 64 / ad_r of them: 8192 x 4096 over 4096, 8
+// adapters of 16 in runs of a thousand rows, 205 to 218 us (1340 TFLOP/s; the layer of one
+// adapter 195); 2048 x 4096 over 4096, 32 adapters, 114 to 122 us; 64 adapters in random
+// order, 14 stages more, 268 us.  Their second operands lie in one resource of less
+// than 0xE0000000 bytes; a lane without a value takes AD_OOB, which no row's offset
+// brings back into it.
+constexpr uint32_t AD_OOB = 0xF0000000u;
 // A list's entry is an adapter below AD_BAD, or with AD_BAD one whose second
 // operand holds an infinity or a NaN: it is read as zeros (times the other rows'
 // zeros it would be a NaN), and its own rows have strips of NaNs.
