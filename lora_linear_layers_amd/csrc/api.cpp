@@ -2786,7 +2786,9 @@ int lora_act8_unpack(int dtype, int64_t M, int64_t d, const uint8_t* codes, cons
 
 size_t lora_act8_linear_workspace_bytes(int dtype, int64_t M, int64_t d_in, const lora_group_member* member, int grad_dtype) {
   const lora_epilogue none{LORA_ACT_NONE, nullptr, nullptr, nullptr};
-  if (check_epi_sizes(dtype, M, d_in, member, &none) != LORA_OK || d_in > LORA_NORM_MAX_DIM) return 0;
+  if (check_epi_sizes(dtype, M, d_in, member, &none) != LORA_OK || d_in > LORA_NORM_MAX_DIM ||
+      (grad_dtype != LORA_F32 && grad_dtype != LORA_BF16))
+    return 0;
   return make_act8_layout(dtype, M, d_in, *member, grad_dtype == LORA_BF16).total;
 }
 
