@@ -122,7 +122,7 @@ def test_multi_validation():
 def test_act8_workspace_of_a_refused_gradient_type():
     lib = L.load()
     member = _lib.GroupMember(32, 8, 1.0, 0, P, None, None, P, P, None, P, P, P, P, None)
-    assert lib.lora_act8_linear_workspace_bytes(1, 4, 64, member, 1) > lib.lora_act8_linear_workspace_bytes(1, 4, 64, member, 0) > 0
+    assert lib.lora_act8_linear_workspace_bytes(1, 4, 64, member, 1) >= lib.lora_act8_linear_workspace_bytes(1, 4, 64, member, 0) > 0
     for bad in (-1, 2, 3):
         assert lib.lora_act8_linear_workspace_bytes(1, 4, 64, member, bad) == 0
 
