@@ -948,7 +948,6 @@ def lora_rmsnorm_bwd(H, weight, rstd, dY, dH=None, need_dX: bool = True, need_dw
     """(dX or None, dweight or None) of lora_rmsnorm_fwd from its H and rstd; dH: the gradient of H itself, where the
     residual stream goes on.  dX is the gradient of X and of the residual."""
     dev, same = _gpu(H), (H.dtype,)
-    dt = L._dtype_code(H)
     if H.dim() != 2:
         raise ValueError("H must be [M, d]")
     M, d = H.shape
@@ -958,9 +957,15 @@ def lora_rmsnorm_bwd(H, weight, rstd, dY, dH=None, need_dX: bool = True, need_dw
     _check(dev, "dY", dY, same, M * d)
     if dH is not None:
         _check(dev, "dH", dH, same, M * d)
+    return _rmsnorm_bwd(H, weight, rstd, dY, dH, need_dX, need_dweight, dweight_dtype, ws)
+
+
+def _rmsnorm_bwd(H, weight, rstd, dY, dH, need_dX, need_dweight, dweight_dtype, ws=None):
+    """lora_rmsnorm_bwd of checked tensors."""
     if not need_dX and not need_dweight:
         return None, None
-    dX = torch.empty(M, d, dtype=H.dtype, device=dev) if need_dX else None
+    dt, dev, (M, d) = L._dtype_code(H), H.device, H.shape
+    dX = torch.empty_like(H) if need_dX else None
     dw, ws_bytes = None, 0
     if need_dweight:
         dw = torch.empty(d, dtype=dweight_dtype, device=dev)
@@ -999,8 +1004,9 @@ class LoraRmsNormFunction(torch.autograd.Function):
         need_X, need_R, need_w = ctx.needs_input_grad[:3]
         if dY is None:  # the stream alone went on
             return dH if need_X else None, dH if need_R else None, None, None, None
-        dX, dw = lora_rmsnorm_bwd(H, weight, rstd, dY.contiguous(), None if dH is None else dH.contiguous(),
-                                  need_X or need_R, need_w, weight.dtype)
+        # (the forward checked what it kept, autograd the gradients' type, shape and device)
+        dX, dw = _rmsnorm_bwd(H, weight, rstd, dY.contiguous(), None if dH is None else dH.contiguous(),
+                              need_X or need_R, need_w, weight.dtype)
         return dX if need_X else None, dX if need_R else None, None if dw is None else dw.view_as(weight), None, None
 
 
@@ -1098,9 +1104,8 @@ class LoraLinearAct8Function(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dY):
         codes, scale8, W, A, B, W_t = ctx.saved_tensors
-        dY = dY.contiguous()
+        dY = dY.contiguous()  # (its type, shape and device are Y's)
         (M, d_in), (d_out, r) = codes.shape, B.shape
-        _check(codes.device, "the gradient of Y", dY, (A.dtype,), M * d_out)
         m = _epi_struct({"W": W, "A": A, "B": B, "scale": ctx.scale, "W_t": W_t}, r, d_out)
         need_dX, _, need_dA, need_dB = ctx.needs_input_grad[:4]
         dX, dA, dB = _act8_bwd(codes, scale8, m, dY, M, d_in, d_out, r, need_dX, None, A.dtype)
@@ -1139,11 +1144,17 @@ def _multi_ws(backward, dt, M, d_in, d_out, n, r, have_wt, need_dX, dev, ws):
 def lora_multi_fwd(X, W, A, B, scales, index, Y=None, ws=None):
     """Y [M, d_out]: row t is W x_t + scales[a] B[a] (A[a] x_t) with a = index[t] (int32 [M]; outside [0, n): W x_t
     alone), for n adapters A [n, r, d_in], B [n, d_out, r] and fp32 scales [n] over one frozen W [d_out, d_in]."""
-    dt, dev, M, d_in, d_out, n, r = _multi_dims(X, W, A, B, scales, index)
+    dims = _multi_dims(X, W, A, B, scales, index)
+    if Y is not None:
+        _check(dims[1], "Y", Y, (X.dtype,), dims[2] * dims[4])
+    return _multi_fwd(dims, X, W, A, B, scales, index, Y, ws)
+
+
+def _multi_fwd(dims, X, W, A, B, scales, index, Y=None, ws=None):
+    """lora_multi_fwd of checked tensors."""
+    dt, dev, M, d_in, d_out, n, r = dims
     if Y is None:
         Y = torch.empty(M, d_out, dtype=X.dtype, device=dev)
-    else:
-        _check(dev, "Y", Y, (X.dtype,), M * d_out)
     ws, ws_bytes = _multi_ws(0, dt, M, d_in, d_out, n, r, 0, 0, dev, ws)
     with _on(dev):
         L._check("lora_multi_fwd", L.lib().lora_multi_fwd(
@@ -1155,13 +1166,24 @@ def lora_multi_fwd(X, W, A, B, scales, index, Y=None, ws=None):
 def lora_multi_bwd(X, W, A, B, scales, index, dY, need_dX: bool = True, W_t=None, grad_dtype=torch.float32, ws=None):
     """(dX or None, dA [n, r, d_in], dB [n, d_out, r]) of lora_multi_fwd, the adapters' gradients in grad_dtype (zeros for
     an adapter without rows); W_t: W's transpose (bf16), where the caller keeps one."""
-    dt, dev, M, d_in, d_out, n, r = _multi_dims(X, W, A, B, scales, index)
+    dims = _multi_dims(X, W, A, B, scales, index)
+    _, dev, M, d_in, d_out, _, _ = dims
     _check(dev, "dY", dY, (X.dtype,), M * d_out)
+    _multi_wt(dev, W_t, d_in, d_out)
+    return _multi_bwd(dims, X, W, A, B, scales, index, dY, need_dX, W_t, grad_dtype, ws)
+
+
+def _multi_wt(dev, W_t, d_in, d_out):
     if W_t is not None:
         _check(dev, "W_t", W_t, (torch.bfloat16,), d_in * d_out)
         if W_t.shape != (d_in, d_out):
             raise ValueError("W_t must be the bf16 [d_in, d_out] transpose of W")
-    dX = torch.empty(M, d_in, dtype=X.dtype, device=dev) if need_dX else None
+
+
+def _multi_bwd(dims, X, W, A, B, scales, index, dY, need_dX, W_t, grad_dtype, ws=None):
+    """lora_multi_bwd of checked tensors."""
+    dt, dev, M, d_in, d_out, n, r = dims
+    dX = torch.empty_like(X) if need_dX else None
     dA = torch.empty(n, r, d_in, dtype=grad_dtype, device=dev)
     dB = torch.empty(n, d_out, r, dtype=grad_dtype, device=dev)
     ws, ws_bytes = _multi_ws(1, dt, M, d_in, d_out, n, r, int(W_t is not None), int(need_dX), dev, ws)
@@ -1178,13 +1200,15 @@ class LoraMultiFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, X, W, A, B, scales, index, W_t=None):
+        ctx.dims = dims = _multi_dims(X, W, A, B, scales, index)
+        _multi_wt(dims[1], W_t, dims[3], dims[4])
         ctx.save_for_backward(X, W, A, B, scales, index, W_t)
-        return lora_multi_fwd(X, W, A, B, scales, index)
+        return _multi_fwd(dims, X, W, A, B, scales, index)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dY):
         X, W, A, B, scales, index, W_t = ctx.saved_tensors
         need_dX, _, need_dA, need_dB = ctx.needs_input_grad[:4]
-        dX, dA, dB = lora_multi_bwd(X, W, A, B, scales, index, dY.contiguous(), need_dX, W_t, X.dtype)
+        dX, dA, dB = _multi_bwd(ctx.dims, X, W, A, B, scales, index, dY.contiguous(), need_dX, W_t, X.dtype)
         return dX, None, dA if need_dA else None, dB if need_dB else None, None, None, None
