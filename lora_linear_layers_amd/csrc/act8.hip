@@ -214,7 +214,7 @@ __device__ __forceinline__ void grad8_tile(char* smem, const Act8Args& p, const 
 #pragma unroll
     for (int i = 0; i < C::IA; ++i) {
       const int row = 8 * (i + C::IA * wave) + (lane >> 3), kk = u * BK + 8 * (i & 1 ? dco : dce);
-      dma(ga, st + 8 * (i + C::IA * wave) * 128, kk < klen && row < p.r8, (uint32_t)((row * p.rows + kk) * 2));
+      dma(ga, st + 8 * (i + C::IA * wave) * 128, kk < klen && row < p.qr, (uint32_t)((row * p.rows + kk) * 2));
     }
     // instruction i of wave w: token rows 16 w + 4 i + lane / 16, the lane landing at chunk lane % 16
 #pragma unroll
@@ -275,13 +275,13 @@ __device__ __forceinline__ void grad8_tile(char* smem, const Act8Args& p, const 
     }
     __builtin_amdgcn_s_waitcnt(pdma::vmcnt_imm(0));
   }
-  float* out = p.gpart + (int64_t)z * p.r8 * p.d;
+  float* out = p.gpart + (int64_t)z * p.qr * p.d;
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
       const int row = 32 * i + 8 * (v >> 2) + 4 * hh + (v & 3);
-      if (row >= p.r8) continue;
+      if (row >= p.qr) continue;
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         const int64_t col = n0 + 64 * wave + 32 * j + l32;
@@ -345,16 +345,16 @@ hipError_t launch_act8_panel_pair(const Act8Args& a, const GemmArgs& b, int sb, 
 
 hipError_t launch_act8_grad_pair(const Act8Args& a, const GemmArgs& b, int sb, hipStream_t st) {
   // (the tokens' stride of Qt, and b as launch_gemm_pair checks it)
-  if (!args_ok(a) || sb < 1 || a.rows * 2 * 128 >= (int64_t)w4::BIG || b.m_store != a.r8 || b.m_load > b.m_store || b.n_load != b.n_store ||
+  if (!args_ok(a) || sb < 1 || a.rows * 2 * 128 >= (int64_t)w4::BIG || b.m_store != a.qr || (a.qr != a.r8 && a.qr != 2 * a.r8) || a.qr > 128 || b.m_load > b.m_store || b.n_load != b.n_store ||
       b.K2 || (b.k_split + sdma::BK) * b.ldb1 * 2 + b.n_store * 2 >= (int64_t)w4::BIG || b.lda1 * 2 * 128 >= (int64_t)w4::BIG)
     return hipErrorInvalidValue;
   const int64_t t0 = (a.d + s8::BN - 1) / s8::BN, t1 = (b.n_store + sdma::BN - 1) / sdma::BN;
   const dim3 grid((unsigned)std::max(t0, t1), (unsigned)(a.gsplits + sb));
   const Act8Pair q{a, b};
   // two blocks a CU where there are blocks for them, as the pair of bf16 ones
-  if (a.r8 <= 64 && t0 * a.gsplits + t1 * sb > 256)
+  if (a.qr <= 64 && t0 * a.gsplits + t1 * sb > 256)
     hipLaunchKernelGGL((act8_grad_kernel<64, 3, 2>), grid, dim3(sdma::NT), 0, st, q);
-  else if (a.r8 <= 64)
+  else if (a.qr <= 64)
     hipLaunchKernelGGL((act8_grad_kernel<64, 6, 4>), grid, dim3(sdma::NT), 0, st, q);
   else
     hipLaunchKernelGGL((act8_grad_kernel<128, 5, 3>), grid, dim3(sdma::NT), 0, st, q);

@@ -903,7 +903,7 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
                   const void* W, const Nf4W* nf4, const void* A, const void* B, const Rope* rope, const void* dY,
                   void* dX, float* dA, float* dB, void* ws, const Layout& L, hipStream_t st,
                   const PanelSlices* ov = nullptr, const void* Xa = nullptr, const uint8_t* keep = nullptr,
-                  const void* Wt_in = nullptr, Act8Args* x8 = nullptr, bool low = false) {
+                  const void* Wt_in = nullptr, Act8Call* x8 = nullptr, bool low = false) {
   // x8: X in 8 bits (act8.hip) instead of X, for layouts that run the panels and
   // the gradients in pairs; low: dA and dB in bf16 there
   // LoRA dropout: Xa is the adapter's (masked) input and `keep` the mask that
@@ -960,11 +960,12 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
     }));
     G = w + L.g;
   }
-  const void* Pt = ov ? ov->Pt : w + L.pt;
+  const void* Pt = ov ? ov->Pt : x8 ? reinterpret_cast<char*>(x8->Pt) : w + L.pt;
   void* Qs = ov ? ov->Qs : w + L.qs;
   const int64_t ldqs = ov ? ov->ldqs : L.r8;
-  void* Qt = ov ? ov->Qt : w + L.qt;
-  float* part = reinterpret_cast<float*>(w + L.part);
+  void* Qt = ov ? ov->Qt : x8 ? reinterpret_cast<char*>(const_cast<uint16_t*>(x8->k.Qt)) : w + L.qt;
+  const int64_t qr = x8 ? x8->k.qr : L.r8;  // rows of Pt and Qt
+  float* part = x8 ? x8->k.gpart : reinterpret_cast<float*>(w + L.part);
   bool at_done = false;  // A^T made with B^T (bf16)
   if (f32) {
     // Pt = (s X A^T)^T  [r8, M8]  (recomputed; pads are zeros)
@@ -996,7 +997,7 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
   } else {
     // Pt = (s X A^T)^T  [r8, M8], recomputed from X (rows M..M8 and columns r..r8 are zeros)
     float* pp = reinterpret_cast<float*>(w + L.ppart);
-    uint16_t* pt = reinterpret_cast<uint16_t*>(w + L.pt);
+    uint16_t* pt = x8 ? x8->Pt : reinterpret_cast<uint16_t*>(w + L.pt);
     if (!ov && !L.pair)
       TRY(panel_bf16(Xp, d_in, A, d_in, M, L.M8, d_in, r, L.r8, L.splits_p, L.ksplit_p, col_scale(scale), pp,
                      nullptr, 0, pt, L.M8, st));
@@ -1030,20 +1031,17 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
       const GemmArgs a = panel_args(Xp, d_in, A, d_in, M, L.M8, d_in, r, L.r8, L.ksplit_p, pp);
       const GemmArgs b = panel_args(G, d_out, Bt, d_out, M, L.M8, d_out, r, L.r8, L.ksplit_q, pq);
       const double el = double(L.M8) * L.r8;
-      const int splits_p = x8 ? x8->splits : L.splits_p;
-      if (x8) {
-        x8->part = pp;
-        x8->Qt = static_cast<const uint16_t*>(Qt);
-      }
+      const int splits_p = x8 ? x8->k.splits : L.splits_p;
+      if (x8) x8->k.part = pp;
       HIPTRY(timed(G_BF16_PANEL_SPLIT_NT, 2 * Md * rr * (ki + ko),
                    (Md + rr) * (ki + ko) * 2 - (x8 ? Md * ki : 0) + 4.0 * (splits_p + L.splits_q) * el, st, [&] {
-                     if (x8) return launch_act8_panel_pair(*x8, b, L.splits_q, st);
+                     if (x8) return launch_act8_panel_pair(x8->k, b, L.splits_q, st);
                      return launch_gemm_pair(G_BF16_PANEL_SPLIT_NT, a, L.splits_p, b, L.splits_q, st);
                    }));
       HIPTRY(timed(K_PANEL, (splits_p + L.splits_q) * el, (4.0 * (splits_p + L.splits_q) + 6) * el, st, [&] {
-        return launch_panel_reduce_pair({pp, splits_p, nullptr, pt},
+        return launch_panel_reduce_pair({pp, splits_p, nullptr, pt, nullptr, 0, qr > L.r8},
                                         {pq, L.splits_q, static_cast<uint16_t*>(Qs), static_cast<uint16_t*>(Qt),
-                                         x8 ? x8->scale8 : nullptr, M},
+                                         x8 ? x8->k.scale8 : nullptr, M, qr > L.r8},
                                         L.M8, L.r8, col_scale(scale), st, cnt, ncnt);
       }));
     } else {
@@ -1133,15 +1131,15 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
   const GemmKind ksplit = f32 ? G_F32_SPLIT_NN_PARTIAL : G_BF16_SPLIT_NN_PARTIAL;
   // bf16: the dB partials have their own buffer and both sums run as one
   // launch (a group's: one for all its members, after the group's dA)
-  float* partb = f32 ? part : (ov && ov->partb ? ov->partb : reinterpret_cast<float*>(w + L.partb));
+  float* partb = f32 ? part : x8 ? x8->partb : (ov && ov->partb ? ov->partb : reinterpret_cast<float*>(w + L.partb));
   ReduceBatch own;
   own.low = low;
   ReduceBatch* red = f32 ? nullptr : (ov && ov->red ? ov->red : &own);
   // dB^T = Pt G  -> partials [splits][r8, d_out] -> dB [d_out, r]
   GemmArgs ab = blank();
   ab.a1 = Pt; ab.lda1 = L.M8; ab.b1 = G; ab.ldb1 = d_out; ab.K1 = M;
-  ab.m_load = L.r8; ab.m_store = L.r8; ab.n_load = d_out; ab.n_store = d_out;
-  ab.k_split = L.ksplit_dB; ab.c = partb; ab.ldc = d_out; ab.part_stride = L.r8 * d_out;
+  ab.m_load = qr; ab.m_store = qr; ab.n_load = d_out; ab.n_store = d_out;
+  ab.k_split = L.ksplit_dB; ab.c = partb; ab.ldc = d_out; ab.part_stride = qr * d_out;
   const double fb = 2 * rr * ko * Md, bb = (rr * Md + Md * ko) * e + 4.0 * L.splits_dB * L.r8 * ko;
   // dA = Qt X -> partials [splits][r8, d_in] -> dA [r, d_in]
   GemmArgs aa = blank();
@@ -1150,16 +1148,16 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
   aa.k_split = L.ksplit_dA; aa.c = part; aa.ldc = d_in; aa.part_stride = L.r8 * d_in;
   const double fa = 2 * rr * ki * Md, ba = (rr * Md + Md * ki) * e + 4.0 * L.splits_dA * L.r8 * ki;
   const bool both = x8 || (L.pair && gemm_pair_fits(ksplit, ab, aa));
-  if (x8) {
-    x8->gpart = part;
-    HIPTRY(timed(ksplit, fa + fb, ba + bb - Md * ki, st, [&] { return launch_act8_grad_pair(*x8, ab, L.splits_dB, st); }));
-  } else if (both)
+  if (x8)
+    HIPTRY(timed(ksplit, fa + fb, ba + bb - Md * ki, st, [&] { return launch_act8_grad_pair(x8->k, ab, L.splits_dB, st); }));
+  else if (both)
     HIPTRY(timed(ksplit, fa + fb, ba + bb, st,
                  [&] { return launch_gemm_pair(ksplit, ab, L.splits_dB, aa, L.splits_dA, st); }));
   else
     HIPTRY(gemm(ksplit, ab, L.splits_dB, st, fb, bb));
   if (red)
-    HIPTRY(red->add(partb, L.splits_dB, r, d_out, L.r8 * d_out, true, dB));
+    // (two parts of a strip: twice the slabs)
+    HIPTRY(red->add(partb, L.splits_dB * (int)(qr / L.r8), r, d_out, L.r8 * d_out, true, dB));
   else
     HIPTRY(timed(K_REDUCE, double(L.splits_dB) * rr * ko, 4.0 * (L.splits_dB + 1) * rr * ko, st, [&] {
       return launch_reduce_splits(partb, L.splits_dB, r, d_out, L.r8 * d_out, true, dB, st);
@@ -1167,7 +1165,7 @@ int backward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, 
   if (!ov) {
     if (!both) HIPTRY(gemm(ksplit, aa, L.splits_dA, st, fa, ba));
     if (red)
-      HIPTRY(red->add(part, L.splits_dA, r, d_in, L.r8 * d_in, false, dA));
+      HIPTRY(red->add(part, L.splits_dA * (int)(qr / L.r8), r, d_in, L.r8 * d_in, false, dA));
     else
       HIPTRY(timed(K_REDUCE, double(L.splits_dA) * rr * ki, 4.0 * (L.splits_dA + 1) * rr * ki, st, [&] {
         return launch_reduce_splits(part, L.splits_dA, r, d_in, L.r8 * d_in, false, dA, st);
@@ -1779,6 +1777,11 @@ struct Act8Layout {
   bool direct = false;
   int splits = 1;
   int64_t ksplit = 0;
+  // Ranks up to 32, direct: P and Q in two bf16 parts, 2 r8 of the 64 rows that the
+  // gradients' tiles have anyway: dA and dB then carry their own rounding alone (0.0017
+  // relative in the mean; with P and Q rounded once, as the layer's own, 0.0024).
+  int64_t qr = 0;
+  size_t pt = 0, qt = 0, gpart = 0, partb = 0;
   size_t x = 0, ga = 0, gb = 0, total = 0;  // (ga, gb: gradients in fp32 before they are rounded)
 };
 
@@ -1789,16 +1792,21 @@ Act8Layout make_act8_layout(int dtype, int64_t M, int64_t d_in, const lora_group
   A.total = A.E.total;
   A.direct = M > 0 && dtype == LORA_BF16 && L.pair && !(L.few.ok && m.dX) && act8_fits(d_in, L.r8) && L.M8 * 2 * 128 < (1 << 30) &&
              (L.ksplit_dB + 64) * m.d_out * 2 + m.d_out * 2 < (1 << 30) && L.M8 * d_in < (int64_t(1) << 40);
+  auto take = [&](size_t bytes) {
+    const size_t at = align256(A.total);
+    A.total = at + align256(bytes);
+    return at;
+  };
   if (A.direct) {
+    A.qr = 2 * L.r8 <= 64 && L.splits_dA <= 32 && L.splits_dB <= 32 ? 2 * L.r8 : L.r8;
+    A.pt = take(size_t(A.qr) * L.M8 * 2);
+    A.qt = take(size_t(A.qr) * L.M8 * 2);
+    A.gpart = take(size_t(L.splits_dA) * A.qr * d_in * 4);
+    A.partb = take(size_t(L.splits_dB) * A.qr * m.d_out * 4);
     // (stages of 128: no more splits than the panel's partials have room for)
     A.ksplit = rup(L.ksplit_p, 128);
     A.splits = (int)cdiv(d_in, A.ksplit);
   } else {
-    auto take = [&](size_t bytes) {
-      const size_t at = align256(A.total);
-      A.total = at + align256(bytes);
-      return at;
-    };
     A.x = take(size_t(M) * d_in * elem_bytes(dtype));
     if (low) {
       A.ga = take(size_t(m.r) * d_in * 4);
@@ -2808,13 +2816,16 @@ int lora_act8_linear_bwd(int dtype, int64_t M, int64_t d_in, const lora_group_me
   hipStream_t st = static_cast<hipStream_t>(stream);
   char* w = static_cast<char*>(ws);
   void* X = w + E.x;
-  Act8Args x8;
-  memset(&x8, 0, sizeof(x8));
+  Act8Call call;
+  memset(&call, 0, sizeof(call));
+  Act8Args& x8 = call.k;
   if (E.direct) {
     const Layout& L = E.E.L;
     x8.codes = codes; x8.scale8 = scale8; x8.M = M; x8.d = d_in;
     x8.A = static_cast<const uint16_t*>(m.A); x8.rows = L.M8; x8.r = m.r; x8.r8 = L.r8;
     x8.splits = E.splits; x8.ksplit = E.ksplit; x8.gsplits = L.splits_dA; x8.gksplit = L.ksplit_dA;
+    x8.qr = E.qr; x8.Qt = reinterpret_cast<uint16_t*>(w + E.qt); x8.gpart = reinterpret_cast<float*>(w + E.gpart);
+    call.Pt = reinterpret_cast<uint16_t*>(w + E.pt); call.partb = reinterpret_cast<float*>(w + E.partb);
   } else if (M > 0) {
     HIPTRY(timed(K_ACT8, double(M) * d_in, double(M) * d_in * (elem_bytes(dtype) + 1), st,
                  [&] { return launch_act8_unpack(elem_bytes(dtype), codes, scale8, M, d_in, X, st); }));
@@ -2826,7 +2837,7 @@ int lora_act8_linear_bwd(int dtype, int64_t M, int64_t d_in, const lora_group_me
   const Nf4W q{m.W_nf4, m.absmax, table16};
   TRY(backward_impl(dtype, M, d_in, m.d_out, m.r, m.scale, X, m.W, m.W_nf4 ? &q : nullptr, m.A, m.B, nullptr, m.dY, m.dX,
                     dA, dB, ws, E.E.L, st, nullptr, nullptr, nullptr, E.E.L.dx_nt && !m.W_nf4 ? m.W_t : nullptr,
-                    E.direct ? &x8 : nullptr, low && E.direct));
+                    E.direct ? &call : nullptr, low && E.direct));
   if (wide)
     HIPTRY(timed(K_ACT8, 0, 6.0 * m.r * (d_in + m.d_out), st, [&] {
       return launch_to_bf16(dA, m.r * d_in, reinterpret_cast<uint16_t*>(m.dA), dB, m.r * m.d_out,

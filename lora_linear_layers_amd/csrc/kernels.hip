@@ -1230,7 +1230,8 @@ constexpr int kMaxPanelSplits = 32;
 __device__ __forceinline__ void panel_reduce_tile(const float* __restrict__ part, int splits, int64_t part_stride,
                                                   int64_t ldp, int64_t rows, int64_t n, const ColScale& scale,
                                                   uint16_t* __restrict__ out, int64_t ldo, uint16_t* __restrict__ outt,
-                                                  int64_t ldot, const float* __restrict__ tscale = nullptr, int64_t tn = 0) {
+                                                  int64_t ldot, const float* __restrict__ tscale = nullptr, int64_t tn = 0,
+                                                  bool rest = false) {
   __shared__ float tile[16][65];
   const int tid = threadIdx.x;
   const int64_t q0 = (int64_t)blockIdx.x * 16, c0 = (int64_t)blockIdx.y * 64;
@@ -1267,7 +1268,14 @@ __device__ __forceinline__ void panel_reduce_tile(const float* __restrict__ part
     const int idx = k * 256 + tid;
     const int cc = idx >> 4, qq = idx & 15;  // consecutive threads: consecutive rows of the transpose
     const int64_t qg = q0 + qq, cg = c0 + cc;
-    if (qg < rows && cg < n) outt[cg * ldot + qg] = f2bf(tile[qq][cc]);
+    if (qg < rows && cg < n) {
+      const float v = tile[qq][cc];
+      const uint16_t h = f2bf(v);
+      outt[cg * ldot + qg] = h;
+      // (nothing of a value that is not finite, or rounds to infinity)
+      const float hv = __builtin_bit_cast(float, (uint32_t)h << 16);
+      if (rest) outt[(n + cg) * ldot + qg] = (h & 0x7F80u) == 0x7F80u ? (uint16_t)0 : f2bf(v - hv);
+    }
   }
 }
 
@@ -1292,7 +1300,7 @@ __global__ void __launch_bounds__(256) panel_reduce_pair_kernel(PanelSum a, Pane
   const bool second = blockIdx.z != 0;
   panel_reduce_tile(second ? b.part : a.part, second ? b.splits : a.splits, rows * n, n, rows, n, scale,
                     second ? b.out : a.out, n, second ? b.outt : a.outt, rows, second ? b.tscale : a.tscale,
-                    second ? b.tn : a.tn);
+                    second ? b.tn : a.tn, second ? b.rest : a.rest);
 }
 
 hipError_t launch_panel_reduce_pair(const PanelSum& a, const PanelSum& b, int64_t rows, int64_t n,

@@ -177,6 +177,7 @@ struct PanelSum {
   uint16_t* outt;
   const float* tscale = nullptr;  // outt's values times their row's power of two (rows [0, tn), 0 past them)
   int64_t tn = 0;
+  bool rest = false;  // outt has n rows more: what the rounding of the first n left, rounded
 };
 hipError_t launch_panel_reduce_pair(const PanelSum& a, const PanelSum& b, int64_t rows, int64_t n,
                                     const ColScale& scale, hipStream_t st, int* zero, int nzero);
@@ -479,10 +480,17 @@ struct Act8Args {
   int splits;
   int64_t ksplit;        // a multiple of 128
   float* part;
-  const uint16_t* Qt;    // [r8, rows], its rows' values times the tokens' scales
+  const uint16_t* Qt;    // [qr, rows], its rows' values times the tokens' scales
+  int64_t qr;            // r8, or 2 r8: the values in two parts
   int gsplits;
   int64_t gksplit;       // a multiple of 64
   float* gpart;
+};
+// Such a backward's own scratch: both strips transposed and the gradients' partials.
+struct Act8Call {
+  Act8Args k;  // (Qt, gpart)
+  uint16_t* Pt;
+  float* partb;
 };
 bool act8_fits(int64_t d, int64_t r8);
 // Beside a bf16 panel (its splits sb) and beside a bf16 gradient, as launch_gemm_pair.
