@@ -729,7 +729,8 @@ int few_backward(const FewPlan& F, int64_t M, int64_t d_in, int64_t d_out, int64
 }
 
 // Pext: when not NULL, the panel s X A^T is already in Pext (row stride
-// ldpext, columns r..r8 zero) and is not computed here (group calls).
+// ldpext, columns r..r8 zero) and is not computed here (group calls; rows with
+// an adapter of their own, whose strips are in Y already: r = 0).
 // ep: the bias / activation / residual epilogue (not with RoPE).
 int forward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, float scale, const void* X,
                  const void* W, const Nf4W* nf4, const void* A, const void* B, const Rope* rope, void* Y, void* ws,
@@ -793,7 +794,10 @@ int forward_impl(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t r, f
   const double Md = double(M), ki = double(d_in), ko = double(d_out), rr = double(r), e = double(eb);
   // panel: P = s * X A^T  [M, r8] (columns r..r8 are exact zeros)
   if (Pext) {
-    // computed by the caller
+    // (computed by the caller; the panel's sum clears the counters otherwise)
+    if (cnt)
+      HIPTRY(timed(K_FILL, 0, 4.0 * L.stream.half, st,
+                   [&] { return launch_fill_zero(reinterpret_cast<float*>(cnt), L.stream.half, st); }));
   } else if (f32) {
     GemmArgs a = blank();
     a.a1 = Xp; a.lda1 = d_in; a.b1 = A; a.ldb1 = d_in; a.K1 = d_in;

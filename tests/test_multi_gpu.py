@@ -379,3 +379,46 @@ def test_few_rows(lib, shape, order):
 @pytest.mark.parametrize("M,k,d", [(20, 4096, 4096), (40, 4096, 8192), (60, 1024, 1024)])
 def test_infinities_of_few_rows_stay_with_their_own(lib, M, k, d):
     test_infinities_stay_with_their_own(lib, torch.bfloat16, M, k, d)
+
+
+def _large_stack(seed, M, k, d, n, r):
+    """Inputs with n adapters on the device, of which the rows carry six and none; and the same with those six alone."""
+    g = torch.Generator().manual_seed(seed)
+    gpu = torch.Generator(device="cuda").manual_seed(seed)
+    normal = lambda *s: torch.randn(*s, generator=gpu, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    X, W, dY = normal(M, k), normal(d, k).div_(math.sqrt(k)), normal(M, d)
+    A, B = normal(n, r, k).div_(math.sqrt(k)), normal(n, d, r).mul_(0.2)
+    scales = (0.25 + torch.rand(n, generator=g)).cuda()
+    used = torch.tensor([0, 7, n // 2 - 1, n // 2, n - 2, n - 1])
+    small = _index(g, M, 6, "random")
+    small[(small < 0) | (small >= 6)] = -1
+    index = torch.where(small < 0, -1, used[small.clamp(min=0).long()].to(torch.int32))
+    used = used.cuda()
+    return (X, W, A, B, scales, index.cuda(), dY), (X, W, A[used], B[used], scales[used], small.cuda(), dY), used
+
+
+@pytest.mark.parametrize("M,k,d,n,r", [(1200, 4096, 14336, 1024, 128), (1200, 1536, 14336, 2048, 64)])
+def test_stacks_past_the_product_kernel(lib, M, k, d, n, r):
+    """Second operands of 0xE0000000 bytes, which the product with the adapters' columns does not take: the strips' part
+    first, then the base product, the last of whose tiles are two blocks' work each.  The workspace holds ones."""
+    args, few, _ = _large_stack(n, M, k, d, n, r)
+    assert args[3].nbytes >= 0xE0000000
+    nb = lib.lib().lora_multi_workspace_bytes(0, 1, M, k, d, n, r, 0, 0)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    (want, tol), *_ = reference(*few)
+    for _ in range(2):
+        Y = lib.lora_multi_fwd(*args[:6], ws=ws.fill_(0xFF))
+        _near(Y, want, tol, "Y")
+
+
+def test_stacks_past_the_product_kernel_backward(lib):
+    M, k, d, n, r = 1200, 14336, 4096, 1024, 128
+    args, few, used = _large_stack(5, M, k, d, n, r)
+    nb = lib.lib().lora_multi_workspace_bytes(1, 1, M, k, d, n, r, 0, 1)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda").fill_(0xFF)
+    dX, dA, dB = lib.lora_multi_bwd(*args, grad_dtype=torch.bfloat16, ws=ws)
+    _, (want, tol), (wA, tA), (wB, tB) = reference(*few)
+    _near(dX, want, tol, "dX")
+    for got, w, t, what in ((dA, wA, tA, "dA"), (dB, wB, tB, "dB")):
+        _near(got[used], w, t + 2.0 ** -8 * (w.abs() + t), what)
+        assert int((got != 0).flatten(1).any(1).sum()) <= len(used)
