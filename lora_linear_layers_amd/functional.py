@@ -632,6 +632,22 @@ def _check_ws(device, ws, nbytes=None):
     return ws
 
 
+def _keep(ctx, *tensors):
+    """save_for_backward, and what _kept checks of each."""
+    ctx.save_for_backward(*tensors)
+    ctx.kept = [None if t is None else (t.dtype, t.shape) for t in tensors]
+
+
+def _kept(ctx, device):
+    """The saved tensors, still contiguous, on the device and of their dtype and shape: saved-tensor hooks may give back
+    any others, and their addresses go to the library."""
+    saved = ctx.saved_tensors
+    for t, kept in zip(saved, ctx.kept):
+        if kept is not None and (t is None or t.device != device or (t.dtype, t.shape) != kept or not t.is_contiguous()):
+            raise ValueError("a saved tensor came back with another device, dtype, shape or strides")
+    return saved
+
+
 def _gpu(t):
     if not t.is_cuda:
         raise ValueError("tensors must be on a GPU")
@@ -990,7 +1006,7 @@ class LoraRmsNormFunction(torch.autograd.Function):
     def forward(ctx, X, residual, weight, eps=1e-5, pack=False):
         Y, H, rstd, codes, scale8 = lora_rmsnorm_fwd(X, weight, eps, residual, pack)
         ctx.set_materialize_grads(False)
-        ctx.save_for_backward(H.contiguous(), weight, rstd)
+        _keep(ctx, H.contiguous(), weight, rstd)
         H = H if residual is not None else None
         if not pack:
             return Y, H
@@ -1000,11 +1016,11 @@ class LoraRmsNormFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dY, dH, *_):
-        H, weight, rstd = ctx.saved_tensors
         need_X, need_R, need_w = ctx.needs_input_grad[:3]
         if dY is None:  # the stream alone went on
             return dH if need_X else None, dH if need_R else None, None, None, None
-        # (the forward checked what it kept, autograd the gradients' type, shape and device)
+        # (autograd checked the gradients' type, shape and device)
+        H, weight, rstd = _kept(ctx, dY.device)
         dX, dw = _rmsnorm_bwd(H, weight, rstd, dY.contiguous(), None if dH is None else dH.contiguous(),
                               need_X or need_R, need_w, weight.dtype)
         return dX if need_X else None, dX if need_R else None, None if dw is None else dw.view_as(weight), None, None
@@ -1096,14 +1112,14 @@ class LoraLinearAct8Function(torch.autograd.Function):
                 if codes.shape != X.shape or codes.device != X.device:
                     raise ValueError("codes must have X's shape and device")
                 _packed(codes, scale8)
-            ctx.save_for_backward(codes, scale8, W, A, B, W_t)
+            _keep(ctx, codes, scale8, W, A, B, W_t)
         ctx.scale = scale
         return Y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dY):
-        codes, scale8, W, A, B, W_t = ctx.saved_tensors
+        codes, scale8, W, A, B, W_t = _kept(ctx, dY.device)
         dY = dY.contiguous()  # (its type, shape and device are Y's)
         (M, d_in), (d_out, r) = codes.shape, B.shape
         m = _epi_struct({"W": W, "A": A, "B": B, "scale": ctx.scale, "W_t": W_t}, r, d_out)
@@ -1202,13 +1218,13 @@ class LoraMultiFunction(torch.autograd.Function):
     def forward(ctx, X, W, A, B, scales, index, W_t=None):
         ctx.dims = dims = _multi_dims(X, W, A, B, scales, index)
         _multi_wt(dims[1], W_t, dims[3], dims[4])
-        ctx.save_for_backward(X, W, A, B, scales, index, W_t)
+        _keep(ctx, X, W, A, B, scales, index, W_t)
         return _multi_fwd(dims, X, W, A, B, scales, index)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dY):
-        X, W, A, B, scales, index, W_t = ctx.saved_tensors
+        X, W, A, B, scales, index, W_t = _kept(ctx, dY.device)
         need_dX, _, need_dA, need_dB = ctx.needs_input_grad[:4]
         dX, dA, dB = _multi_bwd(ctx.dims, X, W, A, B, scales, index, dY.contiguous(), need_dX, W_t, X.dtype)
         return dX, None, dA if need_dA else None, dB if need_dB else None, None, None, None
