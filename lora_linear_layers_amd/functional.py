@@ -542,7 +542,7 @@ class LoraLinearEpiFunction(torch.autograd.Function):
         # (the residual's gradient alone needs no Z)
         Y, Z = lora_linear_epi_fwd(X, member, act, bias, residual,
                                    store_z=act != "none" and any(ctx.needs_input_grad[i] for i in (0, 2, 3, 4)))
-        ctx.save_for_backward(X, W, A, B, Z, W_t)
+        _keep(ctx, X, W, A, B, Z, W_t)
         ctx.scale, ctx.act = scale, act
         ctx.shapes = [None if t is None else t.shape for t in (bias, residual)]
         return Y
@@ -550,7 +550,7 @@ class LoraLinearEpiFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dY):
-        X, W, A, B, Z, W_t = ctx.saved_tensors
+        X, W, A, B, Z, W_t = _kept(ctx, dY.device)
         dY = dY.contiguous()
         dev, (M, d_in), (d_out, r) = X.device, X.shape, B.shape
         _check(dev, "the gradient of Y", dY, (X.dtype,), M * d_out)

@@ -48,7 +48,7 @@ def _epi(t):
     return L.LoraLinearEpiFunction.apply(t["X"].requires_grad_(), t["W"], t["A"].requires_grad_(), t["B"], t["bias"], None, 0.5, "silu")
 
 
-OPS = {"norm": _norm, "act8": _act8, "multi": _multi}
+OPS = {"norm": _norm, "act8": _act8, "multi": _multi, "epi": _epi}
 
 
 @pytest.fixture
