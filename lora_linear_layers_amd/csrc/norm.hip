@@ -517,16 +517,43 @@ void by_width(int d, F&& f) {
 
 bool vec16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// f(first row, rows) of launches that take every row: a launch has fewer than 2^32
+// threads, 2^24 blocks of 256.
+template <class R, class F>
+void by_rows(int64_t M, F&& f) {
+  constexpr int64_t most = int64_t(UINT32_MAX / R::NT) * R::RPB;
+  for (int64_t r0 = 0; r0 < M; r0 += most) f(r0, std::min(most, M - r0));
+}
+template <class R>
+dim3 row_blocks(int64_t M) { return dim3((unsigned)((M + R::RPB - 1) / R::RPB)); }
+
+template <typename T>
+RmsNormArgs rows_of(RmsNormArgs a, int64_t r0, int64_t rows) {
+  auto in = [&](const void*& p, int64_t ld) { p = p ? static_cast<const T*>(p) + r0 * ld : nullptr; };
+  auto out = [&](void*& p) { p = p ? static_cast<T*>(p) + r0 * a.d : nullptr; };
+  in(a.X, a.ldx);
+  in(a.residual, a.ldr);
+  out(a.H);
+  out(a.Y);
+  if (a.codes) a.codes += r0 * a.d;
+  if (a.scale8) a.scale8 += r0;
+  if (a.rstd) a.rstd += r0;
+  a.M = rows;
+  return a;
+}
+
 template <typename T, bool VEC>
-void run_norm(const RmsNormArgs& a, hipStream_t st) {
-  by_width(a.d, [&](auto tpr, auto nv) {
+void run_norm(const RmsNormArgs& all, hipStream_t st) {
+  by_width(all.d, [&](auto tpr, auto nv) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
     using R = Row<TPR, NV, VEC>;
-    const dim3 grid((unsigned)((a.M + R::RPB - 1) / R::RPB));
-    if (a.codes)
-      hipLaunchKernelGGL((rmsnorm_kernel<T, TPR, NV, VEC, true>), grid, dim3(R::NT), 0, st, a);
-    else
-      hipLaunchKernelGGL((rmsnorm_kernel<T, TPR, NV, VEC, false>), grid, dim3(R::NT), 0, st, a);
+    by_rows<R>(all.M, [&](int64_t r0, int64_t rows) {
+      const RmsNormArgs a = rows_of<T>(all, r0, rows);
+      if (a.codes)
+        hipLaunchKernelGGL((rmsnorm_kernel<T, TPR, NV, VEC, true>), row_blocks<R>(rows), dim3(R::NT), 0, st, a);
+      else
+        hipLaunchKernelGGL((rmsnorm_kernel<T, TPR, NV, VEC, false>), row_blocks<R>(rows), dim3(R::NT), 0, st, a);
+    });
   });
 }
 
@@ -535,8 +562,10 @@ void run_pack(const void* X, int64_t ldx, int64_t M, int d, uint8_t* codes, floa
   by_width(d, [&](auto tpr, auto nv) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
     using R = Row<TPR, NV, VEC>;
-    hipLaunchKernelGGL((act8_pack_kernel<T, TPR, NV, VEC>), dim3((unsigned)((M + R::RPB - 1) / R::RPB)), dim3(R::NT), 0, st,
-                       static_cast<const T*>(X), ldx, M, d, codes, scale8);
+    by_rows<R>(M, [&](int64_t r0, int64_t rows) {
+      hipLaunchKernelGGL((act8_pack_kernel<T, TPR, NV, VEC>), row_blocks<R>(rows), dim3(R::NT), 0, st,
+                         static_cast<const T*>(X) + r0 * ldx, ldx, rows, d, codes + r0 * d, scale8 + r0);
+    });
   });
 }
 

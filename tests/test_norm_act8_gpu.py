@@ -555,3 +555,32 @@ def test_act8_function_takes_codes_of_its_input_only(lib):
             f(X, W, A, B, 0.5, *bad)
     with pytest.raises(TypeError):
         f(X, W, A, B, 0.5, codes, s8.double())
+
+
+def test_more_rows_than_a_launch_takes(lib):
+    """2^28 rows and some of 8: blocks of 16 rows and 256 threads, of which a launch takes fewer than 2^24.  Every output
+    is that of the rows in parts, bit for bit, past 2^31 elements."""
+    M, d, part = (1 << 28) + 37, 8, 1 << 25
+    X = torch.randn(M, d, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda", dtype=torch.bfloat16)
+    w = _randn(2, d, dtype=torch.bfloat16)
+    Y, _, rstd, codes, s8 = lib.lora_rmsnorm_fwd(X, w, residual=X, pack=True)
+    pc, ps = lib.lora_act8_pack(X)
+    back = lib.lora_act8_unpack(pc, ps)
+    bits = lambda t: t.view(torch.uint8)  # noqa: E731
+    for a in range(0, M, part):
+        x = X[a:a + part]
+        y, _, r, c, s = lib.lora_rmsnorm_fwd(x, w, residual=x, pack=True)
+        q, e = lib.lora_act8_pack(x)
+        rows = slice(a, a + len(x))
+        for got, want in ((Y, y), (codes, c), (pc, q), (back, lib.lora_act8_unpack(q, e))):
+            assert torch.equal(bits(got[rows]), bits(want))
+        for got, want in ((rstd, r), (s8, s), (ps, e)):
+            assert torch.equal(got[rows], want)
+    # and the parts are right where the launches meet
+    x = X[-64:].float()
+    h = (x + x).bfloat16().double()
+    r = 1 / torch.sqrt(h.square().mean(1) + 1e-5)
+    _near(rstd[-64:], r, 2 * U * r, "rstd")
+    _near(Y[-64:], h * r[:, None] * w.double(), (4 * U + 2.0 ** -8) * (h * r[:, None] * w.double()).abs(), "Y")
+    del X, Y, codes, pc, back
+    torch.cuda.empty_cache()
