@@ -2851,10 +2851,20 @@ int lora_act8_linear_bwd(int dtype, int64_t M, int64_t d_in, const lora_group_me
 }
 
 // ---- an adapter of its own for every row ----
+// Rows of a forward are taken kMultiRows at a time, with one workspace: its launches have
+// a block a row, and a launch has fewer than 2^32 threads.
+constexpr int64_t kMultiRows = int64_t(1) << 23;
+
+static size_t multi_fwd_bytes(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r) {
+  auto bytes = [&](int64_t rows) { return make_multi_layout(false, dtype, rows, d_in, d_out, n, r, false, false).total; };
+  return M <= kMultiRows ? bytes(M) : std::max(bytes(kMultiRows), bytes(M % kMultiRows));
+}
+
 size_t lora_multi_workspace_bytes(int backward, int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r,
                                   int have_w_t, int need_dx) {
   if (check_multi(backward != 0, dtype, M, d_in, d_out, n, r) != LORA_OK) return 0;
-  return make_multi_layout(backward != 0, dtype, M, d_in, d_out, n, r, have_w_t != 0, need_dx != 0).total;
+  if (!backward) return multi_fwd_bytes(dtype, M, d_in, d_out, n, r);
+  return make_multi_layout(true, dtype, M, d_in, d_out, n, r, have_w_t != 0, need_dx != 0).total;
 }
 
 int lora_multi_fwd(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r, const void* X, const void* W,
@@ -2867,12 +2877,20 @@ int lora_multi_fwd(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n,
     TRY(check_ptrs({X, Y}));
     TRY(check_elems({{index, 4}}, true));
   }
-  const MultiLayout L = make_multi_layout(false, dtype, M, d_in, d_out, n, r, false, false);
-  TRY(check_ws_bytes(L.total, ws, ws_bytes));
-  TRY(check_device());
-  if (M == 0) return LORA_OK;
-  const MultiCall c{dtype, M, d_in, d_out, n, r, scales, index};
-  return multi_forward(c, L, X, W, A, B, Y, static_cast<char*>(ws), static_cast<hipStream_t>(stream));
+  const int64_t eb = elem_bytes(dtype);
+  for (int64_t r0 = 0; r0 < M || r0 == 0; r0 += kMultiRows) {
+    const int64_t rows = std::min(kMultiRows, M - r0);
+    const MultiLayout L = make_multi_layout(false, dtype, rows, d_in, d_out, n, r, false, false);
+    if (r0 == 0) {
+      TRY(check_ws_bytes(M <= kMultiRows ? L.total : multi_fwd_bytes(dtype, M, d_in, d_out, n, r), ws, ws_bytes));
+      TRY(check_device());
+      if (M == 0) return LORA_OK;
+    }
+    const MultiCall c{dtype, rows, d_in, d_out, n, r, scales, index + r0};
+    TRY(multi_forward(c, L, static_cast<const char*>(X) + r0 * d_in * eb, W, A, B, static_cast<char*>(Y) + r0 * d_out * eb,
+                      static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
+  }
+  return LORA_OK;
 }
 
 int lora_multi_bwd(int dtype, int64_t M, int64_t d_in, int64_t d_out, int64_t n, int64_t r, const void* X, const void* W,

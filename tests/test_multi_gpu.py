@@ -422,3 +422,30 @@ def test_stacks_past_the_product_kernel_backward(lib):
     for got, w, t, what in ((dA, wA, tA, "dA"), (dB, wB, tB, "dB")):
         _near(got[used], w, t + 2.0 ** -8 * (w.abs() + t), what)
         assert int((got != 0).flatten(1).any(1).sum()) <= len(used)
+
+
+@pytest.mark.parametrize("dtype,M,k,d", [(torch.float32, (1 << 24) + 77, 8, 16), (torch.bfloat16, (1 << 24) + 300, 64, 72)])
+def test_more_rows_than_a_launch_takes(lib, dtype, M, k, d):
+    """Past 2^24 rows: a launch of a block a row would have 2^32 threads.  Workspace of the asked size, between guards."""
+    n, r, part = 5, 8, 1 << 20
+    gpu = torch.Generator(device="cuda").manual_seed(3)
+    X = torch.randn(M, k, generator=gpu, device="cuda", dtype=dtype)
+    _, W, A, B, scales, _, _ = make(3, 1, k, d, n, r, dtype)
+    index = torch.randint(-1, n + 1, (M,), generator=gpu, device="cuda", dtype=torch.int32)
+    nb = lib.lib().lora_multi_workspace_bytes(0, 0 if dtype == torch.float32 else 1, M, k, d, n, r, 0, 0)
+    room = torch.full((nb + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    Y = lib.lora_multi_fwd(X, W, A, B, scales, index, ws=room[256:256 + nb])
+    assert bool((room[:256] == 0xA5).all()) and bool((room[256 + nb:] == 0xA5).all())
+    h, one = H[dtype], torch.zeros(1, r, k, dtype=torch.float64, device="cuda")
+    a = torch.cat((A.double() * scales.double()[:, None, None], one))  # (row n: none)
+    b = torch.cat((B.double(), torch.zeros(1, d, r, dtype=torch.float64, device="cuda")))
+    for t in range(0, M, part):
+        x, i = X[t:t + part].double(), index[t:t + part].long()
+        i = torch.where((i < 0) | (i >= n), n, i)
+        want, tol = x @ W.double().T, (k + r + 4) * U * (x.abs() @ W.double().abs().T)
+        for e in range(n):
+            rows = torch.nonzero(i == e).squeeze(1)
+            P, mP = x[rows] @ a[e].T, x[rows].abs() @ a[e].abs().T
+            want[rows] += P @ b[e].T
+            tol[rows] += (h * P.abs() + (k + 4) * U * mP) @ b[e].abs().T + ((k + r + 4) * U + h) * (mP @ b[e].abs().T)
+        _near(Y[t:t + part], want, tol + h * (want.abs() + tol) + 1e-37, t)
