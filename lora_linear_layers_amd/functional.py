@@ -950,8 +950,8 @@ def lora_rmsnorm_fwd(X, weight, eps: float = 1e-5, residual=None, pack: bool = F
     new = lambda t: torch.empty(M, d, dtype=t, device=dev)  # noqa: E731
     Y = new(X.dtype) if need_y else None
     codes = new(torch.float8_e4m3fn) if pack else None
-    stats = torch.empty(2 if pack else 1, M, dtype=torch.float32, device=dev)
-    rstd, scale8 = stats[0], stats[1] if pack else None
+    rstd = torch.empty(M, dtype=torch.float32, device=dev)
+    scale8 = torch.empty(M, dtype=torch.float32, device=dev) if pack else None
     with _on(dev):
         L._check("lora_rmsnorm_fwd", L.lib().lora_rmsnorm_fwd(
             dt, M, d, float(eps), L._ptr(X), ldx, L._ptr(residual), ldr, L._ptr(weight), L._ptr(H), L._ptr(Y),

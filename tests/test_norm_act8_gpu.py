@@ -584,3 +584,15 @@ def test_more_rows_than_a_launch_takes(lib):
     _near(Y[-64:], h * r[:, None] * w.double(), (4 * U + 2.0 ** -8) * (h * r[:, None] * w.double()).abs(), "Y")
     del X, Y, codes, pc, back
     torch.cuda.empty_cache()
+
+
+def test_norm_outputs_own_their_storage(lib):
+    """Every output is a tensor of its own: the codes' scales may be changed or freed without the backward's rstd."""
+    X, w = _randn(1, 16, 64).requires_grad_(), _randn(2, 64)
+    outs = [t for t in lib.lora_rmsnorm_fwd(X.detach(), w, residual=X.detach(), pack=True)]
+    assert len({t.untyped_storage().data_ptr() for t in outs}) == len(outs)
+    Y, Hh, codes, s8 = lib.LoraRmsNormFunction.apply(X, X.detach(), w, 1e-5, True)
+    (want,) = torch.autograd.grad(Y, X, torch.ones_like(Y), retain_graph=True)
+    s8.mul_(2)
+    (got,) = torch.autograd.grad(Y, X, torch.ones_like(Y))
+    assert torch.equal(got, want)
