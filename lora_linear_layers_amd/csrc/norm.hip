@@ -161,8 +161,10 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 
 // The nearest float to v on the odd side: where v lies between two floats, the one
 // with the odd last bit.  Rounded again to fewer bits, it gives what v itself would.
+// (An infinity past the range: as y is there, a value that has no code.)
 __device__ __forceinline__ float to_odd(double v) {
   const float f = (float)v;
+  if (!finite(f)) return f;
   const double g = f;
   uint32_t b = __builtin_bit_cast(uint32_t, f);
   if (g != v && !(b & 1u)) b += fabs(v) > fabs(g) ? 1u : 0xFFFFFFFFu;

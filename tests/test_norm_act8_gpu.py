@@ -596,3 +596,22 @@ def test_norm_outputs_own_their_storage(lib):
     s8.mul_(2)
     (got,) = torch.autograd.grad(Y, X, torch.ones_like(Y))
     assert torch.equal(got, want)
+
+
+def test_norm_codes_beside_a_value_past_the_range(lib):
+    """A value past fp32's range is an infinity in Y and no code, and the row's scale is that of the others, also where
+    their largest lies on the border of two scales (448 2^-8 here, which 64 bits decide)."""
+    big = torch.finfo(torch.float32).max
+    X = torch.tensor([[1.0, 1.5, 0.25, 0.5]] * 4, device="cuda")
+    r = 1 / math.sqrt((1 + 2.25 + 0.0625 + 0.25) / 4)
+    for step in range(-2, 3):
+        w0 = torch.tensor(1.75 / r, dtype=torch.float32).view(torch.int32).add(step).view(torch.float32)
+        w = torch.tensor([float(w0), big, 1.0, 1.0], device="cuda")
+        Y, _, _, codes, s8 = lib.lora_rmsnorm_fwd(X, w, 0.0, pack=True)
+        assert bool(torch.isinf(Y[:, 1]).all()) and bool(torch.isnan(codes[:, 1].float()).all())
+        h = X.double()
+        y = h / torch.sqrt(h.square().mean(1, keepdim=True)) * w.double()
+        y[:, 1] = math.inf
+        c, s = pack64(y)
+        assert torch.equal(s8.double(), s), (step, s8, s)
+        _same_codes(codes, c)
