@@ -471,7 +471,8 @@ int lora_transpose(const void* src, int64_t rows, int64_t cols, void* dst, void*
  * at least): H [M, d] = h, Y [M, d] = y, rstd fp32 [M], and codes [M, d] with
  * scale8 [M]: y as lora_act8_pack keeps it, rounded once (from y before its
  * rounding to the dtype).  H may be X or the residual (the stream updated in
- * place), Y may be X without a residual; with row strides of d.  The sum of
+ * place), Y may be X without a residual; with row strides of d (others are
+ * refused there).  The sum of
  * squares is kept in 64 bits, rstd in fp32 (root mean squares from 2^-126 to 2^126 have
  * one).  Pointers need their element's alignment only.  1 <= d <= LORA_NORM_MAX_DIM, 0 <= M < 2^31, eps >= 0
  * (a row of zeros with eps 0 gives NaN).

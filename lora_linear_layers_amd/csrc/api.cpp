@@ -2730,6 +2730,9 @@ int lora_rmsnorm_fwd(int dtype, int64_t M, int64_t d, float eps, const void* X, 
   if (M > 0) {
     TRY(check_elems({{X, eb}, {weight, eb}}, true));
     if (!codes != !scale8 || (!Y && !codes && !H && !rstd)) return LORA_ERR_NULL;
+    // (in place: a row's outputs where it was read; else they would be another row's inputs)
+    auto shifts = [&](const void* out) { return out && ((out == X && ldx != d) || (out == residual && ldr != d)); };
+    if (M > 1 && (shifts(H) || shifts(Y))) return LORA_ERR_SHAPE;
     TRY(check_elems({{residual, eb}, {H, eb}, {Y, eb}, {scale8, 4}, {rstd, 4}}, false));
   }
   TRY(check_device());

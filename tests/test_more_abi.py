@@ -134,3 +134,14 @@ def test_multi_backward_rows():
         assert lib.lora_multi_workspace_bytes(1, dtype, (1 << 21) + 1, 64, 64, 2, 8, 0, 1) == 0
         assert lib.lora_multi_workspace_bytes(0, dtype, (1 << 21) + 1, 64, 64, 2, 8, 0, 0) > 0
         assert lib.lora_multi_bwd(dtype, (1 << 21) + 1, 64, 64, 2, 8, P, P, None, P, P, P, P, P, P, P, P, 0, P, 1 << 40, None) == ESHAPE
+
+
+def test_norm_in_place_needs_rows_of_the_width():
+    """Outputs have rows of d elements: over an input with longer rows they would overwrite rows not yet read."""
+    lib = L.load()
+    X, R, far = P, P + 4096, P + 8192
+    for kw in (dict(ldx=72, H=X), dict(ldx=72, Y=X), dict(R=R, ldr=72, H=R), dict(R=R, ldr=72, Y=R), dict(R=R, ldr=64, ldx=72, H=X)):
+        assert _norm(lib, **{"Y": far, **kw}) == ESHAPE, kw
+    # a single row, rows of d elements, or other memory: refused for the alignment of rstd alone
+    for kw in (dict(ldx=72, H=X, M=1), dict(H=X), dict(ldx=72, H=far + 4096), dict(R=R, ldr=64, H=R, ldx=72), dict(Y=X)):
+        assert _norm(lib, **{"Y": far, "rstd": P + 2, **kw}) == EALIGN, kw
