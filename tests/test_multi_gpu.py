@@ -449,3 +449,47 @@ def test_more_rows_than_a_launch_takes(lib, dtype, M, k, d):
             want[rows] += P @ b[e].T
             tol[rows] += (h * P.abs() + (k + 4) * U * mP) @ b[e].abs().T + ((k + r + 4) * U + h) * (mP @ b[e].abs().T)
         _near(Y[t:t + part], want, tol + h * (want.abs() + tol) + 1e-37, t)
+
+
+# up to 64 rows whose product neither the one-launch kernel nor the W stream takes: dot products for the strips in fp32,
+# their part into Y, then the layer's other kernels
+DOT_ROWS = [(17, 4096, 1024, 9, 16), (64, 4096, 1024, 16, 64), (33, 2568, 1032, 7, 24), (40, 2056, 8, 3, 8), (64, 8200, 1000, 64, 128)]
+
+
+@pytest.mark.parametrize("order", ["packed", "random"])
+@pytest.mark.parametrize("shape", DOT_ROWS)
+def test_few_rows_by_dot_products(lib, shape, order):
+    check(lib, make(sum(shape), *shape, torch.bfloat16, order))
+
+
+@pytest.mark.parametrize("M,k,d", [(40, 4096, 1024), (64, 2568, 1032)])
+def test_infinities_of_rows_by_dot_products(lib, M, k, d):
+    test_infinities_stay_with_their_own(lib, torch.bfloat16, M, k, d)
+
+
+@pytest.mark.parametrize("order", ["packed", "random"])
+@pytest.mark.parametrize("shape", [(1000, 1000, 4096, 12, 16), (2600, 1000, 4096, 5, 72), (1200, 1544, 14336, 40, 64), (4096, 1000, 4096, 6, 16),
+                                   (1000, 4096, 1000, 12, 16), (1200, 14336, 1544, 40, 24), (4096, 4096, 1000, 6, 128)])
+def test_ragged_contractions(lib, shape, order):
+    """The tile kernels with a last stage of the base product that is not whole, ahead of the adapters' stages: 128 x 256
+    and 256 x 256 tiles, a block or two each, Y and dX."""
+    check(lib, make(sum(shape), *shape, torch.bfloat16, order))
+
+
+def test_offsets_past_2_31_elements(lib):
+    """X and dX of more than 2^31 elements; dY is zero but for some rows at either end and between."""
+    M, k, d, n, r = (1 << 19) + 300, 4104, 64, 6, 16
+    gpu = torch.Generator(device="cuda").manual_seed(4)
+    X = torch.randn(M, k, generator=gpu, device="cuda", dtype=torch.bfloat16)
+    _, W, A, B, scales, _, _ = make(4, 1, k, d, n, r, torch.bfloat16)
+    index = torch.randint(-1, n, (M,), generator=gpu, device="cuda", dtype=torch.int32)
+    rows = torch.cat([torch.arange(a, a + 300, device="cuda") for a in (0, M // 2 - 7, M - 300)])
+    dY = torch.zeros(M, d, device="cuda", dtype=torch.bfloat16)
+    dY[rows] = torch.randn(900, d, generator=gpu, device="cuda", dtype=torch.bfloat16)
+    Y = lib.lora_multi_fwd(X, W, A, B, scales, index)
+    dX, dA, dB = lib.lora_multi_bwd(X, W, A, B, scales, index, dY)
+    got = (Y[rows], dX[rows], dA, dB)
+    for name, g, (want, tol) in zip(("Y", "dX", "dA", "dB"), got, reference(X[rows], W, A, B, scales, index[rows], dY[rows])):
+        _near(g, want, tol, name)
+    dX[rows] = 0
+    assert not bool(dX.any())

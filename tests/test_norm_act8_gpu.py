@@ -615,3 +615,48 @@ def test_norm_codes_beside_a_value_past_the_range(lib):
         c, s = pack64(y)
         assert torch.equal(s8.double(), s), (step, s8, s)
         _same_codes(codes, c)
+
+
+def test_act8_backward_past_2_31_elements(lib):
+    """Codes of more than 2^31 elements; dY is zero but for some rows at either end and between, whose gradients are
+    those of these rows alone."""
+    M, k, d, r, scale = (1 << 18) + 300, 8208, 64, 16, 0.5
+    gpu = torch.Generator(device="cuda").manual_seed(4)
+    X = torch.randn(M, k, generator=gpu, device="cuda", dtype=torch.bfloat16)
+    codes, s8 = lib.lora_act8_pack(X)
+    rows = torch.cat([torch.arange(a, a + 300, device="cuda") for a in (0, M // 2 - 7, M - 300)])
+    x = X[rows]
+    del X
+    _, W, A, B, dy = _lora(5, 900, k, d, r, torch.bfloat16)
+    dY = torch.zeros(M, d, device="cuda", dtype=torch.bfloat16)
+    dY[rows] = dy
+    _, dA, dB = lib.lora_act8_linear_bwd(codes, s8, {"W": W, "A": A, "B": B, "scale": scale}, dY, need_dX=False)
+    c, s = pack64(x.double())
+    K, a, b, g, h = c * s[:, None], A.double(), B.double(), dy.double(), 2.0 ** -8
+    P, Q, mP, mQ = scale * (K @ a.T), scale * (g @ b), scale * (K.abs() @ a.abs().T), scale * (g.abs() @ b.abs())
+    eP, eQ = h * P.abs() + (k + 4) * U * mP, h * Q.abs() + (d + 4) * U * mQ
+    _near(dA, Q.T @ K, eQ.T @ K.abs() + 902 * U * (mQ.T @ K.abs()) + 1e-37, "dA")
+    _near(dB, g.T @ P, g.abs().T @ eP + 902 * U * (g.abs().T @ mP) + 1e-37, "dB")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", WIDTHS)
+def test_norm_is_as_exact_as_its_type(lib, dtype, d):
+    """The bounds of sums kept in 64 bits.  The reciprocal root is off by half of the sum's error (44 additions of 2^-53)
+    and by 3/2 of the square of its start's (a root and a division in 32 bits, 2^-23): below 2^-44 in all.  rstd is that
+    rounded once, u; y = (h rstd) w takes two products more, 3 u and their second order, then the type's half step.  Codes
+    and scales are those of the exact y, but for values that 2^-44 of themselves could bring across a border."""
+    for M, scale in ((3, 1.0), (64, 1e-12), (257, 1e9)):
+        X, R = ((_randn(d + M + i, M, d) * scale).to(dtype) for i in (5, 6))
+        w, eps = (1 + 0.3 * _randn(d + M + 7, d)).to(dtype), 1e-6 * scale * scale
+        Y, Hh, rstd, codes, s8 = lib.lora_rmsnorm_fwd(X, w, eps, residual=R, pack=True)
+        h, e32 = Hh.double(), torch.tensor(eps, dtype=torch.float32).double().item()
+        r = 1 / torch.sqrt(h.square().mean(1, keepdim=True) + e32)
+        y = h * r * w.double()
+        _near(rstd, r[:, 0], (U + 2.0 ** -44) * r[:, 0], "rstd")
+        _near(Y, y, (3.001 * U + H[dtype] * (1 + 4 * U)) * y.abs() + 1e-37, "Y")
+        (c, s), (lo, sl), (hi, sh) = (pack64(y * (1 + k * 2.0 ** -44)) for k in (0, -1, 1))
+        sure = (sl == sh)
+        assert torch.equal(s8.double()[sure], s[sure])
+        sure = sure[:, None] & (lo == hi)
+        assert torch.equal(codes.double()[sure], c[sure]) and float(sure.double().mean()) > 0.999
