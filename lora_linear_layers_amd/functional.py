@@ -542,17 +542,18 @@ class LoraLinearEpiFunction(torch.autograd.Function):
         # (the residual's gradient alone needs no Z)
         Y, Z = lora_linear_epi_fwd(X, member, act, bias, residual,
                                    store_z=act != "none" and any(ctx.needs_input_grad[i] for i in (0, 2, 3, 4)))
-        _keep(ctx, X, W, A, B, Z, W_t)
-        ctx.scale, ctx.act = scale, act
+        ctx.save_for_backward(X, W, A, B, Z, W_t)
+        ctx.dims, ctx.scale, ctx.act = (*X.shape, *B.shape), scale, act
         ctx.shapes = [None if t is None else t.shape for t in (bias, residual)]
         return Y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dY):
-        X, W, A, B, Z, W_t = _kept(ctx, dY.device)
+        dev, same, (M, d_in, d_out, r) = dY.device, dY.dtype, ctx.dims
+        X, W, A, B, Z, W_t = _kept(ctx, dev, (same, (M, d_in)), (same, (d_out, d_in)), (same, (r, d_in)), (same, (d_out, r)),
+                                   (same, (M, d_out)), (torch.bfloat16, (d_in, d_out)))
         dY = dY.contiguous()
-        dev, (M, d_in), (d_out, r) = X.device, X.shape, B.shape
         _check(dev, "the gradient of Y", dY, (X.dtype,), M * d_out)
         bias, residual = ctx.shapes
         need_dX, _, need_dA, need_dB, need_dbias, need_dR = ctx.needs_input_grad[:6]
@@ -632,18 +633,12 @@ def _check_ws(device, ws, nbytes=None):
     return ws
 
 
-def _keep(ctx, *tensors):
-    """save_for_backward, and what _kept checks of each."""
-    ctx.save_for_backward(*tensors)
-    ctx.kept = [None if t is None else (t.dtype, t.shape) for t in tensors]
-
-
-def _kept(ctx, device):
-    """The saved tensors, still contiguous, on the device and of their dtype and shape: saved-tensor hooks may give back
-    any others, and their addresses go to the library."""
+def _kept(ctx, device, *as_saved):
+    """The saved tensors, still contiguous, on the device and of the dtype and shape that as_saved gives for each:
+    saved-tensor hooks may give back any others, and their addresses go to the library."""
     saved = ctx.saved_tensors
-    for t, kept in zip(saved, ctx.kept):
-        if kept is not None and (t is None or t.device != device or (t.dtype, t.shape) != kept or not t.is_contiguous()):
+    for t, (dtype, shape) in zip(saved, as_saved):
+        if t is not None and (t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous()):
             raise ValueError("a saved tensor came back with another device, dtype, shape or strides")
     return saved
 
@@ -1006,7 +1001,8 @@ class LoraRmsNormFunction(torch.autograd.Function):
     def forward(ctx, X, residual, weight, eps=1e-5, pack=False):
         Y, H, rstd, codes, scale8 = lora_rmsnorm_fwd(X, weight, eps, residual, pack)
         ctx.set_materialize_grads(False)
-        _keep(ctx, H.contiguous(), weight, rstd)
+        ctx.save_for_backward(H.contiguous(), weight, rstd)
+        ctx.weight = weight.shape
         H = H if residual is not None else None
         if not pack:
             return Y, H
@@ -1020,7 +1016,8 @@ class LoraRmsNormFunction(torch.autograd.Function):
         if dY is None:  # the stream alone went on
             return dH if need_X else None, dH if need_R else None, None, None, None
         # (autograd checked the gradients' type, shape and device)
-        H, weight, rstd = _kept(ctx, dY.device)
+        same = dY.dtype
+        H, weight, rstd = _kept(ctx, dY.device, (same, dY.shape), (same, ctx.weight), (torch.float32, dY.shape[:1]))
         dX, dw = _rmsnorm_bwd(H, weight, rstd, dY.contiguous(), None if dH is None else dH.contiguous(),
                               need_X or need_R, need_w, weight.dtype)
         return dX if need_X else None, dX if need_R else None, None if dw is None else dw.view_as(weight), None, None
@@ -1112,16 +1109,18 @@ class LoraLinearAct8Function(torch.autograd.Function):
                 if codes.shape != X.shape or codes.device != X.device:
                     raise ValueError("codes must have X's shape and device")
                 _packed(codes, scale8)
-            _keep(ctx, codes, scale8, W, A, B, W_t)
+            ctx.save_for_backward(codes, scale8, W, A, B, W_t)
+            ctx.dims, ctx.code, ctx.rows = (*X.shape, *B.shape), codes.dtype, scale8.shape
         ctx.scale = scale
         return Y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dY):
-        codes, scale8, W, A, B, W_t = _kept(ctx, dY.device)
+        same, (M, d_in, d_out, r) = dY.dtype, ctx.dims
+        codes, scale8, W, A, B, W_t = _kept(ctx, dY.device, (ctx.code, (M, d_in)), (torch.float32, ctx.rows), (same, (d_out, d_in)),
+                                            (same, (r, d_in)), (same, (d_out, r)), (torch.bfloat16, (d_in, d_out)))
         dY = dY.contiguous()  # (its type, shape and device are Y's)
-        (M, d_in), (d_out, r) = codes.shape, B.shape
         m = _epi_struct({"W": W, "A": A, "B": B, "scale": ctx.scale, "W_t": W_t}, r, d_out)
         need_dX, _, need_dA, need_dB = ctx.needs_input_grad[:4]
         dX, dA, dB = _act8_bwd(codes, scale8, m, dY, M, d_in, d_out, r, need_dX, None, A.dtype)
@@ -1218,13 +1217,17 @@ class LoraMultiFunction(torch.autograd.Function):
     def forward(ctx, X, W, A, B, scales, index, W_t=None):
         ctx.dims = dims = _multi_dims(X, W, A, B, scales, index)
         _multi_wt(dims[1], W_t, dims[3], dims[4])
-        _keep(ctx, X, W, A, B, scales, index, W_t)
+        ctx.save_for_backward(X, W, A, B, scales, index, W_t)
+        ctx.rows = scales.shape, index.shape
         return _multi_fwd(dims, X, W, A, B, scales, index)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dY):
-        X, W, A, B, scales, index, W_t = _kept(ctx, dY.device)
+        same, (_, _, M, d_in, d_out, n, r), (ns, ni) = dY.dtype, ctx.dims, ctx.rows
+        X, W, A, B, scales, index, W_t = _kept(
+            ctx, dY.device, (same, (M, d_in)), (same, (d_out, d_in)), (same, (n, r, d_in)), (same, (n, d_out, r)),
+            (torch.float32, ns), (torch.int32, ni), (torch.bfloat16, (d_in, d_out)))
         need_dX, _, need_dA, need_dB = ctx.needs_input_grad[:4]
         dX, dA, dB = _multi_bwd(ctx.dims, X, W, A, B, scales, index, dY.contiguous(), need_dX, W_t, X.dtype)
         return dX, None, dA if need_dA else None, dB if need_dB else None, None, None, None
