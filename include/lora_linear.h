@@ -472,9 +472,9 @@ int lora_transpose(const void* src, int64_t rows, int64_t cols, void* dst, void*
  * scale8 [M]: y as lora_act8_pack keeps it, rounded once (from y before its
  * rounding to the dtype).  H may be X or the residual (the stream updated in
  * place), Y may be X without a residual; with row strides of d (others are
- * refused there).  The sum of
- * squares is kept in 64 bits, rstd in fp32 (root mean squares from 2^-126 to 2^126 have
- * one).  Pointers need their element's alignment only.  1 <= d <= LORA_NORM_MAX_DIM, 0 <= M < 2^31, eps >= 0
+ * refused there).  The sum of squares is kept in 64 bits, rstd in fp32 (root mean
+ * squares from 2^-126 to 2^126 have one); a y past fp32's range is an infinity,
+ * for the codes too.  Pointers need their element's alignment only.  1 <= d <= LORA_NORM_MAX_DIM, 0 <= M < 2^31, eps >= 0
  * (a row of zeros with eps 0 gives NaN).
  *
  * Backward, for dY [M, d] and, where the stream goes on, dH [M, d] (NULL: 0),
@@ -504,7 +504,9 @@ size_t lora_rmsnorm_workspace_bytes(int64_t M, int64_t d);
  *     code = e4m3(x 2^-e), rounded to nearest even;   x is taken as code 2^e.
  * A value is off by at most 2^-4 of itself, or 2^(e - 10) where it is below
  * 2^(e - 6).  Infinities and NaNs become NaN codes.  lora_act8_unpack
- * writes code 2^e, a number of either type, [M, d].
+ * writes code 2^e, [M, d]: exact in either type, but that bf16 has steps of 2^-133
+ * below 2^-125, and that what was 1.9375 2^127 or more in size, rounded to 2^128,
+ * is an infinity.
  *
  * lora_act8_linear_bwd is the backward of lora_linear_fwd (and of its NF4 form)
  * with the checkpoint in X's place: of the three gradients only the
@@ -539,7 +541,8 @@ size_t lora_act8_linear_workspace_bytes(int dtype, int64_t M, int64_t d_in, cons
  * rows' outputs (dX) and its gradients NaN where the definition may leave some
  * finite, one in a row of X or dY its adapter's gradients; other adapters and rows do
  * not see it.  Y and dX overlap no input.
- * index and scales need their element's alignment only.  Workspace from its own
+ * index and scales need their element's alignment only.  The forward takes any
+ * M < 2^31, 2^23 rows after 2^23 rows with one workspace.  Workspace from its own
  * sizing call (with backward != 0: have_w_t whether W_t is given, need_dx
  * whether dX is).
  *

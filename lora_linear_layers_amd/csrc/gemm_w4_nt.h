@@ -72,8 +72,8 @@ typedef __attribute__((address_space(3))) void lds_void_t;
 // second segment is the tile's adapters', list by list, so that a tile's stages are
 // its contraction's and one for each 64 / ad_r of them: 8192 x 4096 over 4096, 8
 // adapters of 16 in runs of a thousand rows, 205 to 218 us (1340 TFLOP/s; the layer of one
-// adapter 195); 2048 x 4096 over 4096, 32 adapters, 114 to 122 us; 64 adapters in random
-// order, 14 stages more, 268 us.  Their second operands lie in one resource of less
+// adapter 195); 4001 x 4096 over 4096, 32 adapters, 114 to 122 us, 2048 x 4096 (128 x 256 tiles)
+// 65; 8192 rows of 64 adapters in random order, 14 stages more, 268 us.  Their second operands lie in one resource of less
 // than 0xE0000000 bytes; a lane without a value takes AD_OOB, which no row's offset
 // brings back into it.
 constexpr uint32_t AD_OOB = 0xF0000000u;

@@ -56,7 +56,7 @@ __device__ __forceinline__ int adapter_at(const int* index, int64_t t, int64_t M
 // The first block also clears the stream kernel's counters.  Then `chunks` blocks
 // an adapter, which look for infinities and NaNs in their part of its second
 // operand if a row carries it: one adapter's must not reach the others' rows; and the
-// backward's transposes of the stacks.  One launch, 7 to 8 us at 2048 rows of 32 adapters or
+// backward's transposes of the stacks.  One launch, 7 to 8 us at 4001 rows of 32 adapters or
 // 8192 of 8: what its longest blocks wait for, the indexes and then a share of an operand.
 // ---------------------------------------------------------------------------
 // The distinct values >= 0 of a wave's 64, in the order of their first lanes:
@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(256) multi_lists_kernel(const MultiLists q) {
 // tile could have, most of which leave at once, cost 5 of 16 us with 32 adapters:
 // each takes a CU's LDS for its launch.)  Two panels in one launch (the backward's
 // P and Q): splits [0, s0) of the grid are the first one's.
-// A stream of X, as the layer's own panel: 8192 x 4096 twice (P and Q) in 58 us, 2048 x
-// 4096 in 16.  Rows in random order read X again for every 64 columns of their tile's
+// A stream of X, as the layer's own panel: 8192 x 4096 twice (P and Q) in 58 us, 4001 x
+// 4096 in 16, 2048 x 4096 in 12.  Rows in random order read X again for every 64 columns of their tile's
 // adapters (64 of rank 16: 14 times, 525 us).
 __global__ void __launch_bounds__(pdma::NT) __attribute__((amdgpu_waves_per_eu(1, 1)))
 multi_panel_kernel(const GemmPair q) {
@@ -233,7 +233,10 @@ multi_panel_kernel(const GemmPair q) {
 // there, its bit in `mask` is clear like that of a token without adapter, and
 // its adapter's gradients are NaNs (gbad).  The strips are rounded to bf16 here, as the
 // layer's panel is, for the matrix cores: 2^-9 of a strip, next to the output's own
-// rounding.  6 to 7 us at 8192 tokens, the latency of index, partials and stores.
+// rounding.  6 to 7 us at 8192 tokens of 8 adapters, the latency of index, partials and stores;
+// a token's thread reads its adapter's flags (MultiLists::bad) one after the other, which is
+// most of it where few adapters have much data and so many flags: 4001 rows, d_out 14336,
+// 8 adapters of 16 (28 flags) 5.5 us, 2 of 64 (112) 14, one of 128 (224) 25.
 __global__ void __launch_bounds__(256) multi_strip_kernel(const MultiStrip s) {
   __shared__ int ids[64], spoilt[64], bad[64], groups[64];
   __shared__ float sc[64];

@@ -145,7 +145,9 @@ __device__ __forceinline__ bool finite(float x) { return (__builtin_bit_cast(uin
 // The power of two a row is kept at: the smallest 2^e, e >= -126, with
 // top 2^-e <= 448 (1 for a row of zeros).  top = m 2^k, 1 <= m < 2, and 448 is
 // 1.75 2^8: e = k - 8, or k - 7 where m > 1.75.  e4m3 is a floating type, so a
-// power of two costs no precision and any e4m3 code times it is a bf16 number.
+// power of two costs no precision, and an e4m3 code times it is a bf16 number, but for the
+// smallest codes at 2^-126 and 2^-125 (bf16 has steps of 2^-133 there) and 256 at 2^120 (2^128:
+// a value of 1.9375 2^127 or more, which rounds up to it, comes back infinite).
 __device__ __forceinline__ int pack_exponent(float top) {
   const uint32_t b = __builtin_bit_cast(uint32_t, top);
   if (b == 0u) return 0;
@@ -255,12 +257,16 @@ __device__ __forceinline__ double rsqrt64(double s) {
 // are those of the row's exact values: one whose code 32 bits leave open is formed
 // in 64 again (pack_row).  (From 32 bits alone a few codes in a million are the
 // neighbour's.)
-// A row lives in registers between its one read and its writes; a block is a row of
-// more than 1024 elements, or several rows below, so that 16 to 32 bytes a thread and
+// A row lives in registers between its one read and its writes (but see below); a block is a
+// row of more than 1024 elements, or several rows below, so that 16 to 32 bytes a thread and
 // input are in flight on every CU.  8192 x 4096 bf16, residual, Y and codes: 302 MB in
 // 50 us, 6 TB/s, what reads and writes of this mix reach; 65536 x 128: 34 MB in 10 us;
-// 48 x 4096: 3.8 us, the launch.  Odd widths take one element at a time: 2047 x 1001 fp32,
+// 16 x 4096: 3.8 us, the launch.  Odd widths take one element at a time: 2047 x 1001 fp32,
 // 35 MB (out of the caches) in 17 us.
+// With codes, rows of 4097 to 8192 and of more than 16384 elements (NV = 4) lie in scratch
+// memory instead: the border case of pack_row picks a chunk of h by a number that is
+// not a constant, which takes h out of the registers on every row.  8192 x 5120 bf16 with
+// residual 230 us (60 without codes), 4096 x 8192 137 (42), 2048 x 32768 270 (104).
 template <typename T, int TPR, int NV, bool VEC, bool PACK>
 __global__ void __launch_bounds__((Row<TPR, NV, VEC>::NT)) rmsnorm_kernel(const RmsNormArgs a) {
   using R = Row<TPR, NV, VEC>;
@@ -343,7 +349,7 @@ __global__ void __launch_bounds__((Row<TPR, NV, VEC>::NT)) act8_pack_kernel(cons
   pack_row<TPR, NV, VEC, false>(x, d, t, codes + row * (int64_t)d, scale8 + row, red, [](int, double (&)[8]) {});
 }
 
-// x = code * scale, a number of either type: 8 elements a thread.
+// x = code * scale in the type: 8 elements a thread.
 __device__ __forceinline__ void decode4(uint32_t v, float s, float* f) {
   const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)v, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)v, true);
   f[0] = lo[0] * s;
@@ -398,6 +404,8 @@ __global__ void __launch_bounds__(256) to_bf16_kernel(const float* a, int64_t na
 // rmsnorm_dw_kernel sums in order.  Up to 1024 blocks, four a CU: enough loads in
 // flight for the memory's rate (8192 x 4096 bf16 with dH: 268 MB in 50 us, 5.4 TB/s)
 // and 16 MB of partials (4 us); 512 of rows past 8192, whose registers fill a CU with two.
+// Past 16384 elements the registers do not hold a row's x, g and sums (48 to 127 of them
+// spill in the row loop): 2048 x 32768 with dH 260 us, 2 TB/s; x 16384 53 us.
 // ---------------------------------------------------------------------------
 template <typename T, int TPR, int NV, bool VEC>
 __global__ void __launch_bounds__((Row<TPR, NV, VEC>::NT)) rmsnorm_grad_kernel(const RmsNormGradArgs a) {

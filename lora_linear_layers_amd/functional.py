@@ -1050,7 +1050,7 @@ def _packed(codes, scale8, M=None):
 
 
 def lora_act8_unpack(codes, scale8, dtype=torch.bfloat16):
-    """codes * scale8 [M, d] in bf16 or fp32 (exact in both)."""
+    """codes * scale8 [M, d] in bf16 or fp32 (exact, but for bf16 values below 2^-125 and what was rounded to 2^128)."""
     dev, (M, d) = _packed(codes, scale8)
     X = torch.empty(M, d, dtype=dtype, device=dev)
     with _on(dev):
@@ -1211,7 +1211,8 @@ def _multi_bwd(dims, X, W, A, B, scales, index, dY, need_dX, W_t, grad_dtype, ws
 
 
 class LoraMultiFunction(torch.autograd.Function):
-    """Y = LoraMultiFunction.apply(X, W, A, B, scales, index, W_t): lora_multi_fwd with gradients for X, A and B (W frozen)."""
+    """Y = LoraMultiFunction.apply(X, W, A, B, scales, index, W_t): lora_multi_fwd with gradients for X, A and B (W frozen);
+    a backward takes 2^21 rows at most."""
 
     @staticmethod
     def forward(ctx, X, W, A, B, scales, index, W_t=None):
